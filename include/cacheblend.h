@@ -343,6 +343,61 @@ size_t cb_gemm_noalloc_scratch_used(int M, int N, int K, int epilogue, cb_dtype 
  * is shared by every caller: read it after the GEMMs that matter, on their stream. */
 cb_status cb_gemm_get_status(void* stream, int timeout_ms);
 
+/* --------------------------------------------------------------------- 8-bit floating point
+ * (no counterpart on the pages: their models run in 8 bits, [P1] 実験結果, without saying how)
+ * Matrices of e4m3 codes (4 exponent, 3 fraction bits, largest number 448) with fp32 scales.  A
+ * row matrix (activations) has a scale for each group of 128 consecutive channels of a row, a
+ * block matrix (weights) one for each block of 128 rows x 128 channels; the last group or block
+ * may be short.  With a = max(the largest magnitude of the group, 448 * 2^-126):
+ *   scale = a / 448,  code = e4m3(x * (448 / a))  (nearest, ties to even),  value = code * scale.
+ * A group that holds an infinity or a NaN decodes to NaN throughout; a group of zeros to zeros.
+ * Scales of a row matrix are stored group-major, [ceil(cols / 128)][ld_scales] with ld_scales >=
+ * rows (a product's tile of tokens then reads one line per group); scales of a block matrix are
+ * [ceil(rows / 128)][ld_scales] with ld_scales >= ceil(cols / 128).
+ * Codes, fp32 and bf16 matrices are row-major with a pitch in elements; base addresses are
+ * 16-byte aligned, pitches a multiple of 16 bytes, and channels (cols, d, K and the features of
+ * a CB_FP8_SWIGLU_FP8 output) a multiple of 16.  Row scales: 16-byte aligned, ld_scales % 4 == 0.
+ * Entries between a row's end and its pitch are neither read nor written. */
+typedef struct {
+  const void* codes;    /* e4m3 [rows][ld] */
+  long long ld;
+  const float* scales;
+  long long ld_scales;
+} cb_fp8_mat;
+
+/* Quantises x [rows][cols] of dtype (pitch ldx) into codes [rows][ld_codes] and scales:
+ * block_rows 1 makes a row matrix, 128 a block matrix.  rows 0 does nothing. */
+cb_status cb_quantize(const void* x, long long ldx, int rows, int cols, cb_dtype dtype, int block_rows,
+                          void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream);
+
+/* RMS norm with the residual's addition and an 8-bit output, one pass over each row:
+ *   h = residual + x,  residual_out = h,  y = h / sqrt(mean(h^2) + eps) * weight,  quantised as a
+ * row matrix.  h, its sum of squares and y are fp32 (y comes from h before it is rounded to
+ * residual_out's type).  x [rows][d] of x_dtype (pitch ldx); residual, residual_out [rows][d] of
+ * res_dtype with the same pitch ld_res, residual_out may be residual (in place) or NULL (not
+ * kept); residual NULL normalises x alone (residual_out must be NULL then); weight [d] of x_dtype
+ * or NULL for ones.  d <= 32768.  The codes may not overlap an input. */
+cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype, const void* residual, void* residual_out,
+                             long long ld_res, cb_dtype res_dtype, const void* weight, int rows, int d, float eps,
+                             void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream);
+
+/* C = A . B^T of a row matrix A [M][K] and a block matrix B [N][K]: the products of a group are
+ * summed in fp32, multiplied by the group's two scales and summed over the groups in fp32.
+ *   CB_FP8_STORE_F32   C fp32 [M][ldc] = acc
+ *   CB_FP8_ADD_F32     C fp32 [M][ldc] = addend + acc; addend fp32 [M][ldc], may be C
+ *   CB_FP8_SWIGLU_FP8  C e4m3 [M][ldc] and c_scales (a row matrix of N / 2 channels) = the
+ *                      quantised SiLU(gate) * up, with B the gate and B2 the up rows, each
+ *                      [N / 2][K] (N counts both): the input of the down projection
+ *   CB_FP8_STORE_BF16  C bf16 [M][ldc] = acc
+ * addend is read by CB_FP8_ADD_F32 alone, B2 and c_scales (pitch ld_cs) by CB_FP8_SWIGLU_FP8 alone
+ * (NULL otherwise).  C may overlap no input but addend == C.  Runs on the tcgen05 tensor cores.
+ * No workspace; results repeat exactly.  Device-side problems (a bounded wait that gave up) go to
+ * the standalone GEMM status word that cb_gemm_get_status() reads.  M 0 does nothing. */
+enum { CB_FP8_STORE_F32 = 0, CB_FP8_ADD_F32 = 1, CB_FP8_SWIGLU_FP8 = 2, CB_FP8_STORE_BF16 = 3 };
+cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_mat* B2, const float* addend, void* C,
+                      long long ldc, float* c_scales, long long ld_cs, int M, int N, int K, int epilogue,
+                      void* stream);
+
 /* Causal attention of sparse queries over one KV cache ([P3] "어떤 토큰을 다시 계산하는가":
  * selected queries attend under the causal mask to all available K/V).
  * q [m][n_heads][head_dim] dtype; q_pos int32 [m] (positions, < n_kv);

@@ -29,7 +29,7 @@ EXPORTED = ("cb_create", "cb_destroy", "cb_status_string", "cb_last_error", "cb_
             "cb_get_profile", "cb_get_layer_profile", "cb_gemm_noalloc", "cb_gemm_noalloc_error", "cb_gemm_noalloc_scratch_used", "cb_gemm_get_status", "cb_gemm_set_orientation", "cb_gemm_set_pairing", "cb_gemm_describe", "cb_attention_set_tiles", "cb_set_qkv_fusion",
             "cb_set_launch_overlap", "cb_codec_layer_bytes", "cb_kv_encode", "cb_kv_decode", "cb_register_chunk_codec",
             "cb_set_staging", "cb_chunk_hash", "cb_chunk_info_of", "cb_plan_loading", "cb_decode_step",
-            "cb_ratio_schedule", "cb_k_for_ratio")
+            "cb_ratio_schedule", "cb_k_for_ratio", "cb_quantize", "cb_add_rmsnorm_quantize", "cb_gemm_scaled")
 PHASES = ("begin", "staged_rot", "norm", "qkv", "rope", "deviation", "select", "scatter", "attention", "oproj",
           "gateup", "down", "finish")
 
@@ -83,6 +83,11 @@ class CostModel(C.Structure):
                 ("r_min", C.c_double), ("r_max", C.c_double)]
 
 
+class Fp8Mat(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("ld", C.c_longlong), ("scales", C.c_void_p), ("ld_scales", C.c_longlong)]
+
+
+CB_FP8_STORE_F32, CB_FP8_ADD_F32, CB_FP8_SWIGLU_FP8, CB_FP8_STORE_BF16 = 0, 1, 2, 3
 TIER_MISSING, TIER_DEVICE, TIER_HOST = -1, 0, 1
 ACT_USE, ACT_LOAD, ACT_RECOMPUTE = 0, 1, 2
 
@@ -131,6 +136,12 @@ def load_library(path: str = LIB_PATH):
         "cb_gemm_get_status": (st, [vp, C.c_int]),
         "cb_gemm_noalloc_scratch_used": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
         "cb_attention": (st, [vp, i32p, C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, vp, C.c_int, vp]),
+        "cb_quantize": (st, [vp, C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, vp, C.c_longlong, vp, C.c_longlong,
+                             vp]),
+        "cb_add_rmsnorm_quantize": (st, [vp, C.c_longlong, C.c_int, vp, vp, C.c_longlong, C.c_int, vp, C.c_int, C.c_int,
+                                         C.c_float, vp, C.c_longlong, vp, C.c_longlong, vp]),
+        "cb_gemm_scaled": (st, [C.POINTER(Fp8Mat), C.POINTER(Fp8Mat), C.POINTER(Fp8Mat), vp, vp, C.c_longlong, vp,
+                                C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, vp]),
         "cb_codec_layer_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
         "cb_kv_encode": (st, [vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp]),
         "cb_kv_decode": (st, [vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_double, C.c_int, vp, vp,
@@ -332,6 +343,114 @@ def cb_attention(q: torch.Tensor, q_pos: torch.Tensor, k: torch.Tensor, v: torch
     _check(lib.cb_attention(_ptr(q), _ptr(q_pos), m, _ptr(k), _ptr(v), n_kv, H, hkv, dh, _ptr(out),
                             _dtype_code(q.dtype), _stream(stream)))
     return out
+
+
+def _matrix(t: torch.Tensor, dtype, what: str, shape=None) -> int:
+    """Pitch of a 2-D CUDA matrix argument of the 8-bit calls, after checking it."""
+    if t.dtype != dtype:
+        raise CacheBlendError(3, f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or (shape is not None and (t.shape[0] != shape[0] or t.shape[1] < shape[1])):
+        raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}" + ("" if shape is None else f", needs {shape}"))
+    if not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise CacheBlendError(1, f"{what} must be a CUDA matrix with contiguous rows")
+    # the pitch of a single row is never stepped over and may be anything: pass one the library takes
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def row_scales(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """Uninitialised scales of a row matrix: [ceil(cols / 128), rows] with a pitch of whole 16 bytes."""
+    return torch.empty((cols + 127) // 128, (rows + 3) // 4 * 4, dtype=torch.float32, device=device)[:, :rows]
+
+
+def _row_scale_pitch(s: torch.Tensor, rows: int, cols: int, what: str) -> int:
+    ld = _matrix(s, torch.float32, what, ((cols + 127) // 128, rows))
+    return ld if s.shape[0] > 1 else (rows + 3) // 4 * 4  # a single group's pitch is never stepped over
+
+
+def cb_quantize(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = None,
+                scales: Optional[torch.Tensor] = None, stream=None):
+    """(codes e4m3 [rows, cols], fp32 scales) of x [rows, cols]: a row matrix (block_rows 1, scales
+    [ceil(cols / 128), rows], see row_scales) or a block matrix (128, scales [ceil(rows / 128),
+    ceil(cols / 128)])."""
+    lib = load_library()
+    dt = _dtype_code(x.dtype)
+    ldx = _matrix(x, x.dtype, "x")
+    rows, cols = x.shape
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
+    if block_rows == 1:
+        scales = row_scales(rows, cols, x.device) if scales is None else scales
+        lds = _row_scale_pitch(scales, rows, cols, "scales")
+    else:
+        blocks = ((rows + 127) // 128, (cols + 127) // 128)
+        scales = torch.empty(blocks, dtype=torch.float32, device=x.device) if scales is None else scales
+        lds = _matrix(scales, torch.float32, "scales", blocks)
+    ldc = _matrix(codes, torch.float8_e4m3fn, "codes", (rows, cols))
+    _check(lib.cb_quantize(_ptr(x), ldx, rows, cols, dt, int(block_rows), _ptr(codes), ldc, _ptr(scales), lds,
+                           _stream(stream)))
+    return codes, scales
+
+
+def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                            weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                            residual_out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+                            scales: Optional[torch.Tensor] = None, stream=None):
+    """(codes, scales, residual_out) of the RMS norm of residual + x [rows, d]: the quantised rows
+    (a row matrix) and the sum, written to ``residual_out`` when given (it may be ``residual``)."""
+    lib = load_library()
+    dt = _dtype_code(x.dtype)
+    ldx = _matrix(x, x.dtype, "x")
+    rows, d = x.shape
+    rdt, ldr = dt, 0
+    if residual is not None:
+        rdt, ldr = _dtype_code(residual.dtype), _matrix(residual, residual.dtype, "residual", (rows, d))
+        if residual_out is not None and _matrix(residual_out, residual.dtype, "residual_out", (rows, d)) != ldr:
+            raise CacheBlendError(2, "residual and residual_out must have the same pitch")
+    if weight is not None and (weight.dtype != x.dtype or weight.numel() != d or not weight.is_contiguous()):
+        raise CacheBlendError(2, f"weight must be {d} contiguous elements of {x.dtype}")
+    if codes is None:
+        codes = torch.empty(rows, d, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = row_scales(rows, d, x.device) if scales is None else scales
+    ldc, lds = _matrix(codes, torch.float8_e4m3fn, "codes", (rows, d)), _row_scale_pitch(scales, rows, d, "scales")
+    _check(lib.cb_add_rmsnorm_quantize(_ptr(x), ldx, dt, _ptr(residual), _ptr(residual_out), ldr, rdt, _ptr(weight), rows,
+                                       d, float(eps), _ptr(codes), ldc, _ptr(scales), lds, _stream(stream)))
+    return codes, scales, residual_out
+
+
+def _block_mat(codes: torch.Tensor, scales: torch.Tensor, what: str) -> Fp8Mat:
+    n, k = codes.shape
+    ld = _matrix(codes, torch.float8_e4m3fn, what)
+    lds = _matrix(scales, torch.float32, what + "_scales", ((n + 127) // 128, (k + 127) // 128))
+    return Fp8Mat(codes.data_ptr(), ld, scales.data_ptr(), lds)
+
+
+def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_scales: torch.Tensor,
+                   C_out: torch.Tensor, epilogue: int = CB_FP8_STORE_F32, B2: Optional[torch.Tensor] = None,
+                   B2_scales: Optional[torch.Tensor] = None, addend: Optional[torch.Tensor] = None,
+                   C_scales: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """C = A . B^T of a row matrix A [M, K] and a block matrix B [N, K] (cb_quantize): fp32
+    (CB_FP8_STORE_F32), addend + A . B^T in fp32 (CB_FP8_ADD_F32, ``addend`` may be ``C_out``), bf16
+    (CB_FP8_STORE_BF16), or with gate rows B and up rows B2 the quantised SiLU(A B^T) * (A B2^T) as a
+    row matrix C_out, C_scales (CB_FP8_SWIGLU_FP8)."""
+    lib = load_library()
+    M, K = A.shape
+    width = B.shape[0]
+    swiglu = epilogue == CB_FP8_SWIGLU_FP8
+    if B.shape[1] != K or (swiglu and (B2 is None or B2_scales is None or C_scales is None or B2.shape != B.shape)):
+        raise CacheBlendError(2, "operands do not fit each other")
+    a = Fp8Mat(A.data_ptr(), _matrix(A, torch.float8_e4m3fn, "A"), A_scales.data_ptr(),
+               _row_scale_pitch(A_scales, M, K, "A_scales"))
+    b = _block_mat(B, B_scales, "B")
+    b2 = _block_mat(B2, B2_scales, "B2") if swiglu else None
+    out = torch.float8_e4m3fn if swiglu else torch.bfloat16 if epilogue == CB_FP8_STORE_BF16 else torch.float32
+    ldc = _matrix(C_out, out, "C_out", (M, width))
+    if epilogue == CB_FP8_ADD_F32 and (addend is None or _matrix(addend, torch.float32, "addend", (M, width)) != ldc):
+        raise CacheBlendError(2, "addend must have C_out's pitch")
+    lds = _row_scale_pitch(C_scales, M, width, "C_scales") if swiglu else 0
+    _check(lib.cb_gemm_scaled(C.byref(a), C.byref(b), C.byref(b2) if swiglu else None, _ptr(addend), _ptr(C_out), ldc,
+                              _ptr(C_scales) if swiglu else None, lds, M, width * 2 if swiglu else width, K,
+                              int(epilogue), _stream(stream)))
+    return C_out
 
 
 def cb_chunk_hash(ids) -> int:

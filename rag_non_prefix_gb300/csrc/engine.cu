@@ -1341,6 +1341,101 @@ cb_status cb_gemm(const void* A, const void* B, const void* B2, void* C, int M, 
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_gemm");
 }
 
+// Row-major matrix arguments of the 8-bit calls: 16-byte aligned base, pitch of whole 16 bytes.
+static bool bad_mat(const void* p, long long ld, long long cols, int elem) {
+  return !aligned16(p) || ld < cols || (ld * elem) % 16 != 0;
+}
+static bool bad_row_scales(const float* s, long long ld, int rows) {
+  return !aligned16(s) || ld < rows || ld % 4 != 0;
+}
+static const char* const kFp8Layout =
+    "needs 16-byte aligned matrices and row scales, pitches that hold a row and are multiples of 16 bytes";
+
+cb_status cb_quantize(const void* x, long long ldx, int rows, int cols, cb_dtype dtype, int block_rows,
+                          void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream) {
+  if (rows < 0 || cols < 1 || cols % 16) return fail(nullptr, CB_ERR_SHAPE, "cols must be a positive multiple of 16");
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
+  if (block_rows != 1 && block_rows != 128) return fail(nullptr, CB_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+  if (rows == 0) return CB_OK;
+  if (!x || !codes || !scales) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  if (bad_mat(x, ldx, cols, dtype == CB_BF16 ? 2 : 4) || bad_mat(codes, ld_codes, cols, 1) ||
+      (block_rows == 1 ? bad_row_scales(scales, ld_scales, rows)
+                       : (reinterpret_cast<uintptr_t>(scales) & 3) || ld_scales < (cols + 127) / 128))
+    return fail(nullptr, CB_ERR_SHAPE, std::string("cb_quantize ") + kFp8Layout);
+  cudaError_t e = launch_fp8_quantize(x, ldx, rows, cols, dtype, block_rows, codes, ld_codes, scales, ld_scales,
+                                      as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_quantize");
+}
+
+cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype, const void* residual, void* residual_out,
+                             long long ld_res, cb_dtype res_dtype, const void* weight, int rows, int d, float eps,
+                             void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream) {
+  if (rows < 0 || d < 1 || d % 16 || d > 32768)
+    return fail(nullptr, CB_ERR_SHAPE, "d must be a multiple of 16 up to 32768");
+  if ((x_dtype != CB_F32 && x_dtype != CB_BF16) || (res_dtype != CB_F32 && res_dtype != CB_BF16))
+    return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
+  if (!(eps >= 0.f)) return fail(nullptr, CB_ERR_INVALID_ARG, "eps must not be negative");
+  if (residual_out && !residual) return fail(nullptr, CB_ERR_INVALID_ARG, "residual_out needs a residual");
+  if (rows == 0) return CB_OK;
+  if (!x || !codes || !scales) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  const int rb = res_dtype == CB_BF16 ? 2 : 4;
+  if (bad_mat(x, ldx, d, x_dtype == CB_BF16 ? 2 : 4) || bad_mat(codes, ld_codes, d, 1) ||
+      bad_row_scales(scales, ld_scales, rows) || (weight && !aligned16(weight)) ||
+      (residual && bad_mat(residual, ld_res, d, rb)) || (residual_out && !aligned16(residual_out)))
+    return fail(nullptr, CB_ERR_SHAPE, std::string("cb_add_rmsnorm_quantize ") + kFp8Layout);
+  cudaError_t e = launch_add_rmsnorm_fp8(x, ldx, x_dtype, residual, residual_out, ld_res, res_dtype, weight, rows, d,
+                                         eps, codes, ld_codes, scales, ld_scales, as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_add_rmsnorm_quantize");
+}
+
+cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_mat* B2, const float* addend, void* C,
+                      long long ldc, float* c_scales, long long ld_cs, int M, int N, int K, int epilogue,
+                      void* stream) {
+  if (epilogue < 0 || epilogue > CB_FP8_STORE_BF16) return fail(nullptr, CB_ERR_INVALID_ARG, "bad epilogue");
+  const bool swiglu = epilogue == CB_FP8_SWIGLU_FP8;
+  if (M < 0 || N < 1 || K < 1 || K % 16) return fail(nullptr, CB_ERR_SHAPE, "K must be a positive multiple of 16");
+  if (swiglu && N % 32) return fail(nullptr, CB_ERR_SHAPE, "N / 2 must be a multiple of 16");
+  if (M == 0) return CB_OK;
+  if (!A || !B || !C || !A->codes || !A->scales || !B->codes || !B->scales ||
+      (swiglu && (!B2 || !B2->codes || !B2->scales || !c_scales)) || (epilogue == CB_FP8_ADD_F32 && !addend))
+    return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  const int groups = (K + 127) / 128, width = swiglu ? N / 2 : N;
+  auto bad_blocks = [&](const cb_fp8_mat* m) {
+    return bad_mat(m->codes, m->ld, K, 1) || (reinterpret_cast<uintptr_t>(m->scales) & 3) || m->ld_scales < groups;
+  };
+  if (bad_mat(A->codes, A->ld, K, 1) || bad_row_scales(A->scales, A->ld_scales, M) || bad_blocks(B) ||
+      (swiglu && (bad_blocks(B2) || bad_row_scales(c_scales, ld_cs, M))) ||
+      bad_mat(C, ldc, width, swiglu ? 1 : epilogue == CB_FP8_STORE_BF16 ? 2 : 4) ||
+      (epilogue == CB_FP8_ADD_F32 && !aligned16(addend)))
+    return fail(nullptr, CB_ERR_SHAPE, std::string("cb_gemm_scaled ") + kFp8Layout);
+  Fp8Gemm p{};
+  p.a = static_cast<const uint8_t*>(A->codes);
+  p.lda = A->ld;
+  p.a_scale = A->scales;
+  p.ld_as = A->ld_scales;
+  p.b = static_cast<const uint8_t*>(B->codes);
+  p.ldb = B->ld;
+  p.b_scale = B->scales;
+  p.ld_bs = B->ld_scales;
+  const cb_fp8_mat* b2 = swiglu ? B2 : B;
+  p.b2 = static_cast<const uint8_t*>(b2->codes);
+  p.ldb2 = b2->ld;
+  p.b2_scale = b2->scales;
+  p.ld_b2s = b2->ld_scales;
+  p.addend = addend;
+  p.c = C;
+  p.ldc = ldc;
+  p.c_scale = c_scales;
+  p.ld_cs = ld_cs;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.epilogue = epilogue;
+  cudaError_t e = standalone_gemm_status(&p.status);  // device-side problems go to the standalone GEMM status word
+  if (e == cudaSuccess) e = launch_gemm_fp8(p, as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_gemm_scaled");
+}
+
 size_t cb_gemm_scratch_size(void) { return gemm_scratch_bytes(); }
 
 cb_status cb_set_launch_overlap(int enabled) {

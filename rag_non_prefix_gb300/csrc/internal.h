@@ -270,4 +270,28 @@ bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uin
 bool encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
                          uint32_t box_rows);
 
+
+// e4m3 codes with fp32 scales (cb_quantize): the largest code value, and the smallest
+// largest magnitude of a group that its scale stands for.
+constexpr float FP8_MAX = 448.0f;
+constexpr float FP8_AMAX_MIN = 448.0f * 1.17549435e-38f;
+cudaError_t launch_fp8_quantize(const void* x, long long ldx, int rows, int cols, cb_dtype dt, int block_rows,
+                                void* codes, long long ldc, float* scales, long long lds, cudaStream_t s);
+cudaError_t launch_add_rmsnorm_fp8(const void* x, long long ldx, cb_dtype xdt, const void* res, void* res_out,
+                                   long long ldr, cb_dtype rdt, const void* weight, int rows, int d, float eps,
+                                   void* codes, long long ldc, float* scales, long long lds, cudaStream_t s);
+// One cb_gemm_scaled call (N counts gate and up for CB_FP8_SWIGLU_FP8).
+struct Fp8Gemm {
+  const uint8_t *a, *b, *b2;
+  const float *a_scale, *b_scale, *b2_scale;
+  long long lda, ldb, ldb2, ld_as, ld_bs, ld_b2s;
+  const float* addend;
+  void* c;
+  float* c_scale;
+  long long ldc, ld_cs;
+  int M, N, K, epilogue;
+  int32_t* status;
+};
+cudaError_t launch_gemm_fp8(const Fp8Gemm& p, cudaStream_t s);
+
 }  // namespace cb
