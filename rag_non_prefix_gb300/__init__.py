@@ -29,7 +29,8 @@ EXPORTED = ("cb_create", "cb_destroy", "cb_status_string", "cb_last_error", "cb_
             "cb_get_profile", "cb_get_layer_profile", "cb_gemm_noalloc", "cb_gemm_noalloc_error", "cb_gemm_noalloc_scratch_used", "cb_gemm_get_status", "cb_gemm_set_orientation", "cb_gemm_set_pairing", "cb_gemm_describe", "cb_attention_set_tiles", "cb_set_qkv_fusion",
             "cb_set_launch_overlap", "cb_codec_layer_bytes", "cb_kv_encode", "cb_kv_decode", "cb_register_chunk_codec",
             "cb_set_staging", "cb_chunk_hash", "cb_chunk_info_of", "cb_plan_loading", "cb_decode_step",
-            "cb_ratio_schedule", "cb_k_for_ratio", "cb_quantize", "cb_add_rmsnorm_quantize", "cb_gemm_scaled")
+            "cb_ratio_schedule", "cb_k_for_ratio", "cb_quantize", "cb_add_rmsnorm_quantize", "cb_gemm_scaled",
+            "cb_gemm_scaled_set_plan")
 PHASES = ("begin", "staged_rot", "norm", "qkv", "rope", "deviation", "select", "scatter", "attention", "oproj",
           "gateup", "down", "finish")
 
@@ -142,6 +143,7 @@ def load_library(path: str = LIB_PATH):
                                          C.c_float, vp, C.c_longlong, vp, C.c_longlong, vp]),
         "cb_gemm_scaled": (st, [C.POINTER(Fp8Mat), C.POINTER(Fp8Mat), C.POINTER(Fp8Mat), vp, vp, C.c_longlong, vp,
                                 C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, vp]),
+        "cb_gemm_scaled_set_plan": (st, [C.c_int, C.c_int]),
         "cb_codec_layer_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
         "cb_kv_encode": (st, [vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp]),
         "cb_kv_decode": (st, [vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_double, C.c_int, vp, vp,
@@ -451,6 +453,12 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
                               _ptr(C_scales) if swiglu else None, lds, M, width * 2 if swiglu else width, K,
                               int(epilogue), _stream(stream)))
     return C_out
+
+
+def cb_gemm_scaled_set_plan(tokens: int, split: int) -> None:
+    """Process-wide tiling of cb_gemm_scaled: tokens per tile and pairs that divide the channels
+    (0: output from registers); 0, 0 by the library's time model (tuning and tests)."""
+    _check(load_library().cb_gemm_scaled_set_plan(int(tokens), int(split)))
 
 
 def cb_chunk_hash(ids) -> int:

@@ -1436,6 +1436,11 @@ cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_gemm_scaled");
 }
 
+cb_status cb_gemm_scaled_set_plan(int tokens, int split) {
+  if (!gemm_fp8_set_plan(tokens, split)) return fail(nullptr, CB_ERR_INVALID_ARG, "no such plan");
+  return CB_OK;
+}
+
 size_t cb_gemm_scratch_size(void) { return gemm_scratch_bytes(); }
 
 cb_status cb_set_launch_overlap(int enabled) {

@@ -227,6 +227,60 @@ def test_gemm_of_any_number_of_features(m, width, epi):
     assert untouched(whole, m, width)
 
 
+PLANS = [(16, 1), (16, 2), (16, 4), (32, 1), (32, 4), (64, 1), (64, 2), (128, 1), (128, 2), (128, 4), (128, 0), (192, 0),
+         (256, 0)]
+
+
+@pytest.fixture(params=PLANS)
+def plan(request):
+    cb.cb_gemm_scaled_set_plan(*request.param)
+    yield request.param
+    cb.cb_gemm_scaled_set_plan(0, 0)
+
+
+@pytest.mark.parametrize("epi", [F32, ADD, SWIGLU, BF16])
+@pytest.mark.parametrize("m,width,k", [(1, 144, 16), (70, 400, 144), (300, 528, 1168), (261, 5008, 656)])
+def test_every_plan_matches_definition(plan, m, width, k, epi):
+    """Each tiling, with few and many tiles per CTA, odd tails and fewer groups than pairs."""
+    o, whole, csw = operands(m, width, k, epi, seed=m, extra=1)
+    gemm(o, epi)
+    check_gemm(o["a"], o["sa"], o["b"], o["sb"], epi, o["c"], o["addend"], o["b2"], o["sb2"], o["c_scales"])
+    assert untouched(whole, m, width)
+    if epi == SWIGLU:
+        assert untouched(csw, -(-width // 128), m)
+    first = o["c"].clone()
+    gemm(o, epi)
+    assert torch.equal(first.view(torch.uint8), o["c"].view(torch.uint8))
+    if epi == ADD:
+        o["c"].copy_(o["addend"])
+        o["addend"] = o["c"]
+        gemm(o, ADD)
+        assert torch.equal(first, o["c"])
+    cb.cb_gemm_get_status()
+
+
+@pytest.mark.parametrize("epi", [F32, ADD, BF16])
+def test_every_plan_with_ragged_rows(plan, epi):
+    o, whole, _ = operands(41, 301, 272, epi, seed=3)
+    gemm(o, epi)
+    check_gemm(o["a"], o["sa"], o["b"], o["sb"], epi, o["c"], o["addend"])
+    assert untouched(whole, 41, 301)
+
+
+@pytest.mark.parametrize("layout", ["gate first", "up first", "own pitches"])
+def test_every_plan_with_gate_and_up_anywhere(plan, layout):
+    """Gate and up rows in either order in memory, and in matrices of different pitches."""
+    o, _, _ = operands(40, 272, 400, SWIGLU, seed=4)
+    room = torch.zeros(2, 272, 512, dtype=torch.uint8, device="cuda").view(E4M3)
+    gate, up = (room[0], room[1]) if layout == "gate first" else (room[1], room[0])
+    if layout == "own pitches":
+        up = torch.zeros(272, 416, dtype=torch.uint8, device="cuda").view(E4M3)
+    gate[:, :400].copy_(o["b"]), up[:, :400].copy_(o["b2"])
+    o["b"], o["b2"] = gate[:, :400], up[:, :400]
+    gemm(o, SWIGLU)
+    check_gemm(o["a"], o["sa"], o["b"], o["sb"], SWIGLU, o["c"], None, o["b2"], o["sb2"], o["c_scales"])
+
+
 @pytest.mark.parametrize("m,width,k", [(4, 512, 4096), (90, 640, 1040), (600, 512, 528)])
 def test_gemm_adds_in_place_and_repeats(m, width, k):
     o, _, _ = operands(m, width, k, ADD)
