@@ -60,23 +60,6 @@ bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uin
   return r == CUDA_SUCCESS;
 }
 
-// the same for rank dimensions: dims [rank], strides [rank - 1] in bytes, box [rank]
-bool encode_tmap_nd(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
-                    const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz) {
-  EncodeTiledFn fn = get_encoder();
-  if (!fn || rank < 2 || rank > 5) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], estr[5];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-    estr[i] = 1;
-    if (i + 1 < rank) st[i] = strides[i];
-  }
-  return fn(map, dt, rank, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 static bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
                            uint64_t pitch, uint32_t box_inner, uint32_t box_rows,
                            CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {

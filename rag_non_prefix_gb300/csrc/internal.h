@@ -267,8 +267,6 @@ int gemm_pairing();
 // tensor-map encoder (driver entry point, resolved once)
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
                  uint64_t pitch, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
-bool encode_tmap_nd(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
-                    const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz);
 bool encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
                          uint32_t box_rows);
 

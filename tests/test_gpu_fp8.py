@@ -227,8 +227,7 @@ def test_gemm_of_any_number_of_features(m, width, epi):
     assert untouched(whole, m, width)
 
 
-PLANS = [(16, 1), (16, 2), (16, 4), (32, 1), (32, 4), (64, 1), (64, 2), (128, 1), (128, 2), (128, 4), (128, 0), (192, 0),
-         (256, 0)]
+PLANS = [(16, 1), (16, 2), (16, 4), (32, 1), (32, 4), (64, 1), (64, 2), (128, 1), (128, 2), (128, 4), (256, 1)]
 
 
 @pytest.fixture(params=PLANS)
