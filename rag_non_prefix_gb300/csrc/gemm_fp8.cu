@@ -38,12 +38,11 @@ constexpr int ROWS = 128;                  // rows of the tensor core's tile per
 constexpr int A_BYTES = ROWS * 128;        // 16 KiB: 128 rows x one group of channels
 constexpr int MAX_STAGES = 12;
 constexpr int RAW_SLOTS = 4;               // token scales of a group as loaded: slots of 128 floats
-constexpr int SC_SLOTS = 4;                // times the weight blocks' scales: slots of two lists of factors
-constexpr int FACTORS = 2 * 4 * 20;        // one list: 128 tokens, or two warpgroups x four thread classes x (16 + 4)
+constexpr int FACTORS = 2 * 4 * 20;        // token times block scales: 128 tokens, or two warpgroups x four thread classes x (16 + 4)
+constexpr int FACTOR_BYTES = 2 * FACTORS * 4;  // a stage's two lists (two weight blocks)
 constexpr int OFF_RAW = 1024;              // after the barriers
-constexpr int OFF_SC = OFF_RAW + RAW_SLOTS * 512;
-constexpr int OFF_AMAX = OFF_SC + SC_SLOTS * 2 * FACTORS * 4;  // 512 words for the epilogue
-constexpr int OFF_RING = (OFF_AMAX + 2048 + 1023) / 1024 * 1024;
+constexpr int OFF_AMAX = OFF_RAW + RAW_SLOTS * 512;  // 512 words for the epilogue
+constexpr int OFF_SC = OFF_AMAX + 2048;    // factors of every stage, then the ring
 constexpr int SMEM_ALLOC = 232448;         // the per-block maximum (227 KiB), 1 KiB of it aligns the base
 constexpr int SMEM_USE = SMEM_ALLOC - 1024;
 constexpr uint32_t TMEM_COLS = 512;
@@ -51,7 +50,7 @@ constexpr int PART_PITCH = ROWS + 4;       // floats per token of a CTA's partia
 constexpr int SLAB = 2048;                 // many tokens: a warp stages 32 tokens x 64 bytes, twice
 
 // Accumulators in tensor memory: as many groups' sums as fit may wait to be read.
-__host__ __device__ constexpr int n_acc(int columns) { return columns <= 64 ? 8 : columns <= 128 ? 4 : 2; }
+__host__ __device__ constexpr int n_acc(int columns) { return columns <= 128 ? 4 : 2; }
 
 struct Params {
   Fp8Gemm g;
@@ -60,7 +59,7 @@ struct Params {
   int split;        // pairs per cluster, each taking a part of the groups
   int groups;       // ceil(K / 128)
   int stages, stage_bytes;
-  int out_off;      // output area after the ring
+  int ring_off, out_off;  // codes of the stages; output area
   int add_in_place;
   int ragged;       // output rows end inside 16 bytes: a TMA store would write up to the 16th
 };
@@ -203,35 +202,28 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if ((it & 255u) == 255u && (*abort || global_ns() - t0 > 2000000000ull)) return false;
   }
 }
-// Arrival on another CTA's barrier that orders no memory access: what it announces is that tensor
-// memory was read (tcgen05.wait::ld and the tcgen05 fence order that).  With release at cluster
-// scope the same arrival took ~1200 cycles.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// Whether the phase has completed, without waiting: polled ahead of the work that hides its latency.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
+// Arrival of one lane (el) on a barrier of the cluster that orders no memory access.  It announces
+// that tensor memory was read (tcgen05.wait::ld and the tcgen05 fence order that), or follows a fence
+// of its own.  With release at cluster scope the same arrival took ~1200 cycles.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr, uint32_t el) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+      "r"(el)
       : "memory");
-  return ok != 0;
 }
+__device__ __forceinline__ void fence_cta() { asm volatile("fence.acq_rel.cta;" ::: "memory"); }
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
 
 struct Bars {
-  uint64_t full[MAX_STAGES];      // codes of a stage have landed (even CTAs)
+  uint64_t full[MAX_STAGES];      // codes of a stage have landed and both CTAs' factors are written (even CTAs)
   uint64_t done[MAX_STAGES];      // its MMAs are done: the stage is free and the group's sums are readable
-  uint64_t acc_empty[8];          // both CTAs' warps have read an accumulator (even CTAs)
+  uint64_t acc_empty[4];          // both CTAs' warps have read an accumulator (even CTAs)
   uint64_t raw_full[RAW_SLOTS], raw_empty[RAW_SLOTS];
-  uint64_t sc_full[SC_SLOTS], sc_empty[SC_SLOTS];
   uint64_t part_full, part_free;  // few tokens: the cluster's parts are written / read
   uint64_t drain;
   uint32_t tmem_slot;
@@ -241,17 +233,13 @@ static_assert(sizeof(Bars) <= OFF_RAW, "barriers overrun their area");
 
 __device__ __forceinline__ void init_bars(Bars& bars, int split) {
   for (int s = 0; s < MAX_STAGES; ++s) {
-    mbar_init(&bars.full[s], 1);
+    mbar_init(&bars.full[s], 3);  // the producer of codes, the factor warps of both CTAs
     mbar_init(&bars.done[s], 1);
   }
-  for (int b = 0; b < 8; ++b) mbar_init(&bars.acc_empty[b], 16);  // eight warps of both CTAs
+  for (int b = 0; b < 4; ++b) mbar_init(&bars.acc_empty[b], 16);  // eight warps of both CTAs
   for (int s = 0; s < RAW_SLOTS; ++s) {
     mbar_init(&bars.raw_full[s], 1);
     mbar_init(&bars.raw_empty[s], 1);
-  }
-  for (int s = 0; s < SC_SLOTS; ++s) {
-    mbar_init(&bars.sc_full[s], 1);
-    mbar_init(&bars.sc_empty[s], 8);
   }
   mbar_init(&bars.part_full, 16 * split);
   mbar_init(&bars.part_free, 16 * split);
@@ -287,18 +275,22 @@ __device__ __forceinline__ void issue_mmas(Bars& bars, const Params& p, uint8_t*
   const uint32_t ring_u32 = smem_u32(ring), stages = static_cast<uint32_t>(p.stages);
   const uint32_t el = elect_one();
   uint32_t s = 0, ph = 0, sa = ring_u32, b = 0, aph = 1;
-  bool ok = true, full_ready = false, acc_ready = false;  // polled during the previous group's MMAs
+  bool ok = true;
   for (int u = cid; ok && u < p.units; u += NC) {
     for (int g = 0; g < n_groups; ++g) {
-      if ((!acc_ready && !mbar_wait_bounded(&bars.acc_empty[b], aph, abort)) ||
-          (!full_ready && !mbar_wait_bounded(&bars.full[s], ph, abort))) {
+      // (the accumulator last: it is what the MMAs wait for, and each poll costs ~110 cycles)
+      if (!mbar_wait_bounded(&bars.full[s], ph, abort) || !mbar_wait_bounded(&bars.acc_empty[b], aph, abort)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint64_t* done = &bars.done[s];
       const uint64_t da = sw128_desc(sa), db = sw128_desc(sa + A_BYTES);
       const uint32_t tacc = tmem + b * ACC_STRIDE;
+      mma_f8_pair(tacc, da, db, idesc, 0u, el);
+      mma_f8_pair(tacc, da + 2, db + 2, idesc, 1u, el);  // + 32 bytes along K (encoded >> 4)
+      mma_f8_pair(tacc, da + 4, db + 4, idesc, 1u, el);
+      mma_f8_pair(tacc, da + 6, db + 6, idesc, 1u, el);
+      commit_pair_mc_elected(&bars.done[s], pair_mask, el);
       sa += static_cast<uint32_t>(p.stage_bytes);
       if (++s == stages) {
         s = 0;
@@ -309,13 +301,6 @@ __device__ __forceinline__ void issue_mmas(Bars& bars, const Params& p, uint8_t*
         b = 0;
         aph ^= 1u;
       }
-      full_ready = mbar_test(&bars.full[s], ph);
-      acc_ready = mbar_test(&bars.acc_empty[b], aph);
-      mma_f8_pair(tacc, da, db, idesc, 0u, el);
-      mma_f8_pair(tacc, da + 2, db + 2, idesc, 1u, el);  // + 32 bytes along K (encoded >> 4)
-      mma_f8_pair(tacc, da + 4, db + 4, idesc, 1u, el);
-      mma_f8_pair(tacc, da + 6, db + 6, idesc, 1u, el);
-      commit_pair_mc_elected(done, pair_mask, el);
     }
   }
   if (!ok && lane == 0) report_timeout(bars, p.g.status);
@@ -346,11 +331,17 @@ __device__ __forceinline__ void load_scales(Bars& bars, const Params& p, const C
 }
 
 // The factors of a group (a whole warp): token scales times the scales of two weight blocks, sb0 and
-// sb1 of a unit's weight tile; `put` stores token t's two factors into the slot.
-template <int TOKENS, typename Blocks, typename Put>
-__device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const float* raw, float* sc, int g0, int g1,
-                                                int cid, int NC, int lane, Blocks blocks, Put put) {
-  Pos r, s;
+// sb1 of a unit's weight tile; `put` stores token t's two factors into the stage's lists.  A list is
+// free once every reader has read an accumulator n_acc groups further on, which that group's MMAs
+// waited for: when the group stages - n_acc before this one is done.
+template <int TOKENS, int COLUMNS, typename Blocks, typename Put>
+__device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const float* raw, uint8_t* sc, int g0,
+                                                int g1, int cid, int NC, int lane, uint32_t lead, Blocks blocks,
+                                                Put put) {
+  const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(COLUMNS);
+  const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead), el = lane == 0;
+  Pos r, s, done;
+  uint32_t n = 0;
   bool ok = true;
   for (int u = cid; ok && u < p.units; u += NC) {
     const float *sb0, *sb1;
@@ -362,38 +353,43 @@ __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, con
         b0 = __ldg(sb0 + g + lane);
         b1 = __ldg(sb1 + g + lane);
       }
-      ok = mbar_wait_bounded(&bars.raw_full[r.i], r.ph, &bars.abort) &&
-           mbar_wait_bounded(&bars.sc_empty[s.i], s.ph ^ 1u, &bars.abort);
+      ok = mbar_wait_bounded(&bars.raw_full[r.i], r.ph, &bars.abort);
+      if (n >= ahead) {
+        ok = ok && mbar_wait_bounded(&bars.done[done.i], done.ph, &bars.abort);
+        done.next(stages);
+      } else {
+        ++n;
+      }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const float f0 = __shfl_sync(0xffffffffu, b0, i), f1 = __shfl_sync(0xffffffffu, b1, i);
 #pragma unroll
       for (int t = lane; t < TOKENS; t += 32) {
         const float v = raw[r.i * 128 + t];
-        put(sc + s.i * (2 * FACTORS), t, v * f0, v * f1);
+        put(reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES), t, v * f0, v * f1);
       }
+      fence_cta();  // the factors are read in this CTA only
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars.raw_empty[r.i]);
-        mbar_arrive(&bars.sc_full[s.i]);
-      }
+      if (lane == 0) mbar_arrive(&bars.raw_empty[r.i]);
+      mbar_arrive_cluster_relaxed(full_lead + s.i * 8, el);
       r.next(RAW_SLOTS);
-      s.next(SC_SLOTS);
+      s.next(stages);
     }
   }
   if (!ok && lane == 0) report_timeout(bars, p.g.status);
 }
 
 // What every thread does last.
-__device__ __forceinline__ void finish(Bars& bars, const Params& p, uint32_t tmem, int warp) {
+__device__ __forceinline__ void finish(Bars& bars, uint32_t tmem, int warp) {
   tc_fence_before();
   __syncthreads();
   // No CTA leaves, or frees the pair's tensor memory, while another may still reach its barriers or
   // shared memory: every issuer has drained its MMAs, every producer and epilogue has finished.
   cluster_sync_all();
-  // After a timeout anywhere in the cluster, copies issued for stages that were never consumed may
-  // still be in flight: give them time to land before the memory is released.
-  if (bars.abort || (p.g.status != nullptr && (*reinterpret_cast<volatile int32_t*>(p.g.status) & ST_WAIT_TIMEOUT))) {
+  // After a timeout copies issued for stages that were never consumed may still be in flight to this
+  // CTA: give them time to land before the memory is released.  (Its own flag says so: where a stage
+  // was not consumed, its readers gave up too.)
+  if (*const_cast<volatile int*>(&bars.abort)) {
     const uint64_t t0 = global_ns();
     while (global_ns() - t0 < 200000ull) {
     }
@@ -414,19 +410,20 @@ __device__ __forceinline__ void many_registers() { asm volatile("setmaxnreg.inc.
 // features 128 w .. of the tile's 256 (SwiGLU: gate and up of features 64 w .. of 128; the pair's
 // even CTA stages the gate rows, the odd one the up rows).  Output goes through slabs of 32 tokens
 // x 64 bytes per warp, stored by TMA.
-template <bool SWIGLU>
+template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_tokens_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                            const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmS,
                            const __grid_constant__ CUtensorMap tmC, const Params p) {
   constexpr uint32_t ACC_STRIDE = 256;
+  constexpr bool SWIGLU = EPI == CB_FP8_SWIGLU_FP8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem);
   float* raw = reinterpret_cast<float*>(smem + OFF_RAW);
-  float* sc = reinterpret_cast<float*>(smem + OFF_SC);
+  uint8_t* sc = smem + OFF_SC;
   uint32_t* amax = reinterpret_cast<uint32_t*>(smem + OFF_AMAX);  // [2][2][128]
-  uint8_t* ring = smem + OFF_RING;
+  uint8_t* ring = smem + p.ring_off;
   volatile int* abort = &bars.abort;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -482,8 +479,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2 && lane == 0) {
       load_scales<256, 128>(bars, p, &tmS, raw, 0, G, cid, NC, h * 128);
     } else if (warp == 3) {
-      multiply_scales<128>(
-          bars, p, raw, sc, 0, G, cid, NC, lane,
+      multiply_scales<128, 256>(
+          bars, p, raw, sc, 0, G, cid, NC, lane, 0,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // features past the last block are zeros: any block's scale will do
             const int last = (p.width - 1) >> 7;
@@ -508,7 +505,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       return static_cast<uint32_t>(SWIGLU ? (c >> 1) * 128 + w * 64 + (c & 1) * 32 : w * 128 + c * 32);
     };
     uint8_t* mine = smem + p.out_off + (warp - 4) * 2 * SLAB;
-    Pos sl, st;
+    const uint32_t el = lane == 0;
+    Pos st;
     uint32_t b = 0, slab_no = 0;
     bool ok = true;
     int nth = 0;
@@ -523,10 +521,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // Two register buffers: the next read of tensor memory, which may be the next group's first,
       // runs under the sums of the current one.
       uint32_t v[2][32];
-      bool sc_ready = false, acc_ready = false;
-      auto begin = [&]() {  // the group's sums and factors are there: start its first read
-        if (ok && !((sc_ready || mbar_wait_bounded(&bars.sc_full[sl.i], sl.ph, abort)) &&
-                    (acc_ready || mbar_wait_bounded(&bars.done[st.i], st.ph, abort)))) {
+      auto begin = [&]() {  // the group's sums (and its factors) are there: start its first read
+        if (ok && !mbar_wait_bounded(&bars.done[st.i], st.ph, abort)) {
           ok = false;
           report_timeout(bars, p.g.status);
         }
@@ -538,10 +534,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
       for (int g = 0; g < G; ++g) {
         const uint32_t tacc = tmem + b * ACC_STRIDE + lane_base;
-        const float* f = sc + sl.i * (2 * FACTORS) + row;
+        const float* f = reinterpret_cast<const float*>(sc + st.i * FACTOR_BYTES) + row;
         const float fa = f[SWIGLU ? 0 : w * FACTORS], fb = SWIGLU ? f[FACTORS] : fa;
         const uint64_t m0 = pack2(fa, fa), m1 = SWIGLU ? pack2(fb, fb) : m0;
-        uint64_t* sc_empty = &bars.sc_empty[sl.i];
         auto sums = [&](int c) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -554,21 +549,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld32x32(tacc + column(c + 1), v[(c + 1) & 1]);
           } else {
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8);
-              mbar_arrive(sc_empty);
-            }
+            mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8, el);
             b ^= 1u;
             st.next(stages);
-            sl.next(SC_SLOTS);
-            if (g + 1 < G) {
-              sc_ready = mbar_test(&bars.sc_full[sl.i], sl.ph);
-              acc_ready = mbar_test(&bars.done[st.i], st.ph);
-              begin();
-            }
+            sums(c);
+            if (g + 1 < G) begin();
           }
-          sums(c);
+          if (c < 3) sums(c);
         }
       }
 
@@ -585,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && ok) {
-          if (p.add_in_place)
+          if (EPI == CB_FP8_ADD_F32 && p.add_in_place)
             tma_reduce_add_2d(&tmC, slab, f, t0);
           else
             tma_store_2d(&tmC, slab, f, t0);
@@ -626,8 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           put(q, f);
         }
       } else {
-        const bool to_bf16 = p.g.epilogue == CB_FP8_STORE_BF16;
-        const bool add = p.g.epilogue == CB_FP8_ADD_F32;
+        constexpr bool to_bf16 = EPI == CB_FP8_STORE_BF16, add = EPI == CB_FP8_ADD_F32;
         const int tok = t0 + lane;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -688,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     bulk_wait_all();
   }
-  finish(bars, p, tmem, warp);
+  finish(bars, tmem, warp);
 }
 
 // ============================================================================= few tokens
@@ -709,9 +695,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem);
   float* raw = reinterpret_cast<float*>(smem + OFF_RAW);
-  float* sc = reinterpret_cast<float*>(smem + OFF_SC);
+  uint8_t* sc = smem + OFF_SC;
   uint32_t* amax = reinterpret_cast<uint32_t*>(smem + OFF_AMAX);
-  uint8_t* ring = smem + OFF_RING;
+  uint8_t* ring = smem + p.ring_off;
   volatile int* abort = &bars.abort;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -772,8 +758,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2 && lane == 0) {
       load_scales<BT, BT>(bars, p, &tmS, raw, g0, g1, cid, NC, 0);
     } else if (warp == 3) {
-      multiply_scales<BT>(
-          bars, p, raw, sc, g0, g1, cid, NC, lane,
+      multiply_scales<BT, BT>(
+          bars, p, raw, sc, g0, g1, cid, NC, lane, lead,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // rows past the last block are zeros: any block's scale will do
             const int blk = SWIGLU ? wt : min(wt * 2 + h, (p.width - 1) >> 7);
@@ -801,7 +787,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t part_u32 = smem_u32(part);
     const int CS = 2 * p.split;
     const int per = (BT + CS - 1) / CS;  // tokens that each CTA of the cluster finishes
-    Pos sl, st;
+    const uint32_t el = lane == 0;
+    Pos st;
     uint32_t b = 0;
     bool ok = true;
     int nth = 0;
@@ -818,11 +805,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][r] = 0;
       uint32_t lo[2][CH / 2], hi[2][CH / 2];  // two buffers, as above
-      bool sc_ready = false, acc_ready = false;
       auto begin = [&]() {
-        if (ok && !((sc_ready || mbar_wait_bounded(&bars.sc_full[sl.i], sl.ph, abort)) &&
-                    (acc_ready || mbar_wait_bounded(&bars.done[st.i], st.ph, abort))))
-          give_up();
+        if (ok && !mbar_wait_bounded(&bars.done[st.i], st.ph, abort)) give_up();
         __syncwarp();
         tc_fence_after();
         const uint32_t tacc = tmem + b * ACC_STRIDE + lane_base + static_cast<uint32_t>(w * HB);
@@ -833,9 +817,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
       for (int g = g0; g < g1; ++g) {
         const uint32_t tacc = tmem + b * ACC_STRIDE + lane_base + static_cast<uint32_t>(w * HB);
-        const float* sv = sc + sl.i * (2 * FACTORS) + (SWIGLU && quarter >= 2 ? FACTORS : 0) + w * (FACTORS / 2) +
-                          (lane & 3) * 20;
-        uint64_t* sc_empty = &bars.sc_empty[sl.i];
+        const float* sv = reinterpret_cast<const float*>(sc + st.i * FACTOR_BYTES) +
+                          (SWIGLU && quarter >= 2 ? FACTORS : 0) + w * (FACTORS / 2) + (lane & 3) * 20;
         uint64_t f[CH / 8];
         auto sums = [&](int c) {
           const int i = c & 1;
@@ -860,22 +843,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             sums(c);
           } else {
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8);
+            mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8, el);
             if (++b == NACC) b = 0;
             st.next(stages);
-            sl.next(SC_SLOTS);
             if (NCH % 2) sums(c);
-            if (g + 1 < g1) {
-              sc_ready = mbar_test(&bars.sc_full[sl.i], sl.ph);
-              acc_ready = mbar_test(&bars.done[st.i], st.ph);
-              begin();
-            }
+            if (g + 1 < g1) begin();
             if (NCH % 2 == 0) sums(c);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sc_empty);
       }
 
       // ------------------------------------------------------------------ epilogue
@@ -972,7 +947,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane < CS) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.part_free), lane));
     }
   }
-  finish(bars, p, tmem, warp);
+  finish(bars, tmem, warp);
 }
 
 }  // namespace f8
@@ -986,13 +961,18 @@ typedef void (*Kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, 
                        const Params);
 
 // The kernel for `bt` tokens per tile: 256 has the tokens on the rows.
-Kernel kernel_of(int bt, bool swiglu) {
+Kernel kernel_of(int bt, int epilogue) {
+  const bool swiglu = epilogue == CB_FP8_SWIGLU_FP8;
   switch (bt) {
     case 16: return swiglu ? gemm_fp8_weights_kernel<16, true> : gemm_fp8_weights_kernel<16, false>;
     case 32: return swiglu ? gemm_fp8_weights_kernel<32, true> : gemm_fp8_weights_kernel<32, false>;
     case 64: return swiglu ? gemm_fp8_weights_kernel<64, true> : gemm_fp8_weights_kernel<64, false>;
     case 128: return swiglu ? gemm_fp8_weights_kernel<128, true> : gemm_fp8_weights_kernel<128, false>;
-    case 256: return swiglu ? gemm_fp8_tokens_kernel<true> : gemm_fp8_tokens_kernel<false>;
+    case 256:
+      return swiglu                            ? gemm_fp8_tokens_kernel<CB_FP8_SWIGLU_FP8>
+             : epilogue == CB_FP8_ADD_F32    ? gemm_fp8_tokens_kernel<CB_FP8_ADD_F32>
+             : epilogue == CB_FP8_STORE_BF16 ? gemm_fp8_tokens_kernel<CB_FP8_STORE_BF16>
+                                             : gemm_fp8_tokens_kernel<CB_FP8_STORE_F32>;
     default: return nullptr;
   }
 }
@@ -1007,7 +987,7 @@ int resident_clusters(int cs) {
     const int v = cache[ci][dev].load();
     if (v > 0) return v;
   }
-  const void* fn = reinterpret_cast<const void*>(kernel_of(16, false));
+  const void* fn = reinterpret_cast<const void*>(kernel_of(16, CB_FP8_STORE_F32));
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC) != cudaSuccess) return 0;
   cudaLaunchConfig_t q = {};
   q.gridDim = dim3(cs * 64);
@@ -1032,7 +1012,7 @@ int resident_clusters(int cs) {
 std::atomic<int> g_plan{0};
 
 struct Plan {
-  int bt, split, clusters, stages, stage_bytes, out_off;
+  int bt, split, clusters, stages, stage_bytes, ring_off, out_off;
 };
 
 Plan plan(const Fp8Gemm& g) {
@@ -1057,9 +1037,10 @@ Plan plan(const Fp8Gemm& g) {
       const int stage = A_BYTES + (tokens ? A_BYTES : bt * 64);
       const int out = tokens ? 16 * SLAB : (bt * PART_PITCH * 4 + 1023) / 1024 * 1024;
       best_us = us;
-      // (a stage's barrier is read until its accumulator is: at least n_acc(bt) stages, which all have)
-      best = Plan{bt, split, clusters, std::min(MAX_STAGES, (SMEM_USE - OFF_RING - out) / stage), stage, 0};
-      best.out_off = OFF_RING + best.stages * stage;
+      const int room = SMEM_USE - OFF_SC - 1023 - out;
+      best = Plan{bt, split, clusters, std::min(MAX_STAGES, room / (stage + FACTOR_BYTES)), stage, 0, 0};
+      best.ring_off = (OFF_SC + best.stages * FACTOR_BYTES + 1023) / 1024 * 1024;
+      best.out_off = best.ring_off + best.stages * stage;
     }
   };
   for (int bt : {16, 32, 64, 128})
@@ -1075,7 +1056,7 @@ bool gemm_fp8_set_plan(int tokens, int split) {
     g_plan.store(0);
     return true;
   }
-  if (!kernel_of(tokens, false) || (split != 1 && split != 2 && split != 4) || (tokens == 256 && split != 1)) return false;
+  if (!kernel_of(tokens, CB_FP8_STORE_F32) || (split != 1 && split != 2 && split != 4) || (tokens == 256 && split != 1)) return false;
   g_plan.store(tokens * 8 + split);
   return true;
 }
@@ -1084,7 +1065,8 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.M <= 0) return cudaSuccess;
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8, to_bf16 = g.epilogue == CB_FP8_STORE_BF16;
   const Plan pl = plan(g);
-  if (pl.bt == 0 || pl.stages < n_acc(pl.bt)) return cudaErrorInvalidConfiguration;
+  // (a stage's barrier is read until its accumulator is, and its factors are written ahead)
+  if (pl.bt == 0 || pl.stages <= n_acc(pl.bt)) return cudaErrorInvalidConfiguration;
   const bool tokens = pl.bt == 256;
   Params p{};
   p.g = g;
@@ -1095,6 +1077,7 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   p.groups = (g.K + 127) / 128;
   p.stages = pl.stages;
   p.stage_bytes = pl.stage_bytes;
+  p.ring_off = pl.ring_off;
   p.out_off = pl.out_off;
   p.add_in_place = g.epilogue == CB_FP8_ADD_F32 && g.addend == g.c;
   p.ragged = !swiglu && p.width * (to_bf16 ? 2 : 4) % 16 != 0;
@@ -1114,9 +1097,9 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
                 : to_bf16 ? encode_tmap(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.c, p.width, g.M, g.ldc * 2, 32, 32, SW64)
                           : encode_tmap(&mc, F32, g.c, p.width, g.M, g.ldc * 4, 16, 32, SW64));
   if (!ok) return cudaErrorInvalidValue;
-  Kernel fn = kernel_of(pl.bt, swiglu);
-  static DeviceOnce once[2][17];
-  cudaError_t e = max_dynamic_smem_once(reinterpret_cast<const void*>(fn), SMEM_ALLOC, once[swiglu][pl.bt / 16]);
+  Kernel fn = kernel_of(pl.bt, g.epilogue);
+  static DeviceOnce once[4][17];
+  cudaError_t e = max_dynamic_smem_once(reinterpret_cast<const void*>(fn), SMEM_ALLOC, once[g.epilogue][pl.bt / 16]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pl.split * std::min(pl.clusters, p.units));
