@@ -183,8 +183,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (3 us a call less on the GB300's host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s) -> C.c_void_p:
     if s is None:
+        if _raw_stream is not None:
+            return C.c_void_p(_raw_stream(torch.cuda.current_device()))
         s = torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
 
@@ -347,16 +353,29 @@ def cb_attention(q: torch.Tensor, q_pos: torch.Tensor, k: torch.Tensor, v: torch
     return out
 
 
-def _matrix(t: torch.Tensor, dtype, what: str, shape=None) -> int:
-    """Pitch of a 2-D CUDA matrix argument of the 8-bit calls, after checking it."""
+_E4M3 = torch.float8_e4m3fn
+
+
+def _pitch(t: torch.Tensor, dtype, rows: int, cols: int, what: str) -> int:
+    """Pitch of a [rows, cols] matrix argument of the 8-bit calls on the current device, after
+    checking it."""
+    shape, stride = t.shape, t.stride()
     if t.dtype != dtype:
         raise CacheBlendError(3, f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or (shape is not None and (t.shape[0] != shape[0] or t.shape[1] < shape[1])):
-        raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}" + ("" if shape is None else f", needs {shape}"))
-    if not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1):
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise CacheBlendError(2, f"{what} has shape {tuple(shape)}, needs ({rows}, {cols})")
+    if not t.is_cuda or (stride[1] != 1 and cols > 1):
         raise CacheBlendError(1, f"{what} must be a CUDA matrix with contiguous rows")
     # the pitch of a single row is never stepped over and may be anything: pass one the library takes
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    return stride[0] if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _rows_cols(t: torch.Tensor, what: str):
+    if t.dim() != 2:
+        raise CacheBlendError(2, f"{what} must be a matrix, not of shape {tuple(t.shape)}")
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise CacheBlendError(1, f"{what} is on another device than the current one")
+    return t.shape
 
 
 def row_scales(rows: int, cols: int, device="cuda") -> torch.Tensor:
@@ -364,32 +383,27 @@ def row_scales(rows: int, cols: int, device="cuda") -> torch.Tensor:
     return torch.empty((cols + 127) // 128, (rows + 3) // 4 * 4, dtype=torch.float32, device=device)[:, :rows]
 
 
-def _row_scale_pitch(s: torch.Tensor, rows: int, cols: int, what: str) -> int:
-    ld = _matrix(s, torch.float32, what, ((cols + 127) // 128, rows))
-    return ld if s.shape[0] > 1 else (rows + 3) // 4 * 4  # a single group's pitch is never stepped over
-
-
 def cb_quantize(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = None,
                 scales: Optional[torch.Tensor] = None, stream=None):
     """(codes e4m3 [rows, cols], fp32 scales) of x [rows, cols]: a row matrix (block_rows 1, scales
     [ceil(cols / 128), rows], see row_scales) or a block matrix (128, scales [ceil(rows / 128),
     ceil(cols / 128)])."""
-    lib = load_library()
-    dt = _dtype_code(x.dtype)
-    ldx = _matrix(x, x.dtype, "x")
-    rows, cols = x.shape
+    rows, cols = _rows_cols(x, "x")
+    dtype = x.dtype
+    dt = _dtype_code(dtype)
+    ldx = _pitch(x, dtype, rows, cols, "x")
     if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
+        codes = torch.empty(rows, cols, dtype=_E4M3, device=x.device)
+    groups, blocks = (cols + 127) // 128, (rows + 127) // 128
     if block_rows == 1:
         scales = row_scales(rows, cols, x.device) if scales is None else scales
-        lds = _row_scale_pitch(scales, rows, cols, "scales")
+        lds = _pitch(scales, torch.float32, groups, rows, "scales")
     else:
-        blocks = ((rows + 127) // 128, (cols + 127) // 128)
-        scales = torch.empty(blocks, dtype=torch.float32, device=x.device) if scales is None else scales
-        lds = _matrix(scales, torch.float32, "scales", blocks)
-    ldc = _matrix(codes, torch.float8_e4m3fn, "codes", (rows, cols))
-    _check(lib.cb_quantize(_ptr(x), ldx, rows, cols, dt, int(block_rows), _ptr(codes), ldc, _ptr(scales), lds,
-                           _stream(stream)))
+        scales = torch.empty(blocks, groups, dtype=torch.float32, device=x.device) if scales is None else scales
+        lds = _pitch(scales, torch.float32, blocks, groups, "scales")
+    _check(load_library().cb_quantize(x.data_ptr(), ldx, rows, cols, dt, block_rows, codes.data_ptr(),
+                                      _pitch(codes, _E4M3, rows, cols, "codes"), scales.data_ptr(), lds,
+                                      _stream(stream)))
     return codes, scales
 
 
@@ -399,31 +413,40 @@ def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = 
                             scales: Optional[torch.Tensor] = None, stream=None):
     """(codes, scales, residual_out) of the RMS norm of residual + x [rows, d]: the quantised rows
     (a row matrix) and the sum, written to ``residual_out`` when given (it may be ``residual``)."""
-    lib = load_library()
-    dt = _dtype_code(x.dtype)
-    ldx = _matrix(x, x.dtype, "x")
-    rows, d = x.shape
-    rdt, ldr = dt, 0
+    rows, d = _rows_cols(x, "x")
+    dtype = x.dtype
+    rdt = dt = _dtype_code(dtype)
+    ldx = _pitch(x, dtype, rows, d, "x")
+    ldr, res, res_out, w = 0, None, None, None
     if residual is not None:
-        rdt, ldr = _dtype_code(residual.dtype), _matrix(residual, residual.dtype, "residual", (rows, d))
-        if residual_out is not None and _matrix(residual_out, residual.dtype, "residual_out", (rows, d)) != ldr:
-            raise CacheBlendError(2, "residual and residual_out must have the same pitch")
-    if weight is not None and (weight.dtype != x.dtype or weight.numel() != d or not weight.is_contiguous()):
-        raise CacheBlendError(2, f"weight must be {d} contiguous elements of {x.dtype}")
+        rtype = residual.dtype
+        rdt, ldr, res = _dtype_code(rtype), _pitch(residual, rtype, rows, d, "residual"), residual.data_ptr()
+        if residual_out is not None:
+            if _pitch(residual_out, rtype, rows, d, "residual_out") != ldr:
+                raise CacheBlendError(2, "residual and residual_out must have the same pitch")
+            res_out = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise CacheBlendError(1, "residual_out needs a residual")
+    if weight is not None:
+        if weight.dtype != dtype or weight.shape != (d,) or not weight.is_contiguous() or not weight.is_cuda:
+            raise CacheBlendError(2, f"weight must be {d} contiguous CUDA elements of {dtype}")
+        w = weight.data_ptr()
     if codes is None:
-        codes = torch.empty(rows, d, dtype=torch.float8_e4m3fn, device=x.device)
+        codes = torch.empty(rows, d, dtype=_E4M3, device=x.device)
     scales = row_scales(rows, d, x.device) if scales is None else scales
-    ldc, lds = _matrix(codes, torch.float8_e4m3fn, "codes", (rows, d)), _row_scale_pitch(scales, rows, d, "scales")
-    _check(lib.cb_add_rmsnorm_quantize(_ptr(x), ldx, dt, _ptr(residual), _ptr(residual_out), ldr, rdt, _ptr(weight), rows,
-                                       d, float(eps), _ptr(codes), ldc, _ptr(scales), lds, _stream(stream)))
+    _check(load_library().cb_add_rmsnorm_quantize(
+        x.data_ptr(), ldx, dt, res, res_out, ldr, rdt, w, rows, d, eps, codes.data_ptr(),
+        _pitch(codes, _E4M3, rows, d, "codes"), scales.data_ptr(),
+        _pitch(scales, torch.float32, (d + 127) // 128, rows, "scales"), _stream(stream)))
     return codes, scales, residual_out
 
 
-def _block_mat(codes: torch.Tensor, scales: torch.Tensor, what: str) -> Fp8Mat:
-    n, k = codes.shape
-    ld = _matrix(codes, torch.float8_e4m3fn, what)
-    lds = _matrix(scales, torch.float32, what + "_scales", ((n + 127) // 128, (k + 127) // 128))
-    return Fp8Mat(codes.data_ptr(), ld, scales.data_ptr(), lds)
+def _block_mat(codes: torch.Tensor, scales: torch.Tensor, n: int, k: int, what: str) -> Fp8Mat:
+    return Fp8Mat(codes.data_ptr(), _pitch(codes, _E4M3, n, k, what), scales.data_ptr(),
+                  _pitch(scales, torch.float32, (n + 127) // 128, (k + 127) // 128, "its scales"))
+
+
+_SCALED_OUT = {CB_FP8_SWIGLU_FP8: _E4M3, CB_FP8_STORE_BF16: torch.bfloat16}
 
 
 def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_scales: torch.Tensor,
@@ -434,24 +457,25 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
     (CB_FP8_STORE_F32), addend + A . B^T in fp32 (CB_FP8_ADD_F32, ``addend`` may be ``C_out``), bf16
     (CB_FP8_STORE_BF16), or with gate rows B and up rows B2 the quantised SiLU(A B^T) * (A B2^T) as a
     row matrix C_out, C_scales (CB_FP8_SWIGLU_FP8)."""
-    lib = load_library()
-    M, K = A.shape
+    M, K = _rows_cols(A, "A")
     width = B.shape[0]
-    swiglu = epilogue == CB_FP8_SWIGLU_FP8
-    if B.shape[1] != K or (swiglu and (B2 is None or B2_scales is None or C_scales is None or B2.shape != B.shape)):
-        raise CacheBlendError(2, "operands do not fit each other")
-    a = Fp8Mat(A.data_ptr(), _matrix(A, torch.float8_e4m3fn, "A"), A_scales.data_ptr(),
-               _row_scale_pitch(A_scales, M, K, "A_scales"))
-    b = _block_mat(B, B_scales, "B")
-    b2 = _block_mat(B2, B2_scales, "B2") if swiglu else None
-    out = torch.float8_e4m3fn if swiglu else torch.bfloat16 if epilogue == CB_FP8_STORE_BF16 else torch.float32
-    ldc = _matrix(C_out, out, "C_out", (M, width))
-    if epilogue == CB_FP8_ADD_F32 and (addend is None or _matrix(addend, torch.float32, "addend", (M, width)) != ldc):
-        raise CacheBlendError(2, "addend must have C_out's pitch")
-    lds = _row_scale_pitch(C_scales, M, width, "C_scales") if swiglu else 0
-    _check(lib.cb_gemm_scaled(C.byref(a), C.byref(b), C.byref(b2) if swiglu else None, _ptr(addend), _ptr(C_out), ldc,
-                              _ptr(C_scales) if swiglu else None, lds, M, width * 2 if swiglu else width, K,
-                              int(epilogue), _stream(stream)))
+    a = Fp8Mat(A.data_ptr(), _pitch(A, _E4M3, M, K, "A"), A_scales.data_ptr(),
+               _pitch(A_scales, torch.float32, (K + 127) // 128, M, "A_scales"))
+    b = _block_mat(B, B_scales, width, K, "B")
+    ldc = _pitch(C_out, _SCALED_OUT.get(epilogue, torch.float32), M, width, "C_out")
+    b2 = add = cs = None
+    lds, n = 0, width
+    if epilogue == CB_FP8_SWIGLU_FP8:
+        if B2 is None or B2_scales is None or C_scales is None:
+            raise CacheBlendError(1, "CB_FP8_SWIGLU_FP8 needs B2, B2_scales and C_scales")
+        b2, n = _block_mat(B2, B2_scales, width, K, "B2"), 2 * width
+        cs, lds = C_scales.data_ptr(), _pitch(C_scales, torch.float32, (width + 127) // 128, M, "C_scales")
+    elif epilogue == CB_FP8_ADD_F32:
+        if addend is None or _pitch(addend, torch.float32, M, width, "addend") != ldc:
+            raise CacheBlendError(2, "CB_FP8_ADD_F32 needs an addend of C_out's pitch")
+        add = addend.data_ptr()
+    _check(load_library().cb_gemm_scaled(a, b, b2, add, C_out.data_ptr(), ldc, cs, lds, M, n, K, epilogue,
+                                         _stream(stream)))
     return C_out
 
 

@@ -24,12 +24,51 @@ __device__ __forceinline__ float fp8_amax_floor(uint32_t abs_bits) {
   return __uint_as_float(max(abs_bits, __float_as_uint(FP8_AMAX_MIN)));
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-template <int N> __device__ __forceinline__ uint32_t amax_bits(const float* f) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < N; ++j) m = max(m, abs_bits(f[j]));
-  return m;
+// largest magnitude of three values, NaN if one is (one instruction on sm_100 and later)
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
 }
+// largest magnitude of eight values as bits (NaN bits rank above infinity's)
+__device__ __forceinline__ uint32_t amax_bits8(const float* f) {
+  return __float_as_uint(max3_abs(max3_abs(f[0], f[1], f[2]), max3_abs(f[3], f[4], f[5]), max3_abs(f[6], f[7], 0.f)));
+}
+// 8 values as they lie in memory: 4 registers (bf16) or 8 (fp32)
+template <typename T> struct Piece;
+template <> struct Piece<bf16> {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  // magnitudes of bf16 compare as 16-bit integers, two at once
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m & 0xffff0000u, m << 16);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Piece<float> {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    float f[8];
+    get(f);
+    return amax_bits8(f);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
 // maximum over the 16 lanes that hold one group
 __device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
 #pragma unroll
@@ -58,18 +97,17 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
   const int col = (blockIdx.y * 256) + lane * 8;
   const long long row0 = (static_cast<long long>(blockIdx.x) * 8 + warp) * QR_UNROLL;
   const bool in = col < cols;
-  float f[QR_UNROLL][8];
+  Piece<T> v[QR_UNROLL];
+#pragma unroll
+  for (int u = 0; u < QR_UNROLL; ++u)
+    if (in && row0 + u < rows) v[u].load(x + (row0 + u) * ldx + col);
 #pragma unroll
   for (int u = 0; u < QR_UNROLL; ++u) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[u][j] = 0.f;
-    if (in && row0 + u < rows) load8(x + (row0 + u) * ldx + col, f[u]);
-  }
-#pragma unroll
-  for (int u = 0; u < QR_UNROLL; ++u) {
-    const float a = fp8_amax_floor(half_warp_max(amax_bits<8>(f[u])));
+    const float a = fp8_amax_floor(half_warp_max(v[u].amax()));
     if (in && row0 + u < rows) {
-      *reinterpret_cast<uint2*>(codes + (row0 + u) * ldc + col) = fp8_codes8(f[u], FP8_MAX / a);
+      float f[8];
+      v[u].get(f);
+      *reinterpret_cast<uint2*>(codes + (row0 + u) * ldc + col) = fp8_codes8(f, FP8_MAX / a);
       if ((lane & 15) == 0) scales[static_cast<long long>(col >> 7) * lds + row0 + u] = a / FP8_MAX;
     }
   }
@@ -89,16 +127,13 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restric
   const int col = blockIdx.x * 128 + (t & 15) * 8;
   const long long row = static_cast<long long>(blockIdx.y) * 128 + (t >> 4);
   const bool in = col < cols;
-  float f[8][8];
+  Piece<T> v[8];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[u][j] = 0.f;
-    if (in && row + u * 16 < rows) load8(x + (row + u * 16) * ldx + col, f[u]);
-  }
+  for (int u = 0; u < 8; ++u)
+    if (in && row + u * 16 < rows) v[u].load(x + (row + u * 16) * ldx + col);
   uint32_t m = 0;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) m = max(m, amax_bits<8>(f[u]));
+  for (int u = 0; u < 8; ++u) m = max(m, v[u].amax());
   m = __reduce_max_sync(0xffffffffu, m);
   if ((t & 31) == 0) red[t >> 5] = m;
   __syncthreads();
@@ -107,59 +142,36 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restric
   const float a = fp8_amax_floor(m), inv = FP8_MAX / a;
 #pragma unroll
   for (int u = 0; u < 8; ++u)
-    if (in && row + u * 16 < rows)
-      *reinterpret_cast<uint2*>(codes + (row + u * 16) * ldc + col) = fp8_codes8(f[u], inv);
+    if (in && row + u * 16 < rows) {
+      float f[8];
+      v[u].get(f);
+      *reinterpret_cast<uint2*>(codes + (row + u * 16) * ldc + col) = fp8_codes8(f, inv);
+    }
   if (t == 0) scales[static_cast<long long>(blockIdx.y) * lds + blockIdx.x] = a / FP8_MAX;
 }
 
 // ----------------------------------------------------------------------------- norm
-// One CTA per row, the row held in registers from its single read to its codes: thread t owns
-// the 8-channel pieces t, t + blockDim, ... (CH of them), so 16 consecutive lanes hold one group.
-// h = residual + x in fp32; the norm and the codes come from the unrounded h, residual_out gets h
-// rounded to its type.
-template <typename TX, typename TR, int CH>
-__global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restrict__ x, long long ldx,
-                                                               const TR* res, TR* res_out, long long ldr,
-                                                               const TX* __restrict__ weight, int d, float eps,
-                                                               uint8_t* __restrict__ codes, long long ldc,
-                                                               float* __restrict__ scales, long long lds) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ float red[32];
-  const long long row = blockIdx.x;
-  const int t = threadIdx.x, T = blockDim.x;
-  float f[CH][8];
-  float ss = 0.f;
-#pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int c = (t + k * T) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[k][j] = 0.f;
-    if (c < d) load8(x + row * ldx + c, f[k]);
-  }
-  if (res) {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = (t + k * T) * 8;
-      if (c < d) {
-        float r[8];
-        load8(res + row * ldr + c, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[k][j] = r[j] + f[k][j];
-        if (res_out) store8(res_out + row * ldr + c, f[k]);
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < CH; ++k)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss += f[k][j] * f[k][j];
-  ss = warp_sum(ss);
-  if ((t & 31) == 0) red[t >> 5] = ss;
+// A row is held in registers from its single read to its codes: thread t owns the 8-channel pieces
+// t, t + blockDim, ... (CH of them), so 16 consecutive lanes hold one group.  h = residual + x in
+// fp32; the norm and the codes come from the unrounded h, residual_out gets h rounded to its type.
+
+// Sum over the block.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  const int nw = T >> 5;
-  ss = warp_sum((t & 31) < nw ? red[t & 31] : 0.f);
-  const float inv_rms = 1.0f / sqrtf(ss / static_cast<float>(d) + eps);
+  const int n = blockDim.x >> 5;
+  float sum = 0.f;
+  for (int i = 0; i < n; ++i) sum += red[i];
+  return sum;
+}
+
+// Codes and scales of the row h (in f), given 1 / rms.
+template <typename TX, int CH>
+__device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, const TX* __restrict__ weight, int d,
+                                           long long row, uint8_t* __restrict__ codes, long long ldc,
+                                           float* __restrict__ scales, long long lds) {
+  const int t = threadIdx.x, T = blockDim.x;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = (t + k * T) * 8;
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
     // y = u * inv_rms with u = h * w, so y * (448 / max|y|) = u * (448 / max|u|): the codes do not
     // see the norm's rounding (two roundings instead of four), only the scale does.  Where 448 /
     // max|u| could overflow, or the scale's floor applies, the codes come from y itself.
-    const float au = __uint_as_float(half_warp_max(amax_bits<8>(f[k])));
+    const float au = __uint_as_float(half_warp_max(amax_bits8(f[k])));
     const float a = fp8_amax_floor(abs_bits(au * inv_rms));
     float inv = FP8_MAX / au;
     if (!(au > 0x1p-100f && a > FP8_AMAX_MIN)) {
@@ -187,19 +199,67 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
   }
 }
 
+template <typename TX, typename TR, bool RES, int CH>
+__global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restrict__ x, long long ldx,
+                                                               const void* residual, void* residual_out, long long ldr,
+                                                               const TX* __restrict__ weight, int d, float eps,
+                                                               uint8_t* __restrict__ codes, long long ldc,
+                                                               float* __restrict__ scales, long long lds) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ float red[32];
+  const TR* res = static_cast<const TR*>(residual);
+  TR* res_out = static_cast<TR*>(residual_out);
+  const long long row = blockIdx.x;
+  const int t = threadIdx.x, T = blockDim.x;
+  // every read is under way before the first value is needed (residual_out may be residual, so the
+  // compiler may not move a read across its store)
+  Piece<TX> px[CH];
+  Piece<TR> pr[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (t + k * T) * 8;
+    if (c < d) {
+      px[k].load(x + row * ldx + c);
+      if (RES) pr[k].load(res + row * ldr + c);
+    }
+  }
+  float f[CH][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (t + k * T) * 8;
+    float r[8];
+    px[k].get(f[k]);
+    pr[k].get(r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (RES) f[k][j] = r[j] + f[k][j];
+      ss += f[k][j] * f[k][j];
+    }
+    if (RES && res_out && c < d) store8(res_out + row * ldr + c, f[k]);
+  }
+  const float inv_rms = 1.0f / sqrtf(block_sum(ss, red) / static_cast<float>(d) + eps);
+  norm_codes<TX, CH>(f, inv_rms, weight, d, row, codes, ldc, scales, lds);
+}
+
 template <typename TX, typename TR>
 cudaError_t launch_norm(const void* x, long long ldx, const void* res, void* res_out, long long ldr, const void* weight,
                         int rows, int d, float eps, void* codes, long long ldc, float* scales, long long lds,
                         cudaStream_t s) {
-  // threads of a row in whole warps, one piece of 8 channels each
   const int pieces = (d + 7) / 8;
-  auto go = [&](auto kernel, int ch) {
+  auto one = [&](auto kernel, int ch) {
     const int threads = ((pieces + ch - 1) / ch + 31) / 32 * 32;
     return launch_chain(kernel, dim3(rows), dim3(threads), 0, s, static_cast<const TX*>(x), ldx,
-                        static_cast<const TR*>(res), static_cast<TR*>(res_out), ldr, static_cast<const TX*>(weight), d,
-                        eps, static_cast<uint8_t*>(codes), ldc, scales, lds);
+                        res, res_out, ldr, static_cast<const TX*>(weight), d, eps, static_cast<uint8_t*>(codes), ldc, scales, lds);
   };
-  return go(add_rmsnorm_fp8_kernel<TX, TR, 4>, 4);
+  // Pieces per thread: one for short rows and for few rows (the shortest way through a row: 2.4 us for
+  // one row of 4096 against 3.2 us with four; 2000 rows of 1024: 5.0 against 6.5 us), four for many
+  // long ones, whose CTAs then keep more reads under way per barrier (8320 rows of 8192 in bf16: 78
+  // against 97 us; 8320 rows of 7168 with an fp32 residual: 99 against 106 us).
+  const bool one_piece = pieces <= 1024 && (pieces <= 512 || rows <= 608);
+  if (res) return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TR, true, 1>, 1) : one(add_rmsnorm_fp8_kernel<TX, TR, true, 4>, 4);
+  return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1>, 1) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 4>, 4);
 }
 
 }  // namespace

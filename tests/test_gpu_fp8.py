@@ -426,3 +426,26 @@ def test_two_products_at_once():
         gemm(o1, F32, s1), gemm(o2, F32, s2)
         torch.cuda.synchronize()
         assert torch.equal(o1["c"], want[0]) and torch.equal(o2["c"], want[1])
+
+
+def test_binding_refuses_what_does_not_fit():
+    x, res = rand(1, 6, 256), rand(2, 6, 256)
+    codes, scales = cb.cb_quantize(x)
+    b, sb = coded(3, 128, 256, 128)
+    c = torch.empty(6, 128, device="cuda")
+    bad = [lambda: cb.cb_quantize(x, codes=codes[:, :128]), lambda: cb.cb_quantize(x, scales=scales.t()),
+           lambda: cb.cb_quantize(x.t()), lambda: cb.cb_quantize(x[:, :200]), lambda: cb.cb_quantize(x, 128, scales=sb[:, :1]),
+           lambda: cb.cb_quantize(x, codes=codes.view(torch.uint8)), lambda: cb.cb_quantize(x[:, 1:129]),
+           lambda: cb.cb_add_rmsnorm_quantize(x, res[:5]), lambda: cb.cb_add_rmsnorm_quantize(x, residual_out=res),
+           lambda: cb.cb_add_rmsnorm_quantize(x, res, residual_out=res.bfloat16()),
+           lambda: cb.cb_add_rmsnorm_quantize(x, weight=res[0, :128]), lambda: cb.cb_add_rmsnorm_quantize(x, weight=res[0].bfloat16()),
+           lambda: cb.cb_gemm_scaled(codes, scales, b[:, :128], sb, c), lambda: cb.cb_gemm_scaled(codes, scales, b, sb[:, :1], c),
+           lambda: cb.cb_gemm_scaled(codes, scales[:, :5], b, sb, c), lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c[:, :64]),
+           lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c.bfloat16()), lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c, BF16),
+           lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c, ADD), lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c, SWIGLU),
+           lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c, 7),
+           lambda: cb.cb_gemm_scaled(codes, scales, b, sb, c, ADD, addend=rand(1, 6, 256)[:, :128])]
+    for call in bad:
+        with pytest.raises(cb.CacheBlendError):
+            call()
+    torch.cuda.synchronize()
