@@ -12,7 +12,7 @@
 //     16 tokens, and a cluster of S pairs may split the channels.  Every factor is then another one
 //     per column; tensor memory is read as 16 lanes x 256 bits, which leaves a thread the factors of
 //     a quarter of the columns only (with 32 lanes x 1 column it would be all of them).  The factors
-//     cost 32 shared-memory cycles per warp and group at 128 tokens, which is why this form does not
+//     cost a shared-memory cycle per warp, group and four columns, which is why this form does not
 //     serve many tokens: at 256 tokens a group took ~1100 cycles with them and ~850 without.
 // Roles of the warps, in both:
 //   warp 0: TMA producer of codes   warp 1: tensor-memory owner, in even CTAs the MMA issuer
@@ -46,7 +46,7 @@ constexpr int OFF_SC = OFF_AMAX + 2048;    // factors of every stage, then the r
 constexpr int SMEM_ALLOC = 232448;         // the per-block maximum (227 KiB), 1 KiB of it aligns the base
 constexpr int SMEM_USE = SMEM_ALLOC - 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int PART_PITCH = ROWS + 4;       // floats per token of a CTA's partial sums (few tokens)
+constexpr int PART_PITCH = ROWS + 4;       // floats per token and source CTA of the parts (few tokens)
 constexpr int SLAB = 2048;                 // many tokens: a warp stages 32 tokens x 64 bytes, twice
 
 // Accumulators in tensor memory: as many groups' sums as fit may wait to be read.
@@ -126,6 +126,18 @@ template <> __device__ __forceinline__ void tmem_ld16x256<4>(uint32_t taddr, uin
       : "r"(taddr));
 }
 
+// The same for any number of 8-column pieces, as the largest reads that add up to it.
+template <int N8> __device__ __forceinline__ void tmem_ld16x256_all(uint32_t taddr, uint32_t* r) {
+  if constexpr (N8 >= 4) {
+    tmem_ld16x256<4>(taddr, r);
+    tmem_ld16x256_all<N8 - 4>(taddr + 32, r + 16);
+  } else if constexpr (N8 >= 2) {
+    tmem_ld16x256<2>(taddr, r);
+    tmem_ld16x256_all<N8 - 2>(taddr + 16, r + 8);
+  } else if constexpr (N8 == 1) {
+    tmem_ld16x256<1>(taddr, r);
+  }
+}
 // 32 lanes x 32 fp32 columns, without waiting: thread t gets lane t's columns.
 __device__ __forceinline__ void tmem_ld32x32(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -165,27 +177,25 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// N pairs of factors from shared memory
+// N pairs of factors from shared memory (16-byte aligned)
 template <int N> __device__ __forceinline__ void read_factors(const float* s, uint64_t* f) {
-  if (N == 1) {
-    f[0] = *reinterpret_cast<const uint64_t*>(s);
-  } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s + 2 * i);
-      f[i] = v.x;
-      f[i + 1 < N ? i + 1 : i] = v.y;
-    }
+  for (int i = 0; i + 1 < N; i += 2) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s + 2 * i);
+    f[i] = v.x;
+    f[i + 1] = v.y;
   }
+  if (N % 2) f[N - 1] = *reinterpret_cast<const uint64_t*>(s + 2 * (N - 1));
 }
 
 // ----------------------------------------------------------------------------- cluster exchange
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// A value into another CTA's shared memory whose bytes complete on that CTA's barrier.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(__float_as_uint(v)), "r"(bar)
+               : "memory");
 }
-// mbar_wait_bounded with acquire at cluster scope (other CTAs' shared memory is read after it)
+// mbar_wait_bounded with acquire at cluster scope (what other CTAs wrote is read after it)
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
@@ -224,7 +234,8 @@ struct Bars {
   uint64_t done[MAX_STAGES];      // its MMAs are done: the stage is free and the group's sums are readable
   uint64_t acc_empty[4];          // both CTAs' warps have read an accumulator (even CTAs)
   uint64_t raw_full[RAW_SLOTS], raw_empty[RAW_SLOTS];
-  uint64_t part_full, part_free;  // few tokens: the cluster's parts are written / read
+  uint64_t part_full;             // few tokens: the cluster's parts of this CTA's tokens have arrived
+  uint64_t part_free;             // every CTA of the cluster has read its parts
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
@@ -241,7 +252,7 @@ __device__ __forceinline__ void init_bars(Bars& bars, int split) {
     mbar_init(&bars.raw_full[s], 1);
     mbar_init(&bars.raw_empty[s], 1);
   }
-  mbar_init(&bars.part_full, 16 * split);
+  mbar_init(&bars.part_full, 1);
   mbar_init(&bars.part_free, 16 * split);
   mbar_init(&bars.drain, 1);
   bars.abort = 0;
@@ -680,23 +691,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ============================================================================= few tokens
 // Weights on the rows: BT tokens per pair, warpgroup w takes tokens w BT / 2 .. .  SwiGLU: a CTA's
 // rows are 64 gate rows and the 64 up rows of the same features.  A cluster of S pairs splits the
-// groups; every CTA leaves its fp32 sums in its shared memory, and each CTA of the cluster finishes
-// 1 / (2 S) of the tokens for all 256 rows, adding the S parts in a fixed order.
+// groups; each of its 2 S CTAs finishes 1 / (2 S) of the tokens for all 256 rows, adding the S parts
+// in a fixed order.  The parts are pushed into the finishing CTA's shared memory (st.async, counted
+// in bytes on its barrier): a barrier with release at cluster scope and reads from the other side
+// took ~1.3 us longer.  Bound by the weights' bytes; what a call of few groups spends on top is the
+// way through the chip (set-up 0.9 us, first codes 1.7 us, parts and output ~1 us).
 template <int BT, bool SWIGLU>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_weights_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                             const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmS,
                             const __grid_constant__ CUtensorMap, const Params p) {
-  constexpr int HB = BT / 2;                                 // tokens per warpgroup
-  constexpr int CH = HB >= 64 ? 16 : HB >= 32 ? 16 : 8;      // tokens per tensor-memory read
-  constexpr int NCH = HB / CH;
+  constexpr int HB = BT / 2;  // tokens per warpgroup
+  constexpr int N8 = HB / 8;
   constexpr uint32_t NACC = n_acc(BT), ACC_STRIDE = TMEM_COLS / NACC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem);
   float* raw = reinterpret_cast<float*>(smem + OFF_RAW);
   uint8_t* sc = smem + OFF_SC;
-  uint32_t* amax = reinterpret_cast<uint32_t*>(smem + OFF_AMAX);
   uint8_t* ring = smem + p.ring_off;
   volatile int* abort = &bars.abort;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -779,14 +791,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     many_registers();
     const int quarter = warp & 3, w = (warp >> 2) - 1;  // tensor-memory lanes 32 quarter .., tokens w HB ..
-    const int et = threadIdx.x - 128, wt_t = threadIdx.x & 127;  // thread of the eight warps, of its warpgroup
+    const int et = threadIdx.x - 128;  // thread of the eight warps
     const int ri = lane >> 2, ci = (lane & 3) * 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t acc_empty_lead = mapa_shared(smem_u32(bars.acc_empty), lead);
-    float* part = reinterpret_cast<float*>(smem + p.out_off);  // [BT][PART_PITCH]
-    const uint32_t part_u32 = smem_u32(part);
+    const float* part = reinterpret_cast<const float*>(smem + p.out_off);  // [CS][per][PART_PITCH]
+    const uint32_t part_u32 = smem_u32(part), part_full_u32 = smem_u32(&bars.part_full);
     const int CS = 2 * p.split;
-    const int per = (BT + CS - 1) / CS;  // tokens that each CTA of the cluster finishes
+    const int per = BT / CS;  // tokens that each CTA of the cluster finishes (even: BT is a multiple of 16)
     const uint32_t el = lane == 0;
     Pos st;
     uint32_t b = 0;
@@ -804,143 +816,136 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = 0; j < HB / 8; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][r] = 0;
-      uint32_t lo[2][CH / 2], hi[2][CH / 2];  // two buffers, as above
-      auto begin = [&]() {
+#pragma unroll 1
+      for (int g = g0; g < g1; ++g) {
         if (ok && !mbar_wait_bounded(&bars.done[st.i], st.ph, abort)) give_up();
         __syncwarp();
         tc_fence_after();
         const uint32_t tacc = tmem + b * ACC_STRIDE + lane_base + static_cast<uint32_t>(w * HB);
-        tmem_ld16x256<CH / 8>(tacc, lo[0]);
-        tmem_ld16x256<CH / 8>(tacc + (16u << 16), hi[0]);
-      };
-      begin();
-#pragma unroll 1
-      for (int g = g0; g < g1; ++g) {
-        const uint32_t tacc = tmem + b * ACC_STRIDE + lane_base + static_cast<uint32_t>(w * HB);
-        const float* sv = reinterpret_cast<const float*>(sc + st.i * FACTOR_BYTES) +
-                          (SWIGLU && quarter >= 2 ? FACTORS : 0) + w * (FACTORS / 2) + (lane & 3) * 20;
-        uint64_t f[CH / 8];
-        auto sums = [&](int c) {
-          const int i = c & 1;
+        uint32_t lo[N8 * 4], hi[N8 * 4];
+        tmem_ld16x256_all<N8>(tacc, lo);
+        tmem_ld16x256_all<N8>(tacc + (16u << 16), hi);
+        uint64_t f[N8];
+        read_factors<N8>(reinterpret_cast<const float*>(sc + st.i * FACTOR_BYTES) +
+                             (SWIGLU && quarter >= 2 ? FACTORS : 0) + w * (FACTORS / 2) + (lane & 3) * 20,
+                         f);
+        tmem_wait_ld_of<N8 * 4>(lo);
+        tmem_wait_ld_of<N8 * 4>(hi);
+        tc_fence_before();
+        mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8, el);
+        if (++b == NACC) b = 0;
+        st.next(stages);
 #pragma unroll
-          for (int j = 0; j < CH / 8; ++j) {
-            uint64_t* a = acc[c * (CH / 8) + j];
-            a[0] = fma2(pack2u(lo[i][4 * j], lo[i][4 * j + 1]), f[j], a[0]);
-            a[1] = fma2(pack2u(lo[i][4 * j + 2], lo[i][4 * j + 3]), f[j], a[1]);
-            a[2] = fma2(pack2u(hi[i][4 * j], hi[i][4 * j + 1]), f[j], a[2]);
-            a[3] = fma2(pack2u(hi[i][4 * j + 2], hi[i][4 * j + 3]), f[j], a[3]);
-          }
-        };
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-          // (read before the wait: their latency then passes under the tensor-memory read's)
-          read_factors<CH / 8>(sv + c * (CH / 4), f);
-          tmem_wait_ld_of<CH / 2>(lo[c & 1]);
-          tmem_wait_ld_of<CH / 2>(hi[c & 1]);
-          if (c + 1 < NCH) {
-            tmem_ld16x256<CH / 8>(tacc + (c + 1) * CH, lo[(c + 1) & 1]);
-            tmem_ld16x256<CH / 8>(tacc + (c + 1) * CH + (16u << 16), hi[(c + 1) & 1]);
-            sums(c);
-          } else {
-            tc_fence_before();
-            mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8, el);
-            if (++b == NACC) b = 0;
-            st.next(stages);
-            if (NCH % 2) sums(c);
-            if (g + 1 < g1) begin();
-            if (NCH % 2 == 0) sums(c);
-          }
+        for (int j = 0; j < N8; ++j) {
+          acc[j][0] = fma2(pack2u(lo[4 * j], lo[4 * j + 1]), f[j], acc[j][0]);
+          acc[j][1] = fma2(pack2u(lo[4 * j + 2], lo[4 * j + 3]), f[j], acc[j][1]);
+          acc[j][2] = fma2(pack2u(hi[4 * j], hi[4 * j + 1]), f[j], acc[j][2]);
+          acc[j][3] = fma2(pack2u(hi[4 * j + 2], hi[4 * j + 3]), f[j], acc[j][3]);
         }
       }
 
       // ------------------------------------------------------------------ epilogue
       const uint32_t parity = nth & 1;
+      const int n = min(per, p.g.M - t0 - static_cast<int>(rank) * per);  // tokens to finish here (none: <= 0)
+      const int tok0 = t0 + static_cast<int>(rank) * per;
+      if (et == 0) mbar_arrive_expect_tx(&bars.part_full, static_cast<uint32_t>(BT * ROWS * 4));
       // the parts of the previous tile have been read by the whole cluster
       if (ok && !mbar_wait_cluster(&bars.part_free, parity ^ 1u, abort)) give_up();
       __syncwarp();
 #pragma unroll
-      for (int j = 0; j < HB / 8; ++j)
+      for (int j = 0; j < N8; ++j) {
+        const int tok = w * HB + j * 8 + ci;  // and the next one: the same CTA finishes both
+        const uint32_t to = static_cast<uint32_t>(tok / per);
+        const uint32_t bar = mapa_shared(part_full_u32, to);
+        const uint32_t d = mapa_shared(
+            part_u32 + ((rank * per + tok - to * per) * PART_PITCH + quarter * 32 + ri) * 4, to);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float2 v = unpack2(acc[j][r]);
-          float* d = part + (w * HB + j * 8 + ci) * PART_PITCH + quarter * 32 + r * 8 + ri;
-          d[0] = v.x;
-          d[PART_PITCH] = v.y;
+          st_async_f32(d + r * 32, v.x, bar);
+          st_async_f32(d + r * 32 + PART_PITCH * 4, v.y, bar);
         }
-      __syncwarp();
-      if (lane < CS) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.part_full), lane));
-      if (ok && !mbar_wait_cluster(&bars.part_full, parity, abort)) give_up();
-      __syncwarp();
-      const int j0 = static_cast<int>(rank) * per, j1 = min(min(BT, j0 + per), p.g.M - t0);
-      constexpr int AT_ONCE = 4;  // tokens whose remote reads are in flight together
+      }
       if constexpr (!SWIGLU) {
-        const int f = wt * 256 + et;
-        const uint32_t hh = static_cast<uint32_t>(et >> 7);
-        for (int j = j0; j < j1; j += AT_ONCE) {
-          float v[AT_ONCE] = {}, d[AT_ONCE] = {};
-          if (p.g.epilogue == CB_FP8_ADD_F32 && f < p.width) {
+        // thread: 4 features of every fourth token
+        const int q4 = et & 63, f = wt * 256 + q4 * 4, tg = et >> 6;
+        const float* src = part + (q4 >> 5) * per * PART_PITCH + (q4 & 31) * 4;
+        const bool add = p.g.epilogue == CB_FP8_ADD_F32, whole = f + 4 <= p.width;
+        constexpr int AHEAD = 4;  // addends read before the parts are there
+        float4 d[AHEAD];
+        if (add && whole)
 #pragma unroll
-            for (int q = 0; q < AT_ONCE; ++q)
-              if (j + q < j1) d[q] = p.g.addend[static_cast<long long>(t0 + j + q) * p.g.ldc + f];
-          }
+          for (int i = 0; i < AHEAD; ++i)
+            if (tg + 4 * i < n)
+              d[i] = *reinterpret_cast<const float4*>(p.g.addend + static_cast<long long>(tok0 + tg + 4 * i) * p.g.ldc + f);
+        if (ok && !mbar_wait_cluster(&bars.part_full, parity, abort)) give_up();
+        __syncwarp();
+        auto finish_token = [&](int j, bool have, float4 ahead) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int s = 0; s < p.split; ++s) {
-            const uint32_t a = mapa_shared(part_u32 + (j * PART_PITCH + (et & 127)) * 4, 2 * s + hh);
-            float x[AT_ONCE];
-#pragma unroll
-            for (int q = 0; q < AT_ONCE; ++q) x[q] = j + q < j1 ? ld_cluster_f32(a + q * PART_PITCH * 4) : 0.f;
-#pragma unroll
-            for (int q = 0; q < AT_ONCE; ++q) v[q] += x[q];
+            const float4 x = *reinterpret_cast<const float4*>(src + (2 * s * per + j) * PART_PITCH);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
           }
+          const long long o = static_cast<long long>(tok0 + j) * p.g.ldc + f;
+          if (!ok) return;
+          if (whole) {
+            if (p.g.epilogue == CB_FP8_STORE_BF16) {
+              *reinterpret_cast<uint2*>(static_cast<bf16*>(p.g.c) + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+              return;
+            }
+            if (add) {
+              const float4 a = have ? ahead : *reinterpret_cast<const float4*>(p.g.addend + o);
+              v = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+            }
+            *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + o) = v;
+            return;
+          }
+          const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int q = 0; q < AT_ONCE; ++q) {
-            if (j + q >= j1 || f >= p.width || !ok) continue;
-            const long long o = static_cast<long long>(t0 + j + q) * p.g.ldc + f;
+          for (int i = 0; i < 4; ++i) {
+            if (f + i >= p.width) continue;
             if (p.g.epilogue == CB_FP8_STORE_BF16)
-              static_cast<bf16*>(p.g.c)[o] = __float2bfloat16_rn(v[q]);
+              static_cast<bf16*>(p.g.c)[o + i] = __float2bfloat16_rn(x[i]);
             else
-              static_cast<float*>(p.g.c)[o] = p.g.epilogue == CB_FP8_ADD_F32 ? d[q] + v[q] : v[q];
+              static_cast<float*>(p.g.c)[o + i] = add ? p.g.addend[o + i] + x[i] : x[i];
           }
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (tg + 4 * i < n) finish_token(tg + 4 * i, true, d[i]);
+        for (int j = tg + 4 * AHEAD; j < n; j += 4) finish_token(j, false, make_float4(0.f, 0.f, 0.f, 0.f));
       } else {
-        // a warpgroup per four tokens, thread x takes feature x of the tile's 128
-        const uint32_t hh = static_cast<uint32_t>(wt_t >> 6);
-        const int f = wt * 128 + wt_t;
-        for (int jb = j0; jb < j1; jb += 2 * AT_ONCE) {
-          const int j = jb + w * AT_ONCE;
-          float gate[AT_ONCE] = {}, up[AT_ONCE] = {};
+        // a warp per token, lane x takes features 4 x .. of the tile's 128
+        const float* src = part + (lane >> 4) * per * PART_PITCH + (lane & 15) * 4;
+        const int f = wt * 128 + lane * 4;
+        if (ok && !mbar_wait_cluster(&bars.part_full, parity, abort)) give_up();
+        __syncwarp();
+#pragma unroll 2
+        for (int j = warp - 4; j < n; j += 8) {
+          float4 gate = make_float4(0.f, 0.f, 0.f, 0.f), up = gate;
           for (int s = 0; s < p.split; ++s) {
-            const uint32_t a = mapa_shared(part_u32 + (j * PART_PITCH + (wt_t & 63)) * 4, 2 * s + hh);
-            float x[AT_ONCE], y[AT_ONCE];
-#pragma unroll
-            for (int q = 0; q < AT_ONCE; ++q) {
-              x[q] = j + q < j1 ? ld_cluster_f32(a + q * PART_PITCH * 4) : 0.f;
-              y[q] = j + q < j1 ? ld_cluster_f32(a + q * PART_PITCH * 4 + 256) : 0.f;
-            }
-#pragma unroll
-            for (int q = 0; q < AT_ONCE; ++q) {
-              gate[q] += x[q];
-              up[q] += y[q];
-            }
+            const float* x = src + (2 * s * per + j) * PART_PITCH;
+            const float4 a = *reinterpret_cast<const float4*>(x), b4 = *reinterpret_cast<const float4*>(x + 64);
+            gate = make_float4(gate.x + a.x, gate.y + a.y, gate.z + a.z, gate.w + a.w);
+            up = make_float4(up.x + b4.x, up.y + b4.y, up.z + b4.z, up.w + b4.w);
           }
+          const float y[4] = {silu(gate.x) * up.x, silu(gate.y) * up.y, silu(gate.z) * up.z, silu(gate.w) * up.w};
+          uint32_t m = 0;
 #pragma unroll
-          for (int q = 0; q < AT_ONCE; ++q) {
-            gate[q] = silu(gate[q]) * up[q];
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(gate[q]) & 0x7fffffffu);
-            if (lane == 0) amax[(w * AT_ONCE + q) * 4 + quarter] = m;
+          for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+          m = __reduce_max_sync(0xffffffffu, f < p.width ? m : 0u);
+          const float a = __uint_as_float(max(m, __float_as_uint(FP8_AMAX_MIN))), inv = FP8_MAX / a;
+          if (!ok) continue;
+          if (f < p.width) {
+            const uint32_t c01 = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t c23 = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE, __NV_E4M3);
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.g.c) + static_cast<long long>(tok0 + j) * p.g.ldc + f) =
+                c01 | (c23 << 16);
           }
-          named_bar(1 + w, 128);
-#pragma unroll
-          for (int q = 0; q < AT_ONCE; ++q) {
-            const uint32_t* x = amax + (w * AT_ONCE + q) * 4;
-            const float am =
-                __uint_as_float(max(max(max(x[0], x[1]), max(x[2], x[3])), __float_as_uint(FP8_AMAX_MIN)));
-            if (ok && f < p.width && j + q < j1) {
-              static_cast<uint8_t*>(p.g.c)[static_cast<long long>(t0 + j + q) * p.g.ldc + f] =
-                  __nv_cvt_float_to_fp8(gate[q] * (FP8_MAX / am), __NV_SATFINITE, __NV_E4M3);
-              if (wt_t == 0) p.g.c_scale[static_cast<long long>(wt) * p.g.ld_cs + t0 + j + q] = am / FP8_MAX;
-            }
-          }
-          named_bar(1 + w, 128);
+          if (lane == 0) p.g.c_scale[static_cast<long long>(wt) * p.g.ld_cs + tok0 + j] = a / FP8_MAX;
         }
       }
       __syncwarp();
@@ -966,7 +971,10 @@ Kernel kernel_of(int bt, int epilogue) {
   switch (bt) {
     case 16: return swiglu ? gemm_fp8_weights_kernel<16, true> : gemm_fp8_weights_kernel<16, false>;
     case 32: return swiglu ? gemm_fp8_weights_kernel<32, true> : gemm_fp8_weights_kernel<32, false>;
+    case 48: return swiglu ? gemm_fp8_weights_kernel<48, true> : gemm_fp8_weights_kernel<48, false>;
     case 64: return swiglu ? gemm_fp8_weights_kernel<64, true> : gemm_fp8_weights_kernel<64, false>;
+    case 80: return swiglu ? gemm_fp8_weights_kernel<80, true> : gemm_fp8_weights_kernel<80, false>;
+    case 96: return swiglu ? gemm_fp8_weights_kernel<96, true> : gemm_fp8_weights_kernel<96, false>;
     case 128: return swiglu ? gemm_fp8_weights_kernel<128, true> : gemm_fp8_weights_kernel<128, false>;
     case 256:
       return swiglu                            ? gemm_fp8_tokens_kernel<CB_FP8_SWIGLU_FP8>
@@ -1043,7 +1051,7 @@ Plan plan(const Fp8Gemm& g) {
       best.out_off = best.ring_off + best.stages * stage;
     }
   };
-  for (int bt : {16, 32, 64, 128})
+  for (int bt : {16, 32, 48, 64, 80, 96, 128})
     for (int split : {1, 2, 4}) consider(bt, split);
   consider(256, 1);
   return best;
