@@ -481,7 +481,7 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
 
 def cb_gemm_scaled_set_plan(tokens: int, split: int) -> None:
     """Process-wide tiling of cb_gemm_scaled: tokens per tile (16, 32, 48, 64, 80, 96, 128, 256) and
-    pairs that divide the channels (1, 2, 4); 0, 0 by the library's time model (tuning and tests)."""
+    pairs that divide the channels (1 to 4); 0, 0 by the library's time model (tuning and tests)."""
     _check(load_library().cb_gemm_scaled_set_plan(int(tokens), int(split)))
 
 

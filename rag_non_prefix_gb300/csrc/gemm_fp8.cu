@@ -15,9 +15,13 @@
 //     cost a shared-memory cycle per warp, group and four columns, which is why this form does not
 //     serve many tokens: at 256 tokens a group took ~1100 cycles with them and ~850 without.
 // Roles of the warps, in both:
-//   warp 0: TMA producer of codes   warp 1: tensor-memory owner, in even CTAs the MMA issuer
-//   warp 2: TMA producer of token scales   warp 3: multiplies them by the weight blocks' scales
+//   warp 0: TMA producer of codes and token scales
+//   warp 1: tensor-memory owner, in even CTAs the MMA issuer
+//   warps 2, 3: multiply the token scales by the weight blocks' scales, a group each in turn
 //   warps 4-11: scaling, sums and epilogue
+// A barrier poll costs ~110 cycles even when the phase is long over (measured), so that every role
+// waits for one barrier per group where it can: a stage's `full` barrier counts its codes, its
+// factors and the readers of the accumulator that its MMAs overwrite.
 // Every wait is bounded: a warp that gives up records ST_WAIT_TIMEOUT and runs on without waiting
 // or storing, so that the barriers it shares are still met; the cluster meets at its closing
 // barrier before any CTA frees its tensor memory or leaves.
@@ -37,12 +41,10 @@ constexpr int THREADS = 384;
 constexpr int ROWS = 128;                  // rows of the tensor core's tile per CTA
 constexpr int A_BYTES = ROWS * 128;        // 16 KiB: 128 rows x one group of channels
 constexpr int MAX_STAGES = 12;
-constexpr int RAW_SLOTS = 4;               // token scales of a group as loaded: slots of 128 floats
 constexpr int FACTORS = 2 * 4 * 20;        // token times block scales: 128 tokens, or two warpgroups x four thread classes x (16 + 4)
-constexpr int FACTOR_BYTES = 2 * FACTORS * 4;  // a stage's two lists (two weight blocks)
-constexpr int OFF_RAW = 1024;              // after the barriers
-constexpr int OFF_AMAX = OFF_RAW + RAW_SLOTS * 512;  // 512 words for the epilogue
-constexpr int OFF_SC = OFF_AMAX + 2048;    // factors of every stage, then the ring
+constexpr int FACTOR_BYTES = 2 * FACTORS * 4 + 512;  // a stage's two lists (two weight blocks), its token scales
+constexpr int OFF_AMAX = 1024;             // after the barriers: 512 words for the epilogue
+constexpr int OFF_SC = OFF_AMAX + 2048;    // factors and token scales of every stage, then the ring
 constexpr int SMEM_ALLOC = 232448;         // the per-block maximum (227 KiB), 1 KiB of it aligns the base
 constexpr int SMEM_USE = SMEM_ALLOC - 1024;
 constexpr uint32_t TMEM_COLS = 512;
@@ -230,27 +232,24 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
 
 struct Bars {
-  uint64_t full[MAX_STAGES];      // codes of a stage have landed and both CTAs' factors are written (even CTAs)
+  // even CTAs: the codes of a stage have landed, both CTAs' factors are written and the eight warps
+  // of both CTAs have read the accumulator
+  uint64_t full[MAX_STAGES];
   uint64_t done[MAX_STAGES];      // its MMAs are done: the stage is free and the group's sums are readable
-  uint64_t acc_empty[4];          // both CTAs' warps have read an accumulator (even CTAs)
-  uint64_t raw_full[RAW_SLOTS], raw_empty[RAW_SLOTS];
+  uint64_t raw_full[MAX_STAGES];  // the token scales of a stage have landed
   uint64_t part_full;             // few tokens: the cluster's parts of this CTA's tokens have arrived
   uint64_t part_free;             // every CTA of the cluster has read its parts
   uint64_t drain;
   uint32_t tmem_slot;
   int abort;
 };
-static_assert(sizeof(Bars) <= OFF_RAW, "barriers overrun their area");
+static_assert(sizeof(Bars) <= OFF_AMAX, "barriers overrun their area");
 
 __device__ __forceinline__ void init_bars(Bars& bars, int split) {
   for (int s = 0; s < MAX_STAGES; ++s) {
-    mbar_init(&bars.full[s], 3);  // the producer of codes, the factor warps of both CTAs
+    mbar_init(&bars.full[s], 3 + 16);  // the producer of codes, the factor warps, the readers
     mbar_init(&bars.done[s], 1);
-  }
-  for (int b = 0; b < 4; ++b) mbar_init(&bars.acc_empty[b], 16);  // eight warps of both CTAs
-  for (int s = 0; s < RAW_SLOTS; ++s) {
     mbar_init(&bars.raw_full[s], 1);
-    mbar_init(&bars.raw_empty[s], 1);
   }
   mbar_init(&bars.part_full, 1);
   mbar_init(&bars.part_free, 16 * split);
@@ -285,12 +284,11 @@ __device__ __forceinline__ void issue_mmas(Bars& bars, const Params& p, uint8_t*
   const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair));
   const uint32_t ring_u32 = smem_u32(ring), stages = static_cast<uint32_t>(p.stages);
   const uint32_t el = elect_one();
-  uint32_t s = 0, ph = 0, sa = ring_u32, b = 0, aph = 1;
+  uint32_t s = 0, ph = 0, sa = ring_u32, b = 0;
   bool ok = true;
   for (int u = cid; ok && u < p.units; u += NC) {
     for (int g = 0; g < n_groups; ++g) {
-      // (the accumulator last: it is what the MMAs wait for, and each poll costs ~110 cycles)
-      if (!mbar_wait_bounded(&bars.full[s], ph, abort) || !mbar_wait_bounded(&bars.acc_empty[b], aph, abort)) {
+      if (!mbar_wait_bounded(&bars.full[s], ph, abort)) {
         ok = false;
         break;
       }
@@ -308,10 +306,7 @@ __device__ __forceinline__ void issue_mmas(Bars& bars, const Params& p, uint8_t*
         ph ^= 1u;
         sa = ring_u32;
       }
-      if (++b == NACC) {
-        b = 0;
-        aph ^= 1u;
-      }
+      if (++b == NACC) b = 0;
     }
   }
   if (!ok && lane == 0) report_timeout(bars, p.g.status);
@@ -320,74 +315,56 @@ __device__ __forceinline__ void issue_mmas(Bars& bars, const Params& p, uint8_t*
   mbar_wait_bounded(&bars.drain, 0u, nullptr);
 }
 
-// TMA producer of the token scales of TOKENS tokens from `tok_off` of the tile (one thread).
-template <int TILE, int TOKENS>
-__device__ __forceinline__ void load_scales(Bars& bars, const Params& p, const CUtensorMap* tmS, float* raw, int g0,
-                                            int g1, int cid, int NC, int tok_off) {
-  Pos r;
-  bool ok = true;
-  for (int u = cid; ok && u < p.units; u += NC) {
-    const int tok = (u % p.tok_tiles) * TILE + tok_off;
-    for (int g = g0; g < g1; ++g) {
-      if (!mbar_wait_bounded(&bars.raw_empty[r.i], r.ph ^ 1u, &bars.abort)) {
-        ok = false;
-        break;
-      }
-      mbar_arrive_expect_tx(&bars.raw_full[r.i], TOKENS * 4);
-      tma_load_2d(raw + r.i * 128, tmS, &bars.raw_full[r.i], tok, g);
-      r.next(RAW_SLOTS);
-    }
-  }
-  if (!ok) report_timeout(bars, p.g.status);
-}
-
-// The factors of a group (a whole warp): token scales times the scales of two weight blocks, sb0 and
-// sb1 of a unit's weight tile; `put` stores token t's two factors into the stage's lists.  A list is
-// free once every reader has read an accumulator n_acc groups further on, which that group's MMAs
-// waited for: when the group stages - n_acc before this one is done.
+// Factor warp `which` of two (all lanes): the token scales of every second group times the scales of
+// two weight blocks, sb0 and sb1 of a unit's weight tile; `put` stores token t's two factors into the
+// stage's lists.  A list is free once every reader has read an accumulator n_acc groups further on,
+// which that group's MMAs waited for: when the group stages - n_acc before this one is done.
 template <int TOKENS, int COLUMNS, typename Blocks, typename Put>
-__device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const float* raw, uint8_t* sc, int g0,
-                                                int g1, int cid, int NC, int lane, uint32_t lead, Blocks blocks,
-                                                Put put) {
+__device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, uint8_t* sc, int g0, int g1, int cid,
+                                                int NC, int which, int lane, uint32_t lead, Blocks blocks, Put put) {
   const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(COLUMNS);
   const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead), el = lane == 0;
-  Pos r, s, done;
-  uint32_t n = 0;
+  Pos s, done;
+  uint32_t n = 0;  // groups so far
   bool ok = true;
   for (int u = cid; ok && u < p.units; u += NC) {
     const float *sb0, *sb1;
     blocks(u / p.tok_tiles, sb0, sb1);
     float b0 = 0.f, b1 = 0.f;  // 32 groups' block scales, one per lane
-    for (int g = g0; g < g1; ++g) {
+    for (int g = g0; g < g1; ++g, ++n) {
       const int i = (g - g0) & 31;
       if (i == 0 && g + lane < g1) {
         b0 = __ldg(sb0 + g + lane);
         b1 = __ldg(sb1 + g + lane);
       }
-      ok = mbar_wait_bounded(&bars.raw_full[r.i], r.ph, &bars.abort);
-      if (n >= ahead) {
-        ok = ok && mbar_wait_bounded(&bars.done[done.i], done.ph, &bars.abort);
-        done.next(stages);
-      } else {
-        ++n;
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       const float f0 = __shfl_sync(0xffffffffu, b0, i), f1 = __shfl_sync(0xffffffffu, b1, i);
+      if ((n & 1u) == static_cast<uint32_t>(which)) {
+        ok = mbar_wait_bounded(&bars.raw_full[s.i], s.ph, &bars.abort) &&
+             (n < ahead || mbar_wait_bounded(&bars.done[done.i], done.ph, &bars.abort));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        float* lists = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES);
+        const float* raw = lists + 2 * FACTORS;
 #pragma unroll
-      for (int t = lane; t < TOKENS; t += 32) {
-        const float v = raw[r.i * 128 + t];
-        put(reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES), t, v * f0, v * f1);
+        for (int t = lane; t < TOKENS; t += 32) {
+          const float v = raw[t];
+          put(lists, t, v * f0, v * f1);
+        }
+        fence_cta();  // the factors are read in this CTA only
+        __syncwarp();
+        mbar_arrive_cluster_relaxed(full_lead + s.i * 8, el);
       }
-      fence_cta();  // the factors are read in this CTA only
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.raw_empty[r.i]);
-      mbar_arrive_cluster_relaxed(full_lead + s.i * 8, el);
-      r.next(RAW_SLOTS);
       s.next(stages);
+      if (n >= ahead) done.next(stages);
     }
   }
   if (!ok && lane == 0) report_timeout(bars, p.g.status);
+}
+
+// Eight reader warps: the accumulators are free at first.
+__device__ __forceinline__ void free_accumulators(Bars& bars, uint32_t lead, uint32_t n_accumulators, uint32_t el) {
+  const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead);
+  for (uint32_t s = 0; s < n_accumulators; ++s) mbar_arrive_cluster_relaxed(full_lead + s * 8, el);
 }
 
 // What every thread does last.
@@ -431,7 +408,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem);
-  float* raw = reinterpret_cast<float*>(smem + OFF_RAW);
   uint8_t* sc = smem + OFF_SC;
   uint32_t* amax = reinterpret_cast<uint32_t*>(smem + OFF_AMAX);  // [2][2][128]
   uint8_t* ring = smem + p.ring_off;
@@ -479,6 +455,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* a = ring + s.i * static_cast<uint32_t>(p.stage_bytes);
           const uint32_t bar = mapa_shared(smem_u32(&bars.full[s.i]), 0);
           if (h == 0) mbar_arrive_expect_tx(&bars.full[s.i], 4u * A_BYTES);
+          float* raw = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES) + 2 * FACTORS;
+          mbar_arrive_expect_tx(&bars.raw_full[s.i], 128 * 4);
+          tma_load_2d(raw, &tmS, &bars.raw_full[s.i], tt * 256 + h * 128, g);
           tma_load_2d_pair(a, &tmX, bar, g * 128, tt * 256 + h * 128);
           tma_load_2d_pair(a + A_BYTES, w_map, bar, g * 128, wrow);
           s.next(stages);
@@ -487,11 +466,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) report_timeout(bars, p.g.status);
     } else if (warp == 1 && h == 0) {
       issue_mmas<256>(bars, p, ring, tmem, G, cid, NC, 0, rank, lane);
-    } else if (warp == 2 && lane == 0) {
-      load_scales<256, 128>(bars, p, &tmS, raw, 0, G, cid, NC, h * 128);
-    } else if (warp == 3) {
+    } else if (warp >= 2) {
       multiply_scales<128, 256>(
-          bars, p, raw, sc, 0, G, cid, NC, lane, 0,
+          bars, p, sc, 0, G, cid, NC, warp - 2, lane, 0,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // features past the last block are zeros: any block's scale will do
             const int last = (p.width - 1) >> 7;
@@ -499,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             sb1 = SWIGLU ? p.g.b2_scale + static_cast<long long>(wt) * p.g.ld_b2s
                          : p.g.b_scale + static_cast<long long>(min(wt * 2 + 1, last)) * p.g.ld_bs;
           },
-          [](float* slot, int t, float v0, float v1) {
+          [&](float* slot, int t, float v0, float v1) {
             slot[t] = v0;
             slot[FACTORS + t] = v1;
           });
@@ -510,15 +487,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, w = (warp >> 2) - 1;
     const int row = threadIdx.x & 127;  // this thread's token of the CTA's
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t acc_empty_lead = mapa_shared(smem_u32(bars.acc_empty), 0);
+    const uint32_t full_lead = mapa_shared(smem_u32(bars.full), 0);
     // first column of the four reads of 32: SwiGLU takes two of the gate and two of the up features
     const auto column = [&](int c) {
       return static_cast<uint32_t>(SWIGLU ? (c >> 1) * 128 + w * 64 + (c & 1) * 32 : w * 128 + c * 32);
     };
     uint8_t* mine = smem + p.out_off + (warp - 4) * 2 * SLAB;
     const uint32_t el = lane == 0;
+    free_accumulators(bars, 0, 2, el);
     Pos st;
-    uint32_t b = 0, slab_no = 0;
+    uint32_t b = 0, slab_no = 0, next_use = 2;  // next_use: the stage whose MMAs overwrite accumulator b
     bool ok = true;
     int nth = 0;
     for (int u = cid; u < p.units; u += NC, ++nth) {
@@ -560,7 +538,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld32x32(tacc + column(c + 1), v[(c + 1) & 1]);
           } else {
             tc_fence_before();
-            mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8, el);
+            mbar_arrive_cluster_relaxed(full_lead + next_use * 8, el);
+            if (++next_use == stages) next_use = 0;
             b ^= 1u;
             st.next(stages);
             sums(c);
@@ -707,7 +686,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem);
-  float* raw = reinterpret_cast<float*>(smem + OFF_RAW);
   uint8_t* sc = smem + OFF_SC;
   uint8_t* ring = smem + p.ring_off;
   volatile int* abort = &bars.abort;
@@ -761,17 +739,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             tma_load_2d_pair(a, &tmW, bar, g * 128, wt * 256 + h * 128);
           }
           tma_load_2d_pair(a + A_BYTES, &tmX, bar, g * 128, tt * BT + h * HB);
+          float* raw = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES) + 2 * FACTORS;
+          mbar_arrive_expect_tx(&bars.raw_full[s.i], BT * 4);
+          tma_load_2d(raw, &tmS, &bars.raw_full[s.i], tt * BT, g);
           s.next(stages);
         }
       }
       if (!ok) report_timeout(bars, p.g.status);
     } else if (warp == 1 && h == 0) {
       issue_mmas<BT>(bars, p, ring, tmem, g1 - g0, cid, NC, pair, rank, lane);
-    } else if (warp == 2 && lane == 0) {
-      load_scales<BT, BT>(bars, p, &tmS, raw, g0, g1, cid, NC, 0);
-    } else if (warp == 3) {
+    } else if (warp >= 2) {
       multiply_scales<BT, BT>(
-          bars, p, raw, sc, g0, g1, cid, NC, lane, lead,
+          bars, p, sc, g0, g1, cid, NC, warp - 2, lane, lead,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // rows past the last block are zeros: any block's scale will do
             const int blk = SWIGLU ? wt : min(wt * 2 + h, (p.width - 1) >> 7);
@@ -794,14 +773,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int et = threadIdx.x - 128;  // thread of the eight warps
     const int ri = lane >> 2, ci = (lane & 3) * 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t acc_empty_lead = mapa_shared(smem_u32(bars.acc_empty), lead);
+    const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead);
     const float* part = reinterpret_cast<const float*>(smem + p.out_off);  // [CS][per][PART_PITCH]
     const uint32_t part_u32 = smem_u32(part), part_full_u32 = smem_u32(&bars.part_full);
     const int CS = 2 * p.split;
-    const int per = BT / CS;  // tokens that each CTA of the cluster finishes (even: BT is a multiple of 16)
+    const int per = (BT / 2 + CS - 1) / CS * 2;  // tokens that each CTA of the cluster finishes, an even number
+    const int mine = max(0, min(per, BT - static_cast<int>(rank) * per));
     const uint32_t el = lane == 0;
+    free_accumulators(bars, lead, NACC, el);
     Pos st;
-    uint32_t b = 0;
+    uint32_t b = 0, next_use = NACC;  // next_use: the stage whose MMAs overwrite accumulator b
     bool ok = true;
     int nth = 0;
     auto give_up = [&]() {
@@ -832,7 +813,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_wait_ld_of<N8 * 4>(lo);
         tmem_wait_ld_of<N8 * 4>(hi);
         tc_fence_before();
-        mbar_arrive_cluster_relaxed(acc_empty_lead + b * 8, el);
+        mbar_arrive_cluster_relaxed(full_lead + next_use * 8, el);
+        if (++next_use == stages) next_use = 0;
         if (++b == NACC) b = 0;
         st.next(stages);
 #pragma unroll
@@ -846,9 +828,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
       // ------------------------------------------------------------------ epilogue
       const uint32_t parity = nth & 1;
-      const int n = min(per, p.g.M - t0 - static_cast<int>(rank) * per);  // tokens to finish here (none: <= 0)
+      const int n = min(mine, p.g.M - t0 - static_cast<int>(rank) * per);  // tokens to finish here (none: <= 0)
       const int tok0 = t0 + static_cast<int>(rank) * per;
-      if (et == 0) mbar_arrive_expect_tx(&bars.part_full, static_cast<uint32_t>(BT * ROWS * 4));
+      if (et == 0) mbar_arrive_expect_tx(&bars.part_full, static_cast<uint32_t>(mine * CS * ROWS * 4));
       // the parts of the previous tile have been read by the whole cluster
       if (ok && !mbar_wait_cluster(&bars.part_free, parity ^ 1u, abort)) give_up();
       __syncwarp();
@@ -987,10 +969,10 @@ Kernel kernel_of(int bt, int epilogue) {
 
 // Clusters of `cs` CTAs that are resident at once (one CTA per SM), per device.
 int resident_clusters(int cs) {
-  static std::atomic<int> cache[3][64];
+  static std::atomic<int> cache[4][64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const int ci = cs == 2 ? 0 : cs == 4 ? 1 : 2;
+  const int ci = cs / 2 - 1;
   if (dev >= 0 && dev < 64) {
     const int v = cache[ci][dev].load();
     if (v > 0) return v;
@@ -1032,7 +1014,7 @@ Plan plan(const Fp8Gemm& g) {
   double best_us = 1e30;
   auto consider = [&](int bt, int split) {
     if (forced && forced != bt * 8 + split) return;
-    while (split > groups) split /= 2;
+    split = std::min(split, groups);
     const int clusters = resident_clusters(2 * split);
     if (clusters <= 0) return;
     const long long tiles = (g.M + bt - 1) / bt, units = tiles * w_tiles;
@@ -1043,7 +1025,9 @@ Plan plan(const Fp8Gemm& g) {
     const double us = waves * ((groups + split - 1) / split * kb + epi) / 1800.0;
     if (us < best_us) {
       const int stage = A_BYTES + (tokens ? A_BYTES : bt * 64);
-      const int out = tokens ? 16 * SLAB : (bt * PART_PITCH * 4 + 1023) / 1024 * 1024;
+      // (parts: 2 split CTAs' sums of as many tokens as one CTA finishes)
+      const int per = (bt / 2 + 2 * split - 1) / (2 * split) * 2;
+      const int out = tokens ? 16 * SLAB : (2 * split * per * PART_PITCH * 4 + 1023) / 1024 * 1024;
       best_us = us;
       const int room = SMEM_USE - OFF_SC - 1023 - out;
       best = Plan{bt, split, clusters, std::min(MAX_STAGES, room / (stage + FACTOR_BYTES)), stage, 0, 0};
@@ -1052,7 +1036,7 @@ Plan plan(const Fp8Gemm& g) {
     }
   };
   for (int bt : {16, 32, 48, 64, 80, 96, 128})
-    for (int split : {1, 2, 4}) consider(bt, split);
+    for (int split = 1; split <= 4; ++split) consider(bt, split);
   consider(256, 1);
   return best;
 }
@@ -1064,7 +1048,7 @@ bool gemm_fp8_set_plan(int tokens, int split) {
     g_plan.store(0);
     return true;
   }
-  if (!kernel_of(tokens, CB_FP8_STORE_F32) || (split != 1 && split != 2 && split != 4) || (tokens == 256 && split != 1)) return false;
+  if (!kernel_of(tokens, CB_FP8_STORE_F32) || split < 1 || split > 4 || (tokens == 256 && split != 1)) return false;
   g_plan.store(tokens * 8 + split);
   return true;
 }

@@ -227,8 +227,8 @@ def test_gemm_of_any_number_of_features(m, width, epi):
     assert untouched(whole, m, width)
 
 
-PLANS = [(16, 1), (16, 2), (16, 4), (32, 1), (32, 4), (48, 1), (48, 4), (64, 1), (64, 2), (80, 1), (80, 4), (96, 2), (128, 1),
-         (128, 2), (128, 4), (256, 1)]
+PLANS = [(16, 1), (16, 2), (16, 3), (16, 4), (32, 1), (32, 3), (32, 4), (48, 1), (48, 4), (64, 1), (64, 2), (80, 1), (80, 4), (96, 2), (128, 1),
+         (128, 2), (128, 3), (128, 4), (256, 1)]
 
 
 @pytest.fixture(params=PLANS)
