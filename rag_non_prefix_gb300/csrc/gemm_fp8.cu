@@ -15,9 +15,10 @@
 //     cost a shared-memory cycle per warp, group and four columns, which is why this form does not
 //     serve many tokens: at 256 tokens a group took ~1100 cycles with them and ~850 without.
 // Roles of the warps, in both:
-//   warp 0: TMA producer of codes and token scales
+//   warp 0: TMA producer of codes
 //   warp 1: tensor-memory owner, in even CTAs the MMA issuer
-//   warps 2, 3: multiply the token scales by the weight blocks' scales, a group each in turn
+//   warps 2, 3: load the token scales and multiply them by the weight blocks' scales, a group each
+//   in turn
 //   warps 4-11: scaling, sums and epilogue
 // A barrier poll costs ~110 cycles even when the phase is long over (measured), so that every role
 // waits for one barrier per group where it can: a stage's `full` barrier counts its codes, its
@@ -42,9 +43,11 @@ constexpr int ROWS = 128;                  // rows of the tensor core's tile per
 constexpr int A_BYTES = ROWS * 128;        // 16 KiB: 128 rows x one group of channels
 constexpr int MAX_STAGES = 12;
 constexpr int FACTORS = 2 * 4 * 20;        // token times block scales: 128 tokens, or two warpgroups x four thread classes x (16 + 4)
-constexpr int FACTOR_BYTES = 2 * FACTORS * 4 + 512;  // a stage's two lists (two weight blocks), its token scales
+constexpr int FACTOR_BYTES = 2 * FACTORS * 4;  // a stage's two lists (two weight blocks)
+constexpr int RAW_SLOTS = 4;               // token scales as loaded, per factor warp: slots of 128 floats
 constexpr int OFF_AMAX = 1024;             // after the barriers: 512 words for the epilogue
-constexpr int OFF_SC = OFF_AMAX + 2048;    // factors and token scales of every stage, then the ring
+constexpr int OFF_RAW = OFF_AMAX + 2048;
+constexpr int OFF_SC = OFF_RAW + 2 * RAW_SLOTS * 512;  // factors of every stage, then the ring
 constexpr int SMEM_ALLOC = 232448;         // the per-block maximum (227 KiB), 1 KiB of it aligns the base
 constexpr int SMEM_USE = SMEM_ALLOC - 1024;
 constexpr uint32_t TMEM_COLS = 512;
@@ -97,6 +100,25 @@ __device__ __forceinline__ uint32_t elect_one() {
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(el));
   return el;
+}
+// tma_load_2d_pair and the arrival that expects its bytes, by the elected lane of a converged warp
+__device__ __forceinline__ void tma_load_2d_pair_elected(uint32_t smem_dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                                         int c1, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_expect_tx_elected(uint32_t bar, uint32_t bytes, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(el)
+      : "memory");
 }
 // tc_commit_pair_mc by the elected lane of a converged warp
 __device__ __forceinline__ void commit_pair_mc_elected(uint64_t* bar, uint16_t cta_mask, uint32_t el) {
@@ -236,7 +258,7 @@ struct Bars {
   // of both CTAs have read the accumulator
   uint64_t full[MAX_STAGES];
   uint64_t done[MAX_STAGES];      // its MMAs are done: the stage is free and the group's sums are readable
-  uint64_t raw_full[MAX_STAGES];  // the token scales of a stage have landed
+  uint64_t raw_full[2][RAW_SLOTS];  // token scales of a factor warp have landed
   uint64_t part_full;             // few tokens: the cluster's parts of this CTA's tokens have arrived
   uint64_t part_free;             // every CTA of the cluster has read its parts
   uint64_t drain;
@@ -249,8 +271,8 @@ __device__ __forceinline__ void init_bars(Bars& bars, int split) {
   for (int s = 0; s < MAX_STAGES; ++s) {
     mbar_init(&bars.full[s], 3 + 16);  // the producer of codes, the factor warps, the readers
     mbar_init(&bars.done[s], 1);
-    mbar_init(&bars.raw_full[s], 1);
   }
+  for (int s = 0; s < 2 * RAW_SLOTS; ++s) mbar_init(&bars.raw_full[0][s], 1);
   mbar_init(&bars.part_full, 1);
   mbar_init(&bars.part_free, 16 * split);
   mbar_init(&bars.drain, 1);
@@ -315,16 +337,67 @@ __device__ __forceinline__ void issue_mmas(Bars& bars, const Params& p, uint8_t*
   mbar_wait_bounded(&bars.drain, 0u, nullptr);
 }
 
-// Factor warp `which` of two (all lanes): the token scales of every second group times the scales of
-// two weight blocks, sb0 and sb1 of a unit's weight tile; `put` stores token t's two factors into the
-// stage's lists.  A list is free once every reader has read an accumulator n_acc groups further on,
-// which that group's MMAs waited for: when the group stages - n_acc before this one is done.
-template <int TOKENS, int COLUMNS, typename Blocks, typename Put>
-__device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, uint8_t* sc, int g0, int g1, int cid,
-                                                int NC, int which, int lane, uint32_t lead, Blocks blocks, Put put) {
+// TMA producer of codes (a whole warp): `load` starts the copies of group g into stage s.  The
+// stages are waited for in pairs: the second one's MMAs are done after the first one's.
+template <typename Load>
+__device__ __forceinline__ void load_codes(Bars& bars, const Params& p, int g0, int g1, int cid, int NC, int lane,
+                                           Load load) {
+  const uint32_t stages = static_cast<uint32_t>(p.stages);
+  Pos s;
+  bool ok = true;
+  for (int u = cid; ok && u < p.units; u += NC) {
+    const int wt = u / p.tok_tiles, tt = u - wt * p.tok_tiles;
+    for (int g = g0; g < g1; g += 2) {
+      Pos second = s;
+      if (g + 1 < g1) second.next(stages);
+      if (!mbar_wait_bounded(&bars.done[second.i], second.ph ^ 1u, &bars.abort)) {
+        ok = false;
+        break;
+      }
+      load(s.i, wt, tt, g);
+      if (g + 1 < g1) load(second.i, wt, tt, g + 1);
+      s = second;
+      s.next(stages);
+    }
+  }
+  if (!ok && lane == 0) report_timeout(bars, p.g.status);
+}
+
+// Factor warp `which` of two (all lanes): loads the token scales of every second group, RAW_SLOTS of
+// them ahead, and multiplies them by the scales of two weight blocks, sb0 and sb1 of a unit's weight
+// tile; `put` stores token t's two factors into the stage's lists.  A list is free once every reader
+// has read an accumulator n_acc groups further on, which that group's MMAs waited for: when the
+// group stages - n_acc before this one is done.
+template <int TILE, int TOKENS, int COLUMNS, typename Blocks, typename Put>
+__device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const CUtensorMap* tmS, uint8_t* smem,
+                                                int g0, int g1, int cid, int NC, int which, int lane, uint32_t lead,
+                                                int tok_off, Blocks blocks, Put put) {
   const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(COLUMNS);
   const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead), el = lane == 0;
-  Pos s, done;
+  float* raw = reinterpret_cast<float*>(smem + OFF_RAW) + which * RAW_SLOTS * 128;
+  uint8_t* sc = smem + OFF_SC;
+  // the groups of this warp in their order, for the copies: unit, group
+  int lu = cid, lg = g0 + which;
+  while (lu < p.units && lg >= g1) {
+    lg -= g1 - g0;
+    lu += NC;
+  }
+  uint32_t slot_in = 0;
+  auto load_next = [&]() {
+    if (lu >= p.units) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars.raw_full[which][slot_in], TOKENS * 4);
+      tma_load_2d(raw + slot_in * 128, tmS, &bars.raw_full[which][slot_in], (lu % p.tok_tiles) * TILE + tok_off, lg);
+    }
+    if (++slot_in == RAW_SLOTS) slot_in = 0;
+    lg += 2;
+    while (lu < p.units && lg >= g1) {
+      lg -= g1 - g0;
+      lu += NC;
+    }
+  };
+  for (int i = 0; i < RAW_SLOTS; ++i) load_next();
+  Pos s, done, r;
   uint32_t n = 0;  // groups so far
   bool ok = true;
   for (int u = cid; ok && u < p.units; u += NC) {
@@ -337,22 +410,23 @@ __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, uin
         b0 = __ldg(sb0 + g + lane);
         b1 = __ldg(sb1 + g + lane);
       }
-      const float f0 = __shfl_sync(0xffffffffu, b0, i), f1 = __shfl_sync(0xffffffffu, b1, i);
       if ((n & 1u) == static_cast<uint32_t>(which)) {
-        ok = mbar_wait_bounded(&bars.raw_full[s.i], s.ph, &bars.abort) &&
+        const float f0 = __shfl_sync(0xffffffffu, b0, i), f1 = __shfl_sync(0xffffffffu, b1, i);
+        ok = mbar_wait_bounded(&bars.raw_full[which][r.i], r.ph, &bars.abort) &&
              (n < ahead || mbar_wait_bounded(&bars.done[done.i], done.ph, &bars.abort));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         float* lists = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES);
-        const float* raw = lists + 2 * FACTORS;
 #pragma unroll
         for (int t = lane; t < TOKENS; t += 32) {
-          const float v = raw[t];
+          const float v = raw[r.i * 128 + t];
           put(lists, t, v * f0, v * f1);
         }
         fence_cta();  // the factors are read in this CTA only
         __syncwarp();
         mbar_arrive_cluster_relaxed(full_lead + s.i * 8, el);
+        load_next();  // into the slot just read
+        r.next(RAW_SLOTS);
       }
       s.next(stages);
       if (n >= ahead) done.next(stages);
@@ -440,35 +514,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < 4) {
     few_registers();
-    if (warp == 0 && lane == 0) {
-      Pos s;
-      bool ok = true;
+    if (warp == 0) {
+      const uint32_t el = elect_one(), ring_u32 = smem_u32(ring), full_lead = mapa_shared(smem_u32(bars.full), 0);
       const CUtensorMap* w_map = SWIGLU && h ? &tmW2 : &tmW;
-      for (int u = cid; ok && u < p.units; u += NC) {
-        const int wt = u / p.tok_tiles, tt = u - wt * p.tok_tiles;
-        const int wrow = SWIGLU ? wt * 128 : wt * 256 + h * 128;
-        for (int g = 0; g < G; ++g) {
-          if (!mbar_wait_bounded(&bars.done[s.i], s.ph ^ 1u, abort)) {
-            ok = false;
-            break;
-          }
-          uint8_t* a = ring + s.i * static_cast<uint32_t>(p.stage_bytes);
-          const uint32_t bar = mapa_shared(smem_u32(&bars.full[s.i]), 0);
-          if (h == 0) mbar_arrive_expect_tx(&bars.full[s.i], 4u * A_BYTES);
-          float* raw = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES) + 2 * FACTORS;
-          mbar_arrive_expect_tx(&bars.raw_full[s.i], 128 * 4);
-          tma_load_2d(raw, &tmS, &bars.raw_full[s.i], tt * 256 + h * 128, g);
-          tma_load_2d_pair(a, &tmX, bar, g * 128, tt * 256 + h * 128);
-          tma_load_2d_pair(a + A_BYTES, w_map, bar, g * 128, wrow);
-          s.next(stages);
-        }
-      }
-      if (!ok) report_timeout(bars, p.g.status);
+      load_codes(bars, p, 0, G, cid, NC, lane, [&](uint32_t s, int wt, int tt, int g) {
+        const uint32_t a = ring_u32 + s * static_cast<uint32_t>(p.stage_bytes), bar = full_lead + s * 8;
+        if (h == 0) arrive_expect_tx_elected(smem_u32(&bars.full[s]), 4u * A_BYTES, el);
+        tma_load_2d_pair_elected(a, &tmX, bar, g * 128, tt * 256 + h * 128, el);
+        tma_load_2d_pair_elected(a + A_BYTES, w_map, bar, g * 128, SWIGLU ? wt * 128 : wt * 256 + h * 128, el);
+      });
     } else if (warp == 1 && h == 0) {
       issue_mmas<256>(bars, p, ring, tmem, G, cid, NC, 0, rank, lane);
     } else if (warp >= 2) {
-      multiply_scales<128, 256>(
-          bars, p, sc, 0, G, cid, NC, warp - 2, lane, 0,
+      multiply_scales<256, 128, 256>(
+          bars, p, &tmS, smem, 0, G, cid, NC, warp - 2, lane, 0, h * 128,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // features past the last block are zeros: any block's scale will do
             const int last = (p.width - 1) >> 7;
@@ -719,38 +778,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < 4) {
     few_registers();
-    if (warp == 0 && lane == 0) {
-      Pos s;
-      bool ok = true;
-      for (int u = cid; ok && u < p.units; u += NC) {
-        const int wt = u / p.tok_tiles, tt = u - wt * p.tok_tiles;
-        for (int g = g0; g < g1; ++g) {
-          if (!mbar_wait_bounded(&bars.done[s.i], s.ph ^ 1u, abort)) {
-            ok = false;
-            break;
-          }
-          uint8_t* a = ring + s.i * static_cast<uint32_t>(p.stage_bytes);
-          const uint32_t bar = mapa_shared(smem_u32(&bars.full[s.i]), lead);
-          if (h == 0) mbar_arrive_expect_tx(&bars.full[s.i], 2u * (A_BYTES + HB * 128));
-          if (SWIGLU) {
-            tma_load_2d_pair(a, &tmW, bar, g * 128, wt * 128 + h * 64);
-            tma_load_2d_pair(a + A_BYTES / 2, &tmW2, bar, g * 128, wt * 128 + h * 64);
-          } else {
-            tma_load_2d_pair(a, &tmW, bar, g * 128, wt * 256 + h * 128);
-          }
-          tma_load_2d_pair(a + A_BYTES, &tmX, bar, g * 128, tt * BT + h * HB);
-          float* raw = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES) + 2 * FACTORS;
-          mbar_arrive_expect_tx(&bars.raw_full[s.i], BT * 4);
-          tma_load_2d(raw, &tmS, &bars.raw_full[s.i], tt * BT, g);
-          s.next(stages);
+    if (warp == 0) {
+      const uint32_t el = elect_one(), ring_u32 = smem_u32(ring), full_lead = mapa_shared(smem_u32(bars.full), lead);
+      load_codes(bars, p, g0, g1, cid, NC, lane, [&](uint32_t s, int wt, int tt, int g) {
+        const uint32_t a = ring_u32 + s * static_cast<uint32_t>(p.stage_bytes), bar = full_lead + s * 8;
+        if (h == 0) arrive_expect_tx_elected(smem_u32(&bars.full[s]), 2u * (A_BYTES + HB * 128), el);
+        if (SWIGLU) {
+          tma_load_2d_pair_elected(a, &tmW, bar, g * 128, wt * 128 + h * 64, el);
+          tma_load_2d_pair_elected(a + A_BYTES / 2, &tmW2, bar, g * 128, wt * 128 + h * 64, el);
+        } else {
+          tma_load_2d_pair_elected(a, &tmW, bar, g * 128, wt * 256 + h * 128, el);
         }
-      }
-      if (!ok) report_timeout(bars, p.g.status);
+        tma_load_2d_pair_elected(a + A_BYTES, &tmX, bar, g * 128, tt * BT + h * HB, el);
+      });
     } else if (warp == 1 && h == 0) {
       issue_mmas<BT>(bars, p, ring, tmem, g1 - g0, cid, NC, pair, rank, lane);
     } else if (warp >= 2) {
-      multiply_scales<BT, BT>(
-          bars, p, sc, g0, g1, cid, NC, warp - 2, lane, lead,
+      multiply_scales<BT, BT, BT>(
+          bars, p, &tmS, smem, g0, g1, cid, NC, warp - 2, lane, lead, 0,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // rows past the last block are zeros: any block's scale will do
             const int blk = SWIGLU ? wt : min(wt * 2 + h, (p.width - 1) >> 7);
