@@ -52,7 +52,7 @@ constexpr int SMEM_ALLOC = 232448;         // the per-block maximum (227 KiB), 1
 constexpr int SMEM_USE = SMEM_ALLOC - 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int PART_PITCH = ROWS + 4;       // floats per token and source CTA of the parts (few tokens)
-constexpr int SLAB = 2048;                 // many tokens: a warp stages 32 tokens x 64 bytes, twice
+constexpr int SLAB = 2048;                 // many tokens: a warp stages 32 tokens x 64 bytes twice, or x 128 bytes
 
 // Accumulators in tensor memory: as many groups' sums as fit may wait to be read.
 __host__ __device__ constexpr int n_acc(int columns) { return columns <= 128 ? 4 : 2; }
@@ -65,8 +65,6 @@ struct Params {
   int groups;       // ceil(K / 128)
   int stages, stage_bytes;
   int ring_off, out_off;  // codes of the stages; output area
-  int add_in_place;
-  int ragged;       // output rows end inside 16 bytes: a TMA store would write up to the 16th
 };
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
@@ -248,6 +246,10 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
       : "memory");
 }
 __device__ __forceinline__ void fence_cta() { asm volatile("fence.acq_rel.cta;" ::: "memory"); }
+// 16-byte aligned range of global memory into L2 (whole 16 bytes)
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -367,13 +369,14 @@ __device__ __forceinline__ void load_codes(Bars& bars, const Params& p, int g0, 
 
 // Factor warp `which` of two (all lanes): loads the token scales of every second group, RAW_SLOTS of
 // them ahead, and multiplies them by the scales of two weight blocks, sb0 and sb1 of a unit's weight
-// tile; `put` stores token t's two factors into the stage's lists.  A list is free once every reader
+// tile; `put` stores token t's two factors into the stage's lists; `unit` is called as a unit begins.
+// A list is free once every reader
 // has read an accumulator n_acc groups further on, which that group's MMAs waited for: when the
 // group stages - n_acc before this one is done.
-template <int TILE, int TOKENS, int COLUMNS, typename Blocks, typename Put>
+template <int TILE, int TOKENS, int COLUMNS, typename Blocks, typename Put, typename Unit>
 __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const CUtensorMap* tmS, uint8_t* smem,
                                                 int g0, int g1, int cid, int NC, int which, int lane, uint32_t lead,
-                                                int tok_off, Blocks blocks, Put put) {
+                                                int tok_off, Blocks blocks, Put put, Unit unit) {
   const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(COLUMNS);
   const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead), el = lane == 0;
   float* raw = reinterpret_cast<float*>(smem + OFF_RAW) + which * RAW_SLOTS * 128;
@@ -405,6 +408,7 @@ __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, con
   for (int u = cid; ok && u < p.units; u += NC) {
     const float *sb0, *sb1;
     blocks(u / p.tok_tiles, sb0, sb1);
+    unit(u);
     float b0 = 0.f, b1 = 0.f;  // 32 groups' block scales, one per lane
     for (int g = g0; g < g1; ++g, ++n) {
       const int i = (g - g0) & 31;
@@ -472,8 +476,7 @@ __device__ __forceinline__ void many_registers() { asm volatile("setmaxnreg.inc.
 // ============================================================================= many tokens
 // Tokens on the rows: thread r of a warpgroup holds token r of this CTA's 128, warpgroup w the
 // features 128 w .. of the tile's 256 (SwiGLU: gate and up of features 64 w .. of 128; the pair's
-// even CTA stages the gate rows, the odd one the up rows).  Output goes through slabs of 32 tokens
-// x 64 bytes per warp, stored by TMA.
+// even CTA stages the gate rows, the odd one the up rows).
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_tokens_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     prefetch_tmap(&tmX);
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmS);
-    prefetch_tmap(&tmC);
+    if (SWIGLU || EPI == CB_FP8_STORE_BF16) prefetch_tmap(&tmC);
   }
   if (warp == 1) {
     tmem_alloc_pair(&bars.tmem_slot, TMEM_COLS);
@@ -540,6 +543,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           [&](float* slot, int t, float v0, float v1) {
             slot[t] = v0;
             slot[FACTORS + t] = v1;
+          },
+          [&](int u) {
+            // the tile's addend on its way to L2 while its products are summed: 64 tokens a warp
+            if (EPI != CB_FP8_ADD_F32 || p.width % 4 != 0) return;
+            const int wt = u / p.tok_tiles, tt = u - wt * p.tok_tiles;
+            const uint32_t bytes = static_cast<uint32_t>(min(256, p.width - wt * 256)) * 4u;
+            for (int r = lane; r < 64; r += 32) {
+              const int tok = tt * 256 + h * 128 + (warp - 2) * 64 + r;
+              if (tok < p.g.M) prefetch_l2(p.g.addend + static_cast<long long>(tok) * p.g.ldc + wt * 256, bytes);
+            }
           });
     }
     __syncwarp();
@@ -561,8 +574,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     int nth = 0;
     for (int u = cid; u < p.units; u += NC, ++nth) {
-      const int wt = u / p.tok_tiles, tt = u - wt * p.tok_tiles;
-      const int t0 = tt * 256 + h * 128 + quarter * 32;  // the warp's first token
       uint64_t acc[4][16];  // [read][pair of features]
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -611,10 +622,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
 
       // ------------------------------------------------------------------ epilogue
-      // 64 bytes of this thread's token into the next slab (64-byte swizzle), stored at feature f
+      // (an index the compiler cannot know earlier: addresses computed before the sums would be spilled)
+      int tile = u;
+      asm volatile("" : "+r"(tile));
+      const int wt = tile / p.tok_tiles, tt = tile - wt * p.tok_tiles;
+      const int t0 = tt * 256 + h * 128 + quarter * 32;  // the warp's first token
+      // 64 bytes of this thread's token into the next slab (64-byte swizzle), stored by TMA at feature f
       auto put = [&](const uint4* q, int f) {
-        uint8_t* slab = mine + (slab_no & 1u) * SLAB;
-        ++slab_no;
+        uint8_t* slab = mine + (slab_no++ & 1u) * SLAB;
         if (lane == 0) bulk_wait_read_all_but_1();
         __syncwarp();
 #pragma unroll
@@ -622,13 +637,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           *reinterpret_cast<uint4*>(slab + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = q[i];
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && ok) {
-          if (EPI == CB_FP8_ADD_F32 && p.add_in_place)
-            tma_reduce_add_2d(&tmC, slab, f, t0);
-          else
-            tma_store_2d(&tmC, slab, f, t0);
-          bulk_commit();
-        }
+        if (lane == 0 && ok) tma_store_2d(&tmC, slab, f, t0);
+        if (lane == 0) bulk_commit();
       };
       if constexpr (SWIGLU) {
         uint32_t m = 0;
@@ -664,66 +674,83 @@ __global__ void __launch_bounds__(THREADS, 1)
           put(q, f);
         }
       } else {
-        constexpr bool to_bf16 = EPI == CB_FP8_STORE_BF16, add = EPI == CB_FP8_ADD_F32;
-        const int tok = t0 + lane;
+        // A warp's 32 tokens x 32 features turn in its slab (rows of 128 bytes, 8-byte pieces
+        // exchanged by row), so that C is written and the addend read in whole lines, 8 lanes a row.
+        // (The addend read by the tokens' own threads, row by row, cost ~9 us a tile.  16-byte stores
+        // would tie the sums to aligned groups of four registers, which the compiler then moves about
+        // in the main loop: 2048 x 7168 x 7168 in 92 instead of 71 us.)
+        const int r4 = lane >> 3, q4 = (lane & 7) * 4;
+        constexpr int AHEAD = 4;  // reads of the addend under way
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int f0 = wt * 256 + w * 128 + c * 32;
-          if (t0 < p.g.M && f0 < p.width) {  // (uniform in the warp)
-            const long long o = static_cast<long long>(tok) * p.g.ldc + f0;
-            if (p.ragged && f0 + 32 > p.width) {  // the end of the rows, element by element
-              if (ok && tok < p.g.M) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  const float2 x = unpack2(acc[c][j >> 1]);
-                  const float y = j & 1 ? x.y : x.x;
-                  if (f0 + j >= p.width) continue;
-                  if (to_bf16)
-                    static_cast<bf16*>(p.g.c)[o + j] = __float2bfloat16_rn(y);
-                  else
-                    static_cast<float*>(p.g.c)[o + j] = add ? p.g.addend[o + j] + y : y;
-                }
-              }
-              continue;
-            }
+          const int f = wt * 256 + w * 128 + c * 32 + q4;
+          if (t0 >= p.g.M || f - q4 >= p.width) continue;  // (uniform in the warp)
+          const bool whole = f + 4 <= p.width;
+          if (EPI == CB_FP8_STORE_BF16 && (p.width % 8 == 0 || f - q4 + 32 <= p.width)) {
+            // (a TMA store ends at 16 bytes: rows that end elsewhere take the other way)
             uint4 q[4];
-            if (to_bf16) {
-              uint32_t* qw = reinterpret_cast<uint32_t*>(q);
+            uint32_t* qw = reinterpret_cast<uint32_t*>(q);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 x = unpack2(acc[c][j]);
-                qw[j] = pack_bf16x2(x.x, x.y);
-              }
-              put(q, f0);
-            } else {
-              if (add && !p.add_in_place && tok < p.g.M) {
-                const float* a = p.g.addend + o;
-                float4 d[8];
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = unpack2(acc[c][j]);
+              qw[j] = pack_bf16x2(x.x, x.y);
+            }
+            put(q, f - q4);
+            continue;
+          }
+          const long long o = static_cast<long long>(t0 + r4) * p.g.ldc + f;
+          float4 d[AHEAD];
+          auto read_addend = [&](int from) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (f0 + i * 4 < p.width) d[i] = *reinterpret_cast<const float4*>(a + i * 4);
+            for (int i = 0; i < AHEAD; ++i)
+              if (EPI == CB_FP8_ADD_F32 && whole && t0 + r4 + 4 * (from + i) < p.g.M)
+                d[i] = *reinterpret_cast<const float4*>(p.g.addend + o + 4 * (from + i) * p.g.ldc);
+          };
+          read_addend(0);
+          if (EPI == CB_FP8_STORE_BF16 && lane == 0) bulk_wait_read_all();
+          __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (f0 + i * 4 < p.width) {
-                    const float2 x = unpack2(acc[c][2 * i]), y = unpack2(acc[c][2 * i + 1]);
-                    acc[c][2 * i] = pack2(d[i].x + x.x, d[i].y + x.y);
-                    acc[c][2 * i + 1] = pack2(d[i].z + y.x, d[i].w + y.y);
-                  }
-              }
+          for (int j = 0; j < 16; ++j) *reinterpret_cast<uint64_t*>(mine + lane * 128 + ((j ^ (lane & 15)) << 3)) = acc[c][j];
+          __syncwarp();
+          const auto turned = [&](int i) {
+            const int row = r4 + 4 * i;
+            const float4 x = *reinterpret_cast<const float4*>(mine + row * 128 + ((((lane & 7) * 2) ^ (row & 14)) << 3));
+            return row & 1 ? make_float4(x.z, x.w, x.x, x.y) : x;
+          };
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                if (f0 + half * 16 >= p.width) break;
-                uint64_t* qd = reinterpret_cast<uint64_t*>(q);
+          for (int i = 0; i < 8; ++i) {
+            if (i && i % AHEAD == 0) read_addend(i);
+            const float4 x = turned(i);
+            if (!ok || !whole || t0 + r4 + 4 * i >= p.g.M) continue;
+            if (EPI == CB_FP8_STORE_BF16)
+              *reinterpret_cast<uint2*>(static_cast<bf16*>(p.g.c) + o + 4 * i * p.g.ldc) =
+                  make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+            else if (EPI == CB_FP8_ADD_F32)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + o + 4 * i * p.g.ldc) =
+                  make_float4(d[i % AHEAD].x + x.x, d[i % AHEAD].y + x.y, d[i % AHEAD].z + x.z, d[i % AHEAD].w + x.w);
+            else
+              *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + o + 4 * i * p.g.ldc) = x;
+          }
+          if (ok && !whole) {  // rows that end inside four features
+#pragma unroll 1
+            for (int i = 0; i < 8 && t0 + r4 + 4 * i < p.g.M; ++i) {
+              const float4 x = turned(i);
+              const float y[3] = {x.x, x.y, x.z};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) qd[j] = acc[c][half * 8 + j];
-                put(q, f0 + half * 16);
+              for (int k = 0; k < 3; ++k) {
+                if (f + k >= p.width) continue;
+                const long long at = o + 4 * i * p.g.ldc + k;
+                if (EPI == CB_FP8_STORE_BF16)
+                  static_cast<bf16*>(p.g.c)[at] = __float2bfloat16_rn(y[k]);
+                else
+                  static_cast<float*>(p.g.c)[at] = EPI == CB_FP8_ADD_F32 ? p.g.addend[at] + y[k] : y[k];
               }
             }
           }
         }
       }
     }
-    bulk_wait_all();
+    if (SWIGLU || EPI == CB_FP8_STORE_BF16) bulk_wait_all();
   }
   finish(bars, tmem, warp);
 }
@@ -811,7 +838,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int o = tw * (FACTORS / 2) + ((x >> 1) & 3) * 20 + (x >> 3) * 2 + (x & 1);
             slot[o] = v0;
             if (SWIGLU) slot[FACTORS + o] = v1;
-          });
+          },
+          [](int) {});
     }
     __syncwarp();
   } else {
@@ -1119,7 +1147,7 @@ bool gemm_fp8_set_plan(int tokens, int split) {
 
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.M <= 0) return cudaSuccess;
-  const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8, to_bf16 = g.epilogue == CB_FP8_STORE_BF16;
+  const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
   const Plan pl = plan(g);
   // (a stage's barrier is read until its accumulator is, and its factors are written ahead)
   if (pl.bt == 0 || pl.stages <= n_acc(pl.bt)) return cudaErrorInvalidConfiguration;
@@ -1135,10 +1163,8 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   p.stage_bytes = pl.stage_bytes;
   p.ring_off = pl.ring_off;
   p.out_off = pl.out_off;
-  p.add_in_place = g.epilogue == CB_FP8_ADD_F32 && g.addend == g.c;
-  p.ragged = !swiglu && p.width * (to_bf16 ? 2 : 4) % 16 != 0;
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, F32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B, SW64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B;
   const int w_rows = swiglu && !tokens ? 64 : 128;
   CUtensorMap mx, mw, mw2, ms, mc;
   bool ok = encode_tmap(&mx, U8, g.a, g.K, g.M, g.lda, 128, tokens ? 128 : pl.bt / 2, SW) &&
@@ -1148,10 +1174,10 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   mw2 = mw;
   if (swiglu) ok = ok && encode_tmap(&mw2, U8, g.b2, g.K, p.width, g.ldb2, 128, w_rows, SW);
   mc = mx;
-  if (tokens)
-    ok = ok && (swiglu    ? encode_tmap(&mc, U8, g.c, p.width, g.M, g.ldc, 64, 32, SW64)
-                : to_bf16 ? encode_tmap(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.c, p.width, g.M, g.ldc * 2, 32, 32, SW64)
-                          : encode_tmap(&mc, F32, g.c, p.width, g.M, g.ldc * 4, 16, 32, SW64));
+  if (tokens && swiglu) ok = ok && encode_tmap(&mc, U8, g.c, p.width, g.M, g.ldc, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (tokens && g.epilogue == CB_FP8_STORE_BF16)
+    ok = ok && encode_tmap(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.c, p.width, g.M, g.ldc * 2, 32, 32,
+                           CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return cudaErrorInvalidValue;
   Kernel fn = kernel_of(pl.bt, g.epilogue);
   static DeviceOnce once[4][17];
