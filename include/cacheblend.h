@@ -401,7 +401,8 @@ cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_
 /* Tiling of cb_gemm_scaled, process-wide (a tuning and test hook; default 0, 0: chosen per shape by
  * the library's time model).  tokens: per tile of a CTA pair, 16, 32, 48, 64, 80, 96, 128 (the
  * weights on the tensor core's rows) or 256 (the tokens on them); split: pairs of a cluster that divide the
- * channels, 1 to 4 (no more than there are groups of 128; 1 for 256 tokens).  Results agree to
+ * channels, 1 to 4 (no more than there are groups of 128; 1 for 256 tokens).  1, 0: the kernel of up
+ * to 16 tokens, where it applies (else the model's choice of the others).  Results agree to
  * fp32 rounding of the same sums.  Other values: CB_ERR_INVALID_ARG. */
 cb_status cb_gemm_scaled_set_plan(int tokens, int split);
 

@@ -1029,6 +1029,93 @@ __global__ void __launch_bounds__(THREADS, 1)
   finish(bars, tmem, warp);
 }
 
+// ============================================================================= a handful of tokens
+// Up to 16 tokens and a matrix of a few MB: the weights are streamed once through registers and the
+// warps' own matrix instruction (mma.sync m16n8k32, weights on its 16 rows, 8 tokens a column block),
+// without tensor memory, clusters and barriers, whose set-up and hand-over cost more than such a
+// matrix's bytes.  A CTA per 16 features, its 8 warps taking every eighth group; their sums are added
+// in order.  Both operands take their 32 channels in the same permuted order: lane c of four holds 16
+// consecutive bytes of a row, words 0 and 1 for one product and 2 and 3 for the next.  The instruction
+// is slow here (~70 cycles each), which ends its use at larger matrices and more tokens (handful_applies).
+__device__ __forceinline__ void mma_e4m3(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 load16_or_zero(const uint8_t* p, bool in) {
+  return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(256, NT == 1 ? 3 : 2) gemm_fp8_handful_kernel(const Fp8Gemm p) {
+  constexpr int WARPS = 8, UNROLL = 2;  // groups whose reads are under way together
+  __shared__ float red[WARPS][16][NT * 8];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int groups = (p.K + 127) / 128, row0 = blockIdx.x * 16;
+  // (rows past the last one read the last one again; their sums are not stored)
+  const uint8_t* w0 = p.b + min(row0 + r, p.N - 1) * p.ldb + c * 16;
+  const uint8_t* w8 = p.b + min(row0 + r + 8, p.N - 1) * p.ldb + c * 16;
+  const float* sb = p.b_scale + static_cast<long long>(row0 >> 7) * p.ld_bs;
+  float acc[NT][4] = {};
+  for (int gb = warp; gb < groups; gb += WARPS * UNROLL) {
+    uint4 a[UNROLL][2][2];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        const int k = (gb + u * WARPS) * 128 + ch * 64;
+        const bool in = k + c * 16 < p.K;
+        a[u][ch][0] = load16_or_zero(w0 + k, in);
+        a[u][ch][1] = load16_or_zero(w8 + k, in);
+      }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int g = gb + u * WARPS;
+      if (g >= groups) break;
+      const float f = __ldg(sb + g);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int tok = n * 8 + r;
+        float part[4] = {};
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          const int k = g * 128 + ch * 64 + c * 16;
+          const uint4 x = load16_or_zero(p.a + tok * p.lda + k, tok < p.M && k < p.K);
+          const uint4 lo = a[u][ch][0], hi = a[u][ch][1];
+          mma_e4m3(part, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+          mma_e4m3(part, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+        }
+        const int t = n * 8 + 2 * c;
+        const float* sa = p.a_scale + g * p.ld_as + t;
+        const float s0 = t < p.M ? __ldg(sa) * f : 0.f, s1 = t + 1 < p.M ? __ldg(sa + 1) * f : 0.f;
+        acc[n][0] = fmaf(part[0], s0, acc[n][0]);
+        acc[n][1] = fmaf(part[1], s1, acc[n][1]);
+        acc[n][2] = fmaf(part[2], s0, acc[n][2]);
+        acc[n][3] = fmaf(part[3], s1, acc[n][3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp][r + (i >> 1) * 8][n * 8 + 2 * c + (i & 1)] = acc[n][i];
+  __syncthreads();
+  const int row = threadIdx.x & 15, tok = threadIdx.x >> 4, f = row0 + row;
+  if (tok >= p.M || f >= p.N) return;
+  float v = 0.f;
+#pragma unroll
+  for (int s = 0; s < WARPS; ++s) v += red[s][row][tok];
+  const long long o = tok * p.ldc + f;
+  if (p.epilogue == CB_FP8_STORE_BF16)
+    static_cast<bf16*>(p.c)[o] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p.c)[o] = p.epilogue == CB_FP8_ADD_F32 ? p.addend[o] + v : v;
+}
+
 }  // namespace f8
 
 // ============================================================================= planner + launcher
@@ -1093,15 +1180,21 @@ int resident_clusters(int cs) {
 // cb_gemm_scaled_set_plan: tokens per tile (0: the model decides) * 8 + pairs per cluster.
 std::atomic<int> g_plan{0};
 
+constexpr int HANDFUL_PLAN = 1 * 8;  // cb_gemm_scaled_set_plan(1, 0)
+
 struct Plan {
   int bt, split, clusters, stages, stage_bytes, ring_off, out_off;
 };
 
+// Time model (microseconds, measured on GB300 at ~1.9 GHz over 1 .. 1357 tokens of the decoder
+// shapes): a group takes 0.42 us with 256 tokens on the rows and 0.21 + 0.0012 bt us with the weights on
+// them, a unit's output 2 us and 0.9 + 0.04 bt us; units go round the resident clusters (76 of one
+// pair, 36 of two, 23 of three, 15 of four); the weights come at 6.5 TB/s at the most.
 Plan plan(const Fp8Gemm& g) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
   const int width = swiglu ? g.N / 2 : g.N, groups = (g.K + 127) / 128;
   const int w_tiles = swiglu ? (width + 127) / 128 : (width + 255) / 256;
-  const int forced = g_plan.load();
+  const int forced = g_plan.load() == HANDFUL_PLAN ? 0 : g_plan.load();
   Plan best{};
   double best_us = 1e30;
   auto consider = [&](int bt, int split) {
@@ -1112,9 +1205,11 @@ Plan plan(const Fp8Gemm& g) {
     const long long tiles = (g.M + bt - 1) / bt, units = tiles * w_tiles;
     const double waves = static_cast<double>((units + clusters - 1) / clusters);
     const bool tokens = bt == 256;
-    const double kb = tokens ? 700.0 : std::max(5.0 * bt, 500.0);
-    const double epi = tokens ? 3000.0 : 1500.0 + 40.0 * bt / split;
-    const double us = waves * ((groups + split - 1) / split * kb + epi) / 1800.0;
+    const double group_us = tokens ? 0.42 : 0.21 + 0.0012 * bt;
+    const double epi_us = tokens ? 2.0 : 0.9 + 0.04 * bt;
+    const double work = waves * ((groups + split - 1) / split * group_us + epi_us);
+    const double stream = static_cast<double>(g.N) * g.K / 6.5e6;
+    const double us = std::max(work, stream) + 0.15 * std::min(work, stream);
     if (us < best_us) {
       const int stage = A_BYTES + (tokens ? A_BYTES : bt * 64);
       // (parts: 2 split CTAs' sums of as many tokens as one CTA finishes)
@@ -1133,11 +1228,25 @@ Plan plan(const Fp8Gemm& g) {
   return best;
 }
 
+// Where the kernel for a handful of tokens is the faster one: one wave of its CTAs (three an SM, two
+// above 8 tokens) or a small matrix, and few groups per warp.  Measured on GB300 (us, this kernel and
+// the other): 1 token 6.2 / 7.7 at 4096 x 4096, 7.0 / 8.9 at 6144 x 4096, 12.0 / 12.8 at 7168 x 7168,
+// 8.7 / 9.7 at 28672 x 1024, but 10.4 / 9.9 at 8192 x 4096 and 16.3 / 14.8 at 4096 x 14336; 16 tokens
+// 7.4 / 7.9 at 4096 x 4096, but 12.3 / 9.1 at 6144 x 4096.
+bool handful_applies(const Fp8Gemm& g) {
+  const int forced = g_plan.load();
+  if (g.M > 16 || g.epilogue == CB_FP8_SWIGLU_FP8) return false;
+  if (forced) return forced == HANDFUL_PLAN;
+  const int wave = 16 * 152 * (g.M <= 8 ? 3 : 2);  // features
+  if (g.M > 8) return g.K <= 4096 && g.N <= wave;
+  return g.K <= 8192 && (g.N <= wave || static_cast<long long>(g.N) * g.K <= 30ll << 20);
+}
+
 }  // namespace
 
 bool gemm_fp8_set_plan(int tokens, int split) {
-  if (tokens == 0 && split == 0) {
-    g_plan.store(0);
+  if ((tokens == 0 || tokens == 1) && split == 0) {
+    g_plan.store(tokens * 8);
     return true;
   }
   if (!kernel_of(tokens, CB_FP8_STORE_F32) || split < 1 || split > 4 || (tokens == 256 && split != 1)) return false;
@@ -1148,6 +1257,11 @@ bool gemm_fp8_set_plan(int tokens, int split) {
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.M <= 0) return cudaSuccess;
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
+  if (handful_applies(g)) {
+    const dim3 grid((g.N + 15) / 16), block(256);
+    return g.M <= 8 ? launch_chain(gemm_fp8_handful_kernel<1>, grid, block, 0, s, g)
+                    : launch_chain(gemm_fp8_handful_kernel<2>, grid, block, 0, s, g);
+  }
   const Plan pl = plan(g);
   // (a stage's barrier is read until its accumulator is, and its factors are written ahead)
   if (pl.bt == 0 || pl.stages <= n_acc(pl.bt)) return cudaErrorInvalidConfiguration;

@@ -102,7 +102,7 @@ def test_binding_refuses_what_is_no_cuda_matrix(lib):
 
 
 def test_plan_hook_refuses_what_has_no_kernel(lib):
-    for bad in [(8, 1), (16, 0), (16, 5), (40, 1), (64, 8), (192, 1), (256, 2), (512, 1), (-16, 1), (0, 1), (128, -1)]:
+    for bad in [(1, 1), (8, 1), (16, 0), (16, 5), (40, 1), (64, 8), (192, 1), (256, 2), (512, 1), (-16, 1), (0, 1), (128, -1)]:
         assert lib.cb_gemm_scaled_set_plan(*bad) == ARG
-    for ok in [(16, 1), (16, 4), (48, 1), (64, 2), (80, 4), (96, 2), (128, 1), (128, 4), (256, 1), (0, 0)]:
+    for ok in [(1, 0), (16, 1), (16, 4), (48, 1), (64, 2), (80, 4), (96, 2), (128, 1), (128, 4), (256, 1), (0, 0)]:
         assert lib.cb_gemm_scaled_set_plan(*ok) == OK

@@ -227,7 +227,7 @@ def test_gemm_of_any_number_of_features(m, width, epi):
     assert untouched(whole, m, width)
 
 
-PLANS = [(16, 1), (16, 2), (16, 3), (16, 4), (32, 1), (32, 3), (32, 4), (48, 1), (48, 4), (64, 1), (64, 2), (80, 1), (80, 4), (96, 2), (128, 1),
+PLANS = [(1, 0), (16, 1), (16, 2), (16, 3), (16, 4), (32, 1), (32, 3), (32, 4), (48, 1), (48, 4), (64, 1), (64, 2), (80, 1), (80, 4), (96, 2), (128, 1),
          (128, 2), (128, 3), (128, 4), (256, 1)]
 
 
@@ -239,7 +239,8 @@ def plan(request):
 
 
 @pytest.mark.parametrize("epi", [F32, ADD, SWIGLU, BF16])
-@pytest.mark.parametrize("m,width,k", [(1, 144, 16), (70, 400, 144), (300, 528, 1168), (261, 5008, 656)])
+@pytest.mark.parametrize("m,width,k", [(1, 144, 16), (8, 2064, 1296), (15, 272, 4224), (70, 400, 144), (300, 528, 1168),
+                                       (261, 5008, 656)])
 def test_every_plan_matches_definition(plan, m, width, k, epi):
     """Each tiling, with few and many tiles per CTA, odd tails and fewer groups than pairs."""
     o, whole, csw = operands(m, width, k, epi, seed=m, extra=1)
@@ -261,16 +262,18 @@ def test_every_plan_matches_definition(plan, m, width, k, epi):
 
 @pytest.mark.parametrize("epi", [F32, ADD, BF16])
 def test_every_plan_with_ragged_rows(plan, epi):
-    o, whole, _ = operands(41, 301, 272, epi, seed=3)
-    gemm(o, epi)
-    check_gemm(o["a"], o["sa"], o["b"], o["sb"], epi, o["c"], o["addend"])
-    assert untouched(whole, 41, 301)
+    for m in (41, 11):
+        o, whole, _ = operands(m, 301, 272, epi, seed=3)
+        gemm(o, epi)
+        check_gemm(o["a"], o["sa"], o["b"], o["sb"], epi, o["c"], o["addend"])
+        assert untouched(whole, m, 301)
 
 
+@pytest.mark.parametrize("m", [9, 40])
 @pytest.mark.parametrize("layout", ["gate first", "up first", "own pitches"])
-def test_every_plan_with_gate_and_up_anywhere(plan, layout):
+def test_every_plan_with_gate_and_up_anywhere(plan, layout, m):
     """Gate and up rows in either order in memory, and in matrices of different pitches."""
-    o, _, _ = operands(40, 272, 400, SWIGLU, seed=4)
+    o, _, _ = operands(m, 272, 400, SWIGLU, seed=4)
     room = torch.zeros(2, 272, 512, dtype=torch.uint8, device="cuda").view(E4M3)
     gate, up = (room[0], room[1]) if layout == "gate first" else (room[1], room[0])
     if layout == "own pitches":
