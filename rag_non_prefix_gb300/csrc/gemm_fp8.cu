@@ -160,15 +160,12 @@ template <int N8> __device__ __forceinline__ void tmem_ld16x256_all(uint32_t tad
     tmem_ld16x256<1>(taddr, r);
   }
 }
-// 32 lanes x 32 fp32 columns, without waiting: thread t gets lane t's columns.
-__device__ __forceinline__ void tmem_ld32x32(uint32_t taddr, uint32_t* r) {
+// 32 lanes x 16 fp32 columns, without waiting: thread t gets lane t's columns.
+__device__ __forceinline__ void tmem_ld32x16(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 // Waits for this thread's tensor-memory reads; what was read into r may be used after it only.
@@ -246,10 +243,6 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
       : "memory");
 }
 __device__ __forceinline__ void fence_cta() { asm volatile("fence.acq_rel.cta;" ::: "memory"); }
-// 16-byte aligned range of global memory into L2 (whole 16 bytes)
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -369,14 +362,13 @@ __device__ __forceinline__ void load_codes(Bars& bars, const Params& p, int g0, 
 
 // Factor warp `which` of two (all lanes): loads the token scales of every second group, RAW_SLOTS of
 // them ahead, and multiplies them by the scales of two weight blocks, sb0 and sb1 of a unit's weight
-// tile; `put` stores token t's two factors into the stage's lists; `unit` is called as a unit begins.
-// A list is free once every reader
+// tile; `put` stores token t's two factors into the stage's lists.  A list is free once every reader
 // has read an accumulator n_acc groups further on, which that group's MMAs waited for: when the
 // group stages - n_acc before this one is done.
-template <int TILE, int TOKENS, int COLUMNS, typename Blocks, typename Put, typename Unit>
+template <int TILE, int TOKENS, int COLUMNS, typename Blocks, typename Put>
 __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const CUtensorMap* tmS, uint8_t* smem,
                                                 int g0, int g1, int cid, int NC, int which, int lane, uint32_t lead,
-                                                int tok_off, Blocks blocks, Put put, Unit unit) {
+                                                int tok_off, Blocks blocks, Put put) {
   const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(COLUMNS);
   const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead), el = lane == 0;
   float* raw = reinterpret_cast<float*>(smem + OFF_RAW) + which * RAW_SLOTS * 128;
@@ -408,7 +400,6 @@ __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, con
   for (int u = cid; ok && u < p.units; u += NC) {
     const float *sb0, *sb1;
     blocks(u / p.tok_tiles, sb0, sb1);
-    unit(u);
     float b0 = 0.f, b1 = 0.f;  // 32 groups' block scales, one per lane
     for (int g = g0; g < g1; ++g, ++n) {
       const int i = (g - g0) & 31;
@@ -543,16 +534,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           [&](float* slot, int t, float v0, float v1) {
             slot[t] = v0;
             slot[FACTORS + t] = v1;
-          },
-          [&](int u) {
-            // the tile's addend on its way to L2 while its products are summed: 64 tokens a warp
-            if (EPI != CB_FP8_ADD_F32 || p.width % 4 != 0) return;
-            const int wt = u / p.tok_tiles, tt = u - wt * p.tok_tiles;
-            const uint32_t bytes = static_cast<uint32_t>(min(256, p.width - wt * 256)) * 4u;
-            for (int r = lane; r < 64; r += 32) {
-              const int tok = tt * 256 + h * 128 + (warp - 2) * 64 + r;
-              if (tok < p.g.M) prefetch_l2(p.g.addend + static_cast<long long>(tok) * p.g.ldc + wt * 256, bytes);
-            }
           });
     }
     __syncwarp();
@@ -562,9 +543,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int row = threadIdx.x & 127;  // this thread's token of the CTA's
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t full_lead = mapa_shared(smem_u32(bars.full), 0);
-    // first column of the four reads of 32: SwiGLU takes two of the gate and two of the up features
+    // first column of the eight reads of 16: SwiGLU takes 64 of the gate and 64 of the up features
     const auto column = [&](int c) {
-      return static_cast<uint32_t>(SWIGLU ? (c >> 1) * 128 + w * 64 + (c & 1) * 32 : w * 128 + c * 32);
+      return static_cast<uint32_t>(SWIGLU ? (c >> 2) * 128 + w * 64 + (c & 3) * 16 : w * 128 + c * 16);
     };
     uint8_t* mine = smem + p.out_off + (warp - 4) * 2 * SLAB;
     const uint32_t el = lane == 0;
@@ -574,50 +555,47 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     int nth = 0;
     for (int u = cid; u < p.units; u += NC, ++nth) {
-      uint64_t acc[4][16];  // [read][pair of features]
+      uint64_t acc[4][16];  // [32 features][pair of them]
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[c][j] = 0;
-      // Two register buffers: the next read of tensor memory, which may be the next group's first,
-      // runs under the sums of the current one.
-      uint32_t v[2][32];
-      auto begin = [&]() {  // the group's sums (and its factors) are there: start its first read
+      // Two register buffers: the next read of tensor memory runs under the sums of the current one.
+      // (Reads of 32 columns, the next group's first among them, leave the compiler too few
+      // registers: it moves sums about between groups, and 2048 x 7168 x 7168 takes 78 instead of
+      // 72 us in bf16, 103 instead of 96 with an addend.)
+      uint32_t v[2][16];
+#pragma unroll 1
+      for (int g = 0; g < G; ++g) {
         if (ok && !mbar_wait_bounded(&bars.done[st.i], st.ph, abort)) {
           ok = false;
           report_timeout(bars, p.g.status);
         }
         __syncwarp();
         tc_fence_after();
-        tmem_ld32x32(tmem + b * ACC_STRIDE + lane_base + column(0), v[0]);
-      };
-      begin();
-#pragma unroll 1
-      for (int g = 0; g < G; ++g) {
         const uint32_t tacc = tmem + b * ACC_STRIDE + lane_base;
+        tmem_ld32x16(tacc + column(0), v[0]);
         const float* f = reinterpret_cast<const float*>(sc + st.i * FACTOR_BYTES) + row;
         const float fa = f[SWIGLU ? 0 : w * FACTORS], fb = SWIGLU ? f[FACTORS] : fa;
         const uint64_t m0 = pack2(fa, fa), m1 = SWIGLU ? pack2(fb, fb) : m0;
-        auto sums = [&](int c) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[c][j] = fma2(pack2u(v[c & 1][2 * j], v[c & 1][2 * j + 1]), c < 2 ? m0 : m1, acc[c][j]);
-        };
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld_of<32>(v[c & 1]);
-          if (c < 3) {
-            tmem_ld32x32(tacc + column(c + 1), v[(c + 1) & 1]);
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t* sum = v[c & 1];
+          tmem_wait_ld_of<16>(v[c & 1]);
+          if (c < 7) {
+            tmem_ld32x16(tacc + column(c + 1), v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             mbar_arrive_cluster_relaxed(full_lead + next_use * 8, el);
             if (++next_use == stages) next_use = 0;
             b ^= 1u;
             st.next(stages);
-            sums(c);
-            if (g + 1 < G) begin();
           }
-          if (c < 3) sums(c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t& x = acc[c / 2][c % 2 * 8 + j];
+            x = fma2(pack2u(sum[2 * j], sum[2 * j + 1]), c < 4 ? m0 : m1, x);
+          }
         }
       }
 
@@ -700,11 +678,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const long long o = static_cast<long long>(t0 + r4) * p.g.ldc + f;
           float4 d[AHEAD];
+          const int rows = p.g.M - t0 - r4;  // this lane's rows 4 i below it exist
+          const long long step = 4 * p.g.ldc;
+          const float* from_addend = EPI == CB_FP8_ADD_F32 ? p.g.addend + o : nullptr;
           auto read_addend = [&](int from) {
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-              if (EPI == CB_FP8_ADD_F32 && whole && t0 + r4 + 4 * (from + i) < p.g.M)
-                d[i] = *reinterpret_cast<const float4*>(p.g.addend + o + 4 * (from + i) * p.g.ldc);
+            for (int i = 0; i < AHEAD; ++i) {
+              if (EPI == CB_FP8_ADD_F32 && whole && 4 * (from + i) < rows) d[i] = *reinterpret_cast<const float4*>(from_addend);
+              from_addend += step;
+            }
           };
           read_addend(0);
           if (EPI == CB_FP8_STORE_BF16 && lane == 0) bulk_wait_read_all();
@@ -717,19 +699,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float4 x = *reinterpret_cast<const float4*>(mine + row * 128 + ((((lane & 7) * 2) ^ (row & 14)) << 3));
             return row & 1 ? make_float4(x.z, x.w, x.x, x.y) : x;
           };
+          uint8_t* to = static_cast<uint8_t*>(p.g.c) + o * (EPI == CB_FP8_STORE_BF16 ? 2 : 4);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i && i % AHEAD == 0) read_addend(i);
-            const float4 x = turned(i);
-            if (!ok || !whole || t0 + r4 + 4 * i >= p.g.M) continue;
-            if (EPI == CB_FP8_STORE_BF16)
-              *reinterpret_cast<uint2*>(static_cast<bf16*>(p.g.c) + o + 4 * i * p.g.ldc) =
-                  make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-            else if (EPI == CB_FP8_ADD_F32)
-              *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + o + 4 * i * p.g.ldc) =
-                  make_float4(d[i % AHEAD].x + x.x, d[i % AHEAD].y + x.y, d[i % AHEAD].z + x.z, d[i % AHEAD].w + x.w);
-            else
-              *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + o + 4 * i * p.g.ldc) = x;
+            float4 x = turned(i);
+            if (EPI == CB_FP8_ADD_F32) {
+              const float4 a = d[i % AHEAD];
+              x = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+            }
+            if (ok && whole && 4 * i < rows) {
+              if (EPI == CB_FP8_STORE_BF16)
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+              else
+                *reinterpret_cast<float4*>(to) = x;
+            }
+            to += step * (EPI == CB_FP8_STORE_BF16 ? 2 : 4);
           }
           if (ok && !whole) {  // rows that end inside four features
 #pragma unroll 1
@@ -838,8 +823,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int o = tw * (FACTORS / 2) + ((x >> 1) & 3) * 20 + (x >> 3) * 2 + (x & 1);
             slot[o] = v0;
             if (SWIGLU) slot[FACTORS + o] = v1;
-          },
-          [](int) {});
+          });
     }
     __syncwarp();
   } else {
