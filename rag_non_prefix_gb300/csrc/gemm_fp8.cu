@@ -1168,6 +1168,7 @@ constexpr int HANDFUL_PLAN = 1 * 8;  // cb_gemm_scaled_set_plan(1, 0)
 
 struct Plan {
   int bt, split, clusters, stages, stage_bytes, ring_off, out_off;
+  double us;  // expected time
 };
 
 // Time model (microseconds, measured on GB300 at ~1.9 GHz over 1 .. 1357 tokens of the decoder
@@ -1201,7 +1202,7 @@ Plan plan(const Fp8Gemm& g) {
       const int out = tokens ? 16 * SLAB : (2 * split * per * PART_PITCH * 4 + 1023) / 1024 * 1024;
       best_us = us;
       const int room = SMEM_USE - OFF_SC - 1023 - out;
-      best = Plan{bt, split, clusters, std::min(MAX_STAGES, room / (stage + FACTOR_BYTES)), stage, 0, 0};
+      best = Plan{bt, split, clusters, std::min(MAX_STAGES, room / (stage + FACTOR_BYTES)), stage, 0, 0, us};
       best.ring_off = (OFF_SC + best.stages * FACTOR_BYTES + 1023) / 1024 * 1024;
       best.out_off = best.ring_off + best.stages * stage;
     }
@@ -1226,6 +1227,78 @@ bool handful_applies(const Fp8Gemm& g) {
   return g.K <= 8192 && (g.N <= wave || static_cast<long long>(g.N) * g.K <= 30ll << 20);
 }
 
+// The product of the first `n` tokens, or of the first `n` output features, and the rest of it.
+Fp8Gemm first_tokens(const Fp8Gemm& g, int n) {
+  Fp8Gemm r = g;
+  r.M = n;
+  return r;
+}
+long long element_size(const Fp8Gemm& g) {
+  return g.epilogue == CB_FP8_SWIGLU_FP8 ? 1 : g.epilogue == CB_FP8_STORE_BF16 ? 2 : 4;
+}
+Fp8Gemm other_tokens(const Fp8Gemm& g, int n) {
+  Fp8Gemm r = g;
+  r.M = g.M - n;
+  r.a += n * g.lda;
+  r.a_scale += n;
+  r.c = static_cast<uint8_t*>(g.c) + n * g.ldc * element_size(g);
+  if (g.addend) r.addend += n * g.ldc;
+  if (g.c_scale) r.c_scale += n;
+  return r;
+}
+Fp8Gemm first_features(const Fp8Gemm& g, int n) {
+  Fp8Gemm r = g;
+  r.N = g.epilogue == CB_FP8_SWIGLU_FP8 ? 2 * n : n;
+  return r;
+}
+Fp8Gemm other_features(const Fp8Gemm& g, int n) {
+  Fp8Gemm r = g;
+  r.N = g.N - first_features(g, n).N;
+  r.b += n * g.ldb;
+  r.b_scale += n / 128 * g.ld_bs;
+  if (g.b2) {
+    r.b2 += n * g.ldb2;
+    r.b2_scale += n / 128 * g.ld_b2s;
+  }
+  r.c = static_cast<uint8_t*>(g.c) + n * element_size(g);
+  if (g.addend) r.addend += n;
+  if (g.c_scale) r.c_scale += n / 128 * g.ld_cs;
+  return r;
+}
+
+// Many tokens leave most pairs idle in the last round of 256 x 256 tiles when that round is short.
+// Then the tiles that fill whole rounds are computed first and the remaining tokens or features as
+// a product of their own, whose plan spreads them over all pairs (smaller tiles, split channels).
+// Measured on GB300 (us, one part and two): 535 x 7168 x 7168 56 / 40, 535 x 7168 x 20480 136 / 97,
+// 1100 x 4096 x 14336 99 / 70, 1357 x 7168 x 20480 206 / 176, 8320 x 8192 x 8192 433 / 410; where the model promises less than
+// 4 percent two parts took up to 9 percent longer (700 x 8192 x 8192 58 / 63).
+constexpr double SECOND_LAUNCH_US = 4, WORTH_IT = 0.96;
+struct Parts {
+  int tokens = 0, features = 0;  // of the first part; 0, 0: one part
+};
+Parts parts(const Fp8Gemm& g, const Plan& whole) {
+  Parts best;
+  const int pairs = resident_clusters(2);
+  if (pairs <= 0 || g.M <= 256 || g_plan.load()) return best;
+  const int tile = g.epilogue == CB_FP8_SWIGLU_FP8 ? 128 : 256;
+  const int width = g.epilogue == CB_FP8_SWIGLU_FP8 ? g.N / 2 : g.N;
+  const int t = (g.M + 255) / 256, w = (width + tile - 1) / tile;
+  const long long rounds = (static_cast<long long>(t) * w + pairs - 1) / pairs;
+  double us = WORTH_IT * whole.us;
+  // the most tiles along one axis that stay within one round less
+  const long long fewer = (rounds - 1) * pairs;
+  const int tk = static_cast<int>(fewer / w), fk = static_cast<int>(fewer / t);
+  if (tk > 0) {
+    const double both = plan(first_tokens(g, tk * 256)).us + plan(other_tokens(g, tk * 256)).us + SECOND_LAUNCH_US;
+    if (both < us) us = both, best = Parts{tk * 256, 0};
+  }
+  if (fk > 0) {
+    const double both = plan(first_features(g, fk * tile)).us + plan(other_features(g, fk * tile)).us + SECOND_LAUNCH_US;
+    if (both < us) us = both, best = Parts{0, fk * tile};
+  }
+  return best;
+}
+
 }  // namespace
 
 bool gemm_fp8_set_plan(int tokens, int split) {
@@ -1238,15 +1311,8 @@ bool gemm_fp8_set_plan(int tokens, int split) {
   return true;
 }
 
-cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
-  if (g.M <= 0) return cudaSuccess;
+static cudaError_t launch_planned(const Fp8Gemm& g, const Plan& pl, cudaStream_t s) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
-  if (handful_applies(g)) {
-    const dim3 grid((g.N + 15) / 16), block(256);
-    return g.M <= 8 ? launch_chain(gemm_fp8_handful_kernel<1>, grid, block, 0, s, g)
-                    : launch_chain(gemm_fp8_handful_kernel<2>, grid, block, 0, s, g);
-  }
-  const Plan pl = plan(g);
   // (a stage's barrier is read until its accumulator is, and its factors are written ahead)
   if (pl.bt == 0 || pl.stages <= n_acc(pl.bt)) return cudaErrorInvalidConfiguration;
   const bool tokens = pl.bt == 256;
@@ -1295,6 +1361,22 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, mw2, ms, mc, static_cast<const Params>(p));
+}
+
+cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
+  if (g.M <= 0) return cudaSuccess;
+  if (handful_applies(g)) {
+    const dim3 grid((g.N + 15) / 16), block(256);
+    return g.M <= 8 ? launch_chain(gemm_fp8_handful_kernel<1>, grid, block, 0, s, g)
+                    : launch_chain(gemm_fp8_handful_kernel<2>, grid, block, 0, s, g);
+  }
+  const Plan whole = plan(g);
+  const Parts pt = parts(g, whole);
+  if (!pt.tokens && !pt.features) return launch_planned(g, whole, s);
+  const Fp8Gemm first = pt.tokens ? first_tokens(g, pt.tokens) : first_features(g, pt.features);
+  const Fp8Gemm rest = pt.tokens ? other_tokens(g, pt.tokens) : other_features(g, pt.features);
+  const cudaError_t e = launch_planned(first, plan(first), s);
+  return e == cudaSuccess ? launch_planned(rest, plan(rest), s) : e;
 }
 
 }  // namespace cb

@@ -260,6 +260,26 @@ def test_every_plan_matches_definition(plan, m, width, k, epi):
     cb.cb_gemm_get_status()
 
 
+@pytest.mark.parametrize("epi,m,width,k", [
+    (F32, 531, 7190, 4112), (ADD, 531, 7190, 4112), (BF16, 531, 7190, 4112), (SWIGLU, 531, 4128, 4112),
+    (F32, 1101, 8219, 8208), (ADD, 1101, 8219, 8208), (BF16, 1101, 8219, 8208), (SWIGLU, 1101, 4112, 8208)])
+def test_products_computed_in_two_parts(epi, m, width, k):
+    """A last round of few tiles: its tokens (531) or its features (1101) become a product of their own."""
+    o, whole, csw = operands(m, width, k, epi, seed=m, extra=1)
+    gemm(o, epi)
+    check_gemm(o["a"], o["sa"], o["b"], o["sb"], epi, o["c"], o["addend"], o["b2"], o["sb2"], o["c_scales"])
+    assert untouched(whole, m, width)
+    if epi == SWIGLU:
+        assert untouched(csw, -(-width // 128), m)
+    first = o["c"].clone()
+    if epi == ADD:
+        o["c"].copy_(o["addend"])
+        o["addend"] = o["c"]
+    gemm(o, epi)
+    assert torch.equal(first.view(torch.uint8), o["c"].view(torch.uint8))
+    cb.cb_gemm_get_status()
+
+
 @pytest.mark.parametrize("epi", [F32, ADD, BF16])
 def test_every_plan_with_ragged_rows(plan, epi):
     for m in (41, 11):
