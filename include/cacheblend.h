@@ -357,6 +357,7 @@ cb_status cb_gemm_get_status(void* stream, int timeout_ms);
  * Codes, fp32 and bf16 matrices are row-major with a pitch in elements; base addresses are
  * 16-byte aligned, pitches a multiple of 16 bytes, and channels (cols, d, K and the features of
  * a CB_FP8_SWIGLU_FP8 output) a multiple of 16.  Row scales: 16-byte aligned, ld_scales % 4 == 0.
+ * No matrix has more than 2^30 rows or 2^22 channels (CB_ERR_SHAPE).
  * Entries between a row's end and its pitch are neither read nor written. */
 typedef struct {
   const void* codes;    /* e4m3 [rows][ld] */
@@ -390,7 +391,8 @@ cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype
  *                      [N / 2][K] (N counts both): the input of the down projection
  *   CB_FP8_STORE_BF16  C bf16 [M][ldc] = acc
  * addend is read by CB_FP8_ADD_F32 alone, B2 and c_scales (pitch ld_cs) by CB_FP8_SWIGLU_FP8 alone
- * (NULL otherwise).  C may overlap no input but addend == C.  Runs on the tcgen05 tensor cores.
+ * (NULL otherwise).  C may overlap no input but addend == C.  Runs on the tcgen05 tensor cores (a
+ * handful of tokens and few weights: on mma.sync, whose kernel starts sooner).
  * No workspace; results repeat exactly.  Device-side problems (a bounded wait that gave up) go to
  * the standalone GEMM status word that cb_gemm_get_status() reads.  M 0 does nothing. */
 enum { CB_FP8_STORE_F32 = 0, CB_FP8_ADD_F32 = 1, CB_FP8_SWIGLU_FP8 = 2, CB_FP8_STORE_BF16 = 3 };

@@ -195,6 +195,11 @@ def _stream(s) -> C.c_void_p:
     return C.c_void_p(s.cuda_stream if hasattr(s, "cuda_stream") else int(s))
 
 
+def _stream_on(dev: int, s) -> C.c_void_p:
+    """_stream where the current device is known to be ``dev``."""
+    return _raw_stream(dev) if s is None and _raw_stream is not None else _stream(s)
+
+
 def _check(st: int, ctx=None):
     if st != 0:
         lib = load_library()
@@ -356,26 +361,33 @@ def cb_attention(q: torch.Tensor, q_pos: torch.Tensor, k: torch.Tensor, v: torch
 _E4M3 = torch.float8_e4m3fn
 
 
-def _pitch(t: torch.Tensor, dtype, rows: int, cols: int, what: str) -> int:
-    """Pitch of a [rows, cols] matrix argument of the 8-bit calls on the current device, after
-    checking it."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != dtype:
+def _pitch(t: torch.Tensor, dtype, rows: int, cols: int, what: str, dev: int) -> int:
+    """Pitch of a [rows, cols] matrix argument of the 8-bit calls on device ``dev``, after checking it."""
+    if t.dtype is not dtype:
         raise CacheBlendError(3, f"{what} must be {dtype}, not {t.dtype}")
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
-        raise CacheBlendError(2, f"{what} has shape {tuple(shape)}, needs ({rows}, {cols})")
-    if not t.is_cuda or (stride[1] != 1 and cols > 1):
-        raise CacheBlendError(1, f"{what} must be a CUDA matrix with contiguous rows")
+    if t.shape != (rows, cols):
+        raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}, needs ({rows}, {cols})")
+    pitch, step = t.stride()
+    if dev < 0 or t.get_device() != dev or (step != 1 and cols > 1):
+        raise CacheBlendError(1, f"{what} must be a CUDA matrix with contiguous rows on the current device")
     # the pitch of a single row is never stepped over and may be anything: pass one the library takes
-    return stride[0] if rows > 1 else (cols + 15) // 16 * 16
+    return pitch if rows > 1 else (cols + 15) // 16 * 16
+
+
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _rows_cols(t: torch.Tensor, what: str):
-    if t.dim() != 2:
-        raise CacheBlendError(2, f"{what} must be a matrix, not of shape {tuple(t.shape)}")
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+    """(rows, columns, device) of the first matrix argument (_pitch refuses what is on no device)."""
+    shape, dev = t.shape, t.get_device()
+    if len(shape) != 2:
+        raise CacheBlendError(2, f"{what} must be a matrix, not of shape {tuple(shape)}")
+    rows, cols = shape
+    if rows > 0x7FFFFFFF or cols > 0x7FFFFFFF:
+        raise CacheBlendError(2, f"{what} has more than 2^31 - 1 rows or columns")
+    if dev >= 0 and dev != _get_device():
         raise CacheBlendError(1, f"{what} is on another device than the current one")
-    return t.shape
+    return rows, cols, dev
 
 
 def row_scales(rows: int, cols: int, device="cuda") -> torch.Tensor:
@@ -388,22 +400,22 @@ def cb_quantize(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tens
     """(codes e4m3 [rows, cols], fp32 scales) of x [rows, cols]: a row matrix (block_rows 1, scales
     [ceil(cols / 128), rows], see row_scales) or a block matrix (128, scales [ceil(rows / 128),
     ceil(cols / 128)])."""
-    rows, cols = _rows_cols(x, "x")
+    rows, cols, dev = _rows_cols(x, "x")
     dtype = x.dtype
     dt = _dtype_code(dtype)
-    ldx = _pitch(x, dtype, rows, cols, "x")
+    ldx = _pitch(x, dtype, rows, cols, "x", dev)
     if codes is None:
         codes = torch.empty(rows, cols, dtype=_E4M3, device=x.device)
     groups, blocks = (cols + 127) // 128, (rows + 127) // 128
     if block_rows == 1:
         scales = row_scales(rows, cols, x.device) if scales is None else scales
-        lds = _pitch(scales, torch.float32, groups, rows, "scales")
+        lds = _pitch(scales, torch.float32, groups, rows, "scales", dev)
     else:
         scales = torch.empty(blocks, groups, dtype=torch.float32, device=x.device) if scales is None else scales
-        lds = _pitch(scales, torch.float32, blocks, groups, "scales")
+        lds = _pitch(scales, torch.float32, blocks, groups, "scales", dev)
     _check(load_library().cb_quantize(x.data_ptr(), ldx, rows, cols, dt, block_rows, codes.data_ptr(),
-                                      _pitch(codes, _E4M3, rows, cols, "codes"), scales.data_ptr(), lds,
-                                      _stream(stream)))
+                                      _pitch(codes, _E4M3, rows, cols, "codes", dev), scales.data_ptr(), lds,
+                                      _stream_on(dev, stream)))
     return codes, scales
 
 
@@ -413,37 +425,37 @@ def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = 
                             scales: Optional[torch.Tensor] = None, stream=None):
     """(codes, scales, residual_out) of the RMS norm of residual + x [rows, d]: the quantised rows
     (a row matrix) and the sum, written to ``residual_out`` when given (it may be ``residual``)."""
-    rows, d = _rows_cols(x, "x")
+    rows, d, dev = _rows_cols(x, "x")
     dtype = x.dtype
     rdt = dt = _dtype_code(dtype)
-    ldx = _pitch(x, dtype, rows, d, "x")
+    ldx = _pitch(x, dtype, rows, d, "x", dev)
     ldr, res, res_out, w = 0, None, None, None
     if residual is not None:
         rtype = residual.dtype
-        rdt, ldr, res = _dtype_code(rtype), _pitch(residual, rtype, rows, d, "residual"), residual.data_ptr()
+        rdt, ldr, res = _dtype_code(rtype), _pitch(residual, rtype, rows, d, "residual", dev), residual.data_ptr()
         if residual_out is not None:
-            if _pitch(residual_out, rtype, rows, d, "residual_out") != ldr:
+            if _pitch(residual_out, rtype, rows, d, "residual_out", dev) != ldr:
                 raise CacheBlendError(2, "residual and residual_out must have the same pitch")
             res_out = residual_out.data_ptr()
     elif residual_out is not None:
         raise CacheBlendError(1, "residual_out needs a residual")
     if weight is not None:
-        if weight.dtype != dtype or weight.shape != (d,) or not weight.is_contiguous() or not weight.is_cuda:
-            raise CacheBlendError(2, f"weight must be {d} contiguous CUDA elements of {dtype}")
+        if weight.dtype is not dtype or weight.shape != (d,) or not weight.is_contiguous() or weight.get_device() != dev:
+            raise CacheBlendError(2, f"weight must be {d} contiguous elements of {dtype} on the current CUDA device")
         w = weight.data_ptr()
     if codes is None:
         codes = torch.empty(rows, d, dtype=_E4M3, device=x.device)
     scales = row_scales(rows, d, x.device) if scales is None else scales
     _check(load_library().cb_add_rmsnorm_quantize(
         x.data_ptr(), ldx, dt, res, res_out, ldr, rdt, w, rows, d, eps, codes.data_ptr(),
-        _pitch(codes, _E4M3, rows, d, "codes"), scales.data_ptr(),
-        _pitch(scales, torch.float32, (d + 127) // 128, rows, "scales"), _stream(stream)))
+        _pitch(codes, _E4M3, rows, d, "codes", dev), scales.data_ptr(),
+        _pitch(scales, torch.float32, (d + 127) // 128, rows, "scales", dev), _stream_on(dev, stream)))
     return codes, scales, residual_out
 
 
-def _block_mat(codes: torch.Tensor, scales: torch.Tensor, n: int, k: int, what: str) -> Fp8Mat:
-    return Fp8Mat(codes.data_ptr(), _pitch(codes, _E4M3, n, k, what), scales.data_ptr(),
-                  _pitch(scales, torch.float32, (n + 127) // 128, (k + 127) // 128, "its scales"))
+def _block_mat(codes: torch.Tensor, scales: torch.Tensor, n: int, k: int, what: str, dev: int) -> Fp8Mat:
+    return Fp8Mat(codes.data_ptr(), _pitch(codes, _E4M3, n, k, what, dev), scales.data_ptr(),
+                  _pitch(scales, torch.float32, (n + 127) // 128, (k + 127) // 128, what + "_scales", dev))
 
 
 _SCALED_OUT = {CB_FP8_SWIGLU_FP8: _E4M3, CB_FP8_STORE_BF16: torch.bfloat16}
@@ -457,25 +469,29 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
     (CB_FP8_STORE_F32), addend + A . B^T in fp32 (CB_FP8_ADD_F32, ``addend`` may be ``C_out``), bf16
     (CB_FP8_STORE_BF16), or with gate rows B and up rows B2 the quantised SiLU(A B^T) * (A B2^T) as a
     row matrix C_out, C_scales (CB_FP8_SWIGLU_FP8)."""
-    M, K = _rows_cols(A, "A")
+    M, K, dev = _rows_cols(A, "A")
+    if B.dim() != 2:
+        raise CacheBlendError(2, f"B must be a matrix, not of shape {tuple(B.shape)}")
     width = B.shape[0]
-    a = Fp8Mat(A.data_ptr(), _pitch(A, _E4M3, M, K, "A"), A_scales.data_ptr(),
-               _pitch(A_scales, torch.float32, (K + 127) // 128, M, "A_scales"))
-    b = _block_mat(B, B_scales, width, K, "B")
-    ldc = _pitch(C_out, _SCALED_OUT.get(epilogue, torch.float32), M, width, "C_out")
+    a = Fp8Mat(A.data_ptr(), _pitch(A, _E4M3, M, K, "A", dev), A_scales.data_ptr(),
+               _pitch(A_scales, torch.float32, (K + 127) // 128, M, "A_scales", dev))
+    b = _block_mat(B, B_scales, width, K, "B", dev)
+    ldc = _pitch(C_out, _SCALED_OUT.get(epilogue, torch.float32), M, width, "C_out", dev)
     b2 = add = cs = None
     lds, n = 0, width
     if epilogue == CB_FP8_SWIGLU_FP8:
         if B2 is None or B2_scales is None or C_scales is None:
             raise CacheBlendError(1, "CB_FP8_SWIGLU_FP8 needs B2, B2_scales and C_scales")
-        b2, n = _block_mat(B2, B2_scales, width, K, "B2"), 2 * width
-        cs, lds = C_scales.data_ptr(), _pitch(C_scales, torch.float32, (width + 127) // 128, M, "C_scales")
+        b2, n = _block_mat(B2, B2_scales, width, K, "B2", dev), 2 * width
+        cs, lds = C_scales.data_ptr(), _pitch(C_scales, torch.float32, (width + 127) // 128, M, "C_scales", dev)
     elif epilogue == CB_FP8_ADD_F32:
-        if addend is None or _pitch(addend, torch.float32, M, width, "addend") != ldc:
+        if addend is None or _pitch(addend, torch.float32, M, width, "addend", dev) != ldc:
             raise CacheBlendError(2, "CB_FP8_ADD_F32 needs an addend of C_out's pitch")
         add = addend.data_ptr()
+    if n > 0x7FFFFFFF:
+        raise CacheBlendError(2, "B has too many rows")
     _check(load_library().cb_gemm_scaled(a, b, b2, add, C_out.data_ptr(), ldc, cs, lds, M, n, K, epilogue,
-                                         _stream(stream)))
+                                         _stream_on(dev, stream)))
     return C_out
 
 

@@ -1350,10 +1350,13 @@ static bool bad_row_scales(const float* s, long long ld, int rows) {
 }
 static const char* const kFp8Layout =
     "needs 16-byte aligned matrices and row scales, pitches that hold a row and are multiples of 16 bytes";
+constexpr int kFp8Rows = 1 << 30, kFp8Cols = 1 << 22;  // (tile counts and grids stay within their types)
+static const char* const kFp8Sizes = "no more than 2^30 rows and 2^22 channels";
 
 cb_status cb_quantize(const void* x, long long ldx, int rows, int cols, cb_dtype dtype, int block_rows,
                           void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream) {
   if (rows < 0 || cols < 1 || cols % 16) return fail(nullptr, CB_ERR_SHAPE, "cols must be a positive multiple of 16");
+  if (rows > kFp8Rows || cols > kFp8Cols) return fail(nullptr, CB_ERR_SHAPE, kFp8Sizes);
   if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
   if (block_rows != 1 && block_rows != 128) return fail(nullptr, CB_ERR_INVALID_ARG, "block_rows must be 1 or 128");
   if (rows == 0) return CB_OK;
@@ -1372,6 +1375,7 @@ cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype
                              void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream) {
   if (rows < 0 || d < 1 || d % 16 || d > 32768)
     return fail(nullptr, CB_ERR_SHAPE, "d must be a multiple of 16 up to 32768");
+  if (rows > kFp8Rows) return fail(nullptr, CB_ERR_SHAPE, kFp8Sizes);
   if ((x_dtype != CB_F32 && x_dtype != CB_BF16) || (res_dtype != CB_F32 && res_dtype != CB_BF16))
     return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
   if (!(eps >= 0.f)) return fail(nullptr, CB_ERR_INVALID_ARG, "eps must not be negative");
@@ -1394,6 +1398,7 @@ cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_
   if (epilogue < 0 || epilogue > CB_FP8_STORE_BF16) return fail(nullptr, CB_ERR_INVALID_ARG, "bad epilogue");
   const bool swiglu = epilogue == CB_FP8_SWIGLU_FP8;
   if (M < 0 || N < 1 || K < 1 || K % 16) return fail(nullptr, CB_ERR_SHAPE, "K must be a positive multiple of 16");
+  if (M > kFp8Rows || N > kFp8Rows || K > kFp8Cols) return fail(nullptr, CB_ERR_SHAPE, kFp8Sizes);
   if (swiglu && N % 32) return fail(nullptr, CB_ERR_SHAPE, "N / 2 must be a multiple of 16");
   if (M == 0) return CB_OK;
   if (!A || !B || !C || !A->codes || !A->scales || !B->codes || !B->scales ||

@@ -124,8 +124,10 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restric
   pdl_wait();
   __shared__ uint32_t red[8];
   const int t = threadIdx.x;
-  const int col = blockIdx.x * 128 + (t & 15) * 8;
-  const long long row = static_cast<long long>(blockIdx.y) * 128 + (t >> 4);
+  const unsigned groups = (cols + 127) / 128;
+  const unsigned block = blockIdx.x / groups, group = blockIdx.x - block * groups;
+  const int col = group * 128 + (t & 15) * 8;
+  const long long row = static_cast<long long>(block) * 128 + (t >> 4);
   const bool in = col < cols;
   Piece<T> v[8];
 #pragma unroll
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restric
       v[u].get(f);
       *reinterpret_cast<uint2*>(codes + (row + u * 16) * ldc + col) = fp8_codes8(f, inv);
     }
-  if (t == 0) scales[static_cast<long long>(blockIdx.y) * lds + blockIdx.x] = a / FP8_MAX;
+  if (t == 0) scales[static_cast<long long>(block) * lds + group] = a / FP8_MAX;
 }
 
 // ----------------------------------------------------------------------------- norm
@@ -276,7 +278,9 @@ cudaError_t launch_fp8_quantize(const void* x, long long ldx, int rows, int cols
     return launch_chain(quantize_rows_kernel<float>, grid, dim3(256), 0, s, static_cast<const float*>(x), ldx, rows, cols,
                         c, ldc, scales, lds);
   }
-  const dim3 grid((cols + 127) / 128, (rows + 127) / 128);
+  const long long blocks = static_cast<long long>((cols + 127) / 128) * ((rows + 127) / 128);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks));
   if (dt == CB_BF16)
     return launch_chain(quantize_blocks_kernel<bf16>, grid, dim3(256), 0, s, static_cast<const bf16*>(x), ldx, rows, cols,
                         c, ldc, scales, lds);

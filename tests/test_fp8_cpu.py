@@ -27,7 +27,8 @@ def quantize(lib, x=P, ldx=256, rows=8, cols=256, dtype=1, block=1, codes=P, ldc
     (ARG, dict(block=64)), (ARG, dict(x=None)), (ARG, dict(codes=None)), (ARG, dict(scales=None)),
     (SHAPE, dict(ldx=248)), (SHAPE, dict(ldx=260)), (SHAPE, dict(x=ODD)), (SHAPE, dict(codes=ODD)),
     (SHAPE, dict(ldc=240)), (SHAPE, dict(ldc=264)), (SHAPE, dict(scales=ODD)), (SHAPE, dict(lds=4)), (SHAPE, dict(lds=10)),
-    (SHAPE, dict(block=128, lds=1)), (OK, dict(rows=0, x=None, codes=None))])
+    (SHAPE, dict(block=128, lds=1)),
+    (SHAPE, dict(rows=2 ** 30 + 4, lds=2 ** 30 + 4)), (SHAPE, dict(cols=2 ** 22 + 16, ldx=2 ** 23, ldc=2 ** 23)), (OK, dict(rows=0, x=None, codes=None))])
 def test_quantize_refuses(lib, want, bad):
     assert quantize(lib, **bad) == want
     if want:
@@ -44,7 +45,7 @@ def norm(lib, x=P, ldx=256, xdt=1, res=P, res_out=P, ldr=256, rdt=0, w=None, row
     (DTYPE, dict(xdt=5)), (DTYPE, dict(rdt=-1)), (ARG, dict(eps=-1.0)), (ARG, dict(eps=float("nan"))),
     (ARG, dict(res=None)), (ARG, dict(x=None)), (ARG, dict(codes=None)), (ARG, dict(scales=None)), (SHAPE, dict(x=ODD)),
     (SHAPE, dict(ldx=100)), (SHAPE, dict(ldr=255)), (SHAPE, dict(ldr=258)), (SHAPE, dict(res=ODD)), (SHAPE, dict(res_out=ODD)),
-    (SHAPE, dict(w=ODD)), (SHAPE, dict(ldc=128)), (SHAPE, dict(lds=7)), (OK, dict(rows=0, x=None))])
+    (SHAPE, dict(w=ODD)), (SHAPE, dict(ldc=128)), (SHAPE, dict(lds=7)), (SHAPE, dict(rows=2 ** 31 - 1, lds=2 ** 31)), (OK, dict(rows=0, x=None))])
 def test_norm_refuses(lib, want, bad):
     assert norm(lib, **bad) == want
 
@@ -66,7 +67,9 @@ def gemm(lib, a=None, b=None, b2=None, addend=P, c=P, ldc=512, cs=P, lds=8, m=8,
     (SHAPE, dict(a=mat(scales=ODD))), (SHAPE, dict(a=mat(lds=4))), (SHAPE, dict(a=mat(lds=9))), (SHAPE, dict(b=mat(lds=1))),
     (SHAPE, dict(b=mat(codes=ODD))), (SHAPE, dict(b2=mat(ld=16), epi=2)), (SHAPE, dict(c=ODD)), (SHAPE, dict(ldc=508)),
     (SHAPE, dict(ldc=514)), (SHAPE, dict(ldc=516, epi=3)), (SHAPE, dict(ldc=264, epi=2)), (SHAPE, dict(addend=ODD, epi=1)),
-    (SHAPE, dict(cs=ODD, epi=2)), (SHAPE, dict(lds=6, epi=2)), (OK, dict(m=0, c=None))])
+    (SHAPE, dict(cs=ODD, epi=2)), (SHAPE, dict(lds=6, epi=2)),
+    (SHAPE, dict(m=2 ** 30 + 1, a=mat(lds=2 ** 31))), (SHAPE, dict(n=2 ** 30 + 32, ldc=2 ** 31)),
+    (SHAPE, dict(k=2 ** 22 + 16, a=mat(ld=2 ** 23), b=mat(ld=2 ** 23, lds=2 ** 16))), (OK, dict(m=0, c=None))])
 def test_gemm_refuses(lib, want, bad):
     assert gemm(lib, **bad) == want
 

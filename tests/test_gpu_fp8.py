@@ -473,3 +473,25 @@ def test_binding_refuses_what_does_not_fit():
         with pytest.raises(cb.CacheBlendError):
             call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_many_millions_of_rows(block):
+    """More row blocks than a grid's second axis counts: like the quantised first and last rows alone."""
+    rows = 65536 * 128 + 3 * 128 + 5
+    x = rand(9, rows, 16).bfloat16()
+    codes, scales = cb.cb_quantize(x, block)
+    for lo, hi in [(0, 512), (65534 * 128, rows)]:
+        c, s = cb.cb_quantize(x[lo:hi], block)
+        assert torch.equal(c.view(torch.uint8), codes[lo:hi].view(torch.uint8))
+        assert torch.equal(s, scales[:, lo:hi] if block == 1 else scales[lo // 128:-(-hi // 128)])
+
+
+def test_binding_refuses_another_device(monkeypatch):
+    x = torch.zeros(4, 128, device="cuda")
+    codes, scales = cb.cb_quantize(x)
+    monkeypatch.setattr(cb, "_get_device", lambda: torch.cuda.current_device() + 1)
+    for call in (lambda: cb.cb_quantize(x), lambda: cb.cb_add_rmsnorm_quantize(x),
+                 lambda: cb.cb_gemm_scaled(codes, scales, codes, scales, x)):
+        with pytest.raises(cb.CacheBlendError, match="another device"):
+            call()
