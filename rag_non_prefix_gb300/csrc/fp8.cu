@@ -69,11 +69,42 @@ template <> struct Piece<float> {
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
 };
-// maximum over the 16 lanes that hold one group
-__device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+// Maxima of N groups that 16 lanes hold, 8 values a lane, each.  The lanes share the groups out: 5
+// exchanges instead of 16 for four groups, and one lane for each quotient of a group.  A lane's
+// result is that of group my_group<N>() of them; its first lane in the half warp is 16 / N times that.
+template <int N> __device__ __forceinline__ int my_group() {
+  const int l = threadIdx.x;
+  return N == 4 ? (l >> 2) & 3 : N == 2 ? (l >> 3) & 1 : 0;
+}
+template <int N> __device__ __forceinline__ uint32_t group_maxima(const uint32_t (&m)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  const auto from = [](uint32_t v, int lanes) { return __shfl_xor_sync(0xffffffffu, v, lanes); };
+  const bool up = threadIdx.x & 8, odd = threadIdx.x & 4;
+  uint32_t r;
+  if constexpr (N == 4) {
+    const uint32_t even_group = max(up ? m[2] : m[0], from(up ? m[0] : m[2], 8));
+    const uint32_t odd_group = max(up ? m[3] : m[1], from(up ? m[1] : m[3], 8));
+    r = max(odd ? odd_group : even_group, from(odd ? even_group : odd_group, 4));
+  } else {
+    r = N == 2 ? max(up ? m[N - 1] : m[0], from(up ? m[0] : m[N - 1], 8)) : max(m[0], from(m[0], 8));
+    r = max(r, from(r, 4));
+  }
+  r = max(r, from(r, 2));
+  return max(r, from(r, 1));
+}
+// What the lanes of a half warp hold for their k-th group of N.
+template <int N> __device__ __forceinline__ uint32_t of_group(uint32_t v, int k) {
+  return N == 1 ? v : __shfl_sync(0xffffffffu, v, (threadIdx.x & 16) + k * (16 / N));
+}
+template <int N> __device__ __forceinline__ bool first_of_group() { return (threadIdx.x & (16 / N - 1)) == 0; }
+// packed fp32 pairs (one instruction for two values)
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 __device__ __forceinline__ uint2 fp8_codes8(const float* f, float inv) {
   uint32_t h[4];
@@ -85,7 +116,10 @@ __device__ __forceinline__ uint2 fp8_codes8(const float* f, float inv) {
 
 // ----------------------------------------------------------------------------- rows
 // One warp takes 256 channels of a row (16 lanes per group, 8 channels per lane), UNROLL rows at
-// once so that their loads are in flight together.  Bound by HBM: (2 or 4) + 1 bytes per value.
+// once so that their loads are in flight together and one lane takes the quotients of one row's
+// group.  Bound by HBM, (2 or 4) + 1 bytes per value, and behind it by instructions in bf16: 8320 x
+// 8192 35 us (5.8 TB/s; 39 with each row's maximum by itself, 44 with two rows a warp), in fp32 56 us
+// (6.1 TB/s; eight rows a warp 62); 535 x 4096 2.6 us.
 constexpr int QR_UNROLL = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ x, long long ldx, int rows, int cols,
@@ -101,21 +135,27 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
 #pragma unroll
   for (int u = 0; u < QR_UNROLL; ++u)
     if (in && row0 + u < rows) v[u].load(x + (row0 + u) * ldx + col);
+  uint32_t m[QR_UNROLL];
+#pragma unroll
+  for (int u = 0; u < QR_UNROLL; ++u) m[u] = v[u].amax();
+  const float a = fp8_amax_floor(group_maxima<QR_UNROLL>(m));
+  const uint32_t inv = __float_as_uint(FP8_MAX / a);
+  const long long mine = row0 + my_group<QR_UNROLL>();
+  if (first_of_group<QR_UNROLL>() && (col & ~127) < cols && mine < rows)
+    scales[static_cast<long long>(col >> 7) * lds + mine] = a / FP8_MAX;
 #pragma unroll
   for (int u = 0; u < QR_UNROLL; ++u) {
-    const float a = fp8_amax_floor(half_warp_max(v[u].amax()));
-    if (in && row0 + u < rows) {
-      float f[8];
-      v[u].get(f);
-      *reinterpret_cast<uint2*>(codes + (row0 + u) * ldc + col) = fp8_codes8(f, FP8_MAX / a);
-      if ((lane & 15) == 0) scales[static_cast<long long>(col >> 7) * lds + row0 + u] = a / FP8_MAX;
-    }
+    float f[8];
+    v[u].get(f);
+    const uint2 q = fp8_codes8(f, __uint_as_float(of_group<QR_UNROLL>(inv, u)));
+    if (in && row0 + u < rows) *reinterpret_cast<uint2*>(codes + (row0 + u) * ldc + col) = q;
   }
 }
 
 // ----------------------------------------------------------------------------- weight blocks
 // One CTA per 128 x 128 block, held in registers between the maximum and the codes (one read):
-// a half warp per row segment of 128 channels, 8 rows per thread.
+// a half warp per row segment of 128 channels, 8 rows per thread, kept as they lie in memory.
+// Bound by HBM: 20480 x 7168 in bf16 66 us (6.7 TB/s), in fp32 105 us (7.0 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restrict__ x, long long ldx, int rows, int cols,
                                                               uint8_t* __restrict__ codes, long long ldc,
@@ -156,16 +196,17 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restric
 // A row is held in registers from its single read to its codes: thread t owns the 8-channel pieces
 // t, t + blockDim, ... (CH of them), so 16 consecutive lanes hold one group.  h = residual + x in
 // fp32; the norm and the codes come from the unrounded h, residual_out gets h rounded to its type.
+// Bound by HBM for large matrices with a residual (8320 x 8192 in bf16: 73 us, 6.5 TB/s; 8320 x 7168
+// with an fp32 residual 99 us, 6.6 TB/s), by instructions without (8000 x 8192: 41 us, 4.8 TB/s,
+// hence the packed pairs and shared maxima), by a row's latency for few rows (one row 2.1 us).  A
+// stream of bulk copies into shared memory ahead of the sums was no faster.
 
 // Sum over the block.
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  const int n = blockDim.x >> 5;
-  float sum = 0.f;
-  for (int i = 0; i < n; ++i) sum += red[i];
-  return sum;
+  return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.f);
 }
 
 // Codes and scales of the row h (in f), given 1 / rms.
@@ -174,6 +215,7 @@ __device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, con
                                            long long row, uint8_t* __restrict__ codes, long long ldc,
                                            float* __restrict__ scales, long long lds) {
   const int t = threadIdx.x, T = blockDim.x;
+  uint32_t m[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = (t + k * T) * 8;
@@ -181,23 +223,33 @@ __device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, con
       float w[8];
       load8(weight + c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[k][j] *= w[j];
+      for (int j = 0; j < 8; j += 2) {
+        uint64_t u = pair(f[k][j], f[k][j + 1]);
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(u) : "l"(pair(w[j], w[j + 1])));
+        unpair(u, f[k][j], f[k][j + 1]);
+      }
     }
-    // y = u * inv_rms with u = h * w, so y * (448 / max|y|) = u * (448 / max|u|): the codes do not
-    // see the norm's rounding (two roundings instead of four), only the scale does.  Where 448 /
-    // max|u| could overflow, or the scale's floor applies, the codes come from y itself.
-    const float au = __uint_as_float(half_warp_max(amax_bits8(f[k])));
-    const float a = fp8_amax_floor(abs_bits(au * inv_rms));
-    float inv = FP8_MAX / au;
-    if (!(au > 0x1p-100f && a > FP8_AMAX_MIN)) {
+    m[k] = amax_bits8(f[k]);
+  }
+  // y = u * inv_rms with u = h * w, so y * (448 / max|y|) = u * (448 / max|u|): the codes do not
+  // see the norm's rounding (two roundings instead of four), only the scale does.  Where 448 /
+  // max|u| could overflow, or the scale's floor applies, the codes come from y itself (the factor's
+  // sign says so).  Each lane does this for one of its half warp's groups.
+  const float au = __uint_as_float(group_maxima<CH>(m));
+  const float a = fp8_amax_floor(abs_bits(au * inv_rms));
+  const bool direct = au > 0x1p-100f && a > FP8_AMAX_MIN;
+  const uint32_t factor = __float_as_uint(FP8_MAX / (direct ? au : a)) | (direct ? 0u : 0x80000000u);
+  const int group = (t + my_group<CH>() * T) >> 4;
+  if (first_of_group<CH>() && group * 128 < d) scales[static_cast<long long>(group) * lds + row] = a / FP8_MAX;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int c = (t + k * T) * 8;
+    const uint32_t mine = of_group<CH>(factor, k);
+    if (mine >> 31) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[k][j] *= inv_rms;
-      inv = FP8_MAX / a;
     }
-    if (c < d) {
-      *reinterpret_cast<uint2*>(codes + row * ldc + c) = fp8_codes8(f[k], inv);
-      if ((t & 15) == 0) scales[static_cast<long long>(c >> 7) * lds + row] = a / FP8_MAX;
-    }
+    if (c < d) *reinterpret_cast<uint2*>(codes + row * ldc + c) = fp8_codes8(f[k], __uint_as_float(mine & 0x7fffffffu));
   }
 }
 
@@ -227,7 +279,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
     }
   }
   float f[CH][8];
-  float ss = 0.f;
+  uint64_t ss2 = 0;
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = (t + k * T) * 8;
@@ -235,13 +287,17 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
     px[k].get(f[k]);
     pr[k].get(r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (RES) f[k][j] = r[j] + f[k][j];
-      ss += f[k][j] * f[k][j];
+    for (int j = 0; j < 8; j += 2) {
+      uint64_t h = pair(f[k][j], f[k][j + 1]);
+      if (RES) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(h) : "l"(pair(r[j], r[j + 1])));
+      asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(ss2) : "l"(h));
+      unpair(h, f[k][j], f[k][j + 1]);
     }
     if (RES && res_out && c < d) store8(res_out + row * ldr + c, f[k]);
   }
-  const float inv_rms = 1.0f / sqrtf(block_sum(ss, red) / static_cast<float>(d) + eps);
+  float even, odd;
+  unpair(ss2, even, odd);
+  const float inv_rms = 1.0f / sqrtf(block_sum(even + odd, red) / static_cast<float>(d) + eps);
   norm_codes<TX, CH>(f, inv_rms, weight, d, row, codes, ldc, scales, lds);
 }
 
@@ -255,13 +311,15 @@ cudaError_t launch_norm(const void* x, long long ldx, const void* res, void* res
     return launch_chain(kernel, dim3(rows), dim3(threads), 0, s, static_cast<const TX*>(x), ldx,
                         res, res_out, ldr, static_cast<const TX*>(weight), d, eps, static_cast<uint8_t*>(codes), ldc, scales, lds);
   };
-  // Pieces per thread: one for short rows and for few rows (the shortest way through a row: 2.4 us for
-  // one row of 4096 against 3.2 us with four; 2000 rows of 1024: 5.0 against 6.5 us), four for many
-  // long ones, whose CTAs then keep more reads under way per barrier (8320 rows of 8192 in bf16: 78
-  // against 97 us; 8320 rows of 7168 with an fp32 residual: 99 against 106 us).
-  const bool one_piece = pieces <= 1024 && (pieces <= 512 || rows <= 608);
-  if (res) return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TR, true, 1>, 1) : one(add_rmsnorm_fp8_kernel<TX, TR, true, 4>, 4);
-  return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1>, 1) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 4>, 4);
+  // Pieces per thread.  One while the GPU holds all pieces at once (152 SMs x 2048 threads), the
+  // shortest way through a row: 1 x 4096 2.1 us (four 3.2), 535 x 4096 with a residual 6.0 (two 6.3).
+  // Then two with a residual up to 8192 channels (8320 x 4096 39.7 us, one 45.4; 8320 x 8192 73, one
+  // 94, four 74; 1357 x 7168 with an fp32 residual 18.9, one 19.6, four 19.3) and four for longer rows
+  // (8320 x 16384 140, two 184) and without a residual (8320 x 4096 22.7, one 33; 8000 x 8192 41, two 51).
+  const bool one_piece = pieces <= 1024 && static_cast<long long>(rows) * pieces <= 152 * 2048;
+  if (!res) return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1>, 1) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 4>, 4);
+  if (one_piece) return one(add_rmsnorm_fp8_kernel<TX, TR, true, 1>, 1);
+  return pieces <= 1024 ? one(add_rmsnorm_fp8_kernel<TX, TR, true, 2>, 2) : one(add_rmsnorm_fp8_kernel<TX, TR, true, 4>, 4);
 }
 
 }  // namespace
