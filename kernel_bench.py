@@ -7,6 +7,9 @@
     python kernel_bench.py deviation --n 3200 --kvw 1024
     python kernel_bench.py codec --n 3136 --hkv 8 --bits 8
     python kernel_bench.py decode --layers 32 --steps 2
+    python kernel_bench.py quantize --M 20480 --K 7168 --block 128
+    python kernel_bench.py norm_quantize --M 1357 --K 7168
+    python kernel_bench.py gemm_scaled --M 535 --N 28672 --K 4096 --mode swiglu [--plan 256 1]
 
 (`decode` builds the Mistral-7B-shaped model with --layers layers, blends the configuration-2
 prompt, decodes 4 warm-up steps, then --steps steps inside the NVTX range "decode_prof" that
@@ -53,12 +56,16 @@ def _time(fn, iters, warmup=3, flush=None, batch=1):
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("kernel", choices=["gemm", "attention", "rerotate", "select", "deviation", "codec", "decode"])
+    ap.add_argument("kernel", choices=["gemm", "attention", "rerotate", "select", "deviation", "codec", "decode",
+                                       "quantize", "norm_quantize", "gemm_scaled"])
     ap.add_argument("--steps", type=int, default=2)
     ap.add_argument("--M", type=int, default=535)
     ap.add_argument("--N", type=int, default=28672)
     ap.add_argument("--K", type=int, default=4096)
-    ap.add_argument("--mode", default="swiglu", choices=["store", "add", "swiglu"])
+    ap.add_argument("--mode", default="swiglu", choices=["store", "add", "swiglu", "bf16"],
+                    help="epilogue of the products (bf16: gemm_scaled only)")
+    ap.add_argument("--block", type=int, default=1, choices=[1, 128], help="quantize: rows per scale")
+    ap.add_argument("--plan", type=int, nargs=2, default=[0, 0], help="gemm_scaled: cb_gemm_scaled_set_plan")
     ap.add_argument("--H", type=int, default=32)
     ap.add_argument("--Hkv", type=int, default=8)
     ap.add_argument("--m", type=int, default=535)
@@ -87,6 +94,8 @@ def main():
     dev = torch.device("cuda")
     flush = None if a.no_flush else torch.empty(128 * 1024 * 1024, dtype=torch.float32, device=dev)
     out = {"kernel": a.kernel}
+    if a.kernel == "gemm" and a.mode == "bf16":
+        ap.error("--mode bf16 is an epilogue of gemm_scaled")
     if a.kernel == "gemm":
         M, N, K = a.M, a.N, a.K
         scr = None if a.no_stream_k else cb.gemm_scratch(dev)
@@ -107,6 +116,37 @@ def main():
         out.update(shape=[M, N, K], mode=a.mode, stream_k=scr is not None, orientation=a.orientation, pairing=a.pairing,
                    plan=cb.cb_gemm_describe(M, N, K, {"store": 0, "add": 1, "swiglu": 2}[a.mode], 0 if scr is None else scr.numel()), ms=avg, best_ms=best, tflops=fl / (avg * 1e-3) / 1e12,
                    weight_bytes=N * K * 2)
+    elif a.kernel == "quantize":
+        x = torch.randn(a.M, a.K, device=dev).to(torch.bfloat16)
+        codes, scales = cb.cb_quantize(x, a.block)
+        avg, best = _time(lambda: cb.cb_quantize(x, a.block, codes, scales), a.iters, a.warmup, flush, a.batch)
+        by = x.numel() * 3 + scales.numel() * 4
+        out.update(shape=[a.M, a.K], block=a.block, ms=avg, best_ms=best, gbs=by / (avg * 1e-3) / 1e9)
+    elif a.kernel == "norm_quantize":
+        x = torch.randn(a.M, a.K, device=dev).to(torch.bfloat16)
+        h = torch.randn(a.M, a.K, device=dev)
+        w = torch.ones(a.K, dtype=torch.bfloat16, device=dev)
+        codes, scales, _ = cb.cb_add_rmsnorm_quantize(x, h, w, 1e-5, h)
+        avg, best = _time(lambda: cb.cb_add_rmsnorm_quantize(x, h, w, 1e-5, h, codes, scales), a.iters, a.warmup, flush, a.batch)
+        by = x.numel() * (2 + 4 + 4 + 1) + scales.numel() * 4
+        out.update(shape=[a.M, a.K], ms=avg, best_ms=best, gbs=by / (avg * 1e-3) / 1e9)
+    elif a.kernel == "gemm_scaled":
+        M, N, K = a.M, a.N, a.K
+        A = cb.cb_quantize(torch.randn(M, K, device=dev) * 0.5)
+        W = [cb.cb_quantize(torch.randn(N // 2 if a.mode == "swiglu" else N, K, device=dev) * 0.02, 128)
+             for _ in range(2 if a.mode == "swiglu" else 1)]
+        width = W[0][0].shape[0]
+        epi = {"store": cb.CB_FP8_STORE_F32, "add": cb.CB_FP8_ADD_F32, "swiglu": cb.CB_FP8_SWIGLU_FP8,
+               "bf16": cb.CB_FP8_STORE_BF16}[a.mode]
+        C = torch.zeros(M, width, dtype={"swiglu": torch.float8_e4m3fn, "bf16": torch.bfloat16}.get(a.mode, torch.float32),
+                        device=dev)
+        more = dict(B2=W[1][0], B2_scales=W[1][1], C_scales=cb.row_scales(M, width)) if a.mode == "swiglu" else {}
+        if a.mode == "add":
+            more["addend"] = C
+        cb.cb_gemm_scaled_set_plan(*a.plan)
+        avg, best = _time(lambda: cb.cb_gemm_scaled(*A, *W[0], C, epi, **more), a.iters, a.warmup, flush, a.batch)
+        out.update(shape=[M, N, K], mode=a.mode, plan=a.plan, ms=avg, best_ms=best,
+                   tflops=2.0 * M * N * K / (avg * 1e-3) / 1e12, weight_bytes=N * K)
     elif a.kernel == "attention":
         H, Hkv, N, m = a.H, a.Hkv, a.N, a.m
         pos = torch.sort(torch.randperm(N, device=dev)[:m]).values.to(torch.int32)

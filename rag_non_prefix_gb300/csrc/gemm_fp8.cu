@@ -460,14 +460,18 @@ __device__ __forceinline__ void finish(Bars& bars, uint32_t tmem, int warp) {
 }
 
 // Registers: 384 threads launch with 168 each; the four service warps keep 40, the eight others take
-// 232 (128 x 40 + 256 x 232 = 64,512 = 384 x 168).  216 for them spilled: 129 -> 110 us at 2048 x 7168 x 7168.
+// 232 (128 x 40 + 256 x 232 = 64,512 = 384 x 168).
 __device__ __forceinline__ void few_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
 __device__ __forceinline__ void many_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
 
 // ============================================================================= many tokens
 // Tokens on the rows: thread r of a warpgroup holds token r of this CTA's 128, warpgroup w the
 // features 128 w .. of the tile's 256 (SwiGLU: gate and up of features 64 w .. of 128; the pair's
-// even CTA stages the gate rows, the odd one the up rows).
+// even CTA stages the gate rows, the odd one the up rows).  Bound by those eight warps: a group takes
+// ~770 cycles of reading tensor memory and multiplying (~190 instructions a warp) against 512 of
+// tensor core (active 65 % of 2048 x 7168 x 7168 bf16, 69 % with SwiGLU), and by the power limit in
+// long runs.  2048 x 7168 x 7168 bf16 71 us (2.95 PFLOP/s), fp32 72 us, with an addend 93 us; 8320 x
+// 40960 x 7168 SwiGLU 1530 us (3.2 PFLOP/s) before the power limit, 1815 us under it.
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_tokens_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -747,7 +751,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 // in a fixed order.  The parts are pushed into the finishing CTA's shared memory (st.async, counted
 // in bytes on its barrier): a barrier with release at cluster scope and reads from the other side
 // took ~1.3 us longer.  Bound by the weights' bytes; what a call of few groups spends on top is the
-// way through the chip (set-up 0.9 us, first codes 1.7 us, parts and output ~1 us).
+// way through the chip (set-up 0.9 us, first codes 1.7 us, parts and output ~1 us), and the last round
+// of tiles, which may leave pairs idle: 16 x 4096 x 14336 with an addend 15 us (4.0 TB/s), 16 x 28672 x
+// 4096 bf16 26 us (4.5 TB/s), 64 x 28672 x 4096 SwiGLU 33 us, 77 x 11008 x 4112 bf16 19 us.  (A second
+// launch for the last round, which pays for many tokens, made these 2 to 5 us slower.)
 template <int BT, bool SWIGLU>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_weights_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
