@@ -368,7 +368,7 @@ def _pitch(t: torch.Tensor, dtype, rows: int, cols: int, what: str, dev: int) ->
     if t.shape != (rows, cols):
         raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}, needs ({rows}, {cols})")
     pitch, step = t.stride()
-    if dev < 0 or t.get_device() != dev or (step != 1 and cols > 1):
+    if t.get_device() != dev or (step != 1 and cols > 1):
         raise CacheBlendError(1, f"{what} must be a CUDA matrix with contiguous rows on the current device")
     # the pitch of a single row is never stepped over and may be anything: pass one the library takes
     return pitch if rows > 1 else (cols + 15) // 16 * 16
@@ -377,17 +377,20 @@ def _pitch(t: torch.Tensor, dtype, rows: int, cols: int, what: str, dev: int) ->
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _rows_cols(t: torch.Tensor, what: str):
-    """(rows, columns, device) of the first matrix argument (_pitch refuses what is on no device)."""
+def _first(t: torch.Tensor, what: str):
+    """(rows, columns, pitch, device) of the first matrix argument, on the current device."""
     shape, dev = t.shape, t.get_device()
     if len(shape) != 2:
         raise CacheBlendError(2, f"{what} must be a matrix, not of shape {tuple(shape)}")
     rows, cols = shape
+    pitch, step = t.stride()
     if rows > 0x7FFFFFFF or cols > 0x7FFFFFFF:
         raise CacheBlendError(2, f"{what} has more than 2^31 - 1 rows or columns")
-    if dev >= 0 and dev != _get_device():
+    if dev < 0 or (step != 1 and cols > 1):
+        raise CacheBlendError(1, f"{what} must be a CUDA matrix with contiguous rows on the current device")
+    if dev != _get_device():
         raise CacheBlendError(1, f"{what} is on another device than the current one")
-    return rows, cols, dev
+    return rows, cols, pitch if rows > 1 else (cols + 15) // 16 * 16, dev
 
 
 def row_scales(rows: int, cols: int, device="cuda") -> torch.Tensor:
@@ -400,10 +403,8 @@ def cb_quantize(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tens
     """(codes e4m3 [rows, cols], fp32 scales) of x [rows, cols]: a row matrix (block_rows 1, scales
     [ceil(cols / 128), rows], see row_scales) or a block matrix (128, scales [ceil(rows / 128),
     ceil(cols / 128)])."""
-    rows, cols, dev = _rows_cols(x, "x")
-    dtype = x.dtype
-    dt = _dtype_code(dtype)
-    ldx = _pitch(x, dtype, rows, cols, "x", dev)
+    dt = _dtype_code(x.dtype)
+    rows, cols, ldx, dev = _first(x, "x")
     if codes is None:
         codes = torch.empty(rows, cols, dtype=_E4M3, device=x.device)
     groups, blocks = (cols + 127) // 128, (rows + 127) // 128
@@ -425,10 +426,9 @@ def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = 
                             scales: Optional[torch.Tensor] = None, stream=None):
     """(codes, scales, residual_out) of the RMS norm of residual + x [rows, d]: the quantised rows
     (a row matrix) and the sum, written to ``residual_out`` when given (it may be ``residual``)."""
-    rows, d, dev = _rows_cols(x, "x")
     dtype = x.dtype
     rdt = dt = _dtype_code(dtype)
-    ldx = _pitch(x, dtype, rows, d, "x", dev)
+    rows, d, ldx, dev = _first(x, "x")
     ldr, res, res_out, w = 0, None, None, None
     if residual is not None:
         rtype = residual.dtype
@@ -469,11 +469,13 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
     (CB_FP8_STORE_F32), addend + A . B^T in fp32 (CB_FP8_ADD_F32, ``addend`` may be ``C_out``), bf16
     (CB_FP8_STORE_BF16), or with gate rows B and up rows B2 the quantised SiLU(A B^T) * (A B2^T) as a
     row matrix C_out, C_scales (CB_FP8_SWIGLU_FP8)."""
-    M, K, dev = _rows_cols(A, "A")
+    M, K, lda, dev = _first(A, "A")
+    if A.dtype is not _E4M3:
+        raise CacheBlendError(3, f"A must be {_E4M3}, not {A.dtype}")
     if B.dim() != 2:
         raise CacheBlendError(2, f"B must be a matrix, not of shape {tuple(B.shape)}")
     width = B.shape[0]
-    a = Fp8Mat(A.data_ptr(), _pitch(A, _E4M3, M, K, "A", dev), A_scales.data_ptr(),
+    a = Fp8Mat(A.data_ptr(), lda, A_scales.data_ptr(),
                _pitch(A_scales, torch.float32, (K + 127) // 128, M, "A_scales", dev))
     b = _block_mat(B, B_scales, width, K, "B", dev)
     ldc = _pitch(C_out, _SCALED_OUT.get(epilogue, torch.float32), M, width, "C_out", dev)

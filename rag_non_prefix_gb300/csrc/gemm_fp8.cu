@@ -1137,16 +1137,11 @@ Kernel kernel_of(int bt, int epilogue) {
   }
 }
 
-// Clusters of `cs` CTAs that are resident at once (one CTA per SM), per device.
-int resident_clusters(int cs) {
-  static std::atomic<int> cache[4][64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const int ci = cs / 2 - 1;
-  if (dev >= 0 && dev < 64) {
-    const int v = cache[ci][dev].load();
-    if (v > 0) return v;
-  }
+// Clusters of one to four pairs that are resident at once (one CTA per SM); 0 where the query fails.
+struct Resident {
+  int clusters[4];
+};
+int query_resident_clusters(int cs) {
   const void* fn = reinterpret_cast<const void*>(kernel_of(16, CB_FP8_STORE_F32));
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC) != cudaSuccess) return 0;
   cudaLaunchConfig_t q = {};
@@ -1164,8 +1159,21 @@ int resident_clusters(int cs) {
     cudaGetLastError();
     return 0;
   }
-  if (dev >= 0 && dev < 64) cache[ci][dev].store(n);
   return n;
+}
+Resident resident_clusters() {
+  static std::atomic<int> cache[64][4];  // per device
+  Resident r{};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return r;
+  for (int i = 0; i < 4; ++i) {
+    const bool cached = dev >= 0 && dev < 64;
+    if (cached) r.clusters[i] = cache[dev][i].load(std::memory_order_relaxed);
+    if (r.clusters[i] > 0) continue;
+    r.clusters[i] = query_resident_clusters(2 * i + 2);
+    if (cached) cache[dev][i].store(r.clusters[i], std::memory_order_relaxed);
+  }
+  return r;
 }
 
 // cb_gemm_scaled_set_plan: tokens per tile (0: the model decides) * 8 + pairs per cluster.
@@ -1182,7 +1190,7 @@ struct Plan {
 // shapes): a group takes 0.42 us with 256 tokens on the rows and 0.21 + 0.0012 bt us with the weights on
 // them, a unit's output 2 us and 0.9 + 0.04 bt us; units go round the resident clusters (76 of one
 // pair, 36 of two, 23 of three, 15 of four); the weights come at 6.5 TB/s at the most.
-Plan plan(const Fp8Gemm& g) {
+Plan plan(const Fp8Gemm& g, const Resident& resident) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
   const int width = swiglu ? g.N / 2 : g.N, groups = (g.K + 127) / 128;
   const int w_tiles = swiglu ? (width + 127) / 128 : (width + 255) / 256;
@@ -1192,7 +1200,7 @@ Plan plan(const Fp8Gemm& g) {
   auto consider = [&](int bt, int split) {
     if (forced && forced != bt * 8 + split) return;
     split = std::min(split, groups);
-    const int clusters = resident_clusters(2 * split);
+    const int clusters = resident.clusters[split - 1];
     if (clusters <= 0) return;
     const long long tiles = (g.M + bt - 1) / bt, units = tiles * w_tiles;
     const double waves = static_cast<double>((units + clusters - 1) / clusters);
@@ -1214,8 +1222,10 @@ Plan plan(const Fp8Gemm& g) {
       best.out_off = best.ring_off + best.stages * stage;
     }
   };
-  for (int bt : {16, 32, 48, 64, 80, 96, 128})
+  for (int bt : {16, 32, 48, 64, 80, 96, 128}) {
     for (int split = 1; split <= 4; ++split) consider(bt, split);
+    if (bt >= g.M && !forced) break;  // (larger tiles only pad)
+  }
   consider(256, 1);
   return best;
 }
@@ -1283,9 +1293,9 @@ constexpr double SECOND_LAUNCH_US = 4, WORTH_IT = 0.96;
 struct Parts {
   int tokens = 0, features = 0;  // of the first part; 0, 0: one part
 };
-Parts parts(const Fp8Gemm& g, const Plan& whole) {
+Parts parts(const Fp8Gemm& g, const Plan& whole, const Resident& resident) {
   Parts best;
-  const int pairs = resident_clusters(2);
+  const int pairs = resident.clusters[0];
   if (pairs <= 0 || g.M <= 256 || g_plan.load()) return best;
   const int tile = g.epilogue == CB_FP8_SWIGLU_FP8 ? 128 : 256;
   const int width = g.epilogue == CB_FP8_SWIGLU_FP8 ? g.N / 2 : g.N;
@@ -1296,11 +1306,11 @@ Parts parts(const Fp8Gemm& g, const Plan& whole) {
   const long long fewer = (rounds - 1) * pairs;
   const int tk = static_cast<int>(fewer / w), fk = static_cast<int>(fewer / t);
   if (tk > 0) {
-    const double both = plan(first_tokens(g, tk * 256)).us + plan(other_tokens(g, tk * 256)).us + SECOND_LAUNCH_US;
+    const double both = plan(first_tokens(g, tk * 256), resident).us + plan(other_tokens(g, tk * 256), resident).us + SECOND_LAUNCH_US;
     if (both < us) us = both, best = Parts{tk * 256, 0};
   }
   if (fk > 0) {
-    const double both = plan(first_features(g, fk * tile)).us + plan(other_features(g, fk * tile)).us + SECOND_LAUNCH_US;
+    const double both = plan(first_features(g, fk * tile), resident).us + plan(other_features(g, fk * tile), resident).us + SECOND_LAUNCH_US;
     if (both < us) us = both, best = Parts{0, fk * tile};
   }
   return best;
@@ -1377,13 +1387,14 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
     return g.M <= 8 ? launch_chain(gemm_fp8_handful_kernel<1>, grid, block, 0, s, g)
                     : launch_chain(gemm_fp8_handful_kernel<2>, grid, block, 0, s, g);
   }
-  const Plan whole = plan(g);
-  const Parts pt = parts(g, whole);
+  const Resident resident = resident_clusters();
+  const Plan whole = plan(g, resident);
+  const Parts pt = parts(g, whole, resident);
   if (!pt.tokens && !pt.features) return launch_planned(g, whole, s);
   const Fp8Gemm first = pt.tokens ? first_tokens(g, pt.tokens) : first_features(g, pt.features);
   const Fp8Gemm rest = pt.tokens ? other_tokens(g, pt.tokens) : other_features(g, pt.features);
-  const cudaError_t e = launch_planned(first, plan(first), s);
-  return e == cudaSuccess ? launch_planned(rest, plan(rest), s) : e;
+  const cudaError_t e = launch_planned(first, plan(first, resident), s);
+  return e == cudaSuccess ? launch_planned(rest, plan(rest, resident), s) : e;
 }
 
 }  // namespace cb
