@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Dict, List, Optional, Sequence
 
 import torch
@@ -141,7 +142,8 @@ def load_library(path: str = LIB_PATH):
                              vp]),
         "cb_add_rmsnorm_quantize": (st, [vp, C.c_longlong, C.c_int, vp, vp, C.c_longlong, C.c_int, vp, C.c_int, C.c_int,
                                          C.c_float, vp, C.c_longlong, vp, C.c_longlong, vp]),
-        "cb_gemm_scaled": (st, [C.POINTER(Fp8Mat), C.POINTER(Fp8Mat), C.POINTER(Fp8Mat), vp, vp, C.c_longlong, vp,
+        # (the matrices: byref(Fp8Mat), or its bytes)
+        "cb_gemm_scaled": (st, [vp, vp, vp, vp, vp, C.c_longlong, vp,
                                 C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, vp]),
         "cb_gemm_scaled_set_plan": (st, [C.c_int, C.c_int]),
         "cb_codec_layer_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
@@ -434,7 +436,7 @@ def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = 
         rtype = residual.dtype
         rdt, ldr, res = _dtype_code(rtype), _pitch(residual, rtype, rows, d, "residual", dev), residual.data_ptr()
         if residual_out is not None:
-            if _pitch(residual_out, rtype, rows, d, "residual_out", dev) != ldr:
+            if residual_out is not residual and _pitch(residual_out, rtype, rows, d, "residual_out", dev) != ldr:
                 raise CacheBlendError(2, "residual and residual_out must have the same pitch")
             res_out = residual_out.data_ptr()
     elif residual_out is not None:
@@ -453,9 +455,13 @@ def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = 
     return codes, scales, residual_out
 
 
-def _block_mat(codes: torch.Tensor, scales: torch.Tensor, n: int, k: int, what: str, dev: int) -> Fp8Mat:
-    return Fp8Mat(codes.data_ptr(), _pitch(codes, _E4M3, n, k, what, dev), scales.data_ptr(),
-                  _pitch(scales, torch.float32, (n + 127) // 128, (k + 127) // 128, what + "_scales", dev))
+# an Fp8Mat as bytes (a quarter of the time of the structure)
+_pack_mat = struct.Struct("@PqPq").pack
+
+
+def _block_mat(codes: torch.Tensor, scales: torch.Tensor, n: int, k: int, what: str, dev: int) -> bytes:
+    return _pack_mat(codes.data_ptr(), _pitch(codes, _E4M3, n, k, what, dev), scales.data_ptr(),
+                     _pitch(scales, torch.float32, (n + 127) // 128, (k + 127) // 128, what + "_scales", dev))
 
 
 _SCALED_OUT = {CB_FP8_SWIGLU_FP8: _E4M3, CB_FP8_STORE_BF16: torch.bfloat16}
@@ -475,8 +481,8 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
     if B.dim() != 2:
         raise CacheBlendError(2, f"B must be a matrix, not of shape {tuple(B.shape)}")
     width = B.shape[0]
-    a = Fp8Mat(A.data_ptr(), lda, A_scales.data_ptr(),
-               _pitch(A_scales, torch.float32, (K + 127) // 128, M, "A_scales", dev))
+    a = _pack_mat(A.data_ptr(), lda, A_scales.data_ptr(),
+                  _pitch(A_scales, torch.float32, (K + 127) // 128, M, "A_scales", dev))
     b = _block_mat(B, B_scales, width, K, "B", dev)
     ldc = _pitch(C_out, _SCALED_OUT.get(epilogue, torch.float32), M, width, "C_out", dev)
     b2 = add = cs = None
@@ -487,7 +493,7 @@ def cb_gemm_scaled(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_s
         b2, n = _block_mat(B2, B2_scales, width, K, "B2", dev), 2 * width
         cs, lds = C_scales.data_ptr(), _pitch(C_scales, torch.float32, (width + 127) // 128, M, "C_scales", dev)
     elif epilogue == CB_FP8_ADD_F32:
-        if addend is None or _pitch(addend, torch.float32, M, width, "addend", dev) != ldc:
+        if addend is None or (addend is not C_out and _pitch(addend, torch.float32, M, width, "addend", dev) != ldc):
             raise CacheBlendError(2, "CB_FP8_ADD_F32 needs an addend of C_out's pitch")
         add = addend.data_ptr()
     if n > 0x7FFFFFFF:
