@@ -51,7 +51,13 @@ constexpr int OFF_SC = OFF_RAW + 2 * RAW_SLOTS * 512;  // factors of every stage
 constexpr int SMEM_ALLOC = 232448;         // the per-block maximum (227 KiB), 1 KiB of it aligns the base
 constexpr int SMEM_USE = SMEM_ALLOC - 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int PART_PITCH = ROWS + 4;       // floats per token and source CTA of the parts (few tokens)
+// Parts (few tokens): per source CTA and token its 128 rows, row 32 q + 8 r + i as float r of 16-byte piece
+// i + q + 2 (source & 1) (mod 8) of the q-th 128 bytes: a thread of the sums holds r = 0 .. 3 and writes
+// them at once, and lanes that read consecutive rows meet no bank twice.
+__device__ __forceinline__ int part_at(int source, int row) {
+  const int q = row >> 5, r = (row >> 3) & 3;
+  return q * 32 + (((row + q + 2 * (source & 1)) & 7) << 2) + r;
+}
 constexpr int SLAB = 2048;                 // many tokens: a warp stages 32 tokens x 64 bytes twice, or x 128 bytes
 
 // Accumulators in tensor memory: as many groups' sums as fit may wait to be read.
@@ -208,10 +214,10 @@ template <int N> __device__ __forceinline__ void read_factors(const float* s, ui
 }
 
 // ----------------------------------------------------------------------------- cluster exchange
-// A value into another CTA's shared memory whose bytes complete on that CTA's barrier.
-__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
-               "r"(__float_as_uint(v)), "r"(bar)
+// Four values into another CTA's shared memory whose bytes complete on that CTA's barrier.
+__device__ __forceinline__ void st_async_f32x4(uint32_t addr, float x, float y, float z, float w, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(__float_as_uint(z)), "r"(__float_as_uint(w)), "r"(bar)
                : "memory");
 }
 // mbar_wait_bounded with acquire at cluster scope (what other CTAs wrote is read after it)
@@ -840,11 +846,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int ri = lane >> 2, ci = (lane & 3) * 2;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead);
-    const float* part = reinterpret_cast<const float*>(smem + p.out_off);  // [CS][per][PART_PITCH]
+    float* part = reinterpret_cast<float*>(smem + p.out_off);  // [CS][per][ROWS]
+    const uint32_t piece = part_at(rank, quarter * 32 + ri);  // of the rows quarter * 32 + ri + 8 r
     const uint32_t part_u32 = smem_u32(part), part_full_u32 = smem_u32(&bars.part_full);
     const int CS = 2 * p.split;
     const int per = (BT / 2 + CS - 1) / CS * 2;  // tokens that each CTA of the cluster finishes, an even number
     const int mine = max(0, min(per, BT - static_cast<int>(rank) * per));
+    const uint32_t per_inverse = 65536u / per + 1;  // tok / per = tok * per_inverse >> 16 for tok < 128
     const uint32_t el = lane == 0;
     free_accumulators(bars, lead, NACC, el);
     Pos st;
@@ -896,28 +904,33 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t parity = nth & 1;
       const int n = min(mine, p.g.M - t0 - static_cast<int>(rank) * per);  // tokens to finish here (none: <= 0)
       const int tok0 = t0 + static_cast<int>(rank) * per;
-      if (et == 0) mbar_arrive_expect_tx(&bars.part_full, static_cast<uint32_t>(mine * CS * ROWS * 4));
+      if (et == 0) mbar_arrive_expect_tx(&bars.part_full, static_cast<uint32_t>(mine * (CS - 1) * ROWS * 4));
       // the parts of the previous tile have been read by the whole cluster
       if (ok && !mbar_wait_cluster(&bars.part_free, parity ^ 1u, abort)) give_up();
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < N8; ++j) {
         const int tok = w * HB + j * 8 + ci;  // and the next one: the same CTA finishes both
-        const uint32_t to = static_cast<uint32_t>(tok / per);
-        const uint32_t bar = mapa_shared(part_full_u32, to);
-        const uint32_t d = mapa_shared(
-            part_u32 + ((rank * per + tok - to * per) * PART_PITCH + quarter * 32 + ri) * 4, to);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float2 v = unpack2(acc[j][r]);
-          st_async_f32(d + r * 32, v.x, bar);
-          st_async_f32(d + r * 32 + PART_PITCH * 4, v.y, bar);
+        const uint32_t to = static_cast<uint32_t>(tok) * per_inverse >> 16;
+        const uint32_t at = (rank * per + tok - to * per) * ROWS + piece;
+        const float2 v0 = unpack2(acc[j][0]), v1 = unpack2(acc[j][1]), v2 = unpack2(acc[j][2]), v3 = unpack2(acc[j][3]);
+        if (to == rank) {
+          *reinterpret_cast<float4*>(part + at) = make_float4(v0.x, v1.x, v2.x, v3.x);
+          *reinterpret_cast<float4*>(part + at + ROWS) = make_float4(v0.y, v1.y, v2.y, v3.y);
+        } else {
+          const uint32_t bar = mapa_shared(part_full_u32, to), d = mapa_shared(part_u32 + at * 4, to);
+          st_async_f32x4(d, v0.x, v1.x, v2.x, v3.x, bar);
+          st_async_f32x4(d + ROWS * 4, v0.y, v1.y, v2.y, v3.y, bar);
         }
       }
+      named_bar(1, 256);  // this CTA's own parts are written
       if constexpr (!SWIGLU) {
         // thread: 4 features of every fourth token
         const int q4 = et & 63, f = wt * 256 + q4 * 4, tg = et >> 6;
-        const float* src = part + (q4 >> 5) * per * PART_PITCH + (q4 & 31) * 4;
+        const float* src = part + (q4 >> 5) * per * ROWS;
+        int at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = part_at(q4 >> 5, (q4 & 31) * 4 + i);
         const bool add = p.g.epilogue == CB_FP8_ADD_F32, whole = f + 4 <= p.width;
         constexpr int AHEAD = 4;  // addends read before the parts are there
         float4 d[AHEAD];
@@ -931,11 +944,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto finish_token = [&](int j, bool have, float4 ahead) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int s = 0; s < p.split; ++s) {
-            const float4 x = *reinterpret_cast<const float4*>(src + (2 * s * per + j) * PART_PITCH);
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
+            const float* x = src + (2 * s * per + j) * ROWS;
+            v.x += x[at[0]];
+            v.y += x[at[1]];
+            v.z += x[at[2]];
+            v.w += x[at[3]];
           }
           const long long o = static_cast<long long>(tok0 + j) * p.g.ldc + f;
           if (!ok) return;
@@ -967,7 +980,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = tg + 4 * AHEAD; j < n; j += 4) finish_token(j, false, make_float4(0.f, 0.f, 0.f, 0.f));
       } else {
         // a warp per token, lane x takes features 4 x .. of the tile's 128
-        const float* src = part + (lane >> 4) * per * PART_PITCH + (lane & 15) * 4;
+        const float* src = part + (lane >> 4) * per * ROWS;
+        int ga[4], ua[4];  // gate rows, up rows
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ga[i] = part_at(lane >> 4, (lane & 15) * 4 + i);
+          ua[i] = part_at(lane >> 4, 64 + (lane & 15) * 4 + i);
+        }
         const int f = wt * 128 + lane * 4;
         if (ok && !mbar_wait_cluster(&bars.part_full, parity, abort)) give_up();
         __syncwarp();
@@ -980,10 +999,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int j = min(jb + 8 * q, n - 1);  // (past the last token: computed again, not stored)
             float4 gate = make_float4(0.f, 0.f, 0.f, 0.f), up = gate;
             for (int s = 0; s < p.split; ++s) {
-              const float* x = src + (2 * s * per + j) * PART_PITCH;
-              const float4 a = *reinterpret_cast<const float4*>(x), b4 = *reinterpret_cast<const float4*>(x + 64);
-              gate = make_float4(gate.x + a.x, gate.y + a.y, gate.z + a.z, gate.w + a.w);
-              up = make_float4(up.x + b4.x, up.y + b4.y, up.z + b4.z, up.w + b4.w);
+              const float* x = src + (2 * s * per + j) * ROWS;
+              gate = make_float4(gate.x + x[ga[0]], gate.y + x[ga[1]], gate.z + x[ga[2]], gate.w + x[ga[3]]);
+              up = make_float4(up.x + x[ua[0]], up.y + x[ua[1]], up.z + x[ua[2]], up.w + x[ua[3]]);
             }
             y[q][0] = silu(gate.x) * up.x;
             y[q][1] = silu(gate.y) * up.y;
@@ -1214,7 +1232,7 @@ Plan plan(const Fp8Gemm& g, const Resident& resident) {
       const int stage = A_BYTES + (tokens ? A_BYTES : bt * 64);
       // (parts: 2 split CTAs' sums of as many tokens as one CTA finishes)
       const int per = (bt / 2 + 2 * split - 1) / (2 * split) * 2;
-      const int out = tokens ? 16 * SLAB : (2 * split * per * PART_PITCH * 4 + 1023) / 1024 * 1024;
+      const int out = tokens ? 16 * SLAB : (2 * split * per * ROWS * 4 + 1023) / 1024 * 1024;
       best_us = us;
       const int room = SMEM_USE - OFF_SC - 1023 - out;
       best = Plan{bt, split, clusters, std::min(MAX_STAGES, room / (stage + FACTOR_BYTES)), stage, 0, 0, us};
