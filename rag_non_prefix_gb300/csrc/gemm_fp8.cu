@@ -759,8 +759,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 // took ~1.3 us longer.  Bound by the weights' bytes; what a call of few groups spends on top is the
 // way through the chip (set-up 0.9 us, first codes 1.7 us, parts and output ~1 us), and the last round
 // of tiles, which may leave pairs idle: 16 x 4096 x 14336 with an addend 15 us (4.0 TB/s), 16 x 28672 x
-// 4096 bf16 26 us (4.5 TB/s), 64 x 28672 x 4096 SwiGLU 33 us, 77 x 11008 x 4112 bf16 19 us.  (A second
-// launch for the last round, which pays for many tokens, made these 2 to 5 us slower.)
+// 4096 bf16 25 us (4.7 TB/s), 64 x 28672 x 4096 SwiGLU 28.5 us, 77 x 11008 x 4112 bf16 16 us.  (A second
+// launch for the last round, which pays for many tokens, made these 2 to 5 us slower.)  Parts pushed
+// four bytes at a time took 64 x 4096 x 14336 from 16.7 to 17.8 us, 128 x 4096 x 4096 from 13.0 to 17.4.
 template <int BT, bool SWIGLU>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp8_weights_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -1204,10 +1205,11 @@ struct Plan {
   double us;  // expected time
 };
 
-// Time model (microseconds, measured on GB300 at ~1.9 GHz over 1 .. 1357 tokens of the decoder
-// shapes): a group takes 0.42 us with 256 tokens on the rows and 0.21 + 0.0012 bt us with the weights on
-// them, a unit's output 2 us and 0.9 + 0.04 bt us; units go round the resident clusters (76 of one
-// pair, 36 of two, 23 of three, 15 of four); the weights come at 6.5 TB/s at the most.
+// Time model (microseconds, fitted to 3000 runs on GB300 at ~1.9 GHz over 1 .. 1000 tokens of the decoder
+// shapes, where its choice is 0.7 percent slower than the best plan on average): a group takes 0.39 us with
+// 256 tokens on the rows and 0.18 + 0.0017 bt us with the weights on them, a unit's output 1.9 us and
+// 1.7 + 0.017 bt us; units go round the resident clusters (76 of one pair, 36 of two, 23 of three, 15
+// of four); the weights come at 6.5 TB/s at the most.
 Plan plan(const Fp8Gemm& g, const Resident& resident) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
   const int width = swiglu ? g.N / 2 : g.N, groups = (g.K + 127) / 128;
@@ -1223,11 +1225,11 @@ Plan plan(const Fp8Gemm& g, const Resident& resident) {
     const long long tiles = (g.M + bt - 1) / bt, units = tiles * w_tiles;
     const double waves = static_cast<double>((units + clusters - 1) / clusters);
     const bool tokens = bt == 256;
-    const double group_us = tokens ? 0.42 : 0.21 + 0.0012 * bt;
-    const double epi_us = tokens ? 2.0 : 0.9 + 0.04 * bt;
+    const double group_us = tokens ? 0.39 : 0.18 + 0.0017 * bt;
+    const double epi_us = tokens ? 1.9 : 1.7 + 0.017 * bt;
     const double work = waves * ((groups + split - 1) / split * group_us + epi_us);
     const double stream = static_cast<double>(g.N) * g.K / 6.5e6;
-    const double us = std::max(work, stream) + 0.15 * std::min(work, stream);
+    const double us = std::max(work, stream) + 0.13 * std::min(work, stream);
     if (us < best_us) {
       const int stage = A_BYTES + (tokens ? A_BYTES : bt * 64);
       // (parts: 2 split CTAs' sums of as many tokens as one CTA finishes)
