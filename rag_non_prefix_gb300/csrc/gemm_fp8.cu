@@ -476,7 +476,7 @@ __device__ __forceinline__ void many_registers() { asm volatile("setmaxnreg.inc.
 // even CTA stages the gate rows, the odd one the up rows).  Bound by those eight warps: a group takes
 // ~770 cycles of reading tensor memory and multiplying (~190 instructions a warp) against 512 of
 // tensor core (active 65 % of 2048 x 7168 x 7168 bf16, 69 % with SwiGLU), and by the power limit in
-// long runs.  2048 x 7168 x 7168 bf16 71 us (2.95 PFLOP/s), fp32 72 us, with an addend 93 us; 8320 x
+// long runs.  2048 x 7168 x 7168 bf16 71 us (2.95 PFLOP/s), fp32 72 us, with an addend 88 us; 8320 x
 // 40960 x 7168 SwiGLU 1530 us (3.2 PFLOP/s) before the power limit, 1815 us under it.
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // Two register buffers: the next read of tensor memory runs under the sums of the current one.
       // (Reads of 32 columns, the next group's first among them, leave the compiler too few
       // registers: it moves sums about between groups, and 2048 x 7168 x 7168 takes 78 instead of
-      // 72 us in bf16, 103 instead of 96 with an addend.)
+      // 72 us in bf16.)
       uint32_t v[2][16];
 #pragma unroll 1
       for (int g = 0; g < G; ++g) {
@@ -668,7 +668,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         // would tie the sums to aligned groups of four registers, which the compiler then moves about
         // in the main loop: 2048 x 7168 x 7168 in 92 instead of 71 us.)
         const int r4 = lane >> 3, q4 = (lane & 7) * 4;
-        constexpr int AHEAD = 4;  // reads of the addend under way
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int f = wt * 256 + w * 128 + c * 32 + q4;
@@ -687,18 +686,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             continue;
           }
           const long long o = static_cast<long long>(t0 + r4) * p.g.ldc + f;
-          float4 d[AHEAD];
           const int rows = p.g.M - t0 - r4;  // this lane's rows 4 i below it exist
           const long long step = 4 * p.g.ldc;
-          const float* from_addend = EPI == CB_FP8_ADD_F32 ? p.g.addend + o : nullptr;
-          auto read_addend = [&](int from) {
+          // the addends of all eight rows are under way at once (four: 2048 x 7168 x 7168 in 95 instead
+          // of 88 us, which is the burst of all tiles' addends and outputs at HBM's rate)
+          float4 d[8];
+          if constexpr (EPI == CB_FP8_ADD_F32) {
+            const float* from = p.g.addend + o;
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-              if (EPI == CB_FP8_ADD_F32 && whole && 4 * (from + i) < rows) d[i] = *reinterpret_cast<const float4*>(from_addend);
-              from_addend += step;
-            }
-          };
-          read_addend(0);
+            for (int i = 0; i < 8; ++i, from += step)
+              if (whole && 4 * i < rows) d[i] = *reinterpret_cast<const float4*>(from);
+          }
           if (EPI == CB_FP8_STORE_BF16 && lane == 0) bulk_wait_read_all();
           __syncwarp();
 #pragma unroll
@@ -712,10 +710,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* to = static_cast<uint8_t*>(p.g.c) + o * (EPI == CB_FP8_STORE_BF16 ? 2 : 4);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (i && i % AHEAD == 0) read_addend(i);
             float4 x = turned(i);
             if (EPI == CB_FP8_ADD_F32) {
-              const float4 a = d[i % AHEAD];
+              const float4 a = d[i];
               x = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
             }
             if (ok && whole && 4 * i < rows) {
