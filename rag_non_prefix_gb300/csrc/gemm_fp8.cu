@@ -1037,13 +1037,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ============================================================================= a handful of tokens
-// Up to 16 tokens and a matrix of a few MB: the weights are streamed once through registers and the
-// warps' own matrix instruction (mma.sync m16n8k32, weights on its 16 rows, 8 tokens a column block),
-// without tensor memory, clusters and barriers, whose set-up and hand-over cost more than such a
-// matrix's bytes.  A CTA per 16 features, its 8 warps taking every eighth group; their sums are added
-// in order.  Both operands take their 32 channels in the same permuted order: lane c of four holds 16
-// consecutive bytes of a row, words 0 and 1 for one product and 2 and 3 for the next.  The instruction
-// is slow here (~70 cycles each), which ends its use at larger matrices and more tokens (handful_applies).
+// Up to 16 tokens: the weights are streamed once through registers and the warps' own matrix instruction
+// (mma.sync m16n8k32, weights on its 16 rows, 8 tokens a column block), without tensor memory,
+// clusters and barriers, whose set-up and hand-over take longer than a few MB.  A CTA per 16 features, its
+// 8 warps taking every eighth group; their sums are added in order.  Both operands take their 32
+// channels in the same permuted order: lane c of four holds 16 consecutive bytes of a row, words 0 and 1
+// for one product and 2 and 3 for the next.  Bound by the latency of its few reads (1 x 6144 x 4096 6.4 us,
+// 3.9 TB/s) and by HBM for larger matrices (1 x 32000 x 4096 24 us, 5.4 TB/s); the instruction is slow here
+// (~70 cycles each), which ends its use at more tokens (handful_applies).
 __device__ __forceinline__ void mma_e4m3(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -1079,26 +1080,43 @@ __global__ void __launch_bounds__(256, NT == 1 ? 3 : 2) gemm_fp8_handful_kernel(
         a[u][ch][0] = load16_or_zero(w0 + k, in);
         a[u][ch][1] = load16_or_zero(w8 + k, in);
       }
+    // (tokens and scales come with the weights, not after them: 1 x 6144 x 4096 6.6 instead of 7.3 us)
+    uint4 xs[UNROLL][NT][2];
+    float fs[UNROLL], ss[UNROLL][NT][2];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int g = gb + u * WARPS;
+      const bool here = g < groups;
+      fs[u] = here ? __ldg(sb + g) : 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int tok = n * 8 + r, t = n * 8 + 2 * c;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          const int k = g * 128 + ch * 64 + c * 16;
+          xs[u][n][ch] = load16_or_zero(p.a + tok * p.lda + k, tok < p.M && k < p.K);
+        }
+        const float* sa = p.a_scale + g * p.ld_as + t;
+        ss[u][n][0] = here && t < p.M ? __ldg(sa) : 0.f;
+        ss[u][n][1] = here && t + 1 < p.M ? __ldg(sa + 1) : 0.f;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int g = gb + u * WARPS;
       if (g >= groups) break;
-      const float f = __ldg(sb + g);
+      const float f = fs[u];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int tok = n * 8 + r;
         float part[4] = {};
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
-          const int k = g * 128 + ch * 64 + c * 16;
-          const uint4 x = load16_or_zero(p.a + tok * p.lda + k, tok < p.M && k < p.K);
+          const uint4 x = xs[u][n][ch];
           const uint4 lo = a[u][ch][0], hi = a[u][ch][1];
           mma_e4m3(part, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
           mma_e4m3(part, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
         }
-        const int t = n * 8 + 2 * c;
-        const float* sa = p.a_scale + g * p.ld_as + t;
-        const float s0 = t < p.M ? __ldg(sa) * f : 0.f, s1 = t + 1 < p.M ? __ldg(sa + 1) * f : 0.f;
+        const float s0 = ss[u][n][0] * f, s1 = ss[u][n][1] * f;
         acc[n][0] = fmaf(part[0], s0, acc[n][0]);
         acc[n][1] = fmaf(part[1], s1, acc[n][1]);
         acc[n][2] = fmaf(part[2], s0, acc[n][2]);
@@ -1247,18 +1265,16 @@ Plan plan(const Fp8Gemm& g, const Resident& resident) {
   return best;
 }
 
-// Where the kernel for a handful of tokens is the faster one: one wave of its CTAs (three an SM, two
-// above 8 tokens) or a small matrix, and few groups per warp.  Measured on GB300 (us, this kernel and
-// the other): 1 token 6.2 / 7.7 at 4096 x 4096, 7.0 / 8.9 at 6144 x 4096, 12.0 / 12.8 at 7168 x 7168,
-// 8.7 / 9.7 at 28672 x 1024, but 10.4 / 9.9 at 8192 x 4096 and 16.3 / 14.8 at 4096 x 14336; 16 tokens
-// 7.4 / 7.9 at 4096 x 4096, but 12.3 / 9.1 at 6144 x 4096.
+// Where the kernel for a handful of tokens is the faster one.  Up to 8 tokens nearly everywhere but for
+// long sums (us, this kernel and the other, one token): 4096 x 4096 6.0 / 7.7, 6144 x 4096 6.4 / 8.8, 7168 x
+// 7168 11.2 / 12.8, 28672 x 1024 8.7 / 9.3, 32000 x 4096 24.2 / 26.6, but 8192 x 8192 15.6 / 15.0 and 4096 x
+// 14336 15.3 / 14.9.  Up to 16 for one wave of its CTAs (two an SM) and short sums: 16 tokens 6.9 / 7.9
+// at 4096 x 4096, but 10.7 / 9.1 at 6144 x 4096 and 11.0 / 10.8 at 4096 x 8192.
 bool handful_applies(const Fp8Gemm& g) {
   const int forced = g_plan.load();
   if (g.M > 16 || g.epilogue == CB_FP8_SWIGLU_FP8) return false;
   if (forced) return forced == HANDFUL_PLAN;
-  const int wave = 16 * 152 * (g.M <= 8 ? 3 : 2);  // features
-  if (g.M > 8) return g.K <= 4096 && g.N <= wave;
-  return g.K <= 8192 && (g.N <= wave || static_cast<long long>(g.N) * g.K <= 30ll << 20);
+  return g.M > 8 ? g.K <= 4096 && g.N <= 16 * 152 * 2 : g.K <= 8192;
 }
 
 // The product of the first `n` tokens, or of the first `n` output features, and the rest of it.
