@@ -1,5 +1,7 @@
 """The 8-bit operators on the GPU against their definition in 64 bits: quantiser, residual RMS norm,
 block-scaled product and the three together.  Tolerances count roundings (tests/fp8_ref.py)."""
+import threading
+
 import pytest
 import torch
 
@@ -450,6 +452,29 @@ def test_two_products_at_once():
         gemm(o1, F32, s1), gemm(o2, F32, s2)
         torch.cuda.synchronize()
         assert torch.equal(o1["c"], want[0]) and torch.equal(o2["c"], want[1])
+
+
+@pytest.mark.parametrize("m,width", [(300, 1024), (20, 1024), (600, 2048), (5, 512)])
+def test_product_as_a_threads_first_call(m, width):
+    """A thread that has not used the device yet, next to one that has."""
+    o, _, _ = operands(m, width, 1040, F32, seed=6)
+    gemm(o, F32)
+    want = o["c"].clone()
+    o["c"].zero_()
+    torch.cuda.synchronize()
+    stream, failed = torch.cuda.Stream(), []
+
+    def call():
+        try:
+            gemm(o, F32, stream)
+        except cb.CacheBlendError as e:
+            failed.append(e)
+
+    thread = threading.Thread(target=call)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not failed and torch.equal(o["c"], want)
 
 
 def test_binding_refuses_what_does_not_fit():
