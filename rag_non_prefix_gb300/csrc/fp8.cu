@@ -212,9 +212,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // Codes and scales of the row h (in f), given 1 / rms.
 template <typename TX, int CH>
 __device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, const TX* __restrict__ weight, int d,
-                                           long long row, uint8_t* __restrict__ codes, long long ldc,
+                                           int t, int T, long long row, uint8_t* __restrict__ codes, long long ldc,
                                            float* __restrict__ scales, long long lds) {
-  const int t = threadIdx.x, T = blockDim.x;
   uint32_t m[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
@@ -253,10 +252,11 @@ __device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, con
   }
 }
 
-template <typename TX, typename TR, bool RES, int CH>
+// WARP: a row is a warp's, eight rows a CTA; else a CTA's.
+template <typename TX, typename TR, bool RES, int CH, bool WARP>
 __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restrict__ x, long long ldx,
                                                                const void* residual, void* residual_out, long long ldr,
-                                                               const TX* __restrict__ weight, int d, float eps,
+                                                               const TX* __restrict__ weight, int rows, int d, float eps,
                                                                uint8_t* __restrict__ codes, long long ldc,
                                                                float* __restrict__ scales, long long lds) {
   pdl_trigger();
@@ -264,8 +264,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
   __shared__ float red[32];
   const TR* res = static_cast<const TR*>(residual);
   TR* res_out = static_cast<TR*>(residual_out);
-  const long long row = blockIdx.x;
-  const int t = threadIdx.x, T = blockDim.x;
+  const long long row = WARP ? static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x, T = WARP ? 32 : blockDim.x;
+  if (WARP && row >= rows) return;
   // every read is under way before the first value is needed (residual_out may be residual, so the
   // compiler may not move a read across its store)
   Piece<TX> px[CH];
@@ -297,8 +298,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
   }
   float even, odd;
   unpair(ss2, even, odd);
-  const float inv_rms = 1.0f / sqrtf(block_sum(even + odd, red) / static_cast<float>(d) + eps);
-  norm_codes<TX, CH>(f, inv_rms, weight, d, row, codes, ldc, scales, lds);
+  const float sum = WARP ? warp_sum(even + odd) : block_sum(even + odd, red);
+  const float inv_rms = 1.0f / sqrtf(sum / static_cast<float>(d) + eps);
+  norm_codes<TX, CH>(f, inv_rms, weight, d, t, T, row, codes, ldc, scales, lds);
 }
 
 template <typename TX, typename TR>
@@ -306,20 +308,29 @@ cudaError_t launch_norm(const void* x, long long ldx, const void* res, void* res
                         int rows, int d, float eps, void* codes, long long ldc, float* scales, long long lds,
                         cudaStream_t s) {
   const int pieces = (d + 7) / 8;
-  auto one = [&](auto kernel, int ch) {
-    const int threads = ((pieces + ch - 1) / ch + 31) / 32 * 32;
-    return launch_chain(kernel, dim3(rows), dim3(threads), 0, s, static_cast<const TX*>(x), ldx,
-                        res, res_out, ldr, static_cast<const TX*>(weight), d, eps, static_cast<uint8_t*>(codes), ldc, scales, lds);
+  auto one = [&](auto kernel, int ch) {  // ch 0: a row is a warp's
+    const int threads = ch ? ((pieces + ch - 1) / ch + 31) / 32 * 32 : 256;
+    return launch_chain(kernel, dim3(ch ? rows : (rows + 7) / 8), dim3(threads), 0, s, static_cast<const TX*>(x), ldx,
+                        res, res_out, ldr, static_cast<const TX*>(weight), rows, d, eps, static_cast<uint8_t*>(codes), ldc,
+                        scales, lds);
   };
+  // A row per warp up to 512 channels, and for many rows without a residual up to 1024: no barrier, an
+  // eighth of the CTAs (8320 x 256 bf16 4.7 us, a CTA a row 9.2; 8320 x 512 7.3 / 9.3; 4000 x 768
+  // without a residual 3.2 / 4.9; with fp32 residuals 4000 x 768 9.5 / 8.1, hence not).
+  if (pieces <= 64 && res)
+    return pieces <= 32 ? one(add_rmsnorm_fp8_kernel<TX, TR, true, 1, true>, 0) : one(add_rmsnorm_fp8_kernel<TX, TR, true, 2, true>, 0);
+  if (pieces <= 64)
+    return pieces <= 32 ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1, true>, 0) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 2, true>, 0);
+  if (pieces <= 128 && !res && rows >= 1024) return one(add_rmsnorm_fp8_kernel<TX, TX, false, 4, true>, 0);
   // Pieces per thread.  One while the GPU holds all pieces at once (152 SMs x 2048 threads), the
   // shortest way through a row: 1 x 4096 2.1 us (four 3.2), 535 x 4096 with a residual 6.0 (two 6.3).
   // Then two with a residual up to 8192 channels (8320 x 4096 39.7 us, one 45.4; 8320 x 8192 73, one
   // 94, four 74; 1357 x 7168 with an fp32 residual 18.9, one 19.6, four 19.3) and four for longer rows
   // (8320 x 16384 140, two 184) and without a residual (8320 x 4096 22.7, one 33; 8000 x 8192 41, two 51).
   const bool one_piece = pieces <= 1024 && static_cast<long long>(rows) * pieces <= 152 * 2048;
-  if (!res) return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1>, 1) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 4>, 4);
-  if (one_piece) return one(add_rmsnorm_fp8_kernel<TX, TR, true, 1>, 1);
-  return pieces <= 1024 ? one(add_rmsnorm_fp8_kernel<TX, TR, true, 2>, 2) : one(add_rmsnorm_fp8_kernel<TX, TR, true, 4>, 4);
+  if (!res) return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1, false>, 1) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 4, false>, 4);
+  if (one_piece) return one(add_rmsnorm_fp8_kernel<TX, TR, true, 1, false>, 1);
+  return pieces <= 1024 ? one(add_rmsnorm_fp8_kernel<TX, TR, true, 2, false>, 2) : one(add_rmsnorm_fp8_kernel<TX, TR, true, 4, false>, 4);
 }
 
 }  // namespace

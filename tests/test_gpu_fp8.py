@@ -138,6 +138,14 @@ def test_norm_matches_definition(rows, d, xt, rt):
     assert untouched(whole, rows, d) and untouched(sw, scales.shape[0], rows)
 
 
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("bf16", None), ("f32", None)])
+@pytest.mark.parametrize("rows,d", [(9, 128), (613, 256), (1023, 400), (1030, 720), (1029, 1008), (1031, 4112), (700, 8192),
+                                    (330, 8208)])
+def test_norm_of_many_rows(rows, d, xt, rt):
+    """Rows of a warp, of a CTA with one, two and four pieces a thread; rows behind the last one stay."""
+    test_norm_matches_definition(rows, d, xt, rt)
+
+
 def test_norm_in_place_and_without_keeping_the_sum():
     x, res = rand(1, 37, 4096).bfloat16(), rand(2, 37, 4096)
     a = cb.cb_add_rmsnorm_quantize(x, res)
