@@ -5,7 +5,8 @@
 // The tensor core sums the products of one group (four tcgen05.mma kind::f8f6f4 of 32 channels)
 // into tensor memory; eight warps then read that sum, multiply it by the group's two scales and
 // add it to fp32 registers (packed fp32, fma.rn.f32x2), while the tensor core works on the next
-// groups in the rest of tensor memory.  Two kernels, both on CTA pairs (one CTA per SM, M = 256):
+// groups in the rest of tensor memory.  Two kernels, both on CTA pairs (one CTA per SM, M = 256), and a
+// third one for a handful of tokens without tensor memory (below):
 //   - tokens on the tensor core's rows, 256 tokens x 256 features per pair, for many tokens: a
 //     thread's 128 sums belong to one token, so one factor per group scales them all.
 //   - weights on the rows, 256 features x 16 .. 128 tokens per pair, for few tokens: the padding is
