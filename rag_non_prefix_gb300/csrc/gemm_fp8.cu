@@ -1269,8 +1269,9 @@ Plan plan(const Fp8Gemm& g, const Resident& resident) {
 // Where the kernel for a handful of tokens is the faster one.  Up to 8 tokens nearly everywhere but for
 // long sums (us, this kernel and the other, one token): 4096 x 4096 6.0 / 7.7, 6144 x 4096 6.4 / 8.8, 7168 x
 // 7168 11.2 / 12.8, 28672 x 1024 8.7 / 9.3, 57344 x 8192 73 / 80, but 8192 x 8192 15.6 / 15.0 and 4096 x
-// 14336 15.3 / 14.9; and where its many CTAs have little to do each (43776 x 512 9.5 / 8.5, 100000 x 1024 26 / 25).  Up to 16 for one wave of its CTAs (two an SM) and short sums: 16 tokens 6.9 / 7.9
-// at 4096 x 4096, but 10.7 / 9.1 at 6144 x 4096 and 11.0 / 10.8 at 4096 x 8192.
+// 14336 15.3 / 14.9; and where its many CTAs have little to do each (43776 x 512 9.5 / 8.5, 100000 x
+// 1024 26 / 25).  Up to 16 for one wave of its CTAs (two an SM) and short sums: 16 tokens 6.9 / 7.9 at 4096
+// x 4096, but 10.7 / 9.1 at 6144 x 4096 and 11.0 / 10.8 at 4096 x 8192.
 bool handful_applies(const Fp8Gemm& g) {
   const int forced = g_plan.load();
   if (g.M > 16 || g.epilogue == CB_FP8_SWIGLU_FP8) return false;
