@@ -249,6 +249,15 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
       "r"(el)
       : "memory");
 }
+// Arrival of one lane (el) on a barrier of this CTA, with release to the CTA.
+__device__ __forceinline__ void mbar_arrive_elected(uint64_t* bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(el)
+      : "memory");
+}
 __device__ __forceinline__ void fence_cta() { asm volatile("fence.acq_rel.cta;" ::: "memory"); }
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -262,6 +271,7 @@ struct Bars {
   // of both CTAs have read the accumulator
   uint64_t full[MAX_STAGES];
   uint64_t done[MAX_STAGES];      // its MMAs are done: the stage is free and the group's sums are readable
+  uint64_t read[MAX_STAGES];      // few tokens: the eight warps of this CTA have read its factors
   uint64_t raw_full[2][RAW_SLOTS];  // token scales of a factor warp have landed
   uint64_t part_full;             // few tokens: the cluster's parts of this CTA's tokens have arrived
   uint64_t part_free;             // every CTA of the cluster has read its parts
@@ -275,6 +285,7 @@ __device__ __forceinline__ void init_bars(Bars& bars, int split) {
   for (int s = 0; s < MAX_STAGES; ++s) {
     mbar_init(&bars.full[s], 3 + 16);  // the producer of codes, the factor warps, the readers
     mbar_init(&bars.done[s], 1);
+    mbar_init(&bars.read[s], 8);
   }
   for (int s = 0; s < 2 * RAW_SLOTS; ++s) mbar_init(&bars.raw_full[0][s], 1);
   mbar_init(&bars.part_full, 1);
@@ -369,14 +380,20 @@ __device__ __forceinline__ void load_codes(Bars& bars, const Params& p, int g0, 
 
 // Factor warp `which` of two (all lanes): loads the token scales of every second group, RAW_SLOTS of
 // them ahead, and multiplies them by the scales of two weight blocks, sb0 and sb1 of a unit's weight
-// tile; `put` stores token t's two factors into the stage's lists.  A list is free once every reader
-// has read an accumulator n_acc groups further on, which that group's MMAs waited for: when the
-// group stages - n_acc before this one is done.
-template <int TILE, int TOKENS, int COLUMNS, typename Blocks, typename Put>
+// tile; `put` stores token t's two factors into the stage's lists.  When a list is free (the relaxed
+// arrival that frees an accumulator orders no read of the lists):
+//   few tokens: once its readers have announced that they hold the stage's previous factors (`read`,
+//   an arrival that releases their reads to this CTA);
+//   many tokens: once the MMAs n_acc groups later are done, which waited for the accumulator.  Readers
+//   free it after the last of eight reads of tensor memory, when the sums of all reads but the last two
+//   have used both factors (the values of more reads would not fit the registers).  (An arrival on
+//   `read` of its own: 2048 x 7168 x 7168 with an addend 94 -> 100 us, 1357 x 7168 x 20480 170 -> 176.)
+template <int TILE, int TOKENS, typename Blocks, typename Put>
 __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, const CUtensorMap* tmS, uint8_t* smem,
                                                 int g0, int g1, int cid, int NC, int which, int lane, uint32_t lead,
                                                 int tok_off, Blocks blocks, Put put) {
-  const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(COLUMNS);
+  constexpr bool MANY = TILE == 256;
+  const uint32_t stages = static_cast<uint32_t>(p.stages), ahead = stages - n_acc(256);
   const uint32_t full_lead = mapa_shared(smem_u32(bars.full), lead), el = lane == 0;
   float* raw = reinterpret_cast<float*>(smem + OFF_RAW) + which * RAW_SLOTS * 128;
   uint8_t* sc = smem + OFF_SC;
@@ -417,7 +434,8 @@ __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, con
       if ((n & 1u) == static_cast<uint32_t>(which)) {
         const float f0 = __shfl_sync(0xffffffffu, b0, i), f1 = __shfl_sync(0xffffffffu, b1, i);
         ok = mbar_wait_bounded(&bars.raw_full[which][r.i], r.ph, &bars.abort) &&
-             (n < ahead || mbar_wait_bounded(&bars.done[done.i], done.ph, &bars.abort));
+             (MANY ? n < ahead || mbar_wait_bounded(&bars.done[done.i], done.ph, &bars.abort)
+                   : mbar_wait_bounded(&bars.read[s.i], s.ph ^ 1u, &bars.abort));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         float* lists = reinterpret_cast<float*>(sc + s.i * FACTOR_BYTES);
@@ -433,7 +451,7 @@ __device__ __forceinline__ void multiply_scales(Bars& bars, const Params& p, con
         r.next(RAW_SLOTS);
       }
       s.next(stages);
-      if (n >= ahead) done.next(stages);
+      if (MANY && n >= ahead) done.next(stages);
     }
   }
   if (!ok && lane == 0) report_timeout(bars, p.g.status);
@@ -533,7 +551,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1 && h == 0) {
       issue_mmas<256>(bars, p, ring, tmem, G, cid, NC, 0, rank, lane);
     } else if (warp >= 2) {
-      multiply_scales<256, 128, 256>(
+      multiply_scales<256, 128>(
           bars, p, &tmS, smem, 0, G, cid, NC, warp - 2, lane, 0, h * 128,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // features past the last block are zeros: any block's scale will do
@@ -820,7 +838,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1 && h == 0) {
       issue_mmas<BT>(bars, p, ring, tmem, g1 - g0, cid, NC, pair, rank, lane);
     } else if (warp >= 2) {
-      multiply_scales<BT, BT, BT>(
+      multiply_scales<BT, BT>(
           bars, p, &tmS, smem, g0, g1, cid, NC, warp - 2, lane, lead, 0,
           [&](int wt, const float*& sb0, const float*& sb1) {
             // rows past the last block are zeros: any block's scale will do
@@ -886,6 +904,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_wait_ld_of<N8 * 4>(lo);
         tmem_wait_ld_of<N8 * 4>(hi);
         tc_fence_before();
+        __syncwarp();
+        mbar_arrive_elected(&bars.read[st.i], el);
         mbar_arrive_cluster_relaxed(full_lead + next_use * 8, el);
         if (++next_use == stages) next_use = 0;
         if (++b == NACC) b = 0;
@@ -1366,7 +1386,7 @@ bool gemm_fp8_set_plan(int tokens, int split) {
 
 static cudaError_t launch_planned(const Fp8Gemm& g, const Plan& pl, cudaStream_t s) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
-  // (a stage's barrier is read until its accumulator is, and its factors are written ahead)
+  // (readers of a group arrive for the one n_acc further on, whose stage must have ended its previous phase)
   if (pl.bt == 0 || pl.stages <= n_acc(pl.bt)) return cudaErrorInvalidConfiguration;
   const bool tokens = pl.bt == 256;
   Params p{};

@@ -1,0 +1,46 @@
+"""More cases of the 8-bit operators on the GPU: reuse of the products' rings, ranges, offsets, plans,
+against the definition in 64 bits with the bounds of tests/fp8_ref.py."""
+import pytest
+import torch
+
+import rag_non_prefix_gb300 as cb
+from tests import fp8_ref as ref
+from tests._gpu import built
+from tests.test_gpu_fp8 import F32, SWIGLU, check_gemm, gemm, operands
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _build():
+    built()
+
+
+@pytest.fixture
+def set_plan():
+    yield cb.cb_gemm_scaled_set_plan
+    cb.cb_gemm_scaled_set_plan(0, 0)
+
+
+# ---------------------------------------------------------------------------------- rings
+@pytest.mark.parametrize("epi", [F32, SWIGLU])
+@pytest.mark.parametrize("plan", [(16, 1), (16, 3), (32, 2), (48, 1), (64, 1), (80, 3), (96, 1), (128, 1), (128, 2), (256, 1)])
+def test_every_group_meets_its_own_factors(set_plan, plan, epi):
+    """Sums of many more groups than a ring has stages, whose scales differ by orders of magnitude from
+    one group to the next: a list of factors written over before it was read would show."""
+    m, width, k = 130, 640, 7296
+    o, whole, _ = operands(m, width, k, epi, seed=5)
+    o["sa"].mul_(torch.tensor([1.0, 2.0 ** 12, 2.0 ** -12], device="cuda").repeat(19)[:, None])
+    o["sb"].mul_(torch.tensor([1.0, 0.25, 4.0], device="cuda").repeat_interleave(19)[None, :])
+    if epi == SWIGLU:  # gates of about unit size: the products' own bound holds for them as it stands
+        o["sa"].mul_(2.0 ** -9)
+        o["sb2"].mul_(torch.tensor([4.0, 1.0, 0.25], device="cuda").repeat(19)[None, :])
+    set_plan(*plan)
+    gemm(o, epi)
+    check_gemm(o["a"], o["sa"], o["b"], o["sb"], epi, o["c"], None, o["b2"], o["sb2"], o["c_scales"])
+    first = o["c"].view(torch.uint8).clone()
+    for _ in range(20):
+        o["c"].view(torch.uint8).zero_()
+        gemm(o, epi)
+        assert torch.equal(first, o["c"].view(torch.uint8))
+    cb.cb_gemm_get_status()
