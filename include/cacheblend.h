@@ -273,8 +273,9 @@ cb_status cb_gemm_set_orientation(int orientation);
  * 0); 1: never; 2: clusters of one pair; 4: clusters of two pairs (2 and 4 apply where the
  * shape allows pairs: output features a multiple of 256 with the q|k|v split points
  * multiples of 128, SwiGLU features a multiple of 128, K a multiple of 64; a token tile
- * forced by cb_gemm_set_orientation applies to the pairs too).  Results agree to fp32
- * rounding of the same sums.  Other values: CB_ERR_INVALID_ARG. */
+ * forced by cb_gemm_set_orientation applies to the pairs too; clusters of two pairs are used
+ * only where the process sees one GPU and the environment's WORLD_SIZE is unset or 1: runs of
+ * several GPUs load nothing by multicast).  Results agree to fp32 rounding of the same sums.  Other values: CB_ERR_INVALID_ARG. */
 cb_status cb_gemm_set_pairing(int pairing);
 
 /* The schedule a bf16 cb_gemm of M x N x K with `epilogue` and scratch_bytes of scratch

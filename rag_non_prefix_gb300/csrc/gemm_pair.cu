@@ -9,7 +9,8 @@
 // per tensor-core cycle, and L2 -> SM bandwidth is what bounds the single-CTA kernel (ncu on
 // GB300 at 1357 tokens: ~18.5 TB/s of L2 -> SM reads, tensor pipe ~66 % busy).  In a cluster
 // of two pairs both pairs take the same 256 weight rows for two token tiles, and each CTA
-// loads half of its 128 weight rows and multicasts them to its counterpart in the other pair.
+// loads half of its 128 weight rows and multicasts them to its counterpart in the other pair
+// (in runs of one GPU only).
 //   warp 0: TMA producer   warp 1: tensor-memory owner and, in even CTAs, the MMA issuer
 //   warps 2-5: epilogue (tensor memory -> fp32 store, fp32 residual add, or SiLU(gate) * up)
 // A ring stage holds ksub (1 or 2) 64-element atoms of K.  Measured on GB300, each barrier
@@ -25,6 +26,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "internal.h"
@@ -567,6 +569,19 @@ static std::atomic<int> g_pairing{0};
 void gemm_set_pairing(int m) { g_pairing.store(m); }
 int gemm_pairing() { return g_pairing.load(); }
 
+// Clusters of two pairs load by multicast, which only a run of one GPU uses: one GPU visible to the
+// process, and no launcher that says it is a rank of several (WORLD_SIZE, as torchrun sets it).
+static bool run_of_one_gpu() {
+  static const bool one = [] {
+    const char* world = std::getenv("WORLD_SIZE");
+    if (world && std::atoi(world) > 1) return false;
+    int n = 0;
+    if (cudaGetDeviceCount(&n) != cudaSuccess) cudaGetLastError();
+    return n == 1;
+  }();
+  return one;
+}
+
 // Clusters of `cl` CTAs that are resident at once (one CTA per SM), per device.
 static int max_clusters(int cl) {
   static std::atomic<int> cache[2][64];
@@ -640,7 +655,7 @@ bool plan_gemm_pair(int M, int N, int K, int split0, int split1, int mode, int f
   PairPlan best{};
   best.us = 1e30;
   for (int cl = 2; cl <= 4; cl += 2) {
-    if (pm >= 2 && cl != pm) continue;
+    if ((pm >= 2 && cl != pm) || (cl == 4 && !run_of_one_gpu())) continue;
     const int clusters = max_clusters(cl);
     if (clusters <= 0) continue;
     for (int bt = 16; bt <= 256; bt += 16) {
