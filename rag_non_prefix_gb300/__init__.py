@@ -7,6 +7,7 @@ shared library has not been built (``python -m rag_non_prefix_gb300.build``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import struct
@@ -202,6 +203,21 @@ def _stream_on(dev: int, s) -> C.c_void_p:
     return _raw_stream(dev) if s is None and _raw_stream is not None else _stream(s)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _allocating_on(s):
+    """Context in which torch allocates (and fills) for stream ``s`` of a call: the allocator gives out
+    a block as soon as its stream's earlier work covers it, so an output may only come from the stream
+    that the call runs on, and goes back to it."""
+    if s is None:
+        return _HERE
+    if not isinstance(s, torch.cuda.Stream):
+        handle = s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+        s = torch.cuda.ExternalStream(0 if handle == 1 else handle)  # (1: the legacy default stream's other name)
+    return torch.cuda.stream(s)
+
+
 def _check(st: int, ctx=None):
     if st != 0:
         lib = load_library()
@@ -250,7 +266,9 @@ def cb_kv_deviation(k_new: torch.Tensor, v_new: torch.Tensor, k_fus: torch.Tenso
     lib = load_library()
     n = k_new.shape[0]
     width = k_new[0].numel() if n else k_fus[0].numel()
-    out = torch.empty(n, dtype=torch.float32, device=k_new.device) if out is None else out
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty(n, dtype=torch.float32, device=k_new.device)
     _check(lib.cb_kv_deviation(_ptr(k_new), _ptr(v_new), _ptr(k_fus), _ptr(v_fus), _ptr(idx), n, width, mode,
                                _dtype_code(k_fus.dtype), _ptr(out), _stream(stream)))
     return out
@@ -259,7 +277,9 @@ def cb_kv_deviation(k_new: torch.Tensor, v_new: torch.Tensor, k_fus: torch.Tenso
 def cb_select_hkvd(dev: torch.Tensor, cand: Optional[torch.Tensor], k: int, out: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     lib = load_library()
-    out = torch.empty(k, dtype=torch.int32, device=dev.device) if out is None else out
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty(k, dtype=torch.int32, device=dev.device)
     _check(lib.cb_select_hkvd(_ptr(dev), _ptr(cand), dev.numel(), int(k), _ptr(out), _ptr(status), _stream(stream)))
     return out
 
@@ -354,7 +374,9 @@ def cb_attention(q: torch.Tensor, q_pos: torch.Tensor, k: torch.Tensor, v: torch
     lib = load_library()
     m, H, dh = q.shape
     n_kv, hkv, _ = k.shape
-    out = torch.empty_like(q) if out is None else out
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty_like(q)
     _check(lib.cb_attention(_ptr(q), _ptr(q_pos), m, _ptr(k), _ptr(v), n_kv, H, hkv, dh, _ptr(out),
                             _dtype_code(q.dtype), _stream(stream)))
     return out
@@ -407,14 +429,17 @@ def cb_quantize(x: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tens
     ceil(cols / 128)])."""
     dt = _dtype_code(x.dtype)
     rows, cols, ldx, dev = _first(x, "x")
-    if codes is None:
-        codes = torch.empty(rows, cols, dtype=_E4M3, device=x.device)
     groups, blocks = (cols + 127) // 128, (rows + 127) // 128
+    if codes is None or scales is None:
+        with _allocating_on(stream):
+            if codes is None:
+                codes = torch.empty(rows, cols, dtype=_E4M3, device=x.device)
+            if scales is None:
+                scales = (row_scales(rows, cols, x.device) if block_rows == 1 else
+                          torch.empty(blocks, groups, dtype=torch.float32, device=x.device))
     if block_rows == 1:
-        scales = row_scales(rows, cols, x.device) if scales is None else scales
         lds = _pitch(scales, torch.float32, groups, rows, "scales", dev)
     else:
-        scales = torch.empty(blocks, groups, dtype=torch.float32, device=x.device) if scales is None else scales
         lds = _pitch(scales, torch.float32, blocks, groups, "scales", dev)
     _check(load_library().cb_quantize(x.data_ptr(), ldx, rows, cols, dt, block_rows, codes.data_ptr(),
                                       _pitch(codes, _E4M3, rows, cols, "codes", dev), scales.data_ptr(), lds,
@@ -445,9 +470,10 @@ def cb_add_rmsnorm_quantize(x: torch.Tensor, residual: Optional[torch.Tensor] = 
         if weight.dtype is not dtype or weight.shape != (d,) or not weight.is_contiguous() or weight.get_device() != dev:
             raise CacheBlendError(2, f"weight must be {d} contiguous elements of {dtype} on the current CUDA device")
         w = weight.data_ptr()
-    if codes is None:
-        codes = torch.empty(rows, d, dtype=_E4M3, device=x.device)
-    scales = row_scales(rows, d, x.device) if scales is None else scales
+    if codes is None or scales is None:
+        with _allocating_on(stream):
+            codes = torch.empty(rows, d, dtype=_E4M3, device=x.device) if codes is None else codes
+            scales = row_scales(rows, d, x.device) if scales is None else scales
     _check(load_library().cb_add_rmsnorm_quantize(
         x.data_ptr(), ldx, dt, res, res_out, ldr, rdt, w, rows, d, eps, codes.data_ptr(),
         _pitch(codes, _E4M3, rows, d, "codes", dev), scales.data_ptr(),
@@ -540,7 +566,9 @@ def cb_kv_encode(k: torch.Tensor, v: torch.Tensor, bits: int, blob: Optional[tor
     lib = load_library()
     L, n, hkv, dh = k.shape
     nbytes = L * cb_codec_layer_bytes(n, hkv, dh, bits)
-    blob = torch.empty(nbytes, dtype=torch.uint8, device=k.device) if blob is None else blob
+    if blob is None:
+        with _allocating_on(stream):
+            blob = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
     _check(lib.cb_kv_encode(_ptr(k), _ptr(v), L, n, hkv, dh, _dtype_code(k.dtype), int(bits), _ptr(blob),
                             _stream(stream)))
     return blob
@@ -551,8 +579,9 @@ def cb_kv_decode(blob: torch.Tensor, shape, bits: int, delta_pos: int, theta: fl
     """Dequantised k, v [L, n, Hkv, dh] of a blob, keys re-rotated by ``delta_pos`` positions."""
     lib = load_library()
     L, n, hkv, dh = shape
-    k = torch.empty(shape, dtype=dtype, device=blob.device)
-    v = torch.empty_like(k)
+    with _allocating_on(stream):
+        k = torch.empty(shape, dtype=dtype, device=blob.device)
+        v = torch.empty_like(k)
     _check(lib.cb_kv_decode(_ptr(blob), L, n, hkv, dh, int(bits), int(delta_pos), float(theta), _dtype_code(dtype),
                             _ptr(k), _ptr(v), _stream(stream)))
     return k, v
@@ -612,8 +641,9 @@ class Engine:
 
     def precompute_chunk(self, ids: torch.Tensor, stream=None):
         n = ids.numel()
-        k = torch.empty(self.kv_shape(n), dtype=self.dtype, device=self.device)
-        v = torch.empty_like(k)
+        with _allocating_on(stream):
+            k = torch.empty(self.kv_shape(n), dtype=self.dtype, device=self.device)
+            v = torch.empty_like(k)
         _check(self.lib.cb_precompute_chunk(self.ctx, _ptr(ids), n, _ptr(k), _ptr(v), _stream(stream)), self.ctx)
         return k, v
 
@@ -728,11 +758,12 @@ class Engine:
 
     def full_prefill(self, ids: torch.Tensor, want_kv=False, want_hidden=True, stream=None):
         n = ids.numel()
-        out = {"first_token": torch.full((1,), -1, dtype=torch.int32, device=self.device)}
-        out["hidden"] = torch.zeros((n, self.cfg.d_model), dtype=torch.float32, device=self.device) if want_hidden else None
-        if want_kv:
-            out["k"] = torch.empty(self.kv_shape(n), dtype=self.dtype, device=self.device)
-            out["v"] = torch.empty_like(out["k"])
+        with _allocating_on(stream):
+            out = {"first_token": torch.full((1,), -1, dtype=torch.int32, device=self.device)}
+            out["hidden"] = torch.zeros((n, self.cfg.d_model), dtype=torch.float32, device=self.device) if want_hidden else None
+            if want_kv:
+                out["k"] = torch.empty(self.kv_shape(n), dtype=self.dtype, device=self.device)
+                out["v"] = torch.empty_like(out["k"])
         _check(self.lib.cb_full_prefill(self.ctx, _ptr(ids), n, _ptr(out.get("k")), _ptr(out.get("v")),
                                         _ptr(out["hidden"]), _ptr(out["first_token"]), _stream(stream)), self.ctx)
         return out
@@ -743,7 +774,9 @@ class Engine:
         tokens [n] enter at positions n_past[i] (default: each request's prompt length plus the
         steps it already decoded); returns the next tokens [n]."""
         n = len(reqs)
-        out_tokens = torch.empty(n, dtype=torch.int32, device=self.device) if out_tokens is None else out_tokens
+        if out_tokens is None:
+            with _allocating_on(stream):
+                out_tokens = torch.empty(n, dtype=torch.int32, device=self.device)
         arr = (DecodeSeq * n)()
         for i, r in enumerate(reqs):
             past = r["n_tokens"] + r.setdefault("decoded", 0) if n_past is None else int(n_past[i])
