@@ -1231,7 +1231,8 @@ Resident resident_clusters() {
   return r;
 }
 
-// cb_gemm_scaled_set_plan: tokens per tile (0: the model decides) * 8 + pairs per cluster.
+// cb_gemm_scaled_set_plan: tokens per tile (0: the model decides) * 8 + pairs per cluster.  A call reads
+// it once and hands it down (`hook`), so that all its decisions agree.
 std::atomic<int> g_plan{0};
 
 constexpr int HANDFUL_PLAN = 1 * 8;  // cb_gemm_scaled_set_plan(1, 0)
@@ -1246,11 +1247,11 @@ struct Plan {
 // 256 tokens on the rows and 0.18 + 0.0017 bt us with the weights on them, a unit's output 1.9 us and
 // 1.7 + 0.017 bt us; units go round the resident clusters (76 of one pair, 36 of two, 23 of three, 15
 // of four); the weights come at 6.5 TB/s at the most.
-Plan plan(const Fp8Gemm& g, const Resident& resident) {
+Plan plan(const Fp8Gemm& g, const Resident& resident, int hook) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
   const int width = swiglu ? g.N / 2 : g.N, groups = (g.K + 127) / 128;
   const int w_tiles = swiglu ? (width + 127) / 128 : (width + 255) / 256;
-  const int forced = g_plan.load() == HANDFUL_PLAN ? 0 : g_plan.load();
+  const int forced = hook == HANDFUL_PLAN ? 0 : hook;
   Plan best{};
   double best_us = 1e30;
   auto consider = [&](int bt, int split) {
@@ -1292,10 +1293,9 @@ Plan plan(const Fp8Gemm& g, const Resident& resident) {
 // 14336 15.3 / 14.9; and where its many CTAs have little to do each (43776 x 512 9.5 / 8.5, 100000 x
 // 1024 26 / 25).  Up to 16 for one wave of its CTAs (two an SM) and short sums: 16 tokens 6.9 / 7.9 at 4096
 // x 4096, but 10.7 / 9.1 at 6144 x 4096 and 11.0 / 10.8 at 4096 x 8192.
-bool handful_applies(const Fp8Gemm& g) {
-  const int forced = g_plan.load();
+bool handful_applies(const Fp8Gemm& g, int hook) {
   if (g.M > 16 || g.epilogue == CB_FP8_SWIGLU_FP8) return false;
-  if (forced) return forced == HANDFUL_PLAN;
+  if (hook) return hook == HANDFUL_PLAN;
   if (g.M > 8) return g.K <= 4096 && g.N <= 16 * 152 * 2;
   return g.K <= 8192 && (g.K >= 2048 || g.N <= 4 * 16 * 152 * 3);
 }
@@ -1346,29 +1346,42 @@ Fp8Gemm other_features(const Fp8Gemm& g, int n) {
 // 1100 x 4096 x 14336 99 / 70, 1357 x 7168 x 20480 206 / 176, 8320 x 8192 x 8192 433 / 410; where the model promises less than
 // 4 percent two parts took up to 9 percent longer (700 x 8192 x 8192 58 / 63).
 constexpr double SECOND_LAUNCH_US = 4, WORTH_IT = 0.96;
-struct Parts {
-  int tokens = 0, features = 0;  // of the first part; 0, 0: one part
+// How a call runs: the kernel for a handful of tokens, or one or two products with their plans.
+struct Schedule {
+  bool handful = false;
+  int n = 0;
+  Fp8Gemm g[2];
+  Plan pl[2];
 };
-Parts parts(const Fp8Gemm& g, const Plan& whole, const Resident& resident) {
-  Parts best;
+Schedule schedule(const Fp8Gemm& g, int hook) {
+  Schedule one;
+  one.handful = handful_applies(g, hook);
+  if (one.handful) return one;
+  const Resident resident = resident_clusters();
+  one.n = 1;
+  one.g[0] = g;
+  one.pl[0] = plan(g, resident, hook);
   const int pairs = resident.clusters[0];
-  if (pairs <= 0 || g.M <= 256 || g_plan.load()) return best;
+  if (pairs <= 0 || g.M <= 256 || hook) return one;
   const int tile = g.epilogue == CB_FP8_SWIGLU_FP8 ? 128 : 256;
   const int width = g.epilogue == CB_FP8_SWIGLU_FP8 ? g.N / 2 : g.N;
   const int t = (g.M + 255) / 256, w = (width + tile - 1) / tile;
   const long long rounds = (static_cast<long long>(t) * w + pairs - 1) / pairs;
-  double us = WORTH_IT * whole.us;
   // the most tiles along one axis that stay within one round less
   const long long fewer = (rounds - 1) * pairs;
   const int tk = static_cast<int>(fewer / w), fk = static_cast<int>(fewer / t);
-  if (tk > 0) {
-    const double both = plan(first_tokens(g, tk * 256), resident).us + plan(other_tokens(g, tk * 256), resident).us + SECOND_LAUNCH_US;
-    if (both < us) us = both, best = Parts{tk * 256, 0};
-  }
-  if (fk > 0) {
-    const double both = plan(first_features(g, fk * tile), resident).us + plan(other_features(g, fk * tile), resident).us + SECOND_LAUNCH_US;
-    if (both < us) us = both, best = Parts{0, fk * tile};
-  }
+  Schedule best = one;
+  double us = WORTH_IT * one.pl[0].us;
+  auto consider = [&](const Fp8Gemm& first, const Fp8Gemm& rest) {
+    const Plan a = plan(first, resident, hook), b = plan(rest, resident, hook);
+    if (a.us + b.us + SECOND_LAUNCH_US >= us) return;
+    us = a.us + b.us + SECOND_LAUNCH_US;
+    best.n = 2;
+    best.g[0] = first, best.g[1] = rest;
+    best.pl[0] = a, best.pl[1] = b;
+  };
+  if (tk > 0) consider(first_tokens(g, tk * 256), other_tokens(g, tk * 256));
+  if (fk > 0) consider(first_features(g, fk * tile), other_features(g, fk * tile));
   return best;
 }
 
@@ -1384,12 +1397,19 @@ bool gemm_fp8_set_plan(int tokens, int split) {
   return true;
 }
 
-static cudaError_t launch_planned(const Fp8Gemm& g, const Plan& pl, cudaStream_t s) {
+// One product ready to be launched.
+struct Prepared {
+  CUtensorMap mx, mw, mw2, ms, mc;
+  Params p;
+  Kernel fn;
+  int ctas, cluster;
+};
+static cudaError_t prepare(const Fp8Gemm& g, const Plan& pl, Prepared& r) {
   const bool swiglu = g.epilogue == CB_FP8_SWIGLU_FP8;
   // (readers of a group arrive for the one n_acc further on, whose stage must have ended its previous phase)
   if (pl.bt == 0 || pl.stages <= n_acc(pl.bt)) return cudaErrorInvalidConfiguration;
   const bool tokens = pl.bt == 256;
-  Params p{};
+  Params& p = r.p;
   p.g = g;
   p.width = swiglu ? g.N / 2 : g.N;
   p.tok_tiles = (g.M + pl.bt - 1) / pl.bt;
@@ -1403,54 +1423,55 @@ static cudaError_t launch_planned(const Fp8Gemm& g, const Plan& pl, cudaStream_t
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, F32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   const auto SW = CU_TENSOR_MAP_SWIZZLE_128B;
   const int w_rows = swiglu && !tokens ? 64 : 128;
-  CUtensorMap mx, mw, mw2, ms, mc;
-  bool ok = encode_tmap(&mx, U8, g.a, g.K, g.M, g.lda, 128, tokens ? 128 : pl.bt / 2, SW) &&
-            encode_tmap(&ms, F32, g.a_scale, g.M, p.groups, g.ld_as * 4, tokens ? 128 : pl.bt, 1,
+  bool ok = encode_tmap(&r.mx, U8, g.a, g.K, g.M, g.lda, 128, tokens ? 128 : pl.bt / 2, SW) &&
+            encode_tmap(&r.ms, F32, g.a_scale, g.M, p.groups, g.ld_as * 4, tokens ? 128 : pl.bt, 1,
                         CU_TENSOR_MAP_SWIZZLE_NONE) &&
-            encode_tmap(&mw, U8, g.b, g.K, p.width, g.ldb, 128, w_rows, SW);
-  mw2 = mw;
-  if (swiglu) ok = ok && encode_tmap(&mw2, U8, g.b2, g.K, p.width, g.ldb2, 128, w_rows, SW);
-  mc = mx;
-  if (tokens && swiglu) ok = ok && encode_tmap(&mc, U8, g.c, p.width, g.M, g.ldc, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+            encode_tmap(&r.mw, U8, g.b, g.K, p.width, g.ldb, 128, w_rows, SW);
+  r.mw2 = r.mw;
+  if (swiglu) ok = ok && encode_tmap(&r.mw2, U8, g.b2, g.K, p.width, g.ldb2, 128, w_rows, SW);
+  r.mc = r.mx;
+  if (tokens && swiglu) ok = ok && encode_tmap(&r.mc, U8, g.c, p.width, g.M, g.ldc, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (tokens && g.epilogue == CB_FP8_STORE_BF16)
-    ok = ok && encode_tmap(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.c, p.width, g.M, g.ldc * 2, 32, 32,
+    ok = ok && encode_tmap(&r.mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.c, p.width, g.M, g.ldc * 2, 32, 32,
                            CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return cudaErrorInvalidValue;
-  Kernel fn = kernel_of(pl.bt, g.epilogue);
+  r.fn = kernel_of(pl.bt, g.epilogue);
+  r.ctas = 2 * pl.split * std::min(pl.clusters, p.units);
+  r.cluster = 2 * pl.split;
   static DeviceOnce once[4][17];
-  cudaError_t e = max_dynamic_smem_once(reinterpret_cast<const void*>(fn), SMEM_ALLOC, once[g.epilogue][pl.bt / 16]);
-  if (e != cudaSuccess) return e;
+  return max_dynamic_smem_once(reinterpret_cast<const void*>(r.fn), SMEM_ALLOC, once[g.epilogue][pl.bt / 16]);
+}
+static cudaError_t launch(const Prepared& r, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pl.split * std::min(pl.clusters, p.units));
+  cfg.gridDim = dim3(r.ctas);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_ALLOC;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * pl.split;
+  attr[0].val.clusterDim.x = r.cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = launch_overlap_enabled() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, fn, mx, mw, mw2, ms, mc, static_cast<const Params>(p));
+  return cudaLaunchKernelEx(&cfg, r.fn, r.mx, r.mw, r.mw2, r.ms, r.mc, r.p);
 }
 
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.M <= 0) return cudaSuccess;
-  if (handful_applies(g)) {
+  const Schedule sched = schedule(g, g_plan.load());
+  if (sched.handful) {
     const dim3 grid((g.N + 15) / 16), block(256);
     return g.M <= 8 ? launch_chain(gemm_fp8_handful_kernel<1>, grid, block, 0, s, g)
                     : launch_chain(gemm_fp8_handful_kernel<2>, grid, block, 0, s, g);
   }
-  const Resident resident = resident_clusters();
-  const Plan whole = plan(g, resident);
-  const Parts pt = parts(g, whole, resident);
-  if (!pt.tokens && !pt.features) return launch_planned(g, whole, s);
-  const Fp8Gemm first = pt.tokens ? first_tokens(g, pt.tokens) : first_features(g, pt.features);
-  const Fp8Gemm rest = pt.tokens ? other_tokens(g, pt.tokens) : other_features(g, pt.features);
-  const cudaError_t e = launch_planned(first, plan(first, resident), s);
-  return e == cudaSuccess ? launch_planned(rest, plan(rest, resident), s) : e;
+  // (both parts are prepared before one is launched: nothing is enqueued for a call that is refused)
+  Prepared part[2];
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; e == cudaSuccess && i < sched.n; ++i) e = prepare(sched.g[i], sched.pl[i], part[i]);
+  for (int i = 0; e == cudaSuccess && i < sched.n; ++i) e = launch(part[i], s);
+  return e;
 }
 
 }  // namespace cb

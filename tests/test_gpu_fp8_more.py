@@ -1,12 +1,15 @@
 """More cases of the 8-bit operators on the GPU: reuse of the products' rings, ranges, offsets, plans,
 against the definition in 64 bits with the bounds of tests/fp8_ref.py."""
+import ctypes as C
+import subprocess
+
 import pytest
 import torch
 
 import rag_non_prefix_gb300 as cb
 from tests import fp8_ref as ref
 from tests._gpu import built
-from tests.test_gpu_fp8 import F32, SWIGLU, check_gemm, gemm, operands
+from tests.test_gpu_fp8 import ADD, F32, SWIGLU, check_gemm, gemm, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +47,39 @@ def test_every_group_meets_its_own_factors(set_plan, plan, epi):
         gemm(o, epi)
         assert torch.equal(first, o["c"].view(torch.uint8))
     cb.cb_gemm_get_status()
+
+
+# ---------------------------------------------------------------------------------- the tuning hook
+TURNER = """
+#include <pthread.h>
+typedef int (*set_plan)(int, int);
+static set_plan set;
+static volatile int on;
+static pthread_t thread;
+static void *turn(void *unused) {
+  while (on) set(1, 0), set(0, 0);
+  return unused;
+}
+void turner_start(set_plan f) { set = f, on = 1; pthread_create(&thread, 0, turn, 0); }
+void turner_stop(void) { on = 0; pthread_join(thread, 0); }
+"""
+
+
+def test_plan_changed_by_another_thread_in_the_middle_of_calls(set_plan, tmp_path):
+    """A call reads the hook once: it has a plan whatever another thread sets meanwhile."""
+    (tmp_path / "turner.c").write_text(TURNER)
+    subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-pthread", str(tmp_path / "turner.c"), "-o",
+                    str(tmp_path / "turner.so")], check=True)
+    turner = C.CDLL(str(tmp_path / "turner.so"))
+    few, _, _ = operands(40, 512, 640, F32, seed=8)
+    two, _, _ = operands(531, 7190, 4112, ADD, seed=9)  # (two parts, but for the hook)
+    turner.turner_start(C.cast(cb.load_library().cb_gemm_scaled_set_plan, C.c_void_p))
+    try:
+        for _ in range(200):
+            gemm(few, F32)
+            gemm(two, ADD)
+    finally:
+        turner.turner_stop()
+    set_plan(0, 0)
+    check_gemm(few["a"], few["sa"], few["b"], few["sb"], F32, few["c"])
+    check_gemm(two["a"], two["sa"], two["b"], two["sb"], ADD, two["c"], two["addend"])
