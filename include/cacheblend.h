@@ -375,7 +375,8 @@ cb_status cb_quantize(const void* x, long long ldx, int rows, int cols, cb_dtype
 /* RMS norm with the residual's addition and an 8-bit output, one pass over each row:
  *   h = residual + x,  residual_out = h,  y = h / sqrt(mean(h^2) + eps) * weight,  quantised as a
  * row matrix.  h, its sum of squares and y are fp32 (y comes from h before it is rounded to
- * residual_out's type).  x [rows][d] of x_dtype (pitch ldx); residual, residual_out [rows][d] of
+ * residual_out's type; a row whose squares leave fp32's range is summed times a power of two, so
+ * that rows of any finite h have their norm).  x [rows][d] of x_dtype (pitch ldx); residual, residual_out [rows][d] of
  * res_dtype with the same pitch ld_res, residual_out may be residual (in place) or NULL (not
  * kept); residual NULL normalises x alone (residual_out must be NULL then); weight [d] of x_dtype
  * or NULL for ones.  d <= 32768.  The codes may not overlap an input. */

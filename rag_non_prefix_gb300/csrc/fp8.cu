@@ -209,6 +209,33 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.f);
 }
 
+// Sum of the squares of the values in f over the row (a warp's or the CTA's).
+template <int CH, bool WARP> __device__ __forceinline__ float sum_of_squares(const float (&f)[CH][8], float* red) {
+  uint64_t ss2 = 0;
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(ss2) : "l"(pair(f[k][j], f[k][j + 1])));
+  float even, odd;
+  unpair(ss2, even, odd);
+  return WARP ? warp_sum(even + odd) : block_sum(even + odd, red);
+}
+
+// The mean of squares, with eps, of a row (in f) where it came out beyond 2^100 or below 2^-100, so that
+// the sum may have overflowed or gone under: again for the row times 2^-80 (its largest magnitude is
+// then between 2^-30 and 2^48) or 2^100 (2^-49 .. 2^58), which the norm takes out again.  f keeps that
+// row.
+template <int CH, bool WARP>
+__device__ __forceinline__ float rescaled_mean(float (&f)[CH][8], float mean, float eps, int d, float* red) {
+  const float s = mean > 1.0f ? 0x1p-80f : 0x1p100f;
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[k][j] *= s;
+  if (!WARP) __syncthreads();  // (the sums in red have been read)
+  return sum_of_squares<CH, WARP>(f, red) / static_cast<float>(d) + eps * s * s;
+}
+
 // Codes and scales of the row h (in f), given 1 / rms.
 template <typename TX, int CH>
 __device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, const TX* __restrict__ weight, int d,
@@ -252,13 +279,15 @@ __device__ __forceinline__ void norm_codes(float (&f)[CH][8], float inv_rms, con
   }
 }
 
-// WARP: a row is a warp's, eight rows a CTA; else a CTA's.
+// WARP: a row is a warp's, eight rows a CTA; else a CTA's.  (Two pieces a thread, all in bf16: 40 registers
+// let three CTAs of 512 threads share an SM.)
 template <typename TX, typename TR, bool RES, int CH, bool WARP>
-__global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restrict__ x, long long ldx,
-                                                               const void* residual, void* residual_out, long long ldr,
-                                                               const TX* __restrict__ weight, int rows, int d, float eps,
-                                                               uint8_t* __restrict__ codes, long long ldc,
-                                                               float* __restrict__ scales, long long lds) {
+__global__ void __launch_bounds__(CH == 2 && !WARP ? 512 : 1024, CH == 2 && !WARP && sizeof(TX) + sizeof(TR) == 4 ? 3 : 1)
+    add_rmsnorm_fp8_kernel(const TX* __restrict__ x, long long ldx,
+                           const void* residual, void* residual_out, long long ldr,
+                           const TX* __restrict__ weight, int rows, int d, float eps,
+                           uint8_t* __restrict__ codes, long long ldc,
+                           float* __restrict__ scales, long long lds) {
   pdl_trigger();
   pdl_wait();
   __shared__ float red[32];
@@ -299,7 +328,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(const TX* __restr
   float even, odd;
   unpair(ss2, even, odd);
   const float sum = WARP ? warp_sum(even + odd) : block_sum(even + odd, red);
-  const float inv_rms = 1.0f / sqrtf(sum / static_cast<float>(d) + eps);
+  float mean = sum / static_cast<float>(d) + eps;
+  if (mean < 0x1p-100f || mean > 0x1p100f) mean = rescaled_mean<CH, WARP>(f, mean, eps, d, red);  // (uniform in the row)
+  const float inv_rms = 1.0f / sqrtf(mean);
   norm_codes<TX, CH>(f, inv_rms, weight, d, t, T, row, codes, ldc, scales, lds);
 }
 

@@ -9,7 +9,7 @@ import torch
 import rag_non_prefix_gb300 as cb
 from tests import fp8_ref as ref
 from tests._gpu import built
-from tests.test_gpu_fp8 import ADD, F32, SWIGLU, check_gemm, gemm, operands
+from tests.test_gpu_fp8 import ADD, DT, F32, HALF, SWIGLU, check_gemm, check_norm, gemm, operands, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,55 @@ def test_plan_changed_by_another_thread_in_the_middle_of_calls(set_plan, tmp_pat
     set_plan(0, 0)
     check_gemm(few["a"], few["sa"], few["b"], few["sb"], F32, few["c"])
     check_gemm(two["a"], two["sa"], two["b"], two["sb"], ADD, two["c"], two["addend"])
+
+
+# ---------------------------------------------------------------------------------- ranges
+@pytest.mark.parametrize("rt", [None, "f32", "bf16"])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,d", [(3, 16), (9, 256), (40, 512), (1030, 1008), (7, 4096), (1031, 4112), (330, 8208), (2, 32768)])
+def test_norm_of_rows_whose_squares_leave_fp32(rows, d, xt, rt):
+    """Rows of any size that the type has: their squares' sum is infinite, subnormal or zero in fp32."""
+    x = rand(d, rows, d)
+    size = torch.tensor([1e20, 1.0, 1e37, 1e-3, 3e18, 1e30, 1e-30], device="cuda")[torch.arange(rows, device="cuda") % 7]
+    x = (x * size[:, None]).to(DT[xt])
+    res = None if rt is None else (rand(d + 1, rows, d) * size[:, None]).to(DT[rt])
+    weight = (1 + 0.1 * rand(7, d)).to(DT[xt]) if rows % 2 else None
+    out = None if rt is None else torch.empty_like(res)
+    codes, scales, _ = cb.cb_add_rmsnorm_quantize(x, res, weight, 1e-5, out)
+    check_norm(x, res, weight, 1e-5, codes, scales, out)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-36, 1e-20])
+@pytest.mark.parametrize("rt", [None, "f32", "bf16"])
+@pytest.mark.parametrize("rows,d", [(8, 256), (41, 512), (7, 4096), (1031, 4112), (3, 16384)])
+def test_norm_of_tiny_rows_with_little_or_no_eps(rows, d, rt, eps):
+    x = rand(d, rows, d)
+    size = torch.tensor([1e-25, 1.0, 1e-20, 1e-30, 1e20, 3e-19, 1e-36], device="cuda")[torch.arange(rows, device="cuda") % 7]
+    x = x * size[:, None]
+    res = None if rt is None else (rand(d + 1, rows, d) * size[:, None]).to(DT[rt])
+    out = None if rt is None else torch.empty_like(res)
+    codes, scales, _ = cb.cb_add_rmsnorm_quantize(x, res, None, eps, out)
+    # (eps is an fp32 argument: 1e-44 is 7 of its smallest steps 2^-149, that is 9.8e-45)
+    check_norm(x, res, None, float(torch.tensor(eps, dtype=torch.float32)), codes, scales, None)
+    if out is not None:
+        # the sum's rounding to its type is relative only above 2^-126: bf16 numbers below are 2^-133 apart,
+        # fp32 ones 2^-149, and a rounding is off by half of that
+        h = x.double() + res.double()
+        assert torch.all((out.double() - h).abs() <= h.abs() * (HALF[out.dtype] + 2.0 ** -24) + 2.0 ** (-134 if rt == "bf16" else -150))
+
+
+@pytest.mark.parametrize("d", [256, 512, 4096, 16384])
+def test_norm_of_infinite_rows_and_infinite_eps(d):
+    """What is not finite stays so: 1 / inf gives zeros beside an infinity, and 0 * inf a NaN in its group."""
+    x = rand(d, 5, d)
+    x[1] *= 1e30
+    x[1, 17] = float("inf")
+    x[2, 3] = float("nan")
+    x[3] = 0
+    codes, scales, _ = cb.cb_add_rmsnorm_quantize(x)
+    v = ref.values(codes, scales, 1)
+    assert torch.isnan(v[1, :128]).all() and torch.equal(v[1, 128:], torch.zeros_like(v[1, 128:]))
+    assert torch.isnan(v[2]).all() and torch.equal(v[3], torch.zeros_like(v[3]))
+    check_norm(x[4:], None, None, 1e-5, codes[4:], scales[:, 4:], None)
+    codes, scales, _ = cb.cb_add_rmsnorm_quantize(x[4:] * 1e25, eps=float("inf"))
+    assert torch.equal(codes.float(), torch.zeros(1, d, device="cuda"))
