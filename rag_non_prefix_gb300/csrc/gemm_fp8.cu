@@ -263,8 +263,12 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // SiLU with the hardware's exponential and quotient (2 + 1.2 |x| and 2 units in the last place): the
-// IEEE quotient made a tile's epilogue ~1 us longer.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+// IEEE quotient made a tile's epilogue ~1 us longer.  The exponential is that of -|x|, so that the
+// quotient's divisor is at most 2 (beyond 2^126 its result is 0, and exp(-x) is infinite below -88).
+__device__ __forceinline__ float silu(float x) {
+  const float e = __expf(-fabsf(x));
+  return __fdividef(x >= 0.0f ? x : x * e, 1.0f + e);
+}
 
 struct Bars {
   // even CTAs: the codes of a stage have landed, both CTAs' factors are written and the eight warps

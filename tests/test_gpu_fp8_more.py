@@ -135,3 +135,31 @@ def test_norm_of_infinite_rows_and_infinite_eps(d):
     check_norm(x[4:], None, None, 1e-5, codes[4:], scales[:, 4:], None)
     codes, scales, _ = cb.cb_add_rmsnorm_quantize(x[4:] * 1e25, eps=float("inf"))
     assert torch.equal(codes.float(), torch.zeros(1, d, device="cuda"))
+
+
+@pytest.mark.parametrize("plan", [(16, 1), (64, 2), (128, 1), (256, 1)])
+def test_swiglu_of_gates_whose_exponential_overflows(set_plan, plan):
+    """Gates of -87 to -103: exp(-gate) is beyond 2^126 or infinite in fp32, SiLU around -1e-36 to -1e-43
+    is not zero, and up features of 1e36 and more make numbers of ordinary size of it."""
+    m, width, k = 130, 272, 128
+    o, _, _ = operands(m, width, k, SWIGLU)
+    one = torch.zeros(1, k, device="cuda")
+    one[0, 0] = 1.0
+    o["a"].copy_(one.expand(m, k))
+    o["sa"][0] = torch.linspace(0.5, 1.0, m, device="cuda")
+    o["b"].copy_(-one.expand(width, k))
+    o["sb"][:, 0] = torch.tensor([87.8, 100.0, 103.0], device="cuda")
+    o["b2"].copy_(one.expand(width, k) * torch.linspace(-2, 2, width, device="cuda")[:, None])
+    o["sb2"][:, 0] = 1e38
+    set_plan(*plan)
+    gemm(o, SWIGLU)
+    gate, up = ref.product(o["a"], o["sa"], o["b"], o["sb"])[0], ref.product(o["a"], o["sa"], o["b2"], o["sb2"])[0]
+    y = ref.silu64(gate) * up
+    # one product of a group each, which the scales' product and its multiplication round (2 * 2^-24): a
+    # gate off by 2^-23 |gate| moves SiLU by (1 + |gate|) 2^-23; the exponential is off by 2 + 1.2 |gate|
+    # units of 2^-23 or, among the subnormal numbers, by their step 2^-149; its sum with one, the quotient, up
+    # and two products round within 5 units, product and quotient among subnormal numbers by a step each
+    rel = (8 + 2.2 * gate.abs()) * 2.0 ** -23
+    err = y.abs() * rel + (gate.abs() * 2.0 ** -149 + 2.0 ** -148) * up.abs()
+    ref.check_quantised(o["c"], o["c_scales"], y, 1, err=err)
+    assert float(y.abs().max()) > 0.1
