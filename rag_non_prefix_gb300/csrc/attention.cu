@@ -1116,32 +1116,16 @@ int attention_tile_rows(int n_heads, int n_kv_heads, cb_dtype dt) {
   return G >= ta::ROWS ? 1 : ta::ROWS / G;
 }
 
-typedef CUresult (*EncodeTiledFn4)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // 4-D map over a KV cache [L][N][Hkv][128] (bf16): box {64, 1, 128 keys, 1}, 128-byte swizzle.
 bool encode_kv_map(CUtensorMap* map, const void* base, int n_layers, int n_tokens, int n_kv_heads,
                    long long layer_stride_elems) {
-  static EncodeTiledFn4 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<EncodeTiledFn4>(p);
-  }
   const uint64_t row = static_cast<uint64_t>(n_kv_heads) * ta::DH * 2;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(ta::DH), static_cast<cuuint64_t>(n_kv_heads),
-                        static_cast<cuuint64_t>(n_tokens), static_cast<cuuint64_t>(layer_stride_elems ? n_layers : 1)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(ta::DH * 2), row,
-                           layer_stride_elems ? static_cast<cuuint64_t>(layer_stride_elems) * 2 : row * n_tokens};
-  cuuint32_t box[4] = {64, 1, ta::BKV, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const uint64_t dims[4] = {static_cast<uint64_t>(ta::DH), static_cast<uint64_t>(n_kv_heads),
+                            static_cast<uint64_t>(n_tokens), static_cast<uint64_t>(layer_stride_elems ? n_layers : 1)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(ta::DH * 2), row,
+                               layer_stride_elems ? static_cast<uint64_t>(layer_stride_elems) * 2 : row * n_tokens};
+  const uint32_t box[4] = {64, 1, ta::BKV, 1};
+  return encode_tmap_nd(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tiles per CTA of the bf16 attention, process-wide: 0 chosen per launch (two when the

@@ -682,27 +682,12 @@ bool plan_gemm_pair(int M, int N, int K, int split0, int split1, int mode, int f
 // 4-D map over a [heads x 128][K] bf16 weight whose box of 64 rows is rows (i, i + 64) of one
 // head for 32 consecutive i: dims {K, 2, 64, heads}, strides 64 rows, 1 row, 128 rows.
 static bool encode_rope_rows(CUtensorMap* map, const void* w, int K, int heads) {
-  typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static EncodeFn fn = nullptr;
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<EncodeFn>(f);
-  }
   if (heads <= 0 || (reinterpret_cast<uintptr_t>(w) & 15u) != 0) return false;
-  const cuuint64_t row = static_cast<cuuint64_t>(K) * 2;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(K), 2, 64, static_cast<cuuint64_t>(heads)};
-  cuuint64_t strides[3] = {64 * row, row, 128 * row};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(pr::BK), 2, 32, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(w), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const uint64_t row = static_cast<uint64_t>(K) * 2;
+  const uint64_t dims[4] = {static_cast<uint64_t>(K), 2, 64, static_cast<uint64_t>(heads)};
+  const uint64_t strides[3] = {64 * row, row, 128 * row};
+  const uint32_t box[4] = {static_cast<uint32_t>(pr::BK), 2, 32, 1};
+  return encode_tmap_nd(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int CL, bool ROPE>

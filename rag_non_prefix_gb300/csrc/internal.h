@@ -264,11 +264,13 @@ void gemm_set_pairing(int m);  // 0 model, 1 never, 2 clusters of one pair, 4 of
 // launch_gemm's schedule for a bf16 GEMM (single-tensor B) as text; snprintf's return value
 int gemm_describe(int M, int N, int K, int mode, size_t scratch_bytes, char* buf, size_t len);
 int gemm_pairing();
-// tensor-map encoder (driver entry point, resolved once)
+// Tensor-map encoders (driver entry point, resolved once), in any thread: a map of `rank` (at most 5)
+// dimensions, innermost first, strides in bytes from the second one on; and a row-major
+// [rows][inner] one with a row pitch of `pitch` bytes.
+bool encode_tmap_nd(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* base, const uint64_t* dims,
+                    const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz);
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
                  uint64_t pitch, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
-bool encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
-                         uint32_t box_rows);
 
 
 // e4m3 codes with fp32 scales (cb_quantize): the largest code value, and the smallest
