@@ -410,6 +410,14 @@ cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_
  * fp32 rounding of the same sums.  Other values: CB_ERR_INVALID_ARG. */
 cb_status cb_gemm_scaled_set_plan(int tokens, int split);
 
+/* The plan that a cb_gemm_scaled of M x N x K with `epilogue` would run by under the current hook, as a
+ * NUL-terminated line of text in buf (at most len bytes): "handful" for the kernel of up to 16 tokens,
+ * else each product that is launched (one, or two where the tiles of a short last round are a product
+ * of their own) as "tokens=.. features=.. token_tile=.. split=.. clusters=.. stages=.. model_us=..", a second
+ * one after "; ".  "empty" for M 0; "none" where no GPU can be asked.  Sizes as for the product:
+ * CB_ERR_SHAPE; a null buffer or unknown epilogue: CB_ERR_INVALID_ARG. */
+cb_status cb_gemm_scaled_describe(int M, int N, int K, int epilogue, char* buf, size_t len);
+
 /* Causal attention of sparse queries over one KV cache ([P3] "어떤 토큰을 다시 계산하는가":
  * selected queries attend under the causal mask to all available K/V).
  * q [m][n_heads][head_dim] dtype; q_pos int32 [m] (positions, < n_kv);

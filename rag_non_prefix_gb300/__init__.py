@@ -32,7 +32,7 @@ EXPORTED = ("cb_create", "cb_destroy", "cb_status_string", "cb_last_error", "cb_
             "cb_set_launch_overlap", "cb_codec_layer_bytes", "cb_kv_encode", "cb_kv_decode", "cb_register_chunk_codec",
             "cb_set_staging", "cb_chunk_hash", "cb_chunk_info_of", "cb_plan_loading", "cb_decode_step",
             "cb_ratio_schedule", "cb_k_for_ratio", "cb_quantize", "cb_add_rmsnorm_quantize", "cb_gemm_scaled",
-            "cb_gemm_scaled_set_plan")
+            "cb_gemm_scaled_set_plan", "cb_gemm_scaled_describe")
 PHASES = ("begin", "staged_rot", "norm", "qkv", "rope", "deviation", "select", "scatter", "attention", "oproj",
           "gateup", "down", "finish")
 
@@ -147,6 +147,7 @@ def load_library(path: str = LIB_PATH):
         "cb_gemm_scaled": (st, [vp, vp, vp, vp, vp, C.c_longlong, vp,
                                 C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, vp]),
         "cb_gemm_scaled_set_plan": (st, [C.c_int, C.c_int]),
+        "cb_gemm_scaled_describe": (st, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_char_p, C.c_size_t]),
         "cb_codec_layer_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
         "cb_kv_encode": (st, [vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp]),
         "cb_kv_decode": (st, [vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_double, C.c_int, vp, vp,
@@ -533,6 +534,14 @@ def cb_gemm_scaled_set_plan(tokens: int, split: int) -> None:
     """Process-wide tiling of cb_gemm_scaled: tokens per tile (16, 32, 48, 64, 80, 96, 128, 256) and
     pairs that divide the channels (1 to 4); 0, 0 by the library's time model (tuning and tests)."""
     _check(load_library().cb_gemm_scaled_set_plan(int(tokens), int(split)))
+
+
+def cb_gemm_scaled_describe(M: int, N: int, K: int, epilogue: int = CB_FP8_STORE_F32) -> str:
+    """The plan that a cb_gemm_scaled of this shape would run by under the current hook (N counts the
+    gate and up rows of CB_FP8_SWIGLU_FP8)."""
+    buf = C.create_string_buffer(256)
+    _check(load_library().cb_gemm_scaled_describe(int(M), int(N), int(K), int(epilogue), buf, 256))
+    return buf.value.decode()
 
 
 def cb_chunk_hash(ids) -> int:

@@ -1392,15 +1392,20 @@ cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_add_rmsnorm_quantize");
 }
 
+static cb_status gemm_scaled_sizes(int M, int N, int K, int epilogue) {
+  if (epilogue < 0 || epilogue > CB_FP8_STORE_BF16) return fail(nullptr, CB_ERR_INVALID_ARG, "bad epilogue");
+  if (M < 0 || N < 1 || K < 1 || K % 16) return fail(nullptr, CB_ERR_SHAPE, "K must be a positive multiple of 16");
+  if (M > kFp8Rows || N > kFp8Rows || K > kFp8Cols) return fail(nullptr, CB_ERR_SHAPE, kFp8Sizes);
+  if (epilogue == CB_FP8_SWIGLU_FP8 && N % 32) return fail(nullptr, CB_ERR_SHAPE, "N / 2 must be a multiple of 16");
+  return CB_OK;
+}
+
 cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_mat* B2, const float* addend, void* C,
                       long long ldc, float* c_scales, long long ld_cs, int M, int N, int K, int epilogue,
                       void* stream) {
-  if (epilogue < 0 || epilogue > CB_FP8_STORE_BF16) return fail(nullptr, CB_ERR_INVALID_ARG, "bad epilogue");
   const bool swiglu = epilogue == CB_FP8_SWIGLU_FP8;
-  if (M < 0 || N < 1 || K < 1 || K % 16) return fail(nullptr, CB_ERR_SHAPE, "K must be a positive multiple of 16");
-  if (M > kFp8Rows || N > kFp8Rows || K > kFp8Cols) return fail(nullptr, CB_ERR_SHAPE, kFp8Sizes);
-  if (swiglu && N % 32) return fail(nullptr, CB_ERR_SHAPE, "N / 2 must be a multiple of 16");
-  if (M == 0) return CB_OK;
+  const cb_status sizes = gemm_scaled_sizes(M, N, K, epilogue);
+  if (sizes != CB_OK || M == 0) return sizes;
   if (!A || !B || !C || !A->codes || !A->scales || !B->codes || !B->scales ||
       (swiglu && (!B2 || !B2->codes || !B2->scales || !c_scales)) || (epilogue == CB_FP8_ADD_F32 && !addend))
     return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
@@ -1443,6 +1448,17 @@ cb_status cb_gemm_scaled(const cb_fp8_mat* A, const cb_fp8_mat* B, const cb_fp8_
 
 cb_status cb_gemm_scaled_set_plan(int tokens, int split) {
   if (!gemm_fp8_set_plan(tokens, split)) return fail(nullptr, CB_ERR_INVALID_ARG, "no such plan");
+  return CB_OK;
+}
+
+cb_status cb_gemm_scaled_describe(int M, int N, int K, int epilogue, char* buf, size_t len) {
+  if (!buf || len == 0) return fail(nullptr, CB_ERR_INVALID_ARG, "null buffer");
+  const cb_status sizes = gemm_scaled_sizes(M, N, K, epilogue);
+  if (sizes != CB_OK) return sizes;
+  if (M == 0)
+    snprintf(buf, len, "empty");
+  else
+    gemm_fp8_describe(M, N, K, epilogue, buf, len);
   return CB_OK;
 }
 

@@ -31,6 +31,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdio>
 
 #include "common.cuh"
 #include "internal.h"
@@ -1399,6 +1400,27 @@ bool gemm_fp8_set_plan(int tokens, int split) {
   if (!kernel_of(tokens, CB_FP8_STORE_F32) || split < 1 || split > 4 || (tokens == 256 && split != 1)) return false;
   g_plan.store(tokens * 8 + split);
   return true;
+}
+
+void gemm_fp8_describe(int M, int N, int K, int epilogue, char* buf, size_t len) {
+  Fp8Gemm g{};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.epilogue = epilogue;
+  const Schedule sched = schedule(g, g_plan.load());
+  if (sched.handful || sched.pl[0].bt == 0) {
+    snprintf(buf, len, sched.handful ? "handful" : "none");
+    return;
+  }
+  size_t used = 0;
+  for (int i = 0; i < sched.n && used < len; ++i) {
+    const Fp8Gemm& p = sched.g[i];
+    const Plan& pl = sched.pl[i];
+    used += snprintf(buf + used, len - used, "%stokens=%d features=%d token_tile=%d split=%d clusters=%d stages=%d model_us=%.1f",
+                     i ? "; " : "", p.M, epilogue == CB_FP8_SWIGLU_FP8 ? p.N / 2 : p.N, pl.bt, pl.split, pl.clusters,
+                     pl.stages, pl.us);
+  }
 }
 
 // One product ready to be launched.

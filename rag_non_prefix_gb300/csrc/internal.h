@@ -296,5 +296,6 @@ struct Fp8Gemm {
 };
 cudaError_t launch_gemm_fp8(const Fp8Gemm& p, cudaStream_t s);
 bool gemm_fp8_set_plan(int tokens, int split);  // false for a plan that has no kernel
+void gemm_fp8_describe(int M, int N, int K, int epilogue, char* buf, size_t len);
 
 }  // namespace cb

@@ -9,7 +9,7 @@ import torch
 import rag_non_prefix_gb300 as cb
 from tests import fp8_ref as ref
 from tests._gpu import built
-from tests.test_gpu_fp8 import ADD, DT, F32, HALF, SWIGLU, check_gemm, check_norm, gemm, operands, rand
+from tests.test_gpu_fp8 import ADD, BF16, DT, F32, HALF, SWIGLU, check_gemm, check_norm, gemm, operands, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +163,33 @@ def test_swiglu_of_gates_whose_exponential_overflows(set_plan, plan):
     err = y.abs() * rel + (gate.abs() * 2.0 ** -149 + 2.0 ** -148) * up.abs()
     ref.check_quantised(o["c"], o["c_scales"], y, 1, err=err)
     assert float(y.abs().max()) > 0.1
+
+
+# ---------------------------------------------------------------------------------- plans
+def described(m, width, k, epi):
+    text = cb.cb_gemm_scaled_describe(m, 2 * width if epi == SWIGLU else width, k, epi)
+    return [dict(f.split("=") for f in part.split()) for part in text.split("; ")]
+
+
+@pytest.mark.parametrize("epi,m,width,k", [
+    (F32, 531, 7190, 4112), (ADD, 531, 7190, 4112), (BF16, 531, 7190, 4112), (SWIGLU, 531, 4128, 4112),
+    (F32, 1101, 8219, 8208), (ADD, 1101, 8219, 8208), (BF16, 1101, 8219, 8208), (SWIGLU, 1101, 4112, 8208)])
+def test_the_products_in_two_parts_are_launched_in_two(epi, m, width, k):
+    """These shapes (whose results other tests check) do split, 531 tokens by tokens, 1101 by features."""
+    parts = described(m, width, k, epi)
+    assert len(parts) == 2
+    tokens, features = ([int(p[n]) for p in parts] for n in ("tokens", "features"))
+    if m == 531:
+        assert sum(tokens) == m and tokens[0] % 256 == 0 and features == [width, width]
+    else:
+        assert sum(features) == width and features[0] % 128 == 0 and tokens == [m, m]
+    assert parts[0]["token_tile"] == "256"
+
+
+def test_plans_as_described(set_plan):
+    assert cb.cb_gemm_scaled_describe(0, 128, 128) == "empty"
+    assert cb.cb_gemm_scaled_describe(3, 4096, 4096) == "handful"
+    assert "handful" not in cb.cb_gemm_scaled_describe(3, 8192, 4096, SWIGLU)
+    set_plan(48, 2)
+    (part,) = described(531, 7190, 4112, F32)
+    assert (part["tokens"], part["features"], part["token_tile"], part["split"]) == ("531", "7190", "48", "2")
