@@ -193,3 +193,83 @@ def test_plans_as_described(set_plan):
     set_plan(48, 2)
     (part,) = described(531, 7190, 4112, F32)
     assert (part["tokens"], part["features"], part["token_tile"], part["split"]) == ("531", "7190", "48", "2")
+
+
+# ---------------------------------------------------------------------------------- far offsets
+def far(rows, cols, dtype, pitch):
+    """[rows, cols] whose last rows lie more than 2^31 elements in."""
+    assert (rows - 1) * pitch > 2 ** 31
+    return torch.empty(rows, pitch, dtype=dtype, device="cuda")[:, :cols]
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("plan,m", [((64, 1), 66), ((16, 3), 66), ((256, 1), 66), ((1, 0), 16), ((1, 0), 7)])
+@pytest.mark.parametrize("epi", [F32, ADD, BF16, SWIGLU])
+def test_product_with_every_matrix_past_31_bits(set_plan, plan, m, epi):
+    if epi == SWIGLU and plan == (1, 0):
+        plan = (16, 1)  # (that kernel has no such form)
+    width, k = 2176, 2176  # 17 groups
+    o, _, _ = operands(m, width, k, epi, seed=3)
+    set_plan(*plan)
+    gemm(o, epi)
+    want, want_scales = o["c"].clone(), None if epi != SWIGLU else o["c_scales"].clone()
+    pitch = 1 << 25 if m == 66 else 1 << 28 if m == 16 else 1 << 29
+    moved = dict(o)
+    for name, p in (("b", 1 << 20), ("b2", 1 << 20), ("sa", 1 << 27), ("sb", 1 << 27), ("sb2", 1 << 27), ("c_scales", 1 << 27),
+                    ("a", pitch), ("c", pitch), ("addend", pitch)):
+        if o[name] is None:
+            continue
+        rows = o[name].shape[0]
+        moved[name] = far(*o[name].shape, o[name].dtype, max(p, -(-2 ** 31 // (rows - 1)) // 64 * 64 + 64))
+        moved[name].copy_(o[name])
+        if name not in ("a", "c", "addend"):  # (these three stay; the others are tried one by one)
+            gemm(moved, epi)
+            assert same(moved["c"], want)
+            if epi == SWIGLU:
+                assert same(moved["c_scales"], want_scales)
+            moved[name] = o[name]
+            torch.cuda.empty_cache()
+    moved["c"].fill_(7.0)
+    gemm(moved, epi)
+    assert same(moved["c"], want)
+    del moved
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f32", "bf16"), ("bf16", None)])
+@pytest.mark.parametrize("d", [256, 512, 1024, 2176])
+def test_norm_with_every_matrix_past_31_bits(d, xt, rt):
+    rows, pitch = 66, 1 << 25
+    x = rand(1, rows, d).to(DT[xt])
+    res = None if rt is None else rand(2, rows, d).to(DT[rt])
+    out = None if rt is None else torch.empty_like(res)
+    codes, scales, _ = cb.cb_add_rmsnorm_quantize(x, res, None, 1e-5, out)
+    fx, fcodes = far(rows, d, x.dtype, pitch), far(rows, d, codes.dtype, pitch)
+    fx.copy_(x)
+    fres, fout = (None, None) if rt is None else (far(rows, d, res.dtype, pitch), far(rows, d, res.dtype, pitch))
+    if res is not None:
+        fres.copy_(res)
+    groups = d // 128
+    fscales = far(groups, rows, torch.float32, -(-2 ** 31 // (groups - 1)) // 64 * 64 + 64)
+    cb.cb_add_rmsnorm_quantize(fx, fres, None, 1e-5, fout, fcodes, fscales)
+    assert same(fcodes, codes) and same(fscales, scales) and (out is None or same(fout, out))
+    del fx, fres, fout, fcodes, fscales
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_with_every_matrix_past_31_bits(dtype, block):
+    rows, cols, pitch = 66 if block == 1 else 2177, 2176, 1 << 25 if block == 1 else 1 << 20
+    x = rand(1, rows, cols).to(DT[dtype])
+    codes, scales = cb.cb_quantize(x, block)
+    fx, fcodes = far(rows, cols, x.dtype, pitch), far(rows, cols, codes.dtype, pitch)
+    fx.copy_(x)
+    fscales = far(*scales.shape, torch.float32, -(-2 ** 31 // (scales.shape[0] - 1)) // 64 * 64 + 64)
+    cb.cb_quantize(fx, block, fcodes, fscales)
+    assert same(fcodes, codes) and same(fscales, scales)
+    del fx, fcodes, fscales
+    torch.cuda.empty_cache()
