@@ -358,7 +358,8 @@ cb_status cb_gemm_get_status(void* stream, int timeout_ms);
  * Codes, fp32 and bf16 matrices are row-major with a pitch in elements; base addresses are
  * 16-byte aligned, pitches a multiple of 16 bytes, and channels (cols, d, K and the features of
  * a CB_FP8_SWIGLU_FP8 output) a multiple of 16.  Row scales: 16-byte aligned, ld_scales % 4 == 0.
- * No matrix has more than 2^30 rows or 2^22 channels (CB_ERR_SHAPE).
+ * No matrix has more than 2^30 rows or 2^22 channels (CB_ERR_SHAPE).  No output overlaps another
+ * argument, but where a call says so.
  * Entries between a row's end and its pitch are neither read nor written. */
 typedef struct {
   const void* codes;    /* e4m3 [rows][ld] */
@@ -385,7 +386,8 @@ cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype
                              void* codes, long long ld_codes, float* scales, long long ld_scales, void* stream);
 
 /* C = A . B^T of a row matrix A [M][K] and a block matrix B [N][K]: the products of a group are
- * summed in fp32, multiplied by the group's two scales and summed over the groups in fp32.
+ * summed in fp32, multiplied by the product of the group's two scales and summed over the groups in
+ * fp32 (that product is one fp32 number: below 2^-126 it loses digits, beyond 2^128 it is infinite).
  *   CB_FP8_STORE_F32   C fp32 [M][ldc] = acc
  *   CB_FP8_ADD_F32     C fp32 [M][ldc] = addend + acc; addend fp32 [M][ldc], may be C
  *   CB_FP8_SWIGLU_FP8  C e4m3 [M][ldc] and c_scales (a row matrix of N / 2 channels) = the

@@ -145,7 +145,7 @@ def main():
             more["addend"] = C
         cb.cb_gemm_scaled_set_plan(*a.plan)
         avg, best = _time(lambda: cb.cb_gemm_scaled(*A, *W[0], C, epi, **more), a.iters, a.warmup, flush, a.batch)
-        out.update(shape=[M, N, K], mode=a.mode, plan=a.plan, ms=avg, best_ms=best,
+        out.update(shape=[M, N, K], mode=a.mode, plan=cb.cb_gemm_scaled_describe(M, N, K, epi), ms=avg, best_ms=best,
                    tflops=2.0 * M * N * K / (avg * 1e-3) / 1e12, weight_bytes=N * K)
     elif a.kernel == "attention":
         H, Hkv, N, m = a.H, a.Hkv, a.N, a.m

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
 // ----------------------------------------------------------------------------- weight blocks
 // One CTA per 128 x 128 block, held in registers between the maximum and the codes (one read):
 // a half warp per row segment of 128 channels, 8 rows per thread, kept as they lie in memory.
-// Bound by HBM: 20480 x 7168 in bf16 66 us (6.7 TB/s), in fp32 105 us (7.0 TB/s).
+// Bound by HBM: 20480 x 7168 in bf16 63 us (7.0 TB/s), in fp32 102 us (7.2 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restrict__ x, long long ldx, int rows, int cols,
                                                               uint8_t* __restrict__ codes, long long ldc,
@@ -196,10 +196,11 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const T* __restric
 // A row is held in registers from its single read to its codes: thread t owns the 8-channel pieces
 // t, t + blockDim, ... (CH of them), so 16 consecutive lanes hold one group.  h = residual + x in
 // fp32; the norm and the codes come from the unrounded h, residual_out gets h rounded to its type.
-// Bound by HBM for large matrices with a residual (8320 x 8192 in bf16: 73 us, 6.5 TB/s; 8320 x 7168
-// with an fp32 residual 99 us, 6.6 TB/s), by instructions without (8000 x 8192: 41 us, 4.8 TB/s,
-// hence the packed pairs and shared maxima), by a row's latency for few rows (one row 2.1 us).  A
-// stream of bulk copies into shared memory ahead of the sums was no faster.
+// Bound by HBM for large matrices with a residual (8320 x 8192 in bf16: 70 .. 72 us, 6.7 TB/s; 8320 x 7168
+// with an fp32 residual 95 us, 6.9 TB/s), by instructions without (8000 x 8192: 38 us, 5.2 TB/s,
+// hence the packed pairs and shared maxima), by a row's latency for few rows (one row 2.0 us).  A
+// stream of bulk copies into shared memory ahead of the sums was no faster.  The test of the mean's
+// range costs 1 to 2 percent, 4 to 7 where a row is a warp's (8320 x 512 4.5 -> 4.8 us).
 
 // Sum over the block.
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -356,7 +357,7 @@ cudaError_t launch_norm(const void* x, long long ldx, const void* res, void* res
   // Pieces per thread.  One while the GPU holds all pieces at once (152 SMs x 2048 threads), the
   // shortest way through a row: 1 x 4096 2.1 us (four 3.2), 535 x 4096 with a residual 6.0 (two 6.3).
   // Then two with a residual up to 8192 channels (8320 x 4096 39.7 us, one 45.4; 8320 x 8192 73, one
-  // 94, four 74; 1357 x 7168 with an fp32 residual 18.9, one 19.6, four 19.3) and four for longer rows
+  // 94, four 74; 1357 x 7168 with an fp32 residual 18.7, one 19.6, four 19.3) and four for longer rows
   // (8320 x 16384 140, two 184) and without a residual (8320 x 4096 22.7, one 33; 8000 x 8192 41, two 51).
   const bool one_piece = pieces <= 1024 && static_cast<long long>(rows) * pieces <= 152 * 2048;
   if (!res) return one_piece ? one(add_rmsnorm_fp8_kernel<TX, TX, false, 1, false>, 1) : one(add_rmsnorm_fp8_kernel<TX, TX, false, 4, false>, 4);

@@ -1,6 +1,7 @@
 // Product of two e4m3 matrices with a scale per group of 128 channels of a row of A (tokens) and
 // per 128 x 128 block of B (weights):
-//   acc[m][n] = sum over groups g of  sa[g][m] * sb[n / 128][g] * sum_{k in g} A[m][k] B[n][k]
+//   acc[m][n] = sum over groups g of  (sa[g][m] * sb[n / 128][g]) * sum_{k in g} A[m][k] B[n][k]
+// The product of the two scales is one fp32 number, made once per token, weight block and group.
 //
 // The tensor core sums the products of one group (four tcgen05.mma kind::f8f6f4 of 32 channels)
 // into tensor memory; eight warps then read that sum, multiply it by the group's two scales and
@@ -1247,8 +1248,9 @@ struct Plan {
   double us;  // expected time
 };
 
-// Time model (microseconds, fitted to 3000 runs on GB300 at ~1.9 GHz over 1 .. 1000 tokens of the decoder
-// shapes, where its choice is 0.7 percent slower than the best plan on average): a group takes 0.39 us with
+// Time model (microseconds, fitted to 3000 runs on GB300 at ~1.9 GHz over 1 .. 1000 tokens of nine decoder
+// shapes; over 145 of them measured again, each under every tiling, its choice (two products among them)
+// is as fast as the best tiling on average and 11 percent slower at worst): a group takes 0.39 us with
 // 256 tokens on the rows and 0.18 + 0.0017 bt us with the weights on them, a unit's output 1.9 us and
 // 1.7 + 0.017 bt us; units go round the resident clusters (76 of one pair, 36 of two, 23 of three, 15
 // of four); the weights come at 6.5 TB/s at the most.
@@ -1298,11 +1300,12 @@ Plan plan(const Fp8Gemm& g, const Resident& resident, int hook) {
 // 14336 15.3 / 14.9; and where its many CTAs have little to do each (43776 x 512 9.5 / 8.5, 100000 x
 // 1024 26 / 25).  Up to 16 for one wave of its CTAs (two an SM) and short sums: 16 tokens 6.9 / 7.9 at 4096
 // x 4096, but 10.7 / 9.1 at 6144 x 4096 and 11.0 / 10.8 at 4096 x 8192.
+constexpr int GB300_SMS = 152;
 bool handful_applies(const Fp8Gemm& g, int hook) {
   if (g.M > 16 || g.epilogue == CB_FP8_SWIGLU_FP8) return false;
   if (hook) return hook == HANDFUL_PLAN;
-  if (g.M > 8) return g.K <= 4096 && g.N <= 16 * 152 * 2;
-  return g.K <= 8192 && (g.K >= 2048 || g.N <= 4 * 16 * 152 * 3);
+  if (g.M > 8) return g.K <= 4096 && g.N <= 16 * GB300_SMS * 2;
+  return g.K <= 8192 && (g.K >= 2048 || g.N <= 4 * 16 * GB300_SMS * 3);
 }
 
 // The product of the first `n` tokens, or of the first `n` output features, and the rest of it.
