@@ -241,8 +241,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 // Arrival of one lane (el) on a barrier of the cluster that orders no memory access.  It announces
-// that tensor memory was read (tcgen05.wait::ld and the tcgen05 fence order that), or follows a fence
-// of its own.  With release at cluster scope the same arrival took ~1200 cycles.
+// that tensor memory was read (tcgen05.wait::ld and the tcgen05 fence order that) or that parts were
+// read and their values used, or follows a fence of its own.  With release at cluster scope the same
+// arrival took ~1200 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr, uint32_t el) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
