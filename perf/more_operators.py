@@ -248,7 +248,7 @@ def prepare(case, seed):
         if own:
             import rag_non_prefix_gb300 as cb
 
-            s["scratch"] = cb.kv4_scratch()
+            s["scratch"] = cb.kvq_scratch()
         return s
     s["table"], pages = _pages(gen, n, [case["ctx"]] * n, case["page"])
     s["seq"] = torch.arange(n, device="cuda").repeat_interleave(case["t"]).to(torch.int32)
@@ -328,10 +328,10 @@ def run(s):
         if kind == "sample":
             return cb.cb_sample(s["logits"], s["uniform"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"], out=s["out"])
         if kind == "attention":
-            return cb.cb_kv4_attention(s["q"], s["q_pos"], s["pool"], s["table"], out=s["out"], scratch=s.get("scratch"))
+            return cb.cb_kvq_attention(s["q"], s["q_pos"], s["pool"], s["table"], out=s["out"], scratch=s.get("scratch"))
         if kind == "write":
-            cb.cb_kv4_write(s["pool"], s["table"], s["k"], s["v"], s["pos"], s["seq"])
-        return cb.cb_kv4_read(s["pool"], s["table"], s["pos"], s["seq"], delta_pos=s["delta"], theta=THETA, k_out=s["k_out"], v_out=s["v_out"])
+            cb.cb_kvq_write(s["pool"], s["table"], s["k"], s["v"], s["pos"], s["seq"])
+        return cb.cb_kvq_read(s["pool"], s["table"], s["pos"], s["seq"], delta_pos=s["delta"], theta=THETA, k_out=s["k_out"], v_out=s["v_out"])
 
     if kind == "sample":
         return _sample(s)
