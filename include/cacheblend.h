@@ -428,6 +428,67 @@ cb_status cb_gemm_scaled_describe(int M, int N, int K, int epilogue, char* buf, 
 cb_status cb_attention(const void* q, const int32_t* q_pos, int m, const void* k, const void* v, int n_kv,
                        int n_heads, int n_kv_heads, int head_dim, void* out, cb_dtype dtype, void* stream);
 
+/* --------------------------------------------------------------------- KV cache in 4 bits
+ * ([P2] KV量子化とメモリ管理 quantises whole chunks, cb_kv_encode; this form is written token by token and
+ * attended to as it is.)  A group is 32 consecutive channels of one token's key or value of one head, 20 bytes:
+ * 16 of codes, a bf16 scale and a bf16 zero.  With lo, hi the group's smallest and largest number,
+ * d = hi - lo (one IEEE float32 subtraction) and a = max(|lo|, |hi|):
+ *   scale = the smallest bf16 number >= max(d / 14.75, a / 64, 2^-120)
+ *   zero  = floor(4 lo / scale) / 4
+ *   code  = clamp(nearest(x / scale - zero), 0, 15), ties to even      (each of the three exactly)
+ *   value = scale * (code + zero)                                      (exact in float32)
+ * so a value is within scale / 2 of x (and within 2^-7 of it where all of a group is alike).  A group with an infinity or a NaN,
+ * or whose d passes float32's range, decodes to NaN throughout.
+ *
+ * A pool is [n_pages][n_kv_heads][page_tokens / 16] blocks of 20 * head_dim bytes (head_dim 64 or 128;
+ * page_tokens a positive multiple of 16), one block for 16 consecutive positions of one KV head of one layer.
+ * With D = head_dim and NG = D / 32 a block holds, for its token r (0..15):
+ *   key codes    byte r*D/2 + (NG*c + g)*4 + i/2: channel 32g + 8c + i, i < 8, even i in the low nibble
+ *   value codes  byte 8D + 512*(j/4) + 64n + 16*((r%8)/2) + 4*(j%4) + 2*(r%2) + r/8: channels 16j + n, n < 8, (low
+ *                nibble) and 16j + n + 8
+ *   key scales   byte 16D + 4*NG*r: NG bf16 scales, then NG bf16 zeros
+ *   value scales 64*NG bytes further, the same
+ * Position p of sequence s lies in page table[s * ld_table + p / page_tokens], at p % page_tokens; a sequence has
+ * max_pages entries.  Pages of one sequence stand in any order; sequences may share pages that no call writes.
+ * Device-side problems (a sequence >= n_seqs, a position beyond max_pages pages, a page outside 0..n_pages - 1: the
+ * row is not written, reads as zeros, or its keys are left out) go to the standalone status word that
+ * cb_gemm_get_status() reads.  Sizes: n_kv_heads <= 1024, n_seqs <= 2^20, page_tokens * max_pages < 2^31. */
+typedef struct {
+  void* pool;            /* device, 16-byte aligned */
+  int n_pages, page_tokens, n_kv_heads, head_dim;
+  const int32_t* table;  /* device int32 [n_seqs][ld_table] */
+  long long ld_table;    /* >= max_pages */
+  int max_pages, n_seqs;
+} cb_kvq_cache;
+/* Bytes of one page (0 for bad sizes). */
+size_t cb_kvq_page_bytes(int page_tokens, int n_kv_heads, int head_dim);
+
+/* Quantises k, v [rows][n_kv_heads][head_dim] of dtype (pitches ldk, ldv in elements; 16-byte aligned rows) into
+ * the cache: row i goes to position pos[i] of sequence seq[i] (device int32 [rows]; seq NULL: sequence i).
+ * A row with a negative position or sequence is left out.  No two rows of a call name the same position. */
+cb_status cb_kvq_write(const cb_kvq_cache* cache, const void* k, long long ldk, const void* v, long long ldv,
+                       cb_dtype dtype, const int32_t* seq, const int32_t* pos, int rows, void* stream);
+/* Reads rows back: k_out, v_out [rows][n_kv_heads][head_dim] of dtype (pitches as above), the keys turned on by
+ * delta_pos positions (the rotation of cb_rope_rerotate, in fp32; 0: as they are; negative: back).  A row with a
+ * negative position or sequence reads as zeros. */
+cb_status cb_kvq_read(const cb_kvq_cache* cache, const int32_t* seq, const int32_t* pos, int rows, int delta_pos,
+                      double theta, cb_dtype dtype, void* k_out, long long ldk, void* v_out, long long ldv,
+                      void* stream);
+/* Causal attention of new queries over the cache: n_tok tokens of each of the n_seqs sequences.
+ *   q, out  [n_seqs * n_tok][n_heads][head_dim] of dtype (pitches ldq, ldo in elements; 16-byte aligned rows)
+ *   q_pos   int32 [n_seqs * n_tok]: a token attends to positions 0..q_pos of its sequence (its own key written
+ *           before, cb_kvq_write); a negative one (padding) to nothing, its output is zero
+ * Head h reads KV head h / (n_heads / n_kv_heads).  What the cache holds beyond a token's position (NaN too) does not
+ * reach its output.  Scores and sums are fp32; the cache's values enter exactly, weights are rounded to bf16 for
+ * bf16 outputs and not rounded for fp32 ones.  Made for few tokens (decoding, checking drafts): for a long prompt read the rows
+ * back (cb_kvq_read) and use cb_attention.
+ * scratch: cb_kvq_scratch_size() bytes of device memory, 16-byte aligned, zero-filled before its first use and left
+ * ready by each call; calls that share one must not overlap on the GPU.  Results repeat exactly. */
+cb_status cb_kvq_attention(const cb_kvq_cache* cache, const void* q, long long ldq, const int32_t* q_pos, int n_tok,
+                           int n_heads, float scale, cb_dtype dtype, void* out, long long ldo, void* scratch,
+                           size_t scratch_bytes, void* stream);
+size_t cb_kvq_scratch_size(void);
+
 /* --------------------------------------------------------------------- blended prefill */
 
 /* Per-layer ratio of ALL cached tokens of a request to keep recomputed

@@ -32,7 +32,8 @@ EXPORTED = ("cb_create", "cb_destroy", "cb_status_string", "cb_last_error", "cb_
             "cb_set_launch_overlap", "cb_codec_layer_bytes", "cb_kv_encode", "cb_kv_decode", "cb_register_chunk_codec",
             "cb_set_staging", "cb_chunk_hash", "cb_chunk_info_of", "cb_plan_loading", "cb_decode_step",
             "cb_ratio_schedule", "cb_k_for_ratio", "cb_quantize", "cb_add_rmsnorm_quantize", "cb_gemm_scaled",
-            "cb_gemm_scaled_set_plan", "cb_gemm_scaled_describe")
+            "cb_gemm_scaled_set_plan", "cb_gemm_scaled_describe", "cb_kvq_page_bytes", "cb_kvq_write", "cb_kvq_read",
+            "cb_kvq_attention", "cb_kvq_scratch_size")
 PHASES = ("begin", "staged_rot", "norm", "qkv", "rope", "deviation", "select", "scatter", "attention", "oproj",
           "gateup", "down", "finish")
 
@@ -88,6 +89,12 @@ class CostModel(C.Structure):
 
 class Fp8Mat(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("ld", C.c_longlong), ("scales", C.c_void_p), ("ld_scales", C.c_longlong)]
+
+
+class KvqCache(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("n_pages", C.c_int), ("page_tokens", C.c_int), ("n_kv_heads", C.c_int),
+                ("head_dim", C.c_int), ("table", C.c_void_p), ("ld_table", C.c_longlong), ("max_pages", C.c_int),
+                ("n_seqs", C.c_int)]
 
 
 CB_FP8_STORE_F32, CB_FP8_ADD_F32, CB_FP8_SWIGLU_FP8, CB_FP8_STORE_BF16 = 0, 1, 2, 3
@@ -148,6 +155,14 @@ def load_library(path: str = LIB_PATH):
                                 C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, vp]),
         "cb_gemm_scaled_set_plan": (st, [C.c_int, C.c_int]),
         "cb_gemm_scaled_describe": (st, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_char_p, C.c_size_t]),
+        # (the cache: byref(KvqCache), or its bytes)
+        "cb_kvq_page_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
+        "cb_kvq_write": (st, [vp, vp, C.c_longlong, vp, C.c_longlong, C.c_int, i32p, i32p, C.c_int, vp]),
+        "cb_kvq_read": (st, [vp, i32p, i32p, C.c_int, C.c_int, C.c_double, C.c_int, vp, C.c_longlong, vp, C.c_longlong,
+                             vp]),
+        "cb_kvq_attention": (st, [vp, vp, C.c_longlong, i32p, C.c_int, C.c_int, C.c_float, C.c_int, vp, C.c_longlong, vp,
+                                  C.c_size_t, vp]),
+        "cb_kvq_scratch_size": (C.c_size_t, []),
         "cb_codec_layer_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
         "cb_kv_encode": (st, [vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp]),
         "cb_kv_decode": (st, [vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_double, C.c_int, vp, vp,
@@ -542,6 +557,132 @@ def cb_gemm_scaled_describe(M: int, N: int, K: int, epilogue: int = CB_FP8_STORE
     buf = C.create_string_buffer(256)
     _check(load_library().cb_gemm_scaled_describe(int(M), int(N), int(K), int(epilogue), buf, 256))
     return buf.value.decode()
+
+
+# ----------------------------------------------------------------------------- KV cache in 4 bits
+def kvq_pool(n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """Zeroed pages of a 4-bit cache of one layer: uint8 [n_pages, n_kv_heads, page_tokens // 16, 20 * head_dim]."""
+    if page_tokens < 16 or page_tokens % 16 or head_dim not in (64, 128):
+        raise CacheBlendError(2, "page_tokens must be a multiple of 16 and head_dim 64 or 128")
+    return torch.zeros(n_pages, n_kv_heads, page_tokens // 16, 20 * head_dim, dtype=torch.uint8, device=device)
+
+
+def kvq_scratch(device="cuda") -> torch.Tensor:
+    """Zeroed scratch of cb_kvq_attention: calls that may overlap on the GPU (streams, graphs) need one each."""
+    return torch.zeros(load_library().cb_kvq_scratch_size(), dtype=torch.uint8, device=device)
+
+
+# a KvqCache as bytes
+_pack_kvq = struct.Struct("@P4iPq2i").pack
+
+
+def _kvq_cache(pool: torch.Tensor, table: torch.Tensor):
+    """(the cache as bytes, sequences, heads, channels, device)"""
+    shape, ts = pool.shape, table.shape
+    if pool.dtype is not torch.uint8 or table.dtype is not torch.int32:
+        raise CacheBlendError(3, "a pool must be uint8 and a page table int32")
+    if len(shape) != 4 or shape[3] not in (1280, 2560) or len(ts) != 2 or not pool.is_contiguous():
+        raise CacheBlendError(2, "a pool is contiguous [pages, heads, page_tokens // 16, 20 * head_dim], a page table "
+                                 "[sequences, pages]")
+    dev = pool.get_device()
+    if dev < 0 or dev != _get_device() or table.get_device() != dev or (ts[1] > 1 and table.stride(1) != 1):
+        raise CacheBlendError(1, "the pool and its page table must be on the current CUDA device")
+    if max(shape[0], ts[0], ts[1]) > 0x7FFFFFFF or shape[2] >= 1 << 27:
+        raise CacheBlendError(2, "bad sizes of a 4-bit cache")
+    n, heads, blocks, size = shape
+    ld = table.stride(0) if ts[0] > 1 else ts[1]
+    return (_pack_kvq(pool.data_ptr(), n, 16 * blocks, heads, size // 20, table.data_ptr(), ld, ts[1], ts[0]), ts[0],
+            heads, size // 20, dev)
+
+
+def _kvq_rows(t: torch.Tensor, dtype, lead, heads: int, dh: int, what: str, dev: int) -> int:
+    """Pitch in elements of rows [*lead, heads, dh] of ``dtype``, after checking them."""
+    if t.dtype is not dtype:
+        raise CacheBlendError(3, f"{what} must be {dtype}, not {t.dtype}")
+    if t.shape != (*lead, heads, dh):
+        raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}, needs {(*lead, heads, dh)}")
+    if t.get_device() != dev:
+        raise CacheBlendError(1, f"{what} must be on the pool's device")
+    st = t.stride()
+    if st[-1] != 1 or (heads > 1 and st[-2] != dh):
+        raise CacheBlendError(1, f"{what} must have contiguous rows of heads x head_dim")
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
+        raise CacheBlendError(1, f"{what} must have one pitch over sequences and tokens")
+    if len(lead) == 2 and lead[1] > 1:
+        return st[1]
+    return st[0] if lead[0] > 1 else heads * dh
+
+
+def _kvq_index(t: Optional[torch.Tensor], lead, what: str, dev: int):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32:
+        raise CacheBlendError(3, f"{what} must be int32, not {t.dtype}")
+    if t.shape != lead or not t.is_contiguous() or t.get_device() != dev:
+        raise CacheBlendError(2, f"{what} must be contiguous {tuple(lead)} on the pool's device")
+    return t.data_ptr()
+
+
+def cb_kvq_write(pool: torch.Tensor, table: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                 seq: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantises k, v [rows, heads, head_dim] into positions ``pos`` of sequences ``seq`` (None: row i of
+    sequence i) of a 4-bit cache: its ``pool`` (kvq_pool) and page ``table`` int32 [sequences, pages]."""
+    cache, _, heads, dh, dev = _kvq_cache(pool, table)
+    dt, lead = _dtype_code(k.dtype), pos.shape
+    if len(lead) != 1 or lead[0] > 0x7FFFFFFF:
+        raise CacheBlendError(2, "pos must be a vector")
+    _check(load_library().cb_kvq_write(
+        cache, k.data_ptr(), _kvq_rows(k, k.dtype, lead, heads, dh, "k", dev), v.data_ptr(),
+        _kvq_rows(v, k.dtype, lead, heads, dh, "v", dev), dt, _kvq_index(seq, lead, "seq", dev),
+        _kvq_index(pos, lead, "pos", dev), lead[0], _stream_on(dev, stream)))
+
+
+def cb_kvq_read(pool: torch.Tensor, table: torch.Tensor, pos: torch.Tensor, seq: Optional[torch.Tensor] = None,
+                delta_pos: int = 0, theta: float = 10000.0, dtype: torch.dtype = torch.bfloat16,
+                k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None, stream=None):
+    """(k, v) [rows, heads, head_dim] held at positions ``pos`` of sequences ``seq``, the keys turned on by
+    ``delta_pos`` positions; of ``dtype`` unless given to write to."""
+    cache, _, heads, dh, dev = _kvq_cache(pool, table)
+    lead = pos.shape
+    if len(lead) != 1 or lead[0] > 0x7FFFFFFF:
+        raise CacheBlendError(2, "pos must be a vector")
+    if k_out is None or v_out is None:
+        dtype = dtype if k_out is None and v_out is None else (v_out if k_out is None else k_out).dtype
+        with _allocating_on(stream):
+            k_out = torch.empty(*lead, heads, dh, dtype=dtype, device=pool.device) if k_out is None else k_out
+            v_out = torch.empty(*lead, heads, dh, dtype=dtype, device=pool.device) if v_out is None else v_out
+    _check(load_library().cb_kvq_read(
+        cache, _kvq_index(seq, lead, "seq", dev), _kvq_index(pos, lead, "pos", dev), lead[0], int(delta_pos), float(theta),
+        _dtype_code(k_out.dtype), k_out.data_ptr(), _kvq_rows(k_out, k_out.dtype, lead, heads, dh, "k_out", dev),
+        v_out.data_ptr(), _kvq_rows(v_out, k_out.dtype, lead, heads, dh, "v_out", dev), _stream_on(dev, stream)))
+    return k_out, v_out
+
+
+def cb_kvq_attention(q: torch.Tensor, q_pos: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     scratch: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of queries q [sequences, heads, head_dim] or [sequences, tokens, heads, head_dim] over a 4-bit
+    cache: a token sees positions 0..q_pos of its sequence (negative: none, its output is zero).  ``scale``:
+    1 / sqrt(head_dim) if None; ``scratch``: see kvq_scratch (None: made for this call)."""
+    cache, n, heads, dh, dev = _kvq_cache(pool, table)
+    dt, shape = _dtype_code(q.dtype), q.shape
+    if len(shape) not in (3, 4) or shape[0] != n:
+        raise CacheBlendError(2, "q must be [sequences, heads, head_dim] or [sequences, tokens, heads, head_dim]")
+    lead, h = shape[:-2], shape[-2]
+    if h > 1 << 16 or (len(lead) == 2 and lead[1] > 0x7FFFFFFF):
+        raise CacheBlendError(2, "q has too many heads or tokens")
+    if out is None or scratch is None:
+        with _allocating_on(stream):
+            out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+            scratch = kvq_scratch(q.device) if scratch is None else scratch
+    if scratch.get_device() != dev or not scratch.is_contiguous():
+        raise CacheBlendError(1, "scratch must be contiguous on the pool's device")
+    _check(load_library().cb_kvq_attention(
+        cache, q.data_ptr(), _kvq_rows(q, q.dtype, lead, h, dh, "q", dev), _kvq_index(q_pos, lead, "q_pos", dev),
+        lead[1] if len(lead) == 2 else 1, h, dh ** -0.5 if scale is None else float(scale), dt, out.data_ptr(),
+        _kvq_rows(out, q.dtype, lead, h, dh, "out", dev), scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+        _stream_on(dev, stream)))
+    return out
 
 
 def cb_chunk_hash(ids) -> int:

@@ -1392,6 +1392,107 @@ cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_add_rmsnorm_quantize");
 }
 
+// ----------------------------------------------------------------------------- KV cache in 4 bits
+// The cache's sizes and pointers, and where its tokens lie; CB_OK or the refusal.
+static cb_status kvq_view(const cb_kvq_cache* c, cb::KvqView* out) {
+  if (!c) return fail(nullptr, CB_ERR_INVALID_ARG, "null cache");
+  if (c->head_dim != 64 && c->head_dim != 128) return fail(nullptr, CB_ERR_SHAPE, "head_dim must be 64 or 128");
+  if (c->page_tokens < 16 || c->page_tokens % 16 || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->n_pages < 0 ||
+      c->max_pages < 0 || c->n_seqs < 0 || c->n_seqs > (1 << 20) || c->ld_table < c->max_pages ||
+      static_cast<long long>(c->page_tokens) * c->max_pages > 0x7fffffffll)
+    return fail(nullptr, CB_ERR_SHAPE, "bad sizes of a 4-bit cache (page_tokens must be a multiple of 16)");
+  if ((c->n_pages > 0 && !c->pool) || (c->n_seqs > 0 && c->max_pages > 0 && !c->table))
+    return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(c->pool) || (reinterpret_cast<uintptr_t>(c->table) & 3))
+    return fail(nullptr, CB_ERR_INVALID_ARG, "the pool must be 16-byte aligned");
+  *out = {static_cast<uint8_t*>(c->pool), c->table, c->ld_table, c->n_pages, c->page_tokens, c->n_kv_heads, c->max_pages,
+          c->n_seqs};
+  return CB_OK;
+}
+
+// rows of heads x head_dim elements with a pitch
+static bool bad_rows(const void* p, long long ld, long long width, cb_dtype dt) {
+  return bad_mat(p, ld, width, dt == CB_BF16 ? 2 : 4);
+}
+constexpr const char* kKvqRows = "rows must be 16-byte aligned, with a pitch of at least heads * head_dim";
+
+size_t cb_kvq_page_bytes(int page_tokens, int n_kv_heads, int head_dim) {
+  if (page_tokens < 16 || page_tokens % 16 || n_kv_heads < 1 || n_kv_heads > 1024 || (head_dim != 64 && head_dim != 128)) return 0;
+  return static_cast<size_t>(page_tokens / 16) * n_kv_heads * 20 * head_dim;
+}
+
+size_t cb_kvq_scratch_size(void) { return cb::kvq_scratch_bytes(); }
+
+cb_status cb_kvq_write(const cb_kvq_cache* cache, const void* k, long long ldk, const void* v, long long ldv,
+                       cb_dtype dtype, const int32_t* seq, const int32_t* pos, int rows, void* stream) {
+  cb::KvqView c;
+  const cb_status st = kvq_view(cache, &c);
+  if (st != CB_OK) return st;
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
+  if (rows < 0 || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll) return fail(nullptr, CB_ERR_SHAPE, "bad number of rows");
+  if (rows == 0) return CB_OK;
+  if (!k || !v || !pos) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  const long long width = static_cast<long long>(c.n_kv_heads) * cache->head_dim;
+  if (bad_rows(k, ldk, width, dtype) || bad_rows(v, ldv, width, dtype)) return fail(nullptr, CB_ERR_SHAPE, kKvqRows);
+  int32_t* status = nullptr;
+  cudaError_t e = standalone_gemm_status(&status);
+  if (e == cudaSuccess)
+    e = launch_kvq_write(c, cache->head_dim, k, ldk, v, ldv, dtype, seq, pos, rows, status, as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_kvq_write");
+}
+
+cb_status cb_kvq_read(const cb_kvq_cache* cache, const int32_t* seq, const int32_t* pos, int rows, int delta_pos,
+                      double theta, cb_dtype dtype, void* k_out, long long ldk, void* v_out, long long ldv,
+                      void* stream) {
+  cb::KvqView c;
+  const cb_status st = kvq_view(cache, &c);
+  if (st != CB_OK) return st;
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
+  if (rows < 0 || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll || !(theta > 0))
+    return fail(nullptr, CB_ERR_SHAPE, "bad number of rows or theta");
+  if (rows == 0) return CB_OK;
+  if (!k_out || !v_out || !pos) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  const int dh = cache->head_dim;
+  const long long width = static_cast<long long>(c.n_kv_heads) * dh;
+  if (bad_rows(k_out, ldk, width, dtype) || bad_rows(v_out, ldv, width, dtype)) return fail(nullptr, CB_ERR_SHAPE, kKvqRows);
+  float cs[128];
+  for (int i = 0; i < dh / 2 && delta_pos != 0; ++i) {
+    const double a = static_cast<double>(delta_pos) * std::pow(theta, -2.0 * i / dh);
+    cs[2 * i] = static_cast<float>(std::cos(a));
+    cs[2 * i + 1] = static_cast<float>(std::sin(a));
+  }
+  int32_t* status = nullptr;
+  cudaError_t e = standalone_gemm_status(&status);
+  if (e == cudaSuccess)
+    e = launch_kvq_read(c, dh, seq, pos, rows, delta_pos != 0 ? cs : nullptr, dtype, k_out, ldk, v_out, ldv, status,
+                        as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_kvq_read");
+}
+
+cb_status cb_kvq_attention(const cb_kvq_cache* cache, const void* q, long long ldq, const int32_t* q_pos, int n_tok,
+                           int n_heads, float scale, cb_dtype dtype, void* out, long long ldo, void* scratch,
+                           size_t scratch_bytes, void* stream) {
+  cb::KvqView c;
+  const cb_status st = kvq_view(cache, &c);
+  if (st != CB_OK) return st;
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
+  if (n_tok < 0 || n_heads < 1 || n_heads > (1 << 16) || n_heads % c.n_kv_heads)
+    return fail(nullptr, CB_ERR_SHAPE, "n_heads must be a multiple of n_kv_heads");
+  if (static_cast<long long>(c.n_seqs) * n_tok * n_heads > (1ll << 30)) return fail(nullptr, CB_ERR_SHAPE, "too many query rows");
+  if (c.n_seqs == 0 || n_tok == 0) return CB_OK;
+  if (!q || !q_pos || !out) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  const long long width = static_cast<long long>(n_heads) * cache->head_dim;
+  if (bad_rows(q, ldq, width, dtype) || bad_rows(out, ldo, width, dtype)) return fail(nullptr, CB_ERR_SHAPE, kKvqRows);
+  if (!scratch || !aligned16(scratch) || scratch_bytes < cb::kvq_scratch_bytes())
+    return fail(nullptr, CB_ERR_WORKSPACE, "cb_kvq_attention needs cb_kvq_scratch_size() bytes of 16-byte aligned scratch");
+  int32_t* status = nullptr;
+  cudaError_t e = standalone_gemm_status(&status);
+  if (e == cudaSuccess)
+    e = launch_kvq_attention(c, cache->head_dim, q, ldq, q_pos, n_tok, n_heads, scale, dtype, out, ldo, scratch, status,
+                             as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_kvq_attention");
+}
+
 static cb_status gemm_scaled_sizes(int M, int N, int K, int epilogue) {
   if (epilogue < 0 || epilogue > CB_FP8_STORE_BF16) return fail(nullptr, CB_ERR_INVALID_ARG, "bad epilogue");
   if (M < 0 || N < 1 || K < 1 || K % 16) return fail(nullptr, CB_ERR_SHAPE, "K must be a positive multiple of 16");

@@ -298,4 +298,25 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& p, cudaStream_t s);
 bool gemm_fp8_set_plan(int tokens, int split);  // false for a plan that has no kernel
 void gemm_fp8_describe(int M, int N, int K, int epilogue, char* buf, size_t len);
 
+// KV cache in 4 bits (cb_kvq_*).
+// Where a sequence's tokens lie (cb_kvq_cache).
+struct KvqView {
+  uint8_t* pool;
+  const int32_t* table;
+  long long ld_table;
+  int n_pages, page_tokens, n_kv_heads, max_pages, n_seqs;
+};
+constexpr int KVQ_MAX_CTAS = 1024;  // of the attention's grid: its scratch holds two parts for each
+size_t kvq_scratch_bytes();
+cudaError_t launch_kvq_write(const KvqView& c, int head_dim, const void* k, long long ldk, const void* v, long long ldv,
+                             cb_dtype dt, const int32_t* seq, const int32_t* pos, int rows, int32_t* status,
+                             cudaStream_t s);
+// cs_host: (cos, sin) pairs of the keys' rotation, or NULL
+cudaError_t launch_kvq_read(const KvqView& c, int head_dim, const int32_t* seq, const int32_t* pos, int rows,
+                            const float* cs_host, cb_dtype dt, void* k, long long ldk, void* v, long long ldv,
+                            int32_t* status, cudaStream_t s);
+cudaError_t launch_kvq_attention(const KvqView& c, int head_dim, const void* q, long long ldq, const int32_t* q_pos, int T,
+                                 int n_heads, float scale, cb_dtype dt, void* out, long long ldo, void* scratch,
+                                 int32_t* status, cudaStream_t s);
+
 }  // namespace cb

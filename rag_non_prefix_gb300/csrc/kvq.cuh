@@ -1,0 +1,87 @@
+// The 4-bit form of a KV cache (cb_kvq_*): its layout and its arithmetic, shared by the kernels
+// that write, read and attend to it.
+//
+// A group is 32 consecutive channels of one token's key or value of one head:
+//   scale = the smallest bf16 number >= max(d / 14.75, a / 64, 2^-120),  d = hi - lo, a = max(|lo|, |hi|)
+//   zero  = floor(4 lo / scale) / 4,   code = clamp(nearest(x / scale - zero), 0, 15)
+//   value = scale * (code + zero)
+// The zero is a multiple of 1/4 of at most 64, so bf16 holds it; 14.75 steps and a zero at most 1/4 step too
+// low reach over the group.  code + zero has 9 bits and scale 8: the value is exact in fp32, and so is
+// (n + 1/2 + zero) * scale, by which the nearest code is decided exactly without a division.
+//
+// Block of 16 tokens of one head, 20 D bytes (D channels, NG = D / 32 groups), the memory a tensor-core
+// fragment is loaded from without rearrangement:
+//   key codes    token r at r D / 2: word (tq NG + g) holds channels 32 g + 8 tq + i in nibble i, so the lane
+//                of key row r and column pair tq finds its operands of every group in one 16-byte piece
+//   value codes  at 8 D: word ((j / 4) 128 + n 16 + tq 4 + j % 4) holds channels 16 j + n (low nibbles) and
+//                16 j + n + 8 (high ones) of tokens 2 tq, 2 tq + 8, 2 tq + 1, 2 tq + 9 (bytes 0 to 3): one
+//                operand fragment of 16 channels x 16 tokens a word and lane, and a byte belongs to one token
+//   key scales   at 16 D: token r at 4 NG r, NG bf16 scales, then NG zeros
+//   value scales 64 NG bytes further, the same
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+
+namespace cb {
+
+constexpr int KVQ_BLOCK = 16;
+__host__ __device__ constexpr int kvq_block_bytes(int dh) { return 20 * dh; }
+
+// block of 16 tokens that holds position pos of sequence seq, head 0; nullptr (and the status bit) if there
+// is none.  Blocks of the following heads are page_tokens / 16 blocks apart.
+__device__ __forceinline__ uint8_t* kvq_block(const KvqView& c, int seq, int pos, int dh, int32_t* status) {
+  if (seq >= c.n_seqs || pos / c.page_tokens >= c.max_pages) {
+    set_status(status, ST_RANGE);
+    return nullptr;
+  }
+  const int slot = pos / c.page_tokens;
+  const int page = c.table[seq * c.ld_table + slot];
+  if (page < 0 || page >= c.n_pages) {
+    set_status(status, ST_RANGE);
+    return nullptr;
+  }
+  const size_t blocks = c.page_tokens / KVQ_BLOCK;
+  return c.pool + (static_cast<size_t>(page) * c.n_kv_heads * blocks + (pos - slot * c.page_tokens) / KVQ_BLOCK) *
+                      kvq_block_bytes(dh);
+}
+
+// byte of value channels 16 j + n and 16 j + n + 8 of token r
+__device__ __forceinline__ int kvq_value_byte(int dh, int r, int j, int n) {
+  return 8 * dh + 512 * (j >> 2) + 64 * n + 16 * ((r & 7) >> 1) + 4 * (j & 3) + 2 * (r & 1) + (r >> 3);
+}
+
+__device__ __forceinline__ float bf16_up(float x) {  // the smallest bf16 number not below x >= 0
+  return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
+}
+
+// Scale and zero of a group whose smallest and largest numbers are lo and hi (hi infinite for a NaN).
+__device__ __forceinline__ float2 kvq_params(float lo, float hi) {
+  const float d = __fsub_rn(hi, lo), a = fmaxf(-lo, hi);
+  if (!(d < INFINITY)) return make_float2(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u));
+  // the quotient's rounding may land on a bf16 number just below the exact one (14 bits: exact product)
+  float s = bf16_up(__fdiv_rn(d, 14.75f));
+  if (__fmul_rn(s, 14.75f) < d) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
+  const float scale = fmaxf(fmaxf(s, bf16_up(a * 0.015625f)), 7.52316385e-37f);  // (2^-120)
+  float zero = 0.25f * floorf(4.f * __fdiv_rn(lo, scale));
+  if (__fmul_rn(zero, scale) > lo)
+    zero -= 0.25f;
+  else if (__fmul_rn(zero + 0.25f, scale) <= lo)
+    zero += 0.25f;
+  return make_float2(scale, zero);
+}
+
+// The code nearest to x / scale - zero, ties to even, exactly: an estimate by the reciprocal is off by far
+// less than a step, and the signs of x - (n +- 1/2 + zero) scale (one fused operation each, which keeps
+// a sign) put it right.
+__device__ __forceinline__ uint32_t kvq_code(float x, float scale, float inv, float zero) {
+  float n = rintf(__fsub_rn(__fmul_rn(x, inv), zero));
+  const float above = __fmaf_rn(-(n + 0.5f + zero), scale, x), below = __fmaf_rn(-(n - 0.5f + zero), scale, x);
+  const bool odd = static_cast<int>(n) & 1;
+  if (above > 0.f || (above == 0.f && odd))
+    n += 1.f;
+  else if (below < 0.f || (below == 0.f && odd))
+    n -= 1.f;
+  return static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f));
+}
+
+}  // namespace cb

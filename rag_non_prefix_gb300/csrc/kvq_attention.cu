@@ -1,0 +1,592 @@
+// Attention of a few new queries per sequence over a KV cache in 4 bits (layout: kvq.cuh).
+//
+//   out = sum_j softmax_j(scale q . k_j) v_j,  j <= the query's position
+//   q . k     = sum_g scale_g (sum_c q_c code_c + zero_g sum_c q_c)
+//   sum p v_c = sum_j (p_j scale_jg) (code_jc + zero_jg)
+// The codes enter the tensor core as they are, as the bf16 numbers 16 + code (two nibbles of a word become
+// two operands by one shift and one logic operation), so keys and values are never rounded; 16 is taken
+// off with the zero: in the accumulator's start for the keys (zero - 16) sum_c q_c, in a sum of
+// (p scale) (zero - 16) over the keys, kept in fp32, for the values.  p scale is rounded to bf16 (fp32 outputs: to three bf16
+// parts, as are the queries, so that nothing is lost) and the same rounded number multiplies code and zero,
+// so its rounding is one of 2^-9 of the value itself.
+//
+// mma.sync m16n8k16 and not tcgen05: 1 to 16 queries share a key, so the products are small beside the
+// cache's bytes and the operands go from the cache to registers without a rearrangement.  Keys (scores) and channels (values) lie on the 16
+// rows, the queries of a KV head on the 8 columns: the scores' accumulators, scaled and transposed by movmatrix, are the
+// second product's operand.
+//
+// Work: a unit is one KV head of one tile of 8 NT query rows (a sequence's tokens x the heads of its group), cut into
+// quanta of 64 keys.  All quanta stand in one row, divided evenly over the CTAs; a CTA whose share ends inside a unit
+// writes its part (sums, maximum) to scratch, and whichever CTA of that unit is the last to finish
+// merges the parts in the order of the keys, so results repeat exactly.  In a CTA each of 4 warps takes a block of 16
+// keys of a quantum, through a ring of its own in shared memory; no warp waits for another before the end.
+#include <algorithm>
+
+#include "internal.h"
+#include "kvq.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int AW = 4;                    // warps per CTA
+constexpr int QUANTUM = AW * KVQ_BLOCK;  // keys
+constexpr int MAX_ROWS = 16;             // query rows per tile at most
+constexpr float LAZY = 6.f;              // the running maximum moves once a score passes it by 2^6
+
+__host__ __device__ constexpr int slot_floats(int dh) { return MAX_ROWS * (dh + 2); }
+
+struct KvqAttn {
+  KvqView c;
+  const void* q;
+  long long ldq;
+  const int32_t* q_pos;  // [n_seqs][T]
+  int T, G;
+  float scale_log2;
+  void* out;
+  long long ldo;
+  int* counters;  // [KVQ_MAX_CTAS], zero between calls
+  float* parts;   // 2 slots a CTA
+  int tiles_per_seq, n_tiles;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 + nibbles i and i + 4 of a word as two bf16 (16 is 0x4180, with 3 bits below the units)
+template <int I> __device__ __forceinline__ uint32_t nibbles(uint32_t x) {
+  const uint32_t y = I == 0 ? x << 3 : x >> (4 * I - 3);
+  return (y & 0x00780078u) | 0x41804180u;
+}
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// The bf16 parts of x and y, packed: NP parts whose sum is (x, y), exactly for NP = 3; x and y become what is left.
+__device__ __forceinline__ uint32_t split_off(float& x, float& y) {
+  const uint32_t u = pack_bf16x2(x, y);
+  x -= lo_f(u);
+  y -= hi_f(u);
+  return u;
+}
+
+// Quanta of tile `ti` and the number of keys that its rows see.
+__device__ __forceinline__ int tile_quanta(const KvqAttn& p, int ti, int rows, int& len) {
+  const int seq = ti / p.tiles_per_seq, r0 = (ti - seq * p.tiles_per_seq) * rows;
+  const int t1 = (min(r0 + rows, p.T * p.G) - 1) / p.G;
+  int top = -1;
+  for (int t = r0 / p.G; t <= t1; ++t) top = max(top, p.q_pos[static_cast<long long>(seq) * p.T + t]);
+  const int cap = p.c.max_pages * p.c.page_tokens;
+  if (top >= cap) set_status(p.status, ST_RANGE);
+  len = min(top, cap - 1) + 1;
+  return max(1, (len + QUANTUM - 1) / QUANTUM);
+}
+
+template <int DH> struct Words;  // a lane's key codes of one token: a word per group
+template <> struct Words<128> { typedef uint4 type; };
+template <> struct Words<64> { typedef uint2 type; };
+
+// T: queries and outputs; NT: column tiles of 8 query rows; NP: bf16 parts of a query or weight.
+template <typename T, int DH, int NT, int NP> struct Attn {
+  static constexpr int NG = DH / 32, R = 8 * NT, BLK = kvq_block_bytes(DH);
+  static constexpr int STAGES = 4;
+  static constexpr int ROW = DH + 4;  // pitch of the merge buffer, free of bank conflicts
+  static constexpr int RING = AW * STAGES * BLK;
+  static constexpr int MERGE = AW * R * ROW * 4;
+  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+
+  uint32_t qb[NT][NP][NG][4];  // query operands: per group two k-steps of (b0, b1)
+  float qs[NT][NG][2];         // sums of the query's group, of this lane's two columns
+  float o[NT][DH / 16][4];
+  float corr[NT][NG][2];
+  float m[NT][2], l[NT][2];
+  int lim[NT][2];  // last key of this lane's two columns
+
+  __device__ __forceinline__ void load_q(const KvqAttn& p, int seq, int r0, int head) {
+    const int lane = threadIdx.x & 31, rr = lane >> 2, tq = lane & 3, rows = p.T * p.G;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = r0 + nt * 8 + rr;
+      const bool in = row < rows;
+      const int t = in ? row / p.G : 0, g = in ? row - t * p.G : 0;
+      const T* src = static_cast<const T*>(p.q) + (static_cast<long long>(seq) * p.T + t) * p.ldq +
+                     static_cast<long long>(head * p.G + g) * DH + 8 * tq;
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        float f[8] = {};
+        if (in) load8(src + 32 * grp, f);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += f[i];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qs[nt][grp][0] = __shfl_sync(0xffffffffu, sum, 8 * tq);
+        qs[nt][grp][1] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
+#pragma unroll
+        for (int np = 0; np < NP; ++np)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qb[nt][np][grp][i] = split_off(f[i], f[i + 4]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = r0 + nt * 8 + 2 * tq + c;
+        lim[nt][c] = col < rows ? p.q_pos[static_cast<long long>(seq) * p.T + col / p.G] : -1;
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) corr[nt][grp][c] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
+    }
+  }
+
+  // the last key that every row of the tile sees
+  __device__ __forceinline__ int seen_by_all(const KvqAttn& p, int r0) const {
+    const int tq = threadIdx.x & 3, rows = p.T * p.G;
+    int x = 0x7fffffff;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (r0 + nt * 8 + 2 * tq + c < rows) x = min(x, lim[nt][c]);
+    x = min(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return min(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  }
+
+  // 16 keys from key0 on, their block in shared memory.  MASKED: some row does not see all of them (a key
+  // that a row does not see may hold anything, a NaN scale too, and takes no part).
+  template <bool MASKED> __device__ __forceinline__ void block(const uint8_t* blk, int key0, float scale_log2) {
+    const int lane = threadIdx.x & 31, rr = lane >> 2, tq = lane & 3;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+    {
+      uint32_t w[2][NG], ks[2][NG / 2], kz[2][NG / 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        typedef typename Words<DH>::type W;
+        *reinterpret_cast<W*>(w[h]) = *reinterpret_cast<const W*>(blk + (rr + 8 * h) * (DH / 2) + tq * 4 * NG);
+        const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 4 * NG * (rr + 8 * h));
+#pragma unroll
+        for (int i = 0; i < NG / 2; ++i) {
+          ks[h][i] = prm[i];
+          kz[h][i] = prm[NG / 2 + i];
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float s0 = g & 1 ? hi_f(ks[0][g / 2]) : lo_f(ks[0][g / 2]), s1 = g & 1 ? hi_f(ks[1][g / 2]) : lo_f(ks[1][g / 2]);
+        const float z0 = (g & 1 ? hi_f(kz[0][g / 2]) : lo_f(kz[0][g / 2])) - 16.f;
+        const float z1 = (g & 1 ? hi_f(kz[1][g / 2]) : lo_f(kz[1][g / 2])) - 16.f;
+        const uint32_t a0 = nibbles<0>(w[0][g]), a1 = nibbles<0>(w[1][g]), a2 = nibbles<1>(w[0][g]), a3 = nibbles<1>(w[1][g]);
+        const uint32_t b0 = nibbles<2>(w[0][g]), b1 = nibbles<2>(w[1][g]), b2 = nibbles<3>(w[0][g]), b3 = nibbles<3>(w[1][g]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[4] = {z0 * qs[nt][g][0], z0 * qs[nt][g][1], z1 * qs[nt][g][0], z1 * qs[nt][g][1]};
+#pragma unroll
+          for (int np = 0; np < NP; ++np) {
+            mma_bf16(c, a0, a1, a2, a3, qb[nt][np][g][0], qb[nt][np][g][1]);
+            mma_bf16(c, b0, b1, b2, b3, qb[nt][np][g][2], qb[nt][np][g][3]);
+          }
+          s[nt][0] = fmaf(s0, c[0], s[nt][0]);
+          s[nt][1] = fmaf(s0, c[1], s[nt][1]);
+          s[nt][2] = fmaf(s1, c[2], s[nt][2]);
+          s[nt][3] = fmaf(s1, c[3], s[nt][3]);
+        }
+      }
+    }
+    bool up = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[nt][i] *= scale_log2;
+        if (MASKED && key0 + rr + (i >> 1) * 8 > lim[nt][i & 1]) s[nt][i] = -INFINITY;
+        up |= s[nt][i] > m[nt][i & 1] + LAZY;
+      }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = fmaxf(m[nt][c], fmaxf(s[nt][c], s[nt][2 + c]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          const float f = x == -INFINITY ? 1.f : exp2_fast(m[nt][c] - x);
+          m[nt][c] = x;
+          l[nt][c] *= f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) corr[nt][g][c] *= f;
+#pragma unroll
+          for (int j = 0; j < DH / 16; ++j) {
+            o[nt][j][c] *= f;
+            o[nt][j][2 + c] *= f;
+          }
+        }
+    }
+    bool dead[NT][4];  // (MASKED)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dead[nt][i] = MASKED && s[nt][i] == -INFINITY;
+        const float mm = m[nt][i & 1];
+        s[nt][i] = exp2_fast(s[nt][i] - (MASKED && mm == -INFINITY ? 0.f : mm));
+        l[nt][i & 1] += s[nt][i];
+      }
+    uint32_t vs[2][NG / 2], vz[2][NG / 2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 64 * NG + 4 * NG * (rr + 8 * h));
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i) {
+        vs[h][i] = prm[i];
+        vz[h][i] = prm[NG / 2 + i];
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < DH / 64; ++half) {  // 64 channels, two groups, four fragments
+      uint32_t w[4];
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(blk + 8 * DH + 512 * half + 16 * lane);
+#pragma unroll
+      for (int gg = 0; gg < 2; ++gg) {
+        const int g = 2 * half + gg;
+        const float s0 = gg ? hi_f(vs[0][half]) : lo_f(vs[0][half]), s1 = gg ? hi_f(vs[1][half]) : lo_f(vs[1][half]);
+        const float z0 = (gg ? hi_f(vz[0][half]) : lo_f(vz[0][half])) - 16.f;
+        const float z1 = (gg ? hi_f(vz[1][half]) : lo_f(vz[1][half])) - 16.f;
+        uint32_t pb[NT][NP][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[4] = {s[nt][0] * s0, s[nt][1] * s0, s[nt][2] * s1, s[nt][3] * s1};
+          if (MASKED)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (dead[nt][i]) x[i] = 0.f;
+          if (NP > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!MASKED || !dead[nt][i]) corr[nt][g][i & 1] = fmaf(x[i], i < 2 ? z0 : z1, corr[nt][g][i & 1]);
+          }
+#pragma unroll
+          for (int np = 0; np < NP; ++np) {
+            const uint32_t u0 = NP > 1 ? split_off(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+            const uint32_t u1 = NP > 1 ? split_off(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+            if (NP == 1) {
+              const float r[4] = {lo_f(u0), hi_f(u0), lo_f(u1), hi_f(u1)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!MASKED || !dead[nt][i]) corr[nt][g][i & 1] = fmaf(r[i], i < 2 ? z0 : z1, corr[nt][g][i & 1]);
+            }
+            pb[nt][np][0] = transpose8x8(u0);
+            pb[nt][np][1] = transpose8x8(u1);
+          }
+        }
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const uint32_t x = w[2 * gg + jj];
+          const uint32_t a0 = nibbles<0>(x), a1 = nibbles<1>(x), a2 = nibbles<2>(x), a3 = nibbles<3>(x);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int np = 0; np < NP; ++np) mma_bf16(o[nt][2 * g + jj], a0, a1, a2, a3, pb[nt][np][0], pb[nt][np][1]);
+        }
+      }
+    }
+  }
+};
+
+template <int DH> __device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* src) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < (kvq_block_bytes(DH) / 16 + 31) / 32; ++i) {
+    const int c = i * 32 + lane;
+    if (c < kvq_block_bytes(DH) / 16) cp_async16(dst + c * 16, src + c * 16, 16);
+  }
+}
+
+// weight of a part (maximum m, sum l) under the common maximum M; a part without keys has none, a NaN stays one
+__device__ __forceinline__ float part_weight(float m, float l, float M) {
+  return m == -INFINITY && l == 0.f ? 0.f : exp2f(m - M);
+}
+
+template <typename T, int DH, int NT, int NP>
+__global__ void __launch_bounds__(AW * 32) kvq_attention_kernel(const __grid_constant__ KvqAttn p) {
+  typedef Attn<T, DH, NT, NP> A;
+  constexpr int R = A::R, ROW = A::ROW;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ long long scan[AW * 32 + 1];
+  __shared__ int first_tile;
+  __shared__ long long first_base;
+  __shared__ float part_m[AW][R], part_l[AW][R], wts[AW][R], row_m[R], row_l[R];
+  __shared__ int is_last;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, rr = lane >> 2, tq = lane & 3;
+  const int heads = p.c.n_kv_heads, rows = p.T * p.G;
+
+  // this CTA's share of all quanta
+  const int per = (p.n_tiles + AW * 32 - 1) / (AW * 32);
+  long long mine = 0;
+  for (int i = tid * per; i < min(p.n_tiles, (tid + 1) * per); ++i) {
+    int len;
+    mine += tile_quanta(p, i, R, len);
+  }
+  scan[tid + 1] = mine * heads;
+  if (tid == 0) scan[0] = 0;
+  __syncthreads();
+  if (w == 0) {  // inclusive sums, four entries a lane
+    long long x[AW], run = 0;
+#pragma unroll
+    for (int i = 0; i < AW; ++i) x[i] = run += scan[1 + lane * AW + i];
+    long long up = run;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, up, d);
+      if (lane >= d) up += y;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < AW; ++i) scan[1 + lane * AW + i] = x[i] + up - run;
+  }
+  __syncthreads();
+  const long long total = scan[AW * 32];
+  const long long n = min(static_cast<long long>(gridDim.x), total);
+  if (blockIdx.x >= n) return;
+  long long cur = total * blockIdx.x / n;
+  const long long end = total * (blockIdx.x + 1) / n;
+  if (scan[tid] <= cur && cur < scan[tid + 1]) {
+    long long base = scan[tid];
+    int i = tid * per;
+    for (;; ++i) {
+      int len;
+      const long long q = static_cast<long long>(tile_quanta(p, i, R, len)) * heads;
+      if (cur < base + q) break;
+      base += q;
+    }
+    first_tile = i;
+    first_base = base;
+  }
+  __syncthreads();
+  int ti = first_tile;
+  long long base = first_base;
+  const long long begin = cur;
+
+  while (cur < end) {
+    int len;
+    const int nq = tile_quanta(p, ti, R, len);
+    const int head = static_cast<int>((cur - base) / nq);
+    const long long unit = base + static_cast<long long>(head) * nq;
+    const int q0 = static_cast<int>(cur - unit), q1 = static_cast<int>(min(static_cast<long long>(nq), end - unit));
+    const int seq = ti / p.tiles_per_seq, r0 = (ti - seq * p.tiles_per_seq) * R;
+
+    A a;
+    a.load_q(p, seq, r0, head);
+    const int all = a.seen_by_all(p, r0);
+    const int blocks = min((len + KVQ_BLOCK - 1) / KVQ_BLOCK, q1 * AW), per_page = p.c.page_tokens / KVQ_BLOCK;
+    const int b0 = q0 * AW + w, count = blocks > b0 ? (blocks - b0 + AW - 1) / AW : 0;
+    uint8_t* ring = smem + w * A::STAGES * A::BLK;
+    const uint32_t ring_u = smem_u32(ring);
+    uint32_t there = 0;  // bit s: stage s holds a block
+    auto fetch = [&](int i) {
+      if (i < count) {
+        const int b = b0 + i * AW, slot = b / per_page, stage = i % A::STAGES;
+        const int page = p.c.table[seq * p.c.ld_table + slot];
+        const bool ok = page >= 0 && page < p.c.n_pages;
+        if (ok)
+          copy_block<DH>(ring_u + stage * A::BLK,
+                         p.c.pool + ((static_cast<size_t>(page) * heads + head) * per_page + (b - slot * per_page)) * A::BLK);
+        else
+          set_status(p.status, ST_RANGE);
+        there = (there & ~(1u << stage)) | (ok ? 1u << stage : 0u);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < A::STAGES - 1; ++i) fetch(i);
+    for (int i = 0; i < count; ++i) {
+      cp_async_wait<A::STAGES - 2>();
+      __syncwarp();
+      const int stage = i % A::STAGES, key0 = (b0 + i * AW) * KVQ_BLOCK;
+      const bool ok = there >> stage & 1;
+      fetch(i + A::STAGES - 1);
+      if (!ok) continue;
+      if (key0 + KVQ_BLOCK - 1 <= all)
+        a.template block<false>(ring + stage * A::BLK, key0, p.scale_log2);
+      else
+        a.template block<true>(ring + stage * A::BLK, key0, p.scale_log2);
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // every warp is done with its ring: the merge buffer lies over them
+
+    float* buf = reinterpret_cast<float*>(smem) + w * R * ROW;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = nt * 8 + 2 * tq + c;
+        float sum = a.l[nt][c], corr[A::NG];
+#pragma unroll
+        for (int g = 0; g < A::NG; ++g) corr[g] = a.corr[nt][g][c];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+          for (int g = 0; g < A::NG; ++g) corr[g] += __shfl_xor_sync(0xffffffffu, corr[g], d);
+        }
+        if (rr == 0) {
+          part_m[w][row] = a.m[nt][c];
+          part_l[w][row] = sum;
+        }
+#pragma unroll
+        for (int j = 0; j < DH / 16; ++j) {
+          buf[row * ROW + 16 * j + rr] = a.o[nt][j][c] + corr[j / 2];
+          buf[row * ROW + 16 * j + rr + 8] = a.o[nt][j][2 + c] + corr[j / 2];
+        }
+      }
+    __syncthreads();
+    if (tid < R) {
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int i = 0; i < AW; ++i) M = fmaxf(M, part_m[i][tid]);
+#pragma unroll
+      for (int i = 0; i < AW; ++i) {
+        const float x = part_weight(part_m[i][tid], part_l[i][tid], M);
+        wts[i][tid] = x;
+        L += x * part_l[i][tid];
+      }
+      row_m[tid] = M;
+      row_l[tid] = L;
+    }
+    __syncthreads();
+    const bool whole = q1 - q0 == nq;
+    // 2 slots a CTA: the first part of its share, and a later one
+    float* slot = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (cur != begin)) * slot_floats(DH);
+    const float* sm = reinterpret_cast<const float*>(smem);
+    for (int i = tid; i < R * DH; i += AW * 32) {
+      const int row = i / DH, ch = i - row * DH, gr = r0 + row;
+      if (gr >= rows) break;
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < AW; ++k) {
+        const float wt = wts[k][row];
+        if (wt != 0.f) x = fmaf(wt, sm[(k * R + row) * ROW + ch], x);
+      }
+      if (whole) {
+        const int t = gr / p.G;
+        static_cast<T*>(p.out)[(static_cast<long long>(seq) * p.T + t) * p.ldo +
+                               static_cast<long long>(head * p.G + gr - t * p.G) * DH + ch] =
+            from_f<T>(row_l[row] == 0.f ? 0.f : x / row_l[row]);
+      } else {
+        slot[row * DH + ch] = x;
+      }
+    }
+    if (!whole) {
+      if (tid < R) *reinterpret_cast<float2*>(slot + MAX_ROWS * DH + 2 * tid) = make_float2(row_m[tid], row_l[tid]);
+      // CTAs of this unit: share c holds quantum x when total c / n <= x < total (c + 1) / n (rounded down)
+      const int c0 = static_cast<int>(((unit + 1) * n - 1) / total), c1 = static_cast<int>(((unit + nq) * n - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) is_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
+      __syncthreads();
+      if (is_last) {
+        __threadfence();
+        if (tid == 0) p.counters[c0] = 0;
+        const size_t first = 2 * static_cast<size_t>(c0) + (unit != total * c0 / n);
+        for (int i = tid; i < R * DH; i += AW * 32) {
+          const int row = i / DH, ch = i - row * DH, gr = r0 + row;
+          if (gr >= rows) break;
+          float M = -INFINITY, L = 0.f, x = 0.f;
+          for (int c = c0; c <= c1; ++c)
+            M = fmaxf(M, __ldcg(p.parts + (c == c0 ? first : 2 * static_cast<size_t>(c)) * slot_floats(DH) + MAX_ROWS * DH + 2 * row));
+          for (int c = c0; c <= c1; ++c) {
+            const float* s = p.parts + (c == c0 ? first : 2 * static_cast<size_t>(c)) * slot_floats(DH);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + MAX_ROWS * DH + 2 * row));
+            const float wt = part_weight(ml.x, ml.y, M);
+            if (wt != 0.f) {
+              L = fmaf(wt, ml.y, L);
+              x = fmaf(wt, __ldcg(s + row * DH + ch), x);
+            }
+          }
+          const int t = gr / p.G;
+          static_cast<T*>(p.out)[(static_cast<long long>(seq) * p.T + t) * p.ldo +
+                                 static_cast<long long>(head * p.G + gr - t * p.G) * DH + ch] =
+              from_f<T>(L == 0.f ? 0.f : x / L);
+        }
+      }
+    }
+    __syncthreads();  // the merge buffer becomes rings again
+    cur = unit + q1;
+    if (cur == base + static_cast<long long>(nq) * heads) {
+      base = cur;
+      ++ti;
+    }
+  }
+}
+
+template <typename T, int DH, int NT, int NP>
+cudaError_t launch(KvqAttn p, cudaStream_t s) {
+  typedef Attn<T, DH, NT, NP> A;
+  p.tiles_per_seq = (p.T * p.G + A::R - 1) / A::R;
+  p.n_tiles = p.c.n_seqs * p.tiles_per_seq;
+  static DeviceOnce configured;
+  cudaError_t e = max_dynamic_smem_once(reinterpret_cast<const void*>(kvq_attention_kernel<T, DH, NT, NP>), A::SMEM, configured);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int grid = std::min(KVQ_MAX_CTAS, 3 * sms);
+  return launch_chain(kvq_attention_kernel<T, DH, NT, NP>, dim3(grid), dim3(AW * 32), A::SMEM, s, p);
+}
+
+}  // namespace
+
+size_t kvq_scratch_bytes() {
+  return KVQ_MAX_CTAS * sizeof(int) + 2 * static_cast<size_t>(KVQ_MAX_CTAS) * slot_floats(128) * sizeof(float);
+}
+
+cudaError_t launch_kvq_attention(const KvqView& c, int head_dim, const void* q, long long ldq, const int32_t* q_pos, int T,
+                                 int n_heads, float scale, cb_dtype dt, void* out, long long ldo, void* scratch,
+                                 int32_t* status, cudaStream_t s) {
+  KvqAttn p = {};
+  p.c = c;
+  p.q = q;
+  p.ldq = ldq;
+  p.q_pos = q_pos;
+  p.T = T;
+  p.G = n_heads / c.n_kv_heads;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = out;
+  p.ldo = ldo;
+  p.counters = static_cast<int*>(scratch);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + KVQ_MAX_CTAS * sizeof(int));
+  p.status = status;
+  const bool two = T * p.G > 8;
+  if (dt == CB_BF16) {
+    if (head_dim == 128) return two ? launch<bf16, 128, 2, 1>(p, s) : launch<bf16, 128, 1, 1>(p, s);
+    return two ? launch<bf16, 64, 2, 1>(p, s) : launch<bf16, 64, 1, 1>(p, s);
+  }
+  if (head_dim == 128) return two ? launch<float, 128, 2, 3>(p, s) : launch<float, 128, 1, 3>(p, s);
+  return two ? launch<float, 64, 2, 3>(p, s) : launch<float, 64, 1, 3>(p, s);
+}
+
+}  // namespace cb
