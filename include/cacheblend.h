@@ -601,6 +601,32 @@ typedef struct {
 cb_status cb_decode_step(cb_ctx* ctx, const cb_decode_seq* seqs_host, int n_seq, const int32_t* tokens,
                          int32_t* out_tokens, void* stream);
 
+/* --------------------------------------------------------------------- sampling
+ * (the pages decode greedily; a user's answers are drawn.)  A row's tokens stand by falling logit, equal ones by rising
+ * id; with w = exp((x - max) / temperature) three filters each keep a prefix of that order:
+ *   top_k   the first top_k tokens (<= 0 or >= vocab: all)
+ *   top_p   of those the shortest prefix whose mass (sum of w) reaches top_p times theirs, one token at least
+ *           (>= 1: all)
+ *   min_p   the tokens with w >= min_p, that is, of at least min_p times the likeliest one's probability (<= 0: all; > 1 is 1)
+ * and the token drawn is the first whose running mass exceeds uniform times the mass of the shortest of the three.
+ * temperature <= 0 (or NaN): the first token (greedy).  Logits of -infinity and NaN are no tokens; a row of them alone
+ * gives -1.  Where the largest is +infinity, its tokens are equally likely.  Arrays of one entry per row, device;
+ * a NULL filter is off, a NULL temperature is 1. */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} cb_sampling;
+/* logits [rows][vocab] of dtype with a pitch of ld elements (element-aligned; vocab <= 2^18); uniform [rows] in [0, 1):
+ * the same numbers give the same tokens; out int32 [rows].  Weights are exact to about 2^-30 and their
+ * sums exact, whatever the order.  params may be NULL. */
+cb_status cb_sample(const void* logits, long long ld, cb_dtype dtype, int rows, int vocab, const cb_sampling* params,
+                    const float* uniform, int32_t* out, void* stream);
+/* cb_decode_step whose next tokens are drawn (cb_sample on the LM head's fp32 logits) instead of the largest. */
+cb_status cb_decode_step_sample(cb_ctx* ctx, const cb_decode_seq* seqs_host, int n_seq, const int32_t* tokens,
+                                const cb_sampling* params, const float* uniform, int32_t* out_tokens, void* stream);
+
 /* --------------------------------------------------------------------- per-layer API
  * The pages' three calls ([P1] vLLMとの統合): fetch_kv(text, layer_id) loads a layer's
  * cached KV, prefill_layer(input_dict, KVCache) runs the partial prefill of the

@@ -33,7 +33,7 @@ EXPORTED = ("cb_create", "cb_destroy", "cb_status_string", "cb_last_error", "cb_
             "cb_set_staging", "cb_chunk_hash", "cb_chunk_info_of", "cb_plan_loading", "cb_decode_step",
             "cb_ratio_schedule", "cb_k_for_ratio", "cb_quantize", "cb_add_rmsnorm_quantize", "cb_gemm_scaled",
             "cb_gemm_scaled_set_plan", "cb_gemm_scaled_describe", "cb_kvq_page_bytes", "cb_kvq_write", "cb_kvq_read",
-            "cb_kvq_attention", "cb_kvq_scratch_size")
+            "cb_kvq_attention", "cb_kvq_scratch_size", "cb_sample", "cb_decode_step_sample")
 PHASES = ("begin", "staged_rot", "norm", "qkv", "rope", "deviation", "select", "scatter", "attention", "oproj",
           "gateup", "down", "finish")
 
@@ -95,6 +95,10 @@ class KvqCache(C.Structure):
     _fields_ = [("pool", C.c_void_p), ("n_pages", C.c_int), ("page_tokens", C.c_int), ("n_kv_heads", C.c_int),
                 ("head_dim", C.c_int), ("table", C.c_void_p), ("ld_table", C.c_longlong), ("max_pages", C.c_int),
                 ("n_seqs", C.c_int)]
+
+
+class Sampling(C.Structure):
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p)]
 
 
 CB_FP8_STORE_F32, CB_FP8_ADD_F32, CB_FP8_SWIGLU_FP8, CB_FP8_STORE_BF16 = 0, 1, 2, 3
@@ -163,6 +167,9 @@ def load_library(path: str = LIB_PATH):
         "cb_kvq_attention": (st, [vp, vp, C.c_longlong, i32p, C.c_int, C.c_int, C.c_float, C.c_int, vp, C.c_longlong, vp,
                                   C.c_size_t, vp]),
         "cb_kvq_scratch_size": (C.c_size_t, []),
+        # (the filters: byref(Sampling), or its bytes)
+        "cb_sample": (st, [vp, C.c_longlong, C.c_int, C.c_int, C.c_int, vp, vp, i32p, vp]),
+        "cb_decode_step_sample": (st, [vp, C.POINTER(DecodeSeq), C.c_int, i32p, vp, vp, i32p, vp]),
         "cb_codec_layer_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
         "cb_kv_encode": (st, [vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp]),
         "cb_kv_decode": (st, [vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_double, C.c_int, vp, vp,
@@ -685,6 +692,50 @@ def cb_kvq_attention(q: torch.Tensor, q_pos: torch.Tensor, pool: torch.Tensor, t
     return out
 
 
+# ----------------------------------------------------------------------------- sampling
+# a Sampling as bytes
+_pack_sampling = struct.Struct("@4P").pack
+
+
+def _row_values(t: Optional[torch.Tensor], dtype, rows: int, what: str, dev: int) -> int:
+    if t is None:
+        return 0
+    if t.dtype is not dtype:
+        raise CacheBlendError(3, f"{what} must be {dtype}, not {t.dtype}")
+    if t.shape != (rows,) or not t.is_contiguous():
+        raise CacheBlendError(2, f"{what} must be {rows} contiguous values")
+    if t.get_device() != dev:
+        raise CacheBlendError(1, f"{what} must be on the logits' device")
+    return t.data_ptr()
+
+
+def _filters(rows: int, dev: int, temperature, top_k, top_p, min_p) -> bytes:
+    return _pack_sampling(_row_values(temperature, torch.float32, rows, "temperature", dev),
+                          _row_values(top_k, torch.int32, rows, "top_k", dev),
+                          _row_values(top_p, torch.float32, rows, "top_p", dev),
+                          _row_values(min_p, torch.float32, rows, "min_p", dev))
+
+
+def cb_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+              top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+              min_p: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A token id (int32) of each row of logits [rows, vocab], drawn by the row's random number ``uniform`` in [0, 1)
+    after the filters (tensors of a value per row: fp32, top_k int32; None: off).  A temperature of 0 is
+    greedy; a row without a token gives -1."""
+    dt = _dtype_code(logits.dtype)
+    rows, vocab, ld, dev = _first(logits, "logits")
+    if uniform is None:
+        raise CacheBlendError(1, "uniform is needed")
+    if out is None:
+        with _allocating_on(stream):
+            out = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    _check(load_library().cb_sample(logits.data_ptr(), ld, dt, rows, vocab,
+                                    _filters(rows, dev, temperature, top_k, top_p, min_p),
+                                    _row_values(uniform, torch.float32, rows, "uniform", dev),
+                                    _row_values(out, torch.int32, rows, "out", dev), _stream_on(dev, stream)))
+    return out
+
+
 def cb_chunk_hash(ids) -> int:
     """Content key of a chunk: FNV-1a 64 of its token ids (host sequence or tensor)."""
     if isinstance(ids, torch.Tensor):
@@ -919,10 +970,11 @@ class Engine:
         return out
 
     def decode_step(self, reqs, tokens: torch.Tensor, out_tokens: Optional[torch.Tensor] = None, n_past=None,
-                    out_hidden=None, stream=None) -> torch.Tensor:
-        """One greedy decode step of the blended requests ``reqs`` (made with decode_room):
+                    out_hidden=None, stream=None, sampling: Optional[Dict] = None) -> torch.Tensor:
+        """One decode step of the blended requests ``reqs`` (made with decode_room):
         tokens [n] enter at positions n_past[i] (default: each request's prompt length plus the
-        steps it already decoded); returns the next tokens [n]."""
+        steps it already decoded); returns the next tokens [n]: the likeliest ones, or with ``sampling``
+        (cb_sample's ``uniform`` and any of its filters, a value per request) drawn ones."""
         n = len(reqs)
         if out_tokens is None:
             with _allocating_on(stream):
@@ -932,7 +984,16 @@ class Engine:
             past = r["n_tokens"] + r.setdefault("decoded", 0) if n_past is None else int(n_past[i])
             arr[i] = DecodeSeq(r["fused_k"].data_ptr(), r["fused_v"].data_ptr(), int(r["kv_capacity"]), past,
                                None if out_hidden is None else out_hidden[i].data_ptr())
-        _check(self.lib.cb_decode_step(self.ctx, arr, n, _ptr(tokens), _ptr(out_tokens), _stream(stream)), self.ctx)
+        if sampling is None:
+            _check(self.lib.cb_decode_step(self.ctx, arr, n, _ptr(tokens), _ptr(out_tokens), _stream(stream)), self.ctx)
+        else:
+            dev = self.workspace.get_device()
+            filters = _filters(n, dev, *(sampling.get(f) for f in ("temperature", "top_k", "top_p", "min_p")))
+            if unknown := set(sampling) - {"uniform", "temperature", "top_k", "top_p", "min_p"}:
+                raise CacheBlendError(1, f"unknown sampling arguments {sorted(unknown)}")
+            _check(self.lib.cb_decode_step_sample(self.ctx, arr, n, _ptr(tokens), filters,
+                                                  _row_values(sampling.get("uniform"), torch.float32, n, "uniform", dev),
+                                                  _ptr(out_tokens), _stream(stream)), self.ctx)
         if n_past is None:
             for r in reqs:
                 r["decoded"] += 1

@@ -1493,6 +1493,23 @@ cb_status cb_kvq_attention(const cb_kvq_cache* cache, const void* q, long long l
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_kvq_attention");
 }
 
+cb_status cb_sample(const void* logits, long long ld, cb_dtype dtype, int rows, int vocab, const cb_sampling* params,
+                    const float* uniform, int32_t* out, void* stream) {
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
+  if (rows < 0 || rows > (1 << 24) || vocab < 1 || vocab > SAMPLE_MAX_VOCAB || (rows > 1 && ld < vocab))
+    return fail(nullptr, CB_ERR_SHAPE, "sampling takes up to 2^24 rows of 1 to 2^18 logits");
+  if (rows == 0) return CB_OK;
+  if (!logits || !uniform || !out) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  const cb_sampling f = params ? *params : cb_sampling{};
+  auto off = [](const void* p, unsigned size) { return reinterpret_cast<uintptr_t>(p) & (size - 1); };
+  if (off(logits, dtype == CB_BF16 ? 2 : 4) || off(uniform, 4) || off(out, 4) || off(f.temperature, 4) || off(f.top_k, 4) ||
+      off(f.top_p, 4) || off(f.min_p, 4))
+    return fail(nullptr, CB_ERR_INVALID_ARG, "misaligned pointer");
+  cudaError_t e = launch_sample(logits, ld, dtype, rows, vocab, f.temperature, f.top_k, f.top_p, f.min_p, uniform, out,
+                                as_stream(stream));
+  return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_sample");
+}
+
 static cb_status gemm_scaled_sizes(int M, int N, int K, int epilogue) {
   if (epilogue < 0 || epilogue > CB_FP8_STORE_BF16) return fail(nullptr, CB_ERR_INVALID_ARG, "bad epilogue");
   if (M < 0 || N < 1 || K < 1 || K % 16) return fail(nullptr, CB_ERR_SHAPE, "K must be a positive multiple of 16");
@@ -1731,8 +1748,9 @@ cb_status cb_blend_prefill(cb_ctx* ctx, const cb_request* reqs, int n_req, const
 }
 
 // ----------------------------------------------------------------------------- decode
-cb_status cb_decode_step(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, const int32_t* tokens,
-                         int32_t* out_tokens, void* stream) {
+// uniform NULL: the largest logit's token, else drawn (params may be NULL)
+static cb_status decode_step(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, const int32_t* tokens,
+                             const cb_sampling* params, const float* uniform, int32_t* out_tokens, void* stream) {
   if (!ctx || !seqs || !tokens || !out_tokens || n_seq < 1) return fail(ctx, CB_ERR_INVALID_ARG, "bad decode arguments");
   if (!ctx->ws) return fail(ctx, CB_ERR_WORKSPACE, "no workspace bound");
   if (ctx->b.active) return fail(ctx, CB_ERR_STATE, "a blend batch is active (finish it first)");
@@ -1829,12 +1847,30 @@ cb_status cb_decode_step(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, cons
     PhaseScope ps(ctx, CB_PH_FINISH, s, 2 + (n_seq + 15) / 16);
     CB_CUDA(ctx, launch_last_rows_norm(h, d_rows, n_seq, d, c.rms_eps, ctx->xlast, s));
     CB_CUDA(ctx, launch_lm_head(ctx->xlast, n_seq, d, ctx->lm, c.vocab, c.dtype, ctx->logits, s));
-    CB_CUDA(ctx, launch_argmax(ctx->logits, n_seq, c.vocab, nullptr, out_tokens, s));
+    if (uniform) {
+      const cb_sampling f = params ? *params : cb_sampling{};
+      CB_CUDA(ctx, launch_sample(ctx->logits, c.vocab, CB_F32, n_seq, c.vocab, f.temperature, f.top_k, f.top_p, f.min_p,
+                                 uniform, out_tokens, s));
+    } else {
+      CB_CUDA(ctx, launch_argmax(ctx->logits, n_seq, c.vocab, nullptr, out_tokens, s));
+    }
   }
   for (int i = 0; i < n_seq; ++i)
     if (seqs[i].out_hidden)
       CB_CUDA(ctx, cudaMemcpyAsync(seqs[i].out_hidden, h + static_cast<size_t>(i) * d, d * 4, cudaMemcpyDeviceToDevice, s));
   return CB_OK;
+}
+
+cb_status cb_decode_step(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, const int32_t* tokens,
+                         int32_t* out_tokens, void* stream) {
+  return decode_step(ctx, seqs, n_seq, tokens, nullptr, nullptr, out_tokens, stream);
+}
+
+cb_status cb_decode_step_sample(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, const int32_t* tokens,
+                                const cb_sampling* params, const float* uniform, int32_t* out_tokens, void* stream) {
+  if (!ctx || !uniform) return fail(ctx, CB_ERR_INVALID_ARG, "bad decode arguments");
+  if (ctx->cfg.vocab > SAMPLE_MAX_VOCAB) return fail(ctx, CB_ERR_SHAPE, "sampling takes up to 2^18 logits a row");
+  return decode_step(ctx, seqs, n_seq, tokens, params, uniform, out_tokens, stream);
 }
 
 cb_status cb_full_prefill(cb_ctx* ctx, const int32_t* ids, int n, void* k_out, void* v_out, float* out_hidden,

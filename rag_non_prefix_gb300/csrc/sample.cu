@@ -1,0 +1,556 @@
+// Tokens drawn from rows of logits with temperature, top-k, top-p and min-p, from given random numbers.
+//
+//   w_i = exp((x_i - max) / t); tokens stand by falling x, equal ones by rising index.  Every filter keeps a prefix of that
+//   order: the first k; of those the shortest whose mass reaches p times theirs; those with w >= min_p.  The
+//   token is the first whose running kept mass exceeds u times the kept mass.
+// So a filter and the draw are the same question, "at which token does the running count or mass reach a
+// target", answered exactly: weights are whole numbers of 2^-44 (a weight's relative error is near
+// 2^-30: the exponent (x - max) / t log2(e) is carried in two fp32 numbers), and sums of whole numbers do not depend on their order.
+//
+// A row is held in the shared memory of the 1 to 8 CTAs of a cluster, read from memory once.  The running sums come
+// from a histogram of the counts or masses of 2048 ranges of (max - x) / t (a falling function of x); the
+// target's range is cut further by the bits of x and of the index while it holds more tokens than LIST,
+// then its tokens are sorted and summed one by one.  With top-k up to LIST tokens the mass is a matter of those
+// alone.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace cb {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int ST = 1024;     // threads
+constexpr int LIST = 1024;   // tokens that are sorted
+constexpr int BUCKETS = 2048;
+constexpr float REACH = 32.f;  // of (max - x) / t: exp(-31.98) is less than half of 2^-44, weight 0
+constexpr int SHIFT = 44;      // the largest weight is 2^SHIFT
+typedef unsigned long long u64;
+
+// 2^30 2^(j / 32)
+__constant__ uint32_t kExp2[32] = {
+    1073741824u, 1097253708u, 1121280436u, 1145833280u, 1170923762u, 1196563654u, 1222764986u, 1249540052u,
+    1276901417u, 1304861917u, 1333434672u, 1362633090u, 1392470869u, 1422962010u, 1454120821u, 1485961921u,
+    1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u, 1729250827u, 1767116489u,
+    1805811301u, 1845353420u, 1885761398u, 1927054196u, 1969251188u, 2012372174u, 2056437387u, 2101467502u};
+
+struct SampleArgs {
+  const void* logits;
+  long long ld;
+  int vocab;
+  const float *temperature, *top_p, *min_p, *uniform;
+  const int32_t* top_k;
+  int32_t* out;
+  int chunk;  // tokens per CTA
+};
+
+// What the cluster's first CTA decides for all of them.
+struct Ctl {
+  int bucket;   // of the level just looked at
+  int count;    // tokens in it
+  u64 excl;     // sum before the bucket
+  u64 comp;     // the token found
+  u64 incl;     // sum up to and with it
+};
+
+struct __align__(16) Smem {
+  uint32_t hist[3][BUCKETS];
+  u64 tot[BUCKETS];  // first CTA: inclusive sums
+  u64 list[LIST];
+  u64 scan[LIST];
+  u64 warp[32];
+  u64 part[4];  // this CTA's: best token, mass over min_p, number of finite logits
+  Ctl ctl[2];
+  int n_list;
+};
+
+// order of the tokens as one number: by logit, then the lower index first
+__device__ __forceinline__ u64 composite(float x, int idx) {
+  uint32_t u = __float_as_uint(x + 0.f);  // (-0 is 0)
+  u = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return static_cast<u64>(u) << 32 | (0xffffffffu - static_cast<uint32_t>(idx));
+}
+__device__ __forceinline__ float logit_of(u64 comp) {
+  const uint32_t u = static_cast<uint32_t>(comp >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ int index_of(u64 comp) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(comp)); }
+
+__device__ __forceinline__ u64 warp_max64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T> struct Sampler {
+  static constexpr int VEC = 16 / sizeof(T);
+
+  const SampleArgs& a;
+  Smem& s;
+  const T* data;  // this CTA's tokens in shared memory, 16-byte vectors; what is not a token is -infinity
+  int n_vec, first;  // vectors; index of the first vector's first element
+  cg::cluster_group cl;
+  int rank, ranks, tid, lane, warp;
+  int phase = 0;
+  // row
+  float top, c_hi, c_lo, reach;  // largest logit, log2(e) / t in two parts, buckets per unit of max - x
+  uint32_t tab;
+  u64 floor_w = 0;  // min_p's weight
+  u64 eligible = 0; // composite of the last token that top-k keeps
+
+  __device__ Sampler(const SampleArgs& args, Smem& sm) : a(args), s(sm), cl(cg::this_cluster()) {
+    rank = cl.block_rank();
+    ranks = cl.num_blocks();
+    tid = threadIdx.x;
+    lane = tid & 31;
+    warp = tid >> 5;
+    tab = kExp2[lane];
+  }
+
+  // Weight of a token, 2^SHIFT for the largest.  All lanes of a warp take part.
+  __device__ __forceinline__ u64 weight(float x) const {
+    const float d = x == top ? 0.f : x - top;
+    // the difference's own rounding (two-sum), then the exponent in two parts
+    const float b = d - x, de = (x - (d - b)) + (-top - b);
+    float e = d * c_hi;
+    const float el = fmaf(d, c_hi, -e) + fmaf(d, c_lo, (x == top ? 0.f : de) * c_hi);
+    const bool some = e > -46.f;
+    e = some ? e : 0.f;
+    // e = k / 32 + r: 2^(k / 32) from the table, 2^r - 1 by its series (|r ln 2| < 0.011: terms to the fourth)
+    const float km = fmaf(e, 32.f, 12582912.f);
+    const int k = __float_as_int(km) - 0x4b400000;
+    const float r = fmaf(km - 12582912.f, -0.03125f, e) + (some ? el : 0.f);
+    const float y = fmaf(r, 0.693147182f, r * -1.90465421e-9f);
+    const float p = fmaf(y * y, fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f), y);
+    const int t = static_cast<int>(__shfl_sync(0xffffffffu, tab, k & 31));
+    const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, __float2int_rn(p * 4294967296.f)));
+    return some ? (static_cast<u64>(m) << (SHIFT - 30)) >> -(k >> 5) : 0;
+  }
+  __device__ __forceinline__ int bucket0(float x) const {
+    return x == top ? 0 : min(BUCKETS - 1, static_cast<int>((top - x) * reach));
+  }
+
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    // (whole warps walk together: f may use warp-wide operations)
+    for (int v0 = warp * 32; v0 < n_vec; v0 += ST) {
+      const int v = v0 + lane;
+      T e[VEC];
+      if (v < n_vec)
+        *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(data)[v];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float x = v < n_vec ? to_f(e[i]) : -INFINITY;
+        f(x != x ? -INFINITY : x, first + v * VEC + i);
+      }
+    }
+  }
+
+  __device__ __forceinline__ Ctl decide() {  // what the first CTA wrote into ctl[phase], for everyone
+    cl.sync();
+    const Ctl c = *cl.map_shared_rank(&s.ctl[phase], 0);
+    phase ^= 1;
+    return c;
+  }
+
+  // Histogram over the cluster: tokens for which bucket() is not negative, by count or mass; the first CTA gets the
+  // inclusive sums in tot.
+  template <bool MASS, typename B> __device__ __forceinline__ void histogram(B bucket) {
+    for (int i = tid; i < BUCKETS * (MASS ? 3 : 1); i += ST) s.hist[0][i] = 0;
+    __syncthreads();
+    u64 over = 0;
+    each([&](float x, int idx) {
+      const int b = x > -INFINITY ? bucket(x, idx) : -1;
+      // tokens of one value come in crowds (bf16, flat rows): one lane adds for a warp that agrees
+      const u64 w = MASS ? weight(x) : 1;
+      const bool add = b >= 0 && w > 0;
+      if (MASS && add && w >= floor_w) over += w;
+      const unsigned who = __ballot_sync(0xffffffffu, add);
+      if (who == 0) return;
+      const int b0 = __shfl_sync(0xffffffffu, b, __ffs(who) - 1);
+      if (__all_sync(0xffffffffu, !add || b == b0)) {
+        if (MASS) {
+          const uint32_t p0 = __reduce_add_sync(0xffffffffu, add ? static_cast<uint32_t>(w) & 0x7fffu : 0u);
+          const uint32_t p1 = __reduce_add_sync(0xffffffffu, add ? static_cast<uint32_t>(w >> 15) & 0x7fffu : 0u);
+          const uint32_t p2 = __reduce_add_sync(0xffffffffu, add ? static_cast<uint32_t>(w >> 30) : 0u);
+          if (lane == 0) {
+            atomicAdd(&s.hist[0][b0], p0);
+            atomicAdd(&s.hist[1][b0], p1);
+            atomicAdd(&s.hist[2][b0], p2);
+          }
+        } else if (lane == 0) {
+          atomicAdd(&s.hist[0][b0], static_cast<uint32_t>(__popc(who)));
+        }
+      } else if (add) {
+        if (MASS) {
+          atomicAdd(&s.hist[0][b], static_cast<uint32_t>(w) & 0x7fffu);
+          atomicAdd(&s.hist[1][b], static_cast<uint32_t>(w >> 15) & 0x7fffu);
+          if (w >> 30) atomicAdd(&s.hist[2][b], static_cast<uint32_t>(w >> 30));
+        } else {
+          atomicAdd(&s.hist[0][b], 1u);
+        }
+      }
+    });
+    if (MASS) {
+      over = warp_sum64(over);
+      if (lane == 0) s.warp[warp] = over;
+      __syncthreads();
+      if (warp == 0) {
+        over = warp_sum64(s.warp[lane]);
+        if (lane == 0) s.part[1] = over;
+      }
+    }
+    cl.sync();
+    // each CTA sums a slice of the buckets over the cluster
+    const int slice = BUCKETS / ranks;
+    u64* tot = cl.map_shared_rank(s.tot, 0);
+    for (int i = rank * slice + tid; i < (rank + 1) * slice; i += ST) {
+      u64 sum = 0;
+      for (int r = 0; r < ranks; ++r) {
+        const uint32_t* h = cl.map_shared_rank(&s.hist[0][0], r);
+        sum += h[i];
+        if (MASS) sum += (static_cast<u64>(h[BUCKETS + i]) << 15) + (static_cast<u64>(h[2 * BUCKETS + i]) << 30);
+      }
+      tot[i] = sum;
+    }
+    cl.sync();
+    if (rank == 0) {
+      u64 x[2] = {s.tot[2 * tid], s.tot[2 * tid + 1]};
+      x[1] += x[0];
+      const u64 before = block_scan(x[1]) - x[1];
+      __syncthreads();
+      s.tot[2 * tid] = x[0] + before;
+      s.tot[2 * tid + 1] = x[1] + before;
+      __syncthreads();
+    }
+  }
+
+  __device__ __forceinline__ u64 block_scan(u64 v) {  // inclusive, one value a thread
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) s.warp[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      u64 w = s.warp[lane], own = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      s.warp[lane] = w - own;
+    }
+    __syncthreads();
+    return v + s.warp[warp];
+  }
+
+  // first CTA: the bucket in which the running sum reaches target
+  __device__ __forceinline__ void find_bucket(u64 target) {
+    for (int b = tid; b < BUCKETS; b += ST) {
+      const u64 incl = s.tot[b], excl = b ? s.tot[b - 1] : 0;
+      if (excl < target && target <= incl) {
+        s.ctl[phase].bucket = b;
+        s.ctl[phase].excl = excl;
+      }
+    }
+  }
+
+  // The tokens for which take() holds into the first CTA's list; their number for everyone.
+  template <typename P> __device__ __forceinline__ int gather(P take) {
+    if (tid == 0) s.n_list = 0;
+    cl.sync();
+    int* n = cl.map_shared_rank(&s.n_list, 0);
+    u64* list = cl.map_shared_rank(s.list, 0);
+    each([&](float x, int idx) {
+      const bool t = x > -INFINITY && take(x, idx);
+      const unsigned who = __ballot_sync(0xffffffffu, t);
+      if (who == 0) return;
+      int at = 0;
+      if (lane == 0) at = atomicAdd(n, __popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+      if (t && at < LIST) list[at] = composite(x, idx);
+    });
+    cl.sync();
+    return *n;
+  }
+
+  // first CTA: sorts its list, largest first; thread i gets the i-th token, 0 beyond n
+  __device__ __forceinline__ u64 sorted(int n) {
+    u64 v = tid < n ? s.list[tid] : 0;
+    int size = 32;
+    while (size < n) size <<= 1;
+    for (int k = 2; k <= size; k <<= 1) {
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        u64 o;
+        if (j >= 32) {
+          __syncthreads();
+          s.list[tid] = v;
+          __syncthreads();
+          o = s.list[tid ^ j];
+        } else {
+          o = __shfl_xor_sync(0xffffffffu, v, j);
+        }
+        const bool keep_max = ((tid & k) == 0) == ((tid & j) == 0);
+        v = keep_max ? max(v, o) : min(v, o);
+      }
+    }
+    return v;
+  }
+
+  // Token at which the running count (of live tokens) or mass reaches target, from the histogram in tot (first CTA) of
+  // bucket0; all CTAs return it, and the sum up to and with it.  LIVE: whether a token counts.
+  template <bool MASS, typename L> __device__ __forceinline__ Ctl select(u64 target, L live, bool* refined) {
+    if (rank == 0) find_bucket(target);
+    Ctl c = decide();
+    const int b0 = c.bucket;
+    u64 excl = c.excl;
+    // the tokens still in question agree in bucket0 and in the leading bits of their composite
+    int bits = 0;
+    u64 lead = 0;
+    for (;;) {
+      auto in = [&](float x, int idx) {
+        return live(x, idx) && bucket0(x) == b0 && (bits == 0 || composite(x, idx) >> (64 - bits) == lead);
+      };
+      const int n = gather(in);
+      if (n <= LIST) {
+        if (rank == 0) {
+          const u64 t = sorted(n);
+          const u64 mine = MASS ? weight(logit_of(t)) : 1;  // (all lanes)
+          const u64 w = tid < n ? mine : 0;
+          const u64 incl = excl + block_scan(w);
+          if (tid < n && (incl - w < target && target <= incl)) {
+            s.ctl[phase].comp = t;
+            s.ctl[phase].incl = incl;
+          }
+          __syncthreads();
+        }
+        return decide();
+      }
+      *refined = true;
+      // the next bits: 8 of the logit at a time, then the upper 11 of the index's 18 (the 14 before them are ones)
+      const int step = bits < 32 ? 8 : 11, at = bits < 32 ? bits : 46;
+      histogram<MASS>([&](float x, int idx) {
+        const u64 comp = composite(x, idx);
+        return in(x, idx) ? static_cast<int>((1u << step) - 1 - (static_cast<uint32_t>(comp >> (64 - at - step)) & ((1u << step) - 1))) : -1;
+      });
+      if (rank == 0) find_bucket(target - excl);
+      c = decide();
+      excl += c.excl;
+      const u64 digit = static_cast<u64>((1 << step) - 1 - c.bucket);
+      if (bits == 32) lead = lead << 14 | 0x3fff;
+      lead = lead << step | digit;
+      bits = at + step;
+    }
+  }
+};
+
+template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(SampleArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem& s = *reinterpret_cast<Smem*>(raw);
+  T* data = reinterpret_cast<T*>(raw + sizeof(Smem));
+  Sampler<T> z(a, s);
+  constexpr int VEC = Sampler<T>::VEC;
+  const int row = blockIdx.x / z.ranks, tid = z.tid, lane = z.lane, warp = z.warp;
+  const int i0 = min(a.vocab, z.rank * a.chunk), i1 = min(a.vocab, i0 + a.chunk);
+  const T* src = static_cast<const T*>(a.logits) + static_cast<long long>(row) * a.ld + i0;
+  // vectors as they lie in memory: those at the ends may hold a neighbour's elements
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T), n = i1 - i0;
+  z.data = data;
+  z.n_vec = n > 0 ? (off + n + VEC - 1) / VEC : 0;
+  z.first = i0 - off;
+  u64 best = 0;
+  for (int v = tid; v < z.n_vec; v += ST) {
+    T e[VEC];
+    const int at = v * VEC - off;
+    if (at >= 0 && at + VEC <= n) {
+      *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(src + at));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = at + i >= 0 && at + i < n ? src[at + i] : from_f<T>(-INFINITY);
+    }
+    reinterpret_cast<uint4*>(data)[v] = *reinterpret_cast<const uint4*>(e);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float x = to_f(e[i]);
+      if (x > -INFINITY) best = max(best, composite(x, i0 + at + i));
+    }
+  }
+  best = warp_max64(best);
+  if (lane == 0) s.warp[warp] = best;
+  __syncthreads();
+  if (warp == 0) {
+    best = warp_max64(s.warp[lane]);
+    if (lane == 0) s.part[0] = best;
+  }
+  z.cl.sync();
+  best = 0;
+  for (int r = 0; r < z.ranks; ++r) best = max(best, *z.cl.map_shared_rank(&s.part[0], r));
+
+  float t = a.temperature ? a.temperature[row] : 1.f;
+  int k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
+  const float u = a.uniform ? a.uniform[row] : 0.f;
+  if (!(t > 0.f)) k = 1;
+  if (k <= 0 || k >= a.vocab) k = a.vocab;
+  auto finish = [&](u64 comp) {
+    if (z.rank == 0 && tid == 0) a.out[row] = comp == 0 ? -1 : index_of(comp);
+    z.cl.sync();  // (no CTA leaves while another reads its shared memory)
+  };
+  if (best == 0 || k == 1) return finish(best);
+
+  t = fminf(fmaxf(t, 1e-20f), 1e20f);
+  const double c = 1.4426950408889634 / static_cast<double>(t);
+  z.top = logit_of(best);
+  z.c_hi = static_cast<float>(c);
+  z.c_lo = static_cast<float>(c - static_cast<double>(z.c_hi));
+  z.reach = BUCKETS / REACH / t;
+  const u64 one = 1ull << SHIFT;
+  z.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
+  // targets of a mass m: the smallest whole numbers not below top_p m, and above u m
+  auto reach_p = [&](u64 m) {
+    return top_p >= 1.f || !(top_p == top_p) ? m : max(1ull, min(m, static_cast<u64>(ceil(fmax(0.0, static_cast<double>(top_p) * static_cast<double>(m))))));
+  };
+  auto reach_u = [&](u64 m) {
+    return min(m, static_cast<u64>(fmax(0.0, static_cast<double>(u) * static_cast<double>(m))) + 1);
+  };
+
+  bool refined = false;
+  auto all = [](float, int) { return true; };
+  if (k < a.vocab) {
+    z.template histogram<false>([&](float x, int) { return z.bucket0(x); });
+    // the bucket of the k-th token; the last one's tokens weigh nothing
+    if (z.rank == 0) {
+      if (tid == 0) {
+        s.ctl[z.phase].bucket = BUCKETS - 1;
+        s.ctl[z.phase].excl = 0;
+      }
+      __syncthreads();
+      for (int b = tid; b < BUCKETS - 1; b += ST) {
+        const u64 incl = s.tot[b], excl = b ? s.tot[b - 1] : 0;
+        if (excl < static_cast<u64>(k) && static_cast<u64>(k) <= incl) {
+          s.ctl[z.phase].bucket = b;
+          s.ctl[z.phase].count = static_cast<int>(min(incl, static_cast<u64>(a.vocab)));
+        }
+      }
+      __syncthreads();
+    }
+    const Ctl ctl = z.decide();
+    if (ctl.bucket < BUCKETS - 1) {
+      const int b = ctl.bucket;
+      int n = ctl.count;
+      u64 last = 0;
+      if (k > LIST || n > LIST) {
+        last = z.template select<false>(k, all, &refined).comp;
+        n = k;
+      }
+      if (n <= LIST) {  // top-k's tokens (and the rest of their last bucket) fit: the first CTA has all that counts
+        z.gather([&](float x, int idx) { return last ? composite(x, idx) >= last : z.bucket0(x) <= b; });
+        if (z.rank == 0) {
+          const u64 tok = z.sorted(n);
+          const u64 w = z.weight(logit_of(tok));  // (all lanes)
+          const u64 mine = tid < k && tid < n ? w : 0;
+          s.scan[tid] = z.block_scan(mine);
+          __syncthreads();
+          const u64 pm = reach_p(s.scan[ST - 1]);
+          // kept mass: of the shorter prefix
+          const u64 over = z.block_scan(mine >= z.floor_w ? mine : 0);
+          if (tid == ST - 1) s.part[1] = over;
+          const u64 incl = s.scan[tid];
+          if (mine && incl - mine < pm && pm <= incl) s.part[2] = incl;
+          __syncthreads();
+          const u64 want = reach_u(min(s.part[1], s.part[2]));
+          if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
+        }
+        z.cl.sync();
+        return;
+      }
+      z.eligible = last;
+    }
+  }
+
+  const u64 eligible = z.eligible;
+  auto live = [&](float x, int idx) { return eligible == 0 || composite(x, idx) >= eligible; };
+  auto masses = [&] { z.template histogram<true>([&](float x, int idx) { return live(x, idx) ? z.bucket0(x) : -1; }); };
+  masses();
+  if (z.rank == 0 && tid == 0) {
+    u64 over = 0;
+    for (int r = 0; r < z.ranks; ++r) over += *z.cl.map_shared_rank(&s.part[1], r);
+    s.ctl[z.phase].excl = s.tot[BUCKETS - 1];
+    s.ctl[z.phase].incl = over;
+  }
+  const Ctl sums = z.decide();
+  u64 mass = sums.incl;  // what min_p keeps
+  const u64 pm = reach_p(sums.excl);
+  if (pm <= mass && pm < sums.excl) {  // top_p keeps less
+    refined = false;
+    mass = z.template select<true>(pm, live, &refined).incl;
+    if (refined) masses();
+  }
+  const u64 comp = z.template select<true>(reach_u(mass), live, &refined).comp;
+  finish(comp);
+}
+
+template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  static DeviceOnce configured;
+  constexpr int MAX_DATA = 128 << 10;
+  if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>),
+                                 static_cast<int>(sizeof(Smem)) + MAX_DATA + 48, configured)) != cudaSuccess)
+    return e;
+  // CTAs of a row: as many as its size needs, and more while the rows leave SMs idle
+  int ranks = 1;
+  auto chunk = [&](int r) { return (a.vocab + r - 1) / r; };
+  while (ranks < 8 && (chunk(ranks) * sizeof(T) > MAX_DATA || (rows * ranks < sms && chunk(ranks) > 4096))) ranks *= 2;
+  a.chunk = chunk(ranks);
+  const size_t smem = sizeof(Smem) + (a.chunk * sizeof(T) + 47) / 16 * 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * ranks);
+  cfg.blockDim = dim3(ST);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = launch_overlap_enabled() ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const void* logits, long long ld, cb_dtype dt, int rows, int vocab, const float* temperature,
+                          const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, int32_t* out,
+                          cudaStream_t s) {
+  SampleArgs a = {};
+  a.logits = logits;
+  a.ld = ld;
+  a.vocab = vocab;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.uniform = uniform;
+  a.out = out;
+  return dt == CB_BF16 ? launch<bf16>(a, rows, s) : launch<float>(a, rows, s);
+}
+
+}  // namespace cb
