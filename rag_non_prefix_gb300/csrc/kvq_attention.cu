@@ -3,11 +3,14 @@
 //   out = sum_j softmax_j(scale q . k_j) v_j,  j <= the query's position
 //   q . k     = sum_g scale_g (sum_c q_c code_c + zero_g sum_c q_c)
 //   sum p v_c = sum_j (p_j scale_jg) (code_jc + zero_jg)
-// The codes enter the tensor core as they are, as the bf16 numbers 16 + code (two nibbles of a word become
-// two operands by one shift and one logic operation), so keys and values are never rounded; 16 is taken
-// off with the zero: in the accumulator's start for the keys (zero - 16) sum_c q_c, in a sum of
-// (p scale) (zero - 16) over the keys, kept in fp32, for the values.  p scale is rounded to bf16 (fp32 outputs: to three bf16
-// parts, as are the queries, so that nothing is lost) and the same rounded number multiplies code and zero,
+// The codes enter the tensor core as they are, as the bf16 numbers code - 8 (two nibbles of a word become
+// 16 + code by one shift and one logic operation), so keys and values are never rounded; 8 is taken
+// off with the zero: in the accumulator's start for the keys (zero + 8) sum_c q_c, in a sum of
+// (p scale) (zero + 8) over the keys, kept in fp32, for the values.  (16 + code itself would do, but the sums of values that
+// cancel, over a long context, would be 20 times larger and so would what the accumulator's rounding
+// leaves of them.)  p scale is rounded to bf16 (fp32 outputs: to three bf16
+// parts, as are the queries, so that nothing is lost, and blocks of 16 keys are added in fp32 outside of the tensor
+// core, whose accumulator rounds towards zero) and the same rounded number multiplies code and zero,
 // so its rounding is one of 2^-9 of the value itself.
 //
 // mma.sync m16n8k16 and not tcgen05: 1 to 16 queries share a key, so the products are small beside the
@@ -21,6 +24,7 @@
 // merges the parts in the order of the keys, so results repeat exactly.  In a CTA each of 4 warps takes a block of 16
 // keys of a quantum, through a ring of its own in shared memory; no warp waits for another before the end.
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "kvq.cuh"
@@ -31,6 +35,7 @@ namespace {
 
 constexpr int AW = 4;                    // warps per CTA
 constexpr int QUANTUM = AW * KVQ_BLOCK;  // keys
+constexpr int MIN_SHARE = 4;             // quanta of a CTA, at least, where there are few
 constexpr int MAX_ROWS = 16;             // query rows per tile at most
 constexpr float LAZY = 6.f;              // the running maximum moves once a score passes it by 2^6
 
@@ -69,10 +74,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// 16 + nibbles i and i + 4 of a word as two bf16 (16 is 0x4180, with 3 bits below the units)
+// nibbles i and i + 4 of a word less 8, as two bf16 (16 is 0x4180, with 3 bits below the units; 24 is 0x41c0)
 template <int I> __device__ __forceinline__ uint32_t nibbles(uint32_t x) {
-  const uint32_t y = I == 0 ? x << 3 : x >> (4 * I - 3);
-  return (y & 0x00780078u) | 0x41804180u;
+  const uint32_t y = ((I == 0 ? x << 3 : x >> (4 * I - 3)) & 0x00780078u) | 0x41804180u;
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x41c041c0u));
+  return r;
 }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -108,7 +115,8 @@ template <typename T, int DH, int NT, int NP> struct Attn {
   static constexpr int ROW = DH + 4;  // pitch of the merge buffer, free of bank conflicts
   static constexpr int RING = AW * STAGES * BLK;
   static constexpr int MERGE = AW * R * ROW * 4;
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static constexpr int WEIGHTS = R * KVQ_MAX_CTAS * 4;  // of the parts of a unit
+  static constexpr int SMEM = std::max(std::max(RING, MERGE), WEIGHTS);
 
   uint32_t qb[NT][NP][NG][4];  // query operands: per group two k-steps of (b0, b1)
   float qs[NT][NG][2];         // sums of the query's group, of this lane's two columns
@@ -196,8 +204,8 @@ template <typename T, int DH, int NT, int NP> struct Attn {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const float s0 = g & 1 ? hi_f(ks[0][g / 2]) : lo_f(ks[0][g / 2]), s1 = g & 1 ? hi_f(ks[1][g / 2]) : lo_f(ks[1][g / 2]);
-        const float z0 = (g & 1 ? hi_f(kz[0][g / 2]) : lo_f(kz[0][g / 2])) - 16.f;
-        const float z1 = (g & 1 ? hi_f(kz[1][g / 2]) : lo_f(kz[1][g / 2])) - 16.f;
+        const float z0 = (g & 1 ? hi_f(kz[0][g / 2]) : lo_f(kz[0][g / 2])) + 8.f;
+        const float z1 = (g & 1 ? hi_f(kz[1][g / 2]) : lo_f(kz[1][g / 2])) + 8.f;
         const uint32_t a0 = nibbles<0>(w[0][g]), a1 = nibbles<0>(w[1][g]), a2 = nibbles<1>(w[0][g]), a3 = nibbles<1>(w[1][g]);
         const uint32_t b0 = nibbles<2>(w[0][g]), b1 = nibbles<2>(w[1][g]), b2 = nibbles<3>(w[0][g]), b3 = nibbles<3>(w[1][g]);
 #pragma unroll
@@ -272,8 +280,8 @@ template <typename T, int DH, int NT, int NP> struct Attn {
       for (int gg = 0; gg < 2; ++gg) {
         const int g = 2 * half + gg;
         const float s0 = gg ? hi_f(vs[0][half]) : lo_f(vs[0][half]), s1 = gg ? hi_f(vs[1][half]) : lo_f(vs[1][half]);
-        const float z0 = (gg ? hi_f(vz[0][half]) : lo_f(vz[0][half])) - 16.f;
-        const float z1 = (gg ? hi_f(vz[1][half]) : lo_f(vz[1][half])) - 16.f;
+        const float z0 = (gg ? hi_f(vz[0][half]) : lo_f(vz[0][half])) + 8.f;
+        const float z1 = (gg ? hi_f(vz[1][half]) : lo_f(vz[1][half])) + 8.f;
         uint32_t pb[NT][NP][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -306,9 +314,17 @@ template <typename T, int DH, int NT, int NP> struct Attn {
           const uint32_t x = w[2 * gg + jj];
           const uint32_t a0 = nibbles<0>(x), a1 = nibbles<1>(x), a2 = nibbles<2>(x), a3 = nibbles<3>(x);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            if (NP == 1) {
+              mma_bf16(o[nt][2 * g + jj], a0, a1, a2, a3, pb[nt][0][0], pb[nt][0][1]);
+            } else {
+              float c[4] = {};
 #pragma unroll
-            for (int np = 0; np < NP; ++np) mma_bf16(o[nt][2 * g + jj], a0, a1, a2, a3, pb[nt][np][0], pb[nt][np][1]);
+              for (int np = NP - 1; np >= 0; --np) mma_bf16(c, a0, a1, a2, a3, pb[nt][np][0], pb[nt][np][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[nt][2 * g + jj][i] += c[i];
+            }
+          }
         }
       }
     }
@@ -370,7 +386,7 @@ __global__ void __launch_bounds__(AW * 32) kvq_attention_kernel(const __grid_con
   }
   __syncthreads();
   const long long total = scan[AW * 32];
-  const long long n = min(static_cast<long long>(gridDim.x), total);
+  const long long n = min(static_cast<long long>(gridDim.x), (total + MIN_SHARE - 1) / MIN_SHARE);
   if (blockIdx.x >= n) return;
   long long cur = total * blockIdx.x / n;
   const long long end = total * (blockIdx.x + 1) / n;
@@ -511,26 +527,47 @@ __global__ void __launch_bounds__(AW * 32) kvq_attention_kernel(const __grid_con
       if (is_last) {
         __threadfence();
         if (tid == 0) p.counters[c0] = 0;
-        const size_t first = 2 * static_cast<size_t>(c0) + (unit != total * c0 / n);
-        for (int i = tid; i < R * DH; i += AW * 32) {
-          const int row = i / DH, ch = i - row * DH, gr = r0 + row;
-          if (gr >= rows) break;
-          float M = -INFINITY, L = 0.f, x = 0.f;
-          for (int c = c0; c <= c1; ++c)
-            M = fmaxf(M, __ldcg(p.parts + (c == c0 ? first : 2 * static_cast<size_t>(c)) * slot_floats(DH) + MAX_ROWS * DH + 2 * row));
-          for (int c = c0; c <= c1; ++c) {
-            const float* s = p.parts + (c == c0 ? first : 2 * static_cast<size_t>(c)) * slot_floats(DH);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + MAX_ROWS * DH + 2 * row));
-            const float wt = part_weight(ml.x, ml.y, M);
-            if (wt != 0.f) {
-              L = fmaf(wt, ml.y, L);
-              x = fmaf(wt, __ldcg(s + row * DH + ch), x);
-            }
+        // parts c0..c1: the first in its CTA's first or later slot, the others in their CTA's first; a warp's row
+        // at a time, four channels a lane
+        const float* parts = p.parts + 2 * static_cast<size_t>(c0) * slot_floats(DH);
+        const int shift = unit != total * c0 / n ? slot_floats(DH) : 0, np = c1 - c0 + 1;
+        float* wt = reinterpret_cast<float*>(smem) + w * (A::WEIGHTS / 4 / AW);
+        for (int row = w; row < R && r0 + row < rows; row += AW) {
+          float M = -INFINITY, L = 0.f;
+          for (int c = lane; c < np; c += 32)
+            M = fmaxf(M, __ldcg(parts + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift) + MAX_ROWS * DH + 2 * row));
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+          for (int c = lane; c < np; c += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(
+                parts + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift) + MAX_ROWS * DH + 2 * row));
+            const float x = part_weight(ml.x, ml.y, M);
+            wt[c] = x;
+            if (x != 0.f) L = fmaf(x, ml.y, L);
           }
-          const int t = gr / p.G;
-          static_cast<T*>(p.out)[(static_cast<long long>(seq) * p.T + t) * p.ldo +
-                                 static_cast<long long>(head * p.G + gr - t * p.G) * DH + ch] =
-              from_f<T>(L == 0.f ? 0.f : x / L);
+          L = warp_sum(L);
+          __syncwarp();
+          constexpr int CH = DH / 32;  // channels a lane
+          float x[CH] = {};
+          const float* src = parts + row * DH + lane * CH;
+#pragma unroll 8
+          for (int c = 0; c < np; ++c) {
+            const float f = wt[c];
+            float v[CH];
+            const float* at = src + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift);
+            if (CH == 4)
+              *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(at));
+            else
+              *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(at));
+#pragma unroll
+            for (int i = 0; i < CH; ++i) x[i] = f != 0.f ? fmaf(f, v[i], x[i]) : x[i];
+          }
+          __syncwarp();
+          const int gr = r0 + row, t = gr / p.G;
+          T* dst = static_cast<T*>(p.out) + (static_cast<long long>(seq) * p.T + t) * p.ldo +
+                   static_cast<long long>(head * p.G + gr - t * p.G) * DH + lane * CH;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) dst[i] = from_f<T>(L == 0.f ? 0.f : x[i] / L);
         }
       }
     }
@@ -551,10 +588,18 @@ cudaError_t launch(KvqAttn p, cudaStream_t s) {
   static DeviceOnce configured;
   cudaError_t e = max_dynamic_smem_once(reinterpret_cast<const void*>(kvq_attention_kernel<T, DH, NT, NP>), A::SMEM, configured);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int grid = std::min(KVQ_MAX_CTAS, 3 * sms);
+  // as many CTAs as fit at once
+  static std::atomic<int> fits{0};
+  int grid = fits.load(std::memory_order_relaxed);
+  if (grid == 0) {
+    int dev = 0, sms = 0, per_sm = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kvq_attention_kernel<T, DH, NT, NP>, AW * 32, A::SMEM)) != cudaSuccess)
+      return e;
+    grid = std::min(KVQ_MAX_CTAS, std::max(1, per_sm) * sms);
+    fits.store(grid, std::memory_order_relaxed);
+  }
   return launch_chain(kvq_attention_kernel<T, DH, NT, NP>, dim3(grid), dim3(AW * 32), A::SMEM, s, p);
 }
 
