@@ -3,15 +3,15 @@
 //   out = sum_j softmax_j(scale q . k_j) v_j,  j <= the query's position
 //   q . k     = sum_g scale_g (sum_c q_c code_c + zero_g sum_c q_c)
 //   sum p v_c = sum_j (p_j scale_jg) (code_jc + zero_jg)
-// The codes enter the tensor core as they are, as the bf16 numbers code - 8 (two nibbles of a word become
-// 16 + code by one shift and one logic operation), so keys and values are never rounded; 8 is taken
-// off with the zero: in the accumulator's start for the keys (zero + 8) sum_c q_c, in a sum of
-// (p scale) (zero + 8) over the keys, kept in fp32, for the values.  (16 + code itself would do, but the sums of values that
-// cancel, over a long context, would be 20 times larger and so would what the accumulator's rounding
-// leaves of them.)  p scale is rounded to bf16 (fp32 outputs: to three bf16
-// parts, as are the queries, so that nothing is lost, and blocks of 16 keys are added in fp32 outside of the tensor
-// core, whose accumulator rounds towards zero) and the same rounded number multiplies code and zero,
-// so its rounding is one of 2^-9 of the value itself.
+// The codes enter the tensor core as they are, as the bf16 numbers 16 + code (two nibbles of a word become
+// two operands by one shift and one logic operation), so keys and values are never rounded.  Keys: the accumulator
+// starts at (zero - 16) sum_c q_c.  Values: two more products with the operands zero and -16 (both exact in bf16)
+// go into the same accumulator, which so holds the true sums; kept apart, the sums of code and zero of a long
+// context would be hundreds of times larger than the result, and so what the accumulator's rounding towards zero leaves of
+// them.  p scale is rounded to bf16, and the same rounded number multiplies code and zero, so its rounding is one of 2^-9
+// of the value itself.  fp32 outputs: queries and p scale enter as three bf16 parts each, so that nothing is
+// lost, with code - 8 as the operand, the zeros' part in fp32 arithmetic, and blocks of 16 keys added in fp32 outside of
+// the tensor core.
 //
 // mma.sync m16n8k16 and not tcgen05: 1 to 16 queries share a key, so the products are small beside the
 // cache's bytes and the operands go from the cache to registers without a rearrangement.  Keys (scores) and channels (values) lie on the 16
@@ -33,9 +33,11 @@ namespace cb {
 
 namespace {
 
+typedef unsigned long long u64;
 constexpr int AW = 4;                    // warps per CTA
 constexpr int QUANTUM = AW * KVQ_BLOCK;  // keys
 constexpr int MIN_SHARE = 4;             // quanta of a CTA, at least, where there are few
+constexpr int UNIT_COST = 3;             // what a unit costs beside its quanta (queries, first loads, merging): in quanta, measured
 constexpr int MAX_ROWS = 16;             // query rows per tile at most
 constexpr float LAZY = 6.f;              // the running maximum moves once a score passes it by 2^6
 
@@ -58,14 +60,13 @@ struct KvqAttn {
 
 __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -74,10 +75,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// nibbles i and i + 4 of a word less 8, as two bf16 (16 is 0x4180, with 3 bits below the units; 24 is 0x41c0)
-template <int I> __device__ __forceinline__ uint32_t nibbles(uint32_t x) {
-  const uint32_t y = ((I == 0 ? x << 3 : x >> (4 * I - 3)) & 0x00780078u) | 0x41804180u;
-  uint32_t r;
+// 16 + nibbles i and i + 4 of a word as two bf16 (16 is 0x4180, with 3 bits below the units); CENTRED: less 24
+// (both constants in registers: one logic operation)
+template <int I, bool CENTRED> __device__ __forceinline__ uint32_t nibbles(uint32_t x, uint32_t mask, uint32_t sixteen) {
+  uint32_t y, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(I == 0 ? x << 3 : x >> (4 * I - 3)), "r"(mask), "r"(sixteen));
+  if (!CENTRED) return y;
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x41c041c0u));
   return r;
 }
@@ -92,7 +95,7 @@ __device__ __forceinline__ uint32_t split_off(float& x, float& y) {
   return u;
 }
 
-// Quanta of tile `ti` and the number of keys that its rows see.
+// Quanta of a unit of tile `ti`, UNIT_COST without keys first, and the number of keys that its rows see.
 __device__ __forceinline__ int tile_quanta(const KvqAttn& p, int ti, int rows, int& len) {
   const int seq = ti / p.tiles_per_seq, r0 = (ti - seq * p.tiles_per_seq) * rows;
   const int t1 = (min(r0 + rows, p.T * p.G) - 1) / p.G;
@@ -101,7 +104,7 @@ __device__ __forceinline__ int tile_quanta(const KvqAttn& p, int ti, int rows, i
   const int cap = p.c.max_pages * p.c.page_tokens;
   if (top >= cap) set_status(p.status, ST_RANGE);
   len = min(top, cap - 1) + 1;
-  return max(1, (len + QUANTUM - 1) / QUANTUM);
+  return UNIT_COST + (len + QUANTUM - 1) / QUANTUM;
 }
 
 template <int DH> struct Words;  // a lane's key codes of one token: a word per group
@@ -118,15 +121,26 @@ template <typename T, int DH, int NT, int NP> struct Attn {
   static constexpr int WEIGHTS = R * KVQ_MAX_CTAS * 4;  // of the parts of a unit
   static constexpr int SMEM = std::max(std::max(RING, MERGE), WEIGHTS);
 
+  static constexpr bool CENTRED = NP > 1;
+  static constexpr float OFF = CENTRED ? 8.f : -16.f;  // what the operands' offset leaves of a zero
+
+  int lane;
+  uint32_t mask, sixteen, minus16[4];  // (an operand of four registers)
   uint32_t qb[NT][NP][NG][4];  // query operands: per group two k-steps of (b0, b1)
   float qs[NT][NG][2];         // sums of the query's group, of this lane's two columns
   float o[NT][DH / 16][4];
-  float corr[NT][NG][2];
+  float corr[NT][NG][2];  // (fp32) this lane's keys' sums with the zeros
   float m[NT][2], l[NT][2];
   int lim[NT][2];  // last key of this lane's two columns
 
   __device__ __forceinline__ void load_q(const KvqAttn& p, int seq, int r0, int head) {
-    const int lane = threadIdx.x & 31, rr = lane >> 2, tq = lane & 3, rows = p.T * p.G;
+    // read once: the compiler would fetch and rebuild them in every block
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+    asm volatile("mov.u32 %0, 0x00780078;" : "=r"(mask));
+    asm volatile("mov.u32 %0, 0x41804180;" : "=r"(sixteen));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("mov.u32 %0, 0xc180c180;" : "=r"(minus16[i]));
+    const int rr = lane >> 2, tq = lane & 3, rows = p.T * p.G;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = r0 + nt * 8 + rr;
@@ -168,7 +182,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
 
   // the last key that every row of the tile sees
   __device__ __forceinline__ int seen_by_all(const KvqAttn& p, int r0) const {
-    const int tq = threadIdx.x & 3, rows = p.T * p.G;
+    const int tq = lane & 3, rows = p.T * p.G;
     int x = 0x7fffffff;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -179,72 +193,202 @@ template <typename T, int DH, int NT, int NP> struct Attn {
     return min(x, __shfl_xor_sync(0xffffffffu, x, 2));
   }
 
-  // 16 keys from key0 on, their block in shared memory.  MASKED: some row does not see all of them (a key
-  // that a row does not see may hold anything, a NaN scale too, and takes no part).
-  template <bool MASKED> __device__ __forceinline__ void block(const uint8_t* blk, int key0, float scale_log2) {
-    const int lane = threadIdx.x & 31, rr = lane >> 2, tq = lane & 3;
-    float s[NT][4];
+  // Scores (times 1 / scale) of the 16 keys of a block in shared memory: keys rr and rr + 8, columns 2 tq and 2 tq + 1.
+  __device__ __forceinline__ void scores(const uint8_t* blk, float (&s)[NT][4]) const {
+    const int rr = lane >> 2, tq = lane & 3;
+    uint32_t w[2][NG], ks[2][NG / 2], kz[2][NG / 2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < 2; ++h) {
+      typedef typename Words<DH>::type W;
+      *reinterpret_cast<W*>(w[h]) = *reinterpret_cast<const W*>(blk + (rr + 8 * h) * (DH / 2) + tq * 4 * NG);
+      const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 4 * NG * (rr + 8 * h));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-    {
-      uint32_t w[2][NG], ks[2][NG / 2], kz[2][NG / 2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        typedef typename Words<DH>::type W;
-        *reinterpret_cast<W*>(w[h]) = *reinterpret_cast<const W*>(blk + (rr + 8 * h) * (DH / 2) + tq * 4 * NG);
-        const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 4 * NG * (rr + 8 * h));
-#pragma unroll
-        for (int i = 0; i < NG / 2; ++i) {
-          ks[h][i] = prm[i];
-          kz[h][i] = prm[NG / 2 + i];
-        }
+      for (int i = 0; i < NG / 2; ++i) {
+        ks[h][i] = prm[i];
+        kz[h][i] = prm[NG / 2 + i];
       }
+    }
+    // (the groups' products side by side: each waits for the one before it in its own accumulator only)
+    float c[NT][NG][4];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float s0 = g & 1 ? hi_f(ks[0][g / 2]) : lo_f(ks[0][g / 2]), s1 = g & 1 ? hi_f(ks[1][g / 2]) : lo_f(ks[1][g / 2]);
-        const float z0 = (g & 1 ? hi_f(kz[0][g / 2]) : lo_f(kz[0][g / 2])) + 8.f;
-        const float z1 = (g & 1 ? hi_f(kz[1][g / 2]) : lo_f(kz[1][g / 2])) + 8.f;
-        const uint32_t a0 = nibbles<0>(w[0][g]), a1 = nibbles<0>(w[1][g]), a2 = nibbles<1>(w[0][g]), a3 = nibbles<1>(w[1][g]);
-        const uint32_t b0 = nibbles<2>(w[0][g]), b1 = nibbles<2>(w[1][g]), b2 = nibbles<3>(w[0][g]), b3 = nibbles<3>(w[1][g]);
+    for (int g = 0; g < NG; ++g) {
+      const float z0 = (g & 1 ? hi_f(kz[0][g / 2]) : lo_f(kz[0][g / 2])) + OFF;
+      const float z1 = (g & 1 ? hi_f(kz[1][g / 2]) : lo_f(kz[1][g / 2])) + OFF;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float c[4] = {z0 * qs[nt][g][0], z0 * qs[nt][g][1], z1 * qs[nt][g][0], z1 * qs[nt][g][1]};
+      for (int nt = 0; nt < NT; ++nt) {
+        c[nt][g][0] = z0 * qs[nt][g][0];
+        c[nt][g][1] = z0 * qs[nt][g][1];
+        c[nt][g][2] = z1 * qs[nt][g][0];
+        c[nt][g][3] = z1 * qs[nt][g][1];
+      }
+    }
 #pragma unroll
-          for (int np = 0; np < NP; ++np) {
-            mma_bf16(c, a0, a1, a2, a3, qb[nt][np][g][0], qb[nt][np][g][1]);
-            mma_bf16(c, b0, b1, b2, b3, qb[nt][np][g][2], qb[nt][np][g][3]);
+    for (int g = 0; g < NG; ++g) {
+      const uint32_t a0 = nib<0>(w[0][g]), a1 = nib<0>(w[1][g]), a2 = nib<1>(w[0][g]), a3 = nib<1>(w[1][g]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int np = 0; np < NP; ++np) mma_bf16(c[nt][g], a0, a1, a2, a3, qb[nt][np][g][0], qb[nt][np][g][1]);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint32_t a0 = nib<2>(w[0][g]), a1 = nib<2>(w[1][g]), a2 = nib<3>(w[0][g]), a3 = nib<3>(w[1][g]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int np = 0; np < NP; ++np) mma_bf16(c[nt][g], a0, a1, a2, a3, qb[nt][np][g][2], qb[nt][np][g][3]);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float s0 = g & 1 ? hi_f(ks[0][g / 2]) : lo_f(ks[0][g / 2]), s1 = g & 1 ? hi_f(ks[1][g / 2]) : lo_f(ks[1][g / 2]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s[nt][i] = g == 0 ? (i < 2 ? s0 : s1) * c[nt][g][i] : fmaf(i < 2 ? s0 : s1, c[nt][g][i], s[nt][i]);
+    }
+  }
+
+  // Adds the block's values under the weights p (a bit of dead for each that takes no part).
+  template <bool MASKED> __device__ __forceinline__ void values(const uint8_t* blk, const float (&p)[NT][4], uint32_t dead) {
+    const int rr = lane >> 2, tq = lane & 3;
+    const uint8_t* prm = blk + 16 * DH + 64 * NG;  // scales and zeros
+    uint32_t vs[2][NG / 2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i) vs[h][i] = reinterpret_cast<const uint32_t*>(prm + 4 * NG * (rr + 8 * h))[i];
+    // zeros: by this lane's keys rr and rr + 8 (in fp32 arithmetic), or as operands, by the four keys of its columns
+    constexpr bool SIMT = CENTRED || MASKED;
+    constexpr int NZ = SIMT ? 2 : 4;
+    uint32_t vz[NZ][NG / 2];
+#pragma unroll
+    for (int h = 0; h < NZ; ++h)
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i)
+        vz[h][i] = reinterpret_cast<const uint32_t*>(prm + 4 * NG * (SIMT ? rr + 8 * h : 2 * tq + (h & 1) + 4 * (h & 2)))[NG / 2 + i];
+    uint32_t pb[NT][NP][NG][2];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float s0 = g & 1 ? hi_f(vs[0][g / 2]) : lo_f(vs[0][g / 2]), s1 = g & 1 ? hi_f(vs[1][g / 2]) : lo_f(vs[1][g / 2]);
+      const float z0 = (g & 1 ? hi_f(vz[0][g / 2]) : lo_f(vz[0][g / 2])) + (CENTRED ? OFF : 0.f);
+      const float z1 = (g & 1 ? hi_f(vz[1][g / 2]) : lo_f(vz[1][g / 2])) + (CENTRED ? OFF : 0.f);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4] = {p[nt][0] * s0, p[nt][1] * s0, p[nt][2] * s1, p[nt][3] * s1};
+        auto out = [&](int i) { return MASKED && (dead >> (4 * nt + i) & 1); };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (out(i)) x[i] = 0.f;
+        if (CENTRED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!out(i)) corr[nt][g][i & 1] = fmaf(x[i], i < 2 ? z0 : z1, corr[nt][g][i & 1]);
+        }
+#pragma unroll
+        for (int np = 0; np < NP; ++np) {
+          const uint32_t u0 = NP > 1 ? split_off(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+          const uint32_t u1 = NP > 1 ? split_off(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
+          if (MASKED && !CENTRED) {
+            // the zeros' part of the tile's last blocks, where an operand's NaN would reach rows that do not see it
+            const float r[4] = {lo_f(u0), hi_f(u0), lo_f(u1), hi_f(u1)};
+            float add[2] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!out(i)) add[i & 1] = fmaf(r[i], i < 2 ? z0 : z1, add[i & 1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) add[c] += __shfl_xor_sync(0xffffffffu, add[c], d);
+#pragma unroll
+              for (int j = 2 * g; j < 2 * g + 2; ++j) {
+                o[nt][j][c] += add[c];
+                o[nt][j][2 + c] += add[c];
+              }
+            }
           }
-          s[nt][0] = fmaf(s0, c[0], s[nt][0]);
-          s[nt][1] = fmaf(s0, c[1], s[nt][1]);
-          s[nt][2] = fmaf(s1, c[2], s[nt][2]);
-          s[nt][3] = fmaf(s1, c[3], s[nt][3]);
+          pb[nt][np][g][0] = transpose8x8(u0);
+          pb[nt][np][g][1] = transpose8x8(u1);
         }
       }
     }
-    bool up = false;
+    if (!CENTRED) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int j = 0; j < DH / 16; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[nt][i] *= scale_log2;
-        if (MASKED && key0 + rr + (i >> 1) * 8 > lim[nt][i & 1]) s[nt][i] = -INFINITY;
-        up |= s[nt][i] > m[nt][i & 1] + LAZY;
+        for (int nt = 0; nt < NT; ++nt)
+          mma_bf16(o[nt][j], minus16[0], minus16[1], minus16[2], minus16[3], pb[nt][0][j / 2][0], pb[nt][0][j / 2][1]);
+      if (!SIMT) {
+#pragma unroll
+        for (int j = 0; j < DH / 16; ++j) {
+          const uint32_t sel = j / 2 & 1 ? 0x7632 : 0x5410;
+          const uint32_t za = __byte_perm(vz[0][j / 4], vz[1][j / 4], sel), zb = __byte_perm(vz[NZ - 2][j / 4], vz[NZ - 1][j / 4], sel);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][j], za, za, zb, zb, pb[nt][0][j / 2][0], pb[nt][0][j / 2][1]);
+        }
       }
+    }
+#pragma unroll
+    for (int half = 0; half < DH / 64; ++half) {  // 64 channels, four fragments
+      uint32_t w[4];
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(blk + 8 * DH + 512 * half + 16 * lane);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int j = 4 * half + jj;
+        const uint32_t a0 = nib<0>(w[jj]), a1 = nib<1>(w[jj]), a2 = nib<2>(w[jj]), a3 = nib<3>(w[jj]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (!CENTRED) {
+            mma_bf16(o[nt][j], a0, a1, a2, a3, pb[nt][0][j / 2][0], pb[nt][0][j / 2][1]);
+          } else {
+            float c[4] = {};
+#pragma unroll
+            for (int np = NP - 1; np >= 0; --np) mma_bf16(c, a0, a1, a2, a3, pb[nt][np][j / 2][0], pb[nt][np][j / 2][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nt][j][i] += c[i];
+          }
+        }
+      }
+    }
+  }
+
+  // Two blocks of 16 keys from key0 on, 16 AW apart, in shared memory.  MASKED: some row does not see all of them, or one is
+  // not there (a key that a row does not see may hold anything, a NaN scale too, and takes no part).
+  template <bool MASKED>
+  __device__ __forceinline__ void two_blocks(const uint8_t* blk0, const uint8_t* blk1, int key0, uint32_t there, float scale_log2) {
+    const int rr = lane >> 2;
+    float s[2][NT][4];
+    scores(blk0, s[0]);
+    scores(blk1, s[1]);
+    bool up = false;
+    uint32_t dead[2] = {0, 0};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[u][nt][i] *= scale_log2;
+          if (MASKED && (!(there >> u & 1) || key0 + u * 16 * AW + rr + (i >> 1) * 8 > lim[nt][i & 1])) {
+            s[u][nt][i] = -INFINITY;
+            dead[u] |= 1u << (4 * nt + i);
+          }
+          up |= s[u][nt][i] > m[nt][i & 1] + LAZY;
+        }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float x = fmaxf(m[nt][c], fmaxf(s[nt][c], s[nt][2 + c]));
+          float x = fmaxf(m[nt][c], fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
           const float f = x == -INFINITY ? 1.f : exp2_fast(m[nt][c] - x);
           m[nt][c] = x;
           l[nt][c] *= f;
+          if (CENTRED)
 #pragma unroll
-          for (int g = 0; g < NG; ++g) corr[nt][g][c] *= f;
+            for (int g = 0; g < NG; ++g) corr[nt][g][c] *= f;
 #pragma unroll
           for (int j = 0; j < DH / 16; ++j) {
             o[nt][j][c] *= f;
@@ -252,87 +396,24 @@ template <typename T, int DH, int NT, int NP> struct Attn {
           }
         }
     }
-    bool dead[NT][4];  // (MASKED)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dead[nt][i] = MASKED && s[nt][i] == -INFINITY;
-        const float mm = m[nt][i & 1];
-        s[nt][i] = exp2_fast(s[nt][i] - (MASKED && mm == -INFINITY ? 0.f : mm));
-        l[nt][i & 1] += s[nt][i];
-      }
-    uint32_t vs[2][NG / 2], vz[2][NG / 2];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 64 * NG + 4 * NG * (rr + 8 * h));
-#pragma unroll
-      for (int i = 0; i < NG / 2; ++i) {
-        vs[h][i] = prm[i];
-        vz[h][i] = prm[NG / 2 + i];
-      }
-    }
-#pragma unroll
-    for (int half = 0; half < DH / 64; ++half) {  // 64 channels, two groups, four fragments
-      uint32_t w[4];
-      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(blk + 8 * DH + 512 * half + 16 * lane);
-#pragma unroll
-      for (int gg = 0; gg < 2; ++gg) {
-        const int g = 2 * half + gg;
-        const float s0 = gg ? hi_f(vs[0][half]) : lo_f(vs[0][half]), s1 = gg ? hi_f(vs[1][half]) : lo_f(vs[1][half]);
-        const float z0 = (gg ? hi_f(vz[0][half]) : lo_f(vz[0][half])) + 8.f;
-        const float z1 = (gg ? hi_f(vz[1][half]) : lo_f(vz[1][half])) + 8.f;
-        uint32_t pb[NT][NP][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float x[4] = {s[nt][0] * s0, s[nt][1] * s0, s[nt][2] * s1, s[nt][3] * s1};
-          if (MASKED)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (dead[nt][i]) x[i] = 0.f;
-          if (NP > 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!MASKED || !dead[nt][i]) corr[nt][g][i & 1] = fmaf(x[i], i < 2 ? z0 : z1, corr[nt][g][i & 1]);
-          }
-#pragma unroll
-          for (int np = 0; np < NP; ++np) {
-            const uint32_t u0 = NP > 1 ? split_off(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
-            const uint32_t u1 = NP > 1 ? split_off(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
-            if (NP == 1) {
-              const float r[4] = {lo_f(u0), hi_f(u0), lo_f(u1), hi_f(u1)};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!MASKED || !dead[nt][i]) corr[nt][g][i & 1] = fmaf(r[i], i < 2 ? z0 : z1, corr[nt][g][i & 1]);
-            }
-            pb[nt][np][0] = transpose8x8(u0);
-            pb[nt][np][1] = transpose8x8(u1);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float mm = m[nt][i & 1];
+          s[u][nt][i] = exp2_fast(s[u][nt][i] - (MASKED && mm == -INFINITY ? 0.f : mm));
+          l[nt][i & 1] += s[u][nt][i];
         }
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const uint32_t x = w[2 * gg + jj];
-          const uint32_t a0 = nibbles<0>(x), a1 = nibbles<1>(x), a2 = nibbles<2>(x), a3 = nibbles<3>(x);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (NP == 1) {
-              mma_bf16(o[nt][2 * g + jj], a0, a1, a2, a3, pb[nt][0][0], pb[nt][0][1]);
-            } else {
-              float c[4] = {};
-#pragma unroll
-              for (int np = NP - 1; np >= 0; --np) mma_bf16(c, a0, a1, a2, a3, pb[nt][np][0], pb[nt][np][1]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[nt][2 * g + jj][i] += c[i];
-            }
-          }
-        }
-      }
-    }
+    values<MASKED>(blk0, s[0], dead[0]);
+    values<MASKED>(blk1, s[1], dead[1]);
   }
+
+  template <int I> __device__ __forceinline__ uint32_t nib(uint32_t x) const { return nibbles<I, CENTRED>(x, mask, sixteen); }
 };
 
-template <int DH> __device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* src) {
-  const int lane = threadIdx.x & 31;
+template <int DH> __device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* src, int lane) {
 #pragma unroll
   for (int i = 0; i < (kvq_block_bytes(DH) / 16 + 31) / 32; ++i) {
     const int c = i * 32 + lane;
@@ -346,7 +427,7 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) {
 }
 
 template <typename T, int DH, int NT, int NP>
-__global__ void __launch_bounds__(AW * 32) kvq_attention_kernel(const __grid_constant__ KvqAttn p) {
+__global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1 ? 4 : 3) kvq_attention_kernel(const __grid_constant__ KvqAttn p) {
   typedef Attn<T, DH, NT, NP> A;
   constexpr int R = A::R, ROW = A::ROW;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -418,38 +499,50 @@ __global__ void __launch_bounds__(AW * 32) kvq_attention_kernel(const __grid_con
     A a;
     a.load_q(p, seq, r0, head);
     const int all = a.seen_by_all(p, r0);
-    const int blocks = min((len + KVQ_BLOCK - 1) / KVQ_BLOCK, q1 * AW), per_page = p.c.page_tokens / KVQ_BLOCK;
-    const int b0 = q0 * AW + w, count = blocks > b0 ? (blocks - b0 + AW - 1) / AW : 0;
+    const int blocks = min((len + KVQ_BLOCK - 1) / KVQ_BLOCK, (q1 - UNIT_COST) * AW), per_page = p.c.page_tokens / KVQ_BLOCK;
+    const int b0 = max(0, q0 - UNIT_COST) * AW + w, count = blocks > b0 ? (blocks - b0 + AW - 1) / AW : 0;
     uint8_t* ring = smem + w * A::STAGES * A::BLK;
     const uint32_t ring_u = smem_u32(ring);
     uint32_t there = 0;  // bit s: stage s holds a block
+    const uint8_t* at = nullptr;  // each lane: one of this warp's next 32 blocks
     auto fetch = [&](int i) {
       if (i < count) {
-        const int b = b0 + i * AW, slot = b / per_page, stage = i % A::STAGES;
-        const int page = p.c.table[seq * p.c.ld_table + slot];
-        const bool ok = page >= 0 && page < p.c.n_pages;
-        if (ok)
-          copy_block<DH>(ring_u + stage * A::BLK,
-                         p.c.pool + ((static_cast<size_t>(page) * heads + head) * per_page + (b - slot * per_page)) * A::BLK);
-        else
-          set_status(p.status, ST_RANGE);
-        there = (there & ~(1u << stage)) | (ok ? 1u << stage : 0u);
+        if ((i & 31) == 0) {
+          at = nullptr;
+          if (i + lane < count) {
+            const int b = b0 + (i + lane) * AW, slot = b / per_page;
+            const int page = p.c.table[seq * p.c.ld_table + slot];
+            if (page >= 0 && page < p.c.n_pages)
+              at = p.c.pool + ((static_cast<size_t>(page) * heads + head) * per_page + (b - slot * per_page)) * A::BLK;
+            else
+              set_status(p.status, ST_RANGE);
+          }
+        }
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(at), i & 31));
+        const int stage = i % A::STAGES;
+        if (src) copy_block<DH>(ring_u + stage * A::BLK, src, a.lane);
+        there = (there & ~(1u << stage)) | (src ? 1u << stage : 0u);
       }
+    };
+    auto fetch_two = [&](int i) {
+      fetch(i);
+      fetch(i + 1);
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < A::STAGES - 1; ++i) fetch(i);
-    for (int i = 0; i < count; ++i) {
-      cp_async_wait<A::STAGES - 2>();
+    for (int i = 0; i < A::STAGES - 2; i += 2) fetch_two(i);
+    for (int i = 0; i < count; i += 2) {
+      __syncwarp();  // (every lane is done with the stages that are written next)
+      fetch_two(i + A::STAGES - 2);
+      cp_async_wait<A::STAGES / 2 - 1>();
       __syncwarp();
       const int stage = i % A::STAGES, key0 = (b0 + i * AW) * KVQ_BLOCK;
-      const bool ok = there >> stage & 1;
-      fetch(i + A::STAGES - 1);
-      if (!ok) continue;
-      if (key0 + KVQ_BLOCK - 1 <= all)
-        a.template block<false>(ring + stage * A::BLK, key0, p.scale_log2);
-      else
-        a.template block<true>(ring + stage * A::BLK, key0, p.scale_log2);
+      const uint32_t ok = i + 1 < count ? there >> stage & 3u : there >> stage & 1u;
+      const uint8_t* blk = ring + stage * A::BLK;
+      if (ok == 3 && key0 + QUANTUM + KVQ_BLOCK - 1 <= all)
+        a.template two_blocks<false>(blk, blk + A::BLK, key0, 3, p.scale_log2);
+      else if (ok)
+        a.template two_blocks<true>(blk, blk + A::BLK, key0, ok, p.scale_log2);
     }
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with its ring: the merge buffer lies over them
@@ -462,12 +555,13 @@ __global__ void __launch_bounds__(AW * 32) kvq_attention_kernel(const __grid_con
         const int row = nt * 8 + 2 * tq + c;
         float sum = a.l[nt][c], corr[A::NG];
 #pragma unroll
-        for (int g = 0; g < A::NG; ++g) corr[g] = a.corr[nt][g][c];
+        for (int g = 0; g < A::NG; ++g) corr[g] = A::CENTRED ? a.corr[nt][g][c] : 0.f;
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (A::CENTRED)
 #pragma unroll
-          for (int g = 0; g < A::NG; ++g) corr[g] += __shfl_xor_sync(0xffffffffu, corr[g], d);
+            for (int g = 0; g < A::NG; ++g) corr[g] += __shfl_xor_sync(0xffffffffu, corr[g], d);
         }
         if (rr == 0) {
           part_m[w][row] = a.m[nt][c];
