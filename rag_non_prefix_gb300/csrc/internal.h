@@ -306,7 +306,7 @@ struct KvqView {
   long long ld_table;
   int n_pages, page_tokens, n_kv_heads, max_pages, n_seqs;
 };
-constexpr int KVQ_MAX_CTAS = 640;  // of the attention's grid: its scratch holds two parts for each
+constexpr int KVQ_MAX_CTAS = 800;  // of the attention's grid: its scratch holds two parts for each
 size_t kvq_scratch_bytes();
 cudaError_t launch_kvq_write(const KvqView& c, int head_dim, const void* k, long long ldk, const void* v, long long ldv,
                              cb_dtype dt, const int32_t* seq, const int32_t* pos, int rows, int32_t* status,

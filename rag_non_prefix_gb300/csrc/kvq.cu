@@ -1,8 +1,13 @@
 // A KV cache in 4 bits (layout and arithmetic: kvq.cuh): rows quantised as they are written, and read back
 // with their keys turned to new positions.
 //
-// Both kernels give four channels to a lane, so that a group of 32 channels is 8 lanes (its extremes three
-// shuffles) and a row of one head is a warp (128 channels) or half of one (64).
+// Both kernels give eight channels to a lane: a row of one head is 16 lanes (128 channels) or 8, a group of 32
+// channels four of them (its extremes two shuffles), and the row's key codes are one word a lane.  A word of value codes
+// belongs to four tokens (2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of a block), so a warp takes those four rows of
+// 16 at a time: where they are such a word's tokens (a prompt from a multiple of 16 on) it moves whole words,
+// else (decoded tokens, scattered ones) a token's bytes alone.
+#include <algorithm>
+
 #include "internal.h"
 #include "kvq.cuh"
 
@@ -12,97 +17,126 @@ namespace {
 
 constexpr int KVQ_WARPS = 8;
 
-__device__ __forceinline__ void load4(const bf16* p, float* f) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(u.x << 16);
-  f[1] = __uint_as_float(u.x & 0xffff0000u);
-  f[2] = __uint_as_float(u.y << 16);
-  f[3] = __uint_as_float(u.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load4(const float* p, float* f) {
-  const float4 u = *reinterpret_cast<const float4*>(p);
-  f[0] = u.x;
-  f[1] = u.y;
-  f[2] = u.z;
-  f[3] = u.w;
-}
-__device__ __forceinline__ void store4(bf16* p, const float* f) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-__device__ __forceinline__ void store4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
+__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
-// Codes (nibbles 0 to 3) of a lane's four channels, and its group's scale and zero packed as bf16.
-__device__ __forceinline__ uint32_t encode4(const float* x, uint32_t& params) {
-  float lo = INFINITY, hi = -INFINITY;
+// The rows of a warp and where they lie (64 channels: eight lanes of each half of a warp).
+// STEPS 2: in step k the first half takes row 2 tq + 8 k of 16, the second row 2 tq + 1 + 8 k.
+// STEPS 1: two rows of the call, as they come (few rows, whose time is that of one warp's steps).
+template <int DH, int STEPS> struct KvqRows {
+  static constexpr int LANES = DH / 8;
+  int L, tq, g;          // lane of its row; of the row's word of keys: pair of columns and group
+  int row[STEPS], r[STEPS];  // this lane's rows, and which tokens of their blocks they are
+  uint8_t* blk[STEPS];   // their blocks (head 0), or nullptr
+  bool whole;            // the warp's four rows share their words of value codes
+
+  // `unit`: four rows of 16 (STEPS 2), or two rows
+  __device__ __forceinline__ KvqRows(const KvqView& c, const int32_t* seqs, const int32_t* poss, int rows, int unit,
+                                     int32_t* status) {
+    const int lane = threadIdx.x & 31, second = lane / 16;
+    L = lane % LANES;
+    tq = L & 3;
+    g = L >> 2;
+    const int quad = unit & 3;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i] != x[i] ? INFINITY : x[i]);
+    for (int k = 0; k < STEPS; ++k) {
+      row[k] = STEPS == 2 ? (unit >> 2) * 16 + 2 * quad + second + 8 * k : 2 * unit + second;
+      const bool in = row[k] < rows && lane % 16 < LANES;
+      const int pos = in ? poss[row[k]] : -1, seq = in ? (seqs ? seqs[row[k]] : row[k]) : -1;
+      blk[k] = pos >= 0 && seq >= 0 ? kvq_block(c, seq, pos, DH, status) : nullptr;
+      r[k] = pos & 15;
+    }
+    whole = false;
+    if (STEPS == 1) return;
+    const uint8_t* same = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(blk[0]), 0));
+    const bool mine = lane % 16 >= LANES ||
+                      (same && blk[0] == same && blk[STEPS - 1] == same && r[0] == 2 * quad + second && r[STEPS - 1] == r[0] + 8);
+    whole = __all_sync(0xffffffffu, mine);
   }
+};
+
+// Codes of a lane's eight channels, and its group's scale and zero.
+__device__ __forceinline__ uint32_t encode8(const float* x, float3& p) {
+  float lo = x[0], hi = x[0], odd = 0.f;
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+    odd = fmaf(x[i], 0.f, odd);  // NaN once a number is not finite
+  }
+  hi = odd == 0.f ? hi : INFINITY;
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  const float2 p = kvq_params(lo, hi);
-  params = (__float_as_uint(p.x) >> 16) | (__float_as_uint(p.y) & 0xffff0000u);
-  if (!(p.x < INFINITY)) return 0;
-  const float inv = __frcp_rn(p.x);
-  uint32_t c = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c |= kvq_code(x[i], p.x, inv, p.y) << (4 * i);
-  return c;
+  p = kvq_params(lo, hi);
+  return p.x < INFINITY ? kvq_codes(x, p.x, p.y, p.z) : 0;
 }
 
-template <typename T, int DH>
+template <typename T, int DH, int STEPS>
 __global__ void __launch_bounds__(KVQ_WARPS * 32) kvq_write_kernel(KvqView c, const T* __restrict__ k, long long ldk,
                                                                    const T* __restrict__ v, long long ldv,
                                                                    const int32_t* __restrict__ seqs,
-                                                                   const int32_t* __restrict__ poss, int rows,
-                                                                   int32_t* status) {
+                                                                   const int32_t* __restrict__ poss, int rows, int units,
+                                                                   int heads_each, int32_t* status) {
   pdl_trigger();
   pdl_wait();
-  constexpr int LANES = DH / 4, NG = DH / 32;
-  const int L = threadIdx.x % LANES;
-  const long long item = (static_cast<long long>(blockIdx.x) * KVQ_WARPS * 32 + threadIdx.x) / LANES;
-  const int row = static_cast<int>(item / c.n_kv_heads), head = static_cast<int>(item % c.n_kv_heads);
-  // (the lanes of a row that is left out keep up with the shuffles)
-  const bool in = row < rows;
-  const int pos = in ? poss[row] : -1, seq = in ? (seqs ? seqs[row] : row) : -1;
-  float kx[4] = {}, vx[4] = {};
-  uint8_t* blk = nullptr;
-  if (pos >= 0 && seq >= 0) {
-    load4(k + row * ldk + head * DH + 4 * L, kx);
-    load4(v + row * ldv + head * DH + 4 * L, vx);
-    blk = kvq_block(c, seq, pos, DH, status);
-  }
-  uint32_t kp, vp;
-  const uint32_t kc = encode4(kx, kp), vc = encode4(vx, vp);
-  // the value channels 8 up or down are two lanes away; a lane of the lower channels writes the first two
-  // bytes of the pair's four, one of the upper the others
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 2);
-  if (!blk) return;
-  blk += static_cast<size_t>(head) * (c.page_tokens / KVQ_BLOCK) * kvq_block_bytes(DH);
-  const int r = pos % KVQ_BLOCK;
-  const int g = L / 8, tq = L % 8 / 2;
-  *reinterpret_cast<uint16_t*>(blk + r * (DH / 2) + (tq * NG + g) * 4 + (L & 1) * 2) = static_cast<uint16_t>(kc);
-  const bool upper = L & 2;
-  const uint32_t lo = upper ? other : vc, hi = upper ? vc : other;
-  const int n0 = 4 * (L & 1) + (upper ? 2 : 0);
+  constexpr int LANES = DH / 8, NG = DH / 32;
+  const int lane = threadIdx.x & 31, unit = blockIdx.x * KVQ_WARPS + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const KvqRows<DH, STEPS> at(c, seqs, poss, rows, unit, status);
+  const int L = at.L;
+  const size_t head_bytes = static_cast<size_t>(c.page_tokens / KVQ_BLOCK) * kvq_block_bytes(DH);
+  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, c.n_kv_heads);
+  for (int head = h0; head < h1; ++head) {
+    uint32_t half[STEPS];  // value bytes of channels n (low nibbles) and n + 8 (high): n = 0..3 by even lanes, 4..7 by odd ones
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int sh = 4 * ((n0 & 3) + i);
-    blk[kvq_value_byte(DH, r, L / 4, n0 + i)] = static_cast<uint8_t>(((lo >> sh) & 15u) | (((hi >> sh) & 15u) << 4));
-  }
-  if (L % 8 == 0) {
-    uint16_t* p = reinterpret_cast<uint16_t*>(blk + 16 * DH + 4 * NG * r);
-    p[g] = static_cast<uint16_t>(kp);
-    p[NG + g] = static_cast<uint16_t>(kp >> 16);
-    p += 32 * NG;
-    p[g] = static_cast<uint16_t>(vp);
-    p[NG + g] = static_cast<uint16_t>(vp >> 16);
+    for (int s = 0; s < STEPS; ++s) {
+      float kx[8] = {}, vx[8] = {};
+      if (at.blk[s]) {
+        load8(k + at.row[s] * ldk + head * DH + 8 * L, kx);
+        load8(v + at.row[s] * ldv + head * DH + 8 * L, vx);
+      }
+      float3 kp, vp;
+      const uint32_t kc = encode8(kx, kp), vc = encode8(vx, vp);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 1);
+      const uint32_t lo = L & 1 ? other >> 16 : vc, hi = L & 1 ? vc >> 16 : other;
+      // nibbles 0 to 3 of both, interleaved to bytes
+      const uint32_t lo2 = (lo & 0xf) | (lo & 0xf0) << 4 | (lo & 0xf00) << 8 | (lo & 0xf000) << 12;
+      const uint32_t hi2 = (hi & 0xf) | (hi & 0xf0) << 4 | (hi & 0xf00) << 8 | (hi & 0xf000) << 12;
+      half[s] = lo2 | hi2 << 4;
+      if (!at.blk[s]) continue;
+      uint8_t* blk = at.blk[s] + head * head_bytes;
+      const int r = at.r[s];
+      *reinterpret_cast<uint32_t*>(blk + r * (DH / 2) + (at.tq * NG + at.g) * 4) = kc;
+      if (at.tq == 0) {
+        uint16_t* p = reinterpret_cast<uint16_t*>(blk + 16 * DH + 4 * NG * r) + at.g;
+        p[0] = static_cast<uint16_t>(__float_as_uint(kp.x) >> 16);
+        p[NG] = static_cast<uint16_t>(__float_as_uint(kp.y) >> 16);
+        p[32 * NG] = static_cast<uint16_t>(__float_as_uint(vp.x) >> 16);
+        p[33 * NG] = static_cast<uint16_t>(__float_as_uint(vp.y) >> 16);
+      }
+      if (!at.whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          blk[kvq_value_byte(DH, r, L >> 1, 4 * (L & 1) + i)] = static_cast<uint8_t>(half[s] >> (8 * i));
+      }
+    }
+    if (STEPS == 2 && at.whole) {
+      // a lane has the bytes of tokens 2 tq and 2 tq + 8, the lane 16 away those of 2 tq + 1 and 2 tq + 9: two of
+      // the four words each
+      const bool second = lane >= 16;
+      const uint32_t pair0 = __byte_perm(half[0], half[STEPS - 1], 0x5140), pair1 = __byte_perm(half[0], half[STEPS - 1], 0x7362);  // n 0, 1; n 2, 3
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? pair0 : pair1, 16);
+      const uint32_t w0 = second ? __byte_perm(got, pair1, 0x5410) : __byte_perm(pair0, got, 0x5410);
+      const uint32_t w1 = second ? __byte_perm(got, pair1, 0x7632) : __byte_perm(pair0, got, 0x7632);
+      if (lane % 16 < LANES) {
+        uint8_t* blk = at.blk[0] + head * head_bytes;
+        const int at0 = kvq_value_byte(DH, at.r[0] & ~9, L >> 1, 4 * (L & 1) + (second ? 2 : 0));
+        *reinterpret_cast<uint32_t*>(blk + at0) = w0;
+        *reinterpret_cast<uint32_t*>(blk + at0 + 64) = w1;
+      }
+    }
   }
 }
 
@@ -110,54 +144,87 @@ struct KvqTurn {
   float2 cs[64];  // (cos, sin) of channel pairs i, i + head_dim / 2
 };
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(KVQ_WARPS * 32) kvq_read_kernel(KvqView c, const int32_t* __restrict__ seqs,
-                                                                  const int32_t* __restrict__ poss, int rows,
-                                                                  const __grid_constant__ KvqTurn turn, bool turned,
-                                                                  T* __restrict__ k, long long ldk, T* __restrict__ v,
-                                                                  long long ldv, int32_t* status) {
+template <typename T, int DH, int STEPS>
+__global__ void __launch_bounds__(KVQ_WARPS * 32, 4) kvq_read_kernel(KvqView c, const int32_t* __restrict__ seqs,
+                                                                  const int32_t* __restrict__ poss, int rows, int units,
+                                                                  int heads_each, const __grid_constant__ KvqTurn turn,
+                                                                  bool turned, T* __restrict__ k, long long ldk,
+                                                                  T* __restrict__ v, long long ldv, int32_t* status) {
+  __shared__ float2 cs[64];
+  // (read one by one: an indexed kernel argument is fetched lane after lane)
+  if (turned && threadIdx.x < DH / 2) cs[threadIdx.x] = turn.cs[threadIdx.x];
   pdl_trigger();
   pdl_wait();
-  constexpr int LANES = DH / 4, NG = DH / 32;
-  const int L = threadIdx.x % LANES;
-  const long long item = (static_cast<long long>(blockIdx.x) * KVQ_WARPS * 32 + threadIdx.x) / LANES;
-  const int row = static_cast<int>(item / c.n_kv_heads), head = static_cast<int>(item % c.n_kv_heads);
-  const bool in = row < rows;
-  const int pos = in ? poss[row] : -1, seq = in ? (seqs ? seqs[row] : row) : -1;
-  const uint8_t* blk = pos >= 0 && seq >= 0 ? kvq_block(c, seq, pos, DH, status) : nullptr;
-  float kx[4] = {}, vx[4] = {};
-  if (blk) {
-    blk += static_cast<size_t>(head) * (c.page_tokens / KVQ_BLOCK) * kvq_block_bytes(DH);
-    const int r = pos % KVQ_BLOCK, g = L / 8, tq = L % 8 / 2;
-    const uint32_t kc = *reinterpret_cast<const uint16_t*>(blk + r * (DH / 2) + (tq * NG + g) * 4 + (L & 1) * 2);
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(blk + 16 * DH + 4 * NG * r);
-    const float ks = __uint_as_float(static_cast<uint32_t>(p[g]) << 16), kz = __uint_as_float(static_cast<uint32_t>(p[NG + g]) << 16);
-    p += 32 * NG;
-    const float vs = __uint_as_float(static_cast<uint32_t>(p[g]) << 16), vz = __uint_as_float(static_cast<uint32_t>(p[NG + g]) << 16);
-    const int n0 = 4 * (L & 1), up = L & 2 ? 4 : 0;
+  __syncthreads();
+  constexpr int LANES = DH / 8, NG = DH / 32;
+  const int lane = threadIdx.x & 31, unit = blockIdx.x * KVQ_WARPS + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const KvqRows<DH, STEPS> at(c, seqs, poss, rows, unit, status);
+  const int L = at.L;
+  const bool upper = L >= LANES / 2;
+  float co[8], si[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kx[i] = ks * (static_cast<float>((kc >> (4 * i)) & 15u) + kz);
-      vx[i] = vs * (static_cast<float>((blk[kvq_value_byte(DH, r, L / 4, n0 + i)] >> up) & 15) + vz);
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = turned ? cs[(8 * L + i) % (DH / 2)] : make_float2(1.f, 0.f);
+    co[i] = x.x;
+    si[i] = upper ? x.y : -x.y;
+  }
+  const size_t head_bytes = static_cast<size_t>(c.page_tokens / KVQ_BLOCK) * kvq_block_bytes(DH);
+  const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, c.n_kv_heads);
+  for (int head = h0; head < h1; ++head) {
+    uint32_t word[8];  // (whole) value codes of four tokens, channels n and n + 8 for n = 0..7
+    if (at.whole) {
+      const uint8_t* blk = at.blk[0] + head * head_bytes;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        word[i] = lane % 16 < LANES ? *reinterpret_cast<const uint32_t*>(blk + kvq_value_byte(DH, at.r[0] & ~9, L >> 1, i)) : 0;
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      float kx[8] = {}, vx[8] = {};
+      if (at.blk[s]) {
+        const uint8_t* blk = at.blk[s] + head * head_bytes;
+        const int r = at.r[s];
+        const uint32_t kc = *reinterpret_cast<const uint32_t*>(blk + r * (DH / 2) + (at.tq * NG + at.g) * 4);
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(blk + 16 * DH + 4 * NG * r) + at.g;
+        const float ks = bf(p[0]), kz = ks * bf(p[NG]), vs = bf(p[32 * NG]), vz = vs * bf(p[33 * NG]);
+        const int byte = 2 * (r & 1) + (r >> 3), up = L & 1 ? 4 : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          kx[i] = fmaf(static_cast<float>((kc >> (4 * i)) & 15u), ks, kz);  // (exact: 17 bits)
+          const uint32_t vc = at.whole ? word[i] >> (8 * byte) : blk[kvq_value_byte(DH, r, L >> 1, i)];
+          vx[i] = fmaf(static_cast<float>((vc >> up) & 15u), vs, vz);
+        }
+      }
+      if (turned) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float y = __shfl_xor_sync(0xffffffffu, kx[i], LANES / 2);
+          kx[i] = fmaf(y, si[i], kx[i] * co[i]);
+        }
+      }
+      if (at.row[s] < rows && lane % 16 < LANES) {
+        store8(k + at.row[s] * ldk + head * DH + 8 * L, kx);
+        store8(v + at.row[s] * ldv + head * DH + 8 * L, vx);
+      }
     }
   }
-  if (turned) {
-    const bool second = L >= LANES / 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 cs = turn.cs[4 * (second ? L - LANES / 2 : L) + i];
-      const float y = __shfl_xor_sync(0xffffffffu, kx[i], LANES / 2);
-      kx[i] = second ? fmaf(y, cs.y, kx[i] * cs.x) : fmaf(-y, cs.y, kx[i] * cs.x);
-    }
-  }
-  if (!in) return;
-  store4(k + row * ldk + head * DH + 4 * L, kx);
-  store4(v + row * ldv + head * DH + 4 * L, vx);
 }
 
-unsigned kvq_grid(int rows, int heads, int dh) {
-  const long long lanes = static_cast<long long>(rows) * heads * (dh / 4);
-  return static_cast<unsigned>((lanes + KVQ_WARPS * 32 - 1) / (KVQ_WARPS * 32));
+// Units of rows, and the heads that a warp takes one after the other: a head each while there are few, more where
+// that would only look up the rows again.
+struct KvqPlan {
+  int steps, units, heads_each;
+  dim3 grid;
+};
+KvqPlan kvq_plan(int rows, int heads) {
+  KvqPlan p;
+  p.steps = static_cast<long long>(rows) * heads <= 8192 ? 1 : 2;
+  p.units = p.steps == 1 ? (rows + 1) / 2 : (rows + 15) / 16 * 4;
+  const long long warps = static_cast<long long>(p.units) * heads;
+  p.heads_each = static_cast<int>(std::min<long long>(heads, std::max<long long>(1, warps / 16384)));
+  p.grid = dim3((p.units + KVQ_WARPS - 1) / KVQ_WARPS, (heads + p.heads_each - 1) / p.heads_each);
+  return p;
 }
 
 }  // namespace
@@ -165,34 +232,46 @@ unsigned kvq_grid(int rows, int heads, int dh) {
 cudaError_t launch_kvq_write(const KvqView& c, int head_dim, const void* k, long long ldk, const void* v, long long ldv,
                              cb_dtype dt, const int32_t* seq, const int32_t* pos, int rows, int32_t* status,
                              cudaStream_t s) {
-  const dim3 grid(kvq_grid(rows, c.n_kv_heads, head_dim)), block(KVQ_WARPS * 32);
+  const KvqPlan plan = kvq_plan(rows, c.n_kv_heads);
+  const dim3 block(KVQ_WARPS * 32);
   auto go = [&](auto* kernel, auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
-    return launch_chain(kernel, grid, block, 0, s, c, static_cast<T*>(k), ldk, static_cast<T*>(v), ldv, seq, pos, rows,
-                        status);
+    return launch_chain(kernel, plan.grid, block, 0, s, c, static_cast<T*>(k), ldk, static_cast<T*>(v), ldv, seq, pos, rows,
+                        plan.units, plan.heads_each, status);
   };
+  const bool one = plan.steps == 1;
   const bf16* b = nullptr;
   const float* f = nullptr;
-  if (dt == CB_BF16) return head_dim == 128 ? go(kvq_write_kernel<bf16, 128>, b) : go(kvq_write_kernel<bf16, 64>, b);
-  return head_dim == 128 ? go(kvq_write_kernel<float, 128>, f) : go(kvq_write_kernel<float, 64>, f);
+  if (dt == CB_BF16) {
+    if (head_dim == 128) return one ? go(kvq_write_kernel<bf16, 128, 1>, b) : go(kvq_write_kernel<bf16, 128, 2>, b);
+    return one ? go(kvq_write_kernel<bf16, 64, 1>, b) : go(kvq_write_kernel<bf16, 64, 2>, b);
+  }
+  if (head_dim == 128) return one ? go(kvq_write_kernel<float, 128, 1>, f) : go(kvq_write_kernel<float, 128, 2>, f);
+  return one ? go(kvq_write_kernel<float, 64, 1>, f) : go(kvq_write_kernel<float, 64, 2>, f);
 }
 
 cudaError_t launch_kvq_read(const KvqView& c, int head_dim, const int32_t* seq, const int32_t* pos, int rows,
                             const float* cs_host, cb_dtype dt, void* k, long long ldk, void* v, long long ldv,
                             int32_t* status, cudaStream_t s) {
-  const dim3 grid(kvq_grid(rows, c.n_kv_heads, head_dim)), block(KVQ_WARPS * 32);
+  const KvqPlan plan = kvq_plan(rows, c.n_kv_heads);
+  const dim3 block(KVQ_WARPS * 32);
   KvqTurn turn = {};
   if (cs_host)
     for (int i = 0; i < head_dim / 2; ++i) turn.cs[i] = make_float2(cs_host[2 * i], cs_host[2 * i + 1]);
   auto go = [&](auto* kernel, auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
-    return launch_chain(kernel, grid, block, 0, s, c, seq, pos, rows, turn, cs_host != nullptr, static_cast<T*>(k), ldk,
+    return launch_chain(kernel, plan.grid, block, 0, s, c, seq, pos, rows, plan.units, plan.heads_each, turn, cs_host != nullptr, static_cast<T*>(k), ldk,
                         static_cast<T*>(v), ldv, status);
   };
+  const bool one = plan.steps == 1;
   bf16* b = nullptr;
   float* f = nullptr;
-  if (dt == CB_BF16) return head_dim == 128 ? go(kvq_read_kernel<bf16, 128>, b) : go(kvq_read_kernel<bf16, 64>, b);
-  return head_dim == 128 ? go(kvq_read_kernel<float, 128>, f) : go(kvq_read_kernel<float, 64>, f);
+  if (dt == CB_BF16) {
+    if (head_dim == 128) return one ? go(kvq_read_kernel<bf16, 128, 1>, b) : go(kvq_read_kernel<bf16, 128, 2>, b);
+    return one ? go(kvq_read_kernel<bf16, 64, 1>, b) : go(kvq_read_kernel<bf16, 64, 2>, b);
+  }
+  if (head_dim == 128) return one ? go(kvq_read_kernel<float, 128, 1>, f) : go(kvq_read_kernel<float, 128, 2>, f);
+  return one ? go(kvq_read_kernel<float, 64, 1>, f) : go(kvq_read_kernel<float, 64, 2>, f);
 }
 
 }  // namespace cb

@@ -54,34 +54,48 @@ __device__ __forceinline__ float bf16_up(float x) {  // the smallest bf16 number
   return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
 }
 
-// Scale and zero of a group whose smallest and largest numbers are lo and hi (hi infinite for a NaN).
-__device__ __forceinline__ float2 kvq_params(float lo, float hi) {
+// Scale, zero and 1 / scale (approximately) of a group whose smallest and largest numbers are lo and hi (hi infinite if
+// a number is not finite).  Quotients are estimated and put right by exact products (bf16 times 14.75: 14 bits).
+__device__ __forceinline__ float3 kvq_params(float lo, float hi) {
   const float d = __fsub_rn(hi, lo), a = fmaxf(-lo, hi);
-  if (!(d < INFINITY)) return make_float2(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u));
-  // the quotient's rounding may land on a bf16 number just below the exact one (14 bits: exact product)
-  float s = bf16_up(__fdiv_rn(d, 14.75f));
-  if (__fmul_rn(s, 14.75f) < d) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
-  const float scale = fmaxf(fmaxf(s, bf16_up(a * 0.015625f)), 7.52316385e-37f);  // (2^-120)
-  float zero = 0.25f * floorf(4.f * __fdiv_rn(lo, scale));
+  if (!(d < INFINITY)) return make_float3(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u), 0.f);
+  float s = bf16_up(fmaxf(__fmul_rn(d, 1.f / 14.75f), 7.52316385e-37f));  // (2^-120)
+  const float next = __uint_as_float(__float_as_uint(s) + 0x10000u), prev = __uint_as_float(__float_as_uint(s) - 0x10000u);
+  if (__fmul_rn(s, 14.75f) < d)
+    s = next;
+  else if (__fmul_rn(prev, 14.75f) >= d)
+    s = prev;
+  const float scale = fmaxf(fmaxf(s, bf16_up(a * 0.015625f)), 7.52316385e-37f);
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  float zero = 0.25f * floorf(4.f * __fmul_rn(lo, inv));
   if (__fmul_rn(zero, scale) > lo)
     zero -= 0.25f;
   else if (__fmul_rn(zero + 0.25f, scale) <= lo)
     zero += 0.25f;
-  return make_float2(scale, zero);
+  return make_float3(scale, zero, inv);
 }
 
-// The code nearest to x / scale - zero, ties to even, exactly: an estimate by the reciprocal is off by far
-// less than a step, and the signs of x - (n +- 1/2 + zero) scale (one fused operation each, which keeps
-// a sign) put it right.
-__device__ __forceinline__ uint32_t kvq_code(float x, float scale, float inv, float zero) {
-  float n = rintf(__fsub_rn(__fmul_rn(x, inv), zero));
-  const float above = __fmaf_rn(-(n + 0.5f + zero), scale, x), below = __fmaf_rn(-(n - 0.5f + zero), scale, x);
-  const bool odd = static_cast<int>(n) & 1;
-  if (above > 0.f || (above == 0.f && odd))
-    n += 1.f;
-  else if (below < 0.f || (below == 0.f && odd))
-    n -= 1.f;
-  return static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f));
+// Codes of eight numbers of a group, one a nibble: the nearest to x / scale - zero, ties to even, exactly.  The
+// estimate by the reciprocal is off by less than 2^-15 of a step (|x / scale| <= 80, a few roundings), so what lies
+// farther from a tie is right; near a tie n +- 1/2 the sign of x - (n +- 1/2 + zero) scale, one fused operation with
+// an exact factor, which keeps a sign, decides.
+__device__ __forceinline__ uint32_t kvq_codes(const float* x, float scale, float zero, float inv) {
+  const float mul = inv * (1.f / 15.f), add = zero * (-1.f / 15.f);
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = __saturatef(fmaf(x[i], mul, add));  // code / 15 in 0..1
+    const float r = fmaf(y, 15.f, 12582912.f);            // (its last bits are the nearest whole number)
+    const float n = r - 12582912.f, f = fmaf(y, 15.f, -n);
+    uint32_t code = __float_as_uint(r) - 0x4b400000u;
+    if (fabsf(f) > 0.4999f) {
+      const float side = copysignf(1.f, f), e = side * __fmaf_rn(-(n + 0.5f * side + zero), scale, x[i]);
+      if (e > 0.f || (e == 0.f && (code & 1))) code += f > 0.f ? 1 : -1;
+    }
+    c += code << (4 * i);
+  }
+  return c;
 }
 
 }  // namespace cb

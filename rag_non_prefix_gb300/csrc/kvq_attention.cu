@@ -95,7 +95,15 @@ __device__ __forceinline__ uint32_t split_off(float& x, float& y) {
   return u;
 }
 
-// Quanta of a unit of tile `ti`, UNIT_COST without keys first, and the number of keys that its rows see.
+// Quanta of a unit that sees len keys: UNIT_COST without keys first.
+__device__ __forceinline__ int quanta_of(int len) { return UNIT_COST + (len + QUANTUM - 1) / QUANTUM; }
+
+// a / b for numbers that are hardly ever beyond 32 bits
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return a >> 32 | b >> 32 ? a / b : static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
+// Quanta of a unit of tile `ti`, and the number of keys that its rows see.
 __device__ __forceinline__ int tile_quanta(const KvqAttn& p, int ti, int rows, int& len) {
   const int seq = ti / p.tiles_per_seq, r0 = (ti - seq * p.tiles_per_seq) * rows;
   const int t1 = (min(r0 + rows, p.T * p.G) - 1) / p.G;
@@ -104,7 +112,7 @@ __device__ __forceinline__ int tile_quanta(const KvqAttn& p, int ti, int rows, i
   const int cap = p.c.max_pages * p.c.page_tokens;
   if (top >= cap) set_status(p.status, ST_RANGE);
   len = min(top, cap - 1) + 1;
-  return UNIT_COST + (len + QUANTUM - 1) / QUANTUM;
+  return quanta_of(len);
 }
 
 template <int DH> struct Words;  // a lane's key codes of one token: a word per group
@@ -117,30 +125,37 @@ template <typename T, int DH, int NT, int NP> struct Attn {
   static constexpr int STAGES = 4;
   static constexpr int ROW = DH + 4;  // pitch of the merge buffer, free of bank conflicts
   static constexpr int RING = AW * STAGES * BLK;
+  static constexpr int QUERIES = NT * NP * NG * 2 * 32 * 8 + NT * NG * 32 * 8;
   static constexpr int MERGE = AW * R * ROW * 4;
   static constexpr int WEIGHTS = R * KVQ_MAX_CTAS * 4;  // of the parts of a unit
-  static constexpr int SMEM = std::max(std::max(RING, MERGE), WEIGHTS);
+  static constexpr int WORK = std::max(std::max(RING, MERGE), WEIGHTS);
+  static constexpr int SMEM = WORK + QUERIES;
 
   static constexpr bool CENTRED = NP > 1;
   static constexpr float OFF = CENTRED ? 8.f : -16.f;  // what the operands' offset leaves of a zero
 
   int lane;
   uint32_t mask, sixteen, minus16[4];  // (an operand of four registers)
-  uint32_t qb[NT][NP][NG][4];  // query operands: per group two k-steps of (b0, b1)
-  float qs[NT][NG][2];         // sums of the query's group, of this lane's two columns
+  const uint2* qb;   // this lane's query operands in shared memory: [NT][NP][NG][2] pairs (b0, b1), 32 lanes apart
+  const float2* qs;  // sums of the queries' groups, of this lane's two columns: [NT][NG], 32 lanes apart
   float o[NT][DH / 16][4];
   float corr[NT][NG][2];  // (fp32) this lane's keys' sums with the zeros
   float m[NT][2], l[NT][2];
   int lim[NT][2];  // last key of this lane's two columns
 
-  __device__ __forceinline__ void load_q(const KvqAttn& p, int seq, int r0, int head) {
+  // The tile's queries into `dst` (by all warps), and this lane's state.
+  __device__ __forceinline__ void load_q(const KvqAttn& p, int seq, int r0, int head, uint8_t* dst) {
     // read once: the compiler would fetch and rebuild them in every block
     asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
     asm volatile("mov.u32 %0, 0x00780078;" : "=r"(mask));
     asm volatile("mov.u32 %0, 0x41804180;" : "=r"(sixteen));
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("mov.u32 %0, 0xc180c180;" : "=r"(minus16[i]));
-    const int rr = lane >> 2, tq = lane & 3, rows = p.T * p.G;
+    const int rr = lane >> 2, tq = lane & 3, rows = p.T * p.G, w = threadIdx.x >> 5;
+    uint2* b = reinterpret_cast<uint2*>(dst) + lane;
+    float2* sums = reinterpret_cast<float2*>(dst + NT * NP * NG * 2 * 32 * 8) + lane;
+    qb = b;
+    qs = sums;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = r0 + nt * 8 + rr;
@@ -148,8 +163,8 @@ template <typename T, int DH, int NT, int NP> struct Attn {
       const int t = in ? row / p.G : 0, g = in ? row - t * p.G : 0;
       const T* src = static_cast<const T*>(p.q) + (static_cast<long long>(seq) * p.T + t) * p.ldq +
                      static_cast<long long>(head * p.G + g) * DH + 8 * tq;
-#pragma unroll
-      for (int grp = 0; grp < NG; ++grp) {
+      if (w < NG) {  // a warp for each group
+        const int grp = w;
         float f[8] = {};
         if (in) load8(src + 32 * grp, f);
         float sum = 0.f;
@@ -157,12 +172,16 @@ template <typename T, int DH, int NT, int NP> struct Attn {
         for (int i = 0; i < 8; ++i) sum += f[i];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[nt][grp][0] = __shfl_sync(0xffffffffu, sum, 8 * tq);
-        qs[nt][grp][1] = __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
+        const float s0 = __shfl_sync(0xffffffffu, sum, 8 * tq), s1 = __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
+        sums[(nt * NG + grp) * 32] = make_float2(s0, s1);
 #pragma unroll
-        for (int np = 0; np < NP; ++np)
+        for (int np = 0; np < NP; ++np) {
+          uint32_t u[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qb[nt][np][grp][i] = split_off(f[i], f[i + 4]);
+          for (int i = 0; i < 4; ++i) u[i] = split_off(f[i], f[i + 4]);
+          b[((nt * NP + np) * NG + grp) * 2 * 32] = make_uint2(u[0], u[1]);
+          b[(((nt * NP + np) * NG + grp) * 2 + 1) * 32] = make_uint2(u[2], u[3]);
+        }
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -193,59 +212,66 @@ template <typename T, int DH, int NT, int NP> struct Attn {
     return min(x, __shfl_xor_sync(0xffffffffu, x, 2));
   }
 
-  // Scores (times 1 / scale) of the 16 keys of a block in shared memory: keys rr and rr + 8, columns 2 tq and 2 tq + 1.
-  __device__ __forceinline__ void scores(const uint8_t* blk, float (&s)[NT][4]) const {
+  // Scores (times 1 / scale) of the 16 keys of each of two blocks in shared memory: keys rr and rr + 8, columns
+  // 2 tq and 2 tq + 1.
+  __device__ __forceinline__ void scores(const uint8_t* blk0, const uint8_t* blk1, float (&s)[2][NT][4]) const {
     const int rr = lane >> 2, tq = lane & 3;
-    uint32_t w[2][NG], ks[2][NG / 2], kz[2][NG / 2];
+    uint32_t w[2][2][NG], ks[2][2][NG / 2], kz[2][2][NG / 2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      typedef typename Words<DH>::type W;
-      *reinterpret_cast<W*>(w[h]) = *reinterpret_cast<const W*>(blk + (rr + 8 * h) * (DH / 2) + tq * 4 * NG);
-      const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 4 * NG * (rr + 8 * h));
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* blk = u ? blk1 : blk0;
 #pragma unroll
-      for (int i = 0; i < NG / 2; ++i) {
-        ks[h][i] = prm[i];
-        kz[h][i] = prm[NG / 2 + i];
+      for (int h = 0; h < 2; ++h) {
+        typedef typename Words<DH>::type W;
+        *reinterpret_cast<W*>(w[u][h]) = *reinterpret_cast<const W*>(blk + (rr + 8 * h) * (DH / 2) + tq * 4 * NG);
+        const uint32_t* prm = reinterpret_cast<const uint32_t*>(blk + 16 * DH + 4 * NG * (rr + 8 * h));
+#pragma unroll
+        for (int i = 0; i < NG / 2; ++i) {
+          ks[u][h][i] = prm[i];
+          kz[u][h][i] = prm[NG / 2 + i];
+        }
       }
     }
-    // (the groups' products side by side: each waits for the one before it in its own accumulator only)
-    float c[NT][NG][4];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const float z0 = (g & 1 ? hi_f(kz[0][g / 2]) : lo_f(kz[0][g / 2])) + OFF;
-      const float z1 = (g & 1 ? hi_f(kz[1][g / 2]) : lo_f(kz[1][g / 2])) + OFF;
+      auto half = [&](uint32_t x) { return g & 1 ? hi_f(x) : lo_f(x); };
+      float c[2][NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        c[nt][g][0] = z0 * qs[nt][g][0];
-        c[nt][g][1] = z0 * qs[nt][g][1];
-        c[nt][g][2] = z1 * qs[nt][g][0];
-        c[nt][g][3] = z1 * qs[nt][g][1];
+        const float2 q = qs[(nt * NG + g) * 32];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[u][nt][i] = (half(kz[u][i >> 1][g / 2]) + OFF) * (i & 1 ? q.y : q.x);
       }
-    }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const uint32_t a0 = nib<0>(w[0][g]), a1 = nib<0>(w[1][g]), a2 = nib<1>(w[0][g]), a3 = nib<1>(w[1][g]);
+      for (int step = 0; step < 2; ++step) {
+        uint32_t a[2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int np = 0; np < NP; ++np) mma_bf16(c[nt][g], a0, a1, a2, a3, qb[nt][np][g][0], qb[nt][np][g][1]);
-    }
+          for (int h = 0; h < 2; ++h) {
+            a[u][h] = step ? nib<2>(w[u][h][g]) : nib<0>(w[u][h][g]);
+            a[u][2 + h] = step ? nib<3>(w[u][h][g]) : nib<1>(w[u][h][g]);
+          }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const uint32_t a0 = nib<2>(w[0][g]), a1 = nib<2>(w[1][g]), a2 = nib<3>(w[0][g]), a3 = nib<3>(w[1][g]);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int np = 0; np < NP; ++np) {
+            const uint2 b = qb[(((nt * NP + np) * NG + g) * 2 + step) * 32];
 #pragma unroll
-        for (int np = 0; np < NP; ++np) mma_bf16(c[nt][g], a0, a1, a2, a3, qb[nt][np][g][2], qb[nt][np][g][3]);
-    }
+            for (int u = 0; u < 2; ++u) mma_bf16(c[u][nt], a[u][0], a[u][1], a[u][2], a[u][3], b.x, b.y);
+          }
+      }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const float s0 = g & 1 ? hi_f(ks[0][g / 2]) : lo_f(ks[0][g / 2]), s1 = g & 1 ? hi_f(ks[1][g / 2]) : lo_f(ks[1][g / 2]);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[nt][i] = g == 0 ? (i < 2 ? s0 : s1) * c[nt][g][i] : fmaf(i < 2 ? s0 : s1, c[nt][g][i], s[nt][i]);
+          for (int i = 0; i < 4; ++i) {
+            const float k = half(ks[u][i >> 1][g / 2]);
+            s[u][nt][i] = g == 0 ? k * c[u][nt][i] : fmaf(k, c[u][nt][i], s[u][nt][i]);
+          }
     }
   }
 
@@ -358,8 +384,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
   __device__ __forceinline__ void two_blocks(const uint8_t* blk0, const uint8_t* blk1, int key0, uint32_t there, float scale_log2) {
     const int rr = lane >> 2;
     float s[2][NT][4];
-    scores(blk0, s[0]);
-    scores(blk1, s[1]);
+    scores(blk0, blk1, s);
     bool up = false;
     uint32_t dead[2] = {0, 0};
 #pragma unroll
@@ -431,7 +456,9 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   typedef Attn<T, DH, NT, NP> A;
   constexpr int R = A::R, ROW = A::ROW;
   extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int TILES = 256;
   __shared__ long long scan[AW * 32 + 1];
+  __shared__ int tile_len[TILES];
   __shared__ int first_tile;
   __shared__ long long first_base;
   __shared__ float part_m[AW][R], part_l[AW][R], wts[AW][R], row_m[R], row_l[R];
@@ -447,7 +474,15 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   for (int i = tid * per; i < min(p.n_tiles, (tid + 1) * per); ++i) {
     int len;
     mine += tile_quanta(p, i, R, len);
+    if (i < TILES) tile_len[i] = len;
   }
+  // how many keys a tile sees: kept for the first ones, looked up again for the others
+  auto len_of = [&](int i) {
+    int len;
+    if (i < TILES) return tile_len[i];
+    tile_quanta(p, i, R, len);
+    return len;
+  };
   scan[tid + 1] = mine * heads;
   if (tid == 0) scan[0] = 0;
   __syncthreads();
@@ -467,16 +502,22 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   }
   __syncthreads();
   const long long total = scan[AW * 32];
-  const long long n = min(static_cast<long long>(gridDim.x), (total + MIN_SHARE - 1) / MIN_SHARE);
+  const long long n = min(static_cast<long long>(gridDim.x), quotient(total + MIN_SHARE - 1, MIN_SHARE));
   if (blockIdx.x >= n) return;
-  long long cur = total * blockIdx.x / n;
-  const long long end = total * (blockIdx.x + 1) / n;
+  // the first `rest` shares are one quantum longer than `share`
+  const long long share = quotient(total, n), rest = total - share * n;
+  auto begin_of = [&](long long c) { return share * c + min(c, rest); };
+  auto owner_of = [&](long long x) {
+    const long long longer = rest * (share + 1);
+    return static_cast<int>(x < longer ? quotient(x, share + 1) : rest + quotient(x - longer, share));
+  };
+  long long cur = begin_of(blockIdx.x);
+  const long long end = begin_of(blockIdx.x + 1);
   if (scan[tid] <= cur && cur < scan[tid + 1]) {
     long long base = scan[tid];
     int i = tid * per;
     for (;; ++i) {
-      int len;
-      const long long q = static_cast<long long>(tile_quanta(p, i, R, len)) * heads;
+      const long long q = static_cast<long long>(quanta_of(len_of(i))) * heads;
       if (cur < base + q) break;
       base += q;
     }
@@ -489,16 +530,12 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   const long long begin = cur;
 
   while (cur < end) {
-    int len;
-    const int nq = tile_quanta(p, ti, R, len);
-    const int head = static_cast<int>((cur - base) / nq);
+    const int len = len_of(ti), nq = quanta_of(len);
+    const int head = static_cast<int>(quotient(cur - base, nq));
     const long long unit = base + static_cast<long long>(head) * nq;
     const int q0 = static_cast<int>(cur - unit), q1 = static_cast<int>(min(static_cast<long long>(nq), end - unit));
     const int seq = ti / p.tiles_per_seq, r0 = (ti - seq * p.tiles_per_seq) * R;
 
-    A a;
-    a.load_q(p, seq, r0, head);
-    const int all = a.seen_by_all(p, r0);
     const int blocks = min((len + KVQ_BLOCK - 1) / KVQ_BLOCK, (q1 - UNIT_COST) * AW), per_page = p.c.page_tokens / KVQ_BLOCK;
     const int b0 = max(0, q0 - UNIT_COST) * AW + w, count = blocks > b0 ? (blocks - b0 + AW - 1) / AW : 0;
     uint8_t* ring = smem + w * A::STAGES * A::BLK;
@@ -520,7 +557,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
         }
         const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<u64>(at), i & 31));
         const int stage = i % A::STAGES;
-        if (src) copy_block<DH>(ring_u + stage * A::BLK, src, a.lane);
+        if (src) copy_block<DH>(ring_u + stage * A::BLK, src, lane);
         there = (there & ~(1u << stage)) | (src ? 1u << stage : 0u);
       }
     };
@@ -531,6 +568,10 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
     };
 #pragma unroll
     for (int i = 0; i < A::STAGES - 2; i += 2) fetch_two(i);
+    A a;
+    a.load_q(p, seq, r0, head, smem + A::WORK);
+    __syncthreads();
+    const int all = a.seen_by_all(p, r0);
     for (int i = 0; i < count; i += 2) {
       __syncwarp();  // (every lane is done with the stages that are written next)
       fetch_two(i + A::STAGES - 2);
@@ -612,8 +653,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
     }
     if (!whole) {
       if (tid < R) *reinterpret_cast<float2*>(slot + MAX_ROWS * DH + 2 * tid) = make_float2(row_m[tid], row_l[tid]);
-      // CTAs of this unit: share c holds quantum x when total c / n <= x < total (c + 1) / n (rounded down)
-      const int c0 = static_cast<int>(((unit + 1) * n - 1) / total), c1 = static_cast<int>(((unit + nq) * n - 1) / total);
+      const int c0 = owner_of(unit), c1 = owner_of(unit + nq - 1);  // CTAs of this unit
       __threadfence();
       __syncthreads();
       if (tid == 0) is_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
@@ -624,7 +664,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
         // parts c0..c1: the first in its CTA's first or later slot, the others in their CTA's first; a warp's row
         // at a time, four channels a lane
         const float* parts = p.parts + 2 * static_cast<size_t>(c0) * slot_floats(DH);
-        const int shift = unit != total * c0 / n ? slot_floats(DH) : 0, np = c1 - c0 + 1;
+        const int shift = unit != begin_of(c0) ? slot_floats(DH) : 0, np = c1 - c0 + 1;
         float* wt = reinterpret_cast<float*>(smem) + w * (A::WEIGHTS / 4 / AW);
         for (int row = w; row < R && r0 + row < rows; row += AW) {
           float M = -INFINITY, L = 0.f;
