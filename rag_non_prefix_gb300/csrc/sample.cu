@@ -7,11 +7,15 @@
 // target", answered exactly: weights are whole numbers of 2^-44 (a weight's relative error is near
 // 2^-30: the exponent (x - max) / t log2(e) is carried in two fp32 numbers), and sums of whole numbers do not depend on their order.
 //
-// A row is held in the shared memory of the 1 to 8 CTAs of a cluster, read from memory once.  The running sums come
-// from a histogram of the counts or masses of 2048 ranges of (max - x) / t (a falling function of x); the
-// target's range is cut further by the bits of x and of the index while it holds more tokens than LIST,
-// then its tokens are sorted and summed one by one.  With top-k up to LIST tokens the mass is a matter of those
-// alone.
+// A row is held in the shared memory of the 1 to 8 CTAs of a cluster, read from memory once.  Three ways, each of
+// which leaves a row that it cannot settle to the next:
+//   1. top-k of up to a quarter of the cluster's threads: the k-th largest of the threads' own largest logits is a lower
+//      bound for the k-th largest of all, and not many more than k tokens pass it; they are sorted and summed one by one.
+//   2. all tokens: a histogram of near masses over 2048 ranges of (max - x) / t says in which range the
+//      target of top-p and that of the draw lie; one pass over the exact weights sums what lies before those
+//      ranges and collects their tokens, which are sorted; the exact sums show whether the ranges were the right ones.
+//   3. an exact histogram of counts or masses, whose range that holds the target is cut further by the bits of x and of the
+//      index until at most LIST tokens are left (flat rows, crowds of equal logits, top-k beyond 1.'s).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -60,13 +64,15 @@ struct Ctl {
 
 struct __align__(16) Smem {
   uint32_t hist[3][BUCKETS];
-  u64 tot[BUCKETS];  // first CTA: inclusive sums
-  u64 list[LIST];
-  u64 scan[LIST];
+  u64 tot[BUCKETS];     // first CTA: inclusive sums
+  u64 list[2][LIST];    // tokens that this CTA collected
   u64 warp[32];
-  u64 part[4];  // this CTA's: best token, mass over min_p, number of finite logits
+  u64 part[6];          // this CTA's: see the uses
   Ctl ctl[2];
-  int n_list;
+  int n_list[2];
+  // (the first CTA's own, while no histogram is in use)
+  __device__ u64* work() { return reinterpret_cast<u64*>(hist[1]); }
+  __device__ u64* sums() { return reinterpret_cast<u64*>(hist[2]); }
 };
 
 // order of the tokens as one number: by logit, then the lower index first
@@ -81,11 +87,6 @@ __device__ __forceinline__ float logit_of(u64 comp) {
 }
 __device__ __forceinline__ int index_of(u64 comp) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(comp)); }
 
-__device__ __forceinline__ u64 warp_max64(u64 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -136,9 +137,8 @@ template <typename T> struct Sampler {
     const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, __float2int_rn(p * 4294967296.f)));
     return some ? (static_cast<u64>(m) << (SHIFT - 30)) >> -(k >> 5) : 0;
   }
-  __device__ __forceinline__ int bucket0(float x) const {
-    return x == top ? 0 : min(BUCKETS - 1, static_cast<int>((top - x) * reach));
-  }
+  __device__ __forceinline__ float fall(float x) const { return x == top ? 0.f : (top - x) * reach; }
+  __device__ __forceinline__ int bucket0(float x) const { return min(BUCKETS - 1, static_cast<int>(fall(x))); }
 
   template <typename F> __device__ __forceinline__ void each(F f) const {
     // (whole warps walk together: f may use warp-wide operations)
@@ -266,28 +266,26 @@ template <typename T> struct Sampler {
     }
   }
 
-  // The tokens for which take() holds into the first CTA's list; their number for everyone.
-  template <typename P> __device__ __forceinline__ int gather(P take) {
-    if (tid == 0) s.n_list = 0;
-    cl.sync();
-    int* n = cl.map_shared_rank(&s.n_list, 0);
-    u64* list = cl.map_shared_rank(s.list, 0);
-    each([&](float x, int idx) {
-      const bool t = x > -INFINITY && take(x, idx);
-      const unsigned who = __ballot_sync(0xffffffffu, t);
-      if (who == 0) return;
-      int at = 0;
-      if (lane == 0) at = atomicAdd(n, __popc(who));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-      if (t && at < LIST) list[at] = composite(x, idx);
-    });
-    cl.sync();
-    return *n;
+  // A token into one of this CTA's lists (the count goes on where the list is full).
+  __device__ __forceinline__ void collect(int which, float x, int idx) {
+    const int at = atomicAdd(&s.n_list[which], 1);
+    if (at < LIST) s.list[which][at] = composite(x, idx);
   }
-
-  // first CTA: sorts its list, largest first; thread i gets the i-th token, 0 beyond n
-  __device__ __forceinline__ u64 sorted(int n) {
-    u64 v = tid < n ? s.list[tid] : 0;
+  // After the CTAs have collected and the cluster has met: tokens in all lists.
+  __device__ __forceinline__ int collected(int which) const {
+    int n = 0;
+    for (int r = 0; r < ranks; ++r) n += *cl.map_shared_rank(&s.n_list[which], r);
+    return n;
+  }
+  // first CTA: all lists' tokens, largest first; thread i gets the i-th, 0 beyond their number (at most LIST)
+  __device__ __forceinline__ u64 sorted(int which, int n) {
+    u64 v = 0;
+    for (int r = 0, before = 0; r < ranks; ++r) {
+      const int m = *cl.map_shared_rank(&s.n_list[which], r);
+      if (tid >= before && tid < before + m) v = cl.map_shared_rank(&s.list[which][0], r)[tid - before];
+      before += m;
+    }
+    u64* work = s.work();
     int size = 32;
     while (size < n) size <<= 1;
     for (int k = 2; k <= size; k <<= 1) {
@@ -295,9 +293,9 @@ template <typename T> struct Sampler {
         u64 o;
         if (j >= 32) {
           __syncthreads();
-          s.list[tid] = v;
+          work[tid] = v;
           __syncthreads();
-          o = s.list[tid ^ j];
+          o = work[tid ^ j];
         } else {
           o = __shfl_xor_sync(0xffffffffu, v, j);
         }
@@ -305,7 +303,19 @@ template <typename T> struct Sampler {
         v = keep_max ? max(v, o) : min(v, o);
       }
     }
+    __syncthreads();
     return v;
+  }
+
+  // The tokens for which take() holds into the lists 0; their number for everyone.
+  template <typename P> __device__ __forceinline__ int gather(P take) {
+    if (tid == 0) s.n_list[0] = 0;
+    __syncthreads();
+    each([&](float x, int idx) {
+      if (x > -INFINITY && take(x, idx)) collect(0, x, idx);
+    });
+    cl.sync();
+    return collected(0);
   }
 
   // Token at which the running count (of live tokens) or mass reaches target, from the histogram in tot (first CTA) of
@@ -325,7 +335,7 @@ template <typename T> struct Sampler {
       const int n = gather(in);
       if (n <= LIST) {
         if (rank == 0) {
-          const u64 t = sorted(n);
+          const u64 t = sorted(0, n);
           const u64 mine = MASS ? weight(logit_of(t)) : 1;  // (all lanes)
           const u64 w = tid < n ? mine : 0;
           const u64 incl = excl + block_scan(w);
@@ -371,7 +381,7 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   z.data = data;
   z.n_vec = n > 0 ? (off + n + VEC - 1) / VEC : 0;
   z.first = i0 - off;
-  u64 best = 0;
+  float own = -INFINITY;  // this thread's largest
   for (int v = tid; v < z.n_vec; v += ST) {
     T e[VEC];
     const int at = v * VEC - off;
@@ -383,37 +393,56 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     }
     reinterpret_cast<uint4*>(data)[v] = *reinterpret_cast<const uint4*>(e);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float x = to_f(e[i]);
-      if (x > -INFINITY) best = max(best, composite(x, i0 + at + i));
-    }
+    for (int i = 0; i < VEC; ++i) own = fmaxf(own, to_f(e[i]));  // (a NaN is passed over)
   }
-  best = warp_max64(best);
-  if (lane == 0) s.warp[warp] = best;
+  const uint32_t own_key = static_cast<uint32_t>(composite(own, 0) >> 32);
+  uint32_t key = __reduce_max_sync(0xffffffffu, own_key);
+  if (lane == 0) s.warp[warp] = key;
   __syncthreads();
   if (warp == 0) {
-    best = warp_max64(s.warp[lane]);
-    if (lane == 0) s.part[0] = best;
+    key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(s.warp[lane]));
+    if (lane == 0) s.part[0] = key;
   }
-  z.cl.sync();
-  best = 0;
-  for (int r = 0; r < z.ranks; ++r) best = max(best, *z.cl.map_shared_rank(&s.part[0], r));
-
   float t = a.temperature ? a.temperature[row] : 1.f;
   int k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
-  const float u = a.uniform ? a.uniform[row] : 0.f;
+  const float u = a.uniform[row];
   if (!(t > 0.f)) k = 1;
   if (k <= 0 || k >= a.vocab) k = a.vocab;
-  auto finish = [&](u64 comp) {
-    if (z.rank == 0 && tid == 0) a.out[row] = comp == 0 ? -1 : index_of(comp);
-    z.cl.sync();  // (no CTA leaves while another reads its shared memory)
-  };
-  if (best == 0 || k == 1) return finish(best);
+  z.cl.sync();
+  u64 best = 0;
+  for (int r = 0; r < z.ranks; ++r) best = max(best, *z.cl.map_shared_rank(&s.part[0], r));
+  z.top = logit_of(best << 32);
+  // (no CTA leaves while another reads its shared memory)
+  if (!(z.top > -INFINITY)) {
+    if (z.rank == 0 && tid == 0) a.out[row] = -1;
+    z.cl.sync();
+    return;
+  }
+  if (k == 1) {  // the largest logit's first token
+    unsigned at = 0xffffffffu;
+    z.each([&](float x, int idx) {
+      if (x == z.top) at = min(at, static_cast<unsigned>(idx));
+    });
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == 0) s.warp[warp] = at;
+    __syncthreads();
+    if (warp == 0) {
+      at = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(s.warp[lane]));
+      if (lane == 0) s.part[1] = at;
+    }
+    z.cl.sync();
+    if (z.rank == 0 && tid == 0) {
+      u64 first = s.part[1];
+      for (int r = 1; r < z.ranks; ++r) first = min(first, *z.cl.map_shared_rank(&s.part[1], r));
+      a.out[row] = static_cast<int>(first);
+    }
+    z.cl.sync();
+    return;
+  }
 
   t = fminf(fmaxf(t, 1e-20f), 1e20f);
   const double c = 1.4426950408889634 / static_cast<double>(t);
-  z.top = logit_of(best);
   z.c_hi = static_cast<float>(c);
   z.c_lo = static_cast<float>(c - static_cast<double>(z.c_hi));
   z.reach = BUCKETS / REACH / t;
@@ -426,10 +455,48 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   auto reach_u = [&](u64 m) {
     return min(m, static_cast<u64>(fmax(0.0, static_cast<double>(u) * static_cast<double>(m))) + 1);
   };
+  // first CTA, list 0 sorted: the token of a row whose first k tokens are in it
+  auto settle = [&](int n) {
+    const u64 tok = z.sorted(0, n);
+    const u64 w = z.weight(logit_of(tok));  // (all lanes)
+    const u64 mine = tid < k && tid < n ? w : 0;
+    u64* sums = s.sums();
+    const u64 incl = z.block_scan(mine);
+    sums[tid] = incl;
+    __syncthreads();
+    const u64 pm = reach_p(sums[ST - 1]);
+    // kept mass: of the shorter prefix
+    if (mine && incl - mine < pm && pm <= incl) s.part[2] = incl;
+    const u64 over = z.block_scan(mine >= z.floor_w ? mine : 0);
+    if (tid == ST - 1) s.part[3] = over;
+    __syncthreads();
+    const u64 want = reach_u(min(s.part[2], s.part[3]));
+    if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
+  };
 
   bool refined = false;
   auto all = [](float, int) { return true; };
   if (k < a.vocab) {
+    if (k <= z.ranks * (ST / 4)) {
+      // k / ranks of the threads' largest in each CTA, the least of these over the CTAs: at least k tokens pass it.
+      // (20 bits of it: a lower bound is enough)
+      const int each_k = (k + z.ranks - 1) / z.ranks;
+      uint32_t bound = 0;
+      for (int bit = 31; bit >= 12; --bit) {
+        const uint32_t more = bound | 1u << bit;
+        if (__syncthreads_count(own_key >= more) >= each_k) bound = more;
+      }
+      if (tid == 0) s.part[1] = bound;
+      z.cl.sync();
+      for (int r = 0; r < z.ranks; ++r) bound = min(bound, static_cast<uint32_t>(*z.cl.map_shared_rank(&s.part[1], r)));
+      const float least = logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32);
+      const int n_list = z.gather([&](float x, int) { return x >= least; });
+      if (n_list <= LIST) {
+        if (z.rank == 0) settle(n_list);
+        z.cl.sync();
+        return;
+      }
+    }
     z.template histogram<false>([&](float x, int) { return z.bucket0(x); });
     // the bucket of the k-th token; the last one's tokens weigh nothing
     if (z.rank == 0) {
@@ -438,42 +505,14 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
         s.ctl[z.phase].excl = 0;
       }
       __syncthreads();
-      for (int b = tid; b < BUCKETS - 1; b += ST) {
-        const u64 incl = s.tot[b], excl = b ? s.tot[b - 1] : 0;
-        if (excl < static_cast<u64>(k) && static_cast<u64>(k) <= incl) {
-          s.ctl[z.phase].bucket = b;
-          s.ctl[z.phase].count = static_cast<int>(min(incl, static_cast<u64>(a.vocab)));
-        }
-      }
+      z.find_bucket(k);
       __syncthreads();
     }
-    const Ctl ctl = z.decide();
-    if (ctl.bucket < BUCKETS - 1) {
-      const int b = ctl.bucket;
-      int n = ctl.count;
-      u64 last = 0;
-      if (k > LIST || n > LIST) {
-        last = z.template select<false>(k, all, &refined).comp;
-        n = k;
-      }
-      if (n <= LIST) {  // top-k's tokens (and the rest of their last bucket) fit: the first CTA has all that counts
-        z.gather([&](float x, int idx) { return last ? composite(x, idx) >= last : z.bucket0(x) <= b; });
-        if (z.rank == 0) {
-          const u64 tok = z.sorted(n);
-          const u64 w = z.weight(logit_of(tok));  // (all lanes)
-          const u64 mine = tid < k && tid < n ? w : 0;
-          s.scan[tid] = z.block_scan(mine);
-          __syncthreads();
-          const u64 pm = reach_p(s.scan[ST - 1]);
-          // kept mass: of the shorter prefix
-          const u64 over = z.block_scan(mine >= z.floor_w ? mine : 0);
-          if (tid == ST - 1) s.part[1] = over;
-          const u64 incl = s.scan[tid];
-          if (mine && incl - mine < pm && pm <= incl) s.part[2] = incl;
-          __syncthreads();
-          const u64 want = reach_u(min(s.part[1], s.part[2]));
-          if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
-        }
+    if (z.decide().bucket < BUCKETS - 1) {
+      const u64 last = z.template select<false>(k, all, &refined).comp;
+      if (k <= LIST) {  // the first CTA has all that counts
+        z.gather([&](float x, int idx) { return composite(x, idx) >= last; });
+        if (z.rank == 0) settle(k);
         z.cl.sync();
         return;
       }
@@ -483,6 +522,129 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
 
   const u64 eligible = z.eligible;
   auto live = [&](float x, int idx) { return eligible == 0 || composite(x, idx) >= eligible; };
+  if (eligible == 0) {
+    // near masses: each bucket's in 2^-15 of the weight at its upper end (the weight falls by 1/64 over a bucket:
+    // two terms of its series); a CTA has at most 65536 tokens
+    for (int i = tid; i < BUCKETS; i += ST) s.hist[0][i] = 0;
+    if (tid < 2) s.n_list[tid] = 0;
+    __syncthreads();
+    constexpr float STEP = REACH / BUCKETS;
+    z.each([&](float x, int) {
+      const float y = z.fall(x);
+      const int b = static_cast<int>(y);
+      if (x > -INFINITY && b < BUCKETS - 1) {
+        const float f = y - static_cast<float>(b);
+        const int v = __float2int_rn(fmaf(f, fmaf(f, 16384.f * STEP * STEP, -32768.f * STEP), 32768.f));
+        atomicAdd(&s.hist[0][b], static_cast<uint32_t>(v));
+      }
+    });
+    z.cl.sync();
+    if (z.rank == 0) {
+      u64 sum[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = 2 * tid + i;
+        float m = 0.f;
+        for (int r = 0; r < z.ranks; ++r) m += static_cast<float>(z.cl.map_shared_rank(&s.hist[0][0], r)[b]);
+        sum[i] = static_cast<u64>(m * exp2f(static_cast<float>(b) * (-STEP * 1.44269504f) + (SHIFT - 15)));
+      }
+      sum[1] += sum[0];
+      const u64 before = z.block_scan(sum[1]) - sum[1];
+      s.tot[2 * tid] = sum[0] + before;
+      s.tot[2 * tid + 1] = sum[1] + before;
+      __syncthreads();
+      const u64 near_all = s.tot[BUCKETS - 1];
+      const u64 near_p = reach_p(near_all);
+      // min_p's share: up to its own weight's place
+      u64 near_t = near_p;
+      if (z.floor_w > 0) {
+        const float y = -logf(fminf(min_p, 1.f)) / STEP;
+        near_t = min(near_t, max(1ull, s.tot[min(BUCKETS - 1, static_cast<int>(y))]));
+      }
+      const u64 near_u = max(1ull, reach_u(near_t));
+      for (int b = tid; b < BUCKETS; b += ST) {
+        const u64 incl = s.tot[b], excl = b ? s.tot[b - 1] : 0;
+        if (excl < near_p && near_p <= incl) s.ctl[z.phase].count = b;
+        if (excl < near_u && near_u <= incl) s.ctl[z.phase].bucket = b;
+      }
+      __syncthreads();
+    }
+    const Ctl guess = z.decide();
+    const bool with_p = top_p < 1.f;
+    const int bp = guess.count, bu = guess.bucket;
+    // exact sums: all, before bp, before bu, over min_p; and the tokens of the two ranges
+    u64 sum[4] = {};
+    z.each([&](float x, int idx) {
+      const u64 w = z.weight(x);
+      const int b = z.bucket0(x);
+      sum[0] += w;
+      sum[1] += b < bp ? w : 0;
+      sum[2] += b < bu ? w : 0;
+      sum[3] += w >= z.floor_w ? w : 0;
+      if (w > 0) {
+        if (b == bu) z.collect(0, x, idx);
+        if (with_p && b == bp && bp != bu) z.collect(1, x, idx);
+      }
+    });
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u64 v = warp_sum64(sum[i]);
+      if (lane == 0) s.hist[0][(i * 32 + warp) * 2] = static_cast<uint32_t>(v), s.hist[0][(i * 32 + warp) * 2 + 1] = static_cast<uint32_t>(v >> 32);
+    }
+    __syncthreads();
+    if (warp < 4) {
+      const u64 v = warp_sum64(reinterpret_cast<const u64*>(s.hist[0])[warp * 32 + lane]);
+      if (lane == 0) s.part[1 + warp] = v;
+    }
+    z.cl.sync();
+    const int n_u = z.collected(0), n_p = bp == bu ? n_u : z.collected(1);
+    // (every CTA comes to the same result, the first one's below)
+    if (z.rank == 0) {
+      if (tid == 0) s.ctl[z.phase].count = 0;  // settled
+      u64 total[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        total[i] = 0;
+        for (int r = 0; r < z.ranks; ++r) total[i] += *z.cl.map_shared_rank(&s.part[1 + i], r);
+      }
+      // tokens in a list, the number of them: thread i's token, weight and running mass
+      u64 tok = 0, mine = 0, incl = 0;
+      auto load = [&](int which, int n_list, u64 before) {
+        tok = z.sorted(which, n_list);
+        const u64 w = z.weight(logit_of(tok));  // (all lanes)
+        mine = tid < n_list ? w : 0;
+        incl = before + z.block_scan(mine);
+      };
+      u64 mass = total[3];
+      const u64 pm = reach_p(total[0]);
+      bool ok = true;
+      if (with_p && pm <= mass) {
+        ok = n_p <= LIST;
+        if (ok) {
+          load(bp == bu ? 0 : 1, n_p, total[1]);
+          if (tid == 0) s.part[0] = 0;
+          __syncthreads();
+          if (mine && incl - mine < pm && pm <= incl) s.part[0] = incl;
+          __syncthreads();
+          mass = s.part[0];
+          ok = mass > 0;
+        }
+      }
+      if (ok && n_u <= LIST) {
+        load(0, n_u, total[2]);
+        const u64 want = reach_u(mass);
+        if (mine && incl - mine < want && want <= incl) {
+          a.out[row] = index_of(tok);
+          s.ctl[z.phase].count = 1;
+        }
+      }
+      __syncthreads();
+    }
+    if (z.decide().count) {
+      z.cl.sync();
+      return;
+    }
+  }
   auto masses = [&] { z.template histogram<true>([&](float x, int idx) { return live(x, idx) ? z.bucket0(x) : -1; }); };
   masses();
   if (z.rank == 0 && tid == 0) {
@@ -500,7 +662,8 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     if (refined) masses();
   }
   const u64 comp = z.template select<true>(reach_u(mass), live, &refined).comp;
-  finish(comp);
+  if (z.rank == 0 && tid == 0) a.out[row] = index_of(comp);
+  z.cl.sync();
 }
 
 template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s) {
@@ -513,10 +676,10 @@ template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s)
   if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>),
                                  static_cast<int>(sizeof(Smem)) + MAX_DATA + 48, configured)) != cudaSuccess)
     return e;
-  // CTAs of a row: as many as its size needs, and more while the rows leave SMs idle
+  // CTAs of a row: as many as its size needs, and more while all rows' CTAs still run at once
   int ranks = 1;
   auto chunk = [&](int r) { return (a.vocab + r - 1) / r; };
-  while (ranks < 8 && (chunk(ranks) * sizeof(T) > MAX_DATA || (rows * ranks < sms && chunk(ranks) > 4096))) ranks *= 2;
+  while (ranks < 8 && (chunk(ranks) * sizeof(T) > MAX_DATA || (2ll * rows * ranks <= sms && chunk(ranks) > 4096))) ranks *= 2;
   a.chunk = chunk(ranks);
   const size_t smem = sizeof(Smem) + (a.chunk * sizeof(T) + 47) / 16 * 16;
   cudaLaunchConfig_t cfg = {};
