@@ -68,6 +68,9 @@ struct __align__(16) Smem {
   u64 list[2][LIST];    // tokens that this CTA collected
   u64 warp[32];
   u64 part[6];          // this CTA's: see the uses
+  u64 want;             // a target (64-bit floating point is slow: one thread computes it for all)
+  u64 floor_w;
+  float c_hi, c_lo;
   Ctl ctl[2];
   int n_list[2];
   // (the first CTA's own, while no histogram is in use)
@@ -395,6 +398,17 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
 #pragma unroll
     for (int i = 0; i < VEC; ++i) own = fmaxf(own, to_f(e[i]));  // (a NaN is passed over)
   }
+  float t = a.temperature ? a.temperature[row] : 1.f;
+  int k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
+  const float u = a.uniform[row];
+  if (tid == ST - 1) {
+    const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(t, 1e-20f), 1e20f));
+    s.c_hi = static_cast<float>(c);
+    s.c_lo = static_cast<float>(c - static_cast<double>(s.c_hi));
+    const u64 one = 1ull << SHIFT;
+    s.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
+  }
   const uint32_t own_key = static_cast<uint32_t>(composite(own, 0) >> 32);
   uint32_t key = __reduce_max_sync(0xffffffffu, own_key);
   if (lane == 0) s.warp[warp] = key;
@@ -403,10 +417,6 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(s.warp[lane]));
     if (lane == 0) s.part[0] = key;
   }
-  float t = a.temperature ? a.temperature[row] : 1.f;
-  int k = a.top_k ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
-  const float u = a.uniform[row];
   if (!(t > 0.f)) k = 1;
   if (k <= 0 || k >= a.vocab) k = a.vocab;
   z.cl.sync();
@@ -442,18 +452,24 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   }
 
   t = fminf(fmaxf(t, 1e-20f), 1e20f);
-  const double c = 1.4426950408889634 / static_cast<double>(t);
-  z.c_hi = static_cast<float>(c);
-  z.c_lo = static_cast<float>(c - static_cast<double>(z.c_hi));
+  z.c_hi = s.c_hi;
+  z.c_lo = s.c_lo;
   z.reach = BUCKETS / REACH / t;
-  const u64 one = 1ull << SHIFT;
-  z.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
-  // targets of a mass m: the smallest whole numbers not below top_p m, and above u m
+  z.floor_w = s.floor_w;
+  // targets of a mass m: the smallest whole numbers not below top_p m, and above u m (whole blocks call these)
+  auto one_thread = [&](auto f) {
+    __syncthreads();
+    if (tid == 0) s.want = f();
+    __syncthreads();
+    return s.want;
+  };
   auto reach_p = [&](u64 m) {
-    return top_p >= 1.f || !(top_p == top_p) ? m : max(1ull, min(m, static_cast<u64>(ceil(fmax(0.0, static_cast<double>(top_p) * static_cast<double>(m))))));
+    return top_p >= 1.f || !(top_p == top_p) ? m : one_thread([&] {
+      return max(1ull, min(m, static_cast<u64>(ceil(fmax(0.0, static_cast<double>(top_p) * static_cast<double>(m))))));
+    });
   };
   auto reach_u = [&](u64 m) {
-    return min(m, static_cast<u64>(fmax(0.0, static_cast<double>(u) * static_cast<double>(m))) + 1);
+    return one_thread([&] { return min(m, static_cast<u64>(fmax(0.0, static_cast<double>(u) * static_cast<double>(m))) + 1); });
   };
   // first CTA, list 0 sorted: the token of a row whose first k tokens are in it
   auto settle = [&](int n) {
