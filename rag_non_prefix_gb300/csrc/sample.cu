@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -51,6 +52,7 @@ struct SampleArgs {
   const int32_t* top_k;
   int32_t* out;
   int chunk;  // tokens per CTA
+  int rows, wave;  // rows whose CTAs run at once
 };
 
 // What the cluster's first CTA decides for all of them.
@@ -121,41 +123,75 @@ template <typename T> struct Sampler {
     tab = kExp2[lane];
   }
 
-  // Weight of a token, 2^SHIFT for the largest.  All lanes of a warp take part.
+  // Weight of a token, 2^SHIFT for the largest (top is finite).  All lanes of a warp take part.
   __device__ __forceinline__ u64 weight(float x) const {
-    const float d = x == top ? 0.f : x - top;
+    const float d = x - top;
     // the difference's own rounding (two-sum), then the exponent in two parts
     const float b = d - x, de = (x - (d - b)) + (-top - b);
-    float e = d * c_hi;
-    const float el = fmaf(d, c_hi, -e) + fmaf(d, c_lo, (x == top ? 0.f : de) * c_hi);
-    const bool some = e > -46.f;
-    e = some ? e : 0.f;
-    // e = k / 32 + r: 2^(k / 32) from the table, 2^r - 1 by its series (|r ln 2| < 0.011: terms to the fourth)
-    const float km = fmaf(e, 32.f, 12582912.f);
+    const float e = d * c_hi, el = fmaf(d, c_hi, -e) + fmaf(d, c_lo, de * c_hi);
+    // e = k / 32 + r: 2^(k / 32) from the table, 2^r - 1 by its series (|r ln 2| < 0.011: terms to the fourth); below
+    // 2^-47 every 32 bits shifted that far are 0, whatever r is
+    const float ec = fmaxf(e, -47.f), km = fmaf(ec, 32.f, 12582912.f);
     const int k = __float_as_int(km) - 0x4b400000;
-    const float r = fmaf(km - 12582912.f, -0.03125f, e) + (some ? el : 0.f);
+    const float r = fmaf(km - 12582912.f, -0.03125f, ec) + el;
     const float y = fmaf(r, 0.693147182f, r * -1.90465421e-9f);
     const float p = fmaf(y * y, fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f), y);
     const int t = static_cast<int>(__shfl_sync(0xffffffffu, tab, k & 31));
     const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, __float2int_rn(p * 4294967296.f)));
-    return some ? (static_cast<u64>(m) << (SHIFT - 30)) >> -(k >> 5) : 0;
+    return (static_cast<u64>(m) << (SHIFT - 30)) >> -(k >> 5);
   }
-  __device__ __forceinline__ float fall(float x) const { return x == top ? 0.f : (top - x) * reach; }
-  __device__ __forceinline__ int bucket0(float x) const { return min(BUCKETS - 1, static_cast<int>(fall(x))); }
+  // (max - x) / t in buckets, at most the last one; that is 2^-46 and weighs nothing
+  __device__ __forceinline__ float fall(float x) const { return fminf((top - x) * reach, static_cast<float>(BUCKETS - 1)); }
+  __device__ __forceinline__ int bucket0(float x) const {  // the nearest whole number, from a float's last bits
+    return __float_as_int(fall(x) + 8388608.f) & (BUCKETS - 1);
+  }
 
+  // f(logit, index) for all of this CTA's tokens (and some places of -infinity), whole warps together: f may use
+  // warp-wide operations.
   template <typename F> __device__ __forceinline__ void each(F f) const {
-    // (whole warps walk together: f may use warp-wide operations)
-    for (int v0 = warp * 32; v0 < n_vec; v0 += ST) {
-      const int v = v0 + lane;
+    for (int v = tid; v < n_vec; v += ST) {  // (n_vec is a multiple of 32)
       T e[VEC];
-      if (v < n_vec)
-        *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(data)[v];
+      *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(data)[v];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float x = v < n_vec ? to_f(e[i]) : -INFINITY;
-        f(x != x ? -INFINITY : x, first + v * VEC + i);
+      for (int i = 0; i < VEC; ++i) f(to_f(e[i]), first + v * VEC + i);
+    }
+  }
+  // The tokens of at least `least` into list 0: a vector's largest first.
+  __device__ __forceinline__ void collect_from(float least) {
+    for (int v = tid; v < n_vec; v += ST) {
+      uint4 e = reinterpret_cast<const uint4*>(data)[v];
+      float m;
+      largest(e, m, true);
+      if (m < least) continue;
+      const T* x = reinterpret_cast<const T*>(data) + v * VEC;
+      for (int i = 0; i < VEC; ++i)
+        if (to_f(x[i]) >= least) collect(0, to_f(x[i]), first + v * VEC + i);
+    }
+  }
+  // The largest number of a vector into m (if `fresh`, else of m too); a NaN becomes -infinity.
+  static __device__ __forceinline__ void largest(uint4& e, float& m, bool fresh) {
+    uint32_t w[4] = {e.x, e.y, e.z, e.w};
+    if (sizeof(T) == 2) {
+      __nv_bfloat162 top2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+        const uint32_t good = __heq2_mask(h, h);
+        w[i] = (w[i] & good) | (0xff80ff80u & ~good);
+        const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+        top2 = i == 0 ? c : __hmax2(top2, c);
+      }
+      const float2 f = __bfloat1622float2(top2);
+      m = fresh ? fmaxf(f.x, f.y) : fmaxf(m, fmaxf(f.x, f.y));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = __uint_as_float(w[i]);
+        w[i] = x == x ? w[i] : 0xff800000u;
+        m = i == 0 && fresh ? __uint_as_float(w[0]) : fmaxf(m, __uint_as_float(w[i]));
       }
     }
+    e = make_uint4(w[0], w[1], w[2], w[3]);
   }
 
   __device__ __forceinline__ Ctl decide() {  // what the first CTA wrote into ctl[phase], for everyone
@@ -291,13 +327,15 @@ template <typename T> struct Sampler {
     u64* work = s.work();
     int size = 32;
     while (size < n) size <<= 1;
-    for (int k = 2; k <= size; k <<= 1) {
+    // (the warps that hold tokens only, with a barrier of their own)
+    auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"r"(size) : "memory"); };
+    for (int k = 2; tid < size && k <= size; k <<= 1) {
       for (int j = k >> 1; j > 0; j >>= 1) {
         u64 o;
         if (j >= 32) {
-          __syncthreads();
+          meet();
           work[tid] = v;
-          __syncthreads();
+          meet();
           o = work[tid ^ j];
         } else {
           o = __shfl_xor_sync(0xffffffffu, v, j);
@@ -382,21 +420,38 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   // vectors as they lie in memory: those at the ends may hold a neighbour's elements
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T), n = i1 - i0;
   z.data = data;
-  z.n_vec = n > 0 ? (off + n + VEC - 1) / VEC : 0;
+  z.n_vec = n > 0 ? ((off + n + VEC - 1) / VEC + 31) / 32 * 32 : 0;
   z.first = i0 - off;
+  // the row that takes this one's place on the SM, on its way into the second-level cache meanwhile
+  if (tid == 0 && row + a.wave < a.rows && n > 0) {
+    const uintptr_t p = (reinterpret_cast<uintptr_t>(src + static_cast<long long>(a.wave) * a.ld) + 15) & ~static_cast<uintptr_t>(15);
+    const uint32_t bytes = (static_cast<uint32_t>(n) * sizeof(T) - 15) / 16 * 16;
+    if (n * sizeof(T) >= 32) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+  }
   float own = -INFINITY;  // this thread's largest
-  for (int v = tid; v < z.n_vec; v += ST) {
-    T e[VEC];
-    const int at = v * VEC - off;
-    if (at >= 0 && at + VEC <= n) {
-      *reinterpret_cast<uint4*>(e) = __ldg(reinterpret_cast<const uint4*>(src + at));
-    } else {
+  constexpr int BATCH = 4;
+  for (int v0 = tid; v0 < z.n_vec; v0 += BATCH * ST) {
+    uint4 e[BATCH];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = at + i >= 0 && at + i < n ? src[at + i] : from_f<T>(-INFINITY);
+    for (int j = 0; j < BATCH; ++j) {
+      const int v = v0 + j * ST, at = v * VEC - off;
+      if (v < z.n_vec && at >= 0 && at + VEC <= n) {
+        e[j] = __ldg(reinterpret_cast<const uint4*>(src + at));
+      } else if (v < z.n_vec) {
+        T x[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = at + i >= 0 && at + i < n ? src[at + i] : from_f<T>(-INFINITY);
+        e[j] = *reinterpret_cast<const uint4*>(x);
+      }
     }
-    reinterpret_cast<uint4*>(data)[v] = *reinterpret_cast<const uint4*>(e);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) own = fmaxf(own, to_f(e[i]));  // (a NaN is passed over)
+    for (int j = 0; j < BATCH; ++j) {
+      const int v = v0 + j * ST;
+      if (v < z.n_vec) {
+        z.largest(e[j], own, false);
+        reinterpret_cast<uint4*>(data)[v] = e[j];
+      }
+    }
   }
   float t = a.temperature ? a.temperature[row] : 1.f;
   int k = a.top_k ? a.top_k[row] : 0;
@@ -409,8 +464,7 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     const u64 one = 1ull << SHIFT;
     s.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
   }
-  const uint32_t own_key = static_cast<uint32_t>(composite(own, 0) >> 32);
-  uint32_t key = __reduce_max_sync(0xffffffffu, own_key);
+  uint32_t key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(composite(own, 0) >> 32));
   if (lane == 0) s.warp[warp] = key;
   __syncthreads();
   if (warp == 0) {
@@ -429,6 +483,13 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     z.cl.sync();
     return;
   }
+  if (z.top == INFINITY) {  // its tokens are equally likely, the others are none
+    for (int i = tid; i < z.n_vec * VEC; i += ST) data[i] = from_f<T>(to_f(data[i]) == INFINITY ? 0.f : -INFINITY);
+    z.top = 0.f;
+    own = own == INFINITY ? 0.f : -INFINITY;
+    __syncthreads();
+  }
+  const uint32_t own_key = static_cast<uint32_t>(composite(own, 0) >> 32);
   if (k == 1) {  // the largest logit's first token
     unsigned at = 0xffffffffu;
     z.each([&](float x, int idx) {
@@ -506,7 +567,11 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
       z.cl.sync();
       for (int r = 0; r < z.ranks; ++r) bound = min(bound, static_cast<uint32_t>(*z.cl.map_shared_rank(&s.part[1], r)));
       const float least = logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32);
-      const int n_list = z.gather([&](float x, int) { return x >= least; });
+      if (tid == 0) s.n_list[0] = 0;
+      __syncthreads();
+      z.collect_from(least);
+      z.cl.sync();
+      const int n_list = z.collected(0);
       if (n_list <= LIST) {
         if (z.rank == 0) settle(n_list);
         z.cl.sync();
@@ -539,20 +604,16 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   const u64 eligible = z.eligible;
   auto live = [&](float x, int idx) { return eligible == 0 || composite(x, idx) >= eligible; };
   if (eligible == 0) {
-    // near masses: each bucket's in 2^-15 of the weight at its upper end (the weight falls by 1/64 over a bucket:
+    // near masses: each bucket's in 2^-15 of the weight at its middle (a weight changes by 1/64 over a bucket:
     // two terms of its series); a CTA has at most 65536 tokens
     for (int i = tid; i < BUCKETS; i += ST) s.hist[0][i] = 0;
     if (tid < 2) s.n_list[tid] = 0;
     __syncthreads();
     constexpr float STEP = REACH / BUCKETS;
     z.each([&](float x, int) {
-      const float y = z.fall(x);
-      const int b = static_cast<int>(y);
-      if (x > -INFINITY && b < BUCKETS - 1) {
-        const float f = y - static_cast<float>(b);
-        const int v = __float2int_rn(fmaf(f, fmaf(f, 16384.f * STEP * STEP, -32768.f * STEP), 32768.f));
-        atomicAdd(&s.hist[0][b], static_cast<uint32_t>(v));
-      }
+      const float y = z.fall(x), r = y + 8388608.f, f = y - (r - 8388608.f);
+      const float v = fmaf(f, fmaf(f, 16384.f * STEP * STEP, -32768.f * STEP), 32768.f + 8388608.f);
+      if (y < BUCKETS - 1.5f) atomicAdd(&s.hist[0][__float_as_int(r) & (BUCKETS - 1)], __float_as_uint(v) - 0x4b000000u);
     });
     z.cl.sync();
     if (z.rank == 0) {
@@ -590,18 +651,25 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     const int bp = guess.count, bu = guess.bucket;
     // exact sums: all, before bp, before bu, over min_p; and the tokens of the two ranges
     u64 sum[4] = {};
-    z.each([&](float x, int idx) {
-      const u64 w = z.weight(x);
-      const int b = z.bucket0(x);
-      sum[0] += w;
-      sum[1] += b < bp ? w : 0;
-      sum[2] += b < bu ? w : 0;
-      sum[3] += w >= z.floor_w ? w : 0;
-      if (w > 0) {
-        if (b == bu) z.collect(0, x, idx);
-        if (with_p && b == bp && bp != bu) z.collect(1, x, idx);
-      }
-    });
+    auto exact = [&](auto with_top_p, auto with_min_p) {
+      constexpr bool p_on = decltype(with_top_p)::value, m_on = decltype(with_min_p)::value;
+      z.each([&](float x, int idx) {
+        const u64 w = z.weight(x);
+        const int b = z.bucket0(x);
+        sum[0] += w;
+        if (p_on && b < bp) sum[1] += w;
+        if (b < bu) sum[2] += w;
+        if (m_on && w >= z.floor_w) sum[3] += w;
+        if ((b == bu || (p_on && b == bp)) && w > 0) z.collect(b == bu ? 0 : 1, x, idx);
+      });
+      if (!m_on) sum[3] = sum[0];
+    };
+    typedef std::integral_constant<bool, true> On;
+    typedef std::integral_constant<bool, false> Off;
+    if (with_p)
+      z.floor_w > 0 ? exact(On(), On()) : exact(On(), Off());
+    else
+      z.floor_w > 0 ? exact(Off(), On()) : exact(Off(), Off());
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const u64 v = warp_sum64(sum[i]);
@@ -690,14 +758,16 @@ template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s)
   static DeviceOnce configured;
   constexpr int MAX_DATA = 128 << 10;
   if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>),
-                                 static_cast<int>(sizeof(Smem)) + MAX_DATA + 48, configured)) != cudaSuccess)
+                                 static_cast<int>(sizeof(Smem)) + MAX_DATA + 1024, configured)) != cudaSuccess)
     return e;
   // CTAs of a row: as many as its size needs, and more while all rows' CTAs still run at once
   int ranks = 1;
   auto chunk = [&](int r) { return (a.vocab + r - 1) / r; };
   while (ranks < 8 && (chunk(ranks) * sizeof(T) > MAX_DATA || (2ll * rows * ranks <= sms && chunk(ranks) > 4096))) ranks *= 2;
   a.chunk = chunk(ranks);
-  const size_t smem = sizeof(Smem) + (a.chunk * sizeof(T) + 47) / 16 * 16;
+  a.rows = rows;
+  const size_t smem = sizeof(Smem) + (a.chunk * sizeof(T) + 31) / 512 * 512 + 512;  // (whole warps of vectors)
+  a.wave = std::max(1, sms / ranks * (smem < (112 << 10) ? 2 : 1));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * ranks);
   cfg.blockDim = dim3(ST);
