@@ -7,11 +7,12 @@
 // target", answered exactly: weights are whole numbers of 2^-44 (a weight's relative error is near
 // 2^-30: the exponent (x - max) / t log2(e) is carried in two fp32 numbers), and sums of whole numbers do not depend on their order.
 //
-// A row is held in the shared memory of the 1 to 8 CTAs of a cluster, read from memory once.  Three ways, each of
+// A row is dealt with by the 1 to 8 CTAs of a cluster, which read it from memory once and again, two or three
+// times, from the second-level cache (so that two CTAs fit an SM, one working while the other waits).  Three ways, each of
 // which leaves a row that it cannot settle to the next:
-//   1. top-k of up to a quarter of the cluster's threads: the k-th largest of the threads' own largest logits is a lower
+//   1. top-k of up to half of the cluster's threads: the k-th largest of the threads' own largest logits is a lower
 //      bound for the k-th largest of all, and not many more than k tokens pass it; they are sorted and summed one by one.
-//   2. all tokens: a histogram of near masses over 2048 ranges of (max - x) / t says in which range the
+//   2. all tokens: a histogram of near masses over 4096 ranges of (max - x) / t says in which range the
 //      target of top-p and that of the draw lie; one pass over the exact weights sums what lies before those
 //      ranges and collects their tokens, which are sorted; the exact sums show whether the ranges were the right ones.
 //   3. an exact histogram of counts or masses, whose range that holds the target is cut further by the bits of x and of the
@@ -30,9 +31,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int ST = 1024;     // threads
-constexpr int LIST = 1024;   // tokens that are sorted
-constexpr int BUCKETS = 2048;
+constexpr int ST = 512;      // threads
+constexpr int SW = ST / 32;
+constexpr int LIST = ST;     // tokens that are sorted
+constexpr int BUCKETS = 4096;
 constexpr float REACH = 32.f;  // of (max - x) / t: exp(-31.98) is less than half of 2^-44, weight 0
 constexpr int SHIFT = 44;      // the largest weight is 2^SHIFT
 typedef unsigned long long u64;
@@ -103,8 +105,11 @@ template <typename T> struct Sampler {
 
   const SampleArgs& a;
   Smem& s;
-  const T* data;  // this CTA's tokens in shared memory, 16-byte vectors; what is not a token is -infinity
-  int n_vec, first;  // vectors; index of the first vector's first element
+  // this CTA's tokens: 16-byte vectors as they lie in memory, the first and last perhaps with a neighbour's elements
+  const T* src;      // its first token
+  int off, n;        // elements before it in its vector; tokens
+  int n_vec, first;  // vectors, to a multiple of 32; index of the first vector's first element
+  bool inf = false;  // the largest logit is +infinity: those tokens count as 0, the others are none
   cg::cluster_group cl;
   int rank, ranks, tid, lane, warp;
   int phase = 0;
@@ -146,52 +151,89 @@ template <typename T> struct Sampler {
     return __float_as_int(fall(x) + 8388608.f) & (BUCKETS - 1);
   }
 
+  // vector v, what is not a token (a NaN too) as -infinity
+  __device__ __forceinline__ uint4 raw_vector(int v) const {
+    const int at = v * VEC - off;
+    if (at >= 0 && at + VEC <= n) return __ldg(reinterpret_cast<const uint4*>(src + at));
+    T x[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = at + i >= 0 && at + i < n ? src[at + i] : from_f<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(x);
+  }
+  __device__ __forceinline__ uint4 cleaned(uint4 e) const {
+    uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(T) == 2) {
+        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+        const uint32_t good = __heq2_mask(h, h);
+        w[i] = (w[i] & good) | (0xff80ff80u & ~good);
+      } else {
+        const float x = __uint_as_float(w[i]);
+        w[i] = x == x ? w[i] : 0xff800000u;
+      }
+    }
+    if (inf) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (sizeof(T) == 2)
+          w[i] = ((w[i] & 0xffffu) == 0x7f80u ? 0u : 0xff80u) | (w[i] >> 16 == 0x7f80u ? 0u : 0xff800000u);
+        else
+          w[i] = w[i] == 0x7f800000u ? 0u : 0xff800000u;
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // the largest number of a cleaned vector
+  static __device__ __forceinline__ float largest(uint4 e) {
+    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+    if (sizeof(T) == 2) {
+      __nv_bfloat162 h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+      const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+      return fmaxf(f.x, f.y);
+    }
+    return fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+  }
+  static __device__ __forceinline__ float element(uint4 e, int i) {
+    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+    if (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    return __uint_as_float(w[i % 4]);
+  }
+  // f(vector, its first element's index) over this CTA's tokens, whole warps together; some loads ahead
+  template <typename F> __device__ __forceinline__ void vectors(F f) const {
+    constexpr int BATCH = 4;
+    for (int v0 = tid; v0 < n_vec; v0 += BATCH * ST) {
+      uint4 e[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (v0 + j * ST < n_vec) e[j] = raw_vector(v0 + j * ST);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (v0 + j * ST < n_vec) f(cleaned(e[j]), first + (v0 + j * ST) * VEC);
+    }
+  }
   // f(logit, index) for all of this CTA's tokens (and some places of -infinity), whole warps together: f may use
   // warp-wide operations.
   template <typename F> __device__ __forceinline__ void each(F f) const {
+    uint4 next = {};
+    if (tid < n_vec) next = raw_vector(tid);
     for (int v = tid; v < n_vec; v += ST) {  // (n_vec is a multiple of 32)
-      T e[VEC];
-      *reinterpret_cast<uint4*>(e) = reinterpret_cast<const uint4*>(data)[v];
+      const uint4 e = cleaned(next);
+      if (v + ST < n_vec) next = raw_vector(v + ST);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) f(to_f(e[i]), first + v * VEC + i);
+      for (int i = 0; i < VEC; ++i) f(element(e, i), first + v * VEC + i);
     }
   }
   // The tokens of at least `least` into list 0: a vector's largest first.
   __device__ __forceinline__ void collect_from(float least) {
-    for (int v = tid; v < n_vec; v += ST) {
-      uint4 e = reinterpret_cast<const uint4*>(data)[v];
-      float m;
-      largest(e, m, true);
-      if (m < least) continue;
-      const T* x = reinterpret_cast<const T*>(data) + v * VEC;
+    vectors([&](uint4 e, int idx) {
+      if (largest(e) < least) return;
+#pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (to_f(x[i]) >= least) collect(0, to_f(x[i]), first + v * VEC + i);
-    }
-  }
-  // The largest number of a vector into m (if `fresh`, else of m too); a NaN becomes -infinity.
-  static __device__ __forceinline__ void largest(uint4& e, float& m, bool fresh) {
-    uint32_t w[4] = {e.x, e.y, e.z, e.w};
-    if (sizeof(T) == 2) {
-      __nv_bfloat162 top2;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-        const uint32_t good = __heq2_mask(h, h);
-        w[i] = (w[i] & good) | (0xff80ff80u & ~good);
-        const __nv_bfloat162 c = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-        top2 = i == 0 ? c : __hmax2(top2, c);
-      }
-      const float2 f = __bfloat1622float2(top2);
-      m = fresh ? fmaxf(f.x, f.y) : fmaxf(m, fmaxf(f.x, f.y));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = __uint_as_float(w[i]);
-        w[i] = x == x ? w[i] : 0xff800000u;
-        m = i == 0 && fresh ? __uint_as_float(w[0]) : fmaxf(m, __uint_as_float(w[i]));
-      }
-    }
-    e = make_uint4(w[0], w[1], w[2], w[3]);
+        if (element(e, i) >= least) collect(0, element(e, i), idx + i);
+    });
   }
 
   __device__ __forceinline__ Ctl decide() {  // what the first CTA wrote into ctl[phase], for everyone
@@ -244,7 +286,7 @@ template <typename T> struct Sampler {
       if (lane == 0) s.warp[warp] = over;
       __syncthreads();
       if (warp == 0) {
-        over = warp_sum64(s.warp[lane]);
+        over = warp_sum64(lane < SW ? s.warp[lane] : 0);
         if (lane == 0) s.part[1] = over;
       }
     }
@@ -263,14 +305,19 @@ template <typename T> struct Sampler {
     }
     cl.sync();
     if (rank == 0) {
-      u64 x[2] = {s.tot[2 * tid], s.tot[2 * tid + 1]};
-      x[1] += x[0];
-      const u64 before = block_scan(x[1]) - x[1];
-      __syncthreads();
-      s.tot[2 * tid] = x[0] + before;
-      s.tot[2 * tid + 1] = x[1] + before;
-      __syncthreads();
+      running_sums();
     }
+  }
+
+  __device__ __forceinline__ void running_sums() {  // first CTA: tot
+    constexpr int EACH = BUCKETS / ST;
+    u64 x[EACH], sum = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) x[i] = sum += s.tot[EACH * tid + i];
+    const u64 before = block_scan(sum) - sum;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) s.tot[EACH * tid + i] = x[i] + before;
+    __syncthreads();
   }
 
   __device__ __forceinline__ u64 block_scan(u64 v) {  // inclusive, one value a thread
@@ -282,13 +329,13 @@ template <typename T> struct Sampler {
     if (lane == 31) s.warp[warp] = v;
     __syncthreads();
     if (warp == 0) {
-      u64 w = s.warp[lane], own = w;
+      u64 w = lane < SW ? s.warp[lane] : 0, own = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const u64 y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
       }
-      s.warp[lane] = w - own;
+      if (lane < SW) s.warp[lane] = w - own;
     }
     __syncthreads();
     return v + s.warp[warp];
@@ -310,20 +357,32 @@ template <typename T> struct Sampler {
     const int at = atomicAdd(&s.n_list[which], 1);
     if (at < LIST) s.list[which][at] = composite(x, idx);
   }
+  // One value of each CTA (a reading from another takes long: each lane reads one), lane r that of CTA r; `rest` beyond
+  template <typename V> __device__ __forceinline__ V of_each(V* mine, V rest) const {
+    return lane < ranks ? *cl.map_shared_rank(mine, lane) : rest;
+  }
   // After the CTAs have collected and the cluster has met: tokens in all lists.
   __device__ __forceinline__ int collected(int which) const {
-    int n = 0;
-    for (int r = 0; r < ranks; ++r) n += *cl.map_shared_rank(&s.n_list[which], r);
-    return n;
+    return __reduce_add_sync(0xffffffffu, of_each(&s.n_list[which], 0));
   }
   // first CTA: all lists' tokens, largest first; thread i gets the i-th, 0 beyond their number (at most LIST)
   __device__ __forceinline__ u64 sorted(int which, int n) {
-    u64 v = 0;
-    for (int r = 0, before = 0; r < ranks; ++r) {
-      const int m = *cl.map_shared_rank(&s.n_list[which], r);
-      if (tid >= before && tid < before + m) v = cl.map_shared_rank(&s.list[which][0], r)[tid - before];
-      before += m;
+    int end = of_each(&s.n_list[which], 0);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
     }
+    int r = 0, before = 0;  // the list that holds the tid-th token
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      const int e = __shfl_sync(0xffffffffu, end, i);
+      if (tid >= e) {
+        r = i + 1;
+        before = e;
+      }
+    }
+    u64 v = tid < n ? cl.map_shared_rank(&s.list[which][0], r)[tid - before] : 0;
     u64* work = s.work();
     int size = 32;
     while (size < n) size <<= 1;
@@ -406,53 +465,28 @@ template <typename T> struct Sampler {
   }
 };
 
-template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(SampleArgs a) {
+template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(SampleArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
-  T* data = reinterpret_cast<T*>(raw + sizeof(Smem));
   Sampler<T> z(a, s);
   constexpr int VEC = Sampler<T>::VEC;
   const int row = blockIdx.x / z.ranks, tid = z.tid, lane = z.lane, warp = z.warp;
-  const int i0 = min(a.vocab, z.rank * a.chunk), i1 = min(a.vocab, i0 + a.chunk);
-  const T* src = static_cast<const T*>(a.logits) + static_cast<long long>(row) * a.ld + i0;
-  // vectors as they lie in memory: those at the ends may hold a neighbour's elements
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T), n = i1 - i0;
-  z.data = data;
-  z.n_vec = n > 0 ? ((off + n + VEC - 1) / VEC + 31) / 32 * 32 : 0;
-  z.first = i0 - off;
+  const int i0 = min(a.vocab, z.rank * a.chunk), n = min(a.vocab, i0 + a.chunk) - i0;
+  z.src = static_cast<const T*>(a.logits) + static_cast<long long>(row) * a.ld + i0;
+  z.off = static_cast<int>(reinterpret_cast<uintptr_t>(z.src) & 15) / sizeof(T);
+  z.n = n;
+  z.n_vec = n > 0 ? ((z.off + n + VEC - 1) / VEC + 31) / 32 * 32 : 0;
+  z.first = i0 - z.off;
   // the row that takes this one's place on the SM, on its way into the second-level cache meanwhile
-  if (tid == 0 && row + a.wave < a.rows && n > 0) {
-    const uintptr_t p = (reinterpret_cast<uintptr_t>(src + static_cast<long long>(a.wave) * a.ld) + 15) & ~static_cast<uintptr_t>(15);
+  if (tid == 0 && row + a.wave < a.rows && n * sizeof(T) >= 32) {
+    const uintptr_t p = (reinterpret_cast<uintptr_t>(z.src + static_cast<long long>(a.wave) * a.ld) + 15) & ~static_cast<uintptr_t>(15);
     const uint32_t bytes = (static_cast<uint32_t>(n) * sizeof(T) - 15) / 16 * 16;
-    if (n * sizeof(T) >= 32) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
   }
   float own = -INFINITY;  // this thread's largest
-  constexpr int BATCH = 4;
-  for (int v0 = tid; v0 < z.n_vec; v0 += BATCH * ST) {
-    uint4 e[BATCH];
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int v = v0 + j * ST, at = v * VEC - off;
-      if (v < z.n_vec && at >= 0 && at + VEC <= n) {
-        e[j] = __ldg(reinterpret_cast<const uint4*>(src + at));
-      } else if (v < z.n_vec) {
-        T x[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = at + i >= 0 && at + i < n ? src[at + i] : from_f<T>(-INFINITY);
-        e[j] = *reinterpret_cast<const uint4*>(x);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int v = v0 + j * ST;
-      if (v < z.n_vec) {
-        z.largest(e[j], own, false);
-        reinterpret_cast<uint4*>(data)[v] = e[j];
-      }
-    }
-  }
+  z.vectors([&](uint4 e, int) { own = fmaxf(own, z.largest(e)); });
   float t = a.temperature ? a.temperature[row] : 1.f;
   int k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
@@ -468,15 +502,14 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   if (lane == 0) s.warp[warp] = key;
   __syncthreads();
   if (warp == 0) {
-    key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(s.warp[lane]));
+    key = __reduce_max_sync(0xffffffffu, lane < SW ? static_cast<uint32_t>(s.warp[lane]) : 0u);
     if (lane == 0) s.part[0] = key;
   }
   if (!(t > 0.f)) k = 1;
   if (k <= 0 || k >= a.vocab) k = a.vocab;
   z.cl.sync();
-  u64 best = 0;
-  for (int r = 0; r < z.ranks; ++r) best = max(best, *z.cl.map_shared_rank(&s.part[0], r));
-  z.top = logit_of(best << 32);
+  key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(z.of_each(&s.part[0], 0ull)));
+  z.top = logit_of(static_cast<u64>(key) << 32);
   // (no CTA leaves while another reads its shared memory)
   if (!(z.top > -INFINITY)) {
     if (z.rank == 0 && tid == 0) a.out[row] = -1;
@@ -484,10 +517,9 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     return;
   }
   if (z.top == INFINITY) {  // its tokens are equally likely, the others are none
-    for (int i = tid; i < z.n_vec * VEC; i += ST) data[i] = from_f<T>(to_f(data[i]) == INFINITY ? 0.f : -INFINITY);
+    z.inf = true;
     z.top = 0.f;
     own = own == INFINITY ? 0.f : -INFINITY;
-    __syncthreads();
   }
   const uint32_t own_key = static_cast<uint32_t>(composite(own, 0) >> 32);
   if (k == 1) {  // the largest logit's first token
@@ -499,15 +531,12 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     if (lane == 0) s.warp[warp] = at;
     __syncthreads();
     if (warp == 0) {
-      at = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(s.warp[lane]));
+      at = __reduce_min_sync(0xffffffffu, lane < SW ? static_cast<unsigned>(s.warp[lane]) : 0xffffffffu);
       if (lane == 0) s.part[1] = at;
     }
     z.cl.sync();
-    if (z.rank == 0 && tid == 0) {
-      u64 first = s.part[1];
-      for (int r = 1; r < z.ranks; ++r) first = min(first, *z.cl.map_shared_rank(&s.part[1], r));
-      a.out[row] = static_cast<int>(first);
-    }
+    at = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(z.of_each(&s.part[1], 0xffffffffull)));
+    if (z.rank == 0 && tid == 0) a.out[row] = static_cast<int>(at);
     z.cl.sync();
     return;
   }
@@ -554,7 +583,7 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   bool refined = false;
   auto all = [](float, int) { return true; };
   if (k < a.vocab) {
-    if (k <= z.ranks * (ST / 4)) {
+    if (k <= z.ranks * (ST / 2)) {
       // k / ranks of the threads' largest in each CTA, the least of these over the CTAs: at least k tokens pass it.
       // (20 bits of it: a lower bound is enough)
       const int each_k = (k + z.ranks - 1) / z.ranks;
@@ -565,7 +594,7 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
       }
       if (tid == 0) s.part[1] = bound;
       z.cl.sync();
-      for (int r = 0; r < z.ranks; ++r) bound = min(bound, static_cast<uint32_t>(*z.cl.map_shared_rank(&s.part[1], r)));
+      bound = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(z.of_each(&s.part[1], 0xffffffffull)));
       const float least = logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32);
       if (tid == 0) s.n_list[0] = 0;
       __syncthreads();
@@ -604,7 +633,7 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
   const u64 eligible = z.eligible;
   auto live = [&](float x, int idx) { return eligible == 0 || composite(x, idx) >= eligible; };
   if (eligible == 0) {
-    // near masses: each bucket's in 2^-15 of the weight at its middle (a weight changes by 1/64 over a bucket:
+    // near masses: each bucket's in 2^-15 of the weight at its middle (a weight changes by 1/128 over a bucket:
     // two terms of its series); a CTA has at most 65536 tokens
     for (int i = tid; i < BUCKETS; i += ST) s.hist[0][i] = 0;
     if (tid < 2) s.n_list[tid] = 0;
@@ -617,26 +646,38 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     });
     z.cl.sync();
     if (z.rank == 0) {
-      u64 sum[2];
+      constexpr int EACH = BUCKETS / ST;
+      float m[EACH] = {};
+      for (int r0 = 0; r0 < z.ranks; r0 += 2) {
+        uint4 h[2][EACH / 4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int b = 2 * tid + i;
-        float m = 0.f;
-        for (int r = 0; r < z.ranks; ++r) m += static_cast<float>(z.cl.map_shared_rank(&s.hist[0][0], r)[b]);
-        sum[i] = static_cast<u64>(m * exp2f(static_cast<float>(b) * (-STEP * 1.44269504f) + (SHIFT - 15)));
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < EACH / 4; ++i)
+            h[r][i] = r0 + r < z.ranks ? reinterpret_cast<const uint4*>(z.cl.map_shared_rank(&s.hist[0][0], r0 + r))[tid * (EACH / 4) + i]
+                                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < EACH / 4; ++i) {
+            m[4 * i] += static_cast<float>(h[r][i].x);
+            m[4 * i + 1] += static_cast<float>(h[r][i].y);
+            m[4 * i + 2] += static_cast<float>(h[r][i].z);
+            m[4 * i + 3] += static_cast<float>(h[r][i].w);
+          }
       }
-      sum[1] += sum[0];
-      const u64 before = z.block_scan(sum[1]) - sum[1];
-      s.tot[2 * tid] = sum[0] + before;
-      s.tot[2 * tid + 1] = sum[1] + before;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i)
+        s.tot[EACH * tid + i] = static_cast<u64>(m[i] * exp2f(static_cast<float>(EACH * tid + i) * (-STEP * 1.44269504f) + (SHIFT - 15)));
       __syncthreads();
+      z.running_sums();
       const u64 near_all = s.tot[BUCKETS - 1];
       const u64 near_p = reach_p(near_all);
       // min_p's share: up to its own weight's place
       u64 near_t = near_p;
       if (z.floor_w > 0) {
         const float y = -logf(fminf(min_p, 1.f)) / STEP;
-        near_t = min(near_t, max(1ull, s.tot[min(BUCKETS - 1, static_cast<int>(y))]));
+        near_t = min(near_t, max(1ull, s.tot[min(BUCKETS - 1, static_cast<int>(fminf(y, BUCKETS - 1.f)))]));
       }
       const u64 near_u = max(1ull, reach_u(near_t));
       for (int b = tid; b < BUCKETS; b += ST) {
@@ -670,14 +711,15 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
       z.floor_w > 0 ? exact(On(), On()) : exact(On(), Off());
     else
       z.floor_w > 0 ? exact(Off(), On()) : exact(Off(), Off());
+    u64* scratch = s.sums();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const u64 v = warp_sum64(sum[i]);
-      if (lane == 0) s.hist[0][(i * 32 + warp) * 2] = static_cast<uint32_t>(v), s.hist[0][(i * 32 + warp) * 2 + 1] = static_cast<uint32_t>(v >> 32);
+      if (lane == 0) scratch[i * 32 + warp] = v;
     }
     __syncthreads();
     if (warp < 4) {
-      const u64 v = warp_sum64(reinterpret_cast<const u64*>(s.hist[0])[warp * 32 + lane]);
+      const u64 v = warp_sum64(lane < SW ? scratch[warp * 32 + lane] : 0);
       if (lane == 0) s.part[1 + warp] = v;
     }
     z.cl.sync();
@@ -685,12 +727,12 @@ template <typename T> __global__ void __launch_bounds__(ST) sample_kernel(Sample
     // (every CTA comes to the same result, the first one's below)
     if (z.rank == 0) {
       if (tid == 0) s.ctl[z.phase].count = 0;  // settled
-      u64 total[4];
+      // lane 8 i + r: sum i of CTA r
+      u64 total[4], v = (lane & 7) < z.ranks ? z.cl.map_shared_rank(&s.part[1], lane & 7)[lane >> 3] : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        total[i] = 0;
-        for (int r = 0; r < z.ranks; ++r) total[i] += *z.cl.map_shared_rank(&s.part[1 + i], r);
-      }
+      for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[i] = __shfl_sync(0xffffffffu, v, 8 * i);
       // tokens in a list, the number of them: thread i's token, weight and running mass
       u64 tok = 0, mine = 0, incl = 0;
       auto load = [&](int which, int n_list, u64 before) {
@@ -756,22 +798,20 @@ template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s)
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   static DeviceOnce configured;
-  constexpr int MAX_DATA = 128 << 10;
-  if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>),
-                                 static_cast<int>(sizeof(Smem)) + MAX_DATA + 1024, configured)) != cudaSuccess)
+  if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>), static_cast<int>(sizeof(Smem)), configured)) != cudaSuccess)
     return e;
-  // CTAs of a row: as many as its size needs, and more while all rows' CTAs still run at once
+  // CTAs of a row: as its size needs, and more while all rows' CTAs still run at once, two on an SM
+  constexpr int MAX_CHUNK = 65536;  // (sums of 15-bit parts and of near masses stay within 32 bits)
   int ranks = 1;
   auto chunk = [&](int r) { return (a.vocab + r - 1) / r; };
-  while (ranks < 8 && (chunk(ranks) * sizeof(T) > MAX_DATA || (2ll * rows * ranks <= sms && chunk(ranks) > 4096))) ranks *= 2;
+  while (ranks < 8 && (chunk(ranks) > MAX_CHUNK || (1ll * rows * ranks <= sms && chunk(ranks) > 4096))) ranks *= 2;
   a.chunk = chunk(ranks);
   a.rows = rows;
-  const size_t smem = sizeof(Smem) + (a.chunk * sizeof(T) + 31) / 512 * 512 + 512;  // (whole warps of vectors)
-  a.wave = std::max(1, sms / ranks * (smem < (112 << 10) ? 2 : 1));
+  a.wave = std::max(1, 2 * sms / ranks);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * ranks);
   cfg.blockDim = dim3(ST);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = sizeof(Smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
