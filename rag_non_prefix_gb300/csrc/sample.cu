@@ -12,7 +12,7 @@
 // which leaves a row that it cannot settle to the next:
 //   1. top-k of up to half of the cluster's threads: the k-th largest of the threads' own largest logits is a lower
 //      bound for the k-th largest of all, and not many more than k tokens pass it; they are sorted and summed one by one.
-//   2. all tokens: a histogram of near masses over 4096 ranges of (max - x) / t says in which range the
+//   2. all tokens: a histogram of near masses over 8192 ranges of (max - x) / t says in which range the
 //      target of top-p and that of the draw lie; one pass over the exact weights sums what lies before those
 //      ranges and collects their tokens, which are sorted; the exact sums show whether the ranges were the right ones.
 //   3. an exact histogram of counts or masses, whose range that holds the target is cut further by the bits of x and of the
@@ -35,6 +35,7 @@ constexpr int ST = 512;      // threads
 constexpr int SW = ST / 32;
 constexpr int LIST = ST;     // tokens that are sorted
 constexpr int BUCKETS = 4096;
+constexpr int NEAR = 8192;   // of the near masses
 constexpr float REACH = 32.f;  // of (max - x) / t: exp(-31.98) is less than half of 2^-44, weight 0
 constexpr int SHIFT = 44;      // the largest weight is 2^SHIFT
 typedef unsigned long long u64;
@@ -72,6 +73,8 @@ struct __align__(16) Smem {
   u64 list[2][LIST];    // tokens that this CTA collected
   u64 warp[32];
   u64 part[6];          // this CTA's: see the uses
+  uint32_t above[6][8]; // of the threads' largest, by parts of their bits
+  float near[4];
   u64 want;             // a target (64-bit floating point is slow: one thread computes it for all)
   u64 floor_w;
   float c_hi, c_lo;
@@ -201,6 +204,11 @@ template <typename T> struct Sampler {
     if (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     return __uint_as_float(w[i % 4]);
   }
+  __device__ __forceinline__ float near_fall(float x) const {
+    return fminf((top - x) * (reach * (NEAR / BUCKETS)), static_cast<float>(NEAR - 1));
+  }
+  __device__ __forceinline__ int near_bucket(float x) const { return __float_as_int(near_fall(x) + 8388608.f) & (NEAR - 1); }
+
   // f(vector, its first element's index) over this CTA's tokens, whole warps together; some loads ahead
   template <typename F> __device__ __forceinline__ void vectors(F f) const {
     constexpr int BATCH = 4;
@@ -226,8 +234,9 @@ template <typename T> struct Sampler {
       for (int i = 0; i < VEC; ++i) f(element(e, i), first + v * VEC + i);
     }
   }
-  // The tokens of at least `least` into list 0: a vector's largest first.
-  __device__ __forceinline__ void collect_from(float least) {
+  // The tokens of at least `least` into list 0, by the threads whose largest is one: a vector's largest first.
+  __device__ __forceinline__ void collect_from(float least, float own) {
+    if (own < least) return;
     vectors([&](uint4 e, int idx) {
       if (largest(e) < least) return;
 #pragma unroll
@@ -320,25 +329,21 @@ template <typename T> struct Sampler {
     __syncthreads();
   }
 
-  __device__ __forceinline__ u64 block_scan(u64 v) {  // inclusive, one value a thread
+  template <typename V> __device__ __forceinline__ V block_scan(V v) {  // inclusive, one value a thread
+    V* warps = reinterpret_cast<V*>(s.warp);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+      const V y = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += y;
     }
-    if (lane == 31) s.warp[warp] = v;
+    if (lane == 31) warps[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-      u64 w = lane < SW ? s.warp[lane] : 0, own = w;
+    // (every warp sums the ones before it)
+    V w = lane < warp ? warps[lane] : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      if (lane < SW) s.warp[lane] = w - own;
-    }
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
     __syncthreads();
-    return v + s.warp[warp];
+    return v + w;
   }
 
   // first CTA: the bucket in which the running sum reaches target
@@ -365,24 +370,27 @@ template <typename T> struct Sampler {
   __device__ __forceinline__ int collected(int which) const {
     return __reduce_add_sync(0xffffffffu, of_each(&s.n_list[which], 0));
   }
-  // first CTA: all lists' tokens, largest first; thread i gets the i-th, 0 beyond their number (at most LIST)
-  __device__ __forceinline__ u64 sorted(int which, int n) {
+  // first CTA: the i-th token of all CTAs' lists (i below their number)
+  __device__ __forceinline__ u64 token_of(int which, int at, bool in) const {
     int end = of_each(&s.n_list[which], 0);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += y;
     }
-    int r = 0, before = 0;  // the list that holds the tid-th token
+    int r = 0, before = 0;  // the list that holds it
 #pragma unroll
     for (int i = 0; i < 7; ++i) {
       const int e = __shfl_sync(0xffffffffu, end, i);
-      if (tid >= e) {
+      if (at >= e) {
         r = i + 1;
         before = e;
       }
     }
-    u64 v = tid < n ? cl.map_shared_rank(&s.list[which][0], r)[tid - before] : 0;
+    return in ? cl.map_shared_rank(&s.list[which][0], r)[at - before] : 0;
+  }
+  // first CTA: its threads' first n numbers (at most LIST), largest first; thread i gets the i-th
+  __device__ __forceinline__ u64 sorted(u64 v, int n) {
     u64* work = s.work();
     int size = 32;
     while (size < n) size <<= 1;
@@ -435,7 +443,7 @@ template <typename T> struct Sampler {
       const int n = gather(in);
       if (n <= LIST) {
         if (rank == 0) {
-          const u64 t = sorted(0, n);
+          const u64 t = sorted(token_of(0, tid, tid < n), n);
           const u64 mine = MASS ? weight(logit_of(t)) : 1;  // (all lanes)
           const u64 w = tid < n ? mine : 0;
           const u64 incl = excl + block_scan(w);
@@ -485,8 +493,6 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     const uint32_t bytes = (static_cast<uint32_t>(n) * sizeof(T) - 15) / 16 * 16;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
   }
-  float own = -INFINITY;  // this thread's largest
-  z.vectors([&](uint4 e, int) { own = fmaxf(own, z.largest(e)); });
   float t = a.temperature ? a.temperature[row] : 1.f;
   int k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
@@ -498,6 +504,9 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     const u64 one = 1ull << SHIFT;
     s.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
   }
+  if (tid < 48) s.above[0][tid] = 0;
+  float own = -INFINITY;  // this thread's largest
+  z.vectors([&](uint4 e, int) { own = fmaxf(own, z.largest(e)); });
   uint32_t key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(composite(own, 0) >> 32));
   if (lane == 0) s.warp[warp] = key;
   __syncthreads();
@@ -563,7 +572,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   };
   // first CTA, list 0 sorted: the token of a row whose first k tokens are in it
   auto settle = [&](int n) {
-    const u64 tok = z.sorted(0, n);
+    const u64 tok = z.sorted(z.token_of(0, tid, tid < n), n);
     const u64 w = z.weight(logit_of(tok));  // (all lanes)
     const u64 mine = tid < k && tid < n ? w : 0;
     u64* sums = s.sums();
@@ -585,12 +594,24 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   if (k < a.vocab) {
     if (k <= z.ranks * (ST / 2)) {
       // k / ranks of the threads' largest in each CTA, the least of these over the CTAs: at least k tokens pass it.
-      // (20 bits of it: a lower bound is enough)
+      // (18 bits of it, three at a time: a lower bound is enough)
       const int each_k = (k + z.ranks - 1) / z.ranks;
       uint32_t bound = 0;
-      for (int bit = 31; bit >= 12; --bit) {
-        const uint32_t more = bound | 1u << bit;
-        if (__syncthreads_count(own_key >= more) >= each_k) bound = more;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        const int shift = 29 - 3 * i;
+        uint32_t mine = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < 7; ++j) {
+          const unsigned who = __ballot_sync(0xffffffffu, own_key >= bound + ((j + 1) << shift));
+          if (lane == j) mine = __popc(who);
+        }
+        if (mine) atomicAdd(&s.above[i][lane], mine);
+        __syncthreads();
+        uint32_t digit = 0;
+#pragma unroll
+        for (int j = 0; j < 7; ++j) digit += s.above[i][j] >= static_cast<uint32_t>(each_k);
+        bound += digit << shift;
       }
       if (tid == 0) s.part[1] = bound;
       z.cl.sync();
@@ -598,7 +619,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       const float least = logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32);
       if (tid == 0) s.n_list[0] = 0;
       __syncthreads();
-      z.collect_from(least);
+      z.collect_from(least, own);
       z.cl.sync();
       const int n_list = z.collected(0);
       if (n_list <= LIST) {
@@ -635,55 +656,68 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   if (eligible == 0) {
     // near masses: each bucket's in 2^-15 of the weight at its middle (a weight changes by 1/128 over a bucket:
     // two terms of its series); a CTA has at most 65536 tokens
-    for (int i = tid; i < BUCKETS; i += ST) s.hist[0][i] = 0;
+    for (int i = tid; i < NEAR; i += ST) s.hist[0][i] = 0;
     if (tid < 2) s.n_list[tid] = 0;
     __syncthreads();
-    constexpr float STEP = REACH / BUCKETS;
+    constexpr float STEP = REACH / NEAR;
     z.each([&](float x, int) {
-      const float y = z.fall(x), r = y + 8388608.f, f = y - (r - 8388608.f);
+      const float y = z.near_fall(x), r = y + 8388608.f, f = y - (r - 8388608.f);
       const float v = fmaf(f, fmaf(f, 16384.f * STEP * STEP, -32768.f * STEP), 32768.f + 8388608.f);
-      if (y < BUCKETS - 1.5f) atomicAdd(&s.hist[0][__float_as_int(r) & (BUCKETS - 1)], __float_as_uint(v) - 0x4b000000u);
+      if (y < NEAR - 1.5f) atomicAdd(&s.hist[0][__float_as_int(r) & (NEAR - 1)], __float_as_uint(v) - 0x4b000000u);
     });
     z.cl.sync();
     if (z.rank == 0) {
-      constexpr int EACH = BUCKETS / ST;
+      // running masses of this thread's buckets, 1 for the largest logit's token
+      constexpr int EACH = NEAR / ST;
       float m[EACH] = {};
-      for (int r0 = 0; r0 < z.ranks; r0 += 2) {
-        uint4 h[2][EACH / 4];
+      for (int r = 0; r < z.ranks; ++r) {
+        const uint4* h = reinterpret_cast<const uint4*>(z.cl.map_shared_rank(&s.hist[0][0], r)) + tid * (EACH / 4);
+        uint4 v[EACH / 4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < EACH / 4; ++i) v[i] = h[i];
 #pragma unroll
-          for (int i = 0; i < EACH / 4; ++i)
-            h[r][i] = r0 + r < z.ranks ? reinterpret_cast<const uint4*>(z.cl.map_shared_rank(&s.hist[0][0], r0 + r))[tid * (EACH / 4) + i]
-                                       : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int i = 0; i < EACH / 4; ++i) {
-            m[4 * i] += static_cast<float>(h[r][i].x);
-            m[4 * i + 1] += static_cast<float>(h[r][i].y);
-            m[4 * i + 2] += static_cast<float>(h[r][i].z);
-            m[4 * i + 3] += static_cast<float>(h[r][i].w);
-          }
+        for (int i = 0; i < EACH / 4; ++i) {
+          m[4 * i] += static_cast<float>(v[i].x);
+          m[4 * i + 1] += static_cast<float>(v[i].y);
+          m[4 * i + 2] += static_cast<float>(v[i].z);
+          m[4 * i + 3] += static_cast<float>(v[i].w);
+        }
       }
+      auto middle = [&](int i) { return exp2f(static_cast<float>(EACH * tid + i) * (-STEP * 1.44269504f)); };
+      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < EACH; ++i)
-        s.tot[EACH * tid + i] = static_cast<u64>(m[i] * exp2f(static_cast<float>(EACH * tid + i) * (-STEP * 1.44269504f) + (SHIFT - 15)));
+      for (int i = 0; i < EACH; ++i) m[i] = sum = fmaf(m[i] * (1.f / 32768.f), middle(i), sum);
+      const float before = z.block_scan(sum) - sum;
+      const float last_p = -logf(fminf(min_p, 1.f)) / STEP;  // min_p's own place
+      const int at_m = z.floor_w > 0 ? static_cast<int>(fminf(last_p, NEAR - 1.f)) : NEAR - 1;
+      if (tid == 0) {
+        s.ctl[z.phase].count = s.ctl[z.phase].bucket = 0;
+        s.near[1] = INFINITY;
+      }
+      if (tid == ST - 1) s.near[0] = before + sum;
       __syncthreads();
-      z.running_sums();
-      const u64 near_all = s.tot[BUCKETS - 1];
-      const u64 near_p = reach_p(near_all);
-      // min_p's share: up to its own weight's place
-      u64 near_t = near_p;
-      if (z.floor_w > 0) {
-        const float y = -logf(fminf(min_p, 1.f)) / STEP;
-        near_t = min(near_t, max(1ull, s.tot[min(BUCKETS - 1, static_cast<int>(fminf(y, BUCKETS - 1.f)))]));
+      // top_p's range, and the mass up to and with its last token: as if the range's tokens all weighed the same
+      const float near_p = top_p * s.near[0];
+      float excl = before;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        const float incl = before + m[i];
+        if (top_p < 1.f && excl < near_p && near_p <= incl) {
+          const float w = middle(i);
+          s.ctl[z.phase].count = EACH * tid + i;
+          s.near[1] = excl + ceilf((near_p - excl) / w) * w;
+        }
+        if (EACH * tid + i == at_m) s.near[2] = incl;
+        excl = incl;
       }
-      const u64 near_u = max(1ull, reach_u(near_t));
-      for (int b = tid; b < BUCKETS; b += ST) {
-        const u64 incl = s.tot[b], excl = b ? s.tot[b - 1] : 0;
-        if (excl < near_p && near_p <= incl) s.ctl[z.phase].count = b;
-        if (excl < near_u && near_u <= incl) s.ctl[z.phase].bucket = b;
+      __syncthreads();
+      const float near_u = u * fminf(s.near[1], s.near[2]);
+      excl = before;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        const float incl = before + m[i];
+        if (excl <= near_u && near_u < incl) s.ctl[z.phase].bucket = EACH * tid + i;
+        excl = incl;
       }
       __syncthreads();
     }
@@ -696,7 +730,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       constexpr bool p_on = decltype(with_top_p)::value, m_on = decltype(with_min_p)::value;
       z.each([&](float x, int idx) {
         const u64 w = z.weight(x);
-        const int b = z.bucket0(x);
+        const int b = z.near_bucket(x);
         sum[0] += w;
         if (p_on && b < bp) sum[1] += w;
         if (b < bu) sum[2] += w;
@@ -733,33 +767,28 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
 #pragma unroll
       for (int i = 0; i < 4; ++i) total[i] = __shfl_sync(0xffffffffu, v, 8 * i);
-      // tokens in a list, the number of them: thread i's token, weight and running mass
-      u64 tok = 0, mine = 0, incl = 0;
-      auto load = [&](int which, int n_list, u64 before) {
-        tok = z.sorted(which, n_list);
-        const u64 w = z.weight(logit_of(tok));  // (all lanes)
-        mine = tid < n_list ? w : 0;
-        incl = before + z.block_scan(mine);
-      };
-      u64 mass = total[3];
+      u64 mass = total[3];  // what min_p keeps
       const u64 pm = reach_p(total[0]);
-      bool ok = true;
-      if (with_p && pm <= mass) {
-        ok = n_p <= LIST;
-        if (ok) {
-          load(bp == bu ? 0 : 1, n_p, total[1]);
-          if (tid == 0) s.part[0] = 0;
-          __syncthreads();
+      const bool need_p = with_p && pm <= mass, two = need_p && bp != bu;
+      const int n = n_u + (two ? n_p : 0);
+      if (n <= LIST) {
+        // the draw's range comes first in the order
+        const u64 a0 = z.token_of(0, tid, tid < n_u), a1 = two ? z.token_of(1, tid - n_u, tid >= n_u && tid < n) : 0;
+        const u64 tok = z.sorted(tid < n_u ? a0 : a1, n);
+        const u64 w = z.weight(logit_of(tok));  // (all lanes)
+        const u64 mine = tid < n ? w : 0, scan = z.block_scan(mine);
+        if (tid == 0) s.part[0] = s.part[5] = 0;
+        __syncthreads();
+        if (tid == n_u - 1) s.part[5] = scan;
+        __syncthreads();
+        const u64 incl = tid < n_u ? total[2] + scan : total[1] + scan - s.part[5];
+        if (need_p) {
           if (mine && incl - mine < pm && pm <= incl) s.part[0] = incl;
           __syncthreads();
           mass = s.part[0];
-          ok = mass > 0;
         }
-      }
-      if (ok && n_u <= LIST) {
-        load(0, n_u, total[2]);
         const u64 want = reach_u(mass);
-        if (mine && incl - mine < want && want <= incl) {
+        if (mass > 0 && mine && tid < n_u && incl - mine < want && want <= incl) {
           a.out[row] = index_of(tok);
           s.ctl[z.phase].count = 1;
         }
