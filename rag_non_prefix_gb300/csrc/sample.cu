@@ -73,10 +73,9 @@ struct __align__(16) Smem {
   u64 list[2][LIST];    // tokens that this CTA collected
   u64 warp[32];
   u64 part[6];          // this CTA's: see the uses
-  uint32_t above[6][8]; // of the threads' largest, by parts of their bits
+  uint32_t above[SW];   // bounds, a warp's each
   float near[4];
-  u64 want;             // a target (64-bit floating point is slow: one thread computes it for all)
-  u64 floor_w;
+  u64 floor_w;          // (64-bit floating point is slow: one thread computes these for all)
   float c_hi, c_lo;
   Ctl ctl[2];
   int n_list[2];
@@ -101,6 +100,19 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// m f for a fraction f (below 0 and NaN: 0, above 1: m), exactly, rounded down or up
+__device__ __forceinline__ u64 part_of(u64 m, float f, bool up) {
+  if (!(f > 0.f)) return 0;
+  if (f >= 1.f) return m;
+  const uint32_t bits = __float_as_uint(f), e = max(bits >> 23, 1u);
+  const u64 frac = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);  // f = frac 2^(e - 150)
+  const int s = 150 - static_cast<int>(e);                              // 24 to 149
+  const u64 lo = m * frac, hi = __umul64hi(m, frac);                    // (m is below 2^63: hi below 2^23)
+  const u64 q = s < 64 ? lo >> s | hi << (64 - s) : s < 128 ? hi >> (s - 64) : 0;
+  const bool exact = s < 64 ? (lo & ((1ull << s) - 1)) == 0 : lo == 0 && (s < 128 ? (hi & ((1ull << (s - 64)) - 1)) == 0 : hi == 0);
+  return q + (up && !exact);
 }
 
 template <typename T> struct Sampler {
@@ -209,9 +221,28 @@ template <typename T> struct Sampler {
   }
   __device__ __forceinline__ int near_bucket(float x) const { return __float_as_int(near_fall(x) + 8388608.f) & (NEAR - 1); }
 
-  // f(vector, its first element's index) over this CTA's tokens, whole warps together; some loads ahead
+  // f(logit, index) for all of this CTA's tokens (and some places of -infinity), whole warps together: f may use
+  // warp-wide operations.
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    each(f, [](int) {});
+  }
+  // (g(index of its first element) after each vector)
+  template <typename F, typename G> __device__ __forceinline__ void each(F f, G g) const {
+    uint4 next = {};
+    if (tid < n_vec) next = raw_vector(tid);
+#pragma unroll 1
+    for (int v = tid; v < n_vec; v += ST) {  // (n_vec is a multiple of 32)
+      const uint4 e = cleaned(next);
+      if (v + ST < n_vec) next = raw_vector(v + ST);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f(element(e, i), first + v * VEC + i);
+      g(first + v * VEC);
+    }
+  }
+  // f(vector, its first element's index) over this CTA's tokens, some loads ahead
   template <typename F> __device__ __forceinline__ void vectors(F f) const {
-    constexpr int BATCH = 4;
+    constexpr int BATCH = 8;
+#pragma unroll 1
     for (int v0 = tid; v0 < n_vec; v0 += BATCH * ST) {
       uint4 e[BATCH];
 #pragma unroll
@@ -222,27 +253,34 @@ template <typename T> struct Sampler {
         if (v0 + j * ST < n_vec) f(cleaned(e[j]), first + (v0 + j * ST) * VEC);
     }
   }
-  // f(logit, index) for all of this CTA's tokens (and some places of -infinity), whole warps together: f may use
-  // warp-wide operations.
-  template <typename F> __device__ __forceinline__ void each(F f) const {
-    uint4 next = {};
-    if (tid < n_vec) next = raw_vector(tid);
-    for (int v = tid; v < n_vec; v += ST) {  // (n_vec is a multiple of 32)
-      const uint4 e = cleaned(next);
-      if (v + ST < n_vec) next = raw_vector(v + ST);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) f(element(e, i), first + v * VEC + i);
-    }
-  }
-  // The tokens of at least `least` into list 0, by the threads whose largest is one: a vector's largest first.
+  // The tokens of at least `least` into list 0, by the threads whose largest is one.
   __device__ __forceinline__ void collect_from(float least, float own) {
     if (own < least) return;
+    uint32_t some = 0;  // this thread's vectors (at most 32) that hold one
     vectors([&](uint4 e, int idx) {
-      if (largest(e) < least) return;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (element(e, i) >= least) collect(0, element(e, i), idx + i);
+      if (largest(e) >= least) some |= 1u << ((idx - first) / VEC - tid) / ST;
     });
+#pragma unroll 1
+    while (some) {
+      const int v = tid + (__ffs(some) - 1) * ST;
+      some &= some - 1;
+      const uint4 e = cleaned(raw_vector(v));
+      uint32_t hits = 0;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) hits |= (element(e, i) >= least ? 1u : 0u) << i;
+      collect_hits(0, hits, first + v * VEC);
+    }
+  }
+  // The tokens idx + i of the bits i of a mask into a list (few do: one small loop, as the kernel's time on few rows is that of
+  // fetching its instructions).
+  __device__ __forceinline__ void collect_hits(int which, uint32_t hits, int idx) {
+#pragma unroll 1
+    while (hits) {
+      const int at = idx + __ffs(hits) - 1;
+      hits &= hits - 1;
+      const float x = to_f(src[at - first - off]);
+      collect(which, inf ? 0.f : x, at);
+    }
   }
 
   __device__ __forceinline__ Ctl decide() {  // what the first CTA wrote into ctl[phase], for everyone
@@ -504,7 +542,6 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     const u64 one = 1ull << SHIFT;
     s.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
   }
-  if (tid < 48) s.above[0][tid] = 0;
   float own = -INFINITY;  // this thread's largest
   z.vectors([&](uint4 e, int) { own = fmaxf(own, z.largest(e)); });
   uint32_t key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(composite(own, 0) >> 32));
@@ -555,21 +592,9 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   z.c_lo = s.c_lo;
   z.reach = BUCKETS / REACH / t;
   z.floor_w = s.floor_w;
-  // targets of a mass m: the smallest whole numbers not below top_p m, and above u m (whole blocks call these)
-  auto one_thread = [&](auto f) {
-    __syncthreads();
-    if (tid == 0) s.want = f();
-    __syncthreads();
-    return s.want;
-  };
-  auto reach_p = [&](u64 m) {
-    return top_p >= 1.f || !(top_p == top_p) ? m : one_thread([&] {
-      return max(1ull, min(m, static_cast<u64>(ceil(fmax(0.0, static_cast<double>(top_p) * static_cast<double>(m))))));
-    });
-  };
-  auto reach_u = [&](u64 m) {
-    return one_thread([&] { return min(m, static_cast<u64>(fmax(0.0, static_cast<double>(u) * static_cast<double>(m))) + 1); });
-  };
+  // targets of a mass m: the smallest whole numbers not below top_p m, and above u m
+  auto reach_p = [&](u64 m) { return top_p < 1.f ? max(1ull, part_of(m, top_p, true)) : m; };
+  auto reach_u = [&](u64 m) { return min(m, part_of(m, u, false) + 1); };
   // first CTA, list 0 sorted: the token of a row whose first k tokens are in it
   auto settle = [&](int n) {
     const u64 tok = z.sorted(z.token_of(0, tid, tid < n), n);
@@ -582,10 +607,8 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     const u64 pm = reach_p(sums[ST - 1]);
     // kept mass: of the shorter prefix
     if (mine && incl - mine < pm && pm <= incl) s.part[2] = incl;
-    const u64 over = z.block_scan(mine >= z.floor_w ? mine : 0);
-    if (tid == ST - 1) s.part[3] = over;
-    __syncthreads();
-    const u64 want = reach_u(min(s.part[2], s.part[3]));
+    const int over = __syncthreads_count(mine && mine >= z.floor_w);
+    const u64 want = reach_u(min(s.part[2], sums[over - 1]));
     if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
   };
 
@@ -594,25 +617,36 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   if (k < a.vocab) {
     if (k <= z.ranks * (ST / 2)) {
       // k / ranks of the threads' largest in each CTA, the least of these over the CTAs: at least k tokens pass it.
-      // (18 bits of it, three at a time: a lower bound is enough)
-      const int each_k = (k + z.ranks - 1) / z.ranks;
-      uint32_t bound = 0;
+      // Each warp sorts its threads' and names the one that its share of k reaches; of these 16 the largest that
+      // enough threads pass (all but the least may be too large).
+      const int each_k = (k + z.ranks - 1) / z.ranks, in_warp = (each_k + SW - 1) / SW;
+      uint32_t x = own_key;
 #pragma unroll
-      for (int i = 0; i < 6; ++i) {
-        const int shift = 29 - 3 * i;
-        uint32_t mine = 0;
+      for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
-        for (uint32_t j = 0; j < 7; ++j) {
-          const unsigned who = __ballot_sync(0xffffffffu, own_key >= bound + ((j + 1) << shift));
-          if (lane == j) mine = __popc(who);
+        for (int j = size >> 1; j > 0; j >>= 1) {
+          const uint32_t o = __shfl_xor_sync(0xffffffffu, x, j);
+          x = ((lane & size) == 0 || size == 32) == ((lane & j) == 0) ? max(x, o) : min(x, o);
         }
-        if (mine) atomicAdd(&s.above[i][lane], mine);
-        __syncthreads();
-        uint32_t digit = 0;
+      if (lane == in_warp - 1) s.above[warp] = x;
+      __syncthreads();
+      x = s.above[lane & (SW - 1)];
 #pragma unroll
-        for (int j = 0; j < 7; ++j) digit += s.above[i][j] >= static_cast<uint32_t>(each_k);
-        bound += digit << shift;
+      for (int size = 2; size <= SW; size <<= 1)
+#pragma unroll
+        for (int j = size >> 1; j > 0; j >>= 1) {
+          const uint32_t o = __shfl_xor_sync(0xffffffffu, x, j);
+          x = ((lane & size) == 0 || size == SW) == ((lane & j) == 0) ? max(x, o) : min(x, o);
+        }
+      int lo = 0, hi = SW - 1;
+#pragma unroll
+      for (int i = 1; i < SW; i <<= 1) {
+        const int mid = (lo + hi) >> 1;
+        const bool enough = __syncthreads_count(own_key >= __shfl_sync(0xffffffffu, x, mid)) >= each_k;
+        hi = enough ? mid : hi;
+        lo = enough ? lo : min(mid + 1, hi);
       }
+      uint32_t bound = __shfl_sync(0xffffffffu, x, hi);
       if (tid == 0) s.part[1] = bound;
       z.cl.sync();
       bound = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(z.of_each(&s.part[1], 0xffffffffull)));
@@ -666,27 +700,27 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       if (y < NEAR - 1.5f) atomicAdd(&s.hist[0][__float_as_int(r) & (NEAR - 1)], __float_as_uint(v) - 0x4b000000u);
     });
     z.cl.sync();
+    {  // each CTA sums a slice over the cluster, into the first one's tot
+      const int slice = NEAR / z.ranks;
+      float* tot = reinterpret_cast<float*>(z.cl.map_shared_rank(s.tot, 0));
+      for (int b = z.rank * slice + tid; b < (z.rank + 1) * slice; b += ST) {
+        uint32_t h[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) h[r] = r < z.ranks ? z.cl.map_shared_rank(&s.hist[0][0], r)[b] : 0;
+        float m = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) m += static_cast<float>(h[r]);
+        tot[b] = m * (1.f / 32768.f) * exp2f(static_cast<float>(b) * (-STEP * 1.44269504f));
+      }
+    }
+    z.cl.sync();
     if (z.rank == 0) {
       // running masses of this thread's buckets, 1 for the largest logit's token
       constexpr int EACH = NEAR / ST;
-      float m[EACH] = {};
-      for (int r = 0; r < z.ranks; ++r) {
-        const uint4* h = reinterpret_cast<const uint4*>(z.cl.map_shared_rank(&s.hist[0][0], r)) + tid * (EACH / 4);
-        uint4 v[EACH / 4];
-#pragma unroll
-        for (int i = 0; i < EACH / 4; ++i) v[i] = h[i];
-#pragma unroll
-        for (int i = 0; i < EACH / 4; ++i) {
-          m[4 * i] += static_cast<float>(v[i].x);
-          m[4 * i + 1] += static_cast<float>(v[i].y);
-          m[4 * i + 2] += static_cast<float>(v[i].z);
-          m[4 * i + 3] += static_cast<float>(v[i].w);
-        }
-      }
       auto middle = [&](int i) { return exp2f(static_cast<float>(EACH * tid + i) * (-STEP * 1.44269504f)); };
-      float sum = 0.f;
+      float m[EACH], sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < EACH; ++i) m[i] = sum = fmaf(m[i] * (1.f / 32768.f), middle(i), sum);
+      for (int i = 0; i < EACH; ++i) m[i] = sum += reinterpret_cast<const float*>(s.tot)[EACH * tid + i];
       const float before = z.block_scan(sum) - sum;
       const float last_p = -logf(fminf(min_p, 1.f)) / STEP;  // min_p's own place
       const int at_m = z.floor_w > 0 ? static_cast<int>(fminf(last_p, NEAR - 1.f)) : NEAR - 1;
@@ -726,6 +760,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     const int bp = guess.count, bu = guess.bucket;
     // exact sums: all, before bp, before bu, over min_p; and the tokens of the two ranges
     u64 sum[4] = {};
+    uint32_t hits[2] = {};
     auto exact = [&](auto with_top_p, auto with_min_p) {
       constexpr bool p_on = decltype(with_top_p)::value, m_on = decltype(with_min_p)::value;
       z.each([&](float x, int idx) {
@@ -735,7 +770,15 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         if (p_on && b < bp) sum[1] += w;
         if (b < bu) sum[2] += w;
         if (m_on && w >= z.floor_w) sum[3] += w;
-        if ((b == bu || (p_on && b == bp)) && w > 0) z.collect(b == bu ? 0 : 1, x, idx);
+        const uint32_t bit = 1u << (idx - z.first) % VEC;  // (a vector's elements come one after the other)
+        if (b == bu && w > 0) hits[0] |= bit;
+        if (p_on && b == bp && bp != bu && w > 0) hits[1] |= bit;
+      }, [&](int idx) {
+        if (hits[0] | hits[1]) {
+          z.collect_hits(0, hits[0], idx);
+          if (p_on) z.collect_hits(1, hits[1], idx);
+          hits[0] = hits[1] = 0;
+        }
       });
       if (!m_on) sum[3] = sum[0];
     };
