@@ -585,49 +585,58 @@ _pack_kvq = struct.Struct("@P4iPq2i").pack
 
 def _kvq_cache(pool: torch.Tensor, table: torch.Tensor):
     """(the cache as bytes, sequences, heads, channels, device)"""
-    shape, ts = pool.shape, table.shape
     if pool.dtype is not torch.uint8 or table.dtype is not torch.int32:
         raise CacheBlendError(3, "a pool must be uint8 and a page table int32")
+    shape, ts = pool.shape, table.shape
     if len(shape) != 4 or shape[3] not in (1280, 2560) or len(ts) != 2 or not pool.is_contiguous():
         raise CacheBlendError(2, "a pool is contiguous [pages, heads, page_tokens // 16, 20 * head_dim], a page table "
                                  "[sequences, pages]")
-    dev = pool.get_device()
-    if dev < 0 or dev != _get_device() or table.get_device() != dev or (ts[1] > 1 and table.stride(1) != 1):
-        raise CacheBlendError(1, "the pool and its page table must be on the current CUDA device")
-    if max(shape[0], ts[0], ts[1]) > 0x7FFFFFFF or shape[2] >= 1 << 27:
-        raise CacheBlendError(2, "bad sizes of a 4-bit cache")
     n, heads, blocks, size = shape
-    ld = table.stride(0) if ts[0] > 1 else ts[1]
-    return (_pack_kvq(pool.data_ptr(), n, 16 * blocks, heads, size // 20, table.data_ptr(), ld, ts[1], ts[0]), ts[0],
-            heads, size // 20, dev)
+    seqs, pages = ts
+    ld, step = table.stride()
+    dev = pool.get_device()
+    if dev < 0 or dev != _get_device() or table.get_device() != dev or (step != 1 and pages > 1):
+        raise CacheBlendError(1, "the pool and its page table must be on the current CUDA device")
+    dh = size // 20
+    try:
+        return (_pack_kvq(pool.data_ptr(), n, 16 * blocks, heads, dh, table.data_ptr(), ld if seqs > 1 else pages, pages,
+                          seqs), seqs, heads, dh, dev)
+    except struct.error:
+        raise CacheBlendError(2, "bad sizes of a 4-bit cache") from None
 
 
-def _kvq_rows(t: torch.Tensor, dtype, lead, heads: int, dh: int, what: str, dev: int) -> int:
-    """Pitch in elements of rows [*lead, heads, dh] of ``dtype``, after checking them."""
+def _kvq_rows(t: torch.Tensor, dtype, want: tuple, what: str, dev: int) -> int:
+    """Pitch in elements of rows ``want`` = (*rows, heads, channels) of ``dtype``, after checking them."""
     if t.dtype is not dtype:
         raise CacheBlendError(3, f"{what} must be {dtype}, not {t.dtype}")
-    if t.shape != (*lead, heads, dh):
-        raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}, needs {(*lead, heads, dh)}")
+    if t.shape != want:
+        raise CacheBlendError(2, f"{what} has shape {tuple(t.shape)}, needs {want}")
+    st, dh = t.stride(), want[-1]
     if t.get_device() != dev:
         raise CacheBlendError(1, f"{what} must be on the pool's device")
-    st = t.stride()
-    if st[-1] != 1 or (heads > 1 and st[-2] != dh):
+    if st[-1] != 1 or (st[-2] != dh and want[-2] > 1):
         raise CacheBlendError(1, f"{what} must have contiguous rows of heads x head_dim")
-    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * st[1]:
+    if len(want) == 3:
+        return st[0] if want[0] > 1 else want[1] * dh
+    if want[0] > 1 and want[1] > 1 and st[0] != want[1] * st[1]:
         raise CacheBlendError(1, f"{what} must have one pitch over sequences and tokens")
-    if len(lead) == 2 and lead[1] > 1:
-        return st[1]
-    return st[0] if lead[0] > 1 else heads * dh
+    return st[1] if want[1] > 1 else st[0] if want[0] > 1 else want[2] * dh
 
 
-def _kvq_index(t: Optional[torch.Tensor], lead, what: str, dev: int):
-    if t is None:
-        return None
+def _kvq_index(t: torch.Tensor, lead: tuple, what: str, dev: int) -> int:
     if t.dtype is not torch.int32:
         raise CacheBlendError(3, f"{what} must be int32, not {t.dtype}")
-    if t.shape != lead or not t.is_contiguous() or t.get_device() != dev:
+    if t.shape != lead or t.get_device() != dev or not t.is_contiguous():
         raise CacheBlendError(2, f"{what} must be contiguous {tuple(lead)} on the pool's device")
     return t.data_ptr()
+
+
+def _kvq_places(pos: torch.Tensor, seq: Optional[torch.Tensor], dev: int):
+    """(rows, pointers of the positions and sequences of a call's rows)"""
+    lead = pos.shape
+    if len(lead) != 1 or lead[0] > 0x7FFFFFFF:
+        raise CacheBlendError(2, "pos must be a vector")
+    return lead[0], _kvq_index(pos, lead, "pos", dev), None if seq is None else _kvq_index(seq, lead, "seq", dev)
 
 
 def cb_kvq_write(pool: torch.Tensor, table: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
@@ -635,13 +644,11 @@ def cb_kvq_write(pool: torch.Tensor, table: torch.Tensor, k: torch.Tensor, v: to
     """Quantises k, v [rows, heads, head_dim] into positions ``pos`` of sequences ``seq`` (None: row i of
     sequence i) of a 4-bit cache: its ``pool`` (kvq_pool) and page ``table`` int32 [sequences, pages]."""
     cache, _, heads, dh, dev = _kvq_cache(pool, table)
-    dt, lead = _dtype_code(k.dtype), pos.shape
-    if len(lead) != 1 or lead[0] > 0x7FFFFFFF:
-        raise CacheBlendError(2, "pos must be a vector")
-    _check(load_library().cb_kvq_write(
-        cache, k.data_ptr(), _kvq_rows(k, k.dtype, lead, heads, dh, "k", dev), v.data_ptr(),
-        _kvq_rows(v, k.dtype, lead, heads, dh, "v", dev), dt, _kvq_index(seq, lead, "seq", dev),
-        _kvq_index(pos, lead, "pos", dev), lead[0], _stream_on(dev, stream)))
+    rows, at, of = _kvq_places(pos, seq, dev)
+    dtype, want = k.dtype, (rows, heads, dh)
+    _check((_lib or load_library()).cb_kvq_write(
+        cache, k.data_ptr(), _kvq_rows(k, dtype, want, "k", dev), v.data_ptr(), _kvq_rows(v, dtype, want, "v", dev),
+        _dtype_code(dtype), of, at, rows, _stream_on(dev, stream)))
 
 
 def cb_kvq_read(pool: torch.Tensor, table: torch.Tensor, pos: torch.Tensor, seq: Optional[torch.Tensor] = None,
@@ -650,18 +657,18 @@ def cb_kvq_read(pool: torch.Tensor, table: torch.Tensor, pos: torch.Tensor, seq:
     """(k, v) [rows, heads, head_dim] held at positions ``pos`` of sequences ``seq``, the keys turned on by
     ``delta_pos`` positions; of ``dtype`` unless given to write to."""
     cache, _, heads, dh, dev = _kvq_cache(pool, table)
-    lead = pos.shape
-    if len(lead) != 1 or lead[0] > 0x7FFFFFFF:
-        raise CacheBlendError(2, "pos must be a vector")
+    rows, at, of = _kvq_places(pos, seq, dev)
+    want = (rows, heads, dh)
     if k_out is None or v_out is None:
         dtype = dtype if k_out is None and v_out is None else (v_out if k_out is None else k_out).dtype
         with _allocating_on(stream):
-            k_out = torch.empty(*lead, heads, dh, dtype=dtype, device=pool.device) if k_out is None else k_out
-            v_out = torch.empty(*lead, heads, dh, dtype=dtype, device=pool.device) if v_out is None else v_out
-    _check(load_library().cb_kvq_read(
-        cache, _kvq_index(seq, lead, "seq", dev), _kvq_index(pos, lead, "pos", dev), lead[0], int(delta_pos), float(theta),
-        _dtype_code(k_out.dtype), k_out.data_ptr(), _kvq_rows(k_out, k_out.dtype, lead, heads, dh, "k_out", dev),
-        v_out.data_ptr(), _kvq_rows(v_out, k_out.dtype, lead, heads, dh, "v_out", dev), _stream_on(dev, stream)))
+            k_out = torch.empty(want, dtype=dtype, device=pool.device) if k_out is None else k_out
+            v_out = torch.empty(want, dtype=dtype, device=pool.device) if v_out is None else v_out
+    dtype = k_out.dtype
+    _check((_lib or load_library()).cb_kvq_read(
+        cache, of, at, rows, delta_pos, theta, _dtype_code(dtype), k_out.data_ptr(),
+        _kvq_rows(k_out, dtype, want, "k_out", dev), v_out.data_ptr(), _kvq_rows(v_out, dtype, want, "v_out", dev),
+        _stream_on(dev, stream)))
     return k_out, v_out
 
 
@@ -671,24 +678,25 @@ def cb_kvq_attention(q: torch.Tensor, q_pos: torch.Tensor, pool: torch.Tensor, t
     """Attention of queries q [sequences, heads, head_dim] or [sequences, tokens, heads, head_dim] over a 4-bit
     cache: a token sees positions 0..q_pos of its sequence (negative: none, its output is zero).  ``scale``:
     1 / sqrt(head_dim) if None; ``scratch``: see kvq_scratch (None: made for this call)."""
-    cache, n, heads, dh, dev = _kvq_cache(pool, table)
-    dt, shape = _dtype_code(q.dtype), q.shape
+    cache, n, _, dh, dev = _kvq_cache(pool, table)
+    dtype, shape = q.dtype, q.shape
     if len(shape) not in (3, 4) or shape[0] != n:
         raise CacheBlendError(2, "q must be [sequences, heads, head_dim] or [sequences, tokens, heads, head_dim]")
     lead, h = shape[:-2], shape[-2]
     if h > 1 << 16 or (len(lead) == 2 and lead[1] > 0x7FFFFFFF):
         raise CacheBlendError(2, "q has too many heads or tokens")
+    want = (*lead, h, dh)
+    ldq = _kvq_rows(q, dtype, want, "q", dev)
     if out is None or scratch is None:
         with _allocating_on(stream):
-            out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+            out = torch.empty(shape, dtype=dtype, device=q.device) if out is None else out
             scratch = kvq_scratch(q.device) if scratch is None else scratch
     if scratch.get_device() != dev or not scratch.is_contiguous():
         raise CacheBlendError(1, "scratch must be contiguous on the pool's device")
-    _check(load_library().cb_kvq_attention(
-        cache, q.data_ptr(), _kvq_rows(q, q.dtype, lead, h, dh, "q", dev), _kvq_index(q_pos, lead, "q_pos", dev),
-        lead[1] if len(lead) == 2 else 1, h, dh ** -0.5 if scale is None else float(scale), dt, out.data_ptr(),
-        _kvq_rows(out, q.dtype, lead, h, dh, "out", dev), scratch.data_ptr(), scratch.numel() * scratch.element_size(),
-        _stream_on(dev, stream)))
+    _check((_lib or load_library()).cb_kvq_attention(
+        cache, q.data_ptr(), ldq, _kvq_index(q_pos, lead, "q_pos", dev), lead[1] if len(lead) == 2 else 1, h,
+        dh ** -0.5 if scale is None else scale, _dtype_code(dtype), out.data_ptr(),
+        _kvq_rows(out, dtype, want, "out", dev), scratch.data_ptr(), scratch.nbytes, _stream_on(dev, stream)))
     return out
 
 

@@ -459,8 +459,13 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   constexpr int TILES = 256;
   __shared__ long long scan[AW * 32 + 1];
   __shared__ int tile_len[TILES];
-  __shared__ int first_tile;
-  __shared__ long long first_base;
+  // the schedule, kept out of the registers of the loop over the keys
+  __shared__ struct {
+    long long n, share, rest;    // CTAs at work; their shares: share quanta, the first `rest` one more
+    long long begin, end;        // this CTA's
+    long long cur, base, unit;   // where it is; its tile's and its unit's first quantum
+    int ti, len, nq, q0, q1, seq, head, r0;
+  } sc;
   __shared__ float part_m[AW][R], part_l[AW][R], wts[AW][R], row_m[R], row_l[R];
   __shared__ int is_last;
   pdl_trigger();
@@ -504,38 +509,51 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   const long long total = scan[AW * 32];
   const long long n = min(static_cast<long long>(gridDim.x), quotient(total + MIN_SHARE - 1, MIN_SHARE));
   if (blockIdx.x >= n) return;
-  // the first `rest` shares are one quantum longer than `share`
   const long long share = quotient(total, n), rest = total - share * n;
-  auto begin_of = [&](long long c) { return share * c + min(c, rest); };
+  auto begin_of = [&](long long c) { return sc.share * c + min(c, sc.rest); };
   auto owner_of = [&](long long x) {
-    const long long longer = rest * (share + 1);
-    return static_cast<int>(x < longer ? quotient(x, share + 1) : rest + quotient(x - longer, share));
+    const long long longer = sc.rest * (sc.share + 1);
+    return static_cast<int>(x < longer ? quotient(x, sc.share + 1) : sc.rest + quotient(x - longer, sc.share));
   };
-  long long cur = begin_of(blockIdx.x);
-  const long long end = begin_of(blockIdx.x + 1);
-  if (scan[tid] <= cur && cur < scan[tid + 1]) {
-    long long base = scan[tid];
-    int i = tid * per;
-    for (;; ++i) {
-      const long long q = static_cast<long long>(quanta_of(len_of(i))) * heads;
-      if (cur < base + q) break;
-      base += q;
+  {
+    const long long cur = share * blockIdx.x + min(static_cast<long long>(blockIdx.x), rest);
+    if (tid == 0) {
+      sc.n = n;
+      sc.share = share;
+      sc.rest = rest;
+      sc.begin = sc.cur = cur;
+      sc.end = cur + share + (blockIdx.x < rest);
     }
-    first_tile = i;
-    first_base = base;
+    if (scan[tid] <= cur && cur < scan[tid + 1]) {
+      long long base = scan[tid];
+      int i = tid * per;
+      for (;; ++i) {
+        const long long q = static_cast<long long>(quanta_of(len_of(i))) * heads;
+        if (cur < base + q) break;
+        base += q;
+      }
+      sc.ti = i;
+      sc.base = base;
+    }
   }
-  __syncthreads();
-  int ti = first_tile;
-  long long base = first_base;
-  const long long begin = cur;
 
-  while (cur < end) {
-    const int len = len_of(ti), nq = quanta_of(len);
-    const int head = static_cast<int>(quotient(cur - base, nq));
-    const long long unit = base + static_cast<long long>(head) * nq;
-    const int q0 = static_cast<int>(cur - unit), q1 = static_cast<int>(min(static_cast<long long>(nq), end - unit));
-    const int seq = ti / p.tiles_per_seq, r0 = (ti - seq * p.tiles_per_seq) * R;
-
+  for (;;) {
+    __syncthreads();
+    if (sc.cur >= sc.end) break;
+    __syncthreads();
+    if (tid == 0) {  // the next unit, or its part
+      sc.len = len_of(sc.ti);
+      sc.nq = quanta_of(sc.len);
+      sc.head = static_cast<int>(quotient(sc.cur - sc.base, sc.nq));
+      sc.unit = sc.base + static_cast<long long>(sc.head) * sc.nq;
+      sc.q0 = static_cast<int>(sc.cur - sc.unit);
+      sc.q1 = static_cast<int>(min(static_cast<long long>(sc.nq), sc.end - sc.unit));
+      sc.seq = sc.ti / p.tiles_per_seq;
+      sc.r0 = (sc.ti - sc.seq * p.tiles_per_seq) * R;
+    }
+    __syncthreads();
+    {
+    const int len = sc.len, q0 = sc.q0, q1 = sc.q1, seq = sc.seq, head = sc.head, r0 = sc.r0;
     const int blocks = min((len + KVQ_BLOCK - 1) / KVQ_BLOCK, (q1 - UNIT_COST) * AW), per_page = p.c.page_tokens / KVQ_BLOCK;
     const int b0 = max(0, q0 - UNIT_COST) * AW + w, count = blocks > b0 ? (blocks - b0 + AW - 1) / AW : 0;
     uint8_t* ring = smem + w * A::STAGES * A::BLK;
@@ -614,6 +632,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
           buf[row * ROW + 16 * j + rr + 8] = a.o[nt][j][2 + c] + corr[j / 2];
         }
       }
+    }
     __syncthreads();
     if (tid < R) {
       float M = -INFINITY, L = 0.f;
@@ -629,9 +648,10 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
       row_l[tid] = L;
     }
     __syncthreads();
-    const bool whole = q1 - q0 == nq;
+    const int seq = sc.seq, head = sc.head, r0 = sc.r0;
+    const bool whole = sc.q1 - sc.q0 == sc.nq;
     // 2 slots a CTA: the first part of its share, and a later one
-    float* slot = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (cur != begin)) * slot_floats(DH);
+    float* slot = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (sc.cur != sc.begin)) * slot_floats(DH);
     const float* sm = reinterpret_cast<const float*>(smem);
     for (int i = tid; i < R * DH; i += AW * 32) {
       const int row = i / DH, ch = i - row * DH, gr = r0 + row;
@@ -653,7 +673,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
     }
     if (!whole) {
       if (tid < R) *reinterpret_cast<float2*>(slot + MAX_ROWS * DH + 2 * tid) = make_float2(row_m[tid], row_l[tid]);
-      const int c0 = owner_of(unit), c1 = owner_of(unit + nq - 1);  // CTAs of this unit
+      const int c0 = owner_of(sc.unit), c1 = owner_of(sc.unit + sc.nq - 1);  // CTAs of this unit
       __threadfence();
       __syncthreads();
       if (tid == 0) is_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
@@ -664,7 +684,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
         // parts c0..c1: the first in its CTA's first or later slot, the others in their CTA's first; a warp's row
         // at a time, four channels a lane
         const float* parts = p.parts + 2 * static_cast<size_t>(c0) * slot_floats(DH);
-        const int shift = unit != begin_of(c0) ? slot_floats(DH) : 0, np = c1 - c0 + 1;
+        const int shift = sc.unit != begin_of(c0) ? slot_floats(DH) : 0, np = c1 - c0 + 1;
         float* wt = reinterpret_cast<float*>(smem) + w * (A::WEIGHTS / 4 / AW);
         for (int row = w; row < R && r0 + row < rows; row += AW) {
           float M = -INFINITY, L = 0.f;
@@ -706,10 +726,12 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
       }
     }
     __syncthreads();  // the merge buffer becomes rings again
-    cur = unit + q1;
-    if (cur == base + static_cast<long long>(nq) * heads) {
-      base = cur;
-      ++ti;
+    if (tid == 0) {
+      sc.cur = sc.unit + sc.q1;
+      if (sc.cur == sc.base + static_cast<long long>(sc.nq) * heads) {
+        sc.base = sc.cur;
+        ++sc.ti;
+      }
     }
   }
 }
