@@ -7,6 +7,7 @@
 // 16 at a time: where they are such a word's tokens (a prompt from a multiple of 16 on) it moves whole words,
 // else (decoded tokens, scattered ones) a token's bytes alone.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "kvq.cuh"
@@ -171,58 +172,72 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 4) kvq_read_kernel(KvqView c, 
   }
   const size_t head_bytes = static_cast<size_t>(c.page_tokens / KVQ_BLOCK) * kvq_block_bytes(DH);
   const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, c.n_kv_heads);
-  for (int head = h0; head < h1; ++head) {
-    uint32_t word[8];  // (whole) value codes of four tokens, channels n and n + 8 for n = 0..7
-    if (at.whole) {
-      const uint8_t* blk = at.blk[0] + head * head_bytes;
+  // WHOLE: the warp's four rows share their words; every load is on its way before the first is needed
+  auto heads = [&](auto whole_rows) {
+    constexpr bool WHOLE = decltype(whole_rows)::value;
+    for (int head = h0; head < h1; ++head) {
+      uint32_t kc[STEPS] = {}, vc[WHOLE ? 1 : STEPS][8] = {};
+      uint16_t prm[STEPS][4] = {};  // scale and zero of the key, of the value
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        word[i] = lane % 16 < LANES ? *reinterpret_cast<const uint32_t*>(blk + kvq_value_byte(DH, at.r[0] & ~9, L >> 1, i)) : 0;
-    }
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      float kx[8] = {}, vx[8] = {};
-      if (at.blk[s]) {
+      for (int s = 0; s < STEPS; ++s) {
+        if (!at.blk[s]) continue;
         const uint8_t* blk = at.blk[s] + head * head_bytes;
         const int r = at.r[s];
-        const uint32_t kc = *reinterpret_cast<const uint32_t*>(blk + r * (DH / 2) + (at.tq * NG + at.g) * 4);
+        kc[s] = *reinterpret_cast<const uint32_t*>(blk + r * (DH / 2) + (at.tq * NG + at.g) * 4);
         const uint16_t* p = reinterpret_cast<const uint16_t*>(blk + 16 * DH + 4 * NG * r) + at.g;
-        const float ks = bf(p[0]), kz = ks * bf(p[NG]), vs = bf(p[32 * NG]), vz = vs * bf(p[33 * NG]);
-        const int byte = 2 * (r & 1) + (r >> 3), up = L & 1 ? 4 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) prm[s][i] = p[(i & 1) * NG + (i >> 1) * 32 * NG];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          kx[i] = fmaf(static_cast<float>((kc >> (4 * i)) & 15u), ks, kz);  // (exact: 17 bits)
-          const uint32_t vc = at.whole ? word[i] >> (8 * byte) : blk[kvq_value_byte(DH, r, L >> 1, i)];
-          vx[i] = fmaf(static_cast<float>((vc >> up) & 15u), vs, vz);
+          if (!WHOLE)
+            vc[s][i] = blk[kvq_value_byte(DH, r, L >> 1, i)];
+          else if (s == 0)
+            vc[0][i] = *reinterpret_cast<const uint32_t*>(blk + kvq_value_byte(DH, r & ~9, L >> 1, i));
         }
       }
-      if (turned) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        float kx[8], vx[8];
+        const float ks = bf(prm[s][0]), kz = ks * bf(prm[s][1]), vs = bf(prm[s][2]), vz = vs * bf(prm[s][3]);
+        const int up = (WHOLE ? 8 * (2 * (at.r[s] & 1) + (at.r[s] >> 3)) : 0) + (L & 1 ? 4 : 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float y = __shfl_xor_sync(0xffffffffu, kx[i], LANES / 2);
-          kx[i] = fmaf(y, si[i], kx[i] * co[i]);
+          kx[i] = fmaf(static_cast<float>((kc[s] >> (4 * i)) & 15u), ks, kz);  // (exact: 17 bits)
+          vx[i] = fmaf(static_cast<float>((vc[WHOLE ? 0 : s][i] >> up) & 15u), vs, vz);
         }
-      }
-      if (at.row[s] < rows && lane % 16 < LANES) {
-        store8(k + at.row[s] * ldk + head * DH + 8 * L, kx);
-        store8(v + at.row[s] * ldv + head * DH + 8 * L, vx);
+        if (turned) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float y = __shfl_xor_sync(0xffffffffu, kx[i], LANES / 2);
+            kx[i] = fmaf(y, si[i], kx[i] * co[i]);
+          }
+        }
+        if (at.row[s] < rows && lane % 16 < LANES) {
+          store8(k + at.row[s] * ldk + head * DH + 8 * L, kx);
+          store8(v + at.row[s] * ldv + head * DH + 8 * L, vx);
+        }
       }
     }
-  }
+  };
+  if (STEPS == 2 && at.whole)
+    heads(std::true_type());
+  else
+    heads(std::false_type());
 }
 
 // Units of rows, and the heads that a warp takes one after the other: a head each while there are few, more where
-// that would only look up the rows again.
+// that would only look up the rows again: once there are more than `want` warps (measured, 8320 rows of 8 heads written: 44.8 us with
+// the reading back at 4096, 43.8 at 8192, 45.5 at 16384; 4096 rows of 32 heads read: 27.7 us at 3000, 24.8 at 4096, 26.4 at 8192).
 struct KvqPlan {
   int steps, units, heads_each;
   dim3 grid;
 };
-KvqPlan kvq_plan(int rows, int heads) {
+KvqPlan kvq_plan(int rows, int heads, int want) {
   KvqPlan p;
   p.steps = static_cast<long long>(rows) * heads <= 8192 ? 1 : 2;
   p.units = p.steps == 1 ? (rows + 1) / 2 : (rows + 15) / 16 * 4;
   const long long warps = static_cast<long long>(p.units) * heads;
-  p.heads_each = static_cast<int>(std::min<long long>(heads, std::max<long long>(1, warps / 16384)));
+  p.heads_each = static_cast<int>(std::min<long long>(heads, std::max<long long>(1, warps / want)));
   p.grid = dim3((p.units + KVQ_WARPS - 1) / KVQ_WARPS, (heads + p.heads_each - 1) / p.heads_each);
   return p;
 }
@@ -232,7 +247,7 @@ KvqPlan kvq_plan(int rows, int heads) {
 cudaError_t launch_kvq_write(const KvqView& c, int head_dim, const void* k, long long ldk, const void* v, long long ldv,
                              cb_dtype dt, const int32_t* seq, const int32_t* pos, int rows, int32_t* status,
                              cudaStream_t s) {
-  const KvqPlan plan = kvq_plan(rows, c.n_kv_heads);
+  const KvqPlan plan = kvq_plan(rows, c.n_kv_heads, 8192);
   const dim3 block(KVQ_WARPS * 32);
   auto go = [&](auto* kernel, auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
@@ -253,7 +268,7 @@ cudaError_t launch_kvq_write(const KvqView& c, int head_dim, const void* k, long
 cudaError_t launch_kvq_read(const KvqView& c, int head_dim, const int32_t* seq, const int32_t* pos, int rows,
                             const float* cs_host, cb_dtype dt, void* k, long long ldk, void* v, long long ldv,
                             int32_t* status, cudaStream_t s) {
-  const KvqPlan plan = kvq_plan(rows, c.n_kv_heads);
+  const KvqPlan plan = kvq_plan(rows, c.n_kv_heads, 4096);
   const dim3 block(KVQ_WARPS * 32);
   KvqTurn turn = {};
   if (cs_host)

@@ -37,7 +37,7 @@ typedef unsigned long long u64;
 constexpr int AW = 4;                    // warps per CTA
 constexpr int QUANTUM = AW * KVQ_BLOCK;  // keys
 constexpr int MIN_SHARE = 4;             // quanta of a CTA, at least, where there are few
-constexpr int UNIT_COST = 3;             // what a unit costs beside its quanta (queries, first loads, merging): in quanta, measured
+constexpr int UNIT_COST = 6;             // what a unit costs beside its quanta (queries, first loads, merging): in quanta, measured
 constexpr int MAX_ROWS = 16;             // query rows per tile at most
 constexpr float LAZY = 6.f;              // the running maximum moves once a score passes it by 2^6
 
@@ -125,9 +125,9 @@ template <typename T, int DH, int NT, int NP> struct Attn {
   static constexpr int STAGES = 4;
   static constexpr int ROW = DH + 4;  // pitch of the merge buffer, free of bank conflicts
   static constexpr int RING = AW * STAGES * BLK;
-  static constexpr int QUERIES = NT * NP * NG * 2 * 32 * 8 + NT * NG * 32 * 8;
+  static constexpr int QUERIES = NT * NP * NG * 2 * 32 * 8 + NT * NG * 32 * 16;
   static constexpr int MERGE = AW * R * ROW * 4;
-  static constexpr int WEIGHTS = R * KVQ_MAX_CTAS * 4;  // of the parts of a unit
+  static constexpr int WEIGHTS = AW * 2 * KVQ_MAX_CTAS * 4;  // a warp's (maximum or weight, sum) of a row's parts
   static constexpr int WORK = std::max(std::max(RING, MERGE), WEIGHTS);
   static constexpr int SMEM = WORK + QUERIES;
 
@@ -137,14 +137,15 @@ template <typename T, int DH, int NT, int NP> struct Attn {
   int lane;
   uint32_t mask, sixteen, minus16[4];  // (an operand of four registers)
   const uint2* qb;   // this lane's query operands in shared memory: [NT][NP][NG][2] pairs (b0, b1), 32 lanes apart
-  const float2* qs;  // sums of the queries' groups, of this lane's two columns: [NT][NG], 32 lanes apart
+  const float4* qs;  // sums of the queries' groups, of this lane's two columns, and OFF times them: [NT][NG], 32 lanes apart
   float o[NT][DH / 16][4];
   float corr[NT][NG][2];  // (fp32) this lane's keys' sums with the zeros
   float m[NT][2], l[NT][2];
   int lim[NT][2];  // last key of this lane's two columns
 
-  // The tile's queries into `dst` (by all warps), and this lane's state.
-  __device__ __forceinline__ void load_q(const KvqAttn& p, int seq, int r0, int head, uint8_t* dst) {
+  // The tile's queries, a group by each warp, and the columns' last keys: first the loads (float q[NT][8], which the
+  // caller keeps while it starts others), then into shared memory, with this lane's state.
+  __device__ __forceinline__ void load_q(const KvqAttn& p, int seq, int r0, int head, float (&f)[NT][8]) {
     // read once: the compiler would fetch and rebuild them in every block
     asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
     asm volatile("mov.u32 %0, 0x00780078;" : "=r"(mask));
@@ -152,45 +153,54 @@ template <typename T, int DH, int NT, int NP> struct Attn {
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("mov.u32 %0, 0xc180c180;" : "=r"(minus16[i]));
     const int rr = lane >> 2, tq = lane & 3, rows = p.T * p.G, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = r0 + nt * 8 + rr;
+      const int t = row < rows ? row / p.G : 0, g = row - t * p.G;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[nt][i] = 0.f;
+      if (row < rows && w < NG)
+        load8(static_cast<const T*>(p.q) + (static_cast<long long>(seq) * p.T + t) * p.ldq +
+                  static_cast<long long>(head * p.G + g) * DH + 8 * tq + 32 * w,
+              f[nt]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = r0 + nt * 8 + 2 * tq + c;
+        lim[nt][c] = col < rows ? p.q_pos[static_cast<long long>(seq) * p.T + col / p.G] : -1;
+      }
+    }
+  }
+  __device__ __forceinline__ void start(uint8_t* dst, float (&f)[NT][8]) {
+    const int tq = lane & 3, grp = threadIdx.x >> 5;
     uint2* b = reinterpret_cast<uint2*>(dst) + lane;
-    float2* sums = reinterpret_cast<float2*>(dst + NT * NP * NG * 2 * 32 * 8) + lane;
+    float4* sums = reinterpret_cast<float4*>(dst + NT * NP * NG * 2 * 32 * 8) + lane;
     qb = b;
     qs = sums;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = r0 + nt * 8 + rr;
-      const bool in = row < rows;
-      const int t = in ? row / p.G : 0, g = in ? row - t * p.G : 0;
-      const T* src = static_cast<const T*>(p.q) + (static_cast<long long>(seq) * p.T + t) * p.ldq +
-                     static_cast<long long>(head * p.G + g) * DH + 8 * tq;
-      if (w < NG) {  // a warp for each group
-        const int grp = w;
-        float f[8] = {};
-        if (in) load8(src + 32 * grp, f);
+      if (grp < NG) {
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += f[i];
+        for (int i = 0; i < 8; ++i) sum += f[nt][i];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const float s0 = __shfl_sync(0xffffffffu, sum, 8 * tq), s1 = __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
-        sums[(nt * NG + grp) * 32] = make_float2(s0, s1);
+        sums[(nt * NG + grp) * 32] = make_float4(s0, s1, OFF * s0, OFF * s1);
 #pragma unroll
         for (int np = 0; np < NP; ++np) {
           uint32_t u[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) u[i] = split_off(f[i], f[i + 4]);
+          for (int i = 0; i < 4; ++i) u[i] = split_off(f[nt][i], f[nt][i + 4]);
           b[((nt * NP + np) * NG + grp) * 2 * 32] = make_uint2(u[0], u[1]);
           b[(((nt * NP + np) * NG + grp) * 2 + 1) * 32] = make_uint2(u[2], u[3]);
         }
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int col = r0 + nt * 8 + 2 * tq + c;
-        lim[nt][c] = col < rows ? p.q_pos[static_cast<long long>(seq) * p.T + col / p.G] : -1;
         m[nt][c] = -INFINITY;
         l[nt][c] = 0.f;
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) corr[nt][grp][c] = 0.f;
+        for (int g = 0; g < NG; ++g) corr[nt][g][c] = 0.f;
       }
 #pragma unroll
       for (int j = 0; j < DH / 16; ++j)
@@ -238,11 +248,11 @@ template <typename T, int DH, int NT, int NP> struct Attn {
       float c[2][NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float2 q = qs[(nt * NG + g) * 32];
+        const float4 q = qs[(nt * NG + g) * 32];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[u][nt][i] = (half(kz[u][i >> 1][g / 2]) + OFF) * (i & 1 ? q.y : q.x);
+          for (int i = 0; i < 4; ++i) c[u][nt][i] = fmaf(half(kz[u][i >> 1][g / 2]), i & 1 ? q.y : q.x, i & 1 ? q.w : q.z);
       }
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
@@ -457,11 +467,11 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   constexpr int R = A::R, ROW = A::ROW;
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int TILES = 256;
-  __shared__ long long scan[AW * 32 + 1];
+  __shared__ long long scan[AW];
   __shared__ int tile_len[TILES];
   // the schedule, kept out of the registers of the loop over the keys
   __shared__ struct {
-    long long n, share, rest;    // CTAs at work; their shares: share quanta, the first `rest` one more
+    long long share, rest;       // the CTAs' shares: share quanta, the first `rest` one more
     long long begin, end;        // this CTA's
     long long cur, base, unit;   // where it is; its tile's and its unit's first quantum
     int ti, len, nq, q0, q1, seq, head, r0;
@@ -473,13 +483,65 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, rr = lane >> 2, tq = lane & 3;
   const int heads = p.c.n_kv_heads, rows = p.T * p.G;
 
-  // this CTA's share of all quanta
-  const int per = (p.n_tiles + AW * 32 - 1) / (AW * 32);
-  long long mine = 0;
-  for (int i = tid * per; i < min(p.n_tiles, (tid + 1) * per); ++i) {
-    int len;
-    mine += tile_quanta(p, i, R, len);
-    if (i < TILES) tile_len[i] = len;
+  // this CTA's share of all quanta: the tiles' quanta and running sums, by one warp where it has a lane for each
+  const bool few = p.n_tiles <= 32;
+  if (few && w != 0) {
+    // (waits for the first warp below)
+  } else {
+    const int lanes = few ? 32 : AW * 32, per = (p.n_tiles + lanes - 1) / lanes;
+    long long mine = 0;
+    for (int i = tid * per; i < min(p.n_tiles, (tid + 1) * per); ++i) {
+      int len;
+      mine += tile_quanta(p, i, R, len);
+      if (i < TILES) tile_len[i] = len;
+    }
+    mine *= heads;
+    long long sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += y;
+    }
+    if (!few) {
+      if (lane == 31) scan[w] = sum;
+      __syncthreads();
+      long long before = 0;
+#pragma unroll
+      for (int i = 0; i < AW; ++i)
+        if (i < w) before += scan[i];
+      sum += before;
+    }
+    long long total = few ? __shfl_sync(0xffffffffu, sum, 31) : 0;
+    if (!few) {
+#pragma unroll
+      for (int i = 0; i < AW; ++i) total += scan[i];
+    }
+    const long long n = min(static_cast<long long>(gridDim.x), quotient(total + MIN_SHARE - 1, MIN_SHARE));
+    const long long share = quotient(total, n), rest = total - share * n;
+    const long long cur = share * blockIdx.x + min(static_cast<long long>(blockIdx.x), rest);
+    const long long end = blockIdx.x < n ? cur + share + (blockIdx.x < rest) : cur;  // (nothing for the other CTAs)
+    if (tid == 0) {
+      sc.share = share;
+      sc.rest = rest;
+      sc.begin = sc.cur = cur;
+      sc.end = end;
+    }
+    if (cur < end && sum - mine <= cur && cur < sum) {
+      long long base = sum - mine;
+      int i = tid * per;
+      for (;; ++i) {
+        int len = 0;
+        if (i < TILES)
+          len = tile_len[i];
+        else
+          tile_quanta(p, i, R, len);
+        const long long q = static_cast<long long>(quanta_of(len)) * heads;
+        if (cur < base + q) break;
+        base += q;
+      }
+      sc.ti = i;
+      sc.base = base;
+    }
   }
   // how many keys a tile sees: kept for the first ones, looked up again for the others
   auto len_of = [&](int i) {
@@ -488,54 +550,11 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
     tile_quanta(p, i, R, len);
     return len;
   };
-  scan[tid + 1] = mine * heads;
-  if (tid == 0) scan[0] = 0;
-  __syncthreads();
-  if (w == 0) {  // inclusive sums, four entries a lane
-    long long x[AW], run = 0;
-#pragma unroll
-    for (int i = 0; i < AW; ++i) x[i] = run += scan[1 + lane * AW + i];
-    long long up = run;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, up, d);
-      if (lane >= d) up += y;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < AW; ++i) scan[1 + lane * AW + i] = x[i] + up - run;
-  }
-  __syncthreads();
-  const long long total = scan[AW * 32];
-  const long long n = min(static_cast<long long>(gridDim.x), quotient(total + MIN_SHARE - 1, MIN_SHARE));
-  if (blockIdx.x >= n) return;
-  const long long share = quotient(total, n), rest = total - share * n;
   auto begin_of = [&](long long c) { return sc.share * c + min(c, sc.rest); };
   auto owner_of = [&](long long x) {
     const long long longer = sc.rest * (sc.share + 1);
     return static_cast<int>(x < longer ? quotient(x, sc.share + 1) : sc.rest + quotient(x - longer, sc.share));
   };
-  {
-    const long long cur = share * blockIdx.x + min(static_cast<long long>(blockIdx.x), rest);
-    if (tid == 0) {
-      sc.n = n;
-      sc.share = share;
-      sc.rest = rest;
-      sc.begin = sc.cur = cur;
-      sc.end = cur + share + (blockIdx.x < rest);
-    }
-    if (scan[tid] <= cur && cur < scan[tid + 1]) {
-      long long base = scan[tid];
-      int i = tid * per;
-      for (;; ++i) {
-        const long long q = static_cast<long long>(quanta_of(len_of(i))) * heads;
-        if (cur < base + q) break;
-        base += q;
-      }
-      sc.ti = i;
-      sc.base = base;
-    }
-  }
 
   for (;;) {
     __syncthreads();
@@ -584,10 +603,14 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
       fetch(i + 1);
       cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < A::STAGES - 2; i += 2) fetch_two(i);
     A a;
-    a.load_q(p, seq, r0, head, smem + A::WORK);
+    {
+      float q[NT][8];
+      a.load_q(p, seq, r0, head, q);
+#pragma unroll
+      for (int i = 0; i < A::STAGES - 2; i += 2) fetch_two(i);
+      a.start(smem + A::WORK, q);
+    }
     __syncthreads();
     const int all = a.seen_by_all(p, r0);
     for (int i = 0; i < count; i += 2) {
@@ -674,9 +697,11 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
     if (!whole) {
       if (tid < R) *reinterpret_cast<float2*>(slot + MAX_ROWS * DH + 2 * tid) = make_float2(row_m[tid], row_l[tid]);
       const int c0 = owner_of(sc.unit), c1 = owner_of(sc.unit + sc.nq - 1);  // CTAs of this unit
-      __threadfence();
       __syncthreads();
-      if (tid == 0) is_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
+      if (tid == 0) {
+        __threadfence();  // (with the barrier before it: all of the CTA's part)
+        is_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
+      }
       __syncthreads();
       if (is_last) {
         __threadfence();
@@ -687,34 +712,46 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
         const int shift = sc.unit != begin_of(c0) ? slot_floats(DH) : 0, np = c1 - c0 + 1;
         float* wt = reinterpret_cast<float*>(smem) + w * (A::WEIGHTS / 4 / AW);
         for (int row = w; row < R && r0 + row < rows; row += AW) {
-          float M = -INFINITY, L = 0.f;
-          for (int c = lane; c < np; c += 32)
-            M = fmaxf(M, __ldcg(parts + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift) + MAX_ROWS * DH + 2 * row));
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-          for (int c = lane; c < np; c += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(
-                parts + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift) + MAX_ROWS * DH + 2 * row));
-            const float x = part_weight(ml.x, ml.y, M);
-            wt[c] = x;
-            if (x != 0.f) L = fmaf(x, ml.y, L);
-          }
-          L = warp_sum(L);
-          __syncwarp();
-          constexpr int CH = DH / 32;  // channels a lane
-          float x[CH] = {};
-          const float* src = parts + row * DH + lane * CH;
-#pragma unroll 8
-          for (int c = 0; c < np; ++c) {
-            const float f = wt[c];
-            float v[CH];
-            const float* at = src + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift);
+          constexpr int CH = DH / 32, AHEAD = 8;  // channels a lane; parts whose loads are under way together
+          auto part = [&](int c) { return parts + (c ? 2 * static_cast<size_t>(c) * slot_floats(DH) : shift); };
+          auto load = [&](int c, float (&v)[CH]) {
+            const float* at = part(c) + row * DH + lane * CH;
             if (CH == 4)
               *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(at));
             else
               *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(at));
+          };
+          float v[AHEAD][CH];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) x[i] = f != 0.f ? fmaf(f, v[i], x[i]) : x[i];
+          for (int i = 0; i < AHEAD; ++i)
+            if (i < np) load(i, v[i]);
+          float M = -INFINITY, L = 0.f;
+          for (int c = lane; c < np; c += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c) + MAX_ROWS * DH + 2 * row));
+            wt[c] = ml.x;
+            wt[c + KVQ_MAX_CTAS] = ml.y;
+            M = fmaxf(M, ml.x);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+          for (int c = lane; c < np; c += 32) {
+            const float x = part_weight(wt[c], wt[c + KVQ_MAX_CTAS], M);
+            if (x != 0.f) L = fmaf(x, wt[c + KVQ_MAX_CTAS], L);
+            wt[c] = x;
+          }
+          L = warp_sum(L);
+          __syncwarp();
+          float x[CH] = {};
+          for (int c0 = 0; c0 < np; c0 += AHEAD) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+              if (c0 + i < np) {
+                const float f = wt[c0 + i];
+#pragma unroll
+                for (int k = 0; k < CH; ++k) x[k] = f != 0.f ? fmaf(f, v[i][k], x[k]) : x[k];
+                if (c0 + AHEAD + i < np) load(c0 + AHEAD + i, v[i]);
+              }
+            }
           }
           __syncwarp();
           const int gr = r0 + row, t = gr / p.G;
