@@ -452,7 +452,8 @@ cb_status cb_attention(const void* q, const int32_t* q_pos, int m, const void* k
  * max_pages entries.  Pages of one sequence stand in any order; sequences may share pages that no call writes.
  * Device-side problems (a sequence >= n_seqs, a position beyond max_pages pages, a page outside 0..n_pages - 1: the
  * row is not written, reads as zeros, or its keys are left out) go to the standalone status word that
- * cb_gemm_get_status() reads.  Sizes: n_kv_heads <= 1024, n_seqs <= 2^20, page_tokens * max_pages < 2^31. */
+ * cb_gemm_get_status() reads.  Sizes: n_kv_heads <= 1024, n_seqs <= 2^20, page_tokens * max_pages < 2^31, at most 2^30
+ * rows, 2^31 / n_kv_heads and 2^30 query heads a call (CB_ERR_SHAPE).  No output overlaps another argument. */
 typedef struct {
   void* pool;            /* device, 16-byte aligned */
   int n_pages, page_tokens, n_kv_heads, head_dim;

@@ -665,6 +665,8 @@ def cb_kvq_read(pool: torch.Tensor, table: torch.Tensor, pos: torch.Tensor, seq:
             k_out = torch.empty(want, dtype=dtype, device=pool.device) if k_out is None else k_out
             v_out = torch.empty(want, dtype=dtype, device=pool.device) if v_out is None else v_out
     dtype = k_out.dtype
+    if not -0x80000000 <= delta_pos <= 0x7FFFFFFF:
+        raise CacheBlendError(2, "delta_pos is beyond 32 bits")
     _check((_lib or load_library()).cb_kvq_read(
         cache, of, at, rows, delta_pos, theta, _dtype_code(dtype), k_out.data_ptr(),
         _kvq_rows(k_out, dtype, want, "k_out", dev), v_out.data_ptr(), _kvq_rows(v_out, dtype, want, "v_out", dev),

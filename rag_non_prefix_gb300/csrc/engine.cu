@@ -1429,7 +1429,8 @@ cb_status cb_kvq_write(const cb_kvq_cache* cache, const void* k, long long ldk, 
   const cb_status st = kvq_view(cache, &c);
   if (st != CB_OK) return st;
   if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
-  if (rows < 0 || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll) return fail(nullptr, CB_ERR_SHAPE, "bad number of rows");
+  if (rows < 0 || rows > (1 << 30) || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll)
+    return fail(nullptr, CB_ERR_SHAPE, "bad number of rows");
   if (rows == 0) return CB_OK;
   if (!k || !v || !pos) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
   const long long width = static_cast<long long>(c.n_kv_heads) * cache->head_dim;
@@ -1448,7 +1449,7 @@ cb_status cb_kvq_read(const cb_kvq_cache* cache, const int32_t* seq, const int32
   const cb_status st = kvq_view(cache, &c);
   if (st != CB_OK) return st;
   if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
-  if (rows < 0 || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll || !(theta > 0))
+  if (rows < 0 || rows > (1 << 30) || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll || !(theta > 0))
     return fail(nullptr, CB_ERR_SHAPE, "bad number of rows or theta");
   if (rows == 0) return CB_OK;
   if (!k_out || !v_out || !pos) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
@@ -1493,18 +1494,22 @@ cb_status cb_kvq_attention(const cb_kvq_cache* cache, const void* q, long long l
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_kvq_attention");
 }
 
+// null or misaligned arrays of a value per row
+static bool bad_sampling(const cb_sampling* params, const float* uniform, const int32_t* out) {
+  const cb_sampling f = params ? *params : cb_sampling{};
+  auto off = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; };
+  return !uniform || !out || off(uniform) || off(out) || off(f.temperature) || off(f.top_k) || off(f.top_p) || off(f.min_p);
+}
+
 cb_status cb_sample(const void* logits, long long ld, cb_dtype dtype, int rows, int vocab, const cb_sampling* params,
                     const float* uniform, int32_t* out, void* stream) {
   if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
   if (rows < 0 || rows > (1 << 24) || vocab < 1 || vocab > SAMPLE_MAX_VOCAB || (rows > 1 && ld < vocab))
     return fail(nullptr, CB_ERR_SHAPE, "sampling takes up to 2^24 rows of 1 to 2^18 logits");
   if (rows == 0) return CB_OK;
-  if (!logits || !uniform || !out) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  if (!logits || bad_sampling(params, uniform, out) || (reinterpret_cast<uintptr_t>(logits) & (dtype == CB_BF16 ? 1 : 3)))
+    return fail(nullptr, CB_ERR_INVALID_ARG, "null or misaligned pointer");
   const cb_sampling f = params ? *params : cb_sampling{};
-  auto off = [](const void* p, unsigned size) { return reinterpret_cast<uintptr_t>(p) & (size - 1); };
-  if (off(logits, dtype == CB_BF16 ? 2 : 4) || off(uniform, 4) || off(out, 4) || off(f.temperature, 4) || off(f.top_k, 4) ||
-      off(f.top_p, 4) || off(f.min_p, 4))
-    return fail(nullptr, CB_ERR_INVALID_ARG, "misaligned pointer");
   cudaError_t e = launch_sample(logits, ld, dtype, rows, vocab, f.temperature, f.top_k, f.top_p, f.min_p, uniform, out,
                                 as_stream(stream));
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_sample");
@@ -1868,7 +1873,7 @@ cb_status cb_decode_step(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, cons
 
 cb_status cb_decode_step_sample(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, const int32_t* tokens,
                                 const cb_sampling* params, const float* uniform, int32_t* out_tokens, void* stream) {
-  if (!ctx || !uniform) return fail(ctx, CB_ERR_INVALID_ARG, "bad decode arguments");
+  if (!ctx || bad_sampling(params, uniform, out_tokens)) return fail(ctx, CB_ERR_INVALID_ARG, "bad decode arguments");
   if (ctx->cfg.vocab > SAMPLE_MAX_VOCAB) return fail(ctx, CB_ERR_SHAPE, "sampling takes up to 2^18 logits a row");
   return decode_step(ctx, seqs, n_seq, tokens, params, uniform, out_tokens, stream);
 }

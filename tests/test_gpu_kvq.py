@@ -196,6 +196,89 @@ def test_attention_over_the_cache(case, dtype):
     cb.cb_gemm_get_status()
 
 
+def test_many_sequences_and_long_ones():
+    """More tiles than are kept in shared memory, of one to some hundred keys; a sequence whose parts are many."""
+    lens = [1 + (37 * i) % 90 for i in range(300)]
+    pool, table, g = filled(30, lens, 16, 1, 64)
+    q = rand(g, 300, 2, 64).bfloat16()
+    check_attention(q, ints([m - 1 for m in lens]), pool, table)
+    pool, table, g = filled(32, [30000], 256, 1, 128)
+    for dtype in (torch.bfloat16, torch.float32):
+        check_attention(rand(g, 1, 3, 2, 128).to(dtype), ints([[29999, 20000, 29998]]), pool, table)
+
+
+def test_pages_beyond_32_bits():
+    """A pool of 2.5 GB: pages at its end, written, read and attended to."""
+    pool = torch.zeros(31000, 8, 4, 2560, dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 2 ** 31
+    table = ints([[30999, 5, 30998], [3, 30500, 26300]])
+    g = gen(34)
+    k, v = rand(g, 300, 8, 128).bfloat16(), rand(g, 300, 8, 128).bfloat16()
+    pos, seq = [p for p in range(150)] * 2, [0] * 150 + [1] * 150
+    cb.cb_kvq_write(pool, table, k, v, ints(pos), ints(seq))
+    near = [30999, 5, 30998, 3, 30500, 26300]
+    few, small = pool[near].contiguous(), ints([[0, 1, 2], [3, 4, 5]])
+    kr, vr = cb.cb_kvq_read(pool, table, ints(pos), ints(seq), dtype=torch.float32)
+    for got, want in zip((kr, vr), cb.cb_kvq_read(few, small, ints(pos), ints(seq), dtype=torch.float32)):
+        assert torch.equal(got, want)
+    assert torch.equal(kr[:40].double().cpu(), ref.values(k[:40]))
+    q = rand(g, 2, 16, 128).bfloat16()
+    assert torch.equal(cb.cb_kvq_attention(q, ints([149, 149]), pool, table), cb.cb_kvq_attention(q, ints([149, 149]), few, small))
+
+
+def test_padded_queries_of_nan():
+    """A padding row's query may hold anything: its output is zero, and no other row sees it."""
+    pool, table, g = filled(36, [50, 20], 16, 1, 128)
+    q = rand(g, 2, 3, 4, 128).bfloat16()
+    q[0, 1] = float("nan")
+    q[1, 0] = float("inf")
+    got = cb.cb_kvq_attention(q, ints([[48, -1, 49], [-1, 18, 19]]), pool, table)
+    assert torch.all(got[0, 1] == 0) and torch.all(got[1, 0] == 0) and not torch.any(got.isnan())
+    clean = q.clone()
+    clean[0, 1], clean[1, 0] = 0, 0
+    assert torch.equal(got, cb.cb_kvq_attention(clean, ints([[48, -1, 49], [-1, 18, 19]]), pool, table))
+
+
+def test_pages_shared_by_two_sequences():
+    """A common beginning in one set of pages, each sequence going on in its own."""
+    g = gen(38)
+    pool = cb.kvq_pool(6, 16, 2, 64)
+    table = ints([[4, 0, 1], [4, 0, 5]])
+    k, v = rand(g, 32, 2, 64), rand(g, 32, 2, 64)
+    cb.cb_kvq_write(pool, table, k, v, ints(range(32)), ints([1] * 32))
+    own = rand(g, 2, 2, 64)
+    cb.cb_kvq_write(pool, table, own, own, ints([32, 32]))  # (row i of sequence i)
+    check_attention(rand(g, 2, 4, 64).bfloat16(), ints([32, 32]), pool, table)
+
+
+def test_the_first_calls_of_a_process_may_be_captured(tmp_path):
+    """No call needs one before it: all three are captured first, replayed, and give what eager calls give."""
+    code = """
+import torch, rag_non_prefix_gb300 as cb
+pool, table = cb.kvq_pool(4, 16, 1, 64), torch.tensor([[2, 0], [3, 1]], dtype=torch.int32, device="cuda")
+k, q = torch.randn(2, 1, 64, device="cuda"), torch.randn(2, 2, 64, device="cuda")
+pos, x, u = torch.tensor([0, 0], dtype=torch.int32, device="cuda"), torch.randn(2, 500, device="cuda"), torch.rand(2, device="cuda")
+scratch, out = cb.kvq_scratch(), torch.empty_like(q)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    cb.cb_kvq_write(pool, table, k, k, pos)
+    cb.cb_kvq_attention(q, pos, pool, table, out=out, scratch=scratch)
+    kr, vr = cb.cb_kvq_read(pool, table, pos, dtype=torch.float32)
+    tok = cb.cb_sample(x, u)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(tok, cb.cb_sample(x, u)) and torch.equal(out, cb.cb_kvq_attention(q, pos, pool, table))
+assert torch.equal(vr, cb.cb_kvq_read(pool, table, pos, dtype=torch.float32)[1]) and (vr - k).abs().max() < 0.5
+print("fine")
+"""
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 def filled(seed, lens, page, hkv, dh, spare=1):
     pool, table = make(seed, len(lens), max(lens), page, hkv, dh, spare)
     g = gen(seed + 1)

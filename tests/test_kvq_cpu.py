@@ -79,7 +79,7 @@ def test_bad_arguments_are_refused(lib):
     c = cache()
     write = lambda k=256, ldk=128, v=256, ldv=128, dt=1, pos=256, rows=1: lib.cb_kvq_write(c, k, ldk, v, ldv, dt, None, pos, rows, None)  # noqa: E731
     assert [write(k=None), write(v=None), write(pos=None)] == [1, 1, 1]
-    assert [write(k=264), write(v=264), write(ldk=127), write(ldv=120), write(ldk=132), write(rows=-1), write(rows=1 << 30)] == [2] * 7
+    assert [write(k=264), write(v=264), write(ldk=127), write(ldv=120), write(ldk=132), write(rows=-1), write(rows=(1 << 30) + 1)] == [2] * 7
     assert write(dt=7) == 3 and write(rows=0, k=None, v=None, pos=None) == 0
     read = lambda k=256, ldk=128, pos=256, rows=1, theta=1e4, dt=1: lib.cb_kvq_read(c, None, pos, rows, 3, theta, dt, k, ldk, 256, 128, None)  # noqa: E731
     assert [read(k=None), read(pos=None)] == [1, 1] and read(dt=7) == 3 and read(rows=0, k=None) == 0

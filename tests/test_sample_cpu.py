@@ -40,6 +40,7 @@ def test_bad_arguments_are_refused(lib):
         p[field] = 258
         assert call(params=C.byref(cb.Sampling(*p))) == 1
     assert lib.cb_decode_step_sample(None, None, 1, None, None, 256, None, None) == 1
+    assert [call(u=256, out=257), call(u=None, params=C.byref(cb.Sampling(256, 256, 256, 256)))] == [1, 1]
 
 
 def test_the_binding_refuses_before_the_library(lib):
