@@ -79,7 +79,9 @@ struct __align__(16) Smem {
   float c_hi, c_lo;
   Ctl ctl[2];
   int n_list[2];
-  // (the first CTA's own, while no histogram is in use)
+  // (while no histogram is in use: a row's first vectors, and the first CTA's own)
+  static constexpr int STASH = (sizeof(uint32_t) * 3 * BUCKETS + sizeof(u64) * BUCKETS) / 16;
+  __device__ uint4* stash() { return reinterpret_cast<uint4*>(hist[0]); }
   __device__ u64* work() { return reinterpret_cast<u64*>(hist[1]); }
   __device__ u64* sums() { return reinterpret_cast<u64*>(hist[2]); }
 };
@@ -239,26 +241,29 @@ template <typename T> struct Sampler {
       g(first + v * VEC);
     }
   }
-  // f(vector, its first element's index) over this CTA's tokens, some loads ahead
-  template <typename F> __device__ __forceinline__ void vectors(F f) const {
+  // f(vector, its number) over this CTA's tokens from vector v0 on, some loads ahead
+  template <typename F> __device__ __forceinline__ void vectors(int v0, F f) const {
     constexpr int BATCH = 8;
 #pragma unroll 1
-    for (int v0 = tid; v0 < n_vec; v0 += BATCH * ST) {
+    for (v0 += tid; v0 < n_vec; v0 += BATCH * ST) {
       uint4 e[BATCH];
 #pragma unroll
       for (int j = 0; j < BATCH; ++j)
         if (v0 + j * ST < n_vec) e[j] = raw_vector(v0 + j * ST);
 #pragma unroll
       for (int j = 0; j < BATCH; ++j)
-        if (v0 + j * ST < n_vec) f(cleaned(e[j]), first + (v0 + j * ST) * VEC);
+        if (v0 + j * ST < n_vec) f(cleaned(e[j]), v0 + j * ST);
     }
   }
-  // The tokens of at least `least` into list 0, by the threads whose largest is one.
+  // The tokens of at least `least` into list 0, by the threads whose largest is one; the first vectors are in the stash.
   __device__ __forceinline__ void collect_from(float least, float own) {
     if (own < least) return;
     uint32_t some = 0;  // this thread's vectors (at most 32) that hold one
-    vectors([&](uint4 e, int idx) {
-      if (largest(e) >= least) some |= 1u << ((idx - first) / VEC - tid) / ST;
+#pragma unroll 4
+    for (int v = tid; v < min(n_vec, Smem::STASH); v += ST)
+      if (largest(s.stash()[v]) >= least) some |= 1u << v / ST;
+    vectors(Smem::STASH, [&](uint4 e, int v) {
+      if (largest(e) >= least) some |= 1u << v / ST;
     });
 #pragma unroll 1
     while (some) {
@@ -283,8 +288,15 @@ template <typename T> struct Sampler {
     }
   }
 
+  __device__ __forceinline__ void meet() {  // all CTAs of the row
+    if (ranks == 1)
+      __syncthreads();
+    else
+      cl.sync();
+  }
+
   __device__ __forceinline__ Ctl decide() {  // what the first CTA wrote into ctl[phase], for everyone
-    cl.sync();
+    meet();
     const Ctl c = *cl.map_shared_rank(&s.ctl[phase], 0);
     phase ^= 1;
     return c;
@@ -337,7 +349,7 @@ template <typename T> struct Sampler {
         if (lane == 0) s.part[1] = over;
       }
     }
-    cl.sync();
+    meet();
     // each CTA sums a slice of the buckets over the cluster
     const int slice = BUCKETS / ranks;
     u64* tot = cl.map_shared_rank(s.tot, 0);
@@ -350,7 +362,7 @@ template <typename T> struct Sampler {
       }
       tot[i] = sum;
     }
-    cl.sync();
+    meet();
     if (rank == 0) {
       running_sums();
     }
@@ -430,6 +442,28 @@ template <typename T> struct Sampler {
   // first CTA: its threads' first n numbers (at most LIST), largest first; thread i gets the i-th
   __device__ __forceinline__ u64 sorted(u64 v, int n) {
     u64* work = s.work();
+    if (n <= ST / 2) {  // each token's place counted: two threads a token, half of the others each (fewer steps than a sort's)
+      constexpr int HALF = ST / 2;
+      const int i = tid & (HALF - 1), mid = (n + 1) / 2;
+      if (tid < HALF) work[tid] = tid < n ? v : 0;
+      __syncthreads();
+      const u64 mine = work[i];
+      int place = 0;
+      if (i < n) {
+        const int j0 = tid < HALF ? 0 : mid, j1 = tid < HALF ? mid : n;
+#pragma unroll 4
+        for (int j = j0; j < j1; ++j) place += work[j] > mine;
+      }
+      int* upper = reinterpret_cast<int*>(work + 2 * HALF);
+      if (tid >= HALF) upper[i] = place;
+      __syncthreads();
+      u64* out = work + HALF;
+      if (tid < n) out[place + upper[i]] = mine;
+      __syncthreads();
+      v = tid < n ? out[tid] : 0;
+      __syncthreads();
+      return v;
+    }
     int size = 32;
     while (size < n) size <<= 1;
     // (the warps that hold tokens only, with a barrier of their own)
@@ -460,7 +494,7 @@ template <typename T> struct Sampler {
     each([&](float x, int idx) {
       if (x > -INFINITY && take(x, idx)) collect(0, x, idx);
     });
-    cl.sync();
+    meet();
     return collected(0);
   }
 
@@ -535,6 +569,8 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   int k = a.top_k ? a.top_k[row] : 0;
   const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
   const float u = a.uniform[row];
+  if (!(t > 0.f)) k = 1;
+  if (k <= 0 || k >= a.vocab) k = a.vocab;
   if (tid == ST - 1) {
     const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(t, 1e-20f), 1e20f));
     s.c_hi = static_cast<float>(c);
@@ -543,7 +579,11 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     s.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
   }
   float own = -INFINITY;  // this thread's largest
-  z.vectors([&](uint4 e, int) { own = fmaxf(own, z.largest(e)); });
+  const bool keep = k > 1 && k <= z.ranks * (ST / 2) && k < a.vocab;  // (way 1)
+  z.vectors(0, [&](uint4 e, int v) {
+    own = fmaxf(own, z.largest(e));
+    if (keep && v < Smem::STASH) s.stash()[v] = e;
+  });
   uint32_t key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(composite(own, 0) >> 32));
   if (lane == 0) s.warp[warp] = key;
   __syncthreads();
@@ -551,15 +591,13 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     key = __reduce_max_sync(0xffffffffu, lane < SW ? static_cast<uint32_t>(s.warp[lane]) : 0u);
     if (lane == 0) s.part[0] = key;
   }
-  if (!(t > 0.f)) k = 1;
-  if (k <= 0 || k >= a.vocab) k = a.vocab;
-  z.cl.sync();
+  z.meet();
   key = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(z.of_each(&s.part[0], 0ull)));
   z.top = logit_of(static_cast<u64>(key) << 32);
   // (no CTA leaves while another reads its shared memory)
   if (!(z.top > -INFINITY)) {
     if (z.rank == 0 && tid == 0) a.out[row] = -1;
-    z.cl.sync();
+    z.meet();
     return;
   }
   if (z.top == INFINITY) {  // its tokens are equally likely, the others are none
@@ -580,10 +618,10 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       at = __reduce_min_sync(0xffffffffu, lane < SW ? static_cast<unsigned>(s.warp[lane]) : 0xffffffffu);
       if (lane == 0) s.part[1] = at;
     }
-    z.cl.sync();
+    z.meet();
     at = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(z.of_each(&s.part[1], 0xffffffffull)));
     if (z.rank == 0 && tid == 0) a.out[row] = static_cast<int>(at);
-    z.cl.sync();
+    z.meet();
     return;
   }
 
@@ -615,7 +653,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   bool refined = false;
   auto all = [](float, int) { return true; };
   if (k < a.vocab) {
-    if (k <= z.ranks * (ST / 2)) {
+    if (keep) {
       // k / ranks of the threads' largest in each CTA, the least of these over the CTAs: at least k tokens pass it.
       // Each warp sorts its threads' and names the one that its share of k reaches; of these 16 the largest that
       // enough threads pass (all but the least may be too large).
@@ -648,17 +686,17 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       }
       uint32_t bound = __shfl_sync(0xffffffffu, x, hi);
       if (tid == 0) s.part[1] = bound;
-      z.cl.sync();
+      z.meet();
       bound = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(z.of_each(&s.part[1], 0xffffffffull)));
       const float least = logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32);
       if (tid == 0) s.n_list[0] = 0;
       __syncthreads();
       z.collect_from(least, own);
-      z.cl.sync();
+      z.meet();
       const int n_list = z.collected(0);
       if (n_list <= LIST) {
         if (z.rank == 0) settle(n_list);
-        z.cl.sync();
+        z.meet();
         return;
       }
     }
@@ -678,7 +716,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       if (k <= LIST) {  // the first CTA has all that counts
         z.gather([&](float x, int idx) { return composite(x, idx) >= last; });
         if (z.rank == 0) settle(k);
-        z.cl.sync();
+        z.meet();
         return;
       }
       z.eligible = last;
@@ -699,7 +737,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       const float v = fmaf(f, fmaf(f, 16384.f * STEP * STEP, -32768.f * STEP), 32768.f + 8388608.f);
       if (y < NEAR - 1.5f) atomicAdd(&s.hist[0][__float_as_int(r) & (NEAR - 1)], __float_as_uint(v) - 0x4b000000u);
     });
-    z.cl.sync();
+    z.meet();
     {  // each CTA sums a slice over the cluster, into the first one's tot
       const int slice = NEAR / z.ranks;
       float* tot = reinterpret_cast<float*>(z.cl.map_shared_rank(s.tot, 0));
@@ -713,7 +751,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         tot[b] = m * (1.f / 32768.f) * exp2f(static_cast<float>(b) * (-STEP * 1.44269504f));
       }
     }
-    z.cl.sync();
+    z.meet();
     if (z.rank == 0) {
       // running masses of this thread's buckets, 1 for the largest logit's token
       constexpr int EACH = NEAR / ST;
@@ -799,7 +837,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       const u64 v = warp_sum64(lane < SW ? scratch[warp * 32 + lane] : 0);
       if (lane == 0) s.part[1 + warp] = v;
     }
-    z.cl.sync();
+    z.meet();
     const int n_u = z.collected(0), n_p = bp == bu ? n_u : z.collected(1);
     // (every CTA comes to the same result, the first one's below)
     if (z.rank == 0) {
@@ -839,7 +877,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       __syncthreads();
     }
     if (z.decide().count) {
-      z.cl.sync();
+      z.meet();
       return;
     }
   }
@@ -861,7 +899,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   }
   const u64 comp = z.template select<true>(reach_u(mass), live, &refined).comp;
   if (z.rank == 0 && tid == 0) a.out[row] = index_of(comp);
-  z.cl.sync();
+  z.meet();
 }
 
 template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s) {
