@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t split_off(float& x, float& y) {
 }
 
 // Quanta of a unit that sees len keys: UNIT_COST without keys first.
-__device__ __forceinline__ int quanta_of(int len) { return UNIT_COST + (len + QUANTUM - 1) / QUANTUM; }
+__device__ __forceinline__ int quanta_of(int len) { return UNIT_COST + len / QUANTUM + (len % QUANTUM != 0); }
 
 // a / b for numbers that are hardly ever beyond 32 bits
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -209,7 +209,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
     }
   }
 
-  // the last key that every row of the tile sees
+  // the last key that every row of the tile sees (-1: a row sees none)
   __device__ __forceinline__ int seen_by_all(const KvqAttn& p, int r0) const {
     const int tq = lane & 3, rows = p.T * p.G;
     int x = 0x7fffffff;
@@ -219,7 +219,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
       for (int c = 0; c < 2; ++c)
         if (r0 + nt * 8 + 2 * tq + c < rows) x = min(x, lim[nt][c]);
     x = min(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return min(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    return max(min(x, __shfl_xor_sync(0xffffffffu, x, 2)), -1);
   }
 
   // Scores (times 1 / scale) of the 16 keys of each of two blocks in shared memory: keys rr and rr + 8, columns
@@ -456,7 +456,8 @@ template <int DH> __device__ __forceinline__ void copy_block(uint32_t dst, const
   }
 }
 
-// weight of a part (maximum m, sum l) under the common maximum M; a part without keys has none, a NaN stays one
+// weight of a part (maximum m, sum l) under the common maximum M; a part without keys has none (and sums of zero).  Sums are
+// added under weights of zero too: a NaN among them stays one.
 __device__ __forceinline__ float part_weight(float m, float l, float M) {
   return m == -INFINITY && l == 0.f ? 0.f : exp2f(m - M);
 }
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
       const int stage = i % A::STAGES, key0 = (b0 + i * AW) * KVQ_BLOCK;
       const uint32_t ok = i + 1 < count ? there >> stage & 3u : there >> stage & 1u;
       const uint8_t* blk = ring + stage * A::BLK;
-      if (ok == 3 && key0 + QUANTUM + KVQ_BLOCK - 1 <= all)
+      if (ok == 3 && all - key0 >= QUANTUM + KVQ_BLOCK - 1)
         a.template two_blocks<false>(blk, blk + A::BLK, key0, 3, p.scale_log2);
       else if (ok)
         a.template two_blocks<true>(blk, blk + A::BLK, key0, ok, p.scale_log2);
@@ -681,10 +682,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
       if (gr >= rows) break;
       float x = 0.f;
 #pragma unroll
-      for (int k = 0; k < AW; ++k) {
-        const float wt = wts[k][row];
-        if (wt != 0.f) x = fmaf(wt, sm[(k * R + row) * ROW + ch], x);
-      }
+      for (int k = 0; k < AW; ++k) x = fmaf(wts[k][row], sm[(k * R + row) * ROW + ch], x);
       if (whole) {
         const int t = gr / p.G;
         static_cast<T*>(p.out)[(static_cast<long long>(seq) * p.T + t) * p.ldo +
@@ -736,7 +734,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
           for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
           for (int c = lane; c < np; c += 32) {
             const float x = part_weight(wt[c], wt[c + KVQ_MAX_CTAS], M);
-            if (x != 0.f) L = fmaf(x, wt[c + KVQ_MAX_CTAS], L);
+            L = fmaf(x, wt[c + KVQ_MAX_CTAS], L);
             wt[c] = x;
           }
           L = warp_sum(L);
@@ -748,7 +746,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
               if (c0 + i < np) {
                 const float f = wt[c0 + i];
 #pragma unroll
-                for (int k = 0; k < CH; ++k) x[k] = f != 0.f ? fmaf(f, v[i][k], x[k]) : x[k];
+                for (int k = 0; k < CH; ++k) x[k] = fmaf(f, v[i][k], x[k]);
                 if (c0 + AHEAD + i < np) load(c0 + AHEAD + i, v[i]);
               }
             }

@@ -1,4 +1,6 @@
 """A KV cache in 4 bits: written, read back and attended to, against the plain 64-bit form."""
+import math
+
 import pytest
 import torch
 
@@ -454,3 +456,45 @@ def test_refusals_of_the_binding():
     for call in bad:
         with pytest.raises(cb.CacheBlendError):
             call()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_nan_in_keys_of_no_weight(dtype, dh):
+    """A NaN that a row sees reaches it, however little its key weighs, from whichever CTA's part of the sequence."""
+    pool, table, g = filled(40, [3200], 64, 1, dh)
+    k, v, q = torch.zeros(3200, 1, dh, device="cuda"), rand(g, 3200, 1, dh), torch.zeros(1, 2, 3, dh, device="cuda").to(dtype)
+    q[..., 0] = 40.0
+    v[700, 0, 40] = float("nan")
+    k[:1000, 0, 0] = -64.0  # (a weight of exp(-40 * 64 / 8) or less)
+    cb.cb_kvq_write(pool, table, k, v, ints(range(3200)), ints([0] * 3200))
+    got = cb.cb_kvq_attention(q, ints([[3199, 699]]), pool, table)
+    assert torch.all(got[0, 0, :, 32:64].isnan()) and not torch.any(got[0, 1].isnan())
+    assert not torch.any(got[0, 0, :, :32].isnan()) and not torch.any(got[0, 0, :, 64:].isnan())
+    # whole parts without a score that is a number
+    k[:1000, 0, 0] = float("nan")
+    cb.cb_kvq_write(pool, table, k, rand(g, 3200, 1, dh), ints(range(3200)), ints([0] * 3200))
+    assert torch.all(cb.cb_kvq_attention(q, ints([[3199, 699]]), pool, table).isnan())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_sequence_of_almost_2_31_keys(dtype):
+    """The longest sequence there is, 2^31 - 16 positions: one page at all of them but the last 8176."""
+    page, n = 8176, 262657
+    assert page * n == 2 ** 31 - 16
+    pool, table = cb.kvq_pool(2, page, 1, 64), torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    k, v = torch.zeros(page, 1, 64, device="cuda"), torch.ones(page, 1, 64, device="cuda")
+    cb.cb_kvq_write(pool, table, k, v, ints(range(page)), ints([0] * page))
+    cb.cb_kvq_write(pool, table, k + 1, -v, ints(range(page * (n - 1), page * n)), ints([0] * page))
+    q = torch.zeros(1, 3, 1, 64, device="cuda").to(dtype)
+    q[..., 0] = 12.5  # a key of the last page weighs exp(12.5): 8176 of them about as much as all others
+    seen = [page * n, page * n - 4000, page * (n - 1)]
+    got = cb.cb_kvq_attention(q, ints([[x - 1 for x in seen]]), pool, table, scale=1.0)[0, :, 0].double().cpu()
+    for row, x in zip(got, seen):
+        a, b = min(x, page * (n - 1)), max(0, x - page * (n - 1)) * math.exp(12.5)
+        want = (a - b) / (a + b)
+        # weights of 1 and values of +-1 add up exactly within a CTA; at most 800 parts are added in fp32, each step off by
+        # 2^-24 of the sum (2^-14.3), and scores and exponentials are good to 2^-16
+        assert torch.all((row - want).abs() <= 2.0 ** -13 + abs(want) * torch.finfo(dtype).eps / 2)
+    cb.cb_gemm_get_status()
