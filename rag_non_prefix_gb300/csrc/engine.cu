@@ -1393,6 +1393,8 @@ cb_status cb_add_rmsnorm_quantize(const void* x, long long ldx, cb_dtype x_dtype
 }
 
 // ----------------------------------------------------------------------------- KV cache in 4 bits
+static bool off_int32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
+
 // The cache's sizes and pointers, and where its tokens lie; CB_OK or the refusal.
 static cb_status kvq_view(const cb_kvq_cache* c, cb::KvqView* out) {
   if (!c) return fail(nullptr, CB_ERR_INVALID_ARG, "null cache");
@@ -1403,7 +1405,7 @@ static cb_status kvq_view(const cb_kvq_cache* c, cb::KvqView* out) {
     return fail(nullptr, CB_ERR_SHAPE, "bad sizes of a 4-bit cache (page_tokens must be a multiple of 16)");
   if ((c->n_pages > 0 && !c->pool) || (c->n_seqs > 0 && c->max_pages > 0 && !c->table))
     return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
-  if (!aligned16(c->pool) || (reinterpret_cast<uintptr_t>(c->table) & 3))
+  if (!aligned16(c->pool) || off_int32(c->table))
     return fail(nullptr, CB_ERR_INVALID_ARG, "the pool must be 16-byte aligned");
   *out = {static_cast<uint8_t*>(c->pool), c->table, c->ld_table, c->n_pages, c->page_tokens, c->n_kv_heads, c->max_pages,
           c->n_seqs};
@@ -1432,7 +1434,7 @@ cb_status cb_kvq_write(const cb_kvq_cache* cache, const void* k, long long ldk, 
   if (rows < 0 || rows > (1 << 30) || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll)
     return fail(nullptr, CB_ERR_SHAPE, "bad number of rows");
   if (rows == 0) return CB_OK;
-  if (!k || !v || !pos) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  if (!k || !v || !pos || off_int32(pos) || off_int32(seq)) return fail(nullptr, CB_ERR_INVALID_ARG, "null or misaligned pointer");
   const long long width = static_cast<long long>(c.n_kv_heads) * cache->head_dim;
   if (bad_rows(k, ldk, width, dtype) || bad_rows(v, ldv, width, dtype)) return fail(nullptr, CB_ERR_SHAPE, kKvqRows);
   int32_t* status = nullptr;
@@ -1452,7 +1454,8 @@ cb_status cb_kvq_read(const cb_kvq_cache* cache, const int32_t* seq, const int32
   if (rows < 0 || rows > (1 << 30) || static_cast<long long>(rows) * c.n_kv_heads > 0x7fffffffll || !(theta > 0))
     return fail(nullptr, CB_ERR_SHAPE, "bad number of rows or theta");
   if (rows == 0) return CB_OK;
-  if (!k_out || !v_out || !pos) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  if (!k_out || !v_out || !pos || off_int32(pos) || off_int32(seq))
+    return fail(nullptr, CB_ERR_INVALID_ARG, "null or misaligned pointer");
   const int dh = cache->head_dim;
   const long long width = static_cast<long long>(c.n_kv_heads) * dh;
   if (bad_rows(k_out, ldk, width, dtype) || bad_rows(v_out, ldv, width, dtype)) return fail(nullptr, CB_ERR_SHAPE, kKvqRows);
@@ -1479,9 +1482,9 @@ cb_status cb_kvq_attention(const cb_kvq_cache* cache, const void* q, long long l
   if (dtype != CB_F32 && dtype != CB_BF16) return fail(nullptr, CB_ERR_DTYPE, "unknown dtype");
   if (n_tok < 0 || n_heads < 1 || n_heads > (1 << 16) || n_heads % c.n_kv_heads)
     return fail(nullptr, CB_ERR_SHAPE, "n_heads must be a multiple of n_kv_heads");
-  if (static_cast<long long>(c.n_seqs) * n_tok * n_heads > (1ll << 30)) return fail(nullptr, CB_ERR_SHAPE, "too many query rows");
   if (c.n_seqs == 0 || n_tok == 0) return CB_OK;
-  if (!q || !q_pos || !out) return fail(nullptr, CB_ERR_INVALID_ARG, "null pointer");
+  if (static_cast<long long>(n_tok) * n_heads > (1ll << 30) / c.n_seqs) return fail(nullptr, CB_ERR_SHAPE, "too many query rows");
+  if (!q || !q_pos || !out || off_int32(q_pos)) return fail(nullptr, CB_ERR_INVALID_ARG, "null or misaligned pointer");
   const long long width = static_cast<long long>(n_heads) * cache->head_dim;
   if (bad_rows(q, ldq, width, dtype) || bad_rows(out, ldo, width, dtype)) return fail(nullptr, CB_ERR_SHAPE, kKvqRows);
   if (!scratch || !aligned16(scratch) || scratch_bytes < cb::kvq_scratch_bytes())
@@ -1497,8 +1500,8 @@ cb_status cb_kvq_attention(const cb_kvq_cache* cache, const void* q, long long l
 // null or misaligned arrays of a value per row
 static bool bad_sampling(const cb_sampling* params, const float* uniform, const int32_t* out) {
   const cb_sampling f = params ? *params : cb_sampling{};
-  auto off = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; };
-  return !uniform || !out || off(uniform) || off(out) || off(f.temperature) || off(f.top_k) || off(f.top_p) || off(f.min_p);
+  return !uniform || !out || off_int32(uniform) || off_int32(out) || off_int32(f.temperature) || off_int32(f.top_k) ||
+         off_int32(f.top_p) || off_int32(f.min_p);
 }
 
 cb_status cb_sample(const void* logits, long long ld, cb_dtype dtype, int rows, int vocab, const cb_sampling* params,

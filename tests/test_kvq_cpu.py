@@ -109,3 +109,15 @@ def test_the_binding_refuses_before_the_library(lib):
         assert e.value.name == name
     with pytest.raises(cb.CacheBlendError):
         cb.kvq_pool(2, 24, 2, 64, device="cpu")
+
+
+def test_sizes_beyond_64_bits_and_misaligned_indices_are_refused(lib):
+    """n_seqs * n_tok * n_heads that only wraps to a small number; int32 arrays off a multiple of 4 bytes."""
+    many = cache(n_seqs=1 << 20)
+    assert lib.cb_kvq_attention(many, 256, 1 << 20, 256, 1 << 30, 1 << 14, 0.1, 1, 256, 1 << 20, 256, 1 << 30, None) == 2
+    c = cache()
+    assert lib.cb_kvq_write(c, 256, 128, 256, 128, 1, None, 258, 1, None) == 1
+    assert lib.cb_kvq_write(c, 256, 128, 256, 128, 1, 257, 256, 1, None) == 1
+    assert lib.cb_kvq_read(c, None, 258, 1, 0, 1e4, 1, 256, 128, 256, 128, None) == 1
+    assert lib.cb_kvq_read(c, 257, 256, 1, 0, 1e4, 1, 256, 128, 256, 128, None) == 1
+    assert lib.cb_kvq_attention(c, 256, 256, 258, 1, 4, 0.1, 1, 256, 256, 256, 1 << 30, None) == 1
