@@ -911,7 +911,9 @@ template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s)
   if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>), static_cast<int>(sizeof(Smem)), configured)) != cudaSuccess)
     return e;
   // CTAs of a row: as its size needs, and more while all rows' CTAs still run at once, two on an SM
-  constexpr int MAX_CHUNK = 65536;  // (sums of 15-bit parts and of near masses stay within 32 bits)
+  // sums of 15-bit parts and of near masses stay within 32 bits; 32 fp32 vectors a thread, the first off a boundary too
+  constexpr int MAX_CHUNK = 65536 - 3;
+  static_assert(MAX_CHUNK + 3 <= 32 * ST * 4 && SAMPLE_MAX_VOCAB <= 8 * MAX_CHUNK, "collect_from keeps a bit for each of a thread's vectors");
   int ranks = 1;
   auto chunk = [&](int r) { return (a.vocab + r - 1) / r; };
   while (ranks < 8 && (chunk(ranks) > MAX_CHUNK || (1ll * rows * ranks <= sms && chunk(ranks) > 4096))) ranks *= 2;

@@ -218,3 +218,18 @@ def test_decode_step_draws_from_the_logits():
     with pytest.raises(cb.CacheBlendError):
         g.eng.decode_step([b], tok, n_past=[b["n_tokens"]], sampling={"uniform": row([0.5]), "topk": None})
     g.eng.get_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [65520, 65533, 65536])
+def test_the_last_tokens_of_the_largest_rows_a_cta_takes(vocab, dtype):
+    """Rows that start off a 16-byte boundary and whose likely tokens are their last."""
+    rows, g = 200, gen(vocab)
+    wide = torch.randn(rows, vocab + 1, generator=g, device="cuda").to(dtype)
+    x = wide[:, 1:]
+    x[:, -4:] = 20.0
+    got = cb.cb_sample(x, torch.rand(rows, generator=g, device="cuda"), top_k=row([4] * rows, torch.int32))
+    assert set(got.tolist()) == set(range(vocab - 4, vocab))
+    for filters in (dict(top_k=row([4] * rows, torch.int32)), dict(top_p=row([0.9] * rows)), dict(top_k=row([1000] * rows, torch.int32))):
+        got = cb.cb_sample(x, row([0.999] * rows), **filters)
+        assert set(got.tolist()) == {vocab - 1}
