@@ -55,21 +55,56 @@ template <int DH, int STEPS> struct KvqRows {
   }
 };
 
+// A lane's eight numbers of a row as they are loaded (zeros where there is no row), and the smallest and largest of the four
+// lanes' of a group; if a number is not finite, neither is one of these, or their difference.
+struct Eight_bf16 {
+  uint4 u = {};
+  __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void floats(float* x) const { load8(reinterpret_cast<const bf16*>(&u), x); }
+  __device__ __forceinline__ void extremes(float& lo, float& hi) const {
+    // pairs throughout; at last the smallest in the lower half, the largest's negative in the upper
+    auto h = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    auto bits = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+    const uint32_t l = bits(__hmin2_nan(__hmin2_nan(h(u.x), h(u.y)), __hmin2_nan(h(u.z), h(u.w))));
+    const uint32_t m = bits(__hmax2_nan(__hmax2_nan(h(u.x), h(u.y)), __hmax2_nan(h(u.z), h(u.w)))) ^ 0x80008000u;
+    uint32_t both = bits(__hmin2_nan(h(__byte_perm(l, m, 0x5410)), h(__byte_perm(l, m, 0x7632))));
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) both = bits(__hmin2_nan(h(both), h(__shfl_xor_sync(0xffffffffu, both, o))));
+    lo = __uint_as_float(both << 16);
+    hi = -__uint_as_float(both & 0xffff0000u);
+  }
+};
+struct Eight_f32 {
+  float x[8] = {};
+  __device__ __forceinline__ void load(const float* p) { load8(p, x); }
+  __device__ __forceinline__ void floats(float* y) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+  }
+  __device__ __forceinline__ void extremes(float& lo, float& hi) const {
+    lo = hi = x[0];
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      odd = fmaf(x[i], 0.f, odd);  // NaN once a number is not finite
+    }
+    hi = odd == 0.f ? hi : INFINITY;
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+  }
+};
+template <typename T> using Eight = std::conditional_t<std::is_same<T, bf16>::value, Eight_bf16, Eight_f32>;
+
 // Codes of a lane's eight channels, and its group's scale and zero.
-__device__ __forceinline__ uint32_t encode8(const float* x, float3& p) {
-  float lo = x[0], hi = x[0], odd = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    odd = fmaf(x[i], 0.f, odd);  // NaN once a number is not finite
-  }
-  hi = odd == 0.f ? hi : INFINITY;
-#pragma unroll
-  for (int o = 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
+template <typename E> __device__ __forceinline__ uint32_t encode8(const E& e, float3& p) {
+  float x[8], lo, hi;
+  e.extremes(lo, hi);
+  e.floats(x);
   p = kvq_params(lo, hi);
   return p.x < INFINITY ? kvq_codes(x, p.x, p.y, p.z) : 0;
 }
@@ -93,10 +128,10 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32) kvq_write_kernel(KvqView c, co
     uint32_t half[STEPS];  // value bytes of channels n (low nibbles) and n + 8 (high): n = 0..3 by even lanes, 4..7 by odd ones
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      float kx[8] = {}, vx[8] = {};
+      Eight<T> kx, vx;
       if (at.blk[s]) {
-        load8(k + at.row[s] * ldk + head * DH + 8 * L, kx);
-        load8(v + at.row[s] * ldv + head * DH + 8 * L, vx);
+        kx.load(k + at.row[s] * ldk + head * DH + 8 * L);
+        vx.load(v + at.row[s] * ldv + head * DH + 8 * L);
       }
       float3 kp, vp;
       const uint32_t kc = encode8(kx, kp), vc = encode8(vx, vp);
@@ -141,6 +176,17 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32) kvq_write_kernel(KvqView c, co
   }
 }
 
+// `wide`: rows start at multiples of 32 bytes, and eight fp32 numbers are one store
+__device__ __forceinline__ void store_row(bf16* p, const float* x, bool) { store8(p, x); }
+__device__ __forceinline__ void store_row(float* p, const float* x, bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  else
+    store8(p, x);
+}
+
 struct KvqTurn {
   float2 cs[64];  // (cos, sin) of channel pairs i, i + head_dim / 2
 };
@@ -149,7 +195,7 @@ template <typename T, int DH, int STEPS>
 __global__ void __launch_bounds__(KVQ_WARPS * 32, 4) kvq_read_kernel(KvqView c, const int32_t* __restrict__ seqs,
                                                                   const int32_t* __restrict__ poss, int rows, int units,
                                                                   int heads_each, const __grid_constant__ KvqTurn turn,
-                                                                  bool turned, T* __restrict__ k, long long ldk,
+                                                                  bool turned, bool wide, T* __restrict__ k, long long ldk,
                                                                   T* __restrict__ v, long long ldv, int32_t* status) {
   __shared__ float2 cs[64];
   // (read one by one: an indexed kernel argument is fetched lane after lane)
@@ -213,8 +259,8 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 4) kvq_read_kernel(KvqView c, 
           }
         }
         if (at.row[s] < rows && lane % 16 < LANES) {
-          store8(k + at.row[s] * ldk + head * DH + 8 * L, kx);
-          store8(v + at.row[s] * ldv + head * DH + 8 * L, vx);
+          store_row(k + at.row[s] * ldk + head * DH + 8 * L, kx, wide);
+          store_row(v + at.row[s] * ldv + head * DH + 8 * L, vx, wide);
         }
       }
     }
@@ -273,10 +319,11 @@ cudaError_t launch_kvq_read(const KvqView& c, int head_dim, const int32_t* seq, 
   KvqTurn turn = {};
   if (cs_host)
     for (int i = 0; i < head_dim / 2; ++i) turn.cs[i] = make_float2(cs_host[2 * i], cs_host[2 * i + 1]);
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0 && ldk % 8 == 0 && ldv % 8 == 0;
   auto go = [&](auto* kernel, auto* p) {
     using T = std::remove_pointer_t<decltype(p)>;
-    return launch_chain(kernel, plan.grid, block, 0, s, c, seq, pos, rows, plan.units, plan.heads_each, turn, cs_host != nullptr, static_cast<T*>(k), ldk,
-                        static_cast<T*>(v), ldv, status);
+    return launch_chain(kernel, plan.grid, block, 0, s, c, seq, pos, rows, plan.units, plan.heads_each, turn,
+                        cs_host != nullptr, wide, static_cast<T*>(k), ldk, static_cast<T*>(v), ldv, status);
   };
   const bool one = plan.steps == 1;
   bf16* b = nullptr;

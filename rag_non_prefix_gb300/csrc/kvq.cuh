@@ -78,22 +78,30 @@ __device__ __forceinline__ float3 kvq_params(float lo, float hi) {
 
 // Codes of eight numbers of a group, one a nibble: the nearest to x / scale - zero, ties to even, exactly.  The
 // estimate by the reciprocal is off by less than 2^-15 of a step (|x / scale| <= 80, a few roundings), so what lies
-// farther from a tie is right; near a tie n +- 1/2 the sign of x - (n +- 1/2 + zero) scale, one fused operation with
-// an exact factor, which keeps a sign, decides.
+// farther from a tie is right; near a tie n +- 1/2 (hardly ever: one look for all eight) the sign of x - (n +- 1/2 + zero) scale,
+// one fused operation with an exact factor, which keeps a sign, decides.
 __device__ __forceinline__ uint32_t kvq_codes(const float* x, float scale, float zero, float inv) {
   const float mul = inv * (1.f / 15.f), add = zero * (-1.f / 15.f);
   uint32_t c = 0;
+  float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float y = __saturatef(fmaf(x[i], mul, add));  // code / 15 in 0..1
     const float r = fmaf(y, 15.f, 12582912.f);            // (its last bits are the nearest whole number)
-    const float n = r - 12582912.f, f = fmaf(y, 15.f, -n);
-    uint32_t code = __float_as_uint(r) - 0x4b400000u;
-    if (fabsf(f) > 0.4999f) {
-      const float side = copysignf(1.f, f), e = side * __fmaf_rn(-(n + 0.5f * side + zero), scale, x[i]);
-      if (e > 0.f || (e == 0.f && (code & 1))) code += f > 0.f ? 1 : -1;
+    far = fmaxf(far, fabsf(fmaf(y, 15.f, 12582912.f - r)));
+    c += __float_as_uint(r) << (4 * i);
+  }
+  c -= 0x4b400000u * 0x11111111u;
+  if (far > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __saturatef(fmaf(x[i], mul, add));
+      const float n = fmaf(y, 15.f, 12582912.f) - 12582912.f, f = fmaf(y, 15.f, -n);
+      if (fabsf(f) > 0.4999f) {
+        const float side = copysignf(1.f, f), e = side * __fmaf_rn(-(n + 0.5f * side + zero), scale, x[i]);
+        if (e > 0.f || (e == 0.f && (c >> (4 * i) & 1))) c += (f > 0.f ? 1u : 0xffffffffu) << (4 * i);
+      }
     }
-    c += code << (4 * i);
   }
   return c;
 }

@@ -498,3 +498,24 @@ def test_a_sequence_of_almost_2_31_keys(dtype):
         # 2^-24 of the sum (2^-14.3), and scores and exponentials are good to 2^-16
         assert torch.all((row - want).abs() <= 2.0 ** -13 + abs(want) * torch.finfo(dtype).eps / 2)
     cb.cb_gemm_get_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [9, 3000])
+def test_reads_into_strided_outputs(dtype, n):
+    """Outputs at every 16-byte offset and pitch; what lies between their rows stays."""
+    hkv, dh, vec = 3, 64, 16 // dtype.itemsize
+    pool, table, _ = filled(50, [n], 64, hkv, dh)
+    at = (ints(range(n)), ints([0] * n))
+    want = cb.cb_kvq_read(pool, table, *at, dtype=dtype)
+    for start, pad in ((0, vec), (vec, 0), (vec, 3 * vec), (2 * vec, 2 * vec)):
+        bufs = [torch.full((n * (hkv * dh + pad) + 4 * vec,), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+        outs = [b[start:start + n * (hkv * dh + pad)].view(n, -1)[:, :hkv * dh].view(n, hkv, dh) for b in bufs]
+        cb.cb_kvq_read(pool, table, *at, k_out=outs[0], v_out=outs[1])
+        for b, o, w in zip(bufs, outs, want):
+            assert torch.equal(o, w)
+            o.fill_(7.0)
+            assert torch.all(b == 7.0)
+    mixed = torch.empty(n * hkv * dh + vec, dtype=dtype, device="cuda")[vec:].view(n, hkv, dh)
+    got = cb.cb_kvq_read(pool, table, *at, k_out=mixed, dtype=dtype)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
