@@ -1,6 +1,11 @@
 // A KV cache in 4 bits (layout and arithmetic: kvq.cuh): rows quantised as they are written, and read back
 // with their keys turned to new positions.
 //
+// Bounds: 5.25 bytes a number of either tensor at most (fp32 and 5 bits), and for the form some 35 instructions a number written
+// and 13 read.  Prompts are bound by these instructions and the latency of the loads that 32 warps an SM cover (8320 rows of 8 heads
+// of 128 written from bf16 and read back to fp32: 36.7 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to
+// bf16: 24.7 us, 3.6 TB/s); decoded tokens by one warp's chain (16 rows of 8 heads written and read back: 4.6 us, two launches).
+//
 // Both kernels give eight channels to a lane: a row of one head is 16 lanes (128 channels) or 8, a group of 32
 // channels four of them (its extremes two shuffles), and the row's key codes are one word a lane.  A word of value codes
 // belongs to four tokens (2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of a block), so a warp takes those four rows of
@@ -16,7 +21,7 @@ namespace cb {
 
 namespace {
 
-constexpr int KVQ_WARPS = 8;
+constexpr int KVQ_WARPS = 2;  // of a CTA (8: decoded tokens written and read back 5.0 us instead of 4.6, the other sizes alike)
 
 __device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
@@ -110,7 +115,7 @@ template <typename E> __device__ __forceinline__ uint32_t encode8(const E& e, fl
 }
 
 template <typename T, int DH, int STEPS>
-__global__ void __launch_bounds__(KVQ_WARPS * 32) kvq_write_kernel(KvqView c, const T* __restrict__ k, long long ldk,
+__global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_write_kernel(KvqView c, const T* __restrict__ k, long long ldk,
                                                                    const T* __restrict__ v, long long ldv,
                                                                    const int32_t* __restrict__ seqs,
                                                                    const int32_t* __restrict__ poss, int rows, int units,
@@ -126,15 +131,18 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32) kvq_write_kernel(KvqView c, co
   const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, c.n_kv_heads);
   for (int head = h0; head < h1; ++head) {
     uint32_t half[STEPS];  // value bytes of channels n (low nibbles) and n + 8 (high): n = 0..3 by even lanes, 4..7 by odd ones
+    Eight<T> kx[STEPS], vx[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      Eight<T> kx, vx;
       if (at.blk[s]) {
-        kx.load(k + at.row[s] * ldk + head * DH + 8 * L);
-        vx.load(v + at.row[s] * ldv + head * DH + 8 * L);
+        kx[s].load(k + at.row[s] * ldk + head * DH + 8 * L);
+        vx[s].load(v + at.row[s] * ldv + head * DH + 8 * L);
       }
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
       float3 kp, vp;
-      const uint32_t kc = encode8(kx, kp), vc = encode8(vx, vp);
+      const uint32_t kc = encode8(kx[s], kp), vc = encode8(vx[s], vp);
       const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 1);
       const uint32_t lo = L & 1 ? other >> 16 : vc, hi = L & 1 ? vc >> 16 : other;
       // nibbles 0 to 3 of both, interleaved to bytes
@@ -192,14 +200,15 @@ struct KvqTurn {
 };
 
 template <typename T, int DH, int STEPS>
-__global__ void __launch_bounds__(KVQ_WARPS * 32, 4) kvq_read_kernel(KvqView c, const int32_t* __restrict__ seqs,
+__global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_read_kernel(KvqView c, const int32_t* __restrict__ seqs,
                                                                   const int32_t* __restrict__ poss, int rows, int units,
                                                                   int heads_each, const __grid_constant__ KvqTurn turn,
                                                                   bool turned, bool wide, T* __restrict__ k, long long ldk,
                                                                   T* __restrict__ v, long long ldv, int32_t* status) {
   __shared__ float2 cs[64];
   // (read one by one: an indexed kernel argument is fetched lane after lane)
-  if (turned && threadIdx.x < DH / 2) cs[threadIdx.x] = turn.cs[threadIdx.x];
+  if (turned)
+    for (int i = threadIdx.x; i < DH / 2; i += KVQ_WARPS * 32) cs[i] = turn.cs[i];
   pdl_trigger();
   pdl_wait();
   __syncthreads();
@@ -272,8 +281,9 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 4) kvq_read_kernel(KvqView c, 
 }
 
 // Units of rows, and the heads that a warp takes one after the other: a head each while there are few, more where
-// that would only look up the rows again: once there are more than `want` warps (measured, 8320 rows of 8 heads written: 44.8 us with
-// the reading back at 4096, 43.8 at 8192, 45.5 at 16384; 4096 rows of 32 heads read: 27.7 us at 3000, 24.8 at 4096, 26.4 at 8192).
+// that would only look up the rows again: once there are more than `want` warps (measured, 8320 rows of 8 heads written and read
+// back: 36.6 us where both have 4096, 36.7 at 8192 and 4096, 38.9 at 16384; 4096 rows of 32 heads read: 27.3 us at 3000, 24.7 at
+// 4096, 25.7 at 8192).  One step up to 8192 rows and heads: there a warp's chain of loads and stores is the time.
 struct KvqPlan {
   int steps, units, heads_each;
   dim3 grid;
