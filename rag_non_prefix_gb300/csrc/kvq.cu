@@ -1,10 +1,10 @@
 // A KV cache in 4 bits (layout and arithmetic: kvq.cuh): rows quantised as they are written, and read back
 // with their keys turned to new positions.
 //
-// Bounds: 5.25 bytes a number of either tensor at most (fp32 and 5 bits), and for the form some 35 instructions a number written
-// and 13 read.  Prompts are bound by these instructions and the latency of the loads that 32 warps an SM cover (8320 rows of 8 heads
-// of 128 written from bf16 and read back to fp32: 36.7 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to
-// bf16: 24.7 us, 3.6 TB/s); decoded tokens by one warp's chain (16 rows of 8 heads written and read back: 4.6 us, two launches).
+// Bounds: a number is 2 or 4 bytes and 5 bits, and takes some 28 instructions to write and 12 to read.  Prompts are bound by these
+// and by the latency of the loads that 32 warps an SM cover (8320 rows of 8 heads of 128 written from bf16 and read back to
+// fp32: 36.2 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to bf16: 24.7 us, 3.6 TB/s; with the registers of
+// 24 warps an SM 28.4); decoded tokens by one warp's chain (16 rows of 8 heads written and read back: 4.6 us, two launches).
 //
 // Both kernels give eight channels to a lane: a row of one head is 16 lanes (128 channels) or 8, a group of 32
 // channels four of them (its extremes two shuffles), and the row's key codes are one word a lane.  A word of value codes
@@ -105,13 +105,13 @@ struct Eight_f32 {
 };
 template <typename T> using Eight = std::conditional_t<std::is_same<T, bf16>::value, Eight_bf16, Eight_f32>;
 
-// Codes of a lane's eight channels, and its group's scale and zero.
-template <typename E> __device__ __forceinline__ uint32_t encode8(const E& e, float3& p) {
-  float x[8], lo, hi;
-  e.extremes(lo, hi);
+// Codes of a lane's eight channels under their group's scale and zero (kvq_params).
+template <typename E> __device__ __forceinline__ uint32_t encode8(const E& e, uint32_t params) {
+  float x[8];
   e.floats(x);
-  p = kvq_params(lo, hi);
-  return p.x < INFINITY ? kvq_codes(x, p.x, p.y, p.z) : 0;
+  const float scale = __uint_as_float(params << 16), zero = __uint_as_float(params & 0xffff0000u);
+  const uint32_t c = kvq_codes(x, scale, zero, kvq_reciprocal(scale));
+  return scale < INFINITY ? c : 0;
 }
 
 template <typename T, int DH, int STEPS>
@@ -129,6 +129,10 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_write_kern
   const int L = at.L;
   const size_t head_bytes = static_cast<size_t>(c.page_tokens / KVQ_BLOCK) * kvq_block_bytes(DH);
   const int h0 = blockIdx.y * heads_each, h1 = min(h0 + heads_each, c.n_kv_heads);
+  const int mine = at.tq % (2 * STEPS);  // this lane's scale and zero: of step mine / 2, keys or values
+  uint8_t* own_blk = at.tq < 2 * STEPS ? at.blk[mine / 2 && STEPS == 2 ? STEPS - 1 : 0] : nullptr;
+  uint16_t* own_params = own_blk ? reinterpret_cast<uint16_t*>(own_blk + 16 * DH + 4 * NG * at.r[mine / 2 && STEPS == 2 ? STEPS - 1 : 0]) +
+                                       at.g + (mine & 1) * 32 * NG : nullptr;
   for (int head = h0; head < h1; ++head) {
     uint32_t half[STEPS];  // value bytes of channels n (low nibbles) and n + 8 (high): n = 0..3 by even lanes, 4..7 by odd ones
     Eight<T> kx[STEPS], vx[STEPS];
@@ -139,10 +143,26 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_write_kern
         vx[s].load(v + at.row[s] * ldv + head * DH + 8 * L);
       }
     }
+    // the group's scales and zeros, of keys and values of each step, one by each of its four lanes
+    float lo = 0.f, hi = 0.f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      float3 kp, vp;
-      const uint32_t kc = encode8(kx[s], kp), vc = encode8(vx[s], vp);
+      float l, h;
+      kx[s].extremes(l, h);
+      if (mine == 2 * s) lo = l, hi = h;
+      vx[s].extremes(l, h);
+      if (mine == 2 * s + 1) lo = l, hi = h;
+    }
+    const uint32_t params = kvq_params(lo, hi);
+    if (own_params) {
+      uint16_t* p = own_params + head * (head_bytes / 2);
+      p[0] = static_cast<uint16_t>(params);
+      p[NG] = static_cast<uint16_t>(params >> 16);
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const uint32_t kc = encode8(kx[s], __shfl_sync(0xffffffffu, params, (lane & ~3) + 2 * s));
+      const uint32_t vc = encode8(vx[s], __shfl_sync(0xffffffffu, params, (lane & ~3) + 2 * s + 1));
       const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 1);
       const uint32_t lo = L & 1 ? other >> 16 : vc, hi = L & 1 ? vc >> 16 : other;
       // nibbles 0 to 3 of both, interleaved to bytes
@@ -153,13 +173,6 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_write_kern
       uint8_t* blk = at.blk[s] + head * head_bytes;
       const int r = at.r[s];
       *reinterpret_cast<uint32_t*>(blk + r * (DH / 2) + (at.tq * NG + at.g) * 4) = kc;
-      if (at.tq == 0) {
-        uint16_t* p = reinterpret_cast<uint16_t*>(blk + 16 * DH + 4 * NG * r) + at.g;
-        p[0] = static_cast<uint16_t>(__float_as_uint(kp.x) >> 16);
-        p[NG] = static_cast<uint16_t>(__float_as_uint(kp.y) >> 16);
-        p[32 * NG] = static_cast<uint16_t>(__float_as_uint(vp.x) >> 16);
-        p[33 * NG] = static_cast<uint16_t>(__float_as_uint(vp.y) >> 16);
-      }
       if (!at.whole) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -282,7 +295,7 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_read_kerne
 
 // Units of rows, and the heads that a warp takes one after the other: a head each while there are few, more where
 // that would only look up the rows again: once there are more than `want` warps (measured, 8320 rows of 8 heads written and read
-// back: 36.6 us where both have 4096, 36.7 at 8192 and 4096, 38.9 at 16384; 4096 rows of 32 heads read: 27.3 us at 3000, 24.7 at
+// back: 36.6 us where written at 4096, 36.7 at 8192, 38.9 at 16384; 4096 rows of 32 heads read: 27.3 us at 3000, 24.7 at
 // 4096, 25.7 at 8192).  One step up to 8192 rows and heads: there a warp's chain of loads and stores is the time.
 struct KvqPlan {
   int steps, units, heads_each;

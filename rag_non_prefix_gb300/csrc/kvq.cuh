@@ -54,11 +54,16 @@ __device__ __forceinline__ float bf16_up(float x) {  // the smallest bf16 number
   return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
 }
 
-// Scale, zero and 1 / scale (approximately) of a group whose smallest and largest numbers are lo and hi (hi infinite if
-// a number is not finite).  Quotients are estimated and put right by exact products (bf16 times 14.75: 14 bits).
-__device__ __forceinline__ float3 kvq_params(float lo, float hi) {
+__device__ __forceinline__ float kvq_reciprocal(float scale) {  // approximately
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  return inv;
+}
+
+// Scale (lower half) and zero (upper) of a group whose smallest and largest numbers are lo and hi, as bf16 (hi - lo not finite: NaN).
+// Quotients are estimated and put right by exact products (bf16 times 14.75: 14 bits).
+__device__ __forceinline__ uint32_t kvq_params(float lo, float hi) {
   const float d = __fsub_rn(hi, lo), a = fmaxf(-lo, hi);
-  if (!(d < INFINITY)) return make_float3(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u), 0.f);
   float s = bf16_up(fmaxf(__fmul_rn(d, 1.f / 14.75f), 7.52316385e-37f));  // (2^-120)
   const float next = __uint_as_float(__float_as_uint(s) + 0x10000u), prev = __uint_as_float(__float_as_uint(s) - 0x10000u);
   if (__fmul_rn(s, 14.75f) < d)
@@ -66,14 +71,29 @@ __device__ __forceinline__ float3 kvq_params(float lo, float hi) {
   else if (__fmul_rn(prev, 14.75f) >= d)
     s = prev;
   const float scale = fmaxf(fmaxf(s, bf16_up(a * 0.015625f)), 7.52316385e-37f);
-  float inv;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
-  float zero = 0.25f * floorf(4.f * __fmul_rn(lo, inv));
+  float zero = 0.25f * floorf(4.f * __fmul_rn(lo, kvq_reciprocal(scale)));
   if (__fmul_rn(zero, scale) > lo)
     zero -= 0.25f;
   else if (__fmul_rn(zero + 0.25f, scale) <= lo)
     zero += 0.25f;
-  return make_float3(scale, zero, inv);
+  return d < INFINITY ? __float_as_uint(scale) >> 16 | __float_as_uint(zero) : 0x7fc07fc0u;
+}
+
+// The codes c of eight numbers, those near a tie put right (a function of its own, so that the usual way is short).
+inline __device__ __noinline__ uint32_t kvq_ties(uint32_t c, float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
+                                          float scale, float zero, float inv) {
+  const float mul = inv * (1.f / 15.f), add = zero * (-1.f / 15.f);
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = __saturatef(fmaf(x[i], mul, add));
+    const float n = fmaf(y, 15.f, 12582912.f) - 12582912.f, f = fmaf(y, 15.f, -n);
+    if (fabsf(f) > 0.4999f) {
+      const float side = copysignf(1.f, f), e = side * __fmaf_rn(-(n + 0.5f * side + zero), scale, x[i]);
+      if (e > 0.f || (e == 0.f && (c >> (4 * i) & 1))) c += (f > 0.f ? 1u : 0xffffffffu) << (4 * i);
+    }
+  }
+  return c;
 }
 
 // Codes of eight numbers of a group, one a nibble: the nearest to x / scale - zero, ties to even, exactly.  The
@@ -92,18 +112,7 @@ __device__ __forceinline__ uint32_t kvq_codes(const float* x, float scale, float
     c += __float_as_uint(r) << (4 * i);
   }
   c -= 0x4b400000u * 0x11111111u;
-  if (far > 0.4999f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = __saturatef(fmaf(x[i], mul, add));
-      const float n = fmaf(y, 15.f, 12582912.f) - 12582912.f, f = fmaf(y, 15.f, -n);
-      if (fabsf(f) > 0.4999f) {
-        const float side = copysignf(1.f, f), e = side * __fmaf_rn(-(n + 0.5f * side + zero), scale, x[i]);
-        if (e > 0.f || (e == 0.f && (c >> (4 * i) & 1))) c += (f > 0.f ? 1u : 0xffffffffu) << (4 * i);
-      }
-    }
-  }
-  return c;
+  return far > 0.4999f ? kvq_ties(c, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale, zero, inv) : c;
 }
 
 }  // namespace cb

@@ -23,6 +23,13 @@
 // writes its part (sums, maximum) to scratch, and whichever CTA of that unit is the last to finish
 // merges the parts in the order of the keys, so results repeat exactly.  In a CTA each of 4 warps takes a block of 16
 // keys of a quantum, through a ring of its own in shared memory; no warp waits for another before the end.
+//
+// Bounds (8 KV heads of 128, groups of 4): long caches by the instructions, some 1000 a pair of blocks for 5 KB, at 0.83 an issue slot, and
+// by 7 to 10 us of units' beginnings, ends and merges: 32 ragged sequences of up to 8320 keys 65 us, 2.7 TB/s of cache.  4 tokens
+// of 16 sequences (16 rows a KV head: two column tiles share the operands, one step's) 109 us; fp32 outputs 46 us for 4 x
+// 4128 keys of 32 KV heads, three products for each of the others; one sequence of 3200 keys 15 us, a chain of latencies (share 1.7, first
+// loads 1.9, keys 2.6, part to memory 1.9, merge 3.3 us).  Four warps a CTA and four CTAs an SM: 128 registers a thread hold the
+// loop; with five CTAs (96 registers) it spills, eight warps a CTA wait for each other longer, two merge more parts, all slower.
 #include <algorithm>
 #include <atomic>
 
@@ -36,8 +43,12 @@ namespace {
 typedef unsigned long long u64;
 constexpr int AW = 4;                    // warps per CTA
 constexpr int QUANTUM = AW * KVQ_BLOCK;  // keys
-constexpr int MIN_SHARE = 4;             // quanta of a CTA, at least, where there are few
-constexpr int UNIT_COST = 6;             // what a unit costs beside its quanta (queries, first loads, merging): in quanta, measured
+// quanta of a CTA, at least, where there are few: fewer make more parts to merge (one sequence of 3200 keys: 17.0 us with 2, 15.0 with 4,
+// 16.1 with 8, 21.7 with 16)
+constexpr int MIN_SHARE = 4;
+// what a unit costs beside its quanta (queries, first loads, merging), in quanta (32 ragged sequences and one: 83.5 and 17.7 us with 0,
+// 64.9 and 17.0 with 3, 64.7 and 15.0 with 6, 65.1 and 18.1 with 9)
+constexpr int UNIT_COST = 6;
 constexpr int MAX_ROWS = 16;             // query rows per tile at most
 constexpr float LAZY = 6.f;              // the running maximum moves once a score passes it by 2^6
 

@@ -17,6 +17,11 @@
 //      ranges and collects their tokens, which are sorted; the exact sums show whether the ranges were the right ones.
 //   3. an exact histogram of counts or masses, whose range that holds the target is cut further by the bits of x and of the
 //      index until at most LIST tokens are left (flat rows, crowds of equal logits, top-k beyond 1.'s).
+//
+// Bounds: a few rows by the chain of their passes and cluster barriers (one row of 32000 with top-k: 10.3 us; 64 rows of 64000 fp32 with
+// top-p: 36.6 us, of these the exact pass 6.4, the merge of the near masses 5.9, their own pass 3.3), many by the passes' instructions:
+// 512 rows of 64000 bf16 with top-k and top-p 39.4 us, 1.7 TB/s (a row 12 us on half an SM: its loads and maxima 3.9, the bound 1.5,
+// collecting 3.5, sorting and sums 3.0; 1.7 rounds of rows).  512 threads, two CTAs an SM: 1024 threads and one were slower.
 #include <cooperative_groups.h>
 
 #include <algorithm>
