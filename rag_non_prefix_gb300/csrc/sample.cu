@@ -768,39 +768,51 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       const float last_p = -logf(fminf(min_p, 1.f)) / STEP;  // min_p's own place
       const int at_m = z.floor_w > 0 ? static_cast<int>(fminf(last_p, NEAR - 1.f)) : NEAR - 1;
       if (tid == 0) {
-        s.ctl[z.phase].count = s.ctl[z.phase].bucket = 0;
+        s.ctl[z.phase] = {0, 0, NEAR - 1, 0, NEAR - 1};  // first and last range of the draw (bucket, excl), of top_p (count, incl)
         s.near[1] = INFINITY;
       }
       if (tid == ST - 1) s.near[0] = before + sum;
       __syncthreads();
-      // top_p's range, and the mass up to and with its last token: as if the range's tokens all weighed the same
-      const float near_p = top_p * s.near[0];
+      // top_p's range, and the mass up to and with its last token: as if the range's tokens all weighed the same.  Near masses
+      // are off by some 2^-16: where a target lies that near to a border, two ranges stand for one (else about one row
+      // in 4000 went the third way, 20 us more).
+      const float near_p = top_p * s.near[0], room = s.near[0] * (1.f / 32768.f);
+      const float above_p = fminf(near_p + room, 0.5f * (near_p + s.near[0]));  // (targets below the end stay below it)
       float excl = before;
 #pragma unroll
       for (int i = 0; i < EACH; ++i) {
         const float incl = before + m[i];
         if (top_p < 1.f && excl < near_p && near_p <= incl) {
           const float w = middle(i);
-          s.ctl[z.phase].count = EACH * tid + i;
           s.near[1] = excl + ceilf((near_p - excl) / w) * w;
         }
+        if (excl < near_p - room && near_p - room <= incl) s.ctl[z.phase].count = EACH * tid + i;
+        if (excl < above_p && above_p <= incl) s.ctl[z.phase].incl = EACH * tid + i;
         if (EACH * tid + i == at_m) s.near[2] = incl;
         excl = incl;
       }
       __syncthreads();
-      const float near_u = u * fminf(s.near[1], s.near[2]);
+      const float kept = fminf(s.near[1], s.near[2]), near_u = u * kept, above_u = fminf(near_u + room, 0.5f * (near_u + kept));
       excl = before;
 #pragma unroll
       for (int i = 0; i < EACH; ++i) {
         const float incl = before + m[i];
-        if (excl <= near_u && near_u < incl) s.ctl[z.phase].bucket = EACH * tid + i;
+        if (excl <= near_u - room && near_u - room < incl) s.ctl[z.phase].bucket = EACH * tid + i;
+        if (excl <= above_u && above_u < incl) s.ctl[z.phase].excl = EACH * tid + i;
         excl = incl;
       }
       __syncthreads();
     }
     const Ctl guess = z.decide();
     const bool with_p = top_p < 1.f;
-    const int bp = guess.count, bu = guess.bucket;
+    int bp = guess.count, bu = guess.bucket;
+    unsigned more_p = static_cast<unsigned>(guess.incl) - bp, more_u = static_cast<unsigned>(guess.excl) - bu;  // ranges after the first
+    const bool one = bp <= bu + static_cast<int>(more_u);  // both are in the same ranges
+    if (with_p && one) {
+      more_u = max(bp + more_p, bu + more_u) - min(bp, bu);
+      bp = bu = min(bp, bu);
+      more_p = more_u;
+    }
     // exact sums: all, before bp, before bu, over min_p; and the tokens of the two ranges
     u64 sum[4] = {};
     uint32_t hits[2] = {};
@@ -814,8 +826,8 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         if (b < bu) sum[2] += w;
         if (m_on && w >= z.floor_w) sum[3] += w;
         const uint32_t bit = 1u << (idx - z.first) % VEC;  // (a vector's elements come one after the other)
-        if (b == bu && w > 0) hits[0] |= bit;
-        if (p_on && b == bp && bp != bu && w > 0) hits[1] |= bit;
+        if (static_cast<unsigned>(b - bu) <= more_u && w > 0) hits[0] |= bit;
+        if (p_on && static_cast<unsigned>(b - bp) <= more_p && !one && w > 0) hits[1] |= bit;
       }, [&](int idx) {
         if (hits[0] | hits[1]) {
           z.collect_hits(0, hits[0], idx);
@@ -843,7 +855,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       if (lane == 0) s.part[1 + warp] = v;
     }
     z.meet();
-    const int n_u = z.collected(0), n_p = bp == bu ? n_u : z.collected(1);
+    const int n_u = z.collected(0), n_p = one ? n_u : z.collected(1);
     // (every CTA comes to the same result, the first one's below)
     if (z.rank == 0) {
       if (tid == 0) s.ctl[z.phase].count = 0;  // settled
@@ -855,7 +867,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       for (int i = 0; i < 4; ++i) total[i] = __shfl_sync(0xffffffffu, v, 8 * i);
       u64 mass = total[3];  // what min_p keeps
       const u64 pm = reach_p(total[0]);
-      const bool need_p = with_p && pm <= mass, two = need_p && bp != bu;
+      const bool need_p = with_p && pm <= mass, two = need_p && !one;
       const int n = n_u + (two ? n_p : 0);
       if (n <= LIST) {
         // the draw's range comes first in the order
