@@ -24,12 +24,13 @@
 // merges the parts in the order of the keys, so results repeat exactly.  In a CTA each of 4 warps takes a block of 16
 // keys of a quantum, through a ring of its own in shared memory; no warp waits for another before the end.
 //
-// Bounds (8 KV heads of 128, groups of 4): long caches by the instructions, some 1000 a pair of blocks for 5 KB, at 0.83 an issue slot, and
-// by 7 to 10 us of units' beginnings, ends and merges: 32 ragged sequences of up to 8320 keys 65 us, 2.7 TB/s of cache.  4 tokens
-// of 16 sequences (16 rows a KV head: two column tiles share the operands, one step's) 109 us; fp32 outputs 46 us for 4 x
-// 4128 keys of 32 KV heads, three products for each of the others; one sequence of 3200 keys 15 us, a chain of latencies (share 1.7, first
-// loads 1.9, keys 2.6, part to memory 1.9, merge 3.3 us).  Four warps a CTA and four CTAs an SM: 128 registers a thread hold the
-// loop; with five CTAs (96 registers) it spills, eight warps a CTA wait for each other longer, two merge more parts, all slower.
+// Bounds (8 KV heads of 128): long caches by the instructions, some 1000 a pair of blocks for 5 KB, and by 7 to 10 us of units'
+// beginnings, ends and merges: 32 ragged sequences of up to 8320 keys, groups of 7, 63 us, 2.7 TB/s of cache.  4 tokens of 16
+// sequences, groups of 8 (two units of 16 rows a KV head, each of which reads the cache) 109 us; fp32 outputs 46 us for 4 x 4128
+// keys of 32 KV heads, three products for each of the others; one sequence of 3200 keys 15 us, a chain of latencies (share 1.7,
+// first loads 1.9, keys 2.6, part to memory 1.9, merge 3.3 us).  Four warps a CTA, four CTAs an SM: 128 registers a thread hold the
+// loop (32 sequences: with five CTAs spills, with eight warps a CTA, which wait for each other, 69 us, with two, whose parts are
+// many, 105).
 #include <algorithm>
 #include <atomic>
 
