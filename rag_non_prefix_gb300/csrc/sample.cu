@@ -693,7 +693,8 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       if (tid == 0) s.part[1] = bound;
       z.meet();
       bound = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(z.of_each(&s.part[1], 0xffffffffull)));
-      const float least = logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32);
+      // (at least: a number, and of a weight, exp(-33) being none; a row masked by its type's lowest value has its few tokens)
+      const float least = fmaxf(logit_of(static_cast<u64>(max(bound, 0x00800000u)) << 32), z.top - 33.f * t);
       if (tid == 0) s.n_list[0] = 0;
       __syncthreads();
       z.collect_from(least, own);

@@ -233,3 +233,20 @@ def test_the_last_tokens_of_the_largest_rows_a_cta_takes(vocab, dtype):
     for filters in (dict(top_k=row([4] * rows, torch.int32)), dict(top_p=row([0.9] * rows)), dict(top_k=row([1000] * rows, torch.int32))):
         got = cb.cb_sample(x, row([0.999] * rows), **filters)
         assert set(got.tolist()) == {vocab - 1}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [300, 32000, 128256])
+def test_rows_masked_by_the_lowest_value(vocab, dtype):
+    """Fewer tokens than top-k keeps, the others at the type's lowest value, at -infinity, or far below."""
+    g, rng = gen(vocab), np.random.default_rng(vocab)
+    x = likely(g, 8, vocab, dtype)
+    some = torch.rand(8, vocab, generator=g, device="cuda") < 20 / vocab
+    some[:, vocab - 1] = True
+    low = [torch.finfo(dtype).min, -float("inf"), -1e4, -60.0] * 2
+    x = torch.where(some, x, torch.tensor(low, dtype=dtype, device="cuda")[:, None])
+    u, t = list(rng.random(8)), [0.7, 1.0, 2.0, 1.5, 1e-3, 1e3, 20.0, 0.1]
+    check(x, u, t, [50] * 8)
+    check(x, u, t, [200] * 8, [0.9, 0.5, 0.99, 1.0] * 2, [0.0, 0.1, 0.0, 0.01] * 2)
+    check(x, u, t, p=[0.9, 0.5, 0.99, 1.0] * 2)
+    check(torch.full_like(x, torch.finfo(dtype).min), u, t, [50] * 8)
