@@ -231,9 +231,9 @@ template <typename T> struct Sampler {
   // f(logit, index) for all of this CTA's tokens (and some places of -infinity), whole warps together: f may use
   // warp-wide operations.
   template <typename F> __device__ __forceinline__ void each(F f) const {
-    each(f, [](int) {});
+    each([&](float x, int idx, int) { f(x, idx); }, [](int) {});
   }
-  // (g(index of its first element) after each vector)
+  // f(logit, index, place in its vector), and g(index of its first element) after each vector
   template <typename F, typename G> __device__ __forceinline__ void each(F f, G g) const {
     uint4 next = {};
     if (tid < n_vec) next = raw_vector(tid);
@@ -242,7 +242,7 @@ template <typename T> struct Sampler {
       const uint4 e = cleaned(next);
       if (v + ST < n_vec) next = raw_vector(v + ST);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) f(element(e, i), first + v * VEC + i);
+      for (int i = 0; i < VEC; ++i) f(element(e, i), first + v * VEC + i, i);
       g(first + v * VEC);
     }
   }
@@ -732,15 +732,15 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   const u64 eligible = z.eligible;
   auto live = [&](float x, int idx) { return eligible == 0 || composite(x, idx) >= eligible; };
   if (eligible == 0) {
-    // near masses: each bucket's in 2^-15 of the weight at its middle (a weight changes by 1/128 over a bucket:
-    // two terms of its series); a CTA has at most 65536 tokens
+    // near masses: each bucket's in 2^-18 of the weight at its middle (a weight changes by 1/256 over a bucket: two terms of
+    // its series).  More than 16000 tokens of a CTA in one bucket pass 32 bits: such a row goes the third way.
     for (int i = tid; i < NEAR; i += ST) s.hist[0][i] = 0;
     if (tid < 2) s.n_list[tid] = 0;
     __syncthreads();
-    constexpr float STEP = REACH / NEAR;
+    constexpr float STEP = REACH / NEAR, UNIT = 1 << 18;
     z.each([&](float x, int) {
       const float y = z.near_fall(x), r = y + 8388608.f, f = y - (r - 8388608.f);
-      const float v = fmaf(f, fmaf(f, 16384.f * STEP * STEP, -32768.f * STEP), 32768.f + 8388608.f);
+      const float v = fmaf(f, fmaf(f, 0.5f * UNIT * STEP * STEP, -UNIT * STEP), UNIT + 8388608.f);
       if (y < NEAR - 1.5f) atomicAdd(&s.hist[0][__float_as_int(r) & (NEAR - 1)], __float_as_uint(v) - 0x4b000000u);
     });
     z.meet();
@@ -754,7 +754,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         float m = 0.f;
 #pragma unroll
         for (int r = 0; r < 8; ++r) m += static_cast<float>(h[r]);
-        tot[b] = m * (1.f / 32768.f) * exp2f(static_cast<float>(b) * (-STEP * 1.44269504f));
+        tot[b] = m * (1.f / UNIT) * exp2f(static_cast<float>(b) * (-STEP * 1.44269504f));
       }
     }
     z.meet();
@@ -767,17 +767,18 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
       for (int i = 0; i < EACH; ++i) m[i] = sum += reinterpret_cast<const float*>(s.tot)[EACH * tid + i];
       const float before = z.block_scan(sum) - sum;
       const float last_p = -logf(fminf(min_p, 1.f)) / STEP;  // min_p's own place
-      const int at_m = z.floor_w > 0 ? static_cast<int>(fminf(last_p, NEAR - 1.f)) : NEAR - 1;
+      const int at_m = z.floor_w > 0 ? static_cast<int>(fminf(last_p + 0.5f, NEAR - 1.f)) : NEAR - 1;
       if (tid == 0) {
         s.ctl[z.phase] = {0, 0, NEAR - 1, 0, NEAR - 1};  // first and last range of the draw (bucket, excl), of top_p (count, incl)
         s.near[1] = INFINITY;
+        s.near[3] = 0.f;
       }
       if (tid == ST - 1) s.near[0] = before + sum;
       __syncthreads();
       // top_p's range, and the mass up to and with its last token: as if the range's tokens all weighed the same.  Near masses
-      // are off by some 2^-16: where a target lies that near to a border, two ranges stand for one (else about one row
+      // are off by some 2^-20: where a target lies that near to a border, two ranges stand for one (else about one row
       // in 4000 went the third way, 20 us more).
-      const float near_p = top_p * s.near[0], room = s.near[0] * (1.f / 32768.f);
+      const float near_p = top_p * s.near[0], room = s.near[0] * 0x1p-19f;
       const float above_p = fminf(near_p + room, 0.5f * (near_p + s.near[0]));  // (targets below the end stay below it)
       float excl = before;
 #pragma unroll
@@ -786,19 +787,23 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         if (top_p < 1.f && excl < near_p && near_p <= incl) {
           const float w = middle(i);
           s.near[1] = excl + ceilf((near_p - excl) / w) * w;
+          s.near[3] = w;
         }
         if (excl < near_p - room && near_p - room <= incl) s.ctl[z.phase].count = EACH * tid + i;
         if (excl < above_p && above_p <= incl) s.ctl[z.phase].incl = EACH * tid + i;
-        if (EACH * tid + i == at_m) s.near[2] = incl;
+        if (EACH * tid + i == at_m) s.near[2] = excl + fminf(last_p + 0.5f - static_cast<float>(at_m), 1.f) * (incl - excl);
         excl = incl;
       }
       __syncthreads();
-      const float kept = fminf(s.near[1], s.near[2]), near_u = u * kept, above_u = fminf(near_u + room, 0.5f * (near_u + kept));
+      // (the mass kept is known to a token at its end, and no token before weighs less)
+      const bool p_ends = s.near[1] <= s.near[2];
+      const float near_u = u * (p_ends ? s.near[1] : s.near[2]), room_u = room + (p_ends ? s.near[3] : z.floor_w > 0 ? fminf(min_p, 1.f) : 0.f);
+      const float above_u = fminf(near_u + room_u, 0.5f * (near_u + s.near[0]));
       excl = before;
 #pragma unroll
       for (int i = 0; i < EACH; ++i) {
         const float incl = before + m[i];
-        if (excl <= near_u - room && near_u - room < incl) s.ctl[z.phase].bucket = EACH * tid + i;
+        if (excl <= near_u - room_u && near_u - room_u < incl) s.ctl[z.phase].bucket = EACH * tid + i;
         if (excl <= above_u && above_u < incl) s.ctl[z.phase].excl = EACH * tid + i;
         excl = incl;
       }
@@ -806,8 +811,9 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     }
     const Ctl guess = z.decide();
     const bool with_p = top_p < 1.f;
-    int bp = guess.count, bu = guess.bucket;
-    unsigned more_p = static_cast<unsigned>(guess.incl) - bp, more_u = static_cast<unsigned>(guess.excl) - bu;  // ranges after the first
+    // (not the last range, which has the tokens of no weight and what is none)
+    int bp = min(guess.count, NEAR - 2), bu = min(guess.bucket, NEAR - 2);
+    unsigned more_p = min(static_cast<int>(guess.incl), NEAR - 2) - bp, more_u = min(static_cast<int>(guess.excl), NEAR - 2) - bu;  // ranges after the first
     const bool one = bp <= bu + static_cast<int>(more_u);  // both are in the same ranges
     if (with_p && one) {
       more_u = max(bp + more_p, bu + more_u) - min(bp, bu);
@@ -819,17 +825,17 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     uint32_t hits[2] = {};
     auto exact = [&](auto with_top_p, auto with_min_p) {
       constexpr bool p_on = decltype(with_top_p)::value, m_on = decltype(with_min_p)::value;
-      z.each([&](float x, int idx) {
+      z.each([&](float x, int, int i) {
         const u64 w = z.weight(x);
         const int b = z.near_bucket(x);
         sum[0] += w;
-        if (p_on && b < bp) sum[1] += w;
-        if (b < bu) sum[2] += w;
-        if (m_on && w >= z.floor_w) sum[3] += w;
-        const uint32_t bit = 1u << (idx - z.first) % VEC;  // (a vector's elements come one after the other)
-        if (static_cast<unsigned>(b - bu) <= more_u && w > 0) hits[0] |= bit;
-        if (p_on && static_cast<unsigned>(b - bp) <= more_p && !one && w > 0) hits[1] |= bit;
+        if (p_on) sum[1] += b < bp ? w : 0;
+        sum[2] += b < bu ? w : 0;
+        if (m_on) sum[3] += w >= z.floor_w ? w : 0;
+        hits[0] |= (static_cast<unsigned>(b - bu) <= more_u ? 1u : 0u) << i;
+        if (p_on) hits[1] |= (static_cast<unsigned>(b - bp) <= more_p ? 1u : 0u) << i;
       }, [&](int idx) {
+        if (p_on && one) hits[1] = 0;
         if (hits[0] | hits[1]) {
           z.collect_hits(0, hits[0], idx);
           if (p_on) z.collect_hits(1, hits[1], idx);
