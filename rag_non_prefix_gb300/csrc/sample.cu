@@ -21,7 +21,10 @@
 // Bounds: a few rows by the chain of their passes and cluster barriers (one row of 32000 with top-k: 10.3 us; 64 rows of 64000 fp32 with
 // top-p: 36.6 us, of these the exact pass 6.4, the merge of the near masses 5.9, their own pass 3.3), many by the passes' instructions:
 // 512 rows of 64000 bf16 with top-k and top-p 39.4 us, 1.7 TB/s (a row 12 us on half an SM: its loads and maxima 3.9, the bound 1.5,
-// collecting 3.5, sorting and sums 3.0; 1.7 rounds of rows).  512 threads, two CTAs an SM: 1024 threads and one were slower.
+// collecting 3.5, sorting and sums 3.0; 1.7 rounds of rows); with top-p alone 144 us (38 us a row and SM: near masses 10, the exact
+// pass 23, near 90 issue slots a logit and warp).  512 threads, two CTAs an SM: 1024 threads and one were slower.  Rows that 1. and 2.
+// leave to 3. cost 20 us more in small batches and 3 to 8 times as much in large ones: more than 512 logits within 1/256 of
+// each other (spread of 64000 logits below about a quarter of the temperature), or top-k beyond 256 a CTA.
 #include <cooperative_groups.h>
 
 #include <algorithm>
