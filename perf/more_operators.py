@@ -307,17 +307,17 @@ def _sample(s):
     rank = torch.arange(vocab, device=x.device)
     if s["top_k"] is not None:
         w_sorted = torch.where(rank < s["top_k"][:, None], w_sorted, 0.0)
-    total = w_sorted.cumsum(1)
+    before = w_sorted.cumsum(1) - w_sorted
     keep = w_sorted > 0
     if s["top_p"] is not None:
-        keep &= (total - w_sorted < s["top_p"].double()[:, None] * total[:, -1:]) | (rank == 0)
+        keep &= (before < s["top_p"].double()[:, None] * w_sorted.sum(1, keepdim=True)) | (rank == 0)
     if s["min_p"] is not None:
         keep &= w_sorted >= s["min_p"].double()[:, None]
-    kept = torch.where(keep, w_sorted, 0.0)
+    kept = torch.zeros_like(w).scatter_(1, order, torch.where(keep, w_sorted, 0.0))
     total = kept.cumsum(1)
-    hit = (total > s["uniform"].double()[:, None] * total[:, -1:]) & keep
-    at = torch.where(hit.any(1), hit.to(torch.uint8).argmax(1), keep.sum(1) - 1)
-    return order.gather(1, at[:, None])[:, 0].to(torch.int32)
+    hit = (total > s["uniform"].double()[:, None] * total[:, -1:]) & (kept > 0)
+    last = vocab - 1 - (kept.flip(1) > 0).to(torch.uint8).argmax(1)
+    return torch.where(hit.any(1), hit.to(torch.uint8).argmax(1), last).to(torch.int32)
 
 
 def run(s):
@@ -386,7 +386,7 @@ def _values_at(pool, table, seq, pos):
 
 
 def _sample_exact(s):
-    """Row by row: the tokens by falling logit, how many of them are kept, the walk over those."""
+    """Row by row: the kept tokens by falling logit, then the walk over them by rising index."""
     x = s["logits"].double().cpu().numpy()
     row = {k: None if s[k] is None else s[k].double().cpu().numpy() for k in ("uniform", "temperature", "top_k", "top_p", "min_p")}
     out = []
@@ -401,9 +401,10 @@ def _sample_exact(s):
             n = min(n, 1 + int(np.searchsorted(np.cumsum(ws), row["top_p"][i] * ws.sum(), side="left")))
         if row["min_p"] is not None:
             n = min(n, int(np.count_nonzero(ws >= row["min_p"][i])))
-        mass = np.cumsum(ws[:max(n, 1)])
+        kept = np.sort(order[:max(n, 1)])
+        mass = np.cumsum(w[kept])
         at = int(np.searchsorted(mass, row["uniform"][i] * mass[-1], side="right"))
-        out.append(int(order[min(at, mass.size - 1)]))
+        out.append(int(kept[min(at, kept.size - 1)]))
     return torch.tensor(out, dtype=torch.int32, device="cuda")
 
 
