@@ -609,7 +609,9 @@ cb_status cb_decode_step(cb_ctx* ctx, const cb_decode_seq* seqs_host, int n_seq,
  *   top_p   of those the shortest prefix whose mass (sum of w) reaches top_p times theirs, one token at least
  *           (>= 1: all)
  *   min_p   the tokens with w >= min_p, that is, of at least min_p times the likeliest one's probability (<= 0: all; > 1 is 1)
- * and the token drawn is the first whose running mass exceeds uniform times the mass of the shortest of the three.
+ * and the token drawn is the first whose running mass exceeds uniform times the mass of the shortest of the three: along the
+ * same order, or with by_id along rising ids (the running sum of the probabilities as they lie).  Both draw a token by its probability, but
+ * for one number not the same token.
  * temperature <= 0 (or NaN): the first token (greedy).  Logits of -infinity and NaN are no tokens; a row of them alone
  * gives -1.  Where the largest is +infinity, its tokens are equally likely.  Arrays of one entry per row, device;
  * a NULL filter is off, a NULL temperature is 1. */
@@ -618,6 +620,7 @@ typedef struct {
   const int32_t* top_k;
   const float* top_p;
   const float* min_p;
+  int by_id; /* 0: the draw runs along falling logits; else along rising ids */
 } cb_sampling;
 /* logits [rows][vocab] of dtype with a pitch of ld elements (element-aligned; vocab <= 2^18); uniform [rows] in [0, 1):
  * the same numbers give the same tokens; out int32 [rows].  Weights are exact to about 2^-30 and their

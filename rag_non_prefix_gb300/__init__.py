@@ -98,7 +98,8 @@ class KvqCache(C.Structure):
 
 
 class Sampling(C.Structure):
-    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p)]
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p),
+                ("by_id", C.c_int)]
 
 
 CB_FP8_STORE_F32, CB_FP8_ADD_F32, CB_FP8_SWIGLU_FP8, CB_FP8_STORE_BF16 = 0, 1, 2, 3
@@ -704,7 +705,7 @@ def cb_kvq_attention(q: torch.Tensor, q_pos: torch.Tensor, pool: torch.Tensor, t
 
 # ----------------------------------------------------------------------------- sampling
 # a Sampling as bytes
-_pack_sampling = struct.Struct("@4P").pack
+_pack_sampling = struct.Struct("@4Pi0P").pack
 
 
 def _row_values(t: Optional[torch.Tensor], dtype, rows: int, what: str, dev: int) -> int:
@@ -719,19 +720,21 @@ def _row_values(t: Optional[torch.Tensor], dtype, rows: int, what: str, dev: int
     return t.data_ptr()
 
 
-def _filters(rows: int, dev: int, temperature, top_k, top_p, min_p) -> bytes:
+def _filters(rows: int, dev: int, temperature, top_k, top_p, min_p, by_id) -> bytes:
     return _pack_sampling(_row_values(temperature, torch.float32, rows, "temperature", dev),
                           _row_values(top_k, torch.int32, rows, "top_k", dev),
                           _row_values(top_p, torch.float32, rows, "top_p", dev),
-                          _row_values(min_p, torch.float32, rows, "min_p", dev))
+                          _row_values(min_p, torch.float32, rows, "min_p", dev), bool(by_id))
 
 
 def cb_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Optional[torch.Tensor] = None,
               top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
-              min_p: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+              min_p: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None,
+              by_id: bool = False) -> torch.Tensor:
     """A token id (int32) of each row of logits [rows, vocab], drawn by the row's random number ``uniform`` in [0, 1)
     after the filters (tensors of a value per row: fp32, top_k int32; None: off).  A temperature of 0 is
-    greedy; a row without a token gives -1."""
+    greedy; a row without a token gives -1.  The running mass that ``uniform`` cuts goes along falling logits, or
+    with ``by_id`` along rising ids (``searchsorted(cumsum(probabilities), uniform)``)."""
     dt = _dtype_code(logits.dtype)
     rows, vocab, ld, dev = _first(logits, "logits")
     if uniform is None:
@@ -740,7 +743,7 @@ def cb_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Optional
         with _allocating_on(stream):
             out = torch.empty(rows, dtype=torch.int32, device=logits.device)
     _check(load_library().cb_sample(logits.data_ptr(), ld, dt, rows, vocab,
-                                    _filters(rows, dev, temperature, top_k, top_p, min_p),
+                                    _filters(rows, dev, temperature, top_k, top_p, min_p, by_id),
                                     _row_values(uniform, torch.float32, rows, "uniform", dev),
                                     _row_values(out, torch.int32, rows, "out", dev), _stream_on(dev, stream)))
     return out
@@ -984,7 +987,7 @@ class Engine:
         """One decode step of the blended requests ``reqs`` (made with decode_room):
         tokens [n] enter at positions n_past[i] (default: each request's prompt length plus the
         steps it already decoded); returns the next tokens [n]: the likeliest ones, or with ``sampling``
-        (cb_sample's ``uniform`` and any of its filters, a value per request) drawn ones."""
+        (cb_sample's ``uniform`` and any of its filters, a value per request, and ``by_id``) drawn ones."""
         n = len(reqs)
         if out_tokens is None:
             with _allocating_on(stream):
@@ -998,8 +1001,8 @@ class Engine:
             _check(self.lib.cb_decode_step(self.ctx, arr, n, _ptr(tokens), _ptr(out_tokens), _stream(stream)), self.ctx)
         else:
             dev = self.workspace.get_device()
-            filters = _filters(n, dev, *(sampling.get(f) for f in ("temperature", "top_k", "top_p", "min_p")))
-            if unknown := set(sampling) - {"uniform", "temperature", "top_k", "top_p", "min_p"}:
+            filters = _filters(n, dev, *(sampling.get(f) for f in ("temperature", "top_k", "top_p", "min_p", "by_id")))
+            if unknown := set(sampling) - {"uniform", "temperature", "top_k", "top_p", "min_p", "by_id"}:
                 raise CacheBlendError(1, f"unknown sampling arguments {sorted(unknown)}")
             _check(self.lib.cb_decode_step_sample(self.ctx, arr, n, _ptr(tokens), filters,
                                                   _row_values(sampling.get("uniform"), torch.float32, n, "uniform", dev),

@@ -1513,8 +1513,8 @@ cb_status cb_sample(const void* logits, long long ld, cb_dtype dtype, int rows, 
   if (!logits || bad_sampling(params, uniform, out) || (reinterpret_cast<uintptr_t>(logits) & (dtype == CB_BF16 ? 1 : 3)))
     return fail(nullptr, CB_ERR_INVALID_ARG, "null or misaligned pointer");
   const cb_sampling f = params ? *params : cb_sampling{};
-  cudaError_t e = launch_sample(logits, ld, dtype, rows, vocab, f.temperature, f.top_k, f.top_p, f.min_p, uniform, out,
-                                as_stream(stream));
+  cudaError_t e = launch_sample(logits, ld, dtype, rows, vocab, f.temperature, f.top_k, f.top_p, f.min_p, uniform, f.by_id != 0,
+                                out, as_stream(stream));
   return e == cudaSuccess ? CB_OK : cuda_fail(nullptr, e, "cb_sample");
 }
 
@@ -1858,7 +1858,7 @@ static cb_status decode_step(cb_ctx* ctx, const cb_decode_seq* seqs, int n_seq, 
     if (uniform) {
       const cb_sampling f = params ? *params : cb_sampling{};
       CB_CUDA(ctx, launch_sample(ctx->logits, c.vocab, CB_F32, n_seq, c.vocab, f.temperature, f.top_k, f.top_p, f.min_p,
-                                 uniform, out_tokens, s));
+                                 uniform, f.by_id != 0, out_tokens, s));
     } else {
       CB_CUDA(ctx, launch_argmax(ctx->logits, n_seq, c.vocab, nullptr, out_tokens, s));
     }

@@ -319,10 +319,10 @@ cudaError_t launch_kvq_attention(const KvqView& c, int head_dim, const void* q, 
                                  int n_heads, float scale, cb_dtype dt, void* out, long long ldo, void* scratch,
                                  int32_t* status, cudaStream_t s);
 
-// Tokens drawn from rows of logits (cb_sample); NULL filters are off, a NULL temperature is 1.
+// Tokens drawn from rows of logits (cb_sample); NULL filters are off, a NULL temperature is 1.  by_id: along rising ids.
 constexpr int SAMPLE_MAX_VOCAB = 1 << 18;
 cudaError_t launch_sample(const void* logits, long long ld, cb_dtype dt, int rows, int vocab, const float* temperature,
-                          const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, int32_t* out,
-                          cudaStream_t s);
+                          const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, bool by_id,
+                          int32_t* out, cudaStream_t s);
 
 }  // namespace cb

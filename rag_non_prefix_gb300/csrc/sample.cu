@@ -2,7 +2,7 @@
 //
 //   w_i = exp((x_i - max) / t); tokens stand by falling x, equal ones by rising index.  Every filter keeps a prefix of that
 //   order: the first k; of those the shortest whose mass reaches p times theirs; those with w >= min_p.  The
-//   token is the first whose running kept mass exceeds u times the kept mass.
+//   token is the first whose running kept mass exceeds u times the kept mass, along that order or by rising index.
 // So a filter and the draw are the same question, "at which token does the running count or mass reach a
 // target", answered exactly: weights are whole numbers of 2^-44 (a weight's relative error is near
 // 2^-30: the exponent (x - max) / t log2(e) is carried in two fp32 numbers), and sums of whole numbers do not depend on their order.
@@ -17,6 +17,8 @@
 //      ranges and collects their tokens, which are sorted; the exact sums show whether the ranges were the right ones.
 //   3. an exact histogram of counts or masses, whose range that holds the target is cut further by the bits of x and of the
 //      index until at most LIST tokens are left (flat rows, crowds of equal logits, top-k beyond 1.'s).
+// A draw by rising index needs the filters' last token alone: 1. sorts what is kept once more, by index; for the others one pass over the
+// exact weights sums what is kept of each 32 vectors, and the 32 that hold the target are weighed once more, token by token.
 //
 // Bounds: a few rows by the chain of their passes and cluster barriers (one row of 32000 with top-k: 10.3 us; 64 rows of 64000 fp32 with
 // top-p: 36.6 us, of these the exact pass 6.4, the merge of the near masses 5.9, their own pass 3.3), many by the passes' instructions:
@@ -296,6 +298,61 @@ template <typename T> struct Sampler {
     }
   }
 
+  // The draw by rising index over the tokens from `cut` on (as composites) that min_p keeps: the masses of the warps' 32 vectors,
+  // one after the other in memory, then the tokens of those that hold the target of the mass, reach(mass).
+  template <typename R> __device__ __forceinline__ void draw_by_id(u64 cut, R reach, int32_t* out) {
+    auto kept = [&](float x, int idx) {
+      const u64 w = weight(x);
+      return composite(x, idx) >= cut && w >= floor_w ? w : 0;
+    };
+    u64* masses = s.sums();
+    __syncthreads();
+    masses[tid] = 0;
+    __syncthreads();
+    u64 sum = 0;
+    each([&](float x, int idx, int) { sum += kept(x, idx); },
+         [&](int idx) {
+           sum = warp_sum64(sum);
+           if (lane == 0) masses[(idx - first) / (32 * VEC)] = sum;
+           sum = 0;
+         });
+    __syncthreads();
+    const u64 mine = masses[tid], incl = block_scan(mine);
+    if (tid == ST - 1) s.part[4] = incl;  // (part[0] may still be on its way to another CTA)
+    meet();
+    const u64 each_cta = of_each(&s.part[4], static_cast<u64>(0));
+    const u64 total = warp_sum64(each_cta), before = warp_sum64(lane < rank ? each_cta : 0);
+    const u64 want = reach(total);  // (at least 1: the largest logit's token is kept)
+    if (before < want && want - before <= __shfl_sync(0xffffffffu, each_cta, rank)) {
+      const u64 target = want - before;
+      if (incl - mine < target && target <= incl) {
+        s.part[5] = target - (incl - mine);
+        s.n_list[1] = tid;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const int v = s.n_list[1] * 32 + lane;
+        const uint4 e = cleaned(raw_vector(v));
+        u64 w[VEC], own = 0;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) own += w[i] = kept(element(e, i), first + v * VEC + i);
+        u64 run = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 y = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += y;
+        }
+        run -= own;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (run < s.part[5] && s.part[5] <= run + w[i]) *out = first + v * VEC + i;
+          run += w[i];
+        }
+      }
+    }
+    meet();
+  }
+
   __device__ __forceinline__ void meet() {  // all CTAs of the row
     if (ranks == 1)
       __syncthreads();
@@ -553,7 +610,8 @@ template <typename T> struct Sampler {
   }
 };
 
-template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(SampleArgs a) {
+// BY_ID: the draw goes by rising index.
+template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sample_kernel(SampleArgs a) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t raw[];
@@ -654,8 +712,18 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     // kept mass: of the shorter prefix
     if (mine && incl - mine < pm && pm <= incl) s.part[2] = incl;
     const int over = __syncthreads_count(mine && mine >= z.floor_w);
-    const u64 want = reach_u(min(s.part[2], sums[over - 1]));
-    if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
+    const u64 mass = min(s.part[2], sums[over - 1]), want = reach_u(mass);
+    if (!BY_ID) {
+      if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
+      return;
+    }
+    // the kept tokens by rising index, their weights by their places in the order
+    const bool kept = mine && incl <= mass;
+    const int n_kept = __syncthreads_count(kept);
+    s.tot[tid] = mine;
+    const u64 at = z.sorted(kept ? tok << 32 | static_cast<unsigned>(tid) : 0, n_kept);
+    const u64 here = tid < n_kept ? s.tot[static_cast<uint32_t>(at)] : 0, run = z.block_scan(here);
+    if (here && run - here < want && want <= run) a.out[row] = index_of(at >> 32);
   };
 
   bool refined = false;
@@ -734,6 +802,10 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
 
   const u64 eligible = z.eligible;
   auto live = [&](float x, int idx) { return eligible == 0 || composite(x, idx) >= eligible; };
+  if (BY_ID && !(top_p < 1.f)) {  // (nothing to find first)
+    z.draw_by_id(eligible, reach_u, a.out + row);
+    return;
+  }
   if (eligible == 0) {
     // near masses: each bucket's in 2^-18 of the weight at its middle (a weight changes by 1/256 over a bucket: two terms of
     // its series).  More than 16000 tokens of a CTA in one bucket pass 32 bits: such a row goes the third way.
@@ -798,6 +870,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         excl = incl;
       }
       __syncthreads();
+      if (!BY_ID) {
       // (the mass kept is known to a token at its end, and no token before weighs less)
       const bool p_ends = s.near[1] <= s.near[2];
       const float near_u = u * (p_ends ? s.near[1] : s.near[2]), room_u = room + (p_ends ? s.near[3] : z.floor_w > 0 ? fminf(min_p, 1.f) : 0.f);
@@ -811,12 +884,14 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         excl = incl;
       }
       __syncthreads();
+      }
     }
     const Ctl guess = z.decide();
     const bool with_p = top_p < 1.f;
     // (not the last range, which has the tokens of no weight and what is none)
     int bp = min(guess.count, NEAR - 2), bu = min(guess.bucket, NEAR - 2);
     unsigned more_p = min(static_cast<int>(guess.incl), NEAR - 2) - bp, more_u = min(static_cast<int>(guess.excl), NEAR - 2) - bu;  // ranges after the first
+    if (BY_ID) bu = bp, more_u = more_p;
     const bool one = bp <= bu + static_cast<int>(more_u);  // both are in the same ranges
     if (with_p && one) {
       more_u = max(bp + more_p, bu + more_u) - min(bp, bu);
@@ -849,7 +924,7 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
     };
     typedef std::integral_constant<bool, true> On;
     typedef std::integral_constant<bool, false> Off;
-    if (with_p)
+    if (BY_ID || with_p)
       z.floor_w > 0 ? exact(On(), On()) : exact(On(), Off());
     else
       z.floor_w > 0 ? exact(Off(), On()) : exact(Off(), Off());
@@ -890,21 +965,32 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
         if (tid == n_u - 1) s.part[5] = scan;
         __syncthreads();
         const u64 incl = tid < n_u ? total[2] + scan : total[1] + scan - s.part[5];
-        if (need_p) {
-          if (mine && incl - mine < pm && pm <= incl) s.part[0] = incl;
-          __syncthreads();
-          mass = s.part[0];
-        }
-        const u64 want = reach_u(mass);
-        if (mass > 0 && mine && tid < n_u && incl - mine < want && want <= incl) {
-          a.out[row] = index_of(tok);
-          s.ctl[z.phase].count = 1;
+        if (BY_ID) {  // top_p's last token, or that min_p keeps fewer
+          if (need_p ? mine && incl - mine < pm && pm <= incl : tid == 0) {
+            s.ctl[z.phase].comp = need_p ? tok : 0;
+            s.ctl[z.phase].count = 1;
+          }
+        } else {
+          if (need_p) {
+            if (mine && incl - mine < pm && pm <= incl) s.part[0] = incl;
+            __syncthreads();
+            mass = s.part[0];
+          }
+          const u64 want = reach_u(mass);
+          if (mass > 0 && mine && tid < n_u && incl - mine < want && want <= incl) {
+            a.out[row] = index_of(tok);
+            s.ctl[z.phase].count = 1;
+          }
         }
       }
       __syncthreads();
     }
-    if (z.decide().count) {
-      z.meet();
+    const Ctl found = z.decide();
+    if (found.count) {
+      if (BY_ID)
+        z.draw_by_id(found.comp, reach_u, a.out + row);
+      else
+        z.meet();
       return;
     }
   }
@@ -919,23 +1005,30 @@ template <typename T> __global__ void __launch_bounds__(ST, 2) sample_kernel(Sam
   const Ctl sums = z.decide();
   u64 mass = sums.incl;  // what min_p keeps
   const u64 pm = reach_p(sums.excl);
+  u64 cut = eligible;
   if (pm <= mass && pm < sums.excl) {  // top_p keeps less
     refined = false;
-    mass = z.template select<true>(pm, live, &refined).incl;
-    if (refined) masses();
+    const Ctl last = z.template select<true>(pm, live, &refined);
+    mass = last.incl;
+    cut = last.comp;
+    if (!BY_ID && refined) masses();
+  }
+  if (BY_ID) {
+    z.draw_by_id(cut, reach_u, a.out + row);
+    return;
   }
   const u64 comp = z.template select<true>(reach_u(mass), live, &refined).comp;
   if (z.rank == 0 && tid == 0) a.out[row] = index_of(comp);
   z.meet();
 }
 
-template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s) {
+template <typename T, bool BY_ID> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   static DeviceOnce configured;
-  if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T>), static_cast<int>(sizeof(Smem)), configured)) != cudaSuccess)
+  if ((e = max_dynamic_smem_once(reinterpret_cast<const void*>(sample_kernel<T, BY_ID>), static_cast<int>(sizeof(Smem)), configured)) != cudaSuccess)
     return e;
   // CTAs of a row: as its size needs, and more while all rows' CTAs still run at once, two on an SM
   // sums of 15-bit parts and of near masses stay within 32 bits; 32 fp32 vectors a thread, the first off a boundary too
@@ -960,14 +1053,14 @@ template <typename T> cudaError_t launch(SampleArgs a, int rows, cudaStream_t s)
   attr[1].val.programmaticStreamSerializationAllowed = launch_overlap_enabled() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, BY_ID>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const void* logits, long long ld, cb_dtype dt, int rows, int vocab, const float* temperature,
-                          const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, int32_t* out,
-                          cudaStream_t s) {
+                          const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform, bool by_id,
+                          int32_t* out, cudaStream_t s) {
   SampleArgs a = {};
   a.logits = logits;
   a.ld = ld;
@@ -978,7 +1071,8 @@ cudaError_t launch_sample(const void* logits, long long ld, cb_dtype dt, int row
   a.min_p = min_p;
   a.uniform = uniform;
   a.out = out;
-  return dt == CB_BF16 ? launch<bf16>(a, rows, s) : launch<float>(a, rows, s);
+  if (dt == CB_BF16) return by_id ? launch<bf16, true>(a, rows, s) : launch<bf16, false>(a, rows, s);
+  return by_id ? launch<float, true>(a, rows, s) : launch<float, false>(a, rows, s);
 }
 
 }  // namespace cb
