@@ -326,7 +326,7 @@ def run(s):
         import rag_non_prefix_gb300 as cb
 
         if kind == "sample":
-            return cb.cb_sample(s["logits"], s["uniform"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"], out=s["out"])
+            return cb.cb_sample(s["logits"], s["uniform"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"], out=s["out"], by_id=True)
         if kind == "attention":
             return cb.cb_kvq_attention(s["q"], s["q_pos"], s["pool"], s["table"], out=s["out"], scratch=s.get("scratch"))
         if kind == "write":
