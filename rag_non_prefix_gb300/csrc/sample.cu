@@ -293,6 +293,7 @@ template <typename T> struct Sampler {
     while (hits) {
       const int at = idx + __ffs(hits) - 1;
       hits &= hits - 1;
+      if (static_cast<unsigned>(at - first - off) >= static_cast<unsigned>(n)) continue;  // (a neighbour's element)
       const float x = to_f(src[at - first - off]);
       collect(which, inf ? 0.f : x, at);
     }
@@ -890,7 +891,9 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
     const bool with_p = top_p < 1.f;
     // (not the last range, which has the tokens of no weight and what is none)
     int bp = min(guess.count, NEAR - 2), bu = min(guess.bucket, NEAR - 2);
-    unsigned more_p = min(static_cast<int>(guess.incl), NEAR - 2) - bp, more_u = min(static_cast<int>(guess.excl), NEAR - 2) - bu;  // ranges after the first
+    // ranges after the first: none where the last would lie before it (they come from fp32 sums, whose rounding may turn neighbours round; the
+    // exact sums show what was missed)
+    unsigned more_p = max(min(static_cast<int>(guess.incl), NEAR - 2) - bp, 0), more_u = max(min(static_cast<int>(guess.excl), NEAR - 2) - bu, 0);
     if (BY_ID) bu = bp, more_u = more_p;
     const bool one = bp <= bu + static_cast<int>(more_u);  // both are in the same ranges
     if (with_p && one) {
