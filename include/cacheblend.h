@@ -436,7 +436,8 @@ cb_status cb_attention(const void* q, const int32_t* q_pos, int m, const void* k
  *   scale = the smallest bf16 number >= max(d / 14.75, a / 64, 2^-120)
  *   zero  = floor(4 lo / scale) / 4
  *   code  = clamp(nearest(x / scale - zero), 0, 15), ties to even      (each of the three exactly)
- *   value = scale * (code + zero)                                      (exact in float32)
+ *   value = scale * (code + zero)       (exact in float32; an infinity where it passes float32's range, which it does at most
+ *                                        half a step from the largest number)
  * so a value is within scale / 2 of x (and within 2^-7 of it where all of a group is alike).  A group with an infinity or a NaN,
  * or whose d passes float32's range, decodes to NaN throughout.
  *

@@ -1,9 +1,9 @@
 // A KV cache in 4 bits (layout and arithmetic: kvq.cuh): rows quantised as they are written, and read back
 // with their keys turned to new positions.
 //
-// Bounds: a number is 2 or 4 bytes and 5 bits, and takes some 28 instructions to write and 12 to read.  Prompts are bound by these
+// Bounds: a number is 2 or 4 bytes and 5 bits, and takes some 28 instructions to write and 13 to read.  Prompts are bound by these
 // and by the latency of the loads that 32 warps an SM cover (8320 rows of 8 heads of 128 written from bf16 and read back to
-// fp32: 36.2 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to bf16: 24.7 us, 3.6 TB/s; with the registers of
+// fp32: 36.4 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to bf16: 25.4 us, 3.5 TB/s; with the registers of
 // 24 warps an SM 28.4); decoded tokens by one warp's chain (16 rows of 8 heads written and read back: 4.6 us, two launches).
 //
 // Both kernels give eight channels to a lane: a row of one head is 16 lanes (128 channels) or 8, a group of 32
@@ -266,12 +266,13 @@ __global__ void __launch_bounds__(KVQ_WARPS * 32, 32 / KVQ_WARPS) kvq_read_kerne
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         float kx[8], vx[8];
-        const float ks = bf(prm[s][0]), kz = ks * bf(prm[s][1]), vs = bf(prm[s][2]), vz = vs * bf(prm[s][3]);
+        const float ks = bf(prm[s][0]), kz = bf(prm[s][1]), vs = bf(prm[s][2]), vz = bf(prm[s][3]);
         const int up = (WHOLE ? 8 * (2 * (at.r[s] & 1) + (at.r[s] >> 3)) : 0) + (L & 1 ? 4 : 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          kx[i] = fmaf(static_cast<float>((kc[s] >> (4 * i)) & 15u), ks, kz);  // (exact: 17 bits)
-          vx[i] = fmaf(static_cast<float>((vc[WHOLE ? 0 : s][i] >> up) & 15u), vs, vz);
+          // code + zero (9 bits) first: scale times zero alone may pass fp32's range where the value does not
+          kx[i] = (static_cast<float>((kc[s] >> (4 * i)) & 15u) + kz) * ks;  // (exact: 17 bits)
+          vx[i] = (static_cast<float>((vc[WHOLE ? 0 : s][i] >> up) & 15u) + vz) * vs;
         }
         if (turned) {
 #pragma unroll

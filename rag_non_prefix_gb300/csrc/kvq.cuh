@@ -6,7 +6,8 @@
 //   zero  = floor(4 lo / scale) / 4,   code = clamp(nearest(x / scale - zero), 0, 15)
 //   value = scale * (code + zero)
 // The zero is a multiple of 1/4 of at most 64, so bf16 holds it; 14.75 steps and a zero at most 1/4 step too
-// low reach over the group.  code + zero has 9 bits and scale 8: the value is exact in fp32, and so is
+// low reach over the group.  code + zero has 9 bits and scale 8: the value is exact in fp32 (infinite beyond its range;
+// scale zero alone may be where the value is not, so it is not formed), and so is
 // (n + 1/2 + zero) * scale, by which the nearest code is decided exactly without a division.
 //
 // Block of 16 tokens of one head, 20 D bytes (D channels, NG = D / 32 groups), the memory a tensor-core
