@@ -624,8 +624,8 @@ typedef struct {
   int by_id; /* 0: the draw runs along falling logits; else along rising ids */
 } cb_sampling;
 /* logits [rows][vocab] of dtype with a pitch of ld elements (element-aligned; vocab <= 2^18); uniform [rows] in [0, 1):
- * the same numbers give the same tokens; out int32 [rows].  Weights are exact to about 2^-30 and their
- * sums exact, whatever the order.  params may be NULL. */
+ * the same numbers give the same tokens; out int32 [rows].  Weights are exact to about 2^-28 of themselves
+ * and 2^-44 of the largest, their sums exact, whatever the order; min_p is compared to about 2^-28, whatever the weight.  params may be NULL. */
 cb_status cb_sample(const void* logits, long long ld, cb_dtype dtype, int rows, int vocab, const cb_sampling* params,
                     const float* uniform, int32_t* out, void* stream);
 /* cb_decode_step whose next tokens are drawn (cb_sample on the LM head's fp32 logits) instead of the largest. */

@@ -85,8 +85,8 @@ struct __align__(16) Smem {
   u64 part[6];          // this CTA's: see the uses
   uint32_t above[SW];   // bounds, a warp's each
   float near[4];
-  u64 floor_w;          // (64-bit floating point is slow: one thread computes these for all)
-  float c_hi, c_lo;
+  float c_hi, c_lo;     // (64-bit floating point is slow: one thread computes these for all)
+  float m_hi, m_lo;     // t log(min_p)
   Ctl ctl[2];
   int n_list[2];
   // (while no histogram is in use: a row's first vectors, and the first CTA's own)
@@ -143,7 +143,7 @@ template <typename T> struct Sampler {
   // row
   float top, c_hi, c_lo, reach;  // largest logit, log2(e) / t in two parts, buckets per unit of max - x
   uint32_t tab;
-  u64 floor_w = 0;  // min_p's weight
+  float floor_x = -INFINITY;  // the least logit that min_p keeps
   u64 eligible = 0; // composite of the last token that top-k keeps
 
   __device__ Sampler(const SampleArgs& args, Smem& sm) : a(args), s(sm), cl(cg::this_cluster()) {
@@ -161,6 +161,12 @@ template <typename T> struct Sampler {
     // the difference's own rounding (two-sum), then the exponent in two parts
     const float b = d - x, de = (x - (d - b)) + (-top - b);
     const float e = d * c_hi, el = fmaf(d, c_hi, -e) + fmaf(d, c_lo, de * c_hi);
+    int k;
+    const uint32_t m = exp2_of(e, el, &k);
+    return (static_cast<u64>(m) << (SHIFT - 30)) >> -k;
+  }
+  // 2^(e + el) as m 2^(k - 30), m of 31 bits.  All lanes of a warp take part.
+  __device__ __forceinline__ uint32_t exp2_of(float e, float el, int* whole) const {
     // e = k / 32 + r: 2^(k / 32) from the table, 2^r - 1 by its series (|r ln 2| < 0.011: terms to the fourth); below
     // 2^-47 every 32 bits shifted that far are 0, whatever r is
     const float ec = fmaxf(e, -47.f), km = fmaf(ec, 32.f, 12582912.f);
@@ -169,8 +175,17 @@ template <typename T> struct Sampler {
     const float y = fmaf(r, 0.693147182f, r * -1.90465421e-9f);
     const float p = fmaf(y * y, fmaf(y, fmaf(y, 1.f / 24.f, 1.f / 6.f), 0.5f), y);
     const int t = static_cast<int>(__shfl_sync(0xffffffffu, tab, k & 31));
-    const uint32_t m = static_cast<uint32_t>(t + __mulhi(t, __float2int_rn(p * 4294967296.f)));
-    return (static_cast<u64>(m) << (SHIFT - 30)) >> -(k >> 5);
+    *whole = k >> 5;
+    return static_cast<uint32_t>(t + __mulhi(t, __float2int_rn(p * 4294967296.f)));
+  }
+  // log(x) of 2^-46 <= x <= 1 in two parts, as exactly as weights are: an estimate, and what its exponential is off by.  All lanes of a
+  // warp take part.
+  __device__ __forceinline__ float2 log_of(float x) const {
+    const float l = logf(x), e = l * 1.44269502f;
+    int k;
+    const uint32_t m = exp2_of(e, fmaf(l, 1.44269502f, -e) + l * 1.92596299e-8f, &k);
+    const uint32_t want = static_cast<uint32_t>(x * __int_as_float((157 - k) << 23));  // x 2^(30 - k), a whole number
+    return make_float2(l, static_cast<float>(static_cast<int>(want - m)) / static_cast<float>(m));
   }
   // (max - x) / t in buckets, at most the last one; that is 2^-46 and weighs nothing
   __device__ __forceinline__ float fall(float x) const { return fminf((top - x) * reach, static_cast<float>(BUCKETS - 1)); }
@@ -304,7 +319,7 @@ template <typename T> struct Sampler {
   template <typename R> __device__ __forceinline__ void draw_by_id(u64 cut, R reach, int32_t* out) {
     auto kept = [&](float x, int idx) {
       const u64 w = weight(x);
-      return composite(x, idx) >= cut && w >= floor_w ? w : 0;
+      return composite(x, idx) >= cut && x >= floor_x ? w : 0;
     };
     u64* masses = s.sums();
     __syncthreads();
@@ -379,7 +394,7 @@ template <typename T> struct Sampler {
       // tokens of one value come in crowds (bf16, flat rows): one lane adds for a warp that agrees
       const u64 w = MASS ? weight(x) : 1;
       const bool add = b >= 0 && w > 0;
-      if (MASS && add && w >= floor_w) over += w;
+      if (MASS && add && x >= floor_x) over += w;
       const unsigned who = __ballot_sync(0xffffffffu, add);
       if (who == 0) return;
       const int b0 = __shfl_sync(0xffffffffu, b, __ffs(who) - 1);
@@ -642,8 +657,16 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
     const double c = 1.4426950408889634 / static_cast<double>(fminf(fmaxf(t, 1e-20f), 1e20f));
     s.c_hi = static_cast<float>(c);
     s.c_lo = static_cast<float>(c - static_cast<double>(s.c_hi));
-    const u64 one = 1ull << SHIFT;
-    s.floor_w = min_p > 0.f ? min(one, static_cast<u64>(ceil(static_cast<double>(min_p) * static_cast<double>(one)))) : 0;
+  }
+  // w >= min_p is x >= max + t log(min_p): by logits, as weights of few units of 2^-44 say little (and those below 2^-45 nothing)
+  const bool with_m = min_p >= 0x1p-45f;
+  if (with_m && warp == SW - 1) {
+    const float2 l = z.log_of(fminf(min_p, 1.f));
+    const float ts = fminf(fmaxf(t, 1e-20f), 1e20f), hi = ts * l.x;
+    if (lane == 0) {
+      s.m_hi = hi;
+      s.m_lo = fmaf(ts, l.x, -hi) + ts * l.y;
+    }
   }
   float own = -INFINITY;  // this thread's largest
   const bool keep = k > 1 && k <= z.ranks * (ST / 2) && k < a.vocab;  // (way 1)
@@ -696,7 +719,10 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
   z.c_hi = s.c_hi;
   z.c_lo = s.c_lo;
   z.reach = BUCKETS / REACH / t;
-  z.floor_w = s.floor_w;
+  if (with_m) {  // the smallest number not below max + t log(min_p): their sum (two-sum), and what it left out, rounded up
+    const float f = z.top + s.m_hi, b = f - z.top;
+    z.floor_x = __fadd_ru(f, (z.top - (f - b)) + (s.m_hi - b) + s.m_lo);
+  }
   // targets of a mass m: the smallest whole numbers not below top_p m, and above u m
   auto reach_p = [&](u64 m) { return top_p < 1.f ? max(1ull, part_of(m, top_p, true)) : m; };
   auto reach_u = [&](u64 m) { return min(m, part_of(m, u, false) + 1); };
@@ -712,7 +738,7 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
     const u64 pm = reach_p(sums[ST - 1]);
     // kept mass: of the shorter prefix
     if (mine && incl - mine < pm && pm <= incl) s.part[2] = incl;
-    const int over = __syncthreads_count(mine && mine >= z.floor_w);
+    const int over = __syncthreads_count(mine && logit_of(tok) >= z.floor_x);
     const u64 mass = min(s.part[2], sums[over - 1]), want = reach_u(mass);
     if (!BY_ID) {
       if (mine && incl - mine < want && want <= incl) a.out[row] = index_of(tok);
@@ -843,7 +869,7 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
       for (int i = 0; i < EACH; ++i) m[i] = sum += reinterpret_cast<const float*>(s.tot)[EACH * tid + i];
       const float before = z.block_scan(sum) - sum;
       const float last_p = -logf(fminf(min_p, 1.f)) / STEP;  // min_p's own place
-      const int at_m = z.floor_w > 0 ? static_cast<int>(fminf(last_p + 0.5f, NEAR - 1.f)) : NEAR - 1;
+      const int at_m = with_m ? static_cast<int>(fminf(last_p + 0.5f, NEAR - 1.f)) : NEAR - 1;
       if (tid == 0) {
         s.ctl[z.phase] = {0, 0, NEAR - 1, 0, NEAR - 1};  // first and last range of the draw (bucket, excl), of top_p (count, incl)
         s.near[1] = INFINITY;
@@ -874,7 +900,7 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
       if (!BY_ID) {
       // (the mass kept is known to a token at its end, and no token before weighs less)
       const bool p_ends = s.near[1] <= s.near[2];
-      const float near_u = u * (p_ends ? s.near[1] : s.near[2]), room_u = room + (p_ends ? s.near[3] : z.floor_w > 0 ? fminf(min_p, 1.f) : 0.f);
+      const float near_u = u * (p_ends ? s.near[1] : s.near[2]), room_u = room + (p_ends ? s.near[3] : with_m ? fminf(min_p, 1.f) : 0.f);
       const float above_u = fminf(near_u + room_u, 0.5f * (near_u + s.near[0]));
       excl = before;
 #pragma unroll
@@ -912,7 +938,7 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
         sum[0] += w;
         if (p_on) sum[1] += b < bp ? w : 0;
         sum[2] += b < bu ? w : 0;
-        if (m_on) sum[3] += w >= z.floor_w ? w : 0;
+        if (m_on) sum[3] += x >= z.floor_x ? w : 0;
         hits[0] |= (static_cast<unsigned>(b - bu) <= more_u ? 1u : 0u) << i;
         if (p_on) hits[1] |= (static_cast<unsigned>(b - bp) <= more_p ? 1u : 0u) << i;
       }, [&](int idx) {
@@ -928,9 +954,9 @@ template <typename T, bool BY_ID> __global__ void __launch_bounds__(ST, 2) sampl
     typedef std::integral_constant<bool, true> On;
     typedef std::integral_constant<bool, false> Off;
     if (BY_ID || with_p)
-      z.floor_w > 0 ? exact(On(), On()) : exact(On(), Off());
+      with_m ? exact(On(), On()) : exact(On(), Off());
     else
-      z.floor_w > 0 ? exact(Off(), On()) : exact(Off(), Off());
+      with_m ? exact(Off(), On()) : exact(Off(), Off());
     u64* scratch = s.sums();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
