@@ -52,6 +52,7 @@ constexpr int MIN_SHARE = 4;
 constexpr int UNIT_COST = 6;
 constexpr int MAX_ROWS = 16;             // query rows per tile at most
 constexpr float LAZY = 6.f;              // the running maximum moves once a score passes it by 2^6
+constexpr float LOWEST = -3.40282347e38f;  // the maximum of no scores: finite, so that scores of -infinity have a weight of zero beside it
 
 __host__ __device__ constexpr int slot_floats(int dh) { return MAX_ROWS * (dh + 2); }
 
@@ -209,7 +210,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -INFINITY;
+        m[nt][c] = LOWEST;
         l[nt][c] = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) corr[nt][g][c] = 0.f;
@@ -430,7 +431,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
           float x = fmaxf(m[nt][c], fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          const float f = x == -INFINITY ? 1.f : exp2_fast(m[nt][c] - x);
+          const float f = exp2_fast(m[nt][c] - x);
           m[nt][c] = x;
           l[nt][c] *= f;
           if (CENTRED)
@@ -449,8 +450,7 @@ template <typename T, int DH, int NT, int NP> struct Attn {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float mm = m[nt][i & 1];
-          s[u][nt][i] = exp2_fast(s[u][nt][i] - (MASKED && mm == -INFINITY ? 0.f : mm));
+          s[u][nt][i] = exp2_fast(s[u][nt][i] - m[nt][i & 1]);
           l[nt][i & 1] += s[u][nt][i];
         }
     values<MASKED>(blk0, s[0], dead[0]);
@@ -468,11 +468,9 @@ template <int DH> __device__ __forceinline__ void copy_block(uint32_t dst, const
   }
 }
 
-// weight of a part (maximum m, sum l) under the common maximum M; a part without keys has none (and sums of zero).  Sums are
+// weight of a part of maximum m under the common maximum M (a part without keys: m = LOWEST, sums of zero).  Sums are
 // added under weights of zero too: a NaN among them stays one.
-__device__ __forceinline__ float part_weight(float m, float l, float M) {
-  return m == -INFINITY && l == 0.f ? 0.f : exp2f(m - M);
-}
+__device__ __forceinline__ float part_weight(float m, float M) { return exp2f(m - M); }
 
 template <typename T, int DH, int NT, int NP>
 __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1 ? 4 : 3) kvq_attention_kernel(const __grid_constant__ KvqAttn p) {
@@ -671,12 +669,12 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
     }
     __syncthreads();
     if (tid < R) {
-      float M = -INFINITY, L = 0.f;
+      float M = LOWEST, L = 0.f;
 #pragma unroll
       for (int i = 0; i < AW; ++i) M = fmaxf(M, part_m[i][tid]);
 #pragma unroll
       for (int i = 0; i < AW; ++i) {
-        const float x = part_weight(part_m[i][tid], part_l[i][tid], M);
+        const float x = part_weight(part_m[i][tid], M);
         wts[i][tid] = x;
         L += x * part_l[i][tid];
       }
@@ -735,7 +733,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i)
             if (i < np) load(i, v[i]);
-          float M = -INFINITY, L = 0.f;
+          float M = LOWEST, L = 0.f;
           for (int c = lane; c < np; c += 32) {
             const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(c) + MAX_ROWS * DH + 2 * row));
             wt[c] = ml.x;
@@ -745,7 +743,7 @@ __global__ void __launch_bounds__(AW * 32, NT == 2 ? (NP == 1 ? 3 : 2) : NP == 1
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
           for (int c = lane; c < np; c += 32) {
-            const float x = part_weight(wt[c], wt[c + KVQ_MAX_CTAS], M);
+            const float x = part_weight(wt[c], M);
             L = fmaf(x, wt[c + KVQ_MAX_CTAS], L);
             wt[c] = x;
           }
