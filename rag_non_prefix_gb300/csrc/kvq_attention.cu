@@ -789,17 +789,19 @@ cudaError_t launch(KvqAttn p, cudaStream_t s) {
   static DeviceOnce configured;
   cudaError_t e = max_dynamic_smem_once(reinterpret_cast<const void*>(kvq_attention_kernel<T, DH, NT, NP>), A::SMEM, configured);
   if (e != cudaSuccess) return e;
-  // as many CTAs as fit at once
-  static std::atomic<int> fits{0};
-  int grid = fits.load(std::memory_order_relaxed);
+  // as many CTAs as fit at once, per device
+  static std::atomic<int> fits[64];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < 64;
+  int grid = cached ? fits[dev].load(std::memory_order_relaxed) : 0;
   if (grid == 0) {
-    int dev = 0, sms = 0, per_sm = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    int sms = 0, per_sm = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kvq_attention_kernel<T, DH, NT, NP>, AW * 32, A::SMEM)) != cudaSuccess)
       return e;
     grid = std::min(KVQ_MAX_CTAS, std::max(1, per_sm) * sms);
-    fits.store(grid, std::memory_order_relaxed);
+    if (cached) fits[dev].store(grid, std::memory_order_relaxed);
   }
   return launch_chain(kvq_attention_kernel<T, DH, NT, NP>, dim3(grid), dim3(AW * 32), A::SMEM, s, p);
 }
