@@ -482,7 +482,8 @@ cb_status cb_kvq_read(const cb_kvq_cache* cache, const int32_t* seq, const int32
  *           before, cb_kvq_write); a negative one (padding) to nothing, its output is zero
  * Head h reads KV head h / (n_heads / n_kv_heads).  What the cache holds beyond a token's position (NaN too) does not
  * reach its output.  Scores and sums are fp32; the cache's values enter exactly, weights are rounded to bf16 for
- * bf16 outputs and not rounded for fp32 ones.  Made for few tokens (decoding, checking drafts): for a long prompt read the rows
+ * bf16 outputs and not rounded for fp32 ones.  A score of -infinity weighs nothing.  Sums stay within float32 while keys times the largest value
+ * is below 2^117 and queries below 2^127.  Made for few tokens (decoding, checking drafts): for a long prompt read the rows
  * back (cb_kvq_read) and use cb_attention.
  * scratch: cb_kvq_scratch_size() bytes of device memory, 16-byte aligned, zero-filled before its first use and left
  * ready by each call; calls that share one must not overlap on the GPU.  Results repeat exactly. */

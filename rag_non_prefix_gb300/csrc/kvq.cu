@@ -3,7 +3,7 @@
 //
 // Bounds: a number is 2 or 4 bytes and 5 bits, and takes some 28 instructions to write and 13 to read.  Prompts are bound by these
 // and by the latency of the loads that 32 warps an SM cover (8320 rows of 8 heads of 128 written from bf16 and read back to
-// fp32: 36.4 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to bf16: 25.4 us, 3.5 TB/s; with the registers of
+// fp32: 36.5 us for 124 MB, half the rate of a copy; 4096 rows of 32 heads read to bf16: 25.3 us, 3.5 TB/s; with the registers of
 // 24 warps an SM 28.4); decoded tokens by one warp's chain (16 rows of 8 heads written and read back: 4.6 us, two launches).
 //
 // Both kernels give eight channels to a lane: a row of one head is 16 lanes (128 channels) or 8, a group of 32

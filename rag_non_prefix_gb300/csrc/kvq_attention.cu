@@ -8,7 +8,7 @@
 // starts at (zero - 16) sum_c q_c.  Values: two more products with the operands zero and -16 (both exact in bf16)
 // go into the same accumulator, which so holds the true sums; kept apart, the sums of code and zero of a long
 // context would be hundreds of times larger than the result, and so what the accumulator's rounding towards zero leaves of
-// them.  p scale is rounded to bf16, and the same rounded number multiplies code and zero, so its rounding is one of 2^-9
+// them.  p scale is rounded to bf16, and the same rounded number multiplies code and zero, so its rounding is one of 2^-8
 // of the value itself.  fp32 outputs: queries and p scale enter as three bf16 parts each, so that nothing is
 // lost, with code - 8 as the operand, the zeros' part in fp32 arithmetic, and blocks of 16 keys added in fp32 outside of
 // the tensor core.
@@ -25,8 +25,8 @@
 // keys of a quantum, through a ring of its own in shared memory; no warp waits for another before the end.
 //
 // Bounds (8 KV heads of 128): long caches by the instructions, some 1000 a pair of blocks for 5 KB, and by 7 to 10 us of units'
-// beginnings, ends and merges: 32 ragged sequences of up to 8320 keys, groups of 7, 63 us, 2.7 TB/s of cache.  4 tokens of 16
-// sequences, groups of 8 (two units of 16 rows a KV head, each of which reads the cache) 109 us; fp32 outputs 46 us for 4 x 4128
+// beginnings, ends and merges: 32 ragged sequences of up to 8320 keys, groups of 7, 64 us, 2.7 TB/s of cache.  4 tokens of 16
+// sequences, groups of 8 (two units of 16 rows a KV head, each of which reads the cache) 109 us; fp32 outputs 45 us for 4 x 4128
 // keys of 32 KV heads, three products for each of the others; one sequence of 3200 keys 15 us, a chain of latencies (share 1.7,
 // first loads 1.9, keys 2.6, part to memory 1.9, merge 3.3 us).  Four warps a CTA, four CTAs an SM: 128 registers a thread hold the
 // loop (32 sequences: with five CTAs spills, with eight warps a CTA, which wait for each other, 69 us, with two, whose parts are

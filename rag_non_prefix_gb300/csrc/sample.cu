@@ -4,8 +4,9 @@
 //   order: the first k; of those the shortest whose mass reaches p times theirs; those with w >= min_p.  The
 //   token is the first whose running kept mass exceeds u times the kept mass, along that order or by rising index.
 // So a filter and the draw are the same question, "at which token does the running count or mass reach a
-// target", answered exactly: weights are whole numbers of 2^-44 (a weight's relative error is near
-// 2^-30: the exponent (x - max) / t log2(e) is carried in two fp32 numbers), and sums of whole numbers do not depend on their order.
+// target", answered exactly: weights are whole numbers of 2^-44 of the largest (before they are cut to one, off by less than 2^-28 of
+// themselves, 2^-28.7 measured: the exponent (x - max) / t log2(e) is carried in two fp32 numbers), and sums of whole numbers do not depend
+// on their order.  min_p is compared by logits, x >= max + t log(min_p): weights of few units say little.
 //
 // A row is dealt with by the 1 to 8 CTAs of a cluster, which read it from memory once and again, two or three
 // times, from the second-level cache (so that two CTAs fit an SM, one working while the other waits).  Three ways, each of
@@ -20,11 +21,11 @@
 // A draw by rising index needs the filters' last token alone: 1. sorts what is kept once more, by index; for the others one pass over the
 // exact weights sums what is kept of each 32 vectors, and the 32 that hold the target are weighed once more, token by token.
 //
-// Bounds: a few rows by the chain of their passes and cluster barriers (one row of 32000 with top-k: 10.3 us; 64 rows of 64000 fp32 with
-// top-p: 36.6 us, of these the exact pass 6.4, the merge of the near masses 5.9, their own pass 3.3), many by the passes' instructions:
-// 512 rows of 64000 bf16 with top-k and top-p 39.4 us, 1.7 TB/s (a row 12 us on half an SM: its loads and maxima 3.9, the bound 1.5,
-// collecting 3.5, sorting and sums 3.0; 1.7 rounds of rows); with top-p alone 144 us (38 us a row and SM: near masses 10, the exact
-// pass 23, near 90 issue slots a logit and warp).  512 threads, two CTAs an SM: 1024 threads and one were slower.  Rows that 1. and 2.
+// Bounds: a few rows by the chain of their passes and cluster barriers (one row of 32000 with top-k: 10.2 us, by index 11.3; 64 rows of
+// 64000 fp32 with top-p: 35.1 us, of these the exact pass 6.4, the merge of the near masses 5.9, their own pass 3.3, by index 44.6), many by the
+// passes' instructions: 512 rows of 64000 bf16 with top-k and top-p 38.3 us, by index 41.4, 1.7 TB/s (a row 12 us on half an SM: its loads and maxima 3.9, the bound 1.5,
+// collecting 3.5, sorting and sums 3.0; 1.7 rounds of rows); with top-p alone 147 us (38 us a row and SM: near masses 10, the exact
+// pass 23, near 90 issue slots a logit and warp), by index 201; with temperature alone 132, by index, with one pass, 86.  512 threads, two CTAs an SM: 1024 threads and one were slower.  Rows that 1. and 2.
 // leave to 3. cost 20 us more in small batches and 3 to 8 times as much in large ones: more than 512 logits within 1/256 of
 // each other (spread of 64000 logits below about a quarter of the temperature), or top-k beyond 256 a CTA.
 #include <cooperative_groups.h>
